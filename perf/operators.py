@@ -244,7 +244,8 @@ def _plain_codes(x, bits):
     """The values the stored codes stand for: block-wise symmetric codes of 128 elements."""
     qmax = 2 ** (bits - 1) - 1
     v = x.float().view(-1, 128)
-    scale = v.abs().amax(1, keepdim=True) / qmax
+    # by a tensor: torch divides by a number as a product with its reciprocal, which is not fl(a / b)
+    scale = v.abs().amax(1, keepdim=True) / torch.tensor(float(qmax), device="cuda")
     code = torch.where(scale > 0, torch.round(v / scale), 0.0).clamp(-qmax, qmax)
     return (code * scale).to(torch.bfloat16).view(x.shape)
 
@@ -441,7 +442,8 @@ def _exact_ln(s, case):
         # the stored values are defined by binary32 roundings: the scale, the quotient, the product
         top = 2 ** (case["bits"] - 1) - 1
         blocks = s["x"].float().reshape(-1, 128)
-        step = torch.div(blocks.abs().max(dim=1).values, float(top)).unsqueeze(1)
+        divisor = torch.tensor(float(top), device="cuda")   # a tensor, as in _plain_codes
+        step = torch.div(blocks.abs().max(dim=1).values, divisor).unsqueeze(1)
         quotient = torch.div(blocks, torch.where(step == 0, 1.0, step))
         kept = torch.mul(torch.round(quotient), step).bfloat16().double().reshape(v.shape)
         out.update(_exact_ln_grads(kept, s["dy"], s["w"], *_exact_stats(kept)))
