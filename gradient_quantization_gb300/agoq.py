@@ -67,6 +67,25 @@ def _lib_handle():
         L.agoq_device_status.argtypes = [vp]
         L.agoq_test_wait_timeout.argtypes = [i64, vp]
         L.agoq_dbca_pp_bits.argtypes = [i32, i32, i32, vp]
+        f32 = ctypes.c_float
+        L.agoq_layernorm_forward.argtypes = [vp, i64, vp, vp, i32, i64, i64, i32, f32, vp, i64,
+                                             vp, vp, vp, vp, i32, vp]
+        L.agoq_layernorm_backward_workspace_bytes.argtypes = [i64, i64]
+        L.agoq_layernorm_backward_workspace_bytes.restype = i64
+        L.agoq_layernorm_backward.argtypes = [vp, i64, vp, i64, vp, i32, vp, vp, i64, i64, i32,
+                                              vp, i64, vp, vp, vp, i64, vp]
+        L.agoq_layernorm_backward_laaq.argtypes = [vp, vp, i32, vp, i64, vp, i32, i64, i64, f32,
+                                                   vp, i64, vp, vp, vp, i64, vp]
+        L.agoq_grad_list_check.argtypes = [vp, i32]
+        L.agoq_grad_norm_workspace_bytes.argtypes = [i32]
+        L.agoq_grad_norm_workspace_bytes.restype = i64
+        L.agoq_grad_norm.argtypes = [vp, i32, vp, vp, i64, vp]
+        L.agoq_clip_grads.argtypes = [vp, i32, f32, vp, vp]
+        L.agoq_clip_grad_norm.argtypes = [vp, i32, f32, vp, vp, i64, vp]
+        L.agoq_token_logprobs.argtypes = [vp, i64, i32, vp, i64, i64, i32, vp, vp, vp, vp, vp, vp]
+        L.agoq_token_logprobs_backward.argtypes = [vp, i64, i32, vp, i64, i64, vp, vp, vp, vp,
+                                                   vp, i64, vp]
+        L.agoq_token_loss.argtypes = [vp, i64, i32, vp, vp, i64, i64, vp, vp, i64, vp]
         L.agoq_fwd_gemm_quant.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
         for name in ("agoq_quant_act", "agoq_dequant_act", "agoq_grad_accum_fp8",
                      "agoq_reduce_fp8_shards", "agoq_wgrad_gemm_int4",
@@ -75,7 +94,11 @@ def _lib_handle():
                      "agoq_silu_backward", "agoq_rmsnorm_backward", "agoq_rmsnorm_backward_ws",
                      "agoq_rmsnorm_backward_noalloc",
                      "agoq_dbca_pp_bits",
-                     "agoq_fwd_gemm_quant", "agoq_test_wait_timeout"):
+                     "agoq_fwd_gemm_quant", "agoq_test_wait_timeout",
+                     "agoq_layernorm_forward", "agoq_layernorm_backward",
+                     "agoq_layernorm_backward_laaq", "agoq_grad_list_check", "agoq_grad_norm",
+                     "agoq_clip_grads", "agoq_clip_grad_norm", "agoq_token_logprobs",
+                     "agoq_token_logprobs_backward", "agoq_token_loss"):
             getattr(L, name).restype = i32
         _L = L
     return _L
@@ -364,6 +387,314 @@ def agoq_wgrad_gemm_int4_accum_fp8(dY, x_codes, x_scales, M, N, K, master, maste
                                                 _stream(stream)),
            "agoq_wgrad_gemm_int4_accum_fp8")
     return master, master_scales
+
+
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+F32, BF16, F16, E4M3 = 0, 1, 2, 3
+
+
+class _Launch:
+    """The stream of a call, and tensors allocated for it: they belong to that
+    stream, so memory that torch's current stream still uses is not written by
+    another one.  Inputs are the caller's to order and keep alive."""
+
+    def __init__(self, stream, device):
+        current = torch.cuda.current_stream(device)
+        if stream is None:
+            self.handle, self.other = current.cuda_stream, None
+            return
+        self.handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        self.other = None
+        if self.handle != current.cuda_stream:
+            self.other = torch.cuda.ExternalStream(self.handle, device=device)
+
+    def empty(self, shape, dtype, device):
+        if self.other is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.other):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, what, n=None, T=None, dtype=None):
+    """(address, rows, row length, row distance) of a CUDA tensor of FP32, BF16 or FP16
+    whose last dimension is contiguous: two-dimensional, or contiguous throughout."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % what)
+    if t.dtype not in DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError("%s must be %s, got %s" % (what, dtype or "float32, bfloat16 or float16",
+                                                   t.dtype))
+    if t.dim() == 2:
+        rows, length = t.shape
+        ld, step = t.stride()
+        if length > 1 and step != 1:
+            raise ValueError("the last dimension of %s must be contiguous" % what)
+        if rows <= 1 or ld < length:
+            if rows > 1:
+                raise ValueError("rows of %s overlap" % what)
+            ld = length
+    else:
+        if t.dim() == 0 or not t.is_contiguous():
+            raise ValueError("%s must be contiguous, or two-dimensional" % what)
+        length = ld = t.shape[-1]
+        rows = t.numel() // length if length else 0
+    if (n is not None and length != n) or (T is not None and rows != T):
+        raise ValueError("%s must hold %s rows of %s" % (what, T, n))
+    return t.data_ptr(), rows, length, ld
+
+
+def _vector(t, n, what, dtypes):
+    """Address of a contiguous CUDA tensor of n elements (None: 0)."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % what)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous and hold %d values" % (what, n))
+    return t.data_ptr()
+
+
+_F32 = (torch.float32,)
+
+
+def _params(x_dtype, H, w, b=None):
+    """(w, b, param_dtype): weight and bias of one type, FP32 or the activation's."""
+    kinds = (torch.float32, x_dtype)
+    wp, bp = _vector(w, H, "w", kinds), _vector(b, H, "b", kinds)
+    if w is not None and b is not None and w.dtype != b.dtype:
+        raise TypeError("w and b must have one type")
+    ref = w if w is not None else b
+    return wp, bp, DTYPES[ref.dtype] if ref is not None else F32
+
+
+def agoq_layernorm_forward(x, w=None, b=None, eps=1e-5, bits=0, y=None, mean=None, rstd=None,
+                           codes=None, scales=None, want_stats=True, stream=None):
+    """Layer norm over the last dimension of `x` (FP32, BF16 or FP16; two-dimensional with any
+    row distance, or contiguous).  `bits` 4, 5, 6 or 8 also writes the LAAQ codes of x (BF16,
+    rows a multiple of 128).  Returns (y, mean, rstd, codes, scales); codes and scales are None
+    for bits = 0, mean and rstd None unless given or wanted."""
+    xp, T, H, ldx = _rows(x, "x")
+    wp, bp, pd = _params(x.dtype, H, w, b)
+    at, dev = _Launch(stream, x.device), x.device
+    if y is None:
+        y = at.empty(x.shape, x.dtype, dev)
+    yp, _, _, ldy = _rows(y, "y", H, T, x.dtype)
+    if mean is None and want_stats:
+        mean = at.empty(T, torch.float32, dev)
+    if rstd is None and want_stats:
+        rstd = at.empty(T, torch.float32, dev)
+    if bits:
+        if codes is None:
+            codes = at.empty(T * H // BLOCK * record_bytes(bits), torch.uint8, dev)
+        if scales is None:
+            scales = at.empty(T * H // BLOCK, torch.float32, dev)
+    else:
+        codes = scales = None
+    cp = _vector(codes, T * H // BLOCK * record_bytes(bits), "codes", (torch.uint8,))
+    sp = _vector(scales, T * H // BLOCK, "scales", _F32)
+    _check(lib().agoq_layernorm_forward(
+        xp, ldx, wp, bp, pd, T, H, DTYPES[x.dtype], eps, yp, ldy, _vector(mean, T, "mean", _F32),
+        _vector(rstd, T, "rstd", _F32), cp, sp, bits, at.handle), "agoq_layernorm_forward")
+    return y, mean, rstd, codes, scales
+
+
+def agoq_layernorm_backward_workspace_bytes(T, H):
+    """Bytes of scratch the layer norm's backward calls need for dw or db."""
+    return int(lib().agoq_layernorm_backward_workspace_bytes(int(T), int(H)))
+
+
+def _norm_sums(at, T, H, dev, dw, db, want_dw, want_db, workspace):
+    if dw is None and want_dw:
+        dw = at.empty(H, torch.float32, dev)
+    if db is None and want_db:
+        db = at.empty(H, torch.float32, dev)
+    if workspace is None and (dw is not None or db is not None):
+        workspace = at.empty(agoq_layernorm_backward_workspace_bytes(T, H), torch.uint8, dev)
+    if workspace is None:
+        return dw, db, None, 0, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return dw, db, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def agoq_layernorm_backward(x, dy, mean, rstd, w=None, dx=None, dw=None, db=None, want_dw=True,
+                            want_db=True, workspace=None, stream=None):
+    """Layer norm backward from the input and its statistics: returns (dx, dw, db), dw and db
+    FP32 (None unless given or wanted).  dx may be dy or x."""
+    xp, T, H, ldx = _rows(x, "x")
+    dyp, _, _, lddy = _rows(dy, "dy", H, T, x.dtype)
+    wp, _, pd = _params(x.dtype, H, w)
+    at, dev = _Launch(stream, x.device), x.device
+    if dx is None:
+        dx = at.empty(dy.shape, dy.dtype, dev)
+    dxp, _, _, lddx = _rows(dx, "dx", H, T, x.dtype)
+    dw, db, workspace, ws, nws = _norm_sums(at, T, H, dev, dw, db, want_dw, want_db, workspace)
+    _check(lib().agoq_layernorm_backward(
+        xp, ldx, dyp, lddy, wp, pd, _vector(mean, T, "mean", _F32),
+        _vector(rstd, T, "rstd", _F32), T, H, DTYPES[x.dtype], dxp, lddx,
+        _vector(dw, H, "dw", _F32), _vector(db, H, "db", _F32), ws, nws, at.handle),
+        "agoq_layernorm_backward")
+    return dx, dw, db
+
+
+def agoq_layernorm_backward_laaq(codes, scales, bits, dy, eps=1e-5, w=None, dx=None, dw=None,
+                                 db=None, want_dw=True, want_db=True, workspace=None, stream=None):
+    """Layer norm backward from the LAAQ codes of the input (statistics recomputed from the
+    dequantized values): returns (dx, dw, db) as agoq_layernorm_backward."""
+    dyp, T, H, lddy = _rows(dy, "dy", dtype=torch.bfloat16)
+    wp, _, pd = _params(dy.dtype, H, w)
+    at, dev = _Launch(stream, dy.device), dy.device
+    if dx is None:
+        dx = at.empty(dy.shape, dy.dtype, dev)
+    dxp, _, _, lddx = _rows(dx, "dx", H, T, dy.dtype)
+    dw, db, workspace, ws, nws = _norm_sums(at, T, H, dev, dw, db, want_dw, want_db, workspace)
+    blocks = T * H // BLOCK
+    _check(lib().agoq_layernorm_backward_laaq(
+        _vector(codes, blocks * record_bytes(bits), "codes", (torch.uint8,)),
+        _vector(scales, blocks, "scales", _F32), bits, dyp, lddy, wp, pd, T, H, eps, dxp, lddx,
+        _vector(dw, H, "dw", _F32), _vector(db, H, "db", _F32), ws, nws, at.handle),
+        "agoq_layernorm_backward_laaq")
+    return dx, dw, db
+
+
+class _GradTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class GradList:
+    """The gradients that agoq_grad_norm and the clipping calls take, built once and kept.
+
+    grads: CUDA tensors (FP32, BF16 or FP16) and (codes, scales) pairs (FP8 masters: uint8
+    E4M3 codes and FP32 block scales).  outs: for each the tensor that receives the clipped
+    gradient (for a pair: the clipped scales), or None to clip in place.  All are contiguous.
+    The list keeps references to them and a workspace on their device; calls on one list must
+    not overlap in time on the GPU."""
+
+    def __init__(self, grads, outs=None):
+        grads = list(grads)
+        outs = [None] * len(grads) if outs is None else list(outs)
+        if len(outs) != len(grads):
+            raise ValueError("outs must match grads")
+        self.entries = (_GradTensor * max(1, len(grads)))()
+        self.count = len(grads)
+        self.device = None
+        for e, g, o in zip(self.entries, grads, outs):
+            codes, scales = g if isinstance(g, tuple) else (g, None)
+            n = codes.numel() if isinstance(codes, torch.Tensor) else 0
+            if scales is None:
+                e.data = _vector(codes, n, "gradient", tuple(DTYPES))
+                e.out = e.data if o is None else _vector(o, n, "out", (codes.dtype,))
+                e.dtype = DTYPES[codes.dtype]
+            else:
+                e.data = _vector(codes, n, "codes", (torch.uint8,))
+                e.scales = _vector(scales, n // BLOCK, "scales", _F32)
+                e.out = e.scales if o is None else _vector(o, n // BLOCK, "out", _F32)
+                e.dtype = E4M3
+            e.n = n
+            self.device = self.device or codes.device
+        self.device = self.device or torch.device("cuda", torch.cuda.current_device())
+        self.tensors = (grads, outs)
+        _check(lib().agoq_grad_list_check(self.entries, self.count), "agoq_grad_list_check")
+        self.workspace = torch.empty(
+            int(lib().agoq_grad_norm_workspace_bytes(self.count)), dtype=torch.uint8,
+            device=self.device)
+
+    def _scratch(self):
+        return self.workspace.data_ptr(), self.workspace.numel()
+
+
+def agoq_grad_norm(grads, norm=None, stream=None):
+    """Global L2 norm of a GradList -> FP32 CUDA tensor of one element."""
+    at = _Launch(stream, grads.device)
+    if norm is None:
+        norm = at.empty(1, torch.float32, grads.device)
+    _check(lib().agoq_grad_norm(grads.entries, grads.count, _vector(norm, 1, "norm", _F32),
+                                *grads._scratch(), at.handle), "agoq_grad_norm")
+    return norm
+
+
+def agoq_clip_grads(grads, max_norm, norm, stream=None):
+    """Clip a GradList by the norm in the one-element FP32 CUDA tensor `norm`: every gradient
+    times min(1, max_norm / (norm + 1e-6)); of FP8 masters the scales alone change."""
+    at = _Launch(stream, grads.device)
+    _check(lib().agoq_clip_grads(grads.entries, grads.count, max_norm,
+                                 _vector(norm, 1, "norm", _F32), at.handle), "agoq_clip_grads")
+
+
+def agoq_clip_grad_norm(grads, max_norm, norm=None, stream=None):
+    """agoq_grad_norm and agoq_clip_grads in one call; returns the norm before clipping."""
+    at = _Launch(stream, grads.device)
+    if norm is None:
+        norm = at.empty(1, torch.float32, grads.device)
+    _check(lib().agoq_clip_grad_norm(grads.entries, grads.count, max_norm,
+                                     _vector(norm, 1, "norm", _F32), *grads._scratch(),
+                                     at.handle), "agoq_clip_grad_norm")
+    return norm
+
+
+_I64 = (torch.int64,)
+
+
+def agoq_token_logprobs(logits, tokens, k=0, want_entropy=True, logp=None, entropy=None, lse=None,
+                        top_logp=None, top_ids=None, stream=None):
+    """Log probabilities of `tokens` (int64, one a row; negative: ignored) under `logits`
+    (FP32, BF16 or FP16 rows), and the k most likely alternatives of each row.  Returns (logp,
+    entropy, lse, top_logp, top_ids): FP32 [T] each, FP32 and int64 [T][k] (None for k = 0);
+    entropy is None unless given or wanted."""
+    xp, T, V, ld = _rows(logits, "logits")
+    at, dev = _Launch(stream, logits.device), logits.device
+    if logp is None:
+        logp = at.empty(T, torch.float32, dev)
+    if entropy is None and want_entropy:
+        entropy = at.empty(T, torch.float32, dev)
+    if lse is None:
+        lse = at.empty(T, torch.float32, dev)
+    if k > 0 and top_logp is None:
+        top_logp = at.empty((T, k), torch.float32, dev)
+    if k > 0 and top_ids is None:
+        top_ids = at.empty((T, k), torch.int64, dev)
+    _check(lib().agoq_token_logprobs(
+        xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64), T, V, k,
+        _vector(logp, T, "logp", _F32), _vector(entropy, T, "entropy", _F32),
+        _vector(lse, T, "lse", _F32), _vector(top_logp, T * k, "top_logp", _F32),
+        _vector(top_ids, T * k, "top_ids", _I64), at.handle), "agoq_token_logprobs")
+    return logp, entropy, lse, top_logp, top_ids
+
+
+def agoq_token_logprobs_backward(logits, tokens, lse, dlogp, entropy=None, dentropy=None,
+                                 dlogits=None, stream=None):
+    """Gradient of agoq_token_logprobs' logp (and entropy, with `dentropy`) -> dlogits of the
+    logits' type; `dlogits` may be the logits themselves."""
+    xp, T, V, ld = _rows(logits, "logits")
+    at = _Launch(stream, logits.device)
+    if dlogits is None:
+        dlogits = at.empty(logits.shape, logits.dtype, logits.device)
+    dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
+    _check(lib().agoq_token_logprobs_backward(
+        xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64), T, V,
+        _vector(lse, T, "lse", _F32), _vector(entropy, T, "entropy", _F32),
+        _vector(dlogp, T, "dlogp", _F32), _vector(dentropy, T, "dentropy", _F32), dp, ldd,
+        at.handle), "agoq_token_logprobs_backward")
+    return dlogits
+
+
+def agoq_token_loss(logits, tokens, weights=None, logp=None, dlogits=None, stream=None):
+    """Log probabilities of `tokens` and the gradient of the loss -sum(weights * logp) ->
+    (logp FP32 [T], dlogits of the logits' type); `dlogits` may be the logits themselves."""
+    xp, T, V, ld = _rows(logits, "logits")
+    at, dev = _Launch(stream, logits.device), logits.device
+    if logp is None:
+        logp = at.empty(T, torch.float32, dev)
+    if dlogits is None:
+        dlogits = at.empty(logits.shape, logits.dtype, dev)
+    dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
+    _check(lib().agoq_token_loss(
+        xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64),
+        _vector(weights, T, "weights", _F32), T, V, _vector(logp, T, "logp", _F32), dp, ldd,
+        at.handle), "agoq_token_loss")
+    return logp, dlogits
 
 
 def agoq_test_wait_timeout(limit_cycles, stream=None):

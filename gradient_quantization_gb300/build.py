@@ -29,8 +29,12 @@ UNITS = {
     "rmsnorm.cu": ["-fmad=false"],
     "fwd_gemm.cu": ["-fmad=false"],
     "fwd_gemm_k64.cu": ["-fmad=false"],
+    "layernorm.cu": ["-fmad=false"],
+    "grad_norm.cu": ["-fmad=false"],
+    "token_logprobs.cu": ["-fmad=false"],
 }
-HEADERS = ["agoq_device.cuh", "agoq_launch.h", "gemm_common.cuh", "wgrad_gemm_impl.cuh", "fwd_gemm_impl.cuh"]
+HEADERS = ["agoq_device.cuh", "agoq_launch.h", "gemm_common.cuh", "wgrad_gemm_impl.cuh", "fwd_gemm_impl.cuh",
+           "typed_io.cuh"]
 
 
 def _nvcc():

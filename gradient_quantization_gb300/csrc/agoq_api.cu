@@ -8,7 +8,9 @@
 #include "../../include/agoq.h"
 #include "agoq_launch.h"
 
+#include <algorithm>
 #include <cstdint>
+#include <new>
 
 namespace agoq {
 
@@ -42,6 +44,50 @@ agoq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? AGOQ_OK : AGOQ_
 
 cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
 
+// A byte range of an argument; empty for a NULL pointer.
+struct Range {
+    const void *p;
+    uint64_t n;
+};
+
+// Half-open byte range of T rows of `len` elements of `size` bytes, `ld` apart.
+Range rows(const void *p, int64_t T, int64_t len, int64_t ld, int size) {
+    return {p, p && T > 0 ? ((uint64_t)(T - 1) * ld + len) * size : 0};
+}
+Range vec(const void *p, int64_t n, int size) { return {p, p ? (uint64_t)n * size : 0}; }
+
+// A range of a gradient list's tensor, ordered by address.
+struct Span {
+    uintptr_t from, to;
+    int tensor;
+    bool out;
+    bool operator<(const Span &o) const { return from < o.from; }
+};
+
+// Some output overlaps an input or another output.
+template <int O, int I>
+bool any_overlap(const Range (&out)[O], const Range (&in)[I]) {
+    for (int o = 0; o < O; ++o) {
+        for (int i = 0; i < I; ++i)
+            if (overlap(out[o].p, out[o].n, in[i].p, in[i].n)) return true;
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o].p, out[o].n, out[i].p, out[i].n)) return true;
+    }
+    return false;
+}
+
+bool float_dtype(int d) { return d == AGOQ_F32 || d == AGOQ_BF16 || d == AGOQ_F16; }
+int elem_size(int d) { return d == AGOQ_F32 ? 4 : d == AGOQ_E4M3 ? 1 : 2; }
+
+// Sizes of rows that the typed calls take: T rows of n elements, `ld` apart,
+// whose byte offsets stay within 62 bits.
+bool rows_ok(int64_t T, int64_t n, int64_t ld) {
+    return ld >= n && ld <= (1ll << 40) && T <= (1ll << 60) / (ld > 0 ? ld : 1);
+}
+
+constexpr int64_t kMaxHidden = 1ll << 24, kMaxVocab = 1ll << 30;
+constexpr int kMaxTop = 32;
+
 }  // namespace
 }  // namespace agoq
 
@@ -57,7 +103,7 @@ const char *agoq_status_string(agoq_status s) {
         case AGOQ_ERR_ALIAS: return "AGOQ_ERR_ALIAS: an output overlaps an input";
         case AGOQ_ERR_CUDA: return "AGOQ_ERR_CUDA: CUDA runtime error";
         case AGOQ_ERR_TIMEOUT: return "AGOQ_ERR_TIMEOUT: a pipeline wait gave up";
-        case AGOQ_ERR_FORMAT: return "AGOQ_ERR_FORMAT: unsupported intermediate format";
+        case AGOQ_ERR_FORMAT: return "AGOQ_ERR_FORMAT: unsupported intermediate format or element type";
     }
     return "AGOQ_ERR_UNKNOWN";
 }
@@ -362,6 +408,324 @@ agoq_status agoq_fwd_gemm_quant(const void *x_bf16, const void *w_bf16, int T, i
         return AGOQ_ERR_ALIAS;
     return from_cuda(launch_fwd_gemm_quant(x_bf16, w_bf16, T, N, K, bits, y_bf16, codes, scales,
                                            as_stream(stream)));
+}
+
+agoq_status agoq_layernorm_forward(const void *x, int64_t ldx, const void *w, const void *b,
+                                   int param_dtype, int64_t T, int64_t H, int dtype, float eps,
+                                   void *y, int64_t ldy, float *mean, float *rstd, void *codes,
+                                   float *scales, int bits, void *stream) {
+    using namespace agoq;
+    if (!float_dtype(dtype) || (param_dtype != AGOQ_F32 && param_dtype != dtype))
+        return AGOQ_ERR_FORMAT;
+    const bool quant = codes || scales;
+    if (quant && dtype != AGOQ_BF16) return AGOQ_ERR_FORMAT;
+    if (quant && !bits_ok(bits)) return AGOQ_ERR_BITS;
+    if (T < 0 || H < 1 || H > kMaxHidden || !rows_ok(T, H, ldx) || !rows_ok(T, H, ldy) ||
+        !(eps >= 0.0f) || eps > 3.0e38f || (quant && H % kBlockElems))
+        return AGOQ_ERR_SHAPE;
+    if (T == 0) return AGOQ_OK;
+    if (!x || !y || (quant && (!codes || !scales))) return AGOQ_ERR_NULL;
+    const int es = elem_size(dtype), ps = elem_size(param_dtype);
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(w, ps) || !aligned(b, ps) ||
+        !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(codes, 16) || !aligned(scales, 4))
+        return AGOQ_ERR_ALIGN;
+    const uint64_t nb = quant ? (uint64_t)T * H / kBlockElems : 0;
+    const Range xr = rows(x, T, H, ldx, es), yr = rows(y, T, H, ldy, es);
+    const bool in_place = x == y && ldx == ldy;
+    const Range out[5] = {in_place ? Range{y, 0} : yr, vec(mean, T, 4), vec(rstd, T, 4),
+                          {codes, nb * 16 * bits}, {scales, nb * 4}};
+    const Range in[3] = {xr, vec(w, H, ps), vec(b, H, ps)};
+    if (any_overlap(out, in) || (in_place && (overlap(y, yr.n, w, in[1].n) ||
+                                              overlap(y, yr.n, b, in[2].n))))
+        return AGOQ_ERR_ALIAS;
+    const LnForward a{x, ldx, w, b, param_dtype == AGOQ_F32, T, H, dtype, eps, y, ldy,
+                      mean, rstd, codes, scales, bits};
+    return from_cuda(launch_ln_forward(a, as_stream(stream)));
+}
+
+int64_t agoq_layernorm_backward_workspace_bytes(int64_t T, int64_t H) {
+    using namespace agoq;
+    if (T < 0 || H < 1 || H > kMaxHidden || !rows_ok(T, H, H)) return -1;
+    return ln_workspace_floats(T, H) * 4;
+}
+
+static agoq_status layernorm_backward_common(agoq::LnBackward a, int param_dtype,
+                                             int64_t workspace_bytes, void *stream) {
+    using namespace agoq;
+    if (!float_dtype(a.dtype) || (param_dtype != AGOQ_F32 && param_dtype != a.dtype))
+        return AGOQ_ERR_FORMAT;
+    if (a.T < 0 || a.H < 1 || a.H > kMaxHidden || !rows_ok(a.T, a.H, a.ldx) ||
+        !rows_ok(a.T, a.H, a.lddy) || !rows_ok(a.T, a.H, a.lddx) ||
+        (a.bits && (a.H % kBlockElems || !(a.eps >= 0.0f) || a.eps > 3.0e38f)))
+        return AGOQ_ERR_SHAPE;
+    const bool sums = a.dw || a.db;
+    if (a.T == 0 && !sums) return AGOQ_OK;
+    if (a.T > 0) {
+        if (!a.x || !a.dy || !a.dx) return AGOQ_ERR_NULL;
+        if (a.bits ? !a.scales : (!a.mean || !a.rstd)) return AGOQ_ERR_NULL;
+        if (sums && !a.workspace) return AGOQ_ERR_NULL;
+        if (sums && workspace_bytes < ln_workspace_floats(a.T, a.H) * 4) return AGOQ_ERR_SHAPE;
+    }
+    const int es = elem_size(a.dtype), ps = elem_size(param_dtype);
+    if (!aligned(a.x, a.bits ? 16 : es) || !aligned(a.scales, 4) || !aligned(a.dy, es) ||
+        !aligned(a.w, ps) || !aligned(a.mean, 4) || !aligned(a.rstd, 4) || !aligned(a.dx, es) ||
+        !aligned(a.dw, 4) || !aligned(a.db, 4) || (sums && !aligned(a.workspace, 16)))
+        return AGOQ_ERR_ALIGN;
+    const uint64_t nb = (uint64_t)a.T * a.H / kBlockElems;
+    const Range xr = a.bits ? Range{a.x, nb * 16 * a.bits} : rows(a.x, a.T, a.H, a.ldx, es);
+    const Range dyr = rows(a.dy, a.T, a.H, a.lddy, es), dxr = rows(a.dx, a.T, a.H, a.lddx, es);
+    const bool on_dy = a.dx == a.dy && a.lddx == a.lddy;
+    const bool on_x = !a.bits && a.dx == a.x && a.lddx == a.ldx;
+    const Range out[4] = {vec(a.dw, a.H, 4), vec(a.db, a.H, 4),
+                          {a.workspace, sums && a.T > 0
+                                            ? (uint64_t)ln_workspace_floats(a.T, a.H) * 4 : 0},
+                          dxr};
+    const Range in[6] = {on_x ? Range{a.x, 0} : xr, on_dy ? Range{a.dy, 0} : dyr,
+                         vec(a.w, a.H, ps), vec(a.mean, a.T, 4), vec(a.rstd, a.T, 4),
+                         {a.scales, a.scales ? nb * 4 : 0}};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    // x and dy with dx on one of them: the other must be clear of it
+    if (a.T > 0 && on_x && on_dy) return AGOQ_ERR_ALIAS;
+    if (a.T == 0) {
+        cudaError_t e = cudaSuccess;
+        if (a.dw) e = cudaMemsetAsync(a.dw, 0, 4ull * a.H, as_stream(stream));
+        if (e == cudaSuccess && a.db) e = cudaMemsetAsync(a.db, 0, 4ull * a.H, as_stream(stream));
+        return from_cuda(e);
+    }
+    return from_cuda(launch_ln_backward(a, as_stream(stream)));
+}
+
+agoq_status agoq_layernorm_backward(const void *x, int64_t ldx, const void *dy, int64_t lddy,
+                                    const void *w, int param_dtype, const float *mean,
+                                    const float *rstd, int64_t T, int64_t H, int dtype, void *dx,
+                                    int64_t lddx, float *dw, float *db, void *workspace,
+                                    int64_t workspace_bytes, void *stream) {
+    agoq::LnBackward a{};
+    a.x = x, a.ldx = ldx, a.dy = dy, a.lddy = lddy, a.w = w;
+    a.param_f32 = param_dtype == AGOQ_F32;
+    a.mean = mean, a.rstd = rstd, a.T = T, a.H = H, a.dtype = dtype, a.dx = dx, a.lddx = lddx;
+    a.dw = dw, a.db = db, a.workspace = static_cast<float *>(workspace);
+    return layernorm_backward_common(a, param_dtype, workspace_bytes, stream);
+}
+
+agoq_status agoq_layernorm_backward_laaq(const void *codes, const float *scales, int bits,
+                                         const void *dy_bf16, int64_t lddy, const void *w,
+                                         int param_dtype, int64_t T, int64_t H, float eps,
+                                         void *dx_bf16, int64_t lddx, float *dw, float *db,
+                                         void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!agoq::bits_ok(bits)) return AGOQ_ERR_BITS;
+    agoq::LnBackward a{};
+    a.x = codes, a.ldx = H, a.scales = scales, a.bits = bits, a.dy = dy_bf16, a.lddy = lddy, a.w = w;
+    a.param_f32 = param_dtype == AGOQ_F32;
+    a.T = T, a.H = H, a.dtype = AGOQ_BF16, a.eps = eps, a.dx = dx_bf16, a.lddx = lddx;
+    a.dw = dw, a.db = db, a.workspace = static_cast<float *>(workspace);
+    return layernorm_backward_common(a, param_dtype, workspace_bytes, stream);
+}
+
+// One tensor of a gradient list; `clip`: its output too.
+static agoq_status grad_tensor_check(const agoq_grad_tensor &t, bool clip) {
+    using namespace agoq;
+    const bool fp8 = t.dtype == AGOQ_E4M3;
+    if (!fp8 && !float_dtype(t.dtype)) return AGOQ_ERR_FORMAT;
+    if (t.n < 0 || t.n > (1ll << 40) || (fp8 && t.n % kBlockElems)) return AGOQ_ERR_SHAPE;
+    if (t.n == 0) return AGOQ_OK;
+    if (!t.data || (fp8 && !t.scales) || (clip && !t.out)) return AGOQ_ERR_NULL;
+    const int es = fp8 ? 4 : elem_size(t.dtype);
+    if (!aligned(t.data, fp8 ? 16 : es) || (fp8 && !aligned(t.scales, 4)) ||
+        (clip && !aligned(t.out, es)))
+        return AGOQ_ERR_ALIGN;
+    if (!clip) return AGOQ_OK;
+    const Range out = fp8 ? vec(t.out, t.n / kBlockElems, 4) : vec(t.out, t.n, es);
+    if (fp8 && overlap(out.p, out.n, t.data, t.n)) return AGOQ_ERR_ALIAS;
+    const void *from = fp8 ? t.scales : t.data;
+    return t.out != from && overlap(out.p, out.n, from, out.n) ? AGOQ_ERR_ALIAS : AGOQ_OK;
+}
+
+static agoq_status grad_list_ok(const agoq_grad_tensor *tensors, int count, bool clip) {
+    if (count < 0) return AGOQ_ERR_SHAPE;
+    if (count > 0 && !tensors) return AGOQ_ERR_NULL;
+    int64_t total = 0;
+    for (int i = 0; i < count; ++i) {
+        const agoq_status s = grad_tensor_check(tensors[i], clip);
+        if (s != AGOQ_OK) return s;
+        total += tensors[i].n;
+        if (total > (1ll << 43)) return AGOQ_ERR_SHAPE;
+    }
+    return AGOQ_OK;
+}
+
+agoq_status agoq_grad_list_check(const agoq_grad_tensor *tensors, int count) {
+    using namespace agoq;
+    const agoq_status s = grad_list_ok(tensors, count, true);
+    if (s != AGOQ_OK) return s;
+    // Every range that is read or written, by address: a written one must not
+    // meet another tensor's range.
+    Span *spans = new (std::nothrow) Span[count > 0 ? 3 * (size_t)count : 1];
+    if (!spans) return AGOQ_ERR_CUDA;
+    size_t m = 0;
+    for (int i = 0; i < count; ++i) {
+        const agoq_grad_tensor &t = tensors[i];
+        if (t.n == 0) continue;
+        const bool fp8 = t.dtype == AGOQ_E4M3;
+        const uintptr_t d = reinterpret_cast<uintptr_t>(t.data),
+                        o = reinterpret_cast<uintptr_t>(t.out),
+                        c = reinterpret_cast<uintptr_t>(t.scales);
+        const uint64_t db = (uint64_t)t.n * (fp8 ? 1 : elem_size(t.dtype));
+        const uint64_t ob = fp8 ? (uint64_t)t.n / kBlockElems * 4 : db;
+        spans[m++] = {d, d + db, i, false};
+        if (fp8) spans[m++] = {c, c + ob, i, false};
+        spans[m++] = {o, o + ob, i, true};
+    }
+    std::sort(spans, spans + m);
+    bool bad = false;
+    for (size_t i = 0; i < m && !bad; ++i)
+        for (size_t j = i + 1; j < m && spans[j].from < spans[i].to && !bad; ++j)
+            bad = (spans[i].out || spans[j].out) && spans[i].tensor != spans[j].tensor;
+    delete[] spans;
+    return bad ? AGOQ_ERR_ALIAS : AGOQ_OK;
+}
+
+int64_t agoq_grad_norm_workspace_bytes(int count) {
+    return count < 0 ? -1 : agoq::grad_norm_workspace_bytes(count);
+}
+
+static agoq_status grad_norm_ok(const agoq_grad_tensor *tensors, int count, bool clip,
+                                const float *norm, const void *workspace,
+                                int64_t workspace_bytes) {
+    using namespace agoq;
+    const agoq_status s = grad_list_ok(tensors, count, clip);
+    if (s != AGOQ_OK) return s;
+    if (!norm || !workspace) return AGOQ_ERR_NULL;
+    if (workspace_bytes < agoq::grad_norm_workspace_bytes(count)) return AGOQ_ERR_SHAPE;
+    if (!aligned(norm, 4) || !aligned(workspace, 16)) return AGOQ_ERR_ALIGN;
+    const Range out[2] = {{norm, 4}, {workspace, (uint64_t)agoq::grad_norm_workspace_bytes(count)}};
+    for (int i = 0; i < count; ++i) {
+        const agoq_grad_tensor &t = tensors[i];
+        const bool fp8 = t.dtype == AGOQ_E4M3;
+        const Range in[3] = {vec(t.data, t.n, elem_size(t.dtype)),
+                             vec(fp8 ? t.scales : nullptr, t.n / kBlockElems, 4),
+                             fp8 ? vec(clip ? t.out : nullptr, t.n / kBlockElems, 4)
+                                 : vec(clip ? t.out : nullptr, t.n, elem_size(t.dtype))};
+        if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    }
+    return AGOQ_OK;
+}
+
+agoq_status agoq_grad_norm(const agoq_grad_tensor *tensors, int count, float *norm,
+                           void *workspace, int64_t workspace_bytes, void *stream) {
+    using namespace agoq;
+    const agoq_status s = grad_norm_ok(tensors, count, false, norm, workspace, workspace_bytes);
+    if (s != AGOQ_OK) return s;
+    return from_cuda(launch_grad_norm(tensors, count, norm, static_cast<double *>(workspace),
+                                      as_stream(stream)));
+}
+
+agoq_status agoq_clip_grads(const agoq_grad_tensor *tensors, int count, float max_norm,
+                            const float *norm, void *stream) {
+    using namespace agoq;
+    const agoq_status s = grad_list_ok(tensors, count, true);
+    if (s != AGOQ_OK) return s;
+    if (!(max_norm >= 0.0f) || max_norm > 3.0e38f) return AGOQ_ERR_SHAPE;
+    if (!norm) return AGOQ_ERR_NULL;
+    if (!aligned(norm, 4)) return AGOQ_ERR_ALIGN;
+    for (int i = 0; i < count; ++i) {
+        const agoq_grad_tensor &t = tensors[i];
+        const bool fp8 = t.dtype == AGOQ_E4M3;
+        if (overlap(norm, 4, t.out, fp8 ? (uint64_t)t.n / kBlockElems * 4
+                                        : (uint64_t)t.n * elem_size(t.dtype)))
+            return AGOQ_ERR_ALIAS;
+    }
+    return from_cuda(launch_clip_grads(tensors, count, max_norm, norm, as_stream(stream)));
+}
+
+agoq_status agoq_clip_grad_norm(const agoq_grad_tensor *tensors, int count, float max_norm,
+                                float *norm, void *workspace, int64_t workspace_bytes,
+                                void *stream) {
+    using namespace agoq;
+    const agoq_status s = grad_norm_ok(tensors, count, true, norm, workspace, workspace_bytes);
+    if (s != AGOQ_OK) return s;
+    if (!(max_norm >= 0.0f) || max_norm > 3.0e38f) return AGOQ_ERR_SHAPE;
+    const cudaError_t e = launch_grad_norm(tensors, count, norm, static_cast<double *>(workspace),
+                                           as_stream(stream));
+    if (e != cudaSuccess) return from_cuda(e);
+    return from_cuda(launch_clip_grads(tensors, count, max_norm, norm, as_stream(stream)));
+}
+
+agoq_status agoq_token_logprobs(const void *logits, int64_t ld, int dtype, const int64_t *tokens,
+                                int64_t T, int64_t V, int k, float *logp, float *entropy,
+                                float *lse, float *top_logp, int64_t *top_ids, void *stream) {
+    using namespace agoq;
+    if (!float_dtype(dtype)) return AGOQ_ERR_FORMAT;
+    if (T < 0 || V < 1 || V > kMaxVocab || !rows_ok(T, V, ld) || k < 0 || k > kMaxTop || k > V)
+        return AGOQ_ERR_SHAPE;
+    if (T == 0) return AGOQ_OK;
+    if (!logits || !tokens || (k > 0 && (!top_logp || !top_ids))) return AGOQ_ERR_NULL;
+    const int es = elem_size(dtype);
+    if (k == 0) top_logp = nullptr, top_ids = nullptr;
+    if (!aligned(logits, es) || !aligned(tokens, 8) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+        !aligned(lse, 4) || !aligned(top_logp, 4) || !aligned(top_ids, 8))
+        return AGOQ_ERR_ALIGN;
+    const Range out[5] = {vec(logp, T, 4), vec(entropy, T, 4), vec(lse, T, 4),
+                          vec(top_logp, T * k, 4), vec(top_ids, T * k, 8)};
+    const Range in[2] = {rows(logits, T, V, ld, es), vec(tokens, T, 8)};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    TokenLogprobs a{};
+    a.logits = logits, a.ld = ld, a.dtype = dtype, a.tokens = tokens, a.T = T, a.V = V, a.k = k;
+    a.logp = logp, a.entropy = entropy, a.lse = lse, a.top_logp = top_logp, a.top_ids = top_ids;
+    return from_cuda(launch_token_logprobs(a, as_stream(stream)));
+}
+
+agoq_status agoq_token_logprobs_backward(const void *logits, int64_t ld, int dtype,
+                                         const int64_t *tokens, int64_t T, int64_t V,
+                                         const float *lse, const float *entropy,
+                                         const float *dlogp, const float *dentropy, void *dlogits,
+                                         int64_t ldd, void *stream) {
+    using namespace agoq;
+    if (!float_dtype(dtype)) return AGOQ_ERR_FORMAT;
+    if (T < 0 || V < 1 || V > kMaxVocab || !rows_ok(T, V, ld) || !rows_ok(T, V, ldd))
+        return AGOQ_ERR_SHAPE;
+    if (T == 0) return AGOQ_OK;
+    if (!logits || !tokens || !lse || !dlogp || !dlogits || (dentropy && !entropy))
+        return AGOQ_ERR_NULL;
+    const int es = elem_size(dtype);
+    if (!aligned(logits, es) || !aligned(tokens, 8) || !aligned(lse, 4) || !aligned(entropy, 4) ||
+        !aligned(dlogp, 4) || !aligned(dentropy, 4) || !aligned(dlogits, es))
+        return AGOQ_ERR_ALIGN;
+    const Range out[1] = {rows(dlogits, T, V, ldd, es)};
+    const bool in_place = logits == dlogits && ld == ldd;
+    const Range lr = rows(logits, in_place ? 0 : T, V, ld, es);
+    const Range in[6] = {lr,
+                         vec(tokens, T, 8), vec(lse, T, 4), vec(entropy, T, 4), vec(dlogp, T, 4),
+                         vec(dentropy, T, 4)};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    const TokenLogprobsBackward a{logits, ld, dtype, tokens, T, V, lse, entropy, dlogp, dentropy,
+                                  dlogits, ldd};
+    return from_cuda(launch_token_logprobs_backward(a, as_stream(stream)));
+}
+
+agoq_status agoq_token_loss(const void *logits, int64_t ld, int dtype, const int64_t *tokens,
+                            const float *weights, int64_t T, int64_t V, float *logp, void *dlogits,
+                            int64_t ldd, void *stream) {
+    using namespace agoq;
+    if (!float_dtype(dtype)) return AGOQ_ERR_FORMAT;
+    if (T < 0 || V < 1 || V > kMaxVocab || !rows_ok(T, V, ld) || !rows_ok(T, V, ldd))
+        return AGOQ_ERR_SHAPE;
+    if (T == 0) return AGOQ_OK;
+    if (!logits || !tokens || !dlogits) return AGOQ_ERR_NULL;
+    const int es = elem_size(dtype);
+    if (!aligned(logits, es) || !aligned(tokens, 8) || !aligned(weights, 4) || !aligned(logp, 4) ||
+        !aligned(dlogits, es))
+        return AGOQ_ERR_ALIGN;
+    const Range out[2] = {rows(dlogits, T, V, ldd, es), vec(logp, T, 4)};
+    const bool in_place = logits == dlogits && ld == ldd;
+    const Range lr = rows(logits, in_place ? 0 : T, V, ld, es);
+    const Range in[3] = {lr,
+                         vec(tokens, T, 8), vec(weights, T, 4)};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    TokenLogprobs a{};
+    a.logits = logits, a.ld = ld, a.dtype = dtype, a.tokens = tokens, a.T = T, a.V = V;
+    a.logp = logp, a.weights = weights, a.dlogits = dlogits, a.ldd = ldd;
+    return from_cuda(launch_token_logprobs(a, as_stream(stream)));
 }
 
 agoq_status agoq_test_wait_timeout(int64_t limit_cycles, void *stream) {

@@ -471,6 +471,47 @@ __device__ __forceinline__ void load_chunk(const uint32_t *rec, int c, uint32_t 
     }
 }
 
+// ---- writing LAAQ records ----------------------------------------------------
+// Write chunk c (8 codes as (lo, hi)) into the block record `rec` (4*BITS
+// words).  Neighbouring lanes hold neighbouring chunks: lane l's chunk is
+// congruent to l modulo 4.  Every lane of the warp must call this (5 and 6 bits
+// shuffle); `valid` gates the stores.
+template <int BITS>
+__device__ __forceinline__ void store_chunk(uint32_t *rec, int c, uint32_t lo, uint32_t hi,
+                                            bool valid) {
+    if constexpr (BITS == 4) {
+        if (valid) rec[c] = lo;
+    } else if constexpr (BITS == 8) {
+        if (valid) reinterpret_cast<uint2 *>(rec)[c] = make_uint2(lo, hi);
+    } else if constexpr (BITS == 5) {
+        // 4 chunks (160 bits) fill 5 words; chunk q of the group starts at bit
+        // 40q.  Word q >= 1 is the top 8q bits of chunk q-1 below the low
+        // 32-8q bits of chunk q, and word 4 is the top 32 bits of chunk 3.
+        // Each lane sends the next one its top 8(q+1) bits (for q = 3 that is
+        // word 4 itself); hi holds only the chunk's bits 32-39.
+        const int q = c & 3;
+        const uint32_t top = __funnelshift_rc(lo, hi, 32 - 8 * q);
+        const uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+        const uint32_t word = (q == 0 ? 0u : prev) | (lo << (8 * q));
+        uint32_t *w = rec + 5 * (c >> 2);
+        if (valid) {
+            w[q] = word;
+            if (q == 3) w[4] = top;
+        }
+    } else {  // BITS == 6: 2 chunks (96 bits) fill 3 words; chunk 1 starts at bit 48
+        const uint32_t phi = __shfl_up_sync(0xFFFFFFFFu, hi, 1);
+        uint32_t *w = rec + 3 * (c >> 1);
+        if (valid) {
+            if ((c & 1) == 0) {
+                w[0] = lo;
+            } else {
+                w[1] = phi | (lo << 16);
+                w[2] = __funnelshift_r(lo, hi, 16);
+            }
+        }
+    }
+}
+
 // The 8 fields of a chunk as biased binary32 words: word i holds
 // 0x4B000000 + (code_i + 2^(BITS-1)), whose value is 2^23 + code_i + 2^(BITS-1)
 // (field_value's bias trick).  4- and 8-bit fields are moved into place by

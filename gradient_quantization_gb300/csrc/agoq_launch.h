@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "../../include/agoq.h"
+
 namespace agoq {
 
 constexpr int kMaxDevices = 64;
@@ -84,6 +86,81 @@ cudaError_t launch_wgrad_accum_fp8(const void *dY, const void *xc, const float *
                                    int K, void *master, float *master_scales, cudaStream_t st);
 cudaError_t launch_fwd_gemm_quant(const void *x, const void *w, int T, int N, int K, int bits,
                                   void *y, void *codes, float *scales, cudaStream_t st);
+// Layer norm (layernorm.cu).  dtype and bits as in include/agoq.h; row
+// distances in elements; optional pointers may be NULL.
+struct LnForward {
+    const void *x;
+    int64_t ldx;
+    const void *w, *b;
+    bool param_f32;          // w and b are FP32, else of the type of x
+    int64_t T, H;
+    int dtype;
+    float eps;
+    void *y;
+    int64_t ldy;
+    float *mean, *rstd;
+    void *codes;             // LAAQ codes of x (BF16, H a multiple of 128), or NULL
+    float *scales;
+    int bits;
+};
+struct LnBackward {
+    const void *x;           // the input [T][ldx], or with bits != 0 its codes
+    int64_t ldx;
+    const float *scales;
+    int bits;
+    const void *dy;
+    int64_t lddy;
+    const void *w;
+    bool param_f32;
+    const float *mean, *rstd;   // of x; not used with codes
+    int64_t T, H;
+    int dtype;
+    float eps;               // used with codes
+    void *dx;
+    int64_t lddx;
+    float *dw, *db;
+    float *workspace;        // ln_workspace_floats(T, H) floats if dw or db is wanted
+};
+constexpr int kLnPartials = 304;
+int ln_partials(int64_t T);
+// Partial rows of dw and db.
+inline int64_t ln_workspace_floats(int64_t T, int64_t H) {
+    return (int64_t)ln_partials(T) * 2 * H;
+}
+cudaError_t launch_ln_forward(const LnForward &a, cudaStream_t st);
+cudaError_t launch_ln_backward(const LnBackward &a, cudaStream_t st);
+// Global gradient norm and clipping (grad_norm.cu).
+int64_t grad_norm_workspace_bytes(int count);
+cudaError_t launch_grad_norm(const agoq_grad_tensor *tensors, int count, float *norm,
+                             double *workspace, cudaStream_t st);
+cudaError_t launch_clip_grads(const agoq_grad_tensor *tensors, int count, float max_norm,
+                              const float *norm, cudaStream_t st);
+// Token log probabilities (token_logprobs.cu); row distances in elements.
+struct TokenLogprobs {
+    const void *logits;
+    int64_t ld;
+    int dtype;
+    const int64_t *tokens;
+    int64_t T, V;
+    int k;
+    float *logp, *entropy, *lse, *top_logp;   // any may be NULL
+    int64_t *top_ids;
+    const float *weights;                     // of the loss, with dlogits
+    void *dlogits;                            // the loss's gradient, or NULL
+    int64_t ldd;
+};
+struct TokenLogprobsBackward {
+    const void *logits;
+    int64_t ld;
+    int dtype;
+    const int64_t *tokens;
+    int64_t T, V;
+    const float *lse, *entropy, *dlogp, *dentropy;
+    void *dlogits;
+    int64_t ldd;
+};
+cudaError_t launch_token_logprobs(const TokenLogprobs &a, cudaStream_t st);
+cudaError_t launch_token_logprobs_backward(const TokenLogprobsBackward &a, cudaStream_t st);
 // A kernel whose one pipeline wait runs out after `limit_cycles` (failure-path test).
 cudaError_t launch_wait_timeout_probe(long long limit_cycles, cudaStream_t st);
 // Read and clear the forward GEMM's status word (call after synchronising).

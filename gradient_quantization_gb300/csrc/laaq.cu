@@ -48,46 +48,6 @@ __device__ __forceinline__ void st_stream(uint4 *p, uint4 v) {
                  : "memory");
 }
 
-// Write one 8-code chunk set into the block record `rec` (4*BITS words):
-// lane j of the octet holds chunk (j + 8*set) as (lo, hi).  Every lane of the
-// warp must call this (5 and 6 bits shuffle); `valid` gates the stores.
-template <int BITS>
-__device__ __forceinline__ void store_chunk_set(uint32_t *rec, int j, int set, uint32_t lo,
-                                                uint32_t hi, bool valid) {
-    const int c = j + 8 * set;                              // chunk index in the block
-    if constexpr (BITS == 4) {
-        if (valid) rec[c] = lo;
-    } else if constexpr (BITS == 8) {
-        if (valid) reinterpret_cast<uint2 *>(rec)[c] = make_uint2(lo, hi);
-    } else if constexpr (BITS == 5) {
-        // 4 chunks (160 bits) fill 5 words; chunk q of the group starts at bit
-        // 40q.  Word q >= 1 is the top 8q bits of chunk q-1 below the low
-        // 32-8q bits of chunk q, and word 4 is the top 32 bits of chunk 3.
-        // Each lane sends the next one its top 8(q+1) bits (for q = 3 that is
-        // word 4 itself); hi holds only the chunk's bits 32-39.
-        const int q = c & 3;
-        const uint32_t top = __funnelshift_rc(lo, hi, 32 - 8 * q);
-        const uint32_t prev = __shfl_up_sync(kFull, top, 1);
-        const uint32_t word = (q == 0 ? 0u : prev) | (lo << (8 * q));
-        uint32_t *w = rec + 5 * (c >> 2);
-        if (valid) {
-            w[q] = word;
-            if (q == 3) w[4] = top;
-        }
-    } else {  // BITS == 6: 2 chunks (96 bits) fill 3 words; chunk 1 starts at bit 48
-        const uint32_t phi = __shfl_up_sync(kFull, hi, 1);
-        uint32_t *w = rec + 3 * (c >> 1);
-        if (valid) {
-            if ((c & 1) == 0) {
-                w[0] = lo;
-            } else {
-                w[1] = phi | (lo << 16);
-                w[2] = __funnelshift_r(lo, hi, 16);
-            }
-        }
-    }
-}
-
 // A block is owned by an octet of lanes; lane j holds elements 8j..8j+7
 // (chunk j) and 64+8j..64+8j+7 (chunk j+8), so each 16-byte load instruction
 // of a warp reads 4 x 128 contiguous bytes and the per-block work (absmax
@@ -174,10 +134,10 @@ laaq_quant_kernel(const uint4 *__restrict__ x, uint32_t *__restrict__ codes,
             uint32_t *rec = codes + (size_t)(unsigned)blk * kWords;
             if constexpr (kBiased) pack_biased8<BITS>(cb[u], lo, hi);
             else pack_fields8<BITS>(cb[u], lo, hi);
-            store_chunk_set<BITS>(rec, j, 0, lo, hi, valid);
+            store_chunk<BITS>(rec, j, lo, hi, valid);
             if constexpr (kBiased) pack_biased8<BITS>(cb[u] + 8, lo, hi);
             else pack_fields8<BITS>(cb[u] + 8, lo, hi);
-            store_chunk_set<BITS>(rec, j, 1, lo, hi, valid);
+            store_chunk<BITS>(rec, j + 8, lo, hi, valid);
             if (valid && j == 0) scales[blk] = s[u];
         }
 #pragma unroll

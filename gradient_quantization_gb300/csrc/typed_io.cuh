@@ -1,0 +1,139 @@
+// typed_io.cuh -- element types of the operators that accept FP32, BF16 and
+// FP16 tensors: loads and stores of single elements and of 16-byte vectors,
+// with all arithmetic in binary32.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "agoq_device.cuh"
+
+namespace agoq {
+
+// Values of agoq_dtype (include/agoq.h).
+constexpr int kF32 = 0, kBF16 = 1, kF16 = 2, kE4M3 = 3;
+
+// Type DT: its storage word, its size, and the elements of a 16-byte vector.
+template <int DT>
+struct Elem;
+
+template <>
+struct Elem<kF32> {
+    using Word = float;
+    static constexpr int kSize = 4, kVec = 4;
+    __device__ static __forceinline__ float up(Word v) { return v; }
+    __device__ static __forceinline__ Word down(float v) { return v; }
+    __device__ static __forceinline__ void unpack(const uint4 &v, float *f) {
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z);
+        f[3] = __uint_as_float(v.w);
+    }
+    __device__ static __forceinline__ uint4 pack(const float *f) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
+    }
+};
+
+template <>
+struct Elem<kBF16> {
+    using Word = uint16_t;
+    static constexpr int kSize = 2, kVec = 8;
+    __device__ static __forceinline__ float up(Word v) { return __uint_as_float((uint32_t)v << 16); }
+    __device__ static __forceinline__ Word down(float v) { return (Word)pack_bf16x2(v, 0.0f); }
+    __device__ static __forceinline__ void unpack(const uint4 &v, float *f) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16_lo(w[i]);
+            f[2 * i + 1] = bf16_hi(w[i]);
+        }
+    }
+    __device__ static __forceinline__ uint4 pack(const float *f) {
+        return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                          pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    }
+};
+
+template <>
+struct Elem<kF16> {
+    using Word = uint16_t;
+    static constexpr int kSize = 2, kVec = 8;
+    __device__ static __forceinline__ float up(Word v) {
+        return __half2float(__ushort_as_half(v));
+    }
+    __device__ static __forceinline__ Word down(float v) {
+        return __half_as_ushort(__float2half_rn(v));
+    }
+    __device__ static __forceinline__ void unpack(const uint4 &v, float *f) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = up((Word)w[i]);
+            f[2 * i + 1] = up((Word)(w[i] >> 16));
+        }
+    }
+    __device__ static __forceinline__ uint32_t pair(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    __device__ static __forceinline__ uint4 pack(const float *f) {
+        return make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
+    }
+};
+
+// Element i of a tensor of type DT, as binary32.
+template <int DT>
+__device__ __forceinline__ float load_elem(const void *p, int64_t i) {
+    return Elem<DT>::up(__ldg(static_cast<const typename Elem<DT>::Word *>(p) + i));
+}
+
+// The same where the kernel may also write the element (in-place calls): an
+// ordinary load, not through the read-only path.
+template <int DT>
+__device__ __forceinline__ float load_now(const void *p, int64_t i) {
+    return Elem<DT>::up(static_cast<const typename Elem<DT>::Word *>(p)[i]);
+}
+
+// Element i of a tensor of type DT, set to v rounded to nearest even.
+template <int DT>
+__device__ __forceinline__ void store_elem(void *p, int64_t i, float v) {
+    static_cast<typename Elem<DT>::Word *>(p)[i] = Elem<DT>::down(v);
+}
+
+// Byte address of element i.
+template <int DT>
+__device__ __forceinline__ const char *elem_at(const void *p, int64_t i) {
+    return static_cast<const char *>(p) + i * Elem<DT>::kSize;
+}
+template <int DT>
+__device__ __forceinline__ char *elem_at(void *p, int64_t i) {
+    return static_cast<char *>(p) + i * Elem<DT>::kSize;
+}
+
+// Sum over a warp (every lane gets it), in the order of the butterfly.
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+// Sum over a CTA of WARPS warps; every thread gets it.  `red` holds WARPS
+// floats and may be reused after the next __syncthreads().
+template <int WARPS>
+__device__ __forceinline__ float cta_sum(float v, float *red) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) s = __fadd_rn(s, red[i]);
+    return s;
+}
+
+}  // namespace agoq

@@ -56,7 +56,8 @@ typedef enum {
     AGOQ_ERR_ALIAS = 5,   /* an output overlaps an input */
     AGOQ_ERR_CUDA = 6,    /* the CUDA runtime reported an error at launch */
     AGOQ_ERR_TIMEOUT = 7, /* a pipeline wait gave up (see agoq_device_status) */
-    AGOQ_ERR_FORMAT = 8   /* unsupported intermediate format (agoq_grad_accum_fp8_mid) */
+    AGOQ_ERR_FORMAT = 8   /* unsupported intermediate format (agoq_grad_accum_fp8_mid) or
+                             element type (agoq_dtype) */
 } agoq_status;
 
 /* Intermediate formats of the QuanGrad accumulation (agoq_grad_accum_fp8_mid). */
@@ -65,6 +66,15 @@ typedef enum {
     AGOQ_MID_BF16 = 1,
     AGOQ_MID_FP16 = 2
 } agoq_mid_format;
+
+/* Element types of the calls that take one (AGOQ_ERR_FORMAT for any other
+ * value, and where a call does not support the type). */
+typedef enum {
+    AGOQ_F32 = 0,
+    AGOQ_BF16 = 1,
+    AGOQ_F16 = 2,
+    AGOQ_E4M3 = 3   /* an FP8 gradient with block scales (agoq_grad_tensor only) */
+} agoq_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *agoq_status_string(agoq_status status);
@@ -350,6 +360,199 @@ agoq_status agoq_fwd_gemm_quant(const void *x_bf16, const void *w_bf16, int T, i
  * width outside {4, 5, 6, 8}.
  */
 agoq_status agoq_dbca_pp_bits(int stages, int microbatches, int base_bits, int *bits);
+
+/*
+ * Layer norm, forward.  Per row of x [T][H], in binary32 (the variance from the
+ * differences to the mean, not from the sum of squares):
+ *   mu = sum_i x[i] / H;  r = 1 / sqrt(sum_i (x[i] - mu)^2 / H + eps);
+ *   y[i] = R(((x[i] - mu) * r) * w[i] + b[i]),  R rounding to the type of y.
+ * With `codes` the same call also writes the LAAQ codes of x (exactly
+ * agoq_quant_act(x, T*H, bits)): the low-bit input that a training step keeps
+ * for agoq_layernorm_backward_laaq instead of x (AGoQ section 2.A,
+ * "Herberekening versus Caching").
+ *   x      : in, [T] rows of H elements of `dtype` (AGOQ_F32, AGOQ_BF16 or
+ *            AGOQ_F16), row t at x + t * ldx, ldx >= H.
+ *   w, b   : in, [H] weight and bias of `param_dtype` (AGOQ_F32, or `dtype`), or
+ *            NULL: no weight (1), no bias (0).
+ *   y      : out, rows of the type of x, ldy >= H elements apart.
+ *   mean, rstd : out, FP32 [T] (mu and r), or NULL to skip either.
+ *   codes, scales, bits : out, as agoq_quant_act writes them (codes 16-byte
+ *            aligned; then x must be BF16 and H a multiple of 128), or both NULL.
+ * 1 <= H <= 2^24; T may be 0.  x, w, b and y need the alignment of their
+ * elements only; rows whose addresses are all 16-byte aligned move in 16-byte
+ * accesses, others element by element (slower, the same values).  y must not
+ * overlap x except in place (the same address and row distance; not with codes
+ * being anywhere else than outside of both); the outputs must not overlap one
+ * another.  A row with a NaN or an infinity is NaN throughout.
+ */
+agoq_status agoq_layernorm_forward(const void *x, int64_t ldx, const void *w, const void *b,
+                                   int param_dtype, int64_t T, int64_t H, int dtype, float eps,
+                                   void *y, int64_t ldy, float *mean, float *rstd, void *codes,
+                                   float *scales, int bits, void *stream);
+
+/*
+ * Bytes of scratch the layer norm's backward calls need for dw or db of a [T][H]
+ * input (partial rows of both, at most 304: the same for every T beyond that), -1
+ * for sizes they do not take.
+ */
+int64_t agoq_layernorm_backward_workspace_bytes(int64_t T, int64_t H);
+
+/*
+ * Layer norm, backward, from the input and the statistics of the forward call.
+ * With xh[i] = (x[i] - mean[t]) * rstd[t] and g[i] = dy[i] * w[i], in binary32:
+ *   dx[i] = R(rstd[t] * (g[i] - sum_j g[j] / H - xh[i] * sum_j g[j] xh[j] / H))
+ *   dw[i] = sum_t dy[t][i] * xh[t][i],   db[i] = sum_t dy[t][i].
+ *   x, dy  : in, rows of `dtype`, ldx and lddy elements apart.
+ *   w      : in, [H] of `param_dtype`, or NULL (1).
+ *   mean, rstd : in, FP32 [T].
+ *   dx     : out, rows of `dtype`, lddx elements apart; in place of dy or x is allowed
+ *            (the same address and row distance).
+ *   dw, db : out, FP32 [H] (set, not accumulated), or NULL to skip either.
+ *   workspace, workspace_bytes : caller-owned scratch, 16-byte aligned, at least
+ *            agoq_layernorm_backward_workspace_bytes(T, H) bytes, needed when dw or
+ *            db is wanted (else it may be NULL); contents on entry are ignored.
+ *            Calls that share one must not overlap in time on the GPU.
+ * T == 0 sets dw and db to 0.  Sums are formed in a fixed order (no atomics):
+ * results are deterministic on a given GPU model.  Sizes and alignment as the
+ * forward call.
+ */
+agoq_status agoq_layernorm_backward(const void *x, int64_t ldx, const void *dy, int64_t lddy,
+                                    const void *w, int param_dtype, const float *mean,
+                                    const float *rstd, int64_t T, int64_t H, int dtype, void *dx,
+                                    int64_t lddx, float *dw, float *db, void *workspace,
+                                    int64_t workspace_bytes, void *stream);
+
+/*
+ * The same backward from the stored low-bit input (AGoQ section 2.A,
+ * "Herberekening versus Caching"): x is the dequantization of the codes
+ * (exactly agoq_dequant_act), and mean and rstd are recomputed from it.
+ *   codes, scales, bits : in, of the contiguous [T][H] input, H a multiple of 128.
+ *   dy, dx : BF16 rows, lddy and lddx elements apart.
+ * The scratch is needed in every case where dw or db is wanted.  Other
+ * arguments, rules and errors as agoq_layernorm_backward.
+ */
+agoq_status agoq_layernorm_backward_laaq(const void *codes, const float *scales, int bits,
+                                         const void *dy_bf16, int64_t lddy, const void *w,
+                                         int param_dtype, int64_t T, int64_t H, float eps,
+                                         void *dx_bf16, int64_t lddx, float *dw, float *db,
+                                         void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * One gradient of the list that agoq_grad_norm and the clipping calls take.
+ * The list itself is HOST memory, read during the call.
+ */
+typedef struct {
+    void *data;      /* n values of `dtype`; AGOQ_E4M3: n codes (16-byte aligned) */
+    float *scales;   /* AGOQ_E4M3: the n/128 block scales; else NULL */
+    void *out;       /* where the clipped gradient goes: `data` itself (in place), or n values of
+                        `dtype` elsewhere.  AGOQ_E4M3: the n/128 clipped scales, `scales` itself
+                        or elsewhere (the codes do not change).  agoq_grad_norm ignores it. */
+    int64_t n;       /* number of elements, 0 .. 2^40; a multiple of 128 for AGOQ_E4M3 */
+    int32_t dtype;   /* agoq_dtype */
+    int32_t reserved;   /* 0 */
+} agoq_grad_tensor;
+
+/* Bytes of scratch agoq_grad_norm needs for a list of `count` tensors (-1: count < 0). */
+int64_t agoq_grad_norm_workspace_bytes(int count);
+
+/*
+ * Whether the outputs of a list may be written: AGOQ_ERR_ALIAS if a tensor's
+ * `out` overlaps the `data`, `scales` or `out` of another, or its own otherwise
+ * than in place; else the errors of agoq_clip_grads.  Host-side, no GPU work: a
+ * program calls it once for the list that it keeps.
+ */
+agoq_status agoq_grad_list_check(const agoq_grad_tensor *tensors, int count);
+
+/*
+ * The global L2 norm of a list of gradients:
+ *   *norm = fl32(sqrt(sum over all tensors and elements of g^2)),
+ * g = fl32(e4m3(c_i) * scale) for AGOQ_E4M3.  Squares are summed in binary32 over
+ * at most 128 elements and in binary64 beyond; values whose squares leave the
+ * binary32 range are squared in binary64, so neither large nor tiny gradients
+ * are lost.  A NaN or an infinity anywhere makes the norm NaN or infinite.
+ *   tensors, count : the list (host memory), count >= 0.
+ *   norm      : out, one FP32 (device).
+ *   workspace : device scratch, 16-byte aligned, of at least
+ *               agoq_grad_norm_workspace_bytes(count) bytes; contents ignored.
+ * FP32, BF16 and FP16 tensors need the alignment of their elements; 16-byte
+ * aligned ones move in 16-byte accesses.  The order of the sums is fixed: results
+ * are deterministic on a given GPU model.
+ */
+agoq_status agoq_grad_norm(const agoq_grad_tensor *tensors, int count, float *norm,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Clipping by a norm already on the device (a rank that holds a shard of the
+ * gradients adds the squares of all ranks' norms first):
+ *   c = min(1, fl32(max_norm / fl32(*norm + 1e-6))), NaN if *norm is NaN;
+ *   out_i = R(fl32(g_i * c)); AGOQ_E4M3: out scale = fl32(scale * c).
+ * Where c is 1, tensors in place are not touched.  max_norm must be finite and
+ * >= 0 (AGOQ_ERR_SHAPE).  Overlaps between tensors are not checked here: see
+ * agoq_grad_list_check.
+ */
+agoq_status agoq_clip_grads(const agoq_grad_tensor *tensors, int count, float max_norm,
+                            const float *norm, void *stream);
+
+/* agoq_grad_norm followed by agoq_clip_grads with the norm it found. */
+agoq_status agoq_clip_grad_norm(const agoq_grad_tensor *tensors, int count, float max_norm,
+                                float *norm, void *workspace, int64_t workspace_bytes,
+                                void *stream);
+
+/*
+ * Log probabilities of given tokens, with the entropy of each row and its k most
+ * likely alternatives.  Per row x of logits [T][V], in binary32:
+ *   m = max x;  S = sum_i e^(x_i - m);  lse = m + ln S;
+ *   logp = x[token] - lse;  entropy = ln S - sum_i (x_i - m) e^(x_i - m) / S;
+ *   alternatives: the k largest logits by (value descending, index ascending),
+ *   their log probabilities x - lse and their indices.
+ *   logits  : in, rows of `dtype` (AGOQ_F32, AGOQ_BF16, AGOQ_F16), ld >= V elements apart.
+ *   tokens  : in, int64 [T].  A negative token is ignored: its logp is 0.  A token
+ *             >= V gives NaN.
+ *   k       : 0 .. min(32, V).
+ *   logp, entropy, lse : out, FP32 [T]; any may be NULL.
+ *   top_logp, top_ids  : out, FP32 and int64 [T][k]; not used for k = 0.
+ * A logit of -inf has probability 0 (log probability -inf).  A row of nothing
+ * but -inf has lse = -inf, logp = -inf (0 if ignored), entropy 0, and the lowest
+ * indices as alternatives.  A row with a NaN or +inf has NaN statistics;
+ * NaN comes first among its alternatives.  1 <= V <= 2^30.  Logits need the
+ * alignment of their elements only.  Outputs must not overlap the inputs or one
+ * another.
+ */
+agoq_status agoq_token_logprobs(const void *logits, int64_t ld, int dtype, const int64_t *tokens,
+                                int64_t T, int64_t V, int k, float *logp, float *entropy,
+                                float *lse, float *top_logp, int64_t *top_ids, void *stream);
+
+/*
+ * Their gradient: with l_i = x_i - lse and p_i = e^l_i, in binary32,
+ *   dlogits_i = R(dlogp ([i = token] - p_i) - dentropy p_i (l_i + entropy)).
+ *   lse, entropy      : in, FP32 [T], as agoq_token_logprobs gives them.
+ *   dlogp, dentropy   : in, FP32 [T]; dentropy NULL (then entropy may be): 0.
+ *   dlogits : out, rows of `dtype`, ldd >= V elements apart; in place of the logits
+ *             is allowed (the same address and row distance).
+ * The dlogp of an ignored token counts as 0, a token >= V gives a row of NaN, and
+ * a row whose lse is -inf a row of 0.
+ */
+agoq_status agoq_token_logprobs_backward(const void *logits, int64_t ld, int dtype,
+                                         const int64_t *tokens, int64_t T, int64_t V,
+                                         const float *lse, const float *entropy,
+                                         const float *dlogp, const float *dentropy, void *dlogits,
+                                         int64_t ldd, void *stream);
+
+/*
+ * The loss of given tokens and its gradient, reading the logits once where a row
+ * fits on chip: logp as agoq_token_logprobs (the loss of row t is
+ * -weights[t] * logp[t]), and
+ *   dlogits_i = R(weights[t] * (p_i - [i = token])),  p_i = e^(x_i - m) / S.
+ *   weights : in, FP32 [T], or NULL: 1.
+ *   logp    : out, FP32 [T], or NULL.
+ *   dlogits : out, rows of `dtype`, ldd >= V elements apart; in place of the logits
+ *             is allowed (the same address and row distance).
+ * Ignored tokens and rows of nothing but -inf get a gradient of 0, a token >= V a
+ * row of NaN.  Other rules as agoq_token_logprobs.
+ */
+agoq_status agoq_token_loss(const void *logits, int64_t ld, int dtype, const int64_t *tokens,
+                            const float *weights, int64_t T, int64_t V, float *logp, void *dlogits,
+                            int64_t ldd, void *stream);
 
 /*
  * Synchronise `stream`, then read and clear the library's device-side status
