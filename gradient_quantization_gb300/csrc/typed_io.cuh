@@ -82,6 +82,49 @@ struct Elem<kF16> {
     }
 };
 
+// Larger of two vectors' elements, each pair on its own (NaN loses).
+template <int DT>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (DT == kF32) {
+        r = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    } else if constexpr (DT == kBF16) {
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    } else {
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    }
+    return r;
+}
+
+// Largest value of a word (one FP32 or two 16-bit values).
+template <int DT>
+__device__ __forceinline__ float word_max(uint32_t w) {
+    if constexpr (DT == kF32) return __uint_as_float(w);
+    else return fmaxf(Elem<DT>::up((uint16_t)w), Elem<DT>::up((uint16_t)(w >> 16)));
+}
+
+// -infinity in every element of a word.
+template <int DT>
+constexpr uint32_t kNegInfWord = DT == kF32 ? 0xFF800000u : DT == kBF16 ? 0xFF80FF80u : 0xFC00FC00u;
+
+// The 16 bytes from byte `shift` (0, 2, .. 14) on of the 32 bytes (a, b).
+__device__ __forceinline__ uint4 bytes_from(const uint4 &a, const uint4 &b, int shift) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (shift & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (shift & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (shift & 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Element i of a tensor of type DT, as binary32.
 template <int DT>
 __device__ __forceinline__ float load_elem(const void *p, int64_t i) {
