@@ -49,13 +49,12 @@ __device__ __forceinline__ float below_max(float x, float m) {
     return d;
 }
 
-// Rows too long for a cluster's shared memory: a CTA a row, every pass reading
-// the logits again, the alternatives one by one.
+// The loss of rows too long for a cluster's shared memory: a CTA a row, every pass
+// reading the logits again.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenLogprobs a) {
+__global__ void __launch_bounds__(kThreads) token_loss_long_kernel(const TokenLogprobs a) {
     pdl_wait_and_release();
-    __shared__ float red[3][kWarps];
-    __shared__ unsigned long long best;
+    __shared__ float red[2][kWarps];
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const char *row = elem_at<DT>(a.logits, t * a.ld);
         const int64_t token = a.tokens[t];
@@ -64,103 +63,39 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const TokenLog
         for (int64_t i = threadIdx.x; i < a.V; i += kThreads) m = fmaxf(m, load_now<DT>(row, i));
         m = cta_max(m, red[0]);
         if (m == -INFINITY) m = 0.0f;
-        float s = 0.0f, u = 0.0f;
+        float s = 0.0f;
+        for (int64_t i = threadIdx.x; i < a.V; i += kThreads)
+            s = __fadd_rn(s, expf(__fsub_rn(load_now<DT>(row, i), m)));
+        s = cta_sum<kWarps>(s, red[1]);
+        const bool ignored = token < 0, beyond = token >= a.V, empty = s == 0.0f;
+        if (threadIdx.x == 0 && a.logp) {
+            const float lp = at == -INFINITY ? at : __fsub_rn(__fsub_rn(at, m), logf(s));
+            a.logp[t] = ignored ? 0.0f : beyond ? NAN : lp;
+        }
+        float w = a.weights ? a.weights[t] : 1.0f;
+        if (ignored || empty) w = 0.0f;
+        if (beyond) w = NAN;
+        char *out = elem_at<DT>(a.dlogits, t * a.ldd);
         for (int64_t i = threadIdx.x; i < a.V; i += kThreads) {
             const float x = load_now<DT>(row, i);
-            const float d = below_max(x, m), e = expf(d);
-            s = __fadd_rn(s, e);
-            u = __fmaf_rn(d, e, u);
-        }
-        s = cta_sum<kWarps>(s, red[1]);
-        u = cta_sum<kWarps>(u, red[2]);
-        const float ls = logf(s);
-        const bool ignored = token < 0, beyond = token >= a.V, empty = s == 0.0f;
-        if (threadIdx.x == 0) {
-            float lp = at == -INFINITY ? at : __fsub_rn(__fsub_rn(at, m), ls);
-            if (ignored) lp = 0.0f;
-            if (beyond) lp = NAN;
-            if (a.logp) a.logp[t] = lp;
-            if (a.entropy) a.entropy[t] = empty ? 0.0f : __fsub_rn(ls, __fdiv_rn(u, s));
-            if (a.lse) a.lse[t] = __fadd_rn(m, ls);
-        }
-        uint64_t last = ~0ull;
-        for (int j = 0; j < a.k; ++j) {
-            uint64_t b = 0;
-            for (int64_t i = threadIdx.x; i < a.V; i += kThreads) {
-                const uint64_t k = order_key(load_now<DT>(row, i), (uint32_t)i);
-                if (k < last && k > b) b = k;
+            float g = 0.0f;
+            if (w != 0.0f) {
+                g = __fdiv_rn(expf(__fsub_rn(x, m)), s);
+                g = __fmul_rn(w, i == token ? __fsub_rn(g, 1.0f) : g);
             }
-            if (threadIdx.x == 0) best = 0;
-            __syncthreads();
-            atomicMax(&best, b);
-            __syncthreads();
-            last = best;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                const uint32_t i = 0xFFFFFFFFu - (uint32_t)last;
-                const float x = load_now<DT>(row, i);
-                a.top_ids[t * a.k + j] = i;
-                a.top_logp[t * a.k + j] =
-                    x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, m), ls);
-            }
-        }
-        if (a.dlogits) {
-            float w = a.weights ? a.weights[t] : 1.0f;
-            if (ignored || empty) w = 0.0f;
-            if (beyond) w = NAN;
-            char *out = elem_at<DT>(a.dlogits, t * a.ldd);
-            for (int64_t i = threadIdx.x; i < a.V; i += kThreads) {
-                const float x = load_now<DT>(row, i);
-                float g = 0.0f;
-                if (w != 0.0f) {
-                    g = __fdiv_rn(expf(__fsub_rn(x, m)), s);
-                    g = __fmul_rn(w, i == token ? __fsub_rn(g, 1.0f) : g);
-                }
-                store_elem<DT>(out, i, g);
-            }
+            store_elem<DT>(out, i, g);
         }
         __syncthreads();
     }
 }
 
-// ---- rows held on chip ----------------------------------------------------------
+// ---- one pass over a row --------------------------------------------------------
 //
-// A cluster of C CTAs takes a row; each CTA copies its slice of the row into
-// shared memory once and makes every pass over it there: the maximum, the sums
-// and the candidates for the alternatives, and the gradient.  The slices are cut
-// at the 16-byte boundaries of memory, so a row may start anywhere; the up to two
-// vectors that the row fills only in part are padded with -inf.  CTAs work with
-// their slice's maximum; the C maxima and sums meet once, through distributed
-// shared memory.
-//
-// Alternatives: a slice's vectors fall into 64 groups by the thread that holds
-// them.  The k-th largest of the groups' maxima is a bound that at least k
-// elements reach and, when large logits are not all in few groups, few others: about
-// 1.2 k for k = 20.  The elements above it and those equal to it are collected in
-// two lists and ranked by counting.  Too many equal ones (masks, constant rows):
-// the first of them are found in order.  Too many above it, or NaN: the k largest
-// are found one by one.
-constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
-constexpr int kGroups = 64, kGroupLanes = kRowThreads / kGroups;
-constexpr int kTopMax = 32;
-constexpr int kList = 256;                    // entries of a candidate list
-constexpr int kMaxCluster = 8;
-constexpr int kSliceBytes = 70 * 1024;        // three CTAs an SM
-constexpr int kMaxSliceBytes = 212 * 1024;    // one CTA an SM
-static_assert(kTopMax <= kGroups && kMaxCluster * kTopMax <= kList, "lists hold what they must");
-
-struct RowShared {
-    float red[2][kRowWarps];
-    float groups[kGroups];
-    float bound;                  // the k-th largest of the groups' maxima
-    int above, equal;             // entries of the lists (may exceed kList)
-    float max, sum, first;        // of the slice: m, sum e^(x-m), sum (x-m) e^(x-m)
-    float token;                  // the token's logit, in the CTA that holds it
-    float all[3];                 // of the row: m, sum, first
-    unsigned long long best;
-    unsigned long long top[kTopMax];
-    unsigned long long list[2][kList];
-};
+// A thread adds e^(x - ref) and (x - ref) e^(x - ref) with a reference of its own:
+// a vector whose largest element exceeds it by more than 8 raises it (rare after
+// the first vectors), so there is no pass for the maximum, and the exponentials of
+// the largest elements stay below e^8.  References and sums of the threads, warps and
+// CTAs of a row are joined at its end.
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float r;
@@ -170,13 +105,184 @@ __device__ __forceinline__ float exp2_approx(float x) {
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp_approx(float x) { return exp2_approx(__fmul_rn(x, kLog2e)); }
 
-__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+constexpr float kLowest = -3.402823466e38f;   // reference of a thread that has seen nothing
+
+// x moved from reference `from` to `to` >= from: the factor of the sums.  A factor
+// of 0 keeps NaN sums and makes all others 0.
+struct Sums {
+    float ref, sum, first;
+    __device__ __forceinline__ void move(float to) {
+        const float d = __fsub_rn(ref, to), f = exp_approx(d);
+        first = __fmul_rn(f, f == 0.0f ? first : __fmaf_rn(d, sum, first));
+        sum = __fmul_rn(f, sum);
+        ref = to;
+    }
+};
+
+// The sums of a warp's lanes (every lane gets them).
+__device__ __forceinline__ Sums warp_join(Sums s) {
+    s.move(warp_max(s.ref));
+    s.sum = warp_sum(s.sum);
+    s.first = warp_sum(s.first);
+    return s;
 }
-template <int N>
-__device__ __forceinline__ void copies_left() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+
+// ENTROPY: with the sums of (x - ref) e^(x - ref).
+template <int DT, bool ENTROPY>
+struct Online {
+    float ref = kLowest;
+    uint64_t sum2 = 0, first2 = 0;
+    uint32_t low = 0;      // 16-bit types, ref > kLowRef: a pair far below ref
+
+    // The sums of (x - ref) e^(x - ref) must not see x = -inf; where the exponential
+    // is 0 anyway, 16-bit types raise x to `low` two at a time: -1000 below a
+    // positive reference, the lowest finite value below one in (kLowRef, 0], which
+    // is still more than 500 above it.
+    static constexpr float kLowRef = DT == kF16 ? -65000.0f : -1e38f;
+    __device__ __forceinline__ void raise(float to) {
+        Sums s{ref, __fadd_rn(lo_f32(sum2), hi_f32(sum2)),
+               __fadd_rn(lo_f32(first2), hi_f32(first2))};
+        s.move(to);
+        ref = to;
+        sum2 = f32x2(s.sum, 0.0f);
+        first2 = f32x2(s.first, 0.0f);
+        if constexpr (ENTROPY && DT == kBF16) low = to > 0.0f ? 0xC47AC47Au : 0xFF7FFF7Fu;
+        if constexpr (ENTROPY && DT == kF16) low = to > 0.0f ? 0xE3D0E3D0u : 0xFBFFFBFFu;
+    }
+
+    // Add a vector whose largest element is `most`.
+    __device__ __forceinline__ void add(uint4 v, float most) {
+        constexpr int N = Elem<DT>::kVec;
+        if (most > __fadd_rn(ref, 8.0f)) raise(most);
+        bool each = ENTROPY && DT == kF32;     // (x - ref) bounded one by one
+        if constexpr (ENTROPY && DT != kF32) {
+            each = !(ref > kLowRef);
+            if (!each) {
+                v.x = raised(v.x);
+                v.y = raised(v.y);
+                v.z = raised(v.z);
+                v.w = raised(v.w);
+            }
+        }
+        float f[N];
+        Elem<DT>::unpack(v, f);
+        const uint64_t r2 = f32x2(ref, ref), l2 = f32x2(kLog2e, kLog2e);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            uint64_t d = sub_f32x2(f32x2(f[i], f[i + 1]), r2);
+            if (each) {
+                float lo = lo_f32(d), hi = hi_f32(d);
+                asm("max.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(-1000.0f));
+                asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(-1000.0f));
+                d = f32x2(lo, hi);
+            }
+            const uint64_t x = mul_f32x2(d, l2);
+            const uint64_t e = f32x2(exp2_approx(lo_f32(x)), exp2_approx(hi_f32(x)));
+            sum2 = add_f32x2(sum2, e);
+            if constexpr (ENTROPY) first2 = fma_f32x2(d, e, first2);
+        }
+    }
+
+    __device__ __forceinline__ uint32_t raised(uint32_t w) const {
+        uint32_t r;
+        if constexpr (DT == kBF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(low));
+        else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(low));
+        return r;
+    }
+
+    __device__ __forceinline__ Sums sums() const {
+        return {ref, __fadd_rn(lo_f32(sum2), hi_f32(sum2)),
+                __fadd_rn(lo_f32(first2), hi_f32(first2))};
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t vec_max(const uint4 &v) {
+    return max_word<DT>(max_word<DT>(v.x, v.y), max_word<DT>(v.z, v.w));
 }
+
+// A CTA's slice of a row, cut at the 16-byte boundaries of memory: n vectors, of
+// which the row's first and last may be filled in part only.
+template <int DT>
+struct Slice {
+    using E = Elem<DT>;
+    const char *row;
+    int64_t V;
+    int64_t start;                // element of the first vector's first lane (may be negative)
+    int n;
+    __device__ __forceinline__ Slice(const char *row_, int64_t V_, int C, int rank)
+        : row(row_), V(V_) {
+        const int skip = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / E::kSize;
+        const int64_t vectors = (V + skip + E::kVec - 1) / E::kVec;
+        const int64_t per = (vectors + C - 1) / C, left = vectors - rank * per;
+        n = (int)(left < 0 ? 0 : left < per ? left : per);
+        start = rank * per * E::kVec - skip;
+    }
+    __device__ __forceinline__ int64_t at(int j) const { return start + (int64_t)j * E::kVec; }
+    __device__ __forceinline__ bool whole(int j) const { return at(j) >= 0 && at(j) + E::kVec <= V; }
+    __device__ __forceinline__ bool has(int64_t e) const {
+        return e >= 0 && e < V && e >= start && e < at(n);
+    }
+    // Vector j with -inf where the row has no element.
+    __device__ __forceinline__ uint4 part(int j) const {
+        typename E::Word w[E::kVec];
+#pragma unroll
+        for (int i = 0; i < E::kVec; ++i) {
+            const int64_t e = at(j) + i;
+            w[i] = E::down(-INFINITY);
+            if (e >= 0 && e < V) w[i] = reinterpret_cast<const typename E::Word *>(row)[e];
+        }
+        uint4 v;
+        __builtin_memcpy(&v, w, 16);
+        return v;
+    }
+    __device__ __forceinline__ uint4 load(int j) const {
+        if (j >= n) return make_uint4(kNegInfWord<DT>, kNegInfWord<DT>, kNegInfWord<DT>,
+                                      kNegInfWord<DT>);
+        if (!whole(j)) return part(j);
+        uint4 v;
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(elem_at<DT>(row, at(j))));
+        return v;
+    }
+};
+
+// ---- statistics and alternatives ------------------------------------------------
+//
+// A CTA (for few rows: a cluster, each CTA a slice) streams a row once, the next
+// batch of vectors in flight while one is added.
+//
+// Alternatives: a row's vectors fall into 64 groups by the threads that hold them.
+// The k-th largest of the groups' maxima is a bound that at least k elements reach
+// and, unless the large logits sit in few groups, few others (about 1.2 k for k = 20).
+// The bound of the first batch, and later of the first four, lets the pass collect
+// candidates as it goes; the bound of the whole row selects among them, and
+// counting ranks what is left.  Where that fails (more candidates than the list
+// holds, as in ascending rows; fewer than k finite logits; NaN) the slice is read
+// again: elements above the bound and equal to it in two lists, of the equal ones the
+// first in order; and where even the former are too many, the k largest one by one.
+constexpr int kStatThreads = 256, kStatWarps = kStatThreads / 32;
+constexpr int kBatch = 4;
+constexpr int kGroups = 64, kGroupLanes = kStatThreads / kGroups;
+constexpr int kTopMax = 32;
+constexpr int kList = 1024, kShortList = 256;
+constexpr int kMaxCluster = 8;
+static_assert(kTopMax <= kGroups && kMaxCluster * kTopMax <= kShortList &&
+              kMaxCluster * kTopMax <= kStatThreads, "lists hold what they must");
+
+struct StatShared {
+    Sums warps[kStatWarps];
+    Sums slice;                   // of the CTA's slice
+    float groups[kGroups];
+    float bound;
+    float token;                  // the token's logit, in the CTA that holds it
+    int count;                    // candidates (may exceed kList)
+    int above, equal;             // of the second reading
+    unsigned long long best;
+    unsigned long long top[kTopMax];
+    unsigned long long list[kList];
+};
 
 __device__ __forceinline__ float key_value(uint64_t key) {
     const uint32_t k = (uint32_t)(key >> 32);
@@ -184,33 +290,51 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 }
 __device__ __forceinline__ uint32_t key_index(uint64_t key) { return 0xFFFFFFFFu - (uint32_t)key; }
 
-// A row's slice in this CTA, as vectors of kVec elements: vector j of the slice is
-// at byte 16 j of shared memory and holds the row's elements at(j) ...
-template <int DT>
-struct Slice {
-    using E = Elem<DT>;
-    const uint4 *data;
-    int n;                        // vectors
-    int64_t start;                // element of the first vector's first lane (may be negative)
-    int64_t V;
-    __device__ __forceinline__ int64_t at(int j) const { return start + (int64_t)j * E::kVec; }
-    __device__ __forceinline__ bool whole(int j) const { return at(j) >= 0 && at(j) + E::kVec <= V; }
-};
+// sh.bound: the want-th largest maximum of the groups, whose threads hold `most`.
+__device__ __forceinline__ void find_bound(float most, int want, StatShared &sh) {
+#pragma unroll
+    for (int o = 1; o < kGroupLanes; o <<= 1)
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    if (threadIdx.x % kGroupLanes == 0) sh.groups[threadIdx.x / kGroupLanes] = most;
+    __syncthreads();
+    if (threadIdx.x < kGroups) {
+        const float g = sh.groups[threadIdx.x];
+        int larger = 0;
+#pragma unroll 16
+        for (int i = 0; i < kGroups; ++i) {
+            const float o = sh.groups[i];
+            larger += o > g || (o == g && i < (int)threadIdx.x);
+        }
+        if (larger == want - 1) sh.bound = g;
+    }
+    __syncthreads();
+}
 
-// The k largest keys of the slice that `keep` accepts, one by one.
+// Place those of n keys that are at least `least` and among the k largest into top.
+__device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n, uint64_t least,
+                                          int k, unsigned long long *top) {
+    for (int i = threadIdx.x; i < n; i += kStatThreads) {
+        const uint64_t key = keys[i];
+        if (key < least) continue;
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += keys[j] > key;
+        if (rank < k) top[rank] = key;
+    }
+}
+
+// The k largest keys of the slice, one by one.
 template <int DT>
-__device__ __noinline__ void top_one_by_one(const Slice<DT> s, int k, RowShared &sh) {
+__device__ __noinline__ void top_one_by_one(const Slice<DT> s, int k, StatShared &sh) {
     uint64_t last = ~0ull;
     for (int j = 0; j < k; ++j) {
         uint64_t b = 0;
-        for (int v = threadIdx.x; v < s.n; v += kRowThreads) {
+        for (int v = threadIdx.x; v < s.n; v += kStatThreads) {
             float f[Elem<DT>::kVec];
-            Elem<DT>::unpack(s.data[v], f);
+            Elem<DT>::unpack(s.load(v), f);
 #pragma unroll
             for (int i = 0; i < Elem<DT>::kVec; ++i) {
-                const int64_t e = s.at(v) + i;
-                if (e < 0 || e >= s.V) continue;
-                const uint64_t key = order_key(f[i], (uint32_t)e);
+                if (!s.has(s.at(v) + i)) continue;
+                const uint64_t key = order_key(f[i], (uint32_t)(s.at(v) + i));
                 if (key < last && key > b) b = key;
             }
         }
@@ -225,22 +349,21 @@ __device__ __noinline__ void top_one_by_one(const Slice<DT> s, int k, RowShared 
     }
 }
 
-// The first `want` elements equal to the bound, in order, by one warp.
+// The first `want` elements equal to the bound, in order, by one warp, into `to`.
 template <int DT>
-__device__ __noinline__ void first_equal(const Slice<DT> s, int want, RowShared &sh) {
+__device__ __noinline__ void first_equal(const Slice<DT> s, int want, float bound,
+                                         unsigned long long *to) {
     const int lane = threadIdx.x & 31;
     int found = 0;
     for (int v0 = 0; v0 < s.n && found < want; v0 += 32) {
         const int v = v0 + lane;
         uint32_t hits = 0;
-        float f[Elem<DT>::kVec];
         if (v < s.n) {
-            Elem<DT>::unpack(s.data[v], f);
+            float f[Elem<DT>::kVec];
+            Elem<DT>::unpack(s.load(v), f);
 #pragma unroll
-            for (int i = 0; i < Elem<DT>::kVec; ++i) {
-                const int64_t e = s.at(v) + i;
-                if (e >= 0 && e < s.V && f[i] == sh.bound) hits |= 1u << i;
-            }
+            for (int i = 0; i < Elem<DT>::kVec; ++i)
+                if (s.has(s.at(v) + i) && f[i] == bound) hits |= 1u << i;
         }
         int before = __popc(hits);
 #pragma unroll
@@ -253,7 +376,7 @@ __device__ __noinline__ void first_equal(const Slice<DT> s, int want, RowShared 
 #pragma unroll
         for (int i = 0; i < Elem<DT>::kVec; ++i) {
             if ((hits >> i) & 1u) {
-                if (at < want) sh.list[1][at] = order_key(sh.bound, (uint32_t)(s.at(v) + i));
+                if (at < want) to[at] = order_key(bound, (uint32_t)(s.at(v) + i));
                 ++at;
             }
         }
@@ -261,81 +384,255 @@ __device__ __noinline__ void first_equal(const Slice<DT> s, int want, RowShared 
     }
 }
 
-// Place the k largest of n + m keys (two lists) into top, by counting.
-__device__ __forceinline__ void rank_keys(const unsigned long long *a, int n,
-                                          const unsigned long long *b, int m, int k,
-                                          unsigned long long *top) {
-    for (int i = threadIdx.x; i < n + m; i += kRowThreads) {
-        const uint64_t key = i < n ? a[i] : b[i - n];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += a[j] > key;
-        for (int j = 0; j < m; ++j) rank += b[j] > key;
-        if (rank < k) top[rank] = key;
+// The alternatives from a second reading, with the bound of the whole slice.
+template <int DT>
+__device__ __noinline__ void read_again(const Slice<DT> s, int want, bool nan, StatShared &sh) {
+    const float bound = sh.bound;
+    unsigned long long *above = sh.list, *equal = sh.list + kShortList;
+    __syncthreads();
+    if (threadIdx.x == 0) sh.above = sh.equal = 0;
+    if (nan) {
+        top_one_by_one<DT>(s, want, sh);
+        return;
+    }
+    __syncthreads();
+    for (int v = threadIdx.x; v < s.n; v += kStatThreads) {
+        float f[Elem<DT>::kVec];
+        Elem<DT>::unpack(s.load(v), f);
+#pragma unroll
+        for (int i = 0; i < Elem<DT>::kVec; ++i) {
+            if (!(f[i] >= bound) || !s.has(s.at(v) + i)) continue;
+            const bool more = f[i] > bound;
+            // equal ones are counted no further than it matters
+            if (!more && *(volatile int *)&sh.equal > kShortList) continue;
+            const int at = atomicAdd(more ? &sh.above : &sh.equal, 1);
+            if (at < kShortList) (more ? above : equal)[at] = order_key(f[i], (uint32_t)(s.at(v) + i));
+        }
+    }
+    __syncthreads();
+    const int na = sh.above;
+    int ne = sh.equal;
+    if (na > kShortList) {
+        top_one_by_one<DT>(s, want, sh);
+        return;
+    }
+    if (na >= want) ne = 0;
+    if (ne > kShortList) {
+        ne = want - na;
+        if (threadIdx.x < 32) first_equal<DT>(s, ne, bound, equal);
+        __syncthreads();
+    }
+    // one list: all equal ones rank behind
+    for (int i = threadIdx.x; i < ne; i += kStatThreads) sh.list[2 * kShortList + i] = equal[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < ne; i += kStatThreads) above[na + i] = sh.list[2 * kShortList + i];
+    __syncthreads();
+    rank_keys(above, na + ne, 0, want, sh.top);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const TokenLogprobs a) {
+    constexpr int N = Elem<DT>::kVec;
+    __shared__ StatShared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int want = a.k;
+    pdl_wait_and_release();
+    for (int64_t t = blockIdx.x / C; t < a.T; t += gridDim.x / C) {
+        const char *row = elem_at<DT>(a.logits, t * a.ld);
+        const Slice<DT> s(row, a.V, C, rank);
+        const int64_t token = a.tokens[t];
+        if (threadIdx.x == 0) {
+            sh.count = 0;
+            if (s.has(token)) sh.token = load_now<DT>(row, token);
+        }
+        if (threadIdx.x < kTopMax) sh.top[threadIdx.x] = 0;
+        Online<DT, true> sums;
+        uint32_t most = kNegInfWord<DT>;
+        float bound = INFINITY;
+        const int batches = (s.n + kBatch * kStatThreads - 1) / (kBatch * kStatThreads);
+        uint4 cur[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) cur[i] = s.load(i * kStatThreads + threadIdx.x);
+        for (int b = 0; b < batches; ++b) {
+            uint4 next[kBatch];
+            const int j0 = b * kBatch * kStatThreads + threadIdx.x, j1 = j0 + kBatch * kStatThreads;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) next[i] = s.load(j1 + i * kStatThreads);
+            if (want && (b == 0 || b == 4)) {
+                uint32_t w = most;
+                if (b == 0) {
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) w = max_word<DT>(w, vec_max<DT>(cur[i]));
+                }
+                find_bound(word_max<DT>(w), want, sh);
+                bound = fmaxf(sh.bound, kLowest);     // -inf is no candidate
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const uint32_t w = vec_max<DT>(cur[i]);
+                const float vm = word_max<DT>(w);
+                most = max_word<DT>(most, w);
+                sums.add(cur[i], vm);
+                if (vm >= bound) {
+                    float f[N];
+                    Elem<DT>::unpack(cur[i], f);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        if (!(f[k] >= bound)) continue;
+                        const int at = atomicAdd(&sh.count, 1);
+                        if (at < kList)
+                            sh.list[at] = order_key(f[k], (uint32_t)(s.at(j0 + i * kStatThreads) + k));
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) cur[i] = next[i];
+        }
+        const Sums mine = warp_join(sums.sums());
+        if (lane == 0) sh.warps[warp] = mine;
+        if (want) find_bound(word_max<DT>(most), want, sh);
+        else __syncthreads();
+        Sums all = warp_join(lane < kStatWarps ? sh.warps[lane] : Sums{kLowest, 0.0f, 0.0f});
+        if (want) {
+            const int count = sh.count;
+            const float full = sh.bound;
+            // enough candidates: those at the row's bound, or (few finite ones) all
+            const bool nan = all.sum != all.sum;
+            if (count > kList || nan || (full == -INFINITY && count < want)) {
+                read_again<DT>(s, want, nan, sh);
+            } else {
+                rank_keys(sh.list, count, order_key(full, 0xFFFFFFFFu), want, sh.top);
+            }
+        }
+        if (C > 1) {
+            if (threadIdx.x == 0) sh.slice = all;
+            cluster.sync();
+            if (rank == 0)
+                all = warp_join(lane < C ? cluster.map_shared_rank(&sh, lane)->slice
+                                         : Sums{kLowest, 0.0f, 0.0f});
+        } else {
+            __syncthreads();
+        }
+        if (rank == 0) {
+            const float ls = logf(all.sum);
+            if (threadIdx.x == 0) {
+                float lp = 0.0f;
+                if (token >= a.V) {
+                    lp = NAN;
+                } else if (token >= 0) {
+                    const int skip = -(int)s.start;
+                    const int64_t vectors = (a.V + skip + N - 1) / N, per = (vectors + C - 1) / C;
+                    const int owner = C > 1 ? (int)((token + skip) / N / per) : 0;
+                    const float x = cluster.map_shared_rank(&sh, owner)->token;
+                    lp = x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), ls);
+                }
+                if (a.logp) a.logp[t] = lp;
+                if (a.entropy)
+                    a.entropy[t] = all.sum == 0.0f ? 0.0f : __fsub_rn(ls, __fdiv_rn(all.first, all.sum));
+                if (a.lse) a.lse[t] = __fadd_rn(all.ref, ls);
+            }
+            if (want && C > 1) {
+                // the slices' alternatives: those that reach every slice's last one
+                const int i = threadIdx.x;
+                uint64_t key = 0, least = 0;
+                if (i < C * want) key = cluster.map_shared_rank(&sh, i / want)->top[i % want];
+                if (lane < C) least = cluster.map_shared_rank(&sh, lane)->top[want - 1];
+#pragma unroll
+                for (int o = 1; o < kMaxCluster; o <<= 1) {
+                    const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, least, o);
+                    least = other > least ? other : least;
+                }
+                least = __shfl_sync(0xFFFFFFFFu, least, 0);
+                if (threadIdx.x == 0) sh.count = 0;
+                __syncthreads();
+                if (key != 0 && key >= least) sh.list[atomicAdd(&sh.count, 1)] = key;
+                __syncthreads();
+                rank_keys(sh.list, sh.count, 0, want, sh.top);
+                __syncthreads();
+            }
+            if (threadIdx.x < want) {
+                const uint64_t key = sh.top[threadIdx.x];
+                const float x = key_value(key);
+                a.top_ids[t * want + threadIdx.x] = key_index(key);
+                a.top_logp[t * want + threadIdx.x] =
+                    x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), ls);
+            }
+        }
+        if (C > 1) cluster.sync();     // the leader has read this CTA's shared memory
+        else __syncthreads();
     }
 }
 
-// Gradient of the loss for eight (four) logits: w e^(x - m) / S.
+// ---- the loss and its gradient --------------------------------------------------
+//
+// A cluster of C CTAs takes a row; each CTA copies its slice into shared memory,
+// adds its exponentials as it arrives, and writes its gradient from there: the
+// logits are read once.  Join of the CTAs' sums through distributed shared memory.
+constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
+constexpr int kSliceBytes = 72 * 1024;        // three CTAs an SM
+constexpr int kMaxSliceBytes = 216 * 1024;    // one CTA an SM
+
+struct RowShared {
+    Sums warps[kRowWarps];
+    Sums slice, row;
+    float token;                  // the token's logit, in the CTA that holds it
+};
+
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Gradient of a vector of logits: scale e^(x - ref).
 template <int DT>
-__device__ __forceinline__ void loss_grad(const uint4 &v, float m, float scale, float *g) {
+__device__ __forceinline__ void loss_grad(const uint4 &v, float ref, float scale, float *g) {
     constexpr int N = Elem<DT>::kVec;
     float f[N];
     Elem<DT>::unpack(v, f);
-    const uint64_t m2 = f32x2(m, m), l2 = f32x2(kLog2e, kLog2e), s2 = f32x2(scale, scale);
+    const uint64_t r2 = f32x2(ref, ref), l2 = f32x2(kLog2e, kLog2e), s2 = f32x2(scale, scale);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        const uint64_t t = mul_f32x2(sub_f32x2(f32x2(f[i], f[i + 1]), m2), l2);
+        const uint64_t t = mul_f32x2(sub_f32x2(f32x2(f[i], f[i + 1]), r2), l2);
         const uint64_t p = mul_f32x2(f32x2(exp2_approx(lo_f32(t)), exp2_approx(hi_f32(t))), s2);
         g[i] = lo_f32(p);
         g[i + 1] = hi_f32(p);
     }
 }
 
-// LOSS: logp and the gradient; else logp, entropy, lse and the alternatives.
-template <int DT, bool LOSS>
-__global__ void __launch_bounds__(kRowThreads) token_rows_kernel(const TokenLogprobs a) {
+template <int DT>
+__global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenLogprobs a) {
     using E = Elem<DT>;
+    using Word = typename E::Word;
     constexpr int N = E::kVec;
-    extern __shared__ __align__(16) uint4 slice[];
+    extern __shared__ __align__(16) uint4 data[];
     __shared__ RowShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(slice));
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(data));
+    const Word *words = reinterpret_cast<const Word *>(data);
     pdl_wait_and_release();
     for (int64_t t = blockIdx.x / C; t < a.T; t += gridDim.x / C) {
-        const char *row = elem_at<DT>(a.logits, t * a.ld);
-        const int skip = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / E::kSize;
-        const int64_t vectors = (a.V + skip + N - 1) / N, per = (vectors + C - 1) / C;
-        const int64_t v0 = rank * per, left = vectors - v0;
+        const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), a.V, C, rank);
         const int64_t token = a.tokens[t];
-        Slice<DT> s;
-        s.data = slice;
-        s.n = (int)(left < 0 ? 0 : left < per ? left : per);
-        s.start = v0 * N - skip;
-        s.V = a.V;
-        const int steps = (int)((per + kRowThreads - 1) / kRowThreads);
-        // in four groups of copies, so that the maximum starts with the first
+        const int steps = (s.n + kRowThreads - 1) / kRowThreads;
+        // in four groups of copies, so that the sums start with the first
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             for (int i = steps * q / 4; i < steps * (q + 1) / 4; ++i) {
                 const int j = i * kRowThreads + threadIdx.x;
                 if (j >= s.n) break;
-                if (s.whole(j)) {
-                    copy16(base + 16u * j, elem_at<DT>(row, s.at(j)));
-                } else {
-                    typename E::Word *to = reinterpret_cast<typename E::Word *>(slice + j);
-                    const typename E::Word *from =
-                        reinterpret_cast<const typename E::Word *>(row);
-                    slice[j] = make_uint4(kNegInfWord<DT>, kNegInfWord<DT>, kNegInfWord<DT>,
-                                          kNegInfWord<DT>);
-#pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        if (s.at(j) + k >= 0 && s.at(j) + k < a.V) to[k] = from[s.at(j) + k];
-                }
+                if (s.whole(j)) copy16(base + 16u * j, elem_at<DT>(s.row, s.at(j)));
+                else data[j] = s.part(j);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        uint32_t top = kNegInfWord<DT>;
+        Online<DT, false> sums;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (q == 0) copies_left<3>();
@@ -345,227 +642,70 @@ __global__ void __launch_bounds__(kRowThreads) token_rows_kernel(const TokenLogp
             for (int i = steps * q / 4; i < steps * (q + 1) / 4; ++i) {
                 const int j = i * kRowThreads + threadIdx.x;
                 if (j >= s.n) break;
-                const uint4 v = slice[j];
-                top = max_word<DT>(top, max_word<DT>(max_word<DT>(v.x, v.y),
-                                                     max_word<DT>(v.z, v.w)));
+                const uint4 v = data[j];
+                sums.add(v, word_max<DT>(vec_max<DT>(v)));
             }
         }
-        float m = word_max<DT>(top);
-#pragma unroll
-        for (int o = 1; o < kGroupLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (threadIdx.x % kGroupLanes == 0) sh.groups[threadIdx.x / kGroupLanes] = m;
-        m = warp_max(m);
-        if (lane == 0) sh.red[0][warp] = m;
+        const Sums mine = warp_join(sums.sums());
+        if (lane == 0) sh.warps[warp] = mine;
         __syncthreads();
-        m = sh.red[0][0];
+        Sums all = warp_join(lane < kRowWarps ? sh.warps[lane] : Sums{kLowest, 0.0f, 0.0f});
+        if (threadIdx.x == 0 && s.has(token)) sh.token = E::up(words[token - s.start]);
+        if (C > 1) {
+            if (threadIdx.x == 0) sh.slice = all;
+            cluster.sync();
+            if (warp == 0) {
+                all = warp_join(lane < C ? cluster.map_shared_rank(&sh, lane)->slice
+                                         : Sums{kLowest, 0.0f, 0.0f});
+                if (lane == 0) sh.row = all;
+            }
+            __syncthreads();
+            all = sh.row;
+        }
+        const bool ignored = token < 0, beyond = token >= a.V, empty = all.sum == 0.0f;
+        // the CTA that holds the token (the first one for a token outside)
+        if (threadIdx.x == 0 && a.logp && (ignored || beyond ? rank == 0 : s.has(token))) {
+            const float x = sh.token;
+            const float lp = x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), logf(all.sum));
+            a.logp[t] = ignored ? 0.0f : beyond ? NAN : lp;
+        }
+        float w = a.weights ? a.weights[t] : 1.0f;
+        if (ignored || empty) w = 0.0f;
+        if (beyond) w = NAN;
+        const float scale = __fdiv_rn(w, all.sum);
+        // Vectors of the output row: its 16-byte boundaries may lie elsewhere.
+        char *out = elem_at<DT>(a.dlogits, t * a.ldd);
+        const int oskip = (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize;
+        const int64_t e0 = s.start < 0 ? 0 : s.start;
+        const int64_t e1 = s.at(s.n) < a.V ? s.at(s.n) : a.V;
+        const int64_t o0 = (e0 + oskip) / N;
+        const int no = e1 > e0 ? (int)((e1 + oskip + N - 1) / N - o0) : 0;
+        for (int j = threadIdx.x; j < no; j += kRowThreads) {
+            const int64_t e = (o0 + j) * N - oskip;
+            if (e >= e0 && e + N <= e1) {
+                const int at = (int)(e - s.start), shift = at % N * E::kSize;
+                uint4 v = data[at / N];
+                if (shift) v = bytes_from(v, data[at / N + 1], shift);
+                float g[N];
+                loss_grad<DT>(v, all.ref, scale, g);
+                if (w == 0.0f) {
 #pragma unroll
-        for (int i = 1; i < kRowWarps; ++i) m = fmaxf(m, sh.red[0][i]);
-        const float slice_max = m;
-        if (m == -INFINITY) m = 0.0f;
-        const int want = (int)(a.k < a.V ? a.k : a.V);
-        bool collect = false;
-        float bound = 0.0f;
-        if constexpr (!LOSS) {
-            collect = want > 0;
-            if (collect) {
-                if (threadIdx.x < kGroups) {
-                    const float g = sh.groups[threadIdx.x];
-                    int larger = 0;
-                    for (int i = 0; i < kGroups; ++i) {
-                        const float o = sh.groups[i];
-                        larger += o > g || (o == g && i < (int)threadIdx.x);
-                    }
-                    if (larger == want - 1) sh.bound = g;
+                    for (int i = 0; i < N; ++i) g[i] = 0.0f;
                 }
-                if (threadIdx.x < kTopMax) sh.top[threadIdx.x] = 0;
-                if (threadIdx.x == 0) sh.above = sh.equal = 0;
-                __syncthreads();
-                bound = sh.bound;
-            }
-        }
-        // the token's logit
-        if (threadIdx.x == 0 && token >= 0 && token < a.V) {
-            const int64_t e = token - s.start;
-            if (e >= 0 && e < (int64_t)s.n * N)
-                sh.token = E::up(reinterpret_cast<const typename E::Word *>(slice)[e]);
-        }
-        uint64_t sum2 = 0, first2 = 0;
-        const uint64_t m2 = f32x2(m, m), l2 = f32x2(kLog2e, kLog2e);
-        for (int j = threadIdx.x; j < s.n; j += kRowThreads) {
-            const uint4 v = slice[j];
-            float f[N];
-            E::unpack(v, f);
+                if (token >= e && token < e + N) {
 #pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                uint64_t d = sub_f32x2(f32x2(f[i], f[i + 1]), m2);
-                if constexpr (!LOSS) {
-                    // not below -1000, so that (x - m) e^(x - m) is 0 for x = -inf
-                    float lo = lo_f32(d), hi = hi_f32(d);
-                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(-1000.0f));
-                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(-1000.0f));
-                    d = f32x2(lo, hi);
+                    for (int i = 0; i < N; ++i)
+                        if (token == e + i) g[i] = __fsub_rn(g[i], w);
                 }
-                const uint64_t x = mul_f32x2(d, l2);
-                const uint64_t e = f32x2(exp2_approx(lo_f32(x)), exp2_approx(hi_f32(x)));
-                sum2 = add_f32x2(sum2, e);
-                if constexpr (!LOSS) first2 = fma_f32x2(d, e, first2);
-            }
-            if (collect) {
-                const float most = word_max<DT>(max_word<DT>(max_word<DT>(v.x, v.y),
-                                                             max_word<DT>(v.z, v.w)));
-                if (most >= bound) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int64_t e = s.at(j) + i;
-                        if (!(f[i] >= bound) || e < 0 || e >= a.V) continue;
-                        const int which = f[i] > bound ? 0 : 1;
-                        const int at = atomicAdd(which ? &sh.equal : &sh.above, 1);
-                        if (at < kList) sh.list[which][at] = order_key(f[i], (uint32_t)e);
-                    }
-                }
-            }
-        }
-        float sum = warp_sum(__fadd_rn(lo_f32(sum2), hi_f32(sum2)));
-        float first = LOSS ? 0.0f : warp_sum(__fadd_rn(lo_f32(first2), hi_f32(first2)));
-        __syncthreads();   // red has been read
-        if (lane == 0) {
-            sh.red[0][warp] = sum;
-            sh.red[1][warp] = first;
-        }
-        __syncthreads();
-        sum = first = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kRowWarps; ++i) {
-            sum = __fadd_rn(sum, sh.red[0][i]);
-            first = __fadd_rn(first, sh.red[1][i]);
-        }
-        if (threadIdx.x == 0) {
-            sh.max = slice_max;
-            sh.sum = sum;
-            sh.first = first;
-        }
-        if constexpr (!LOSS) {
-            if (collect) {
-                const int above = sh.above, equal = sh.equal;
-                if (above > kList || sum != sum) {
-                    top_one_by_one<DT>(s, want, sh);
-                } else {
-                    int ties = above >= want ? 0 : equal;
-                    if (ties > kList) {
-                        ties = want - above;
-                        if (warp == 0) first_equal<DT>(s, ties, sh);
-                        __syncthreads();
-                    }
-                    rank_keys(sh.list[0], above, sh.list[1], ties, want, sh.top);
-                }
-            }
-        }
-        if (C > 1) cluster.sync();
-        else __syncthreads();
-        // the row's maximum and sums
-        if (warp == 0) {
-            float mc = -INFINITY, sc = 0.0f, fc = 0.0f;
-            if (lane < C) {
-                const RowShared *o = cluster.map_shared_rank(&sh, lane);
-                mc = o->max;
-                sc = o->sum;
-                fc = o->first;
-            }
-            const float mr = warp_max(mc), ref = mr == -INFINITY ? 0.0f : mr;
-            const float d = __fsub_rn(mc, ref), f = lane < C ? exp_approx(d) : 0.0f;
-            // a slice that counts for nothing may have d = -inf
-            const bool none = f == 0.0f && sc == sc;
-            const float rs = warp_sum(none ? 0.0f : __fmul_rn(f, sc));
-            const float rf = warp_sum(none ? 0.0f : __fmul_rn(f, __fmaf_rn(d, sc, fc)));
-            if (lane == 0) {
-                sh.all[0] = ref;
-                sh.all[1] = rs;
-                sh.all[2] = rf;
-            }
-        }
-        __syncthreads();
-        const float rm = sh.all[0], rs = sh.all[1], rf = sh.all[2];
-        const float ls = logf(rs);
-        const bool ignored = token < 0, beyond = token >= a.V, empty = rs == 0.0f;
-        if (rank == 0) {
-            if (threadIdx.x == 0) {
-                float lp = 0.0f;
-                if (beyond) lp = NAN;
-                else if (!ignored) {
-                    const float x = cluster.map_shared_rank(&sh, (int)((token + skip) / N / per))->token;
-                    lp = x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, rm), ls);
-                }
-                if (a.logp) a.logp[t] = lp;
-                if (!LOSS && a.entropy)
-                    a.entropy[t] = empty ? 0.0f : __fsub_rn(ls, __fdiv_rn(rf, rs));
-                if (!LOSS && a.lse) a.lse[t] = __fadd_rn(rm, ls);
-            }
-            if constexpr (!LOSS) {
-                if (collect && C > 1) {
-                    // the slices' alternatives: those that reach every slice's k-th
-                    const int i = threadIdx.x;
-                    uint64_t key = 0, least = 0;
-                    if (i < C * want) key = cluster.map_shared_rank(&sh, i / want)->top[i % want];
-                    for (int c = 0; c < C; ++c) {
-                        const uint64_t o = cluster.map_shared_rank(&sh, c)->top[want - 1];
-                        least = o > least ? o : least;
-                    }
-                    if (threadIdx.x == 0) sh.above = 0;
-                    __syncthreads();
-                    if (key != 0 && key >= least) sh.list[0][atomicAdd(&sh.above, 1)] = key;
-                    __syncthreads();
-                    rank_keys(sh.list[0], sh.above, nullptr, 0, want, sh.top);
-                    __syncthreads();
-                }
-                if (threadIdx.x < want) {
-                    const uint64_t key = sh.top[threadIdx.x];
-                    const float x = key_value(key);
-                    a.top_ids[t * want + threadIdx.x] = key_index(key);
-                    a.top_logp[t * want + threadIdx.x] =
-                        x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, rm), ls);
-                }
-            }
-        }
-        if constexpr (LOSS) {
-            float w = a.weights ? a.weights[t] : 1.0f;
-            if (ignored || empty) w = 0.0f;
-            if (beyond) w = NAN;
-            const float scale = __fdiv_rn(w, rs);
-            // Vectors of the output row: its 16-byte boundaries may lie elsewhere.
-            char *out = elem_at<DT>(a.dlogits, t * a.ldd);
-            const int oskip = (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize;
-            const int64_t e0 = s.start < 0 ? 0 : s.start;
-            const int64_t stop = s.start + (int64_t)s.n * N, e1 = stop < a.V ? stop : a.V;
-            const int64_t o0 = (e0 + oskip) / N;
-            const int no = e1 > e0 ? (int)((e1 + oskip + N - 1) / N - o0) : 0;
-            const typename E::Word *words = reinterpret_cast<const typename E::Word *>(slice);
-            for (int j = threadIdx.x; j < no; j += kRowThreads) {
-                const int64_t e = (o0 + j) * N - oskip;
-                if (e >= e0 && e + N <= e1) {
-                    const int at = (int)(e - s.start), sh_bytes = at % N * E::kSize;
-                    uint4 v = slice[at / N];
-                    if (sh_bytes) v = bytes_from(v, slice[at / N + 1], sh_bytes);
-                    float g[N];
-                    loss_grad<DT>(v, rm, scale, g);
-                    if (w == 0.0f) {
-#pragma unroll
-                        for (int i = 0; i < N; ++i) g[i] = 0.0f;
-                    }
-                    if (token >= e && token < e + N) {
-#pragma unroll
-                        for (int i = 0; i < N; ++i)
-                            if (token == e + i) g[i] = __fsub_rn(g[i], w);
-                    }
-                    *reinterpret_cast<uint4 *>(elem_at<DT>(out, e)) = E::pack(g);
-                } else {
-                    for (int i = 0; i < N; ++i) {
-                        if (e + i < e0 || e + i >= e1) continue;
-                        const float x = E::up(words[e + i - s.start]);
-                        float g = 0.0f;
-                        if (w != 0.0f) g = __fmul_rn(exp_approx(__fsub_rn(x, rm)), scale);
-                        if (token == e + i) g = __fsub_rn(g, w);
-                        store_elem<DT>(out, e + i, g);
-                    }
+                *reinterpret_cast<uint4 *>(elem_at<DT>(out, e)) = E::pack(g);
+            } else {
+                for (int i = 0; i < N; ++i) {
+                    if (e + i < e0 || e + i >= e1) continue;
+                    const float x = E::up(words[e + i - s.start]);
+                    float g = 0.0f;
+                    if (w != 0.0f) g = __fmul_rn(exp_approx(__fsub_rn(x, all.ref)), scale);
+                    if (token == e + i) g = __fsub_rn(g, w);
+                    store_elem<DT>(out, e + i, g);
                 }
             }
         }
@@ -574,11 +714,11 @@ __global__ void __launch_bounds__(kRowThreads) token_rows_kernel(const TokenLogp
     }
 }
 
-// The CTAs of a row's cluster: slices of at most kSliceBytes where eight CTAs
-// allow it (three CTAs an SM, whose copies and passes overlap), and more CTAs a
+// The CTAs of a row's cluster in the loss: slices of at most kSliceBytes where eight
+// CTAs allow it (three CTAs an SM, whose copies and passes overlap), and more CTAs a
 // row while the rows alone do not fill two CTAs an SM, down to 4 KB.  0: the row
 // does not fit on chip.
-int row_cluster(int64_t T, int64_t V, int size) {
+int loss_cluster(int64_t T, int64_t V, int size) {
     const int64_t bytes = V * size + 16;
     int c = 1;
     while (c < kMaxCluster && bytes > c * (int64_t)kSliceBytes) c *= 2;
@@ -587,13 +727,23 @@ int row_cluster(int64_t T, int64_t V, int size) {
     return c;
 }
 
-template <int DT, bool LOSS>
-cudaError_t launch_rows(const TokenLogprobs &a, int c, cudaStream_t st) {
+// The CTAs of a row's cluster in the statistics: one, and more while the rows do not
+// fill two CTAs an SM, down to 8 KB.
+int stats_cluster(int64_t T, int64_t V, int size) {
+    int c = 1;
+    while (c < kMaxCluster && T * c < 2 * sm_count() && V * size > c * 16384ll) c *= 2;
+    return c;
+}
+
+int row_grid(int64_t T, int c) { return (int)(T < (1 << 24) ? T : 1 << 24) * c; }
+
+template <int DT>
+cudaError_t launch_loss(const TokenLogprobs &a, int c, cudaStream_t st) {
     static bool ready[kMaxDevices];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= kMaxDevices) dev = 0;
-    auto kernel = token_rows_kernel<DT, LOSS>;
+    auto kernel = token_loss_kernel<DT>;
     if (!ready[dev]) {
         const cudaError_t e = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSliceBytes + 32);
@@ -603,15 +753,13 @@ cudaError_t launch_rows(const TokenLogprobs &a, int c, cudaStream_t st) {
     // a row that starts inside a vector has one vector more
     const int64_t vectors = (a.V + 2 * Elem<DT>::kVec - 2) / Elem<DT>::kVec;
     const size_t smem = (size_t)((vectors + c - 1) / c) * 16;
-    const int64_t rows = a.T < (1 << 24) ? a.T : 1 << 24;
-    return launch_pdl_clusters(kernel, (int)(rows * c), kRowThreads, c, smem, st, a);
+    return launch_pdl_clusters(kernel, row_grid(a.T, c), kRowThreads, c, smem, st, a);
 }
 
-template <bool LOSS>
-cudaError_t rows_of_type(const TokenLogprobs &a, int c, cudaStream_t st) {
-    return a.dtype == kF32    ? launch_rows<kF32, LOSS>(a, c, st)
-           : a.dtype == kBF16 ? launch_rows<kBF16, LOSS>(a, c, st)
-                              : launch_rows<kF16, LOSS>(a, c, st);
+template <int DT>
+cudaError_t launch_stats(const TokenLogprobs &a, cudaStream_t st) {
+    const int c = stats_cluster(a.T, a.V, Elem<DT>::kSize);
+    return launch_pdl_clusters(token_stats_kernel<DT>, row_grid(a.T, c), kStatThreads, c, 0, st, a);
 }
 
 template <int DT>
@@ -650,11 +798,20 @@ int grid_for(int64_t rows) {
 }  // namespace
 
 cudaError_t launch_token_logprobs(const TokenLogprobs &a, cudaStream_t st) {
-    const int c = row_cluster(a.T, a.V, a.dtype == kF32 ? 4 : 2);
-    if (c) return a.dlogits ? rows_of_type<true>(a, c, st) : rows_of_type<false>(a, c, st);
-    auto k = a.dtype == kF32    ? token_logprobs_kernel<kF32>
-             : a.dtype == kBF16 ? token_logprobs_kernel<kBF16>
-                                : token_logprobs_kernel<kF16>;
+    if (!a.dlogits) {
+        return a.dtype == kF32    ? launch_stats<kF32>(a, st)
+               : a.dtype == kBF16 ? launch_stats<kBF16>(a, st)
+                                  : launch_stats<kF16>(a, st);
+    }
+    const int c = loss_cluster(a.T, a.V, a.dtype == kF32 ? 4 : 2);
+    if (c) {
+        return a.dtype == kF32    ? launch_loss<kF32>(a, c, st)
+               : a.dtype == kBF16 ? launch_loss<kBF16>(a, c, st)
+                                  : launch_loss<kF16>(a, c, st);
+    }
+    auto k = a.dtype == kF32    ? token_loss_long_kernel<kF32>
+             : a.dtype == kBF16 ? token_loss_long_kernel<kBF16>
+                                : token_loss_long_kernel<kF16>;
     return launch_pdl(k, grid_for(a.T), kThreads, 0, st, a);
 }
 
