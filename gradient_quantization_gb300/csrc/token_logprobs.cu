@@ -127,50 +127,55 @@ __device__ __forceinline__ Sums warp_join(Sums s) {
     return s;
 }
 
+template <int DT>
+__device__ __forceinline__ uint32_t vec_max(const uint4 &v) {
+    return max_word<DT>(max_word<DT>(v.x, v.y), max_word<DT>(v.z, v.w));
+}
+
 // ENTROPY: with the sums of (x - ref) e^(x - ref).
 template <int DT, bool ENTROPY>
 struct Online {
-    float ref = kLowest;
+    float ref = kLowest, limit = kLowest;      // limit = ref + 8
     uint64_t sum2 = 0, first2 = 0;
-    uint32_t low = 0;      // 16-bit types, ref > kLowRef: a pair far below ref
-
-    // The sums of (x - ref) e^(x - ref) must not see x = -inf; where the exponential
+    // The sums of (x - ref) e^(x - ref) must not see x = -inf.  Where the exponential
     // is 0 anyway, 16-bit types raise x to `low` two at a time: -1000 below a
-    // positive reference, the lowest finite value below one in (kLowRef, 0], which
-    // is still more than 500 above it.
+    // positive reference, the lowest finite value below one in (kLowRef, 0], which is
+    // still more than 500 above it.  Below kLowRef values are so far apart that
+    // every product is 0 (or, of FP16, less than 1e-12), and none is added.
+    uint32_t low = kNegInfWord<DT>;
     static constexpr float kLowRef = DT == kF16 ? -65000.0f : -1e38f;
+
     __device__ __forceinline__ void raise(float to) {
-        Sums s{ref, __fadd_rn(lo_f32(sum2), hi_f32(sum2)),
-               __fadd_rn(lo_f32(first2), hi_f32(first2))};
+        Sums s = sums();
         s.move(to);
         ref = to;
+        limit = __fadd_rn(to, 8.0f);
         sum2 = f32x2(s.sum, 0.0f);
         first2 = f32x2(s.first, 0.0f);
-        if constexpr (ENTROPY && DT == kBF16) low = to > 0.0f ? 0xC47AC47Au : 0xFF7FFF7Fu;
-        if constexpr (ENTROPY && DT == kF16) low = to > 0.0f ? 0xE3D0E3D0u : 0xFBFFFBFFu;
+        if constexpr (ENTROPY && DT == kBF16)
+            low = to > 0.0f ? 0xC47AC47Au : to > kLowRef ? 0xFF7FFF7Fu : kNegInfWord<DT>;
+        if constexpr (ENTROPY && DT == kF16)
+            low = to > 0.0f ? 0xE3D0E3D0u : to > kLowRef ? 0xFBFFFBFFu : kNegInfWord<DT>;
     }
 
     // Add a vector whose largest element is `most`.
     __device__ __forceinline__ void add(uint4 v, float most) {
         constexpr int N = Elem<DT>::kVec;
-        if (most > __fadd_rn(ref, 8.0f)) raise(most);
-        bool each = ENTROPY && DT == kF32;     // (x - ref) bounded one by one
+        if (most > limit) raise(most);
         if constexpr (ENTROPY && DT != kF32) {
-            each = !(ref > kLowRef);
-            if (!each) {
-                v.x = raised(v.x);
-                v.y = raised(v.y);
-                v.z = raised(v.z);
-                v.w = raised(v.w);
-            }
+            v.x = raised(v.x);
+            v.y = raised(v.y);
+            v.z = raised(v.z);
+            v.w = raised(v.w);
         }
+        const bool products = ENTROPY && (DT == kF32 || ref > kLowRef);
         float f[N];
         Elem<DT>::unpack(v, f);
         const uint64_t r2 = f32x2(ref, ref), l2 = f32x2(kLog2e, kLog2e);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
             uint64_t d = sub_f32x2(f32x2(f[i], f[i + 1]), r2);
-            if (each) {
+            if constexpr (ENTROPY && DT == kF32) {
                 float lo = lo_f32(d), hi = hi_f32(d);
                 asm("max.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(-1000.0f));
                 asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(-1000.0f));
@@ -179,7 +184,7 @@ struct Online {
             const uint64_t x = mul_f32x2(d, l2);
             const uint64_t e = f32x2(exp2_approx(lo_f32(x)), exp2_approx(hi_f32(x)));
             sum2 = add_f32x2(sum2, e);
-            if constexpr (ENTROPY) first2 = fma_f32x2(d, e, first2);
+            if (products) first2 = fma_f32x2(d, e, first2);
         }
     }
 
@@ -196,55 +201,56 @@ struct Online {
     }
 };
 
+// The vector of a row of V elements from element e on, -inf where there is none.
 template <int DT>
-__device__ __forceinline__ uint32_t vec_max(const uint4 &v) {
-    return max_word<DT>(max_word<DT>(v.x, v.y), max_word<DT>(v.z, v.w));
+__device__ __noinline__ uint4 partial(const typename Elem<DT>::Word *row, int V, int e) {
+    typename Elem<DT>::Word w[Elem<DT>::kVec];
+#pragma unroll
+    for (int i = 0; i < Elem<DT>::kVec; ++i) {
+        w[i] = Elem<DT>::down(-INFINITY);
+        if (e + i >= 0 && e + i < V) w[i] = row[e + i];
+    }
+    uint4 v;
+    __builtin_memcpy(&v, w, 16);
+    return v;
 }
 
 // A CTA's slice of a row, cut at the 16-byte boundaries of memory: n vectors, of
-// which the row's first and last may be filled in part only.
+// which the row's first and last may be filled in part only; those in [from, to) are
+// whole.  (Elements are counted in 32 bits: a row has at most 2^30.)
 template <int DT>
 struct Slice {
     using E = Elem<DT>;
-    const char *row;
-    int64_t V;
-    int64_t start;                // element of the first vector's first lane (may be negative)
-    int n;
-    __device__ __forceinline__ Slice(const char *row_, int64_t V_, int C, int rank)
-        : row(row_), V(V_) {
-        const int skip = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / E::kSize;
-        const int64_t vectors = (V + skip + E::kVec - 1) / E::kVec;
-        const int64_t per = (vectors + C - 1) / C, left = vectors - rank * per;
-        n = (int)(left < 0 ? 0 : left < per ? left : per);
+    const typename E::Word *row;
+    const uint4 *vec;             // vector 0, 16-byte aligned (maybe before the row's start)
+    int V, start;                 // start: element of vector 0's first lane (may be negative)
+    int n, from, to;
+    __device__ __forceinline__ Slice(const char *row_, int V_, int C, int rank)
+        : row(reinterpret_cast<const typename E::Word *>(row_)), V(V_) {
+        const int skip = (int)(reinterpret_cast<uintptr_t>(row_) & 15u) / E::kSize;
+        const int vectors = (V + skip + E::kVec - 1) / E::kVec;
+        const int per = C > 1 ? (vectors + C - 1) / C : vectors, left = vectors - rank * per;
+        n = left < 0 ? 0 : left < per ? left : per;
         start = rank * per * E::kVec - skip;
+        vec = reinterpret_cast<const uint4 *>(row_ + (int64_t)start * E::kSize);
+        from = start < 0 && n > 0 ? 1 : 0;
+        to = n > from && at(n) > V ? n - 1 : n;
     }
-    __device__ __forceinline__ int64_t at(int j) const { return start + (int64_t)j * E::kVec; }
-    __device__ __forceinline__ bool whole(int j) const { return at(j) >= 0 && at(j) + E::kVec <= V; }
-    __device__ __forceinline__ bool has(int64_t e) const {
-        return e >= 0 && e < V && e >= start && e < at(n);
-    }
+    __device__ __forceinline__ int at(int j) const { return start + j * E::kVec; }
+    __device__ __forceinline__ int first() const { return start < 0 ? 0 : start; }
+    __device__ __forceinline__ int end() const { return at(n) < V ? at(n) : V; }
+    __device__ __forceinline__ bool has(int64_t e) const { return e >= first() && e < end(); }
     // Vector j with -inf where the row has no element.
-    __device__ __forceinline__ uint4 part(int j) const {
-        typename E::Word w[E::kVec];
-#pragma unroll
-        for (int i = 0; i < E::kVec; ++i) {
-            const int64_t e = at(j) + i;
-            w[i] = E::down(-INFINITY);
-            if (e >= 0 && e < V) w[i] = reinterpret_cast<const typename E::Word *>(row)[e];
-        }
-        uint4 v;
-        __builtin_memcpy(&v, w, 16);
-        return v;
-    }
+    __device__ __forceinline__ uint4 part(int j) const { return partial<DT>(row, V, at(j)); }
     __device__ __forceinline__ uint4 load(int j) const {
-        if (j >= n) return make_uint4(kNegInfWord<DT>, kNegInfWord<DT>, kNegInfWord<DT>,
-                                      kNegInfWord<DT>);
-        if (!whole(j)) return part(j);
         uint4 v;
         asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "l"(elem_at<DT>(row, at(j))));
+                     : "l"(vec + j));
         return v;
+    }
+    __device__ __forceinline__ uint4 any(int j) const {
+        return j >= from && j < to ? load(j) : part(j);
     }
 };
 
@@ -272,16 +278,16 @@ static_assert(kTopMax <= kGroups && kMaxCluster * kTopMax <= kShortList &&
               kMaxCluster * kTopMax <= kStatThreads, "lists hold what they must");
 
 struct StatShared {
+    float groups[kGroups];        // 16-byte aligned
     Sums warps[kStatWarps];
     Sums slice;                   // of the CTA's slice
-    float groups[kGroups];
     float bound;
     float token;                  // the token's logit, in the CTA that holds it
     int count;                    // candidates (may exceed kList)
-    int above, equal;             // of the second reading
+    int above, equal;             // entries of the shorter lists
     unsigned long long best;
     unsigned long long top[kTopMax];
-    unsigned long long list[kList];
+    unsigned long long list[kList], few[kShortList];
 };
 
 __device__ __forceinline__ float key_value(uint64_t key) {
@@ -300,25 +306,41 @@ __device__ __forceinline__ void find_bound(float most, int want, StatShared &sh)
     if (threadIdx.x < kGroups) {
         const float g = sh.groups[threadIdx.x];
         int larger = 0;
-#pragma unroll 16
-        for (int i = 0; i < kGroups; ++i) {
-            const float o = sh.groups[i];
-            larger += o > g || (o == g && i < (int)threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < kGroups; i += 4) {
+            const float4 o = *reinterpret_cast<const float4 *>(sh.groups + i);
+            const int me = threadIdx.x;
+            larger += (o.x > g || (o.x == g && i < me)) + (o.y > g || (o.y == g && i + 1 < me)) +
+                      (o.z > g || (o.z == g && i + 2 < me)) + (o.w > g || (o.w == g && i + 3 < me));
         }
         if (larger == want - 1) sh.bound = g;
     }
     __syncthreads();
 }
 
-// Place those of n keys that are at least `least` and among the k largest into top.
-__device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n, uint64_t least,
-                                          int k, unsigned long long *top) {
+// Place the k largest of n keys into top, by counting.
+__device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n, int k,
+                                          unsigned long long *top) {
     for (int i = threadIdx.x; i < n; i += kStatThreads) {
         const uint64_t key = keys[i];
-        if (key < least) continue;
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) rank += keys[j] > key;
         if (rank < k) top[rank] = key;
+    }
+}
+
+// Those elements of a vector that reach the bound become candidates.
+template <int DT>
+__device__ __noinline__ void collect(uint4 v, float bound, uint32_t element, int *count,
+                                     unsigned long long *list) {
+    float f[Elem<DT>::kVec];
+    Elem<DT>::unpack(v, f);
+#pragma unroll
+    for (int k = 0; k < Elem<DT>::kVec; ++k) {
+        if (!(f[k] >= bound)) continue;
+        const int at = atomicAdd(count, 1);
+        if (at < kList) list[at] = order_key(f[k], element + k);
     }
 }
 
@@ -330,7 +352,7 @@ __device__ __noinline__ void top_one_by_one(const Slice<DT> s, int k, StatShared
         uint64_t b = 0;
         for (int v = threadIdx.x; v < s.n; v += kStatThreads) {
             float f[Elem<DT>::kVec];
-            Elem<DT>::unpack(s.load(v), f);
+            Elem<DT>::unpack(s.any(v), f);
 #pragma unroll
             for (int i = 0; i < Elem<DT>::kVec; ++i) {
                 if (!s.has(s.at(v) + i)) continue;
@@ -360,7 +382,7 @@ __device__ __noinline__ void first_equal(const Slice<DT> s, int want, float boun
         uint32_t hits = 0;
         if (v < s.n) {
             float f[Elem<DT>::kVec];
-            Elem<DT>::unpack(s.load(v), f);
+            Elem<DT>::unpack(s.any(v), f);
 #pragma unroll
             for (int i = 0; i < Elem<DT>::kVec; ++i)
                 if (s.has(s.at(v) + i) && f[i] == bound) hits |= 1u << i;
@@ -398,7 +420,7 @@ __device__ __noinline__ void read_again(const Slice<DT> s, int want, bool nan, S
     __syncthreads();
     for (int v = threadIdx.x; v < s.n; v += kStatThreads) {
         float f[Elem<DT>::kVec];
-        Elem<DT>::unpack(s.load(v), f);
+        Elem<DT>::unpack(s.any(v), f);
 #pragma unroll
         for (int i = 0; i < Elem<DT>::kVec; ++i) {
             if (!(f[i] >= bound) || !s.has(s.at(v) + i)) continue;
@@ -427,39 +449,56 @@ __device__ __noinline__ void read_again(const Slice<DT> s, int want, bool nan, S
     __syncthreads();
     for (int i = threadIdx.x; i < ne; i += kStatThreads) above[na + i] = sh.list[2 * kShortList + i];
     __syncthreads();
-    rank_keys(above, na + ne, 0, want, sh.top);
+    rank_keys(above, na + ne, want, sh.top);
 }
 
 template <int DT>
 __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const TokenLogprobs a) {
     constexpr int N = Elem<DT>::kVec;
-    __shared__ StatShared sh;
+    __shared__ __align__(16) StatShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int want = a.k;
     pdl_wait_and_release();
     for (int64_t t = blockIdx.x / C; t < a.T; t += gridDim.x / C) {
-        const char *row = elem_at<DT>(a.logits, t * a.ld);
-        const Slice<DT> s(row, a.V, C, rank);
+        const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), (int)a.V, C, rank);
         const int64_t token = a.tokens[t];
         if (threadIdx.x == 0) {
-            sh.count = 0;
-            if (s.has(token)) sh.token = load_now<DT>(row, token);
+            sh.count = sh.above = 0;
+            if (s.has(token)) sh.token = Elem<DT>::up(s.row[token]);
         }
         if (threadIdx.x < kTopMax) sh.top[threadIdx.x] = 0;
         Online<DT, true> sums;
         uint32_t most = kNegInfWord<DT>;
-        float bound = INFINITY;
-        const int batches = (s.n + kBatch * kStatThreads - 1) / (kBatch * kStatThreads);
+        float bound = kLowest;                        // -inf is no candidate
+        auto load_batch = [&](int j, uint4 (&v)[kBatch]) {
+            if (j + (kBatch - 1) * kStatThreads < s.to) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) v[i] = s.load(j + i * kStatThreads);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    v[i] = make_uint4(kNegInfWord<DT>, kNegInfWord<DT>, kNegInfWord<DT>,
+                                      kNegInfWord<DT>);
+                    if (j + i * kStatThreads < s.to) v[i] = s.load(j + i * kStatThreads);
+                }
+            }
+        };
+        auto take = [&](const uint4 &v, int j) {
+            const uint32_t w = vec_max<DT>(v);
+            const float vm = word_max<DT>(w);
+            most = max_word<DT>(most, w);
+            sums.add(v, vm);
+            if (want && vm >= bound) collect<DT>(v, bound, s.at(j), &sh.count, sh.list);
+        };
+        constexpr int kStep = kBatch * kStatThreads;
         uint4 cur[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) cur[i] = s.load(i * kStatThreads + threadIdx.x);
-        for (int b = 0; b < batches; ++b) {
+        load_batch(s.from + threadIdx.x, cur);
+        for (int j0 = s.from, b = 0; j0 < s.to; j0 += kStep, ++b) {
+            const int j = j0 + threadIdx.x;
             uint4 next[kBatch];
-            const int j0 = b * kBatch * kStatThreads + threadIdx.x, j1 = j0 + kBatch * kStatThreads;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) next[i] = s.load(j1 + i * kStatThreads);
+            if (j0 + kStep < s.to) load_batch(j + kStep, next);
             if (want && (b == 0 || b == 4)) {
                 uint32_t w = most;
                 if (b == 0) {
@@ -467,29 +506,16 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
                     for (int i = 0; i < kBatch; ++i) w = max_word<DT>(w, vec_max<DT>(cur[i]));
                 }
                 find_bound(word_max<DT>(w), want, sh);
-                bound = fmaxf(sh.bound, kLowest);     // -inf is no candidate
+                bound = fmaxf(sh.bound, kLowest);
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const uint32_t w = vec_max<DT>(cur[i]);
-                const float vm = word_max<DT>(w);
-                most = max_word<DT>(most, w);
-                sums.add(cur[i], vm);
-                if (vm >= bound) {
-                    float f[N];
-                    Elem<DT>::unpack(cur[i], f);
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        if (!(f[k] >= bound)) continue;
-                        const int at = atomicAdd(&sh.count, 1);
-                        if (at < kList)
-                            sh.list[at] = order_key(f[k], (uint32_t)(s.at(j0 + i * kStatThreads) + k));
-                    }
-                }
-            }
+            for (int i = 0; i < kBatch; ++i) take(cur[i], j + i * kStatThreads);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) cur[i] = next[i];
         }
+        // the vectors filled in part
+        if (threadIdx.x == 0 && s.from > 0) take(s.part(0), 0);
+        if (threadIdx.x == 32 && s.to < s.n) take(s.part(s.to), s.to);
         const Sums mine = warp_join(sums.sums());
         if (lane == 0) sh.warps[warp] = mine;
         if (want) find_bound(word_max<DT>(most), want, sh);
@@ -503,7 +529,17 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
             if (count > kList || nan || (full == -INFINITY && count < want)) {
                 read_again<DT>(s, want, nan, sh);
             } else {
-                rank_keys(sh.list, count, order_key(full, 0xFFFFFFFFu), want, sh.top);
+                // those that reach it, usually few, move to a list of their own
+                const uint64_t least = order_key(full, 0xFFFFFFFFu);
+                for (int i = threadIdx.x; i < count; i += kStatThreads) {
+                    const uint64_t key = sh.list[i];
+                    if (key < least) continue;
+                    const int at = atomicAdd(&sh.above, 1);
+                    if (at < kShortList) sh.few[at] = key;
+                }
+                __syncthreads();
+                if (sh.above <= kShortList) rank_keys(sh.few, sh.above, want, sh.top);
+                else rank_keys(sh.list, count, want, sh.top);
             }
         }
         if (C > 1) {
@@ -522,9 +558,8 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
                 if (token >= a.V) {
                     lp = NAN;
                 } else if (token >= 0) {
-                    const int skip = -(int)s.start;
-                    const int64_t vectors = (a.V + skip + N - 1) / N, per = (vectors + C - 1) / C;
-                    const int owner = C > 1 ? (int)((token + skip) / N / per) : 0;
+                    // (rank 0's slice is the longest, and starts at -skip)
+                    const int owner = C > 1 ? ((int)token - s.start) / N / s.n : 0;
                     const float x = cluster.map_shared_rank(&sh, owner)->token;
                     lp = x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), ls);
                 }
@@ -549,7 +584,7 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
                 __syncthreads();
                 if (key != 0 && key >= least) sh.list[atomicAdd(&sh.count, 1)] = key;
                 __syncthreads();
-                rank_keys(sh.list, sh.count, 0, want, sh.top);
+                rank_keys(sh.list, sh.count, want, sh.top);
                 __syncthreads();
             }
             if (threadIdx.x < want) {
@@ -618,16 +653,17 @@ __global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenL
     const Word *words = reinterpret_cast<const Word *>(data);
     pdl_wait_and_release();
     for (int64_t t = blockIdx.x / C; t < a.T; t += gridDim.x / C) {
-        const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), a.V, C, rank);
+        const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), (int)a.V, C, rank);
         const int64_t token = a.tokens[t];
         const int steps = (s.n + kRowThreads - 1) / kRowThreads;
         // in four groups of copies, so that the sums start with the first
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            for (int i = steps * q / 4; i < steps * (q + 1) / 4; ++i) {
-                const int j = i * kRowThreads + threadIdx.x;
-                if (j >= s.n) break;
-                if (s.whole(j)) copy16(base + 16u * j, elem_at<DT>(s.row, s.at(j)));
+            int j = (steps * q / 4) * kRowThreads + threadIdx.x;
+            const int stop = min(s.n, (steps * (q + 1) / 4) * kRowThreads);
+#pragma unroll 2
+            for (; j < stop; j += kRowThreads) {
+                if (j >= s.from && j < s.to) copy16(base + 16u * j, s.vec + j);
                 else data[j] = s.part(j);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -639,9 +675,10 @@ __global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenL
             if (q == 1) copies_left<2>();
             if (q == 2) copies_left<1>();
             if (q == 3) copies_left<0>();
-            for (int i = steps * q / 4; i < steps * (q + 1) / 4; ++i) {
-                const int j = i * kRowThreads + threadIdx.x;
-                if (j >= s.n) break;
+            int j = (steps * q / 4) * kRowThreads + threadIdx.x;
+            const int stop = min(s.n, (steps * (q + 1) / 4) * kRowThreads);
+#pragma unroll 2
+            for (; j < stop; j += kRowThreads) {
                 const uint4 v = data[j];
                 sums.add(v, word_max<DT>(vec_max<DT>(v)));
             }
@@ -673,41 +710,46 @@ __global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenL
         if (ignored || empty) w = 0.0f;
         if (beyond) w = NAN;
         const float scale = __fdiv_rn(w, all.sum);
-        // Vectors of the output row: its 16-byte boundaries may lie elsewhere.
         char *out = elem_at<DT>(a.dlogits, t * a.ldd);
+        const int mine_token = s.has(token) ? (int)token : -1;
+        // The vectors of the output row (its 16-byte boundaries may lie elsewhere) that
+        // hold elements of the slice only, and the elements before and after them.
         const int oskip = (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize;
-        const int64_t e0 = s.start < 0 ? 0 : s.start;
-        const int64_t e1 = s.at(s.n) < a.V ? s.at(s.n) : a.V;
-        const int64_t o0 = (e0 + oskip) / N;
-        const int no = e1 > e0 ? (int)((e1 + oskip + N - 1) / N - o0) : 0;
-        for (int j = threadIdx.x; j < no; j += kRowThreads) {
-            const int64_t e = (o0 + j) * N - oskip;
-            if (e >= e0 && e + N <= e1) {
-                const int at = (int)(e - s.start), shift = at % N * E::kSize;
-                uint4 v = data[at / N];
-                if (shift) v = bytes_from(v, data[at / N + 1], shift);
-                float g[N];
-                loss_grad<DT>(v, all.ref, scale, g);
-                if (w == 0.0f) {
+        const int e0 = s.first(), e1 = s.end();
+        const int o0 = (e0 + oskip + N - 1) / N, o1 = e1 > e0 ? (e1 + oskip) / N : o0;
+        uint4 *ovec = reinterpret_cast<uint4 *>(out - oskip * E::kSize);
+        const int token_vec = mine_token >= 0 ? (mine_token + oskip) / N : -1;
+        const int shift = (e0 + oskip + N - 1) / N * N - oskip - s.start;   // of o0 in the slice
+        const uint4 *from = data + shift / N;
+        const int off = shift % N * E::kSize;
+        auto one = [&](const uint4 &v, int o) {
+            float g[N];
+            loss_grad<DT>(v, all.ref, scale, g);
+            if (o == token_vec) {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) g[i] = 0.0f;
-                }
-                if (token >= e && token < e + N) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        if (token == e + i) g[i] = __fsub_rn(g[i], w);
-                }
-                *reinterpret_cast<uint4 *>(elem_at<DT>(out, e)) = E::pack(g);
-            } else {
-                for (int i = 0; i < N; ++i) {
-                    if (e + i < e0 || e + i >= e1) continue;
-                    const float x = E::up(words[e + i - s.start]);
-                    float g = 0.0f;
-                    if (w != 0.0f) g = __fmul_rn(exp_approx(__fsub_rn(x, all.ref)), scale);
-                    if (token == e + i) g = __fsub_rn(g, w);
-                    store_elem<DT>(out, e + i, g);
-                }
+                for (int i = 0; i < N; ++i)
+                    if (o * N - oskip + i == mine_token) g[i] = __fsub_rn(g[i], w);
             }
+            ovec[o] = E::pack(g);
+        };
+        if (w == 0.0f) {
+            for (int o = o0 + threadIdx.x; o < o1; o += kRowThreads) ovec[o] = make_uint4(0, 0, 0, 0);
+        } else if (off == 0) {
+#pragma unroll 2
+            for (int o = o0 + threadIdx.x; o < o1; o += kRowThreads) one(from[o - o0], o);
+        } else {
+            for (int o = o0 + threadIdx.x; o < o1; o += kRowThreads)
+                one(bytes_from(from[o - o0], from[o - o0 + 1], off), o);
+        }
+        // elements of output vectors shared with other slices or rows
+        const int head = min(e1, o0 * N - oskip), tail = max(head, o1 * N - oskip);
+        const int i = threadIdx.x;
+        if (i < head - e0 + e1 - tail) {
+            const int e = i < head - e0 ? e0 + i : tail + i - (head - e0);
+            float g = 0.0f;
+            if (w != 0.0f) g = __fmul_rn(exp_approx(__fsub_rn(E::up(words[e - s.start]), all.ref)), scale);
+            if (e == mine_token) g = __fsub_rn(g, w);
+            store_elem<DT>(out, e, g);
         }
         if (C > 1) cluster.sync();     // the others have read this CTA's shared memory
         else __syncthreads();
