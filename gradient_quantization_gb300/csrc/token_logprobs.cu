@@ -256,26 +256,30 @@ struct Slice {
 
 // ---- statistics and alternatives ------------------------------------------------
 //
-// A CTA (for few rows: a cluster, each CTA a slice) streams a row once, the next
-// batch of vectors in flight while one is added.
+// A CTA (for few rows: a cluster, each CTA a slice) streams its rows once, through a
+// ring of shared memory whose copies run ahead of the sums and across rows; a
+// thread reads only what it copied, so the ring needs no barrier.
 //
 // Alternatives: a row's vectors fall into 64 groups by the threads that hold them.
 // The k-th largest of the groups' maxima is a bound that at least k elements reach
 // and, unless the large logits sit in few groups, few others (about 1.2 k for k = 20).
-// The bound of the first batch, and later of the first four, lets the pass collect
-// candidates as it goes; the bound of the whole row selects among them, and
-// counting ranks what is left.  Where that fails (more candidates than the list
+// The bounds of the first batch, of the first 4, 16, ... let the pass collect
+// candidate vectors as it goes; the bound of the whole row selects their elements,
+// and counting ranks what is left.  Where that fails (more candidates than the list
 // holds, as in ascending rows; fewer than k finite logits; NaN) the slice is read
 // again: elements above the bound and equal to it in two lists, of the equal ones the
 // first in order; and where even the former are too many, the k largest one by one.
 constexpr int kStatThreads = 256, kStatWarps = kStatThreads / 32;
-constexpr int kBatch = 4;
+constexpr int kBatch = 4;                     // vectors a thread and stage
+constexpr int kStages = 3;                    // of shared memory, each thread's own
+constexpr int kStep = kBatch * kStatThreads;
 constexpr int kGroups = 64, kGroupLanes = kStatThreads / kGroups;
 constexpr int kTopMax = 32;
-constexpr int kList = 1024, kShortList = 256;
+constexpr int kList = 768, kShortList = 256;
 constexpr int kMaxCluster = 8;
 static_assert(kTopMax <= kGroups && kMaxCluster * kTopMax <= kShortList &&
-              kMaxCluster * kTopMax <= kStatThreads, "lists hold what they must");
+              kMaxCluster * kTopMax <= kStatThreads && 3 * kShortList <= kList,
+              "lists hold what they must");
 
 struct StatShared {
     float groups[kGroups];        // 16-byte aligned
@@ -283,11 +287,18 @@ struct StatShared {
     Sums slice;                   // of the CTA's slice
     float bound;
     float token;                  // the token's logit, in the CTA that holds it
-    int count;                    // candidates (may exceed kList)
+    int count;                    // candidate vectors (may exceed kList)
     int above, equal;             // entries of the shorter lists
     unsigned long long best;
     unsigned long long top[kTopMax];
-    unsigned long long list[kList], few[kShortList];
+    // Candidate vectors and their first elements' indices; later lists of keys.
+    union {
+        uint4 vec[kList];
+        unsigned long long list[2 * kList];
+    };
+    int element[kList];
+    unsigned long long few[kShortList];
+    uint4 ring[kStages][kBatch][kStatThreads];
 };
 
 __device__ __forceinline__ float key_value(uint64_t key) {
@@ -327,20 +338,6 @@ __device__ __forceinline__ void rank_keys(const unsigned long long *keys, int n,
 #pragma unroll 4
         for (int j = 0; j < n; ++j) rank += keys[j] > key;
         if (rank < k) top[rank] = key;
-    }
-}
-
-// Those elements of a vector that reach the bound become candidates.
-template <int DT>
-__device__ __noinline__ void collect(uint4 v, float bound, uint32_t element, int *count,
-                                     unsigned long long *list) {
-    float f[Elem<DT>::kVec];
-    Elem<DT>::unpack(v, f);
-#pragma unroll
-    for (int k = 0; k < Elem<DT>::kVec; ++k) {
-        if (!(f[k] >= bound)) continue;
-        const int at = atomicAdd(count, 1);
-        if (at < kList) list[at] = order_key(f[k], element + k);
     }
 }
 
@@ -452,15 +449,74 @@ __device__ __noinline__ void read_again(const Slice<DT> s, int want, bool nan, S
     rank_keys(above, na + ne, want, sh.top);
 }
 
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The copies of a CTA's rows into the ring, ahead of the sums and across rows.
+template <int DT>
+struct Fetch {
+    const TokenLogprobs &a;
+    StatShared &sh;
+    int C, rank, stage = 0;
+    int64_t t;
+    const uint4 *vec;             // of the row being fetched: its next vector for this thread
+    int left;                     // vectors of the slice from that one on
+    __device__ __forceinline__ Fetch(const TokenLogprobs &a_, StatShared &sh_, int64_t t_, int C_,
+                                     int rank_)
+        : a(a_), sh(sh_), C(C_), rank(rank_), t(t_) {
+        row();
+    }
+    // Start row t, or the next one that has whole vectors.
+    __device__ __forceinline__ void row() {
+        left = 0;
+        vec = nullptr;
+        for (; t < a.T; t += gridDim.x / C) {
+            const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), (int)a.V, C, rank);
+            if (s.to <= s.from) continue;
+            vec = s.vec + s.from + threadIdx.x;
+            left = s.to - s.from;
+            return;
+        }
+    }
+    __device__ __forceinline__ void next() {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if ((int)threadIdx.x + i * kStatThreads < left)
+                copy16(&sh.ring[stage][i][threadIdx.x], vec + i * kStatThreads);
+        copies_commit();
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        vec += kStep;
+        left -= kStep;
+        if (left <= 0 && t < a.T) {
+            t += gridDim.x / C;
+            row();
+        }
+    }
+};
+
 template <int DT>
 __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const TokenLogprobs a) {
     constexpr int N = Elem<DT>::kVec;
-    __shared__ __align__(16) StatShared sh;
+    extern __shared__ __align__(16) uint8_t shared_bytes[];
+    StatShared &sh = *reinterpret_cast<StatShared *>(shared_bytes);
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int want = a.k;
     pdl_wait_and_release();
+    Fetch<DT> fetch(a, sh, blockIdx.x / C, C, rank);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch.next();
+    int stage = 0;
     for (int64_t t = blockIdx.x / C; t < a.T; t += gridDim.x / C) {
         const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), (int)a.V, C, rank);
         const int64_t token = a.tokens[t];
@@ -469,37 +525,38 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
             if (s.has(token)) sh.token = Elem<DT>::up(s.row[token]);
         }
         if (threadIdx.x < kTopMax) sh.top[threadIdx.x] = 0;
+        if (want) __syncthreads();                    // before the first candidate
         Online<DT, true> sums;
         uint32_t most = kNegInfWord<DT>;
         float bound = kLowest;                        // -inf is no candidate
-        auto load_batch = [&](int j, uint4 (&v)[kBatch]) {
-            if (j + (kBatch - 1) * kStatThreads < s.to) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) v[i] = s.load(j + i * kStatThreads);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    v[i] = make_uint4(kNegInfWord<DT>, kNegInfWord<DT>, kNegInfWord<DT>,
-                                      kNegInfWord<DT>);
-                    if (j + i * kStatThreads < s.to) v[i] = s.load(j + i * kStatThreads);
-                }
-            }
-        };
         auto take = [&](const uint4 &v, int j) {
             const uint32_t w = vec_max<DT>(v);
             const float vm = word_max<DT>(w);
             most = max_word<DT>(most, w);
             sums.add(v, vm);
-            if (want && vm >= bound) collect<DT>(v, bound, s.at(j), &sh.count, sh.list);
+            if (want && vm >= bound) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < kList) {
+                    sh.vec[at] = v;
+                    sh.element[at] = s.at(j);
+                }
+            }
         };
-        constexpr int kStep = kBatch * kStatThreads;
-        uint4 cur[kBatch];
-        load_batch(s.from + threadIdx.x, cur);
         for (int j0 = s.from, b = 0; j0 < s.to; j0 += kStep, ++b) {
             const int j = j0 + threadIdx.x;
-            uint4 next[kBatch];
-            if (j0 + kStep < s.to) load_batch(j + kStep, next);
-            if (want && (b == 0 || b == 4)) {
+            copies_left<kStages - 2>();
+            uint4 cur[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                cur[i] = sh.ring[stage][i][threadIdx.x];
+                if (j + i * kStatThreads >= s.to)
+                    cur[i] = make_uint4(kNegInfWord<DT>, kNegInfWord<DT>, kNegInfWord<DT>,
+                                        kNegInfWord<DT>);
+            }
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+            fetch.next();
+            // a bound from the first batch, from the first 4, 16, 64, ...
+            if (want && (b == 0 || ((b & (b - 1)) == 0 && (b & 0x55555554)))) {
                 uint32_t w = most;
                 if (b == 0) {
 #pragma unroll
@@ -510,8 +567,6 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) take(cur[i], j + i * kStatThreads);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) cur[i] = next[i];
         }
         // the vectors filled in part
         if (threadIdx.x == 0 && s.from > 0) take(s.part(0), 0);
@@ -524,22 +579,28 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
         if (want) {
             const int count = sh.count;
             const float full = sh.bound;
-            // enough candidates: those at the row's bound, or (few finite ones) all
             const bool nan = all.sum != all.sum;
-            if (count > kList || nan || (full == -INFINITY && count < want)) {
+            if (count > kList || nan) {
                 read_again<DT>(s, want, nan, sh);
             } else {
-                // those that reach it, usually few, move to a list of their own
-                const uint64_t least = order_key(full, 0xFFFFFFFFu);
+                // their elements that reach it, usually few
+                const float least = fmaxf(full, kLowest);
                 for (int i = threadIdx.x; i < count; i += kStatThreads) {
-                    const uint64_t key = sh.list[i];
-                    if (key < least) continue;
-                    const int at = atomicAdd(&sh.above, 1);
-                    if (at < kShortList) sh.few[at] = key;
+                    float f[N];
+                    Elem<DT>::unpack(sh.vec[i], f);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        if (!(f[k] >= least)) continue;
+                        const int at = atomicAdd(&sh.above, 1);
+                        if (at < kShortList) sh.few[at] = order_key(f[k], sh.element[i] + k);
+                    }
                 }
                 __syncthreads();
-                if (sh.above <= kShortList) rank_keys(sh.few, sh.above, want, sh.top);
-                else rank_keys(sh.list, count, want, sh.top);
+                const int few = sh.above;
+                if (few > kShortList || (full == -INFINITY && few < want))
+                    read_again<DT>(s, want, false, sh);
+                else
+                    rank_keys(sh.few, few, want, sh.top);
             }
         }
         if (C > 1) {
@@ -605,7 +666,7 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
 // A cluster of C CTAs takes a row; each CTA copies its slice into shared memory,
 // adds its exponentials as it arrives, and writes its gradient from there: the
 // logits are read once.  Join of the CTAs' sums through distributed shared memory.
-constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kSliceBytes = 72 * 1024;        // three CTAs an SM
 constexpr int kMaxSliceBytes = 216 * 1024;    // one CTA an SM
 
@@ -614,14 +675,6 @@ struct RowShared {
     Sums slice, row;
     float token;                  // the token's logit, in the CTA that holds it
 };
-
-__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_left() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // Gradient of a vector of logits: scale e^(x - ref).
 template <int DT>
@@ -649,7 +702,6 @@ __global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenL
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(data));
     const Word *words = reinterpret_cast<const Word *>(data);
     pdl_wait_and_release();
     for (int64_t t = blockIdx.x / C; t < a.T; t += gridDim.x / C) {
@@ -663,10 +715,10 @@ __global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenL
             const int stop = min(s.n, (steps * (q + 1) / 4) * kRowThreads);
 #pragma unroll 2
             for (; j < stop; j += kRowThreads) {
-                if (j >= s.from && j < s.to) copy16(base + 16u * j, s.vec + j);
+                if (j >= s.from && j < s.to) copy16(data + j, s.vec + j);
                 else data[j] = s.part(j);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            copies_commit();
         }
         Online<DT, false> sums;
 #pragma unroll
@@ -779,19 +831,25 @@ int stats_cluster(int64_t T, int64_t V, int size) {
 
 int row_grid(int64_t T, int c) { return (int)(T < (1 << 24) ? T : 1 << 24) * c; }
 
-template <int DT>
-cudaError_t launch_loss(const TokenLogprobs &a, int c, cudaStream_t st) {
-    static bool ready[kMaxDevices];
+// Allow `kernel` `bytes` of dynamic shared memory (once a device).
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes, bool *ready) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= kMaxDevices) dev = 0;
+    if (ready[dev]) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    ready[dev] = e == cudaSuccess;
+    return e;
+}
+
+template <int DT>
+cudaError_t launch_loss(const TokenLogprobs &a, int c, cudaStream_t st) {
+    static bool ready[kMaxDevices];
     auto kernel = token_loss_kernel<DT>;
-    if (!ready[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSliceBytes + 32);
-        if (e != cudaSuccess) return e;
-        ready[dev] = true;
-    }
+    const cudaError_t e = allow_shared(kernel, kMaxSliceBytes + 32, ready);
+    if (e != cudaSuccess) return e;
     // a row that starts inside a vector has one vector more
     const int64_t vectors = (a.V + 2 * Elem<DT>::kVec - 2) / Elem<DT>::kVec;
     const size_t smem = (size_t)((vectors + c - 1) / c) * 16;
@@ -800,8 +858,13 @@ cudaError_t launch_loss(const TokenLogprobs &a, int c, cudaStream_t st) {
 
 template <int DT>
 cudaError_t launch_stats(const TokenLogprobs &a, cudaStream_t st) {
+    static bool ready[kMaxDevices];
+    auto kernel = token_stats_kernel<DT>;
+    const cudaError_t e = allow_shared(kernel, sizeof(StatShared), ready);
+    if (e != cudaSuccess) return e;
     const int c = stats_cluster(a.T, a.V, Elem<DT>::kSize);
-    return launch_pdl_clusters(token_stats_kernel<DT>, row_grid(a.T, c), kStatThreads, c, 0, st, a);
+    const int64_t most = 3 * sm_count() / c, rows = a.T < most ? a.T : most;
+    return launch_pdl_clusters(kernel, (int)rows * c, kStatThreads, c, sizeof(StatShared), st, a);
 }
 
 template <int DT>
