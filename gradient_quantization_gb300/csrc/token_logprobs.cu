@@ -670,6 +670,13 @@ constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kSliceBytes = 72 * 1024;        // three CTAs an SM
 constexpr int kMaxSliceBytes = 216 * 1024;    // one CTA an SM
 
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 struct RowShared {
     Sums warps[kRowWarps];
     Sums slice, row;
@@ -707,30 +714,37 @@ __global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenL
     for (int64_t t = blockIdx.x / C; t < a.T; t += gridDim.x / C) {
         const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), (int)a.V, C, rank);
         const int64_t token = a.tokens[t];
-        const int steps = (s.n + kRowThreads - 1) / kRowThreads;
-        // in four groups of copies, so that the sums start with the first
+        const int steps = (s.to - s.from + kRowThreads - 1) / kRowThreads;
+        auto part_of = [&](int q) {       // vectors of the q-th of four groups of copies
+            return min(s.to, s.from + steps * q / 4 * kRowThreads);
+        };
+        // four groups, so that the sums start with the first
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            int j = (steps * q / 4) * kRowThreads + threadIdx.x;
-            const int stop = min(s.n, (steps * (q + 1) / 4) * kRowThreads);
+            const int stop = part_of(q + 1);
 #pragma unroll 2
-            for (; j < stop; j += kRowThreads) {
-                if (j >= s.from && j < s.to) copy16(data + j, s.vec + j);
-                else data[j] = s.part(j);
-            }
+            for (int j = part_of(q) + threadIdx.x; j < stop; j += kRowThreads)
+                copy16(data + j, s.vec + j);
             copies_commit();
         }
+        // the vectors filled in part, while the copies run
         Online<DT, false> sums;
+        const int edge = threadIdx.x == 0 && s.from > 0 ? 0
+                         : threadIdx.x == 32 && s.to < s.n ? s.to : -1;
+        if (edge >= 0) {
+            const uint4 v = s.part(edge);
+            data[edge] = v;
+            sums.add(v, word_max<DT>(vec_max<DT>(v)));
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (q == 0) copies_left<3>();
             if (q == 1) copies_left<2>();
             if (q == 2) copies_left<1>();
             if (q == 3) copies_left<0>();
-            int j = (steps * q / 4) * kRowThreads + threadIdx.x;
-            const int stop = min(s.n, (steps * (q + 1) / 4) * kRowThreads);
+            const int stop = part_of(q + 1);
 #pragma unroll 2
-            for (; j < stop; j += kRowThreads) {
+            for (int j = part_of(q) + threadIdx.x; j < stop; j += kRowThreads) {
                 const uint4 v = data[j];
                 sums.add(v, word_max<DT>(vec_max<DT>(v)));
             }
@@ -750,6 +764,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenL
             }
             __syncthreads();
             all = sh.row;
+            cluster_arrive();              // the others' shared memory has been read
         }
         const bool ignored = token < 0, beyond = token >= a.V, empty = all.sum == 0.0f;
         // the CTA that holds the token (the first one for a token outside)
@@ -803,8 +818,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenL
             if (e == mine_token) g = __fsub_rn(g, w);
             store_elem<DT>(out, e, g);
         }
-        if (C > 1) cluster.sync();     // the others have read this CTA's shared memory
-        else __syncthreads();
+        if (C > 1) cluster_wait();
+        __syncthreads();
     }
 }
 
