@@ -132,6 +132,31 @@ __device__ __forceinline__ uint32_t vec_max(const uint4 &v) {
     return max_word<DT>(max_word<DT>(v.x, v.y), max_word<DT>(v.z, v.w));
 }
 
+// x - ref of a vector's elements, in pairs (one rounding each: the mixed-precision
+// addition takes a 16-bit operand as it is, without a conversion).
+template <int DT>
+__device__ __forceinline__ void differences(const uint4 &v, float ref, uint64_t *d) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == kF32) {
+        d[0] = sub_f32x2(u32x2(w[0], w[1]), f32x2(ref, ref));
+        d[1] = sub_f32x2(u32x2(w[2], w[3]), f32x2(ref, ref));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            if constexpr (DT == kBF16)
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                    "add.rn.f32.bf16 %0, a, %3;\n\tadd.rn.f32.bf16 %1, b, %3;\n\t}"
+                    : "=f"(lo), "=f"(hi) : "r"(w[i]), "f"(-ref));
+            else
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                    "add.rn.f32.f16 %0, a, %3;\n\tadd.rn.f32.f16 %1, b, %3;\n\t}"
+                    : "=f"(lo), "=f"(hi) : "r"(w[i]), "f"(-ref));
+            d[i] = f32x2(lo, hi);
+        }
+    }
+}
+
 // ENTROPY: with the sums of (x - ref) e^(x - ref).
 template <int DT, bool ENTROPY>
 struct Online {
@@ -158,10 +183,14 @@ struct Online {
             low = to > 0.0f ? 0xE3D0E3D0u : to > kLowRef ? 0xFBFFFBFFu : kNegInfWord<DT>;
     }
 
-    // Add a vector whose largest element is `most`.
-    __device__ __forceinline__ void add(uint4 v, float most) {
-        constexpr int N = Elem<DT>::kVec;
+    // Add a vector whose largest element is at most `most`.
+    __device__ __forceinline__ void add(const uint4 &v, float most) {
         if (most > limit) raise(most);
+        add(v);
+    }
+    // Add a vector whose elements do not exceed the limit.
+    __device__ __forceinline__ void add(uint4 v) {
+        constexpr int N = Elem<DT>::kVec;
         if constexpr (ENTROPY && DT != kF32) {
             v.x = raised(v.x);
             v.y = raised(v.y);
@@ -169,22 +198,21 @@ struct Online {
             v.w = raised(v.w);
         }
         const bool products = ENTROPY && (DT == kF32 || ref > kLowRef);
-        float f[N];
-        Elem<DT>::unpack(v, f);
-        const uint64_t r2 = f32x2(ref, ref), l2 = f32x2(kLog2e, kLog2e);
+        const uint64_t l2 = f32x2(kLog2e, kLog2e);
+        uint64_t d[N / 2];
+        differences<DT>(v, ref, d);
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            uint64_t d = sub_f32x2(f32x2(f[i], f[i + 1]), r2);
+        for (int i = 0; i < N / 2; ++i) {
             if constexpr (ENTROPY && DT == kF32) {
-                float lo = lo_f32(d), hi = hi_f32(d);
+                float lo = lo_f32(d[i]), hi = hi_f32(d[i]);
                 asm("max.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(-1000.0f));
                 asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(-1000.0f));
-                d = f32x2(lo, hi);
+                d[i] = f32x2(lo, hi);
             }
-            const uint64_t x = mul_f32x2(d, l2);
+            const uint64_t x = mul_f32x2(d[i], l2);
             const uint64_t e = f32x2(exp2_approx(lo_f32(x)), exp2_approx(hi_f32(x)));
             sum2 = add_f32x2(sum2, e);
-            if (products) first2 = fma_f32x2(d, e, first2);
+            if (products) first2 = fma_f32x2(d[i], e, first2);
         }
     }
 
@@ -529,17 +557,11 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
         Online<DT, true> sums;
         uint32_t most = kNegInfWord<DT>;
         float bound = kLowest;                        // -inf is no candidate
-        auto take = [&](const uint4 &v, int j) {
-            const uint32_t w = vec_max<DT>(v);
-            const float vm = word_max<DT>(w);
-            most = max_word<DT>(most, w);
-            sums.add(v, vm);
-            if (want && vm >= bound) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kList) {
-                    sh.vec[at] = v;
-                    sh.element[at] = s.at(j);
-                }
+        auto candidate = [&](const uint4 &v, int j) {
+            const int at = atomicAdd(&sh.count, 1);
+            if (at < kList) {
+                sh.vec[at] = v;
+                sh.element[at] = s.at(j);
             }
         };
         for (int j0 = s.from, b = 0; j0 < s.to; j0 += kStep, ++b) {
@@ -547,30 +569,49 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
             copies_left<kStages - 2>();
             uint4 cur[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                cur[i] = sh.ring[stage][i][threadIdx.x];
-                if (j + i * kStatThreads >= s.to)
-                    cur[i] = make_uint4(kNegInfWord<DT>, kNegInfWord<DT>, kNegInfWord<DT>,
-                                        kNegInfWord<DT>);
+            for (int i = 0; i < kBatch; ++i) cur[i] = sh.ring[stage][i][threadIdx.x];
+            if (j0 + kStep > s.to) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    if (j + i * kStatThreads >= s.to)
+                        cur[i] = make_uint4(kNegInfWord<DT>, kNegInfWord<DT>, kNegInfWord<DT>,
+                                            kNegInfWord<DT>);
             }
             stage = stage + 1 == kStages ? 0 : stage + 1;
             fetch.next();
+            // one check a batch against the sums' reference and the candidates' bound
+            uint32_t w[kBatch], all = kNegInfWord<DT>;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                w[i] = vec_max<DT>(cur[i]);
+                all = max_word<DT>(all, w[i]);
+            }
+            const float vm = word_max<DT>(all);
             // a bound from the first batch, from the first 4, 16, 64, ...
             if (want && (b == 0 || ((b & (b - 1)) == 0 && (b & 0x55555554)))) {
-                uint32_t w = most;
-                if (b == 0) {
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) w = max_word<DT>(w, vec_max<DT>(cur[i]));
-                }
-                find_bound(word_max<DT>(w), want, sh);
+                find_bound(b == 0 ? vm : word_max<DT>(most), want, sh);
                 bound = fmaxf(sh.bound, kLowest);
             }
+            most = max_word<DT>(most, all);
+            if (vm > sums.limit) sums.raise(vm);
+            if (want && vm >= bound) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) take(cur[i], j + i * kStatThreads);
+                for (int i = 0; i < kBatch; ++i)
+                    if (word_max<DT>(w[i]) >= bound) candidate(cur[i], j + i * kStatThreads);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) sums.add(cur[i]);
         }
         // the vectors filled in part
-        if (threadIdx.x == 0 && s.from > 0) take(s.part(0), 0);
-        if (threadIdx.x == 32 && s.to < s.n) take(s.part(s.to), s.to);
+        const int edge = threadIdx.x == 0 && s.from > 0 ? 0
+                         : threadIdx.x == 32 && s.to < s.n ? s.to : -1;
+        if (edge >= 0) {
+            const uint4 v = s.part(edge);
+            const uint32_t wv = vec_max<DT>(v);
+            most = max_word<DT>(most, wv);
+            sums.add(v, word_max<DT>(wv));
+            if (want && word_max<DT>(wv) >= bound) candidate(v, edge);
+        }
         const Sums mine = warp_join(sums.sums());
         if (lane == 0) sh.warps[warp] = mine;
         if (want) find_bound(word_max<DT>(most), want, sh);
@@ -687,15 +728,15 @@ struct RowShared {
 template <int DT>
 __device__ __forceinline__ void loss_grad(const uint4 &v, float ref, float scale, float *g) {
     constexpr int N = Elem<DT>::kVec;
-    float f[N];
-    Elem<DT>::unpack(v, f);
-    const uint64_t r2 = f32x2(ref, ref), l2 = f32x2(kLog2e, kLog2e), s2 = f32x2(scale, scale);
+    uint64_t d[N / 2];
+    differences<DT>(v, ref, d);
+    const uint64_t l2 = f32x2(kLog2e, kLog2e), s2 = f32x2(scale, scale);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const uint64_t t = mul_f32x2(sub_f32x2(f32x2(f[i], f[i + 1]), r2), l2);
+    for (int i = 0; i < N / 2; ++i) {
+        const uint64_t t = mul_f32x2(d[i], l2);
         const uint64_t p = mul_f32x2(f32x2(exp2_approx(lo_f32(t)), exp2_approx(hi_f32(t))), s2);
-        g[i] = lo_f32(p);
-        g[i + 1] = hi_f32(p);
+        g[2 * i] = lo_f32(p);
+        g[2 * i + 1] = hi_f32(p);
     }
 }
 
