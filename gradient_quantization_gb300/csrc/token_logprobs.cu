@@ -297,16 +297,15 @@ struct Slice {
 // holds, as in ascending rows; fewer than k finite logits; NaN) the slice is read
 // again: elements above the bound and equal to it in two lists, of the equal ones the
 // first in order; and where even the former are too many, the k largest one by one.
-constexpr int kStatThreads = 256, kStatWarps = kStatThreads / 32;
+constexpr int kStatThreads = 128, kStatWarps = kStatThreads / 32;
 constexpr int kBatch = 4;                     // vectors a thread and stage
 constexpr int kStages = 3;                    // of shared memory, each thread's own
 constexpr int kStep = kBatch * kStatThreads;
 constexpr int kGroups = 64, kGroupLanes = kStatThreads / kGroups;
 constexpr int kTopMax = 32;
-constexpr int kList = 768, kShortList = 256;
+constexpr int kList = 512, kShortList = 256;
 constexpr int kMaxCluster = 8;
-static_assert(kTopMax <= kGroups && kMaxCluster * kTopMax <= kShortList &&
-              kMaxCluster * kTopMax <= kStatThreads && 3 * kShortList <= kList,
+static_assert(kTopMax <= kGroups && kMaxCluster * kTopMax <= kShortList && 3 * kShortList <= 2 * kList,
               "lists hold what they must");
 
 struct StatShared {
@@ -532,7 +531,7 @@ struct Fetch {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const TokenLogprobs a) {
+__global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const TokenLogprobs a) {
     constexpr int N = Elem<DT>::kVec;
     extern __shared__ __align__(16) uint8_t shared_bytes[];
     StatShared &sh = *reinterpret_cast<StatShared *>(shared_bytes);
@@ -637,11 +636,15 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
                     }
                 }
                 __syncthreads();
-                const int few = sh.above;
-                if (few > kShortList || (full == -INFINITY && few < want))
-                    read_again<DT>(s, want, false, sh);
-                else
-                    rank_keys(sh.few, few, want, sh.top);
+                int few = sh.above;
+                if (full == -INFINITY && few < want) {
+                    // all finite ones, and the first of the others
+                    if (warp == 0) first_equal<DT>(s, want - few, full, sh.few + few);
+                    few = min(want, s.end() - s.first());
+                    __syncthreads();
+                }
+                if (few > kShortList) read_again<DT>(s, want, false, sh);
+                else rank_keys(sh.few, few, want, sh.top);
             }
         }
         if (C > 1) {
@@ -672,9 +675,7 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
             }
             if (want && C > 1) {
                 // the slices' alternatives: those that reach every slice's last one
-                const int i = threadIdx.x;
-                uint64_t key = 0, least = 0;
-                if (i < C * want) key = cluster.map_shared_rank(&sh, i / want)->top[i % want];
+                uint64_t least = 0;
                 if (lane < C) least = cluster.map_shared_rank(&sh, lane)->top[want - 1];
 #pragma unroll
                 for (int o = 1; o < kMaxCluster; o <<= 1) {
@@ -684,7 +685,10 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
                 least = __shfl_sync(0xFFFFFFFFu, least, 0);
                 if (threadIdx.x == 0) sh.count = 0;
                 __syncthreads();
-                if (key != 0 && key >= least) sh.list[atomicAdd(&sh.count, 1)] = key;
+                for (int i = threadIdx.x; i < C * want; i += kStatThreads) {
+                    const uint64_t key = cluster.map_shared_rank(&sh, i / want)->top[i % want];
+                    if (key != 0 && key >= least) sh.list[atomicAdd(&sh.count, 1)] = key;
+                }
                 __syncthreads();
                 rank_keys(sh.list, sh.count, want, sh.top);
                 __syncthreads();
@@ -709,6 +713,7 @@ __global__ void __launch_bounds__(kStatThreads, 3) token_stats_kernel(const Toke
 // logits are read once.  Join of the CTAs' sums through distributed shared memory.
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kSliceBytes = 72 * 1024;        // three CTAs an SM
+constexpr int64_t kOneSliceBytes = 108 * 1024;   // two, where that saves the cluster
 constexpr int kMaxSliceBytes = 216 * 1024;    // one CTA an SM
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -864,24 +869,26 @@ __global__ void __launch_bounds__(kRowThreads, 3) token_loss_kernel(const TokenL
     }
 }
 
-// The CTAs of a row's cluster in the loss: slices of at most kSliceBytes where eight
-// CTAs allow it (three CTAs an SM, whose copies and passes overlap), and more CTAs a
-// row while the rows alone do not fill two CTAs an SM, down to 4 KB.  0: the row
-// does not fit on chip.
+// The CTAs of a row's cluster in the loss: one for rows of up to kOneSliceBytes (4096
+// rows of 100 KB: 126 us, 138 us as two slices), else slices of at most kSliceBytes
+// where eight CTAs allow it (three CTAs an SM, whose copies and passes overlap: 1021
+// rows of 200 KB took 91 us as four slices, 98 us as two), and more CTAs a row while
+// the rows alone do not fill two CTAs an SM, down to 4 KB.  0: the row does not fit on
+// chip.
 int loss_cluster(int64_t T, int64_t V, int size) {
     const int64_t bytes = V * size + 16;
     int c = 1;
-    while (c < kMaxCluster && bytes > c * (int64_t)kSliceBytes) c *= 2;
+    while (c < kMaxCluster && bytes > (c == 1 ? kOneSliceBytes : c * (int64_t)kSliceBytes)) c *= 2;
     if (bytes > c * (int64_t)kMaxSliceBytes) return 0;
     while (c < kMaxCluster && T * c < 2 * sm_count() && bytes > c * 8192ll) c *= 2;
     return c;
 }
 
 // The CTAs of a row's cluster in the statistics: one, and more while the rows do not
-// fill two CTAs an SM, down to 8 KB.
+// fill two CTAs an SM, down to 4 KB.
 int stats_cluster(int64_t T, int64_t V, int size) {
     int c = 1;
-    while (c < kMaxCluster && T * c < 2 * sm_count() && V * size > c * 16384ll) c *= 2;
+    while (c < kMaxCluster && T * c < 2 * sm_count() && V * size > c * 8192ll) c *= 2;
     return c;
 }
 
@@ -919,8 +926,9 @@ cudaError_t launch_stats(const TokenLogprobs &a, cudaStream_t st) {
     const cudaError_t e = allow_shared(kernel, sizeof(StatShared), ready);
     if (e != cudaSuccess) return e;
     const int c = stats_cluster(a.T, a.V, Elem<DT>::kSize);
-    const int64_t most = 3 * sm_count() / c, rows = a.T < most ? a.T : most;
-    return launch_pdl_clusters(kernel, (int)rows * c, kStatThreads, c, sizeof(StatShared), st, a);
+    const int64_t most = 6 * sm_count() / c;
+    const int rows = (int)(a.T < most ? a.T : most);
+    return launch_pdl_clusters(kernel, rows * c, kStatThreads, c, sizeof(StatShared), st, a);
 }
 
 template <int DT>
