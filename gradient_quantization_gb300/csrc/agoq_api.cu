@@ -645,10 +645,8 @@ agoq_status agoq_clip_grad_norm(const agoq_grad_tensor *tensors, int count, floa
     const agoq_status s = grad_norm_ok(tensors, count, true, norm, workspace, workspace_bytes);
     if (s != AGOQ_OK) return s;
     if (!(max_norm >= 0.0f) || max_norm > 3.0e38f) return AGOQ_ERR_SHAPE;
-    const cudaError_t e = launch_grad_norm(tensors, count, norm, static_cast<double *>(workspace),
-                                           as_stream(stream));
-    if (e != cudaSuccess) return from_cuda(e);
-    return from_cuda(launch_clip_grads(tensors, count, max_norm, norm, as_stream(stream)));
+    return from_cuda(launch_clip_grad_norm(tensors, count, max_norm, norm,
+                                           static_cast<double *>(workspace), as_stream(stream)));
 }
 
 agoq_status agoq_token_logprobs(const void *logits, int64_t ld, int dtype, const int64_t *tokens,

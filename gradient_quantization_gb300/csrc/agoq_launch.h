@@ -154,6 +154,8 @@ cudaError_t launch_grad_norm(const agoq_grad_tensor *tensors, int count, float *
                              double *workspace, cudaStream_t st);
 cudaError_t launch_clip_grads(const agoq_grad_tensor *tensors, int count, float max_norm,
                               const float *norm, cudaStream_t st);
+cudaError_t launch_clip_grad_norm(const agoq_grad_tensor *tensors, int count, float max_norm,
+                                  float *norm, double *workspace, cudaStream_t st);
 // Token log probabilities (token_logprobs.cu); row distances in elements.
 struct TokenLogprobs {
     const void *logits;
