@@ -29,6 +29,19 @@ int resident_per_sm(K kernel, int threads, size_t smem, int *cache) {
     return cache[dev];
 }
 
+// Allow `kernel` `bytes` of dynamic shared memory (once a device).
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes, bool *ready) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDevices) dev = 0;
+    if (ready[dev]) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    ready[dev] = e == cudaSuccess;
+    return e;
+}
+
 // Launch `kernel` with programmatic stream serialization: it may be scheduled
 // while the previous kernel on the stream is finishing.  Every kernel launched
 // this way begins with pdl_wait_and_release() (griddepcontrol.wait) before

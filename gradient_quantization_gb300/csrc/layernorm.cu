@@ -26,6 +26,15 @@ __device__ __forceinline__ float param(const void *p, bool f32, int64_t i, float
     return f32 ? load_elem<kF32>(p, i) : load_elem<DT>(p, i);
 }
 
+// fl(s / n) for n >= 1 with inv = fl(1 / n): the product, corrected by its remainder
+// (P. Markstein, IBM J. Res. Dev. 34(1), 1990); a quotient that overflows or is not
+// finite stays as the product gives it.
+__device__ __forceinline__ float divided(float s, float n, float inv) {
+    const float q = __fmul_rn(s, inv);
+    const float c = __fmaf_rn(__fmaf_rn(-q, n, s), inv, q);
+    return fabsf(q) < 3e38f && fabsf(s) > 1e-30f ? c : q;
+}
+
 // LAAQ codes of a block of 128 BF16 values held by a half warp, lane c (0..15)
 // having elements 8c..8c+7; the same codes and scale as agoq_quant_act.  All
 // lanes of the warp call it; `valid` gates the stores.
@@ -77,6 +86,219 @@ __global__ void __launch_bounds__(kThreads) ln_forward_kernel(
         if (threadIdx.x == 0) {
             if (mean) mean[t] = mu;
             if (rstd) rstd[t] = r;
+        }
+    }
+}
+
+// Threads that share a row: the CTA, or for short rows one of several groups of
+// whole warps in it, each with rows of its own and a barrier of its own.
+struct Group {
+    int size, id, tid;            // threads; which of the CTA's groups; thread in the group
+    __device__ __forceinline__ explicit Group(int size_)
+        : size(size_), id(threadIdx.x / size_), tid(threadIdx.x % size_) {}
+    __device__ __forceinline__ void sync() const {
+        asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(size) : "memory");
+    }
+};
+
+// The sums of the group's values (each thread gets them), in a fixed order; `red`
+// holds 32 floats a value and is free again after the group's next barrier.
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float *red, const Group &g) {
+    const int lane = threadIdx.x & 31, warp = g.tid >> 5, warps = g.size >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    if (warps == 1) return;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[32 * i + warp] = v[i];
+    }
+    g.sync();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? red[32 * i + lane] : 0.0f);
+}
+constexpr int kMaxGroups = 8;                 // of a CTA
+
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Parameters of the elements that a thread of a group holds: vectors tid, tid + size,
+// ..., NV of them.
+template <int DT, int NV>
+__device__ __forceinline__ void load_params(const void *p, bool f32, int vectors, float none,
+                                            const Group &g, float *f) {
+    constexpr int V = Elem<DT>::kVec;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int j = g.tid + i * g.size;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            f[i * V + k] = j < vectors ? param<DT>(p, f32, (int64_t)j * V + k, none) : 0.0f;
+    }
+}
+
+// Rows that start at 16-byte boundaries and hold whole vectors: a group of threads a
+// row and step, NV vectors a thread, the row in registers from its one reading to
+// its writing.  Copies into a ring of shared memory run kRing - 1 rows ahead; a thread
+// reads only what it copied, so the ring needs no barrier.  BITS: the codes of x too,
+// a half warp holding a block of 128.
+template <int NV>
+constexpr int kRing = NV == 4 ? 3 : 4;       // stages (1024 threads: 192 KB)
+
+template <int DT, int BITS, int NV>
+__global__ void __launch_bounds__(NV == 4 ? 1024 : 512)
+ln_forward_rows_kernel(const LnForward a, int size) {
+    using E = Elem<DT>;
+    constexpr int V = E::kVec, F = NV * V;
+    constexpr int kStages = kRing<NV>;
+    constexpr bool kKeep = F <= 16;      // w and b stay in registers
+    extern __shared__ __align__(16) uint4 ring[];
+    __shared__ float red[kMaxGroups][2][32];
+    const Group g(size);
+    const int threads = blockDim.x, vectors = (int)(a.H / V);
+    const int64_t step = (int64_t)gridDim.x * (threads / size);
+    const int64_t first = (int64_t)blockIdx.x * (threads / size) + g.id;
+    const float inv = __frcp_rn((float)a.H);
+    pdl_wait_and_release();
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < a.T) {
+            const uint4 *row = reinterpret_cast<const uint4 *>(elem_at<DT>(a.x, t * a.ldx));
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (g.tid + i * size < vectors)
+                    copy16(ring + (stage * NV + i) * threads + threadIdx.x, row + g.tid + i * size);
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
+    float w[kKeep ? F : 1], b[kKeep ? F : 1];
+    if constexpr (kKeep) {
+        load_params<DT, NV>(a.w, a.param_f32, vectors, 1.0f, g, w);
+        load_params<DT, NV>(a.b, a.param_f32, vectors, 0.0f, g, b);
+    }
+    int stage = 0;
+    for (int64_t t = first; t < a.T; t += step) {
+        copies_left<kStages - 2>();
+        uint4 v[NV];
+        float f[F];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (g.tid + i * size < vectors) v[i] = ring[(stage * NV + i) * threads + threadIdx.x];
+            E::unpack(v[i], f + i * V);
+        }
+        fetch(t + (kStages - 1) * step, (stage + kStages - 1) % kStages);
+        stage = (stage + 1) % kStages;
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < F; ++i) s[0] = __fadd_rn(s[0], f[i]);
+        row_sums(s, red[g.id][0], g);
+        const float mu = divided(s[0], (float)a.H, inv);
+        float q[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (g.tid + i * size >= vectors) continue;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float d = __fsub_rn(f[i * V + k], mu);
+                q[0] = __fmaf_rn(d, d, q[0]);
+            }
+        }
+        row_sums(q, red[g.id][1], g);
+        const float var = divided(q[0], (float)a.H, inv);
+        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(var, a.eps)));
+        uint4 *out = reinterpret_cast<uint4 *>(elem_at<DT>(a.y, t * a.ldy));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = g.tid + i * size;
+            if (j < vectors) {
+                float y[V];
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float xh = __fmul_rn(__fsub_rn(f[i * V + k], mu), r);
+                    const int64_t e = (int64_t)j * V + k;
+                    y[k] = kKeep ? __fmaf_rn(xh, w[kKeep ? i * V + k : 0], b[kKeep ? i * V + k : 0])
+                                 : __fmaf_rn(xh, param<DT>(a.w, a.param_f32, e, 1.0f),
+                                             param<DT>(a.b, a.param_f32, e, 0.0f));
+                }
+                out[j] = E::pack(y);
+            }
+            if constexpr (BITS != 0) {
+                const int64_t blk = t * (a.H / kBlock) + j / 16;
+                quantize_block16<BITS>(v[i], threadIdx.x & 15,
+                                       static_cast<uint32_t *>(a.codes) + blk * 4 * BITS,
+                                       a.scales + blk, j < vectors);
+            }
+        }
+        if (g.tid == 0) {
+            if (a.mean) a.mean[t] = mu;
+            if (a.rstd) a.rstd[t] = r;
+        }
+    }
+}
+
+// Rows of any alignment: the same, an element a thread and step, NE elements a
+// thread; the next row's elements are loaded before this one's sums.
+template <int DT, int NE>
+__global__ void __launch_bounds__(1024) ln_forward_elems_kernel(const LnForward a) {
+    using E = Elem<DT>;
+    using Word = typename E::Word;
+    __shared__ float red[2][32];
+    const Group g(blockDim.x);
+    const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H;
+    const float inv = __frcp_rn((float)a.H);
+    pdl_wait_and_release();
+    Word next[NE];
+    auto fetch = [&](int64_t t) {
+        const Word *row = reinterpret_cast<const Word *>(elem_at<DT>(a.x, t * a.ldx));
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            next[i] = Word(0);
+            if (tid + i * threads < H) next[i] = row[tid + i * threads];
+        }
+    };
+    if (blockIdx.x < a.T) fetch(blockIdx.x);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        float f[NE];
+#pragma unroll
+        for (int i = 0; i < NE; ++i) f[i] = E::up(next[i]);
+        if (t + gridDim.x < a.T) fetch(t + gridDim.x);
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NE; ++i) s[0] = __fadd_rn(s[0], f[i]);
+        row_sums(s, red[0], g);
+        const float mu = divided(s[0], (float)a.H, inv);
+        float q[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const float d = __fsub_rn(f[i], mu);
+            if (tid + i * threads < H) q[0] = __fmaf_rn(d, d, q[0]);
+        }
+        row_sums(q, red[1], g);
+        const float var = divided(q[0], (float)a.H, inv);
+        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(var, a.eps)));
+        char *out = elem_at<DT>(a.y, t * a.ldy);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int e = tid + i * threads;
+            if (e >= H) break;
+            const float xh = __fmul_rn(__fsub_rn(f[i], mu), r);
+            store_elem<DT>(out, e, __fmaf_rn(xh, param<DT>(a.w, a.param_f32, e, 1.0f),
+                                             param<DT>(a.b, a.param_f32, e, 0.0f)));
+        }
+        if (tid == 0) {
+            if (a.mean) a.mean[t] = mu;
+            if (a.rstd) a.rstd[t] = r;
         }
     }
 }
@@ -188,18 +410,194 @@ __global__ void __launch_bounds__(kThreads) ln_backward_kernel(
     }
 }
 
-// dw and db: the P partial rows in order.
+// Rows that start at 16-byte boundaries and hold whole vectors: as the forward pass,
+// x and dy read once, dx written once.  A thread adds its columns' terms of dw and db
+// in registers over all rows of its group; the groups of a CTA join theirs in order,
+// and the CTA writes one row of the partial sums ([grid][2][H]).
+template <int DT, int BITS, int NV>
+__global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward a, int size) {
+    using E = Elem<DT>;
+    constexpr int V = E::kVec, F = NV * V;
+    constexpr int kStages = kRing<NV>, kWords = 4 * BITS;
+    constexpr int kParts = BITS ? 1 : 2;             // dy, and x
+    extern __shared__ __align__(16) uint4 ring[];
+    __shared__ float red[kMaxGroups][2][64];
+    const Group g(size);
+    const int threads = blockDim.x, vectors = (int)(a.H / V), groups = threads / size;
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const int64_t first = (int64_t)blockIdx.x * groups + g.id;
+    const float inv = __frcp_rn((float)a.H);
+    const bool sums = a.dw || a.db;
+    pdl_wait_and_release();
+    // slot i of part p of a stage
+    auto slot = [&](int stage, int p, int i) {
+        return ring + ((stage * kParts + p) * NV + i) * threads + threadIdx.x;
+    };
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < a.T) {
+            const uint4 *dy = reinterpret_cast<const uint4 *>(elem_at<DT>(a.dy, t * a.lddy));
+            const uint4 *x = reinterpret_cast<const uint4 *>(elem_at<DT>(a.x, BITS ? 0 : t * a.ldx));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (g.tid + i * size < vectors) {
+                    copy16(slot(stage, 0, i), dy + g.tid + i * size);
+                    if constexpr (BITS == 0) copy16(slot(stage, 1, i), x + g.tid + i * size);
+                }
+            }
+        }
+        copies_commit();
+    };
+    // what does not come in 16-byte copies is loaded a row ahead into registers
+    uint32_t lo[BITS ? NV : 1], hi[BITS ? NV : 1];
+    float scale[BITS ? NV : 1], mean = 0.0f, rstd = 0.0f;
+    auto ahead = [&](int64_t t) {
+        if (t >= a.T) return;
+        if constexpr (BITS == 0) {
+            mean = __ldg(a.mean + t);
+            rstd = __ldg(a.rstd + t);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int j = g.tid + i * size;
+                if (j >= vectors) continue;
+                const int64_t blk = t * (a.H / kBlock) + j / 16;
+                load_chunk<BITS>(static_cast<const uint32_t *>(a.x) + blk * kWords, j & 15, lo[i], hi[i]);
+                scale[i] = __ldg(a.scales + blk);
+            }
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
+    ahead(first);
+    float w[F], dw[F], db[F];
+    load_params<DT, NV>(a.w, a.param_f32, vectors, 1.0f, g, w);
+#pragma unroll
+    for (int i = 0; i < F; ++i) dw[i] = db[i] = 0.0f;
+    int stage = 0;
+    for (int64_t t = first; t < a.T; t += step) {
+        copies_left<kStages - 2>();
+        float x[F], d[F];                 // x, then xh; dy
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            uint4 vx = make_uint4(0, 0, 0, 0), vd = vx;
+            if (g.tid + i * size < vectors) {
+                vd = *slot(stage, 0, i);
+                if constexpr (BITS == 0) vx = *slot(stage, 1, i);
+                else vx = dequantize_chunk<BITS>(lo[i], hi[i], scale[i]);
+            }
+            E::unpack(vx, x + i * V);
+            E::unpack(vd, d + i * V);
+        }
+        float mu = mean, r = rstd;
+        fetch(t + (kStages - 1) * step, (stage + kStages - 1) % kStages);
+        ahead(t + step);
+        stage = (stage + 1) % kStages;
+        float s0, s1;
+        if constexpr (BITS == 0) {
+            float s[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                x[i] = __fmul_rn(__fsub_rn(x[i], mu), r);
+                const float gi = __fmul_rn(d[i], w[i]);
+                s[0] = __fadd_rn(s[0], gi);
+                s[1] = __fmaf_rn(gi, x[i], s[1]);
+            }
+            row_sums(s, red[g.id][(t / step) & 1], g);
+            s0 = divided(s[0], (float)a.H, inv);
+            s1 = divided(s[1], (float)a.H, inv);
+        } else {
+            float s[2] = {0.0f, 0.0f}, q[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                s[0] = __fadd_rn(s[0], x[i]);
+                s[1] = __fmaf_rn(d[i], w[i], s[1]);
+            }
+            row_sums(s, red[g.id][0], g);
+            mu = divided(s[0], (float)a.H, inv);
+            s0 = divided(s[1], (float)a.H, inv);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const bool in = g.tid + i * size < vectors;
+#pragma unroll
+                for (int k = i * V; k < (i + 1) * V; ++k) {
+                    x[k] = in ? __fsub_rn(x[k], mu) : 0.0f;
+                    q[0] = __fmaf_rn(x[k], x[k], q[0]);
+                    q[1] = __fmaf_rn(__fmul_rn(d[k], w[k]), x[k], q[1]);
+                }
+            }
+            row_sums(q, red[g.id][1], g);
+            const float var = divided(q[0], (float)a.H, inv);
+            r = __frcp_rn(__fsqrt_rn(__fadd_rn(var, a.eps)));
+            s1 = divided(__fmul_rn(q[1], r), (float)a.H, inv);
+#pragma unroll
+            for (int i = 0; i < F; ++i) x[i] = __fmul_rn(x[i], r);
+        }
+        uint4 *out = reinterpret_cast<uint4 *>(elem_at<DT>(a.dx, t * a.lddx));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (g.tid + i * size >= vectors) continue;
+            float o[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int n = i * V + k;
+                o[k] = __fmul_rn(r, __fmaf_rn(-x[n], s1, __fsub_rn(__fmul_rn(d[n], w[n]), s0)));
+                dw[n] = __fmaf_rn(d[n], x[n], dw[n]);
+                db[n] = __fadd_rn(db[n], d[n]);
+            }
+            out[g.tid + i * size] = E::pack(o);
+        }
+    }
+    if (!sums) return;
+    float *mine = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
+    float *joined = reinterpret_cast<float *>(ring);          // [2][H], for several groups
+    copies_left<0>();
+    for (int who = 0; who < groups; ++who) {
+        if (groups > 1) __syncthreads();
+        if (g.id != who) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = g.tid + i * size;
+            if (j >= vectors) continue;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                float *pw = (groups > 1 ? joined : mine) + j * V + k, *pb = pw + a.H;
+                const int n = i * V + k;
+                *pw = groups > 1 && who > 0 ? __fadd_rn(*pw, dw[n]) : dw[n];
+                *pb = groups > 1 && who > 0 ? __fadd_rn(*pb, db[n]) : db[n];
+            }
+        }
+    }
+    if (groups > 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * (int)a.H; i += threads) mine[i] = joined[i];
+    }
+}
+
+// dw and db: the P partial rows.  A CTA takes 32 columns; its eight warps add every
+// eighth row, and their sums are added in order.
 __global__ void __launch_bounds__(kThreads) ln_backward_join_kernel(
     const float *__restrict__ partials, int64_t H, int P, float *__restrict__ dw,
     float *__restrict__ db) {
     pdl_wait_and_release();
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < 2 * H;
-         i += (int64_t)gridDim.x * kThreads) {
+    __shared__ float sums[kWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < 2 * H; c0 += (int64_t)gridDim.x * 32) {
+        const int64_t i = c0 + lane;
         float *out = i < H ? dw : db;
-        if (!out) continue;
         float s = 0.0f;
-        for (int p = 0; p < P; ++p) s = __fadd_rn(s, __ldg(partials + (int64_t)p * 2 * H + i));
-        out[i < H ? i : i - H] = s;
+        if (i < 2 * H && out) {
+#pragma unroll 8
+            for (int p = warp; p < P; p += kWarps)
+                s = __fadd_rn(s, __ldg(partials + (int64_t)p * 2 * H + i));
+        }
+        sums[warp][lane] = s;
+        __syncthreads();
+        if (warp == 0 && i < 2 * H && out) {
+#pragma unroll
+            for (int k = 1; k < kWarps; ++k) s = __fadd_rn(s, sums[k][lane]);
+            out[i < H ? i : i - H] = s;
+        }
+        __syncthreads();
     }
 }
 
@@ -208,22 +606,110 @@ int grid_for(int64_t units, int per_sm) {
     return (int)(units < most ? (units > 0 ? units : 1) : most);
 }
 
+bool on16(const void *p, int64_t ld, int size) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
+}
+
+int threads_for(int64_t units, int per) {
+    const int64_t t = (units + per - 1) / per;
+    return (int)((t + 31) / 32 * 32);
+}
+
+// CTAs of a kernel whose CTAs stay for many units of work: as many as are resident.
+template <typename K>
+int resident_ctas(K kernel, int threads, size_t smem, int64_t units) {
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    return grid_for(units, per_sm > 0 ? per_sm : 1);
+}
+
+// Groups of `size` threads in a CTA: 256 threads, for rows shorter than that.
+int groups_of(int size) { return size <= 128 ? 256 / size : 1; }
+
+template <int DT, int BITS, int NV>
+cudaError_t forward_rows(const LnForward &a, cudaStream_t st) {
+    const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
+    const int threads = size * groups;
+    const size_t smem = (size_t)kRing<NV> * NV * threads * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_forward_rows_kernel<DT, BITS, NV>;
+    const cudaError_t e =
+        allow_shared(kernel, (size_t)kRing<NV> * NV * (NV == 4 ? 1024 : 512) * 16, ready);
+    if (e != cudaSuccess) return e;
+    const int ctas = resident_ctas(kernel, threads, smem, (a.T + groups - 1) / groups);
+    return launch_pdl_clusters(kernel, ctas, threads, 1, smem, st, a, size);
+}
+
+template <int DT, int NE>
+cudaError_t forward_elems(const LnForward &a, cudaStream_t st) {
+    const int threads = threads_for(a.H, NE);
+    auto kernel = ln_forward_elems_kernel<DT, NE>;
+    return launch_pdl_clusters(kernel, resident_ctas(kernel, threads, 0, a.T), threads, 1, 0, st, a);
+}
+
+// Vectors a thread: one for rows of up to 128 vectors (few threads a row wait for one
+// another less), two up to 1024 (512 threads), four up to 4096.  0: no row of vectors.
+template <int DT>
+int row_vectors(int64_t H) {
+    constexpr int V = Elem<DT>::kVec;
+    if (H % V) return 0;
+    const int64_t n = H / V;
+    return n <= 128 ? 1 : n <= 1024 ? 2 : n <= 4096 ? 4 : 0;
+}
+
+template <int DT, int BITS>
+cudaError_t forward_bits(const LnForward &a, cudaStream_t st) {
+    if (on16(a.x, a.ldx, Elem<DT>::kSize) && on16(a.y, a.ldy, Elem<DT>::kSize)) {
+        switch (row_vectors<DT>(a.H)) {
+            case 1: return forward_rows<DT, BITS, 1>(a, st);
+            case 2: return forward_rows<DT, BITS, 2>(a, st);
+            case 4: return forward_rows<DT, BITS, 4>(a, st);
+        }
+    }
+    if (a.H <= 512) return forward_elems<DT, 4>(a, st);
+    if (a.H <= 16384) return forward_elems<DT, 16>(a, st);
+    return launch_pdl(ln_forward_kernel<DT>, grid_for(a.T, 8), kThreads, 0, st, a.x, a.ldx, a.w, a.b,
+                      a.param_f32, a.T, a.H, a.eps, a.y, a.ldy, a.mean, a.rstd);
+}
+
+// Where dw or db is wanted, the partial sums of P CTAs become dw and db.
+cudaError_t join(const LnBackward &a, int P, cudaStream_t st) {
+    if (!a.dw && !a.db) return cudaSuccess;
+    return launch_pdl(ln_backward_join_kernel, grid_for((2 * a.H + 31) / 32, 8), kThreads, 0, st,
+                      a.workspace, a.H, P, a.dw, a.db);
+}
+
+template <int DT, int BITS, int NV>
+cudaError_t backward_rows(const LnBackward &a, cudaStream_t st) {
+    const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
+    const int threads = size * groups;
+    constexpr int kSlots = kRing<NV> * NV * (BITS ? 1 : 2);
+    const size_t smem = (size_t)kSlots * threads * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_backward_rows_kernel<DT, BITS, NV>;
+    const cudaError_t e = allow_shared(kernel, (size_t)kSlots * 512 * 16, ready);
+    if (e != cudaSuccess) return e;
+    int P = resident_ctas(kernel, threads, smem, (a.T + groups - 1) / groups);
+    if (P > kLnPartials) P = kLnPartials;
+    const cudaError_t r = launch_pdl_clusters(kernel, P, threads, 1, smem, st, a, size);
+    return r != cudaSuccess ? r : join(a, P, st);
+}
+
+// Elements a thread holds: eight for rows of up to 2048, sixteen up to 8192 (more
+// would not leave registers for dw and db).
 template <int DT, int BITS>
 cudaError_t backward(const Input<DT, BITS> &in, const LnBackward &a, cudaStream_t st) {
+    constexpr int kSize = Elem<DT>::kSize, V = Elem<DT>::kVec;
+    if ((BITS || on16(a.x, a.ldx, kSize)) && on16(a.dy, a.lddy, kSize) && on16(a.dx, a.lddx, kSize) &&
+        a.H % V == 0 && a.H <= 8192)
+        return a.H <= 2048 ? backward_rows<DT, BITS, 8 / V>(a, st)
+                           : backward_rows<DT, BITS, 16 / V>(a, st);
     const bool sums = a.dw || a.db;
     const int P = sums ? ln_partials(a.T) : grid_for(a.T, 8);
     const cudaError_t e = launch_pdl(ln_backward_kernel<DT, BITS>, P, kThreads, 0, st, in, a.dy,
                                      a.lddy, a.w, a.param_f32, a.mean, a.rstd, a.T, a.H, a.eps,
                                      a.dx, a.lddx, sums ? a.workspace : nullptr);
-    if (e != cudaSuccess || !sums) return e;
-    return launch_pdl(ln_backward_join_kernel, grid_for((2 * a.H + kThreads - 1) / kThreads, 8),
-                      kThreads, 0, st, a.workspace, a.H, P, a.dw, a.db);
-}
-
-template <int DT>
-cudaError_t forward(const LnForward &a, cudaStream_t st) {
-    return launch_pdl(ln_forward_kernel<DT>, grid_for(a.T, 8), kThreads, 0, st, a.x, a.ldx, a.w, a.b,
-                      a.param_f32, a.T, a.H, a.eps, a.y, a.ldy, a.mean, a.rstd);
+    return e != cudaSuccess ? e : join(a, P, st);
 }
 
 template <int BITS>
@@ -239,15 +725,23 @@ cudaError_t codes(const LnForward &a, cudaStream_t st) {
 int ln_partials(int64_t T) { return (int)(T < kLnPartials ? T : kLnPartials); }
 
 cudaError_t launch_ln_forward(const LnForward &a, cudaStream_t st) {
-    cudaError_t e = a.dtype == kF32    ? forward<kF32>(a, st)
-                    : a.dtype == kBF16 ? forward<kBF16>(a, st)
-                                       : forward<kF16>(a, st);
-    if (e != cudaSuccess || !a.codes) return e;
+    if (a.dtype == kF32) return forward_bits<kF32, 0>(a, st);
+    if (a.dtype == kF16) return forward_bits<kF16, 0>(a, st);
+    if (!a.codes) return forward_bits<kBF16, 0>(a, st);
+    // y may be x's place: rows that the norm does not quantize are quantized first
+    const bool rows = on16(a.x, a.ldx, 2) && on16(a.y, a.ldy, 2) && row_vectors<kBF16>(a.H);
+    if (!rows) {
+        const cudaError_t e = a.bits == 4   ? codes<4>(a, st)
+                              : a.bits == 5 ? codes<5>(a, st)
+                              : a.bits == 6 ? codes<6>(a, st)
+                                            : codes<8>(a, st);
+        return e != cudaSuccess ? e : forward_bits<kBF16, 0>(a, st);
+    }
     switch (a.bits) {
-        case 4: return codes<4>(a, st);
-        case 5: return codes<5>(a, st);
-        case 6: return codes<6>(a, st);
-        default: return codes<8>(a, st);
+        case 4: return forward_bits<kBF16, 4>(a, st);
+        case 5: return forward_bits<kBF16, 5>(a, st);
+        case 6: return forward_bits<kBF16, 6>(a, st);
+        default: return forward_bits<kBF16, 8>(a, st);
     }
 }
 

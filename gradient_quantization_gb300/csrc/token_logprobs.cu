@@ -894,19 +894,6 @@ int stats_cluster(int64_t T, int64_t V, int size) {
 
 int row_grid(int64_t T, int c) { return (int)(T < (1 << 24) ? T : 1 << 24) * c; }
 
-// Allow `kernel` `bytes` of dynamic shared memory (once a device).
-template <typename K>
-cudaError_t allow_shared(K kernel, size_t bytes, bool *ready) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= kMaxDevices) dev = 0;
-    if (ready[dev]) return cudaSuccess;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    ready[dev] = e == cudaSuccess;
-    return e;
-}
-
 template <int DT>
 cudaError_t launch_loss(const TokenLogprobs &a, int c, cudaStream_t st) {
     static bool ready[kMaxDevices];
