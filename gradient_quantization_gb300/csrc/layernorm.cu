@@ -35,26 +35,6 @@ __device__ __forceinline__ float divided(float s, float n, float inv) {
     return fabsf(q) < 3e38f && fabsf(s) > 1e-30f ? c : q;
 }
 
-// LAAQ codes of a block of 128 BF16 values held by a half warp, lane c (0..15)
-// having elements 8c..8c+7; the same codes and scale as agoq_quant_act.  All
-// lanes of the warp call it; `valid` gates the stores.
-template <int BITS>
-__device__ __forceinline__ void quantize_block16(const uint4 &v, int c, uint32_t *rec, float *scale,
-                                                 bool valid) {
-    constexpr int kQmax = (1 << (BITS - 1)) - 1;
-    constexpr int kBias = BITS < 8 ? 1 << (BITS - 1) : 0;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    const float s = bf16_div_qmax<kQmax>(halfwarp_max(bf16_absmax<4>(w)));
-    float f[8];
-    Elem<kBF16>::unpack(v, f);
-    uint32_t cb[8], lo, hi;
-    integer_codes_n<kQmax, 8, kBias>(f, s, cb);
-    if constexpr (BITS < 8) pack_biased8<BITS>(cb, lo, hi);
-    else pack_fields8<BITS>(cb, lo, hi);
-    store_chunk<BITS>(rec, c, lo, hi, valid);
-    if (valid && c == 0) *scale = s;
-}
-
 // ---- forward ------------------------------------------------------------------
 
 // One CTA a row, one element a thread and step; any length, stride and
@@ -90,8 +70,12 @@ __global__ void __launch_bounds__(kThreads) ln_forward_kernel(
     }
 }
 
-// Threads that share a row: the CTA, or for short rows one of several groups of
-// whole warps in it, each with rows of its own and a barrier of its own.
+// ---- rows of vectors ------------------------------------------------------------
+
+// Threads that share a row: the CTA, or for short rows one of several groups in it
+// (8, 16 or 32 lanes, or whole warps with a barrier of their own), each with rows of
+// its own.
+constexpr int kMaxGroups = 4;                 // of more than one warp, in a CTA
 struct Group {
     int size, id, tid;            // threads; which of the CTA's groups; thread in the group
     __device__ __forceinline__ explicit Group(int size_)
@@ -102,13 +86,20 @@ struct Group {
 };
 
 // The sums of the group's values (each thread gets them), in a fixed order; `red`
-// holds 32 floats a value and is free again after the group's next barrier.
+// holds 32 floats a value and is free again after the group's next barrier.  All
+// threads of a warp call it.
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float *red, const Group &g) {
-    const int lane = threadIdx.x & 31, warp = g.tid >> 5, warps = g.size >> 5;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-    if (warps == 1) return;
+    for (int o = 16; o > 0; o >>= 1) {
+        if (o < g.size) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], o));
+        }
+    }
+    if (g.size <= 32) return;
+    const int warp = g.tid >> 5, warps = g.size >> 5;
     if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < N; ++i) red[32 * i + warp] = v[i];
@@ -117,185 +108,327 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float *red, const Group 
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? red[32 * i + lane] : 0.0f);
 }
-constexpr int kMaxGroups = 8;                 // of a CTA
 
-__device__ __forceinline__ void copy16(void *to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
-                 "l"(from)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_left() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// The i-th of the NV vectors of a row that a thread of a group holds.  16-bit types:
+// an octet of lanes holds blocks of 128 elements, lane j their vectors j and j + 8.
+template <int DT>
+__device__ __forceinline__ int place(const Group &g, int i) {
+    if constexpr (DT == kF32) return g.tid + i * g.size;
+    else return (g.tid >> 3) * 16 + (g.tid & 7) + 8 * (i & 1) + (i >> 1) * 2 * g.size;
 }
 
-// Parameters of the elements that a thread of a group holds: vectors tid, tid + size,
-// ..., NV of them.
-template <int DT, int NV>
-__device__ __forceinline__ void load_params(const void *p, bool f32, int vectors, float none,
-                                            const Group &g, float *f) {
+// Weight or bias of vector j, in pairs (FP32, or the type of the activation).
+template <int DT>
+__device__ __forceinline__ void load_params(const void *p, bool f32, int j, float none,
+                                            uint64_t *out) {
     constexpr int V = Elem<DT>::kVec;
+    float f[V];
+    const char *at = static_cast<const char *>(p) + (int64_t)j * V * (f32 ? 4 : Elem<DT>::kSize);
+    if (!p) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = g.tid + i * g.size;
+        for (int k = 0; k < V; ++k) f[k] = none;
+    } else if (reinterpret_cast<uintptr_t>(p) & 15u) {
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            f[i * V + k] = j < vectors ? param<DT>(p, f32, (int64_t)j * V + k, none) : 0.0f;
+        for (int k = 0; k < V; ++k) f[k] = param<DT>(p, f32, (int64_t)j * V + k, none);
+    } else if (!f32) {
+        Elem<DT>::unpack(__ldg(reinterpret_cast<const uint4 *>(at)), f);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k)
+            Elem<kF32>::unpack(__ldg(reinterpret_cast<const uint4 *>(at) + k), f + 4 * k);
     }
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) out[k] = f32x2(f[2 * k], f[2 * k + 1]);
+}
+
+// LAAQ codes of a block of 128 BF16 values held by an octet of lanes, lane j having
+// vectors j and j + 8; the same codes and scale as agoq_quant_act.  All lanes of
+// the warp call it; `valid` gates the stores.
+template <int BITS>
+__device__ __forceinline__ void quantize_octet(const uint4 &a, const uint4 &b, uint32_t *rec,
+                                               float *scale, bool valid) {
+    constexpr int kQmax = (1 << (BITS - 1)) - 1;
+    constexpr int kBias = BITS < 8 ? 1 << (BITS - 1) : 0;
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const float s = bf16_div_qmax<kQmax>(octet_max(bf16_absmax<8>(w)));
+    const int j = threadIdx.x & 7;
+    uint32_t cb[16], lo, hi;
+    if (s >= 0x1p-96f) {
+        corrected_codes16<kBias>(w, s, cb);
+    } else {
+        float f[16];
+        Elem<kBF16>::unpack(a, f);
+        Elem<kBF16>::unpack(b, f + 8);
+        integer_codes_n<kQmax, 16, kBias>(f, s, cb);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (BITS < 8) pack_biased8<BITS>(cb + 8 * h, lo, hi);
+        else pack_fields8<BITS>(cb + 8 * h, lo, hi);
+        store_chunk<BITS>(rec, j + 8 * h, lo, hi, valid);
+    }
+    if (valid && j == 0) *scale = s;
 }
 
 // Rows that start at 16-byte boundaries and hold whole vectors: a group of threads a
 // row and step, NV vectors a thread, the row in registers from its one reading to
 // its writing.  Copies into a ring of shared memory run kRing - 1 rows ahead; a thread
-// reads only what it copied, so the ring needs no barrier.  BITS: the codes of x too,
-// a half warp holding a block of 128.
-template <int NV>
-constexpr int kRing = NV == 4 ? 3 : 4;       // stages (1024 threads: 192 KB)
+// reads only what it copied, so the ring needs no barrier.  BITS: the codes of x too.
+template <int F>
+constexpr int kRing = F == 32 ? 3 : 4;       // stages (1024 threads: 192 KB)
 
 template <int DT, int BITS, int NV>
-__global__ void __launch_bounds__(NV == 4 ? 1024 : 512)
+__global__ void __launch_bounds__(NV * Elem<DT>::kVec == 32 ? 1024 : 512,
+                                  NV * Elem<DT>::kVec == 32 || BITS ? 1 : 2)
 ln_forward_rows_kernel(const LnForward a, int size) {
     using E = Elem<DT>;
-    constexpr int V = E::kVec, F = NV * V;
-    constexpr int kStages = kRing<NV>;
+    constexpr int V = E::kVec, F = NV * V, P = V / 2;
+    constexpr int kStages = kRing<F>;
     constexpr bool kKeep = F <= 16;      // w and b stay in registers
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ float red[kMaxGroups][2][32];
     const Group g(size);
-    const int threads = blockDim.x, vectors = (int)(a.H / V);
-    const int64_t step = (int64_t)gridDim.x * (threads / size);
-    const int64_t first = (int64_t)blockIdx.x * (threads / size) + g.id;
-    const float inv = __frcp_rn((float)a.H);
+    const int threads = blockDim.x, vectors = (int)(a.H / V), groups = threads / size;
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const float n = (float)a.H, inv = __frcp_rn(n);
+    float (*const mine)[32] = red[size > 32 ? g.id : 0];
     pdl_wait_and_release();
     auto fetch = [&](int64_t t, int stage) {
         if (t < a.T) {
             const uint4 *row = reinterpret_cast<const uint4 *>(elem_at<DT>(a.x, t * a.ldx));
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (g.tid + i * size < vectors)
-                    copy16(ring + (stage * NV + i) * threads + threadIdx.x, row + g.tid + i * size);
+            for (int i = 0; i < NV; ++i) {
+                const int j = place<DT>(g, i);
+                if (j < vectors) copy16(ring + (stage * NV + i) * threads + threadIdx.x, row + j);
+            }
         }
         copies_commit();
     };
+    const int64_t first = (int64_t)blockIdx.x * groups;      // of the CTA
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
-    float w[kKeep ? F : 1], b[kKeep ? F : 1];
+    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step + g.id, s);
+    uint64_t w[kKeep ? F / 2 : 1], b[kKeep ? F / 2 : 1];
     if constexpr (kKeep) {
-        load_params<DT, NV>(a.w, a.param_f32, vectors, 1.0f, g, w);
-        load_params<DT, NV>(a.b, a.param_f32, vectors, 0.0f, g, b);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = place<DT>(g, i) < vectors ? place<DT>(g, i) : 0;
+            load_params<DT>(a.w, a.param_f32, j, 1.0f, w + i * P);
+            load_params<DT>(a.b, a.param_f32, j, 0.0f, b + i * P);
+        }
     }
     int stage = 0;
-    for (int64_t t = first; t < a.T; t += step) {
+    for (int64_t t0 = first; t0 < a.T; t0 += step) {
+        const int64_t t = t0 + g.id;
+        const bool row = t < a.T;
         copies_left<kStages - 2>();
         uint4 v[NV];
-        float f[F];
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             v[i] = make_uint4(0, 0, 0, 0);
-            if (g.tid + i * size < vectors) v[i] = ring[(stage * NV + i) * threads + threadIdx.x];
-            E::unpack(v[i], f + i * V);
+            if (row && place<DT>(g, i) < vectors)
+                v[i] = ring[(stage * NV + i) * threads + threadIdx.x];
+            add_elems<DT>(v[i], sum);
         }
-        fetch(t + (kStages - 1) * step, (stage + kStages - 1) % kStages);
-        stage = (stage + 1) % kStages;
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int i = 0; i < F; ++i) s[0] = __fadd_rn(s[0], f[i]);
-        row_sums(s, red[g.id][0], g);
-        const float mu = divided(s[0], (float)a.H, inv);
-        float q[1] = {0.0f};
+        fetch(t + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        float s[1] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]))};
+        row_sums(s, mine[0], g);
+        const float mu = divided(s[0], n, inv);
+        uint64_t d[F / 2], q0 = 0, q1 = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (g.tid + i * size >= vectors) continue;
+            differences<DT>(v[i], mu, d + i * P);
+            if (place<DT>(g, i) < vectors) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float d = __fsub_rn(f[i * V + k], mu);
-                q[0] = __fmaf_rn(d, d, q[0]);
+                for (int k = i * P; k < i * P + P; k += 2) {
+                    q0 = fma_f32x2(d[k], d[k], q0);
+                    q1 = fma_f32x2(d[k + 1], d[k + 1], q1);
+                }
             }
         }
-        row_sums(q, red[g.id][1], g);
-        const float var = divided(q[0], (float)a.H, inv);
-        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(var, a.eps)));
+        float q[1] = {__fadd_rn(sum_pair(q0), sum_pair(q1))};
+        row_sums(q, mine[1], g);
+        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(divided(q[0], n, inv), a.eps)));
+        const uint64_t r2 = f32x2(r, r);
         uint4 *out = reinterpret_cast<uint4 *>(elem_at<DT>(a.y, t * a.ldy));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = g.tid + i * size;
-            if (j < vectors) {
-                float y[V];
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float xh = __fmul_rn(__fsub_rn(f[i * V + k], mu), r);
-                    const int64_t e = (int64_t)j * V + k;
-                    y[k] = kKeep ? __fmaf_rn(xh, w[kKeep ? i * V + k : 0], b[kKeep ? i * V + k : 0])
-                                 : __fmaf_rn(xh, param<DT>(a.w, a.param_f32, e, 1.0f),
-                                             param<DT>(a.b, a.param_f32, e, 0.0f));
-                }
-                out[j] = E::pack(y);
+            const int j = place<DT>(g, i);
+            uint64_t *y = d + i * P;
+            if (!row || j >= vectors) continue;
+            uint64_t wj[P], bj[P];
+            if constexpr (!kKeep) {
+                load_params<DT>(a.w, a.param_f32, j, 1.0f, wj);
+                load_params<DT>(a.b, a.param_f32, j, 0.0f, bj);
             }
-            if constexpr (BITS != 0) {
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+                y[k] = fma_f32x2(mul_f32x2(y[k], r2), kKeep ? w[kKeep ? i * P + k : 0] : wj[k],
+                                 kKeep ? b[kKeep ? i * P + k : 0] : bj[k]);
+            out[j] = pack2<DT>(y);
+        }
+        if constexpr (BITS != 0) {
+#pragma unroll
+            for (int i = 0; i < NV; i += 2) {
+                const int j = place<DT>(g, i);
                 const int64_t blk = t * (a.H / kBlock) + j / 16;
-                quantize_block16<BITS>(v[i], threadIdx.x & 15,
-                                       static_cast<uint32_t *>(a.codes) + blk * 4 * BITS,
-                                       a.scales + blk, j < vectors);
+                quantize_octet<BITS>(v[i], v[i + 1], static_cast<uint32_t *>(a.codes) + blk * 4 * BITS,
+                                     a.scales + blk, row && j < vectors);
             }
         }
-        if (g.tid == 0) {
+        if (g.tid == 0 && row) {
             if (a.mean) a.mean[t] = mu;
             if (a.rstd) a.rstd[t] = r;
         }
     }
 }
 
-// Rows of any alignment: the same, an element a thread and step, NE elements a
-// thread; the next row's elements are loaded before this one's sums.
+// ---- rows of any alignment ------------------------------------------------------
+
+// A row of H elements in shared memory as it lies in global memory: vector j at the
+// 16-byte boundary before the row's start plus 16 j.
+template <int DT>
+struct RowCopy {
+    using Word = typename Elem<DT>::Word;
+    const Word *row;
+    int H, skip, from, to, n;     // vectors [from, to) are whole, n in all
+    __device__ __forceinline__ RowCopy(const void *row_, int H_)
+        : row(static_cast<const Word *>(row_)), H(H_) {
+        constexpr int V = Elem<DT>::kVec;
+        skip = (int)(reinterpret_cast<uintptr_t>(row_) & 15u) / Elem<DT>::kSize;
+        n = (H + skip + V - 1) / V;
+        from = skip ? 1 : 0;
+        to = max((H + skip) / V, from);
+    }
+    __device__ __forceinline__ void copy(uint4 *to_shared) const {
+        const uint4 *vec = reinterpret_cast<const uint4 *>(row - skip);
+        for (int j = from + threadIdx.x; j < to; j += blockDim.x) copy16(to_shared + j, vec + j);
+    }
+    // The elements in vectors that the row fills in part, at most 16: the i-th's
+    // index, or -1.
+    __device__ __forceinline__ int edge(int i) const {
+        constexpr int V = Elem<DT>::kVec;
+        const int head = min(H, from * V - (from ? skip : 0)), tail = max(head, to * V - skip);
+        const int e = i < head ? i : tail + i - head;
+        return e < H ? e : -1;
+    }
+};
+
+// Writes the row from shared memory (in the layout of RowCopy for its own address).
+template <int DT>
+__device__ __forceinline__ void write_row(void *row, int H, const uint4 *from_shared) {
+    using Word = typename Elem<DT>::Word;
+    const RowCopy<DT> r(row, H);
+    uint4 *vec = reinterpret_cast<uint4 *>(static_cast<Word *>(row) - r.skip);
+    for (int j = r.from + threadIdx.x; j < r.to; j += blockDim.x) vec[j] = from_shared[j];
+    const int e = threadIdx.x < 16 ? r.edge(threadIdx.x) : -1;
+    if (e >= 0)
+        static_cast<Word *>(row)[e] = reinterpret_cast<const Word *>(from_shared)[r.skip + e];
+}
+
+// The rows of one tensor through a ring of shared memory.  The few elements outside
+// whole vectors take a register on their way: loaded with the row's copies and stored
+// a row later, so that nothing waits for them.
+template <int DT, int STAGES>
+struct RowRing {
+    using Word = typename Elem<DT>::Word;
+    const void *p;
+    int64_t ld, T, step;
+    int H, vectors;               // of a stage
+    uint4 *ring;
+    Word held = Word(0);
+    int held_at = -1;             // word of the ring where it belongs
+    __device__ __forceinline__ void fetch(int64_t t, int stage) {
+        settle();
+        if (t >= T) return;
+        const RowCopy<DT> r(elem_at<DT>(p, t * ld), H);
+        r.copy(ring + stage * vectors);
+        const int e = threadIdx.x < 16 ? r.edge(threadIdx.x) : -1;
+        if (e >= 0) {
+            held = r.row[e];
+            held_at = stage * vectors * Elem<DT>::kVec + r.skip + e;
+        }
+    }
+    __device__ __forceinline__ void settle() {
+        if (held_at >= 0) reinterpret_cast<Word *>(ring)[held_at] = held;
+        held_at = -1;
+    }
+    // The words of row t, which is in `stage`.
+    __device__ __forceinline__ const Word *row(int64_t t, int stage) const {
+        const int skip = (int)(reinterpret_cast<uintptr_t>(elem_at<DT>(p, t * ld)) & 15u) /
+                         Elem<DT>::kSize;
+        return reinterpret_cast<const Word *>(ring + stage * vectors) + skip;
+    }
+};
+constexpr int kAnyStages = 3;
+
+// Vectors of a row of H elements that may start anywhere in one.
+template <int DT>
+__host__ __device__ constexpr int row_slots(int H) {
+    return (H + 2 * Elem<DT>::kVec - 2) / Elem<DT>::kVec;
+}
+
+// A CTA a row and step, NE elements a thread (tid, tid + threads, ...), whatever the
+// alignment: the rows are copied and written in 16-byte vectors at the boundaries of
+// their own addresses, with shared memory in between.
 template <int DT, int NE>
-__global__ void __launch_bounds__(1024) ln_forward_elems_kernel(const LnForward a) {
+__global__ void __launch_bounds__(1024) ln_forward_any_kernel(const LnForward a) {
     using E = Elem<DT>;
     using Word = typename E::Word;
+    extern __shared__ __align__(16) uint4 ring[];
     __shared__ float red[2][32];
     const Group g(blockDim.x);
-    const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H;
-    const float inv = __frcp_rn((float)a.H);
+    const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H, vectors = row_slots<DT>(H);
+    const float n = (float)a.H, inv = __frcp_rn(n);
+    const int64_t step = gridDim.x;
+    RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
+    uint4 *staged = ring + kAnyStages * vectors;                  // two rows of y
     pdl_wait_and_release();
-    Word next[NE];
-    auto fetch = [&](int64_t t) {
-        const Word *row = reinterpret_cast<const Word *>(elem_at<DT>(a.x, t * a.ldx));
+#pragma unroll
+    for (int s = 0; s < kAnyStages - 1; ++s) {
+        x.fetch(blockIdx.x + s * step, s);
+        copies_commit();
+    }
+    int stage = 0, half = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += step) {
+        copies_left<kAnyStages - 2>();
+        x.settle();
+        __syncthreads();                                          // the row is complete
+        x.fetch(t + (kAnyStages - 1) * step, stage == 0 ? kAnyStages - 1 : stage - 1);
+        copies_commit();
+        const Word *row = x.row(t, stage);
+        stage = stage + 1 == kAnyStages ? 0 : stage + 1;
+        float f[NE], s[1] = {0.0f}, q[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            next[i] = Word(0);
-            if (tid + i * threads < H) next[i] = row[tid + i * threads];
+            f[i] = tid + i * threads < H ? E::up(row[tid + i * threads]) : 0.0f;
+            s[0] = __fadd_rn(s[0], f[i]);
         }
-    };
-    if (blockIdx.x < a.T) fetch(blockIdx.x);
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        float f[NE];
-#pragma unroll
-        for (int i = 0; i < NE; ++i) f[i] = E::up(next[i]);
-        if (t + gridDim.x < a.T) fetch(t + gridDim.x);
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int i = 0; i < NE; ++i) s[0] = __fadd_rn(s[0], f[i]);
         row_sums(s, red[0], g);
-        const float mu = divided(s[0], (float)a.H, inv);
-        float q[1] = {0.0f};
+        const float mu = divided(s[0], n, inv);
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const float d = __fsub_rn(f[i], mu);
-            if (tid + i * threads < H) q[0] = __fmaf_rn(d, d, q[0]);
+            f[i] = __fsub_rn(f[i], mu);
+            if (tid + i * threads < H) q[0] = __fmaf_rn(f[i], f[i], q[0]);
         }
         row_sums(q, red[1], g);
-        const float var = divided(q[0], (float)a.H, inv);
-        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(var, a.eps)));
-        char *out = elem_at<DT>(a.y, t * a.ldy);
+        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(divided(q[0], n, inv), a.eps)));
+        void *out = elem_at<DT>(a.y, t * a.ldy);
+        uint4 *mine = staged + half * vectors;
+        half ^= 1;
+        Word *words = reinterpret_cast<Word *>(mine) +
+                      (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             const int e = tid + i * threads;
             if (e >= H) break;
-            const float xh = __fmul_rn(__fsub_rn(f[i], mu), r);
-            store_elem<DT>(out, e, __fmaf_rn(xh, param<DT>(a.w, a.param_f32, e, 1.0f),
-                                             param<DT>(a.b, a.param_f32, e, 0.0f)));
+            words[e] = E::down(__fmaf_rn(__fmul_rn(f[i], r), param<DT>(a.w, a.param_f32, e, 1.0f),
+                                         param<DT>(a.b, a.param_f32, e, 0.0f)));
         }
+        __syncthreads();
+        write_row<DT>(out, H, mine);
         if (tid == 0) {
             if (a.mean) a.mean[t] = mu;
             if (a.rstd) a.rstd[t] = r;
@@ -303,7 +436,8 @@ __global__ void __launch_bounds__(1024) ln_forward_elems_kernel(const LnForward 
     }
 }
 
-// The codes of x, a half warp a block.
+// The codes of x on their own (rows that the kernels above do not quantize): an octet
+// of lanes a block, any row distance.
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) ln_codes_kernel(const void *__restrict__ x, int64_t ldx,
                                                             int64_t T, int64_t H,
@@ -311,23 +445,25 @@ __global__ void __launch_bounds__(kThreads) ln_codes_kernel(const void *__restri
                                                             float *__restrict__ scales) {
     pdl_wait_and_release();
     const int64_t per_row = H / kBlock, blocks = T * per_row;
-    const int c = threadIdx.x & 15;
-    const int64_t stride = (int64_t)gridDim.x * (kThreads / 16);
+    const int j = threadIdx.x & 7;
+    const int64_t stride = (int64_t)gridDim.x * (kThreads / 8);
     // every lane of a warp takes the same number of steps
-    for (int64_t b0 = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 5) * 2; b0 < blocks;
+    for (int64_t b0 = (int64_t)blockIdx.x * (kThreads / 8) + (threadIdx.x >> 5) * 4; b0 < blocks;
          b0 += stride) {
-        const int64_t blk = b0 + ((threadIdx.x >> 4) & 1);
+        const int64_t blk = b0 + ((threadIdx.x >> 3) & 3);
         const bool valid = blk < blocks;
-        uint32_t v[4] = {0, 0, 0, 0};
+        uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (valid) {
             const uint16_t *p = static_cast<const uint16_t *>(x) + (blk / per_row) * ldx +
-                                (blk % per_row) * kBlock + 8 * c;
+                                (blk % per_row) * kBlock + 8 * j;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = (uint32_t)__ldg(p + 2 * i) | ((uint32_t)__ldg(p + 2 * i + 1) << 16);
+            for (int i = 0; i < 8; ++i) {
+                const int e = 2 * i + (i >= 4 ? 56 : 0);
+                v[i] = (uint32_t)__ldg(p + e) | ((uint32_t)__ldg(p + e + 1) << 16);
+            }
         }
-        quantize_block16<BITS>(make_uint4(v[0], v[1], v[2], v[3]), c, codes + blk * 4 * BITS,
-                               scales + blk, valid);
+        quantize_octet<BITS>(make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7]),
+                             codes + blk * 4 * BITS, scales + blk, valid);
     }
 }
 
@@ -414,20 +550,19 @@ __global__ void __launch_bounds__(kThreads) ln_backward_kernel(
 // x and dy read once, dx written once.  A thread adds its columns' terms of dw and db
 // in registers over all rows of its group; the groups of a CTA join theirs in order,
 // and the CTA writes one row of the partial sums ([grid][2][H]).
-template <int DT, int BITS, int NV>
+template <int DT, int BITS>
 __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward a, int size) {
     using E = Elem<DT>;
-    constexpr int V = E::kVec, F = NV * V;
-    constexpr int kStages = kRing<NV>, kWords = 4 * BITS;
+    constexpr int V = E::kVec, F = 16, NV = F / V, P = V / 2;
+    constexpr int kStages = BITS ? 4 : 3, kWords = 4 * BITS;
     constexpr int kParts = BITS ? 1 : 2;             // dy, and x
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ float red[kMaxGroups][2][64];
     const Group g(size);
     const int threads = blockDim.x, vectors = (int)(a.H / V), groups = threads / size;
     const int64_t step = (int64_t)gridDim.x * groups;
-    const int64_t first = (int64_t)blockIdx.x * groups + g.id;
-    const float inv = __frcp_rn((float)a.H);
-    const bool sums = a.dw || a.db;
+    const float n = (float)a.H, inv = __frcp_rn(n);
+    float (*const mine)[64] = red[size > 32 ? g.id : 0];
     pdl_wait_and_release();
     // slot i of part p of a stage
     auto slot = [&](int stage, int p, int i) {
@@ -439,116 +574,133 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
             const uint4 *x = reinterpret_cast<const uint4 *>(elem_at<DT>(a.x, BITS ? 0 : t * a.ldx));
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (g.tid + i * size < vectors) {
-                    copy16(slot(stage, 0, i), dy + g.tid + i * size);
-                    if constexpr (BITS == 0) copy16(slot(stage, 1, i), x + g.tid + i * size);
+                const int j = place<DT>(g, i);
+                if (j < vectors) {
+                    copy16(slot(stage, 0, i), dy + j);
+                    if constexpr (BITS == 0) copy16(slot(stage, 1, i), x + j);
                 }
             }
         }
         copies_commit();
     };
     // what does not come in 16-byte copies is loaded a row ahead into registers
-    uint32_t lo[BITS ? NV : 1], hi[BITS ? NV : 1];
-    float scale[BITS ? NV : 1], mean = 0.0f, rstd = 0.0f;
+    uint32_t lo[2], hi[2];
+    float scale = 0.0f, mean = 0.0f, rstd = 0.0f;
     auto ahead = [&](int64_t t) {
         if (t >= a.T) return;
         if constexpr (BITS == 0) {
             mean = __ldg(a.mean + t);
             rstd = __ldg(a.rstd + t);
         } else {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int j = g.tid + i * size;
-                if (j >= vectors) continue;
-                const int64_t blk = t * (a.H / kBlock) + j / 16;
-                load_chunk<BITS>(static_cast<const uint32_t *>(a.x) + blk * kWords, j & 15, lo[i], hi[i]);
-                scale[i] = __ldg(a.scales + blk);
-            }
+            const int j = place<DT>(g, 0);           // the octet's block
+            if (j >= vectors) return;
+            const int64_t blk = t * (a.H / kBlock) + j / 16;
+            const uint32_t *rec = static_cast<const uint32_t *>(a.x) + blk * kWords;
+            load_chunk<BITS>(rec, j & 7, lo[0], hi[0]);
+            load_chunk<BITS>(rec, (j & 7) + 8, lo[1], hi[1]);
+            scale = __ldg(a.scales + blk);
         }
     };
+    const int64_t first = (int64_t)blockIdx.x * groups;      // of the CTA
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
-    ahead(first);
-    float w[F], dw[F], db[F];
-    load_params<DT, NV>(a.w, a.param_f32, vectors, 1.0f, g, w);
+    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step + g.id, s);
+    ahead(first + g.id);
+    uint64_t w[F / 2], dw[F / 2], db[F / 2];
 #pragma unroll
-    for (int i = 0; i < F; ++i) dw[i] = db[i] = 0.0f;
-    int stage = 0;
-    for (int64_t t = first; t < a.T; t += step) {
+    for (int i = 0; i < NV; ++i)
+        load_params<DT>(a.w, a.param_f32, place<DT>(g, i) < vectors ? place<DT>(g, i) : 0, 1.0f,
+                        w + i * P);
+#pragma unroll
+    for (int i = 0; i < F / 2; ++i) dw[i] = db[i] = 0;
+    int stage = 0, half = 0;
+    for (int64_t t0 = first; t0 < a.T; t0 += step) {
+        const int64_t t = t0 + g.id;
+        const bool row = t < a.T;
         copies_left<kStages - 2>();
-        float x[F], d[F];                 // x, then xh; dy
+        uint64_t x[F / 2], d[F / 2];      // xh; dy
+        float mu = mean, r = rstd, s0, s1;
+        uint4 vx[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            uint4 vx = make_uint4(0, 0, 0, 0), vd = vx;
-            if (g.tid + i * size < vectors) {
+            uint4 vd = make_uint4(0, 0, 0, 0);
+            vx[i] = vd;
+            if (row && place<DT>(g, i) < vectors) {
                 vd = *slot(stage, 0, i);
-                if constexpr (BITS == 0) vx = *slot(stage, 1, i);
-                else vx = dequantize_chunk<BITS>(lo[i], hi[i], scale[i]);
+                if constexpr (BITS == 0) vx[i] = *slot(stage, 1, i);
+                else vx[i] = dequantize_chunk<BITS>(lo[i], hi[i], scale);
             }
-            E::unpack(vx, x + i * V);
-            E::unpack(vd, d + i * V);
+            unpack2<DT>(vd, d + i * P);
         }
-        float mu = mean, r = rstd;
-        fetch(t + (kStages - 1) * step, (stage + kStages - 1) % kStages);
+        fetch(t + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
         ahead(t + step);
-        stage = (stage + 1) % kStages;
-        float s0, s1;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        uint64_t g0 = 0, g1 = 0;
         if constexpr (BITS == 0) {
-            float s[2] = {0.0f, 0.0f};
+            // (lanes and rows beyond the end have dy = 0: their terms are 0)
+            const uint64_t r2 = f32x2(r, r);
 #pragma unroll
-            for (int i = 0; i < F; ++i) {
-                x[i] = __fmul_rn(__fsub_rn(x[i], mu), r);
-                const float gi = __fmul_rn(d[i], w[i]);
-                s[0] = __fadd_rn(s[0], gi);
-                s[1] = __fmaf_rn(gi, x[i], s[1]);
+            for (int i = 0; i < NV; ++i) differences<DT>(vx[i], mu, x + i * P);
+#pragma unroll
+            for (int k = 0; k < F / 2; ++k) {
+                x[k] = mul_f32x2(x[k], r2);
+                const uint64_t gk = mul_f32x2(d[k], w[k]);
+                g0 = add_f32x2(g0, gk);
+                g1 = fma_f32x2(gk, x[k], g1);
             }
-            row_sums(s, red[g.id][(t / step) & 1], g);
-            s0 = divided(s[0], (float)a.H, inv);
-            s1 = divided(s[1], (float)a.H, inv);
+            float s[2] = {sum_pair(g0), sum_pair(g1)};
+            row_sums(s, mine[half], g);
+            half ^= 1;
+            s0 = divided(s[0], n, inv);
+            s1 = divided(s[1], n, inv);
         } else {
-            float s[2] = {0.0f, 0.0f}, q[2] = {0.0f, 0.0f};
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < F; ++i) {
-                s[0] = __fadd_rn(s[0], x[i]);
-                s[1] = __fmaf_rn(d[i], w[i], s[1]);
-            }
-            row_sums(s, red[g.id][0], g);
-            mu = divided(s[0], (float)a.H, inv);
-            s0 = divided(s[1], (float)a.H, inv);
+            for (int i = 0; i < NV; ++i) add_elems<DT>(vx[i], sum);
+#pragma unroll
+            for (int k = 0; k < F / 2; ++k) g0 = fma_f32x2(d[k], w[k], g0);
+            float s[2] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])),
+                          sum_pair(g0)};
+            row_sums(s, mine[0], g);
+            mu = divided(s[0], n, inv);
+            s0 = divided(s[1], n, inv);
+            uint64_t q0 = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const bool in = g.tid + i * size < vectors;
+                differences<DT>(vx[i], mu, x + i * P);
+                if (place<DT>(g, i) < vectors) {
 #pragma unroll
-                for (int k = i * V; k < (i + 1) * V; ++k) {
-                    x[k] = in ? __fsub_rn(x[k], mu) : 0.0f;
-                    q[0] = __fmaf_rn(x[k], x[k], q[0]);
-                    q[1] = __fmaf_rn(__fmul_rn(d[k], w[k]), x[k], q[1]);
+                    for (int k = i * P; k < i * P + P; ++k) {
+                        q0 = fma_f32x2(x[k], x[k], q0);
+                        g1 = fma_f32x2(mul_f32x2(d[k], w[k]), x[k], g1);
+                    }
                 }
             }
-            row_sums(q, red[g.id][1], g);
-            const float var = divided(q[0], (float)a.H, inv);
-            r = __frcp_rn(__fsqrt_rn(__fadd_rn(var, a.eps)));
-            s1 = divided(__fmul_rn(q[1], r), (float)a.H, inv);
+            float q[2] = {sum_pair(q0), sum_pair(g1)};
+            row_sums(q, mine[1], g);
+            r = __frcp_rn(__fsqrt_rn(__fadd_rn(divided(q[0], n, inv), a.eps)));
+            s1 = divided(__fmul_rn(q[1], r), n, inv);
+            const uint64_t r2 = f32x2(r, r);
 #pragma unroll
-            for (int i = 0; i < F; ++i) x[i] = __fmul_rn(x[i], r);
+            for (int k = 0; k < F / 2; ++k) x[k] = mul_f32x2(x[k], r2);
         }
+        const uint64_t r2 = f32x2(r, r), s02 = f32x2(s0, s0), s12 = f32x2(-s1, -s1);
         uint4 *out = reinterpret_cast<uint4 *>(elem_at<DT>(a.dx, t * a.lddx));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (g.tid + i * size >= vectors) continue;
-            float o[V];
+            if (!row || place<DT>(g, i) >= vectors) continue;
+            uint64_t o[P];
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const int n = i * V + k;
-                o[k] = __fmul_rn(r, __fmaf_rn(-x[n], s1, __fsub_rn(__fmul_rn(d[n], w[n]), s0)));
-                dw[n] = __fmaf_rn(d[n], x[n], dw[n]);
-                db[n] = __fadd_rn(db[n], d[n]);
+            for (int k = 0; k < P; ++k) {
+                const int m = i * P + k;
+                o[k] = mul_f32x2(r2, fma_f32x2(x[m], s12, sub_f32x2(mul_f32x2(d[m], w[m]), s02)));
+                dw[m] = fma_f32x2(d[m], x[m], dw[m]);
+                db[m] = add_f32x2(db[m], d[m]);
             }
-            out[g.tid + i * size] = E::pack(o);
+            out[place<DT>(g, i)] = pack2<DT>(o);
         }
     }
-    if (!sums) return;
-    float *mine = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
+    if (!a.dw && !a.db) return;
+    float *partial = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
     float *joined = reinterpret_cast<float *>(ring);          // [2][H], for several groups
     copies_left<0>();
     for (int who = 0; who < groups; ++who) {
@@ -556,20 +708,115 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
         if (g.id != who) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = g.tid + i * size;
+            const int j = place<DT>(g, i);
             if (j >= vectors) continue;
+            float *pw = (groups > 1 ? joined : partial) + j * V, *pb = pw + a.H;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                float *pw = (groups > 1 ? joined : mine) + j * V + k, *pb = pw + a.H;
-                const int n = i * V + k;
-                *pw = groups > 1 && who > 0 ? __fadd_rn(*pw, dw[n]) : dw[n];
-                *pb = groups > 1 && who > 0 ? __fadd_rn(*pb, db[n]) : db[n];
+                const int m = i * P + k / 2;
+                const float vw = k & 1 ? hi_f32(dw[m]) : lo_f32(dw[m]);
+                const float vb = k & 1 ? hi_f32(db[m]) : lo_f32(db[m]);
+                pw[k] = who > 0 ? __fadd_rn(pw[k], vw) : vw;
+                pb[k] = who > 0 ? __fadd_rn(pb[k], vb) : vb;
             }
         }
     }
     if (groups > 1) {
         __syncthreads();
-        for (int i = threadIdx.x; i < 2 * (int)a.H; i += threads) mine[i] = joined[i];
+        for (int i = threadIdx.x; i < 2 * (int)a.H; i += threads) partial[i] = joined[i];
+    }
+}
+
+// Rows of any alignment: as the forward pass, x and dy through rings, dx through
+// shared memory.
+template <int DT, int NE>
+__global__ void __launch_bounds__(512) ln_backward_any_kernel(const LnBackward a) {
+    using E = Elem<DT>;
+    using Word = typename E::Word;
+    extern __shared__ __align__(16) uint4 ring[];
+    __shared__ float red[2][64];
+    const Group g(blockDim.x);
+    const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H, vectors = row_slots<DT>(H);
+    const float n = (float)a.H, inv = __frcp_rn(n);
+    const int64_t step = gridDim.x;
+    RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
+    RowRing<DT, kAnyStages> y{a.dy, a.lddy, a.T, step, H, vectors, ring + kAnyStages * vectors};
+    uint4 *staged = ring + 2 * kAnyStages * vectors;              // two rows of dx
+    pdl_wait_and_release();
+#pragma unroll
+    for (int s = 0; s < kAnyStages - 1; ++s) {
+        x.fetch(blockIdx.x + s * step, s);
+        y.fetch(blockIdx.x + s * step, s);
+        copies_commit();
+    }
+    float w[NE], dw[NE], db[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        w[i] = tid + i * threads < H ? param<DT>(a.w, a.param_f32, tid + i * threads, 1.0f) : 0.0f;
+        dw[i] = db[i] = 0.0f;
+    }
+    float mean = 0.0f, rstd = 0.0f;
+    auto ahead = [&](int64_t t) {
+        if (t < a.T) {
+            mean = __ldg(a.mean + t);
+            rstd = __ldg(a.rstd + t);
+        }
+    };
+    ahead(blockIdx.x);
+    int stage = 0, half = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += step) {
+        copies_left<kAnyStages - 2>();
+        x.settle();
+        y.settle();
+        __syncthreads();                                          // the rows are complete
+        const int into = stage == 0 ? kAnyStages - 1 : stage - 1;
+        x.fetch(t + (kAnyStages - 1) * step, into);
+        y.fetch(t + (kAnyStages - 1) * step, into);
+        copies_commit();
+        const float mu = mean, r = rstd;
+        ahead(t + step);
+        const Word *rx = x.row(t, stage), *ry = y.row(t, stage);
+        stage = stage + 1 == kAnyStages ? 0 : stage + 1;
+        float xh[NE], d[NE], s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int e = tid + i * threads;
+            xh[i] = d[i] = 0.0f;
+            if (e < H) {
+                xh[i] = __fmul_rn(__fsub_rn(E::up(rx[e]), mu), r);
+                d[i] = E::up(ry[e]);
+            }
+            const float gi = __fmul_rn(d[i], w[i]);
+            s[0] = __fadd_rn(s[0], gi);
+            s[1] = __fmaf_rn(gi, xh[i], s[1]);
+        }
+        row_sums(s, red[half], g);
+        const float s0 = divided(s[0], n, inv), s1 = divided(s[1], n, inv);
+        void *out = elem_at<DT>(a.dx, t * a.lddx);
+        uint4 *mine = staged + half * vectors;
+        half ^= 1;
+        Word *words = reinterpret_cast<Word *>(mine) +
+                      (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int e = tid + i * threads;
+            if (e < H)
+                words[e] = E::down(
+                    __fmul_rn(r, __fmaf_rn(-xh[i], s1, __fsub_rn(__fmul_rn(d[i], w[i]), s0))));
+            dw[i] = __fmaf_rn(d[i], xh[i], dw[i]);
+            db[i] = __fadd_rn(db[i], d[i]);
+        }
+        __syncthreads();
+        write_row<DT>(out, H, mine);
+    }
+    if (!a.dw && !a.db) return;
+    float *partial = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int e = tid + i * threads;
+        if (e >= H) break;
+        partial[e] = dw[i];
+        partial[a.H + e] = db[i];
     }
 }
 
@@ -610,10 +857,13 @@ bool on16(const void *p, int64_t ld, int size) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0;
 }
 
+// Threads of a row's group that holds `units` in shares of `per`: 8, 16, or whole warps.
 int threads_for(int64_t units, int per) {
     const int64_t t = (units + per - 1) / per;
-    return (int)((t + 31) / 32 * 32);
+    return t <= 8 ? 8 : t <= 16 ? 16 : (int)((t + 31) / 32 * 32);
 }
+// Groups of `size` threads in a CTA: 256 threads, for rows shorter than that.
+int groups_of(int size) { return size <= 128 ? 256 / size : 1; }
 
 // CTAs of a kernel whose CTAs stay for many units of work: as many as are resident.
 template <typename K>
@@ -623,51 +873,51 @@ int resident_ctas(K kernel, int threads, size_t smem, int64_t units) {
     return grid_for(units, per_sm > 0 ? per_sm : 1);
 }
 
-// Groups of `size` threads in a CTA: 256 threads, for rows shorter than that.
-int groups_of(int size) { return size <= 128 ? 256 / size : 1; }
-
 template <int DT, int BITS, int NV>
 cudaError_t forward_rows(const LnForward &a, cudaStream_t st) {
+    constexpr int F = NV * Elem<DT>::kVec;
     const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
     const int threads = size * groups;
-    const size_t smem = (size_t)kRing<NV> * NV * threads * 16;
+    const size_t smem = (size_t)kRing<F> * NV * threads * 16;
     static bool ready[kMaxDevices];
     auto kernel = ln_forward_rows_kernel<DT, BITS, NV>;
-    const cudaError_t e =
-        allow_shared(kernel, (size_t)kRing<NV> * NV * (NV == 4 ? 1024 : 512) * 16, ready);
+    // a ring of rows of 64 KB, the longest
+    const cudaError_t e = allow_shared(kernel, (size_t)kRing<F> * (F == 32 ? 2 : 1) * 32768, ready);
     if (e != cudaSuccess) return e;
     const int ctas = resident_ctas(kernel, threads, smem, (a.T + groups - 1) / groups);
     return launch_pdl_clusters(kernel, ctas, threads, 1, smem, st, a, size);
 }
 
+constexpr int kLongRow = 65536;          // bytes
+
+// Dynamic shared memory of the kernels for any alignment may reach this.
+constexpr size_t kMostShared = 220 * 1024;
+
 template <int DT, int NE>
-cudaError_t forward_elems(const LnForward &a, cudaStream_t st) {
-    const int threads = threads_for(a.H, NE);
-    auto kernel = ln_forward_elems_kernel<DT, NE>;
-    return launch_pdl_clusters(kernel, resident_ctas(kernel, threads, 0, a.T), threads, 1, 0, st, a);
+cudaError_t forward_any(const LnForward &a, cudaStream_t st) {
+    const int threads = (int)((a.H + 32 * NE - 1) / (32 * NE)) * 32;
+    const size_t smem = (size_t)(kAnyStages + 2) * row_slots<DT>((int)a.H) * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_forward_any_kernel<DT, NE>;
+    const cudaError_t e = allow_shared(kernel, kMostShared, ready);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_clusters(kernel, resident_ctas(kernel, threads, smem, a.T), threads, 1, smem,
+                               st, a);
 }
 
-// Vectors a thread: one for rows of up to 128 vectors (few threads a row wait for one
-// another less), two up to 1024 (512 threads), four up to 4096.  0: no row of vectors.
-template <int DT>
-int row_vectors(int64_t H) {
-    constexpr int V = Elem<DT>::kVec;
-    if (H % V) return 0;
-    const int64_t n = H / V;
-    return n <= 128 ? 1 : n <= 1024 ? 2 : n <= 4096 ? 4 : 0;
-}
-
+// The kernel for the rows: whole vectors, 16 elements a thread for rows of up to 8192
+// (w and b in registers too), 32 up to 64 KB; any alignment where five rows fit
+// shared memory; else element by element.
 template <int DT, int BITS>
 cudaError_t forward_bits(const LnForward &a, cudaStream_t st) {
-    if (on16(a.x, a.ldx, Elem<DT>::kSize) && on16(a.y, a.ldy, Elem<DT>::kSize)) {
-        switch (row_vectors<DT>(a.H)) {
-            case 1: return forward_rows<DT, BITS, 1>(a, st);
-            case 2: return forward_rows<DT, BITS, 2>(a, st);
-            case 4: return forward_rows<DT, BITS, 4>(a, st);
-        }
+    constexpr int V = Elem<DT>::kVec;
+    if (on16(a.x, a.ldx, Elem<DT>::kSize) && on16(a.y, a.ldy, Elem<DT>::kSize) && a.H % V == 0) {
+        if (a.H <= 8192) return forward_rows<DT, BITS, 16 / V>(a, st);
+        if (a.H <= kLongRow / Elem<DT>::kSize) return forward_rows<DT, BITS, 32 / V>(a, st);
     }
-    if (a.H <= 512) return forward_elems<DT, 4>(a, st);
-    if (a.H <= 16384) return forward_elems<DT, 16>(a, st);
+    if (a.H <= 512) return forward_any<DT, 4>(a, st);
+    if (a.H <= 16384 && (size_t)(kAnyStages + 2) * row_slots<DT>((int)a.H) * 16 <= kMostShared)
+        return forward_any<DT, 16>(a, st);
     return launch_pdl(ln_forward_kernel<DT>, grid_for(a.T, 8), kThreads, 0, st, a.x, a.ldx, a.w, a.b,
                       a.param_f32, a.T, a.H, a.eps, a.y, a.ldy, a.mean, a.rstd);
 }
@@ -679,14 +929,15 @@ cudaError_t join(const LnBackward &a, int P, cudaStream_t st) {
                       a.workspace, a.H, P, a.dw, a.db);
 }
 
-template <int DT, int BITS, int NV>
+template <int DT, int BITS>
 cudaError_t backward_rows(const LnBackward &a, cudaStream_t st) {
+    constexpr int NV = 16 / Elem<DT>::kVec;
     const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
     const int threads = size * groups;
-    constexpr int kSlots = kRing<NV> * NV * (BITS ? 1 : 2);
+    constexpr int kSlots = (BITS ? 4 : 3) * NV * (BITS ? 1 : 2);
     const size_t smem = (size_t)kSlots * threads * 16;
     static bool ready[kMaxDevices];
-    auto kernel = ln_backward_rows_kernel<DT, BITS, NV>;
+    auto kernel = ln_backward_rows_kernel<DT, BITS>;
     const cudaError_t e = allow_shared(kernel, (size_t)kSlots * 512 * 16, ready);
     if (e != cudaSuccess) return e;
     int P = resident_ctas(kernel, threads, smem, (a.T + groups - 1) / groups);
@@ -695,15 +946,34 @@ cudaError_t backward_rows(const LnBackward &a, cudaStream_t st) {
     return r != cudaSuccess ? r : join(a, P, st);
 }
 
-// Elements a thread holds: eight for rows of up to 2048, sixteen up to 8192 (more
-// would not leave registers for dw and db).
+template <int DT, int NE>
+cudaError_t backward_any(const LnBackward &a, cudaStream_t st) {
+    const int threads = (int)((a.H + 32 * NE - 1) / (32 * NE)) * 32;
+    const size_t smem = (size_t)(2 * kAnyStages + 2) * row_slots<DT>((int)a.H) * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_backward_any_kernel<DT, NE>;
+    const cudaError_t e = allow_shared(kernel, kMostShared, ready);
+    if (e != cudaSuccess) return e;
+    int P = resident_ctas(kernel, threads, smem, a.T);
+    if (P > kLnPartials) P = kLnPartials;
+    const cudaError_t r = launch_pdl_clusters(kernel, P, threads, 1, smem, st, a);
+    return r != cudaSuccess ? r : join(a, P, st);
+}
+
+// Whole vectors and any alignment for rows of up to 8192 (16 elements a thread: more
+// would not leave registers for dw and db), any alignment from a tensor only and where
+// eight rows fit shared memory; else element by element.
 template <int DT, int BITS>
 cudaError_t backward(const Input<DT, BITS> &in, const LnBackward &a, cudaStream_t st) {
     constexpr int kSize = Elem<DT>::kSize, V = Elem<DT>::kVec;
     if ((BITS || on16(a.x, a.ldx, kSize)) && on16(a.dy, a.lddy, kSize) && on16(a.dx, a.lddx, kSize) &&
         a.H % V == 0 && a.H <= 8192)
-        return a.H <= 2048 ? backward_rows<DT, BITS, 8 / V>(a, st)
-                           : backward_rows<DT, BITS, 16 / V>(a, st);
+        return backward_rows<DT, BITS>(a, st);
+    if constexpr (BITS == 0) {
+        if (a.H <= 512) return backward_any<DT, 4>(a, st);
+        if (a.H <= 8192 && (size_t)(2 * kAnyStages + 2) * row_slots<DT>((int)a.H) * 16 <= kMostShared)
+            return backward_any<DT, 16>(a, st);
+    }
     const bool sums = a.dw || a.db;
     const int P = sums ? ln_partials(a.T) : grid_for(a.T, 8);
     const cudaError_t e = launch_pdl(ln_backward_kernel<DT, BITS>, P, kThreads, 0, st, in, a.dy,
@@ -715,7 +985,7 @@ cudaError_t backward(const Input<DT, BITS> &in, const LnBackward &a, cudaStream_
 template <int BITS>
 cudaError_t codes(const LnForward &a, cudaStream_t st) {
     const int64_t blocks = a.T * (a.H / kBlock);
-    return launch_pdl(ln_codes_kernel<BITS>, grid_for((blocks + 15) / 16, 8), kThreads, 0, st, a.x,
+    return launch_pdl(ln_codes_kernel<BITS>, grid_for((blocks + 31) / 32, 8), kThreads, 0, st, a.x,
                       a.ldx, a.T, a.H, static_cast<uint32_t *>(a.codes), a.scales);
 }
 
@@ -729,7 +999,7 @@ cudaError_t launch_ln_forward(const LnForward &a, cudaStream_t st) {
     if (a.dtype == kF16) return forward_bits<kF16, 0>(a, st);
     if (!a.codes) return forward_bits<kBF16, 0>(a, st);
     // y may be x's place: rows that the norm does not quantize are quantized first
-    const bool rows = on16(a.x, a.ldx, 2) && on16(a.y, a.ldy, 2) && row_vectors<kBF16>(a.H);
+    const bool rows = on16(a.x, a.ldx, 2) && on16(a.y, a.ldy, 2) && a.H <= kLongRow / 2;
     if (!rows) {
         const cudaError_t e = a.bits == 4   ? codes<4>(a, st)
                               : a.bits == 5 ? codes<5>(a, st)

@@ -132,31 +132,6 @@ __device__ __forceinline__ uint32_t vec_max(const uint4 &v) {
     return max_word<DT>(max_word<DT>(v.x, v.y), max_word<DT>(v.z, v.w));
 }
 
-// x - ref of a vector's elements, in pairs (one rounding each: the mixed-precision
-// addition takes a 16-bit operand as it is, without a conversion).
-template <int DT>
-__device__ __forceinline__ void differences(const uint4 &v, float ref, uint64_t *d) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (DT == kF32) {
-        d[0] = sub_f32x2(u32x2(w[0], w[1]), f32x2(ref, ref));
-        d[1] = sub_f32x2(u32x2(w[2], w[3]), f32x2(ref, ref));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float lo, hi;
-            if constexpr (DT == kBF16)
-                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-                    "add.rn.f32.bf16 %0, a, %3;\n\tadd.rn.f32.bf16 %1, b, %3;\n\t}"
-                    : "=f"(lo), "=f"(hi) : "r"(w[i]), "f"(-ref));
-            else
-                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-                    "add.rn.f32.f16 %0, a, %3;\n\tadd.rn.f32.f16 %1, b, %3;\n\t}"
-                    : "=f"(lo), "=f"(hi) : "r"(w[i]), "f"(-ref));
-            d[i] = f32x2(lo, hi);
-        }
-    }
-}
-
 // ENTROPY: with the sums of (x - ref) e^(x - ref).
 template <int DT, bool ENTROPY>
 struct Online {
@@ -474,18 +449,6 @@ __device__ __noinline__ void read_again(const Slice<DT> s, int want, bool nan, S
     for (int i = threadIdx.x; i < ne; i += kStatThreads) above[na + i] = sh.list[2 * kShortList + i];
     __syncthreads();
     rank_keys(above, na + ne, want, sh.top);
-}
-
-__device__ __forceinline__ void copy16(void *to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
-                 "l"(from)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_left() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The copies of a CTA's rows into the ring, ahead of the sums and across rows.

@@ -125,6 +125,84 @@ __device__ __forceinline__ uint4 bytes_from(const uint4 &a, const uint4 &b, int 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// x - ref of a vector's elements, in pairs (one rounding each: the mixed-precision
+// addition takes a 16-bit operand as it is, without a conversion).
+template <int DT>
+__device__ __forceinline__ void differences(const uint4 &v, float ref, uint64_t *d) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == kF32) {
+        d[0] = sub_f32x2(u32x2(w[0], w[1]), f32x2(ref, ref));
+        d[1] = sub_f32x2(u32x2(w[2], w[3]), f32x2(ref, ref));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            if constexpr (DT == kBF16)
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                    "add.rn.f32.bf16 %0, a, %3;\n\tadd.rn.f32.bf16 %1, b, %3;\n\t}"
+                    : "=f"(lo), "=f"(hi) : "r"(w[i]), "f"(-ref));
+            else
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                    "add.rn.f32.f16 %0, a, %3;\n\tadd.rn.f32.f16 %1, b, %3;\n\t}"
+                    : "=f"(lo), "=f"(hi) : "r"(w[i]), "f"(-ref));
+            d[i] = f32x2(lo, hi);
+        }
+    }
+}
+
+// Add a vector's elements to four sums (one rounding each).
+template <int DT>
+__device__ __forceinline__ void add_elems(const uint4 &v, float (&acc)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float &lo = acc[(2 * i) & 3], &hi = acc[(2 * i + 1) & 3];
+        if constexpr (DT == kF32)
+            acc[i] = __fadd_rn(acc[i], __uint_as_float(w[i]));
+        else if constexpr (DT == kBF16)
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                "add.rn.f32.bf16 %0, a, %0;\n\tadd.rn.f32.bf16 %1, b, %1;\n\t}"
+                : "+f"(lo), "+f"(hi) : "r"(w[i]));
+        else
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                "add.rn.f32.f16 %0, a, %0;\n\tadd.rn.f32.f16 %1, b, %1;\n\t}"
+                : "+f"(lo), "+f"(hi) : "r"(w[i]));
+    }
+}
+
+// A vector's elements as binary32 pairs, and back.
+template <int DT>
+__device__ __forceinline__ void unpack2(const uint4 &v, uint64_t *p) {
+    float f[Elem<DT>::kVec];
+    Elem<DT>::unpack(v, f);
+#pragma unroll
+    for (int i = 0; i < Elem<DT>::kVec / 2; ++i) p[i] = f32x2(f[2 * i], f[2 * i + 1]);
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack2(const uint64_t *p) {
+    float f[Elem<DT>::kVec];
+#pragma unroll
+    for (int i = 0; i < Elem<DT>::kVec / 2; ++i) {
+        f[2 * i] = lo_f32(p[i]);
+        f[2 * i + 1] = hi_f32(p[i]);
+    }
+    return Elem<DT>::pack(f);
+}
+__device__ __forceinline__ float sum_pair(uint64_t p) { return __fadd_rn(lo_f32(p), hi_f32(p)); }
+
+// ---- asynchronous copies of 16 bytes into shared memory -------------------------
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Element i of a tensor of type DT, as binary32.
 template <int DT>
 __device__ __forceinline__ float load_elem(const void *p, int64_t i) {
