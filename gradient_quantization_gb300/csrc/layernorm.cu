@@ -26,13 +26,11 @@ __device__ __forceinline__ float param(const void *p, bool f32, int64_t i, float
     return f32 ? load_elem<kF32>(p, i) : load_elem<DT>(p, i);
 }
 
-// fl(s / n) for n >= 1 with inv = fl(1 / n): the product, corrected by its remainder
-// (P. Markstein, IBM J. Res. Dev. 34(1), 1990); a quotient that overflows or is not
-// finite stays as the product gives it.
-__device__ __forceinline__ float divided(float s, float n, float inv) {
-    const float q = __fmul_rn(s, inv);
-    const float c = __fmaf_rn(__fmaf_rn(-q, n, s), inv, q);
-    return fabsf(q) < 3e38f && fabsf(s) > 1e-30f ? c : q;
+// 1 / sqrt(v): the hardware's approximation, off by less than 2^-22.
+__device__ __forceinline__ float inv_sqrt(float v) {
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // ---- forward ------------------------------------------------------------------
@@ -86,27 +84,38 @@ struct Group {
 };
 
 // The sums of the group's values (each thread gets them), in a fixed order; `red`
-// holds 32 floats a value and is free again after the group's next barrier.  All
-// threads of a warp call it.
+// holds kRed floats a value, 0 where no warp writes, and is free again after the group's
+// next barrier.  All threads of a warp call it.
+constexpr int kRed = 32;
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float *red, const Group &g) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        if (o < g.size) {
+    if (g.size < 32) {
+        for (int o = g.size >> 1; o > 0; o >>= 1) {
 #pragma unroll
             for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], o));
         }
+        return;
     }
-    if (g.size <= 32) return;
-    const int warp = g.tid >> 5, warps = g.size >> 5;
-    if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) red[32 * i + warp] = v[i];
+    for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], o));
+    }
+    if (g.size == 32) return;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[kRed * i + (g.tid >> 5)] = v[i];
     }
     g.sync();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < warps ? red[32 * i + lane] : 0.0f);
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    for (int k = 0; k < g.size; k += 128) {           // four warps' sums
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float4 f = *reinterpret_cast<const float4 *>(red + kRed * i + (k >> 5));
+            v[i] = __fadd_rn(v[i], __fadd_rn(__fadd_rn(f.x, f.y), __fadd_rn(f.z, f.w)));
+        }
+    }
 }
 
 // The i-th of the NV vectors of a row that a thread of a group holds.  16-bit types:
@@ -176,48 +185,59 @@ __device__ __forceinline__ void quantize_octet(const uint4 &a, const uint4 &b, u
 // its writing.  Copies into a ring of shared memory run kRing - 1 rows ahead; a thread
 // reads only what it copied, so the ring needs no barrier.  BITS: the codes of x too.
 template <int F>
-constexpr int kRing = F == 32 ? 3 : 4;       // stages (1024 threads: 192 KB)
+constexpr int kRing = F == 32 ? 3 : 4;       // stages (rows of 64 KB: 192 KB)
 
-template <int DT, int BITS, int NV>
-__global__ void __launch_bounds__(NV * Elem<DT>::kVec == 32 ? 1024 : 512,
-                                  NV * Elem<DT>::kVec == 32 || BITS ? 1 : 2)
+template <int DT, int BITS, int NV, int LIMIT>
+__global__ void __launch_bounds__(LIMIT, LIMIT > 256 ? 1 : NV * Elem<DT>::kVec == 32 || BITS ? 2 : 3)
 ln_forward_rows_kernel(const LnForward a, int size) {
-    using E = Elem<DT>;
-    constexpr int V = E::kVec, F = NV * V, P = V / 2;
+    constexpr int V = Elem<DT>::kVec, F = NV * V, P = V / 2;
     constexpr int kStages = kRing<F>;
     constexpr bool kKeep = F <= 16;      // w and b stay in registers
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ float red[kMaxGroups][2][32];
+    __shared__ __align__(16) float red[kMaxGroups][2][kRed];
     const Group g(size);
-    const int threads = blockDim.x, vectors = (int)(a.H / V), groups = threads / size;
+    const int vectors = (int)(a.H / V), groups = blockDim.x / size;
     const int64_t step = (int64_t)gridDim.x * groups;
-    const float n = (float)a.H, inv = __frcp_rn(n);
-    float (*const mine)[32] = red[size > 32 ? g.id : 0];
-    pdl_wait_and_release();
-    auto fetch = [&](int64_t t, int stage) {
-        if (t < a.T) {
-            const uint4 *row = reinterpret_cast<const uint4 *>(elem_at<DT>(a.x, t * a.ldx));
+    const float inv = __frcp_rn((float)a.H);
+    float (*const mine)[kRed] = red[size > 32 ? g.id : 0];
+    for (int i = threadIdx.x; i < kMaxGroups * 2 * kRed; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+    __syncthreads();
+    // slot i of stage s: shared + s * stage_bytes + i * slot_bytes
+    const uint32_t shared = shared_address(ring + threadIdx.x);
+    const uint32_t slot_bytes = blockDim.x * 16, stage_bytes = NV * slot_bytes;
+    bool in[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int j = place<DT>(g, i);
-                if (j < vectors) copy16(ring + (stage * NV + i) * threads + threadIdx.x, row + j);
-            }
+    for (int i = 0; i < NV; ++i) in[i] = place<DT>(g, i) < vectors;
+    const int64_t first = (int64_t)blockIdx.x * groups;      // of the CTA
+    pdl_wait_and_release();
+    // the next row to copy, and its pointer
+    int64_t tf = first + g.id;
+    const int64_t x_step = step * a.ldx * Elem<DT>::kSize, y_step = step * a.ldy * Elem<DT>::kSize;
+    const char *xf = elem_at<DT>(a.x, tf * a.ldx);
+    uint32_t into = shared;
+    auto fetch = [&]() {
+        if (tf < a.T) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) copy16(into + i * slot_bytes, xf + place<DT>(g, i) * 16);
         }
         copies_commit();
+        tf += step;
+        xf += x_step;
+        into = into == shared + (kStages - 1) * stage_bytes ? shared : into + stage_bytes;
     };
-    const int64_t first = (int64_t)blockIdx.x * groups;      // of the CTA
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step + g.id, s);
+    for (int s = 0; s < kStages - 1; ++s) fetch();
     uint64_t w[kKeep ? F / 2 : 1], b[kKeep ? F / 2 : 1];
     if constexpr (kKeep) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = place<DT>(g, i) < vectors ? place<DT>(g, i) : 0;
-            load_params<DT>(a.w, a.param_f32, j, 1.0f, w + i * P);
-            load_params<DT>(a.b, a.param_f32, j, 0.0f, b + i * P);
+            load_params<DT>(a.w, a.param_f32, in[i] ? place<DT>(g, i) : 0, 1.0f, w + i * P);
+            load_params<DT>(a.b, a.param_f32, in[i] ? place<DT>(g, i) : 0, 0.0f, b + i * P);
         }
     }
-    int stage = 0;
+    uint32_t from = shared;
+    char *out = elem_at<DT>(a.y, (first + g.id) * a.ldy);
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
         const int64_t t = t0 + g.id;
         const bool row = t < a.T;
@@ -227,20 +247,19 @@ ln_forward_rows_kernel(const LnForward a, int size) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             v[i] = make_uint4(0, 0, 0, 0);
-            if (row && place<DT>(g, i) < vectors)
-                v[i] = ring[(stage * NV + i) * threads + threadIdx.x];
+            if (row && in[i]) v[i] = load_shared(from + i * slot_bytes);
             add_elems<DT>(v[i], sum);
         }
-        fetch(t + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        from = from == shared + (kStages - 1) * stage_bytes ? shared : from + stage_bytes;
+        fetch();
         float s[1] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]))};
         row_sums(s, mine[0], g);
-        const float mu = divided(s[0], n, inv);
+        const float mu = __fmul_rn(s[0], inv);
         uint64_t d[F / 2], q0 = 0, q1 = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             differences<DT>(v[i], mu, d + i * P);
-            if (place<DT>(g, i) < vectors) {
+            if (in[i]) {
 #pragma unroll
                 for (int k = i * P; k < i * P + P; k += 2) {
                     q0 = fma_f32x2(d[k], d[k], q0);
@@ -250,14 +269,13 @@ ln_forward_rows_kernel(const LnForward a, int size) {
         }
         float q[1] = {__fadd_rn(sum_pair(q0), sum_pair(q1))};
         row_sums(q, mine[1], g);
-        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(divided(q[0], n, inv), a.eps)));
+        const float r = inv_sqrt(__fmaf_rn(q[0], inv, a.eps));
         const uint64_t r2 = f32x2(r, r);
-        uint4 *out = reinterpret_cast<uint4 *>(elem_at<DT>(a.y, t * a.ldy));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = place<DT>(g, i);
             uint64_t *y = d + i * P;
-            if (!row || j >= vectors) continue;
+            if (!row || !in[i]) continue;
             uint64_t wj[P], bj[P];
             if constexpr (!kKeep) {
                 load_params<DT>(a.w, a.param_f32, j, 1.0f, wj);
@@ -267,15 +285,15 @@ ln_forward_rows_kernel(const LnForward a, int size) {
             for (int k = 0; k < P; ++k)
                 y[k] = fma_f32x2(mul_f32x2(y[k], r2), kKeep ? w[kKeep ? i * P + k : 0] : wj[k],
                                  kKeep ? b[kKeep ? i * P + k : 0] : bj[k]);
-            out[j] = pack2<DT>(y);
+            *reinterpret_cast<uint4 *>(out + j * 16) = pack2<DT>(y);
         }
+        out += y_step;
         if constexpr (BITS != 0) {
 #pragma unroll
             for (int i = 0; i < NV; i += 2) {
-                const int j = place<DT>(g, i);
-                const int64_t blk = t * (a.H / kBlock) + j / 16;
+                const int64_t blk = t * (a.H / kBlock) + place<DT>(g, i) / 16;
                 quantize_octet<BITS>(v[i], v[i + 1], static_cast<uint32_t *>(a.codes) + blk * 4 * BITS,
-                                     a.scales + blk, row && j < vectors);
+                                     a.scales + blk, row && in[i]);
             }
         }
         if (g.tid == 0 && row) {
@@ -374,14 +392,16 @@ __host__ __device__ constexpr int row_slots(int H) {
 // alignment: the rows are copied and written in 16-byte vectors at the boundaries of
 // their own addresses, with shared memory in between.
 template <int DT, int NE>
-__global__ void __launch_bounds__(1024) ln_forward_any_kernel(const LnForward a) {
+__global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) {
     using E = Elem<DT>;
     using Word = typename E::Word;
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ float red[2][32];
+    __shared__ __align__(16) float red[2][kRed];
+    if (threadIdx.x < 2 * kRed) (&red[0][0])[threadIdx.x] = 0.0f;
+    if (blockDim.x == 32) red[1][threadIdx.x] = 0.0f;
     const Group g(blockDim.x);
     const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H, vectors = row_slots<DT>(H);
-    const float n = (float)a.H, inv = __frcp_rn(n);
+    const float inv = __frcp_rn((float)a.H);
     const int64_t step = gridDim.x;
     RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
     uint4 *staged = ring + kAnyStages * vectors;                  // two rows of y
@@ -391,6 +411,13 @@ __global__ void __launch_bounds__(1024) ln_forward_any_kernel(const LnForward a)
         x.fetch(blockIdx.x + s * step, s);
         copies_commit();
     }
+    const int held = (H - tid + threads - 1) / threads;           // elements of this thread
+    float w[NE], b[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        w[i] = i < held ? param<DT>(a.w, a.param_f32, tid + i * threads, 1.0f) : 0.0f;
+        b[i] = i < held ? param<DT>(a.b, a.param_f32, tid + i * threads, 0.0f) : 0.0f;
+    }
     int stage = 0, half = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += step) {
         copies_left<kAnyStages - 2>();
@@ -398,35 +425,31 @@ __global__ void __launch_bounds__(1024) ln_forward_any_kernel(const LnForward a)
         __syncthreads();                                          // the row is complete
         x.fetch(t + (kAnyStages - 1) * step, stage == 0 ? kAnyStages - 1 : stage - 1);
         copies_commit();
-        const Word *row = x.row(t, stage);
+        const Word *row = x.row(t, stage) + tid;
         stage = stage + 1 == kAnyStages ? 0 : stage + 1;
         float f[NE], s[1] = {0.0f}, q[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            f[i] = tid + i * threads < H ? E::up(row[tid + i * threads]) : 0.0f;
+            f[i] = i < held ? E::up(row[i * threads]) : 0.0f;
             s[0] = __fadd_rn(s[0], f[i]);
         }
         row_sums(s, red[0], g);
-        const float mu = divided(s[0], n, inv);
+        const float mu = __fmul_rn(s[0], inv);
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             f[i] = __fsub_rn(f[i], mu);
-            if (tid + i * threads < H) q[0] = __fmaf_rn(f[i], f[i], q[0]);
+            if (i < held) q[0] = __fmaf_rn(f[i], f[i], q[0]);
         }
         row_sums(q, red[1], g);
-        const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(divided(q[0], n, inv), a.eps)));
+        const float r = inv_sqrt(__fmaf_rn(q[0], inv, a.eps));
         void *out = elem_at<DT>(a.y, t * a.ldy);
         uint4 *mine = staged + half * vectors;
         half ^= 1;
         Word *words = reinterpret_cast<Word *>(mine) +
-                      (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize;
+                      (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize + tid;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = tid + i * threads;
-            if (e >= H) break;
-            words[e] = E::down(__fmaf_rn(__fmul_rn(f[i], r), param<DT>(a.w, a.param_f32, e, 1.0f),
-                                         param<DT>(a.b, a.param_f32, e, 0.0f)));
-        }
+        for (int i = 0; i < NE; ++i)
+            if (i < held) words[i * threads] = E::down(__fmaf_rn(__fmul_rn(f[i], r), w[i], b[i]));
         __syncthreads();
         write_row<DT>(out, H, mine);
         if (tid == 0) {
@@ -557,31 +580,44 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
     constexpr int kStages = BITS ? 4 : 3, kWords = 4 * BITS;
     constexpr int kParts = BITS ? 1 : 2;             // dy, and x
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ float red[kMaxGroups][2][64];
+    __shared__ __align__(16) float red[kMaxGroups][2][2 * kRed];
     const Group g(size);
     const int threads = blockDim.x, vectors = (int)(a.H / V), groups = threads / size;
     const int64_t step = (int64_t)gridDim.x * groups;
-    const float n = (float)a.H, inv = __frcp_rn(n);
-    float (*const mine)[64] = red[size > 32 ? g.id : 0];
+    const float inv = __frcp_rn((float)a.H);
+    float (*const mine)[2 * kRed] = red[size > 32 ? g.id : 0];
+    for (int i = threadIdx.x; i < kMaxGroups * 4 * kRed; i += threads) (&red[0][0][0])[i] = 0.0f;
+    __syncthreads();
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) in[i] = place<DT>(g, i) < vectors;
     pdl_wait_and_release();
-    // slot i of part p of a stage
-    auto slot = [&](int stage, int p, int i) {
-        return ring + ((stage * kParts + p) * NV + i) * threads + threadIdx.x;
-    };
-    auto fetch = [&](int64_t t, int stage) {
-        if (t < a.T) {
-            const uint4 *dy = reinterpret_cast<const uint4 *>(elem_at<DT>(a.dy, t * a.lddy));
-            const uint4 *x = reinterpret_cast<const uint4 *>(elem_at<DT>(a.x, BITS ? 0 : t * a.ldx));
+    // slot i of part p of stage s: shared + s * stage_bytes + (p * NV + i) * slot_bytes
+    const uint32_t shared = shared_address(ring + threadIdx.x);
+    const uint32_t slot_bytes = threads * 16, stage_bytes = kParts * NV * slot_bytes;
+    const int64_t first = (int64_t)blockIdx.x * groups;      // of the CTA
+    // the next row to copy, and its pointers
+    int64_t tf = first + g.id;
+    const char *dyf = elem_at<DT>(a.dy, tf * a.lddy);
+    const char *xf = BITS ? nullptr : elem_at<DT>(a.x, tf * a.ldx);
+    const int64_t dy_step = step * a.lddy * E::kSize, x_step = step * a.ldx * E::kSize;
+    uint32_t into = shared;
+    auto fetch = [&]() {
+        if (tf < a.T) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int j = place<DT>(g, i);
-                if (j < vectors) {
-                    copy16(slot(stage, 0, i), dy + j);
-                    if constexpr (BITS == 0) copy16(slot(stage, 1, i), x + j);
+                if (in[i]) {
+                    copy16(into + i * slot_bytes, dyf + place<DT>(g, i) * 16);
+                    if constexpr (BITS == 0)
+                        copy16(into + (NV + i) * slot_bytes, xf + place<DT>(g, i) * 16);
                 }
             }
         }
         copies_commit();
+        tf += step;
+        dyf += dy_step;
+        if constexpr (BITS == 0) xf += x_step;
+        into = into == shared + (kStages - 1) * stage_bytes ? shared : into + stage_bytes;
     };
     // what does not come in 16-byte copies is loaded a row ahead into registers
     uint32_t lo[2], hi[2];
@@ -601,18 +637,19 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
             scale = __ldg(a.scales + blk);
         }
     };
-    const int64_t first = (int64_t)blockIdx.x * groups;      // of the CTA
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step + g.id, s);
+    for (int s = 0; s < kStages - 1; ++s) fetch();
     ahead(first + g.id);
     uint64_t w[F / 2], dw[F / 2], db[F / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        load_params<DT>(a.w, a.param_f32, place<DT>(g, i) < vectors ? place<DT>(g, i) : 0, 1.0f,
-                        w + i * P);
+        load_params<DT>(a.w, a.param_f32, in[i] ? place<DT>(g, i) : 0, 1.0f, w + i * P);
 #pragma unroll
     for (int i = 0; i < F / 2; ++i) dw[i] = db[i] = 0;
-    int stage = 0, half = 0;
+    uint32_t from = shared;
+    int half = 0;
+    char *out = elem_at<DT>(a.dx, (first + g.id) * a.lddx);
+    const int64_t dx_step = step * a.lddx * E::kSize;
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
         const int64_t t = t0 + g.id;
         const bool row = t < a.T;
@@ -624,16 +661,16 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
         for (int i = 0; i < NV; ++i) {
             uint4 vd = make_uint4(0, 0, 0, 0);
             vx[i] = vd;
-            if (row && place<DT>(g, i) < vectors) {
-                vd = *slot(stage, 0, i);
-                if constexpr (BITS == 0) vx[i] = *slot(stage, 1, i);
+            if (row && in[i]) {
+                vd = load_shared(from + i * slot_bytes);
+                if constexpr (BITS == 0) vx[i] = load_shared(from + (NV + i) * slot_bytes);
                 else vx[i] = dequantize_chunk<BITS>(lo[i], hi[i], scale);
             }
             unpack2<DT>(vd, d + i * P);
         }
-        fetch(t + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+        from = from == shared + (kStages - 1) * stage_bytes ? shared : from + stage_bytes;
+        fetch();
         ahead(t + step);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
         uint64_t g0 = 0, g1 = 0;
         if constexpr (BITS == 0) {
             // (lanes and rows beyond the end have dy = 0: their terms are 0)
@@ -650,8 +687,8 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
             float s[2] = {sum_pair(g0), sum_pair(g1)};
             row_sums(s, mine[half], g);
             half ^= 1;
-            s0 = divided(s[0], n, inv);
-            s1 = divided(s[1], n, inv);
+            s0 = __fmul_rn(s[0], inv);
+            s1 = __fmul_rn(s[1], inv);
         } else {
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -661,13 +698,13 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
             float s[2] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])),
                           sum_pair(g0)};
             row_sums(s, mine[0], g);
-            mu = divided(s[0], n, inv);
-            s0 = divided(s[1], n, inv);
+            mu = __fmul_rn(s[0], inv);
+            s0 = __fmul_rn(s[1], inv);
             uint64_t q0 = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 differences<DT>(vx[i], mu, x + i * P);
-                if (place<DT>(g, i) < vectors) {
+                if (in[i]) {
 #pragma unroll
                     for (int k = i * P; k < i * P + P; ++k) {
                         q0 = fma_f32x2(x[k], x[k], q0);
@@ -677,17 +714,16 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
             }
             float q[2] = {sum_pair(q0), sum_pair(g1)};
             row_sums(q, mine[1], g);
-            r = __frcp_rn(__fsqrt_rn(__fadd_rn(divided(q[0], n, inv), a.eps)));
-            s1 = divided(__fmul_rn(q[1], r), n, inv);
+            r = inv_sqrt(__fmaf_rn(q[0], inv, a.eps));
+            s1 = __fmul_rn(__fmul_rn(q[1], r), inv);
             const uint64_t r2 = f32x2(r, r);
 #pragma unroll
             for (int k = 0; k < F / 2; ++k) x[k] = mul_f32x2(x[k], r2);
         }
         const uint64_t r2 = f32x2(r, r), s02 = f32x2(s0, s0), s12 = f32x2(-s1, -s1);
-        uint4 *out = reinterpret_cast<uint4 *>(elem_at<DT>(a.dx, t * a.lddx));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (!row || place<DT>(g, i) >= vectors) continue;
+            if (!row || !in[i]) continue;
             uint64_t o[P];
 #pragma unroll
             for (int k = 0; k < P; ++k) {
@@ -696,8 +732,9 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
                 dw[m] = fma_f32x2(d[m], x[m], dw[m]);
                 db[m] = add_f32x2(db[m], d[m]);
             }
-            out[place<DT>(g, i)] = pack2<DT>(o);
+            *reinterpret_cast<uint4 *>(out + place<DT>(g, i) * 16) = pack2<DT>(o);
         }
+        out += dx_step;
     }
     if (!a.dw && !a.db) return;
     float *partial = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
@@ -734,10 +771,11 @@ __global__ void __launch_bounds__(512) ln_backward_any_kernel(const LnBackward a
     using E = Elem<DT>;
     using Word = typename E::Word;
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ float red[2][64];
+    __shared__ __align__(16) float red[2][2 * kRed];
+    for (int i = threadIdx.x; i < 4 * kRed; i += blockDim.x) (&red[0][0])[i] = 0.0f;
     const Group g(blockDim.x);
     const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H, vectors = row_slots<DT>(H);
-    const float n = (float)a.H, inv = __frcp_rn(n);
+    const float inv = __frcp_rn((float)a.H);
     const int64_t step = gridDim.x;
     RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
     RowRing<DT, kAnyStages> y{a.dy, a.lddy, a.T, step, H, vectors, ring + kAnyStages * vectors};
@@ -749,10 +787,11 @@ __global__ void __launch_bounds__(512) ln_backward_any_kernel(const LnBackward a
         y.fetch(blockIdx.x + s * step, s);
         copies_commit();
     }
+    const int held = (H - tid + threads - 1) / threads;           // elements of this thread
     float w[NE], dw[NE], db[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        w[i] = tid + i * threads < H ? param<DT>(a.w, a.param_f32, tid + i * threads, 1.0f) : 0.0f;
+        w[i] = i < held ? param<DT>(a.w, a.param_f32, tid + i * threads, 1.0f) : 0.0f;
         dw[i] = db[i] = 0.0f;
     }
     float mean = 0.0f, rstd = 0.0f;
@@ -775,33 +814,31 @@ __global__ void __launch_bounds__(512) ln_backward_any_kernel(const LnBackward a
         copies_commit();
         const float mu = mean, r = rstd;
         ahead(t + step);
-        const Word *rx = x.row(t, stage), *ry = y.row(t, stage);
+        const Word *rx = x.row(t, stage) + tid, *ry = y.row(t, stage) + tid;
         stage = stage + 1 == kAnyStages ? 0 : stage + 1;
         float xh[NE], d[NE], s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const int e = tid + i * threads;
             xh[i] = d[i] = 0.0f;
-            if (e < H) {
-                xh[i] = __fmul_rn(__fsub_rn(E::up(rx[e]), mu), r);
-                d[i] = E::up(ry[e]);
+            if (i < held) {
+                xh[i] = __fmul_rn(__fsub_rn(E::up(rx[i * threads]), mu), r);
+                d[i] = E::up(ry[i * threads]);
             }
             const float gi = __fmul_rn(d[i], w[i]);
             s[0] = __fadd_rn(s[0], gi);
             s[1] = __fmaf_rn(gi, xh[i], s[1]);
         }
         row_sums(s, red[half], g);
-        const float s0 = divided(s[0], n, inv), s1 = divided(s[1], n, inv);
+        const float s0 = __fmul_rn(s[0], inv), s1 = __fmul_rn(s[1], inv);
         void *out = elem_at<DT>(a.dx, t * a.lddx);
         uint4 *mine = staged + half * vectors;
         half ^= 1;
         Word *words = reinterpret_cast<Word *>(mine) +
-                      (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize;
+                      (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize + tid;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const int e = tid + i * threads;
-            if (e < H)
-                words[e] = E::down(
+            if (i < held)
+                words[i * threads] = E::down(
                     __fmul_rn(r, __fmaf_rn(-xh[i], s1, __fsub_rn(__fmul_rn(d[i], w[i]), s0))));
             dw[i] = __fmaf_rn(d[i], xh[i], dw[i]);
             db[i] = __fadd_rn(db[i], d[i]);
@@ -873,14 +910,14 @@ int resident_ctas(K kernel, int threads, size_t smem, int64_t units) {
     return grid_for(units, per_sm > 0 ? per_sm : 1);
 }
 
-template <int DT, int BITS, int NV>
+template <int DT, int BITS, int NV, int LIMIT>
 cudaError_t forward_rows(const LnForward &a, cudaStream_t st) {
     constexpr int F = NV * Elem<DT>::kVec;
     const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
     const int threads = size * groups;
     const size_t smem = (size_t)kRing<F> * NV * threads * 16;
     static bool ready[kMaxDevices];
-    auto kernel = ln_forward_rows_kernel<DT, BITS, NV>;
+    auto kernel = ln_forward_rows_kernel<DT, BITS, NV, LIMIT>;
     // a ring of rows of 64 KB, the longest
     const cudaError_t e = allow_shared(kernel, (size_t)kRing<F> * (F == 32 ? 2 : 1) * 32768, ready);
     if (e != cudaSuccess) return e;
@@ -905,19 +942,20 @@ cudaError_t forward_any(const LnForward &a, cudaStream_t st) {
                                st, a);
 }
 
-// The kernel for the rows: whole vectors, 16 elements a thread for rows of up to 8192
+// The kernel for the rows: whole vectors, 16 elements a thread for rows of up to 4096
 // (w and b in registers too), 32 up to 64 KB; any alignment where five rows fit
 // shared memory; else element by element.
 template <int DT, int BITS>
 cudaError_t forward_bits(const LnForward &a, cudaStream_t st) {
     constexpr int V = Elem<DT>::kVec;
     if (on16(a.x, a.ldx, Elem<DT>::kSize) && on16(a.y, a.ldy, Elem<DT>::kSize) && a.H % V == 0) {
-        if (a.H <= 8192) return forward_rows<DT, BITS, 16 / V>(a, st);
-        if (a.H <= kLongRow / Elem<DT>::kSize) return forward_rows<DT, BITS, 32 / V>(a, st);
+        if (a.H <= 4096) return forward_rows<DT, BITS, 16 / V, 256>(a, st);
+        if (a.H <= 8192) return forward_rows<DT, BITS, 32 / V, 256>(a, st);
+        if (a.H <= kLongRow / Elem<DT>::kSize) return forward_rows<DT, BITS, 32 / V, 1024>(a, st);
     }
     if (a.H <= 512) return forward_any<DT, 4>(a, st);
     if (a.H <= 16384 && (size_t)(kAnyStages + 2) * row_slots<DT>((int)a.H) * 16 <= kMostShared)
-        return forward_any<DT, 16>(a, st);
+        return a.H <= 8192 ? forward_any<DT, 16>(a, st) : forward_any<DT, 32>(a, st);
     return launch_pdl(ln_forward_kernel<DT>, grid_for(a.T, 8), kThreads, 0, st, a.x, a.ldx, a.w, a.b,
                       a.param_f32, a.T, a.H, a.eps, a.y, a.ldy, a.mean, a.rstd);
 }
