@@ -393,26 +393,30 @@ DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 
 
-class _Launch:
-    """The stream of a call, and tensors allocated for it: they belong to that
-    stream, so memory that torch's current stream still uses is not written by
-    another one.  Inputs are the caller's to order and keep alive."""
+_empty = torch.empty
+_raw_stream = torch._C._cuda_getCurrentRawStream      # torch.cuda.current_stream() costs 2 us
 
-    def __init__(self, stream, device):
-        current = torch.cuda.current_stream(device)
-        if stream is None:
-            self.handle, self.other = current.cuda_stream, None
-            return
-        self.handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-        self.other = None
-        if self.handle != current.cuda_stream:
-            self.other = torch.cuda.ExternalStream(self.handle, device=device)
 
-    def empty(self, shape, dtype, device):
-        if self.other is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.other):
-            return torch.empty(shape, dtype=dtype, device=device)
+def _launch(stream, device):
+    """(handle, other) of a call's stream: other is None for torch's current stream, else the
+    stream to allocate on (see _new)."""
+    current = _raw_stream(device.index)
+    if stream is None:
+        return current, None
+    handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if handle == current:
+        return handle, None
+    return handle, torch.cuda.ExternalStream(handle, device=device)
+
+
+def _new(other, shape, dtype, device):
+    """A tensor allocated for a call's stream: it belongs to that stream, so memory that
+    torch's current stream still uses is not written by another one.  (Inputs are the caller's
+    to order and keep alive.)"""
+    if other is None:
+        return _empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(other):
+        return _empty(shape, dtype=dtype, device=device)
 
 
 def _rows(t, what, n=None, T=None, dtype=None):
@@ -476,26 +480,29 @@ def agoq_layernorm_forward(x, w=None, b=None, eps=1e-5, bits=0, y=None, mean=Non
     for bits = 0, mean and rstd None unless given or wanted."""
     xp, T, H, ldx = _rows(x, "x")
     wp, bp, pd = _params(x.dtype, H, w, b)
-    at, dev = _Launch(stream, x.device), x.device
+    dev = x.device
+    handle, other = _launch(stream, dev)
     if y is None:
-        y = at.empty(x.shape, x.dtype, dev)
-    yp, _, _, ldy = _rows(y, "y", H, T, x.dtype)
+        y = _new(other, x.shape, x.dtype, dev)
+        yp, ldy = y.data_ptr(), H
+    else:
+        yp, _, _, ldy = _rows(y, "y", H, T, x.dtype)
     if mean is None and want_stats:
-        mean = at.empty(T, torch.float32, dev)
+        mean = _new(other, T, torch.float32, dev)
     if rstd is None and want_stats:
-        rstd = at.empty(T, torch.float32, dev)
+        rstd = _new(other, T, torch.float32, dev)
     if bits:
         if codes is None:
-            codes = at.empty(T * H // BLOCK * record_bytes(bits), torch.uint8, dev)
+            codes = _new(other, T * H // BLOCK * record_bytes(bits), torch.uint8, dev)
         if scales is None:
-            scales = at.empty(T * H // BLOCK, torch.float32, dev)
+            scales = _new(other, T * H // BLOCK, torch.float32, dev)
     else:
         codes = scales = None
     cp = _vector(codes, T * H // BLOCK * record_bytes(bits), "codes", (torch.uint8,))
     sp = _vector(scales, T * H // BLOCK, "scales", _F32)
     _check(lib().agoq_layernorm_forward(
         xp, ldx, wp, bp, pd, T, H, DTYPES[x.dtype], eps, yp, ldy, _vector(mean, T, "mean", _F32),
-        _vector(rstd, T, "rstd", _F32), cp, sp, bits, at.handle), "agoq_layernorm_forward")
+        _vector(rstd, T, "rstd", _F32), cp, sp, bits, handle), "agoq_layernorm_forward")
     return y, mean, rstd, codes, scales
 
 
@@ -504,13 +511,13 @@ def agoq_layernorm_backward_workspace_bytes(T, H):
     return int(lib().agoq_layernorm_backward_workspace_bytes(int(T), int(H)))
 
 
-def _norm_sums(at, T, H, dev, dw, db, want_dw, want_db, workspace):
+def _norm_sums(other, T, H, dev, dw, db, want_dw, want_db, workspace):
     if dw is None and want_dw:
-        dw = at.empty(H, torch.float32, dev)
+        dw = _new(other, H, torch.float32, dev)
     if db is None and want_db:
-        db = at.empty(H, torch.float32, dev)
+        db = _new(other, H, torch.float32, dev)
     if workspace is None and (dw is not None or db is not None):
-        workspace = at.empty(agoq_layernorm_backward_workspace_bytes(T, H), torch.uint8, dev)
+        workspace = _new(other, agoq_layernorm_backward_workspace_bytes(T, H), torch.uint8, dev)
     if workspace is None:
         return dw, db, None, 0, 0
     if not workspace.is_cuda or not workspace.is_contiguous():
@@ -525,15 +532,16 @@ def agoq_layernorm_backward(x, dy, mean, rstd, w=None, dx=None, dw=None, db=None
     xp, T, H, ldx = _rows(x, "x")
     dyp, _, _, lddy = _rows(dy, "dy", H, T, x.dtype)
     wp, _, pd = _params(x.dtype, H, w)
-    at, dev = _Launch(stream, x.device), x.device
+    dev = x.device
+    handle, other = _launch(stream, dev)
     if dx is None:
-        dx = at.empty(dy.shape, dy.dtype, dev)
+        dx = _new(other, dy.shape, dy.dtype, dev)
     dxp, _, _, lddx = _rows(dx, "dx", H, T, x.dtype)
-    dw, db, workspace, ws, nws = _norm_sums(at, T, H, dev, dw, db, want_dw, want_db, workspace)
+    dw, db, workspace, ws, nws = _norm_sums(other, T, H, dev, dw, db, want_dw, want_db, workspace)
     _check(lib().agoq_layernorm_backward(
         xp, ldx, dyp, lddy, wp, pd, _vector(mean, T, "mean", _F32),
         _vector(rstd, T, "rstd", _F32), T, H, DTYPES[x.dtype], dxp, lddx,
-        _vector(dw, H, "dw", _F32), _vector(db, H, "db", _F32), ws, nws, at.handle),
+        _vector(dw, H, "dw", _F32), _vector(db, H, "db", _F32), ws, nws, handle),
         "agoq_layernorm_backward")
     return dx, dw, db
 
@@ -544,16 +552,17 @@ def agoq_layernorm_backward_laaq(codes, scales, bits, dy, eps=1e-5, w=None, dx=N
     dequantized values): returns (dx, dw, db) as agoq_layernorm_backward."""
     dyp, T, H, lddy = _rows(dy, "dy", dtype=torch.bfloat16)
     wp, _, pd = _params(dy.dtype, H, w)
-    at, dev = _Launch(stream, dy.device), dy.device
+    dev = dy.device
+    handle, other = _launch(stream, dev)
     if dx is None:
-        dx = at.empty(dy.shape, dy.dtype, dev)
+        dx = _new(other, dy.shape, dy.dtype, dev)
     dxp, _, _, lddx = _rows(dx, "dx", H, T, dy.dtype)
-    dw, db, workspace, ws, nws = _norm_sums(at, T, H, dev, dw, db, want_dw, want_db, workspace)
+    dw, db, workspace, ws, nws = _norm_sums(other, T, H, dev, dw, db, want_dw, want_db, workspace)
     blocks = T * H // BLOCK
     _check(lib().agoq_layernorm_backward_laaq(
         _vector(codes, blocks * record_bytes(bits), "codes", (torch.uint8,)),
         _vector(scales, blocks, "scales", _F32), bits, dyp, lddy, wp, pd, T, H, eps, dxp, lddx,
-        _vector(dw, H, "dw", _F32), _vector(db, H, "db", _F32), ws, nws, at.handle),
+        _vector(dw, H, "dw", _F32), _vector(db, H, "db", _F32), ws, nws, handle),
         "agoq_layernorm_backward_laaq")
     return dx, dw, db
 
@@ -607,30 +616,30 @@ class GradList:
 
 def agoq_grad_norm(grads, norm=None, stream=None):
     """Global L2 norm of a GradList -> FP32 CUDA tensor of one element."""
-    at = _Launch(stream, grads.device)
+    handle, other = _launch(stream, grads.device)
     if norm is None:
-        norm = at.empty(1, torch.float32, grads.device)
+        norm = _new(other, 1, torch.float32, grads.device)
     _check(lib().agoq_grad_norm(grads.entries, grads.count, _vector(norm, 1, "norm", _F32),
-                                *grads._scratch(), at.handle), "agoq_grad_norm")
+                                *grads._scratch(), handle), "agoq_grad_norm")
     return norm
 
 
 def agoq_clip_grads(grads, max_norm, norm, stream=None):
     """Clip a GradList by the norm in the one-element FP32 CUDA tensor `norm`: every gradient
     times min(1, max_norm / (norm + 1e-6)); of FP8 masters the scales alone change."""
-    at = _Launch(stream, grads.device)
+    handle, other = _launch(stream, grads.device)
     _check(lib().agoq_clip_grads(grads.entries, grads.count, max_norm,
-                                 _vector(norm, 1, "norm", _F32), at.handle), "agoq_clip_grads")
+                                 _vector(norm, 1, "norm", _F32), handle), "agoq_clip_grads")
 
 
 def agoq_clip_grad_norm(grads, max_norm, norm=None, stream=None):
     """agoq_grad_norm and agoq_clip_grads in one call; returns the norm before clipping."""
-    at = _Launch(stream, grads.device)
+    handle, other = _launch(stream, grads.device)
     if norm is None:
-        norm = at.empty(1, torch.float32, grads.device)
+        norm = _new(other, 1, torch.float32, grads.device)
     _check(lib().agoq_clip_grad_norm(grads.entries, grads.count, max_norm,
                                      _vector(norm, 1, "norm", _F32), *grads._scratch(),
-                                     at.handle), "agoq_clip_grad_norm")
+                                     handle), "agoq_clip_grad_norm")
     return norm
 
 
@@ -644,22 +653,23 @@ def agoq_token_logprobs(logits, tokens, k=0, want_entropy=True, logp=None, entro
     entropy, lse, top_logp, top_ids): FP32 [T] each, FP32 and int64 [T][k] (None for k = 0);
     entropy is None unless given or wanted."""
     xp, T, V, ld = _rows(logits, "logits")
-    at, dev = _Launch(stream, logits.device), logits.device
+    dev = logits.device
+    handle, other = _launch(stream, dev)
     if logp is None:
-        logp = at.empty(T, torch.float32, dev)
+        logp = _new(other, T, torch.float32, dev)
     if entropy is None and want_entropy:
-        entropy = at.empty(T, torch.float32, dev)
+        entropy = _new(other, T, torch.float32, dev)
     if lse is None:
-        lse = at.empty(T, torch.float32, dev)
+        lse = _new(other, T, torch.float32, dev)
     if k > 0 and top_logp is None:
-        top_logp = at.empty((T, k), torch.float32, dev)
+        top_logp = _new(other, (T, k), torch.float32, dev)
     if k > 0 and top_ids is None:
-        top_ids = at.empty((T, k), torch.int64, dev)
+        top_ids = _new(other, (T, k), torch.int64, dev)
     _check(lib().agoq_token_logprobs(
         xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64), T, V, k,
         _vector(logp, T, "logp", _F32), _vector(entropy, T, "entropy", _F32),
         _vector(lse, T, "lse", _F32), _vector(top_logp, T * k, "top_logp", _F32),
-        _vector(top_ids, T * k, "top_ids", _I64), at.handle), "agoq_token_logprobs")
+        _vector(top_ids, T * k, "top_ids", _I64), handle), "agoq_token_logprobs")
     return logp, entropy, lse, top_logp, top_ids
 
 
@@ -668,15 +678,15 @@ def agoq_token_logprobs_backward(logits, tokens, lse, dlogp, entropy=None, dentr
     """Gradient of agoq_token_logprobs' logp (and entropy, with `dentropy`) -> dlogits of the
     logits' type; `dlogits` may be the logits themselves."""
     xp, T, V, ld = _rows(logits, "logits")
-    at = _Launch(stream, logits.device)
+    handle, other = _launch(stream, logits.device)
     if dlogits is None:
-        dlogits = at.empty(logits.shape, logits.dtype, logits.device)
+        dlogits = _new(other, logits.shape, logits.dtype, logits.device)
     dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
     _check(lib().agoq_token_logprobs_backward(
         xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64), T, V,
         _vector(lse, T, "lse", _F32), _vector(entropy, T, "entropy", _F32),
         _vector(dlogp, T, "dlogp", _F32), _vector(dentropy, T, "dentropy", _F32), dp, ldd,
-        at.handle), "agoq_token_logprobs_backward")
+        handle), "agoq_token_logprobs_backward")
     return dlogits
 
 
@@ -684,16 +694,17 @@ def agoq_token_loss(logits, tokens, weights=None, logp=None, dlogits=None, strea
     """Log probabilities of `tokens` and the gradient of the loss -sum(weights * logp) ->
     (logp FP32 [T], dlogits of the logits' type); `dlogits` may be the logits themselves."""
     xp, T, V, ld = _rows(logits, "logits")
-    at, dev = _Launch(stream, logits.device), logits.device
+    dev = logits.device
+    handle, other = _launch(stream, dev)
     if logp is None:
-        logp = at.empty(T, torch.float32, dev)
+        logp = _new(other, T, torch.float32, dev)
     if dlogits is None:
-        dlogits = at.empty(logits.shape, logits.dtype, dev)
+        dlogits = _new(other, logits.shape, logits.dtype, dev)
     dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
     _check(lib().agoq_token_loss(
         xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64),
         _vector(weights, T, "weights", _F32), T, V, _vector(logp, T, "logp", _F32), dp, ldd,
-        at.handle), "agoq_token_loss")
+        handle), "agoq_token_loss")
     return logp, dlogits
 
 

@@ -598,15 +598,18 @@ static agoq_status grad_norm_ok(const agoq_grad_tensor *tensors, int count, bool
     if (!norm || !workspace) return AGOQ_ERR_NULL;
     if (workspace_bytes < agoq::grad_norm_workspace_bytes(count)) return AGOQ_ERR_SHAPE;
     if (!aligned(norm, 4) || !aligned(workspace, 16)) return AGOQ_ERR_ALIGN;
-    const Range out[2] = {{norm, 4}, {workspace, (uint64_t)agoq::grad_norm_workspace_bytes(count)}};
+    const uint64_t wb = (uint64_t)agoq::grad_norm_workspace_bytes(count);
+    if (overlap(norm, 4, workspace, wb)) return AGOQ_ERR_ALIAS;
+    const uintptr_t pn = reinterpret_cast<uintptr_t>(norm), pw = reinterpret_cast<uintptr_t>(workspace);
     for (int i = 0; i < count; ++i) {
         const agoq_grad_tensor &t = tensors[i];
         const bool fp8 = t.dtype == AGOQ_E4M3;
-        const Range in[3] = {vec(t.data, t.n, elem_size(t.dtype)),
-                             vec(fp8 ? t.scales : nullptr, t.n / kBlockElems, 4),
-                             fp8 ? vec(clip ? t.out : nullptr, t.n / kBlockElems, 4)
-                                 : vec(clip ? t.out : nullptr, t.n, elem_size(t.dtype))};
-        if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+        const uint64_t db = (uint64_t)t.n * elem_size(t.dtype), sb = (uint64_t)t.n / kBlockElems * 4;
+        const Range in[3] = {{t.data, db}, {t.scales, fp8 ? sb : 0}, {t.out, clip ? (fp8 ? sb : db) : 0}};
+        for (int k = 0; k < 3; ++k) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(in[k].p), e = p + in[k].n;
+            if (in[k].n && ((p < pn + 4 && pn < e) || (p < pw + wb && pw < e))) return AGOQ_ERR_ALIAS;
+        }
     }
     return AGOQ_OK;
 }

@@ -28,12 +28,14 @@ constexpr int kPart = 8;                // vectors of a thread
 constexpr int kChunk = kPart * kThreads;
 constexpr int kMaxCtas = 1216;          // partial sums of a launch
 constexpr int kCtasPerSm = 4;
-constexpr int kList = 800, kMidList = 256, kShortList = 64;
+constexpr int kList = 1000, kMidList = 192, kShortList = 64;
 
 struct Entry {
     const char *data;
-    char *out;
-    const float *scales;
+    union {
+        const float *scales;            // of an FP8 master, for the norm
+        char *out;                      // for clipping
+    };
     int64_t n;
     int first;                          // index of its first chunk
     int dtype;
@@ -346,8 +348,8 @@ int fill(List<N> &l, const agoq_grad_tensor *t, int at, int count, bool clip) {
         Entry &e = l.e[l.count++];
         const bool scales = clip && t[at].dtype == kE4M3;
         e.data = static_cast<const char *>(scales ? (const void *)t[at].scales : t[at].data);
-        e.out = static_cast<char *>(t[at].out);
-        e.scales = t[at].scales;
+        if (clip) e.out = static_cast<char *>(t[at].out);
+        else e.scales = t[at].scales;
         e.n = scales ? t[at].n / kBlock : t[at].n;
         e.dtype = scales ? kF32 : t[at].dtype;
         e.first = l.chunks;

@@ -41,8 +41,8 @@ __device__ __forceinline__ float cta_max(float v, float *red) {
     return s;
 }
 
-// x - m, not below -1000 (where its exponential is 0 too): for x = -inf the
-// product with the exponential must be 0.  NaN stays NaN.
+// x - m, not below -1000 (where its exponential is 0 too): for x = -inf its product
+// with the exponential must be 0.  NaN stays NaN.
 __device__ __forceinline__ float below_max(float x, float m) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(__fsub_rn(x, m)), "f"(-1000.0f));
@@ -881,31 +881,116 @@ cudaError_t launch_stats(const TokenLogprobs &a, cudaStream_t st) {
     return launch_pdl_clusters(kernel, rows * c, kStatThreads, c, sizeof(StatShared), st, a);
 }
 
-template <int DT>
+// ---- the gradient of the statistics ----------------------------------------------
+//
+// One reading and one writing, nothing kept: a CTA takes a tile of a row, four vectors
+// a thread at the 16-byte boundaries of the output, its copies or loads issued before
+// the row's five scalars are used.  SHIFTED: some rows' logits lie across the output's
+// boundaries; the tile then passes through shared memory, where an output vector is cut
+// from two of the input's.
+constexpr int kTilePart = 4;
+constexpr int kTile = kTilePart * kThreads;             // vectors
+
+template <int DT, bool SHIFTED>
 __global__ void __launch_bounds__(kThreads)
-token_logprobs_backward_kernel(const TokenLogprobsBackward a) {
+token_logprobs_backward_kernel(const TokenLogprobsBackward a, int tiles) {
+    using E = Elem<DT>;
+    using Word = typename E::Word;
+    constexpr int N = E::kVec;
+    __shared__ uint4 input[SHIFTED ? kTile + 1 : 1];
     pdl_wait_and_release();
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const char *row = elem_at<DT>(a.logits, t * a.ld);
-        char *out = elem_at<DT>(a.dlogits, t * a.ldd);
+    const int V = (int)a.V;
+    for (int64_t unit = blockIdx.x; unit < a.T * tiles; unit += gridDim.x) {
+        const int64_t t = unit / tiles;
+        const int tile = (int)(unit - t * tiles) * kTile;
+        const Word *row = reinterpret_cast<const Word *>(elem_at<DT>(a.logits, t * a.ld));
+        Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.dlogits, t * a.ldd));
+        const int skip = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / E::kSize;
+        const int oskip = (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize;
+        const int shift = SHIFTED ? (skip - oskip + N) & (N - 1) : 0;     // elements
+        // the input vector that holds the first element of an output vector
+        const uint4 *vec = reinterpret_cast<const uint4 *>(row - skip) - (SHIFTED && skip < oskip);
+        uint4 *ovec = reinterpret_cast<uint4 *>(out - oskip);
+        const int vectors = (V + oskip + N - 1) / N;
+        uint4 v[SHIFTED ? 1 : kTilePart];
+        if constexpr (SHIFTED) {
+            for (int i = threadIdx.x; i <= kTile; i += kThreads) {
+                const int e = (tile + i) * N - oskip - shift;
+                if (e >= 0 && e + N <= V) copy16(input + i, vec + tile + i);
+            }
+            copies_commit();
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTilePart; ++i) {
+                const int o = tile + i * kThreads + threadIdx.x, e = o * N - oskip;
+                if (e >= 0 && e + N <= V) v[i] = vec[o];
+            }
+        }
         const int64_t token = a.tokens[t];
         const float lse = a.lse[t];
-        const bool empty = lse == -INFINITY;
-        float dl = a.dlogp[t], de = a.dentropy ? a.dentropy[t] : 0.0f;
-        const float h = a.dentropy ? a.entropy[t] : 0.0f;
-        if (token < 0 || empty) dl = 0.0f;
-        if (token >= a.V) dl = NAN;
-        if (empty) de = 0.0f;
-        for (int64_t i = threadIdx.x; i < a.V; i += kThreads) {
-            const float x = load_now<DT>(row, i);
-            float g = 0.0f;
-            if (!empty) {
-                const float l = below_max(x, lse), p = expf(l);
-                g = -__fmul_rn(p, __fmaf_rn(de, __fadd_rn(l, h), dl));
-                if (i == token) g = __fadd_rn(g, dl);
-            }
-            store_elem<DT>(out, i, g);
+        float dl = a.dlogp[t], de = 0.0f, h = 0.0f;
+        if (a.dentropy) {
+            de = a.dentropy[t];
+            h = a.entropy[t];
         }
+        const bool empty = lse == -INFINITY;
+        if (token < 0) dl = 0.0f;
+        if (token >= a.V) dl = NAN;
+        // g = p (c0 + c1 l), l = x - lse
+        const float c0 = -__fmaf_rn(de, h, dl), c1 = -de;
+        const int at = token >= 0 && token < a.V ? (int)token : -1;
+        if constexpr (SHIFTED) {
+            copies_left<0>();
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < kTilePart; ++i) {
+            const int k0 = i * kThreads + threadIdx.x, o = tile + k0, e = o * N - oskip;
+            if (o >= vectors) break;
+            // (a shifted vector needs two whole input vectors)
+            if (SHIFTED && shift ? e >= N && e + 2 * N <= V : e >= 0 && e + N <= V) {
+                if (empty) {
+                    ovec[o] = make_uint4(0, 0, 0, 0);
+                    continue;
+                }
+                uint4 x;
+                if constexpr (SHIFTED) x = bytes_from(input[k0], input[k0 + 1], shift * E::kSize);
+                else x = v[i];
+                uint64_t l[N / 2];
+                differences<DT>(x, lse, l);
+                float g[N];
+#pragma unroll
+                for (int k = 0; k < N / 2; ++k) {
+                    float lo = lo_f32(l[k]), hi = hi_f32(l[k]);
+                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(-1000.0f));
+                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(-1000.0f));
+                    l[k] = f32x2(lo, hi);
+                    const uint64_t y = mul_f32x2(l[k], f32x2(kLog2e, kLog2e));
+                    const uint64_t p = f32x2(exp2_approx(lo_f32(y)), exp2_approx(hi_f32(y)));
+                    const uint64_t q = mul_f32x2(p, fma_f32x2(l[k], f32x2(c1, c1), f32x2(c0, c0)));
+                    g[2 * k] = lo_f32(q);
+                    g[2 * k + 1] = hi_f32(q);
+                }
+                if ((unsigned)(at - e) < (unsigned)N) {
+#pragma unroll
+                    for (int k = 0; k < N; ++k)
+                        if (e + k == at) g[k] = __fadd_rn(g[k], dl);
+                }
+                ovec[o] = E::pack(g);
+            } else {
+                for (int k = 0; k < N; ++k) {
+                    if (e + k < 0 || e + k >= V) continue;
+                    float g = 0.0f;
+                    if (!empty) {
+                        const float l = below_max(E::up(row[e + k]), lse);
+                        g = __fmul_rn(exp_approx(l), __fmaf_rn(l, c1, c0));
+                        if (e + k == at) g = __fadd_rn(g, dl);
+                    }
+                    out[e + k] = E::down(g);
+                }
+            }
+        }
+        if constexpr (SHIFTED) __syncthreads();       // input is copied again
     }
 }
 
@@ -934,11 +1019,27 @@ cudaError_t launch_token_logprobs(const TokenLogprobs &a, cudaStream_t st) {
     return launch_pdl(k, grid_for(a.T), kThreads, 0, st, a);
 }
 
+namespace {
+
+template <int DT>
+cudaError_t launch_backward(const TokenLogprobsBackward &a, cudaStream_t st) {
+    constexpr int kSize = Elem<DT>::kSize, N = Elem<DT>::kVec;
+    // rows of both tensors that all start at the same place between 16-byte boundaries
+    const bool level = ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.dlogits)) & 15u) == 0 &&
+                       (a.T == 1 || (a.ld - a.ldd) * kSize % 16 == 0);
+    const int64_t tiles = (a.V + N - 1 + (int64_t)kTile * N - 1) / ((int64_t)kTile * N);
+    const int64_t units = a.T * tiles, most = 1 << 30;
+    return launch_pdl(level ? token_logprobs_backward_kernel<DT, false>
+                            : token_logprobs_backward_kernel<DT, true>,
+                      (int)(units < most ? units : most), kThreads, 0, st, a, (int)tiles);
+}
+
+}  // namespace
+
 cudaError_t launch_token_logprobs_backward(const TokenLogprobsBackward &a, cudaStream_t st) {
-    auto k = a.dtype == kF32    ? token_logprobs_backward_kernel<kF32>
-             : a.dtype == kBF16 ? token_logprobs_backward_kernel<kBF16>
-                                : token_logprobs_backward_kernel<kF16>;
-    return launch_pdl(k, grid_for(a.T), kThreads, 0, st, a);
+    return a.dtype == kF32    ? launch_backward<kF32>(a, st)
+           : a.dtype == kBF16 ? launch_backward<kBF16>(a, st)
+                              : launch_backward<kF16>(a, st);
 }
 
 }  // namespace agoq

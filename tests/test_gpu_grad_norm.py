@@ -53,7 +53,7 @@ LISTS = {
     "odd": [(1, BF16), (3, F16), (0, F32), (7, F32), (127, BF16), (129, F16), (4097, F32)],
     "long": [(3_000_001, BF16), (17, F32), (1_000_003, F16), (500_000, F32)],
     "masters": [(128, "e4m3"), (128 * 300, "e4m3"), (128 * 4001, "e4m3"), (4096, F32)],
-    "many": [(64 + 5 * i, (F32, BF16, F16)[i % 3]) for i in range(900)],
+    "many": [(64 + 5 * i, (F32, BF16, F16)[i % 3]) for i in range(1100)],
     "ends": [(8192, F32), (8193, F32), (16384, BF16), (16383, F16), (32768, "e4m3"),
              (32768 + 128, "e4m3")],
 }
