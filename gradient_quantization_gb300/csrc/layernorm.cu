@@ -83,12 +83,16 @@ struct Group {
     }
 };
 
-// The sums of the group's values (each thread gets them), in a fixed order; `red`
-// holds kRed floats a value, 0 where no warp writes, and is free again after the group's
-// next barrier.  All threads of a warp call it.
+// The sums of N = 1, 2 or 4 values over the group (each thread gets them), in a fixed
+// order; `red` holds kRed floats a value, 0 where no warp writes, and is free again
+// after the group's next barrier.  All threads of a warp call it.  Several values halve
+// in number at each of the first exchanges, a half warp (quarter) going on with its
+// own: six shuffles for four values.
 constexpr int kRed = 32;
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float *red, const Group &g) {
+    static_assert(N == 1 || N == 2 || N == 4, "values");
+    const int lane = threadIdx.x & 31;
     if (g.size < 32) {
         for (int o = g.size >> 1; o > 0; o >>= 1) {
 #pragma unroll
@@ -96,16 +100,29 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float *red, const Group 
         }
         return;
     }
+    float s[N];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int i = 0; i < N; ++i) s[i] = v[i];
+    int o = 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xFFFFFFFFu, v[i], o));
+    for (int m = N / 2; m > 0; m >>= 1) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+            const float keep = upper ? s[m + i] : s[i], give = upper ? s[i] : s[m + i];
+            s[i] = __fadd_rn(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+        }
+        o >>= 1;
     }
-    if (g.size == 32) return;
-    if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) red[kRed * i + (g.tid >> 5)] = v[i];
+    for (; o > 0; o >>= 1) s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xFFFFFFFFu, s[0], o));
+    // lane 32 / N * i has the warp's sum of value i (N = 4: of 0, 1, 2, 3 in order)
+    if (g.size == 32) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, s[0], 32 / N * i);
+        return;
     }
+    if (lane % (32 / N) == 0) red[kRed * (lane / (32 / N)) + (g.tid >> 5)] = s[0];
     g.sync();
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.0f;
@@ -570,76 +587,93 @@ __global__ void __launch_bounds__(kThreads) ln_backward_kernel(
 }
 
 // Rows that start at 16-byte boundaries and hold whole vectors: as the forward pass,
-// x and dy read once, dx written once.  A thread adds its columns' terms of dw and db
-// in registers over all rows of its group; the groups of a CTA join theirs in order,
-// and the CTA writes one row of the partial sums ([grid][2][H]).
+// x and dy read once, dx written once; R rows a group and step, whose sums share the
+// exchanges and the barrier.  The rows are unpacked twice from the ring, once for the
+// sums and once for the results: that costs less than the registers that would hold
+// them.  A thread adds its columns' terms of dw and db in registers over all rows of
+// its group; the groups of a CTA join theirs in order, and the CTA writes one row of the
+// partial sums ([grid][2][H]).
+template <int DT>
+constexpr int kBackRows = DT == kF32 ? 1 : 2;
+constexpr int kBackStages = 3;
+
 template <int DT, int BITS>
 __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward a, int size) {
     using E = Elem<DT>;
-    constexpr int V = E::kVec, F = 16, NV = F / V, P = V / 2;
-    constexpr int kStages = BITS ? 4 : 3, kWords = 4 * BITS;
+    constexpr int V = E::kVec, F = 16, NV = F / V, P = V / 2, R = kBackRows<DT>;
+    constexpr int kStages = kBackStages, kWords = 4 * BITS;
     constexpr int kParts = BITS ? 1 : 2;             // dy, and x
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ __align__(16) float red[kMaxGroups][2][2 * kRed];
+    __shared__ __align__(16) float red[kMaxGroups][2][2 * R * kRed];
     const Group g(size);
     const int threads = blockDim.x, vectors = (int)(a.H / V), groups = threads / size;
-    const int64_t step = (int64_t)gridDim.x * groups;
+    const int64_t step = (int64_t)gridDim.x * groups * R;
     const float inv = __frcp_rn((float)a.H);
-    float (*const mine)[2 * kRed] = red[size > 32 ? g.id : 0];
-    for (int i = threadIdx.x; i < kMaxGroups * 4 * kRed; i += threads) (&red[0][0][0])[i] = 0.0f;
+    float (*const mine)[2 * R * kRed] = red[size > 32 ? g.id : 0];
+    for (int i = threadIdx.x; i < kMaxGroups * 4 * R * kRed; i += threads) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) in[i] = place<DT>(g, i) < vectors;
     pdl_wait_and_release();
-    // slot i of part p of stage s: shared + s * stage_bytes + (p * NV + i) * slot_bytes
+    // slot i of part p of row r of stage s: shared + s * stage_bytes +
+    // ((r * kParts + p) * NV + i) * slot_bytes
     const uint32_t shared = shared_address(ring + threadIdx.x);
-    const uint32_t slot_bytes = threads * 16, stage_bytes = kParts * NV * slot_bytes;
-    const int64_t first = (int64_t)blockIdx.x * groups;      // of the CTA
-    // the next row to copy, and its pointers
-    int64_t tf = first + g.id;
+    const uint32_t slot_bytes = threads * 16, stage_bytes = R * kParts * NV * slot_bytes;
+    const int64_t first = (int64_t)blockIdx.x * groups * R;      // of the CTA
+    // the next rows to copy, and their pointers
+    int64_t tf = first + g.id * R;
     const char *dyf = elem_at<DT>(a.dy, tf * a.lddy);
     const char *xf = BITS ? nullptr : elem_at<DT>(a.x, tf * a.ldx);
-    const int64_t dy_step = step * a.lddy * E::kSize, x_step = step * a.ldx * E::kSize;
+    const int64_t dy_row = a.lddy * E::kSize, x_row = a.ldx * E::kSize;
     uint32_t into = shared;
     auto fetch = [&]() {
-        if (tf < a.T) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (tf + r >= a.T) break;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (in[i]) {
-                    copy16(into + i * slot_bytes, dyf + place<DT>(g, i) * 16);
+                    copy16(into + (r * kParts * NV + i) * slot_bytes,
+                           dyf + r * dy_row + place<DT>(g, i) * 16);
                     if constexpr (BITS == 0)
-                        copy16(into + (NV + i) * slot_bytes, xf + place<DT>(g, i) * 16);
+                        copy16(into + ((r * kParts + 1) * NV + i) * slot_bytes,
+                               xf + r * x_row + place<DT>(g, i) * 16);
                 }
             }
         }
         copies_commit();
         tf += step;
-        dyf += dy_step;
-        if constexpr (BITS == 0) xf += x_step;
+        dyf += step * dy_row;
+        if constexpr (BITS == 0) xf += step * x_row;
         into = into == shared + (kStages - 1) * stage_bytes ? shared : into + stage_bytes;
     };
-    // what does not come in 16-byte copies is loaded a row ahead into registers
-    uint32_t lo[2], hi[2];
-    float scale = 0.0f, mean = 0.0f, rstd = 0.0f;
+    // what does not come in 16-byte copies is loaded a step ahead into registers
+    uint32_t lo[R][2], hi[R][2];
+    float scale[R], mean[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) scale[r] = mean[r] = rstd[r] = 0.0f;
     auto ahead = [&](int64_t t) {
-        if (t >= a.T) return;
-        if constexpr (BITS == 0) {
-            mean = __ldg(a.mean + t);
-            rstd = __ldg(a.rstd + t);
-        } else {
-            const int j = place<DT>(g, 0);           // the octet's block
-            if (j >= vectors) return;
-            const int64_t blk = t * (a.H / kBlock) + j / 16;
-            const uint32_t *rec = static_cast<const uint32_t *>(a.x) + blk * kWords;
-            load_chunk<BITS>(rec, j & 7, lo[0], hi[0]);
-            load_chunk<BITS>(rec, (j & 7) + 8, lo[1], hi[1]);
-            scale = __ldg(a.scales + blk);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (t + r >= a.T) return;
+            if constexpr (BITS == 0) {
+                mean[r] = __ldg(a.mean + t + r);
+                rstd[r] = __ldg(a.rstd + t + r);
+            } else {
+                const int j = place<DT>(g, 0);           // the octet's block
+                if (!in[0]) return;
+                const int64_t blk = (t + r) * (a.H / kBlock) + j / 16;
+                const uint32_t *rec = static_cast<const uint32_t *>(a.x) + blk * kWords;
+                load_chunk<BITS>(rec, j & 7, lo[r][0], hi[r][0]);
+                load_chunk<BITS>(rec, (j & 7) + 8, lo[r][1], hi[r][1]);
+                scale[r] = __ldg(a.scales + blk);
+            }
         }
     };
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) fetch();
-    ahead(first + g.id);
+    ahead(first + g.id * R);
     uint64_t w[F / 2], dw[F / 2], db[F / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -648,93 +682,123 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
     for (int i = 0; i < F / 2; ++i) dw[i] = db[i] = 0;
     uint32_t from = shared;
     int half = 0;
-    char *out = elem_at<DT>(a.dx, (first + g.id) * a.lddx);
-    const int64_t dx_step = step * a.lddx * E::kSize;
+    char *out = elem_at<DT>(a.dx, (first + g.id * R) * a.lddx);
+    const int64_t dx_row = a.lddx * E::kSize;
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
-        const int64_t t = t0 + g.id;
-        const bool row = t < a.T;
+        const int64_t t = t0 + g.id * R;
         copies_left<kStages - 2>();
-        uint64_t x[F / 2], d[F / 2];      // xh; dy
-        float mu = mean, r = rstd, s0, s1;
-        uint4 vx[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            uint4 vd = make_uint4(0, 0, 0, 0);
-            vx[i] = vd;
-            if (row && in[i]) {
-                vd = load_shared(from + i * slot_bytes);
-                if constexpr (BITS == 0) vx[i] = load_shared(from + (NV + i) * slot_bytes);
-                else vx[i] = dequantize_chunk<BITS>(lo[i], hi[i], scale);
+        float mu[R], rs[R], s0[R], s1[R];
+        uint4 vx[R][NV];                  // of codes: the dequantized row
+        // the row's vector i of dy and (not of codes) x; 0 beyond its end and beyond T
+        auto load = [&](int r, int i, uint4 &d, uint4 &x) {
+            d = x = make_uint4(0, 0, 0, 0);
+            if (t + r < a.T && in[i]) {
+                d = load_shared(from + (r * kParts * NV + i) * slot_bytes);
+                if constexpr (BITS == 0) x = load_shared(from + ((r * kParts + 1) * NV + i) * slot_bytes);
             }
-            unpack2<DT>(vd, d + i * P);
+            if constexpr (BITS != 0) x = vx[r][i];
+        };
+        if constexpr (BITS != 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    vx[r][i] = make_uint4(0, 0, 0, 0);
+                    if (t + r < a.T && in[i])
+                        vx[r][i] = dequantize_chunk<BITS>(lo[r][i & 1], hi[r][i & 1], scale[r]);
+                }
         }
-        from = from == shared + (kStages - 1) * stage_bytes ? shared : from + stage_bytes;
-        fetch();
-        ahead(t + step);
-        uint64_t g0 = 0, g1 = 0;
-        if constexpr (BITS == 0) {
-            // (lanes and rows beyond the end have dy = 0: their terms are 0)
-            const uint64_t r2 = f32x2(r, r);
+        float s[2 * R];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) differences<DT>(vx[i], mu, x + i * P);
-#pragma unroll
-            for (int k = 0; k < F / 2; ++k) {
-                x[k] = mul_f32x2(x[k], r2);
-                const uint64_t gk = mul_f32x2(d[k], w[k]);
-                g0 = add_f32x2(g0, gk);
-                g1 = fma_f32x2(gk, x[k], g1);
-            }
-            float s[2] = {sum_pair(g0), sum_pair(g1)};
-            row_sums(s, mine[half], g);
-            half ^= 1;
-            s0 = __fmul_rn(s[0], inv);
-            s1 = __fmul_rn(s[1], inv);
-        } else {
+        for (int r = 0; r < R; ++r) {
+            mu[r] = mean[r];
+            rs[r] = rstd[r];
+            const uint64_t r2 = f32x2(rs[r], rs[r]);
+            uint64_t g0 = 0, g1 = 0;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < NV; ++i) add_elems<DT>(vx[i], sum);
-#pragma unroll
-            for (int k = 0; k < F / 2; ++k) g0 = fma_f32x2(d[k], w[k], g0);
-            float s[2] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])),
-                          sum_pair(g0)};
-            row_sums(s, mine[0], g);
-            mu = __fmul_rn(s[0], inv);
-            s0 = __fmul_rn(s[1], inv);
-            uint64_t q0 = 0;
-#pragma unroll
             for (int i = 0; i < NV; ++i) {
-                differences<DT>(vx[i], mu, x + i * P);
-                if (in[i]) {
+                uint4 vd, v;
+                uint64_t d[P], x[P];
+                load(r, i, vd, v);
+                unpack2<DT>(vd, d);
+                if constexpr (BITS == 0) differences<DT>(v, mu[r], x);
+                else add_elems<DT>(v, sum);
 #pragma unroll
-                    for (int k = i * P; k < i * P + P; ++k) {
-                        q0 = fma_f32x2(x[k], x[k], q0);
-                        g1 = fma_f32x2(mul_f32x2(d[k], w[k]), x[k], g1);
-                    }
+                for (int k = 0; k < P; ++k) {
+                    const uint64_t gk = mul_f32x2(d[k], w[i * P + k]);
+                    g0 = add_f32x2(g0, gk);
+                    if constexpr (BITS == 0) g1 = fma_f32x2(gk, mul_f32x2(x[k], r2), g1);
                 }
             }
-            float q[2] = {sum_pair(q0), sum_pair(g1)};
-            row_sums(q, mine[1], g);
-            r = inv_sqrt(__fmaf_rn(q[0], inv, a.eps));
-            s1 = __fmul_rn(__fmul_rn(q[1], r), inv);
-            const uint64_t r2 = f32x2(r, r);
-#pragma unroll
-            for (int k = 0; k < F / 2; ++k) x[k] = mul_f32x2(x[k], r2);
+            s[2 * r] = sum_pair(g0);
+            s[2 * r + 1] = BITS ? __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]))
+                                : sum_pair(g1);
         }
-        const uint64_t r2 = f32x2(r, r), s02 = f32x2(s0, s0), s12 = f32x2(-s1, -s1);
+        fetch();
+        ahead(t + step);
+        row_sums(s, mine[BITS ? 0 : half], g);
+        half ^= 1;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!row || !in[i]) continue;
-            uint64_t o[P];
+        for (int r = 0; r < R; ++r) {
+            s0[r] = __fmul_rn(s[2 * r], inv);
+            s1[r] = __fmul_rn(s[2 * r + 1], inv);
+        }
+        if constexpr (BITS != 0) {
+            // the statistics of the dequantized row, and sum g (x - mu)
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                const int m = i * P + k;
-                o[k] = mul_f32x2(r2, fma_f32x2(x[m], s12, sub_f32x2(mul_f32x2(d[m], w[m]), s02)));
-                dw[m] = fma_f32x2(d[m], x[m], dw[m]);
-                db[m] = add_f32x2(db[m], d[m]);
+            for (int r = 0; r < R; ++r) {
+                mu[r] = s1[r];
+                uint64_t q0 = 0, g1 = 0;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    uint4 vd, v;
+                    uint64_t d[P], x[P];
+                    load(r, i, vd, v);
+                    unpack2<DT>(vd, d);
+                    differences<DT>(v, mu[r], x);
+                    if (!in[i]) continue;
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        q0 = fma_f32x2(x[k], x[k], q0);
+                        g1 = fma_f32x2(mul_f32x2(d[k], w[i * P + k]), x[k], g1);
+                    }
+                }
+                s[2 * r] = sum_pair(q0);
+                s[2 * r + 1] = sum_pair(g1);
             }
-            *reinterpret_cast<uint4 *>(out + place<DT>(g, i) * 16) = pack2<DT>(o);
+            row_sums(s, mine[1], g);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                rs[r] = inv_sqrt(__fmaf_rn(s[2 * r], inv, a.eps));
+                s1[r] = __fmul_rn(__fmul_rn(s[2 * r + 1], rs[r]), inv);
+            }
         }
-        out += dx_step;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint64_t r2 = f32x2(rs[r], rs[r]), s02 = f32x2(s0[r], s0[r]),
+                           s12 = f32x2(-s1[r], -s1[r]);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (t + r >= a.T || !in[i]) continue;
+                uint4 vd, v;
+                uint64_t d[P], x[P], o[P];
+                load(r, i, vd, v);
+                unpack2<DT>(vd, d);
+                differences<DT>(v, mu[r], x);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    const int m = i * P + k;
+                    x[k] = mul_f32x2(x[k], r2);
+                    o[k] = mul_f32x2(r2, fma_f32x2(x[k], s12, sub_f32x2(mul_f32x2(d[k], w[m]), s02)));
+                    dw[m] = fma_f32x2(d[k], x[k], dw[m]);
+                    db[m] = add_f32x2(db[m], d[k]);
+                }
+                *reinterpret_cast<uint4 *>(out + r * dx_row + place<DT>(g, i) * 16) = pack2<DT>(o);
+            }
+        }
+        out += step * dx_row;
+        from = from == shared + (kStages - 1) * stage_bytes ? shared : from + stage_bytes;
     }
     if (!a.dw && !a.db) return;
     float *partial = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
@@ -969,16 +1033,16 @@ cudaError_t join(const LnBackward &a, int P, cudaStream_t st) {
 
 template <int DT, int BITS>
 cudaError_t backward_rows(const LnBackward &a, cudaStream_t st) {
-    constexpr int NV = 16 / Elem<DT>::kVec;
+    constexpr int NV = 16 / Elem<DT>::kVec, R = kBackRows<DT>;
     const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
     const int threads = size * groups;
-    constexpr int kSlots = (BITS ? 4 : 3) * NV * (BITS ? 1 : 2);
+    constexpr int kSlots = kBackStages * R * NV * (BITS ? 1 : 2);
     const size_t smem = (size_t)kSlots * threads * 16;
     static bool ready[kMaxDevices];
     auto kernel = ln_backward_rows_kernel<DT, BITS>;
     const cudaError_t e = allow_shared(kernel, (size_t)kSlots * 512 * 16, ready);
     if (e != cudaSuccess) return e;
-    int P = resident_ctas(kernel, threads, smem, (a.T + groups - 1) / groups);
+    int P = resident_ctas(kernel, threads, smem, (a.T + groups * R - 1) / (groups * R));
     if (P > kLnPartials) P = kLnPartials;
     const cudaError_t r = launch_pdl_clusters(kernel, P, threads, 1, smem, st, a, size);
     return r != cudaSuccess ? r : join(a, P, st);
