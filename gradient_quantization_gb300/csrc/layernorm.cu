@@ -197,50 +197,56 @@ __device__ __forceinline__ void quantize_octet(const uint4 &a, const uint4 &b, u
     if (valid && j == 0) *scale = s;
 }
 
-// Rows that start at 16-byte boundaries and hold whole vectors: a group of threads a
-// row and step, NV vectors a thread, the row in registers from its one reading to
-// its writing.  Copies into a ring of shared memory run kRing - 1 rows ahead; a thread
-// reads only what it copied, so the ring needs no barrier.  BITS: the codes of x too.
+// Rows that start at 16-byte boundaries and hold whole vectors: a group of threads R
+// rows and step (their sums share the exchanges and the barriers), NV vectors of a row a
+// thread.  Copies into a ring of shared memory run kRing - 1 steps ahead; a thread
+// reads only what it copied, so the ring needs no barrier, and the row is read from
+// there for each of its passes.  BITS: the codes of x too.
 template <int F>
 constexpr int kRing = F == 32 ? 3 : 4;       // stages (rows of 64 KB: 192 KB)
+template <int DT, int NV>
+constexpr int kRows = DT != kF32 && NV == 2 ? 2 : 1;
 
 template <int DT, int BITS, int NV, int LIMIT>
 __global__ void __launch_bounds__(LIMIT, LIMIT > 256 ? 1 : NV * Elem<DT>::kVec == 32 || BITS ? 2 : 3)
 ln_forward_rows_kernel(const LnForward a, int size) {
-    constexpr int V = Elem<DT>::kVec, F = NV * V, P = V / 2;
+    constexpr int V = Elem<DT>::kVec, F = NV * V, P = V / 2, R = kRows<DT, NV>;
     constexpr int kStages = kRing<F>;
     constexpr bool kKeep = F <= 16;      // w and b stay in registers
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ __align__(16) float red[kMaxGroups][2][kRed];
+    __shared__ __align__(16) float red[kMaxGroups][2][R * kRed];
     const Group g(size);
     const int vectors = (int)(a.H / V), groups = blockDim.x / size;
-    const int64_t step = (int64_t)gridDim.x * groups;
+    const int64_t step = (int64_t)gridDim.x * groups * R;
     const float inv = __frcp_rn((float)a.H);
-    float (*const mine)[kRed] = red[size > 32 ? g.id : 0];
-    for (int i = threadIdx.x; i < kMaxGroups * 2 * kRed; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+    float (*const mine)[R * kRed] = red[size > 32 ? g.id : 0];
+    for (int i = threadIdx.x; i < kMaxGroups * 2 * R * kRed; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
-    // slot i of stage s: shared + s * stage_bytes + i * slot_bytes
+    // slot i of row r of stage s: shared + s * stage_bytes + (r * NV + i) * slot_bytes
     const uint32_t shared = shared_address(ring + threadIdx.x);
-    const uint32_t slot_bytes = blockDim.x * 16, stage_bytes = NV * slot_bytes;
+    const uint32_t slot_bytes = blockDim.x * 16, stage_bytes = R * NV * slot_bytes;
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) in[i] = place<DT>(g, i) < vectors;
-    const int64_t first = (int64_t)blockIdx.x * groups;      // of the CTA
+    const int64_t first = (int64_t)blockIdx.x * groups * R;      // of the CTA
     pdl_wait_and_release();
-    // the next row to copy, and its pointer
-    int64_t tf = first + g.id;
-    const int64_t x_step = step * a.ldx * Elem<DT>::kSize, y_step = step * a.ldy * Elem<DT>::kSize;
+    // the next rows to copy, and their pointer
+    int64_t tf = first + g.id * R;
+    const int64_t x_row = a.ldx * Elem<DT>::kSize, y_row = a.ldy * Elem<DT>::kSize;
     const char *xf = elem_at<DT>(a.x, tf * a.ldx);
     uint32_t into = shared;
     auto fetch = [&]() {
-        if (tf < a.T) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (tf + r >= a.T) break;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (in[i]) copy16(into + i * slot_bytes, xf + place<DT>(g, i) * 16);
+                if (in[i])
+                    copy16(into + (r * NV + i) * slot_bytes, xf + r * x_row + place<DT>(g, i) * 16);
         }
         copies_commit();
         tf += step;
-        xf += x_step;
+        xf += step * x_row;
         into = into == shared + (kStages - 1) * stage_bytes ? shared : into + stage_bytes;
     };
 #pragma unroll
@@ -254,69 +260,81 @@ ln_forward_rows_kernel(const LnForward a, int size) {
         }
     }
     uint32_t from = shared;
-    char *out = elem_at<DT>(a.y, (first + g.id) * a.ldy);
+    char *out = elem_at<DT>(a.y, (first + g.id * R) * a.ldy);
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
-        const int64_t t = t0 + g.id;
-        const bool row = t < a.T;
+        const int64_t t = t0 + g.id * R;
         copies_left<kStages - 2>();
-        uint4 v[NV];
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // the row's vector i; 0 beyond its end and beyond T
+        auto load = [&](int r, int i) {
+            return t + r < a.T && in[i] ? load_shared(from + (r * NV + i) * slot_bytes)
+                                        : make_uint4(0, 0, 0, 0);
+        };
+        float s[R], mu[R], rs[R];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (row && in[i]) v[i] = load_shared(from + i * slot_bytes);
-            add_elems<DT>(v[i], sum);
+        for (int r = 0; r < R; ++r) {
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < NV; ++i) add_elems<DT>(load(r, i), sum);
+            s[r] = __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]));
         }
-        from = from == shared + (kStages - 1) * stage_bytes ? shared : from + stage_bytes;
         fetch();
-        float s[1] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]))};
         row_sums(s, mine[0], g);
-        const float mu = __fmul_rn(s[0], inv);
-        uint64_t d[F / 2], q0 = 0, q1 = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            differences<DT>(v[i], mu, d + i * P);
-            if (in[i]) {
+        for (int r = 0; r < R; ++r) {
+            mu[r] = __fmul_rn(s[r], inv);
+            uint64_t q0 = 0, q1 = 0;
 #pragma unroll
-                for (int k = i * P; k < i * P + P; k += 2) {
+            for (int i = 0; i < NV; ++i) {
+                uint64_t d[P];
+                differences<DT>(load(r, i), mu[r], d);
+                if (!in[i]) continue;
+#pragma unroll
+                for (int k = 0; k < P; k += 2) {
                     q0 = fma_f32x2(d[k], d[k], q0);
                     q1 = fma_f32x2(d[k + 1], d[k + 1], q1);
                 }
             }
+            s[r] = __fadd_rn(sum_pair(q0), sum_pair(q1));
         }
-        float q[1] = {__fadd_rn(sum_pair(q0), sum_pair(q1))};
-        row_sums(q, mine[1], g);
-        const float r = inv_sqrt(__fmaf_rn(q[0], inv, a.eps));
-        const uint64_t r2 = f32x2(r, r);
+        row_sums(s, mine[1], g);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = place<DT>(g, i);
-            uint64_t *y = d + i * P;
-            if (!row || !in[i]) continue;
-            uint64_t wj[P], bj[P];
-            if constexpr (!kKeep) {
-                load_params<DT>(a.w, a.param_f32, j, 1.0f, wj);
-                load_params<DT>(a.b, a.param_f32, j, 0.0f, bj);
+        for (int r = 0; r < R; ++r) {
+            rs[r] = inv_sqrt(__fmaf_rn(s[r], inv, a.eps));
+            const uint64_t r2 = f32x2(rs[r], rs[r]);
+            uint4 v[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int j = place<DT>(g, i);
+                v[i] = load(r, i);
+                if (t + r >= a.T || !in[i]) continue;
+                uint64_t y[P], wj[P], bj[P];
+                differences<DT>(v[i], mu[r], y);
+                if constexpr (!kKeep) {
+                    load_params<DT>(a.w, a.param_f32, j, 1.0f, wj);
+                    load_params<DT>(a.b, a.param_f32, j, 0.0f, bj);
+                }
+#pragma unroll
+                for (int k = 0; k < P; ++k)
+                    y[k] = fma_f32x2(mul_f32x2(y[k], r2), kKeep ? w[kKeep ? i * P + k : 0] : wj[k],
+                                     kKeep ? b[kKeep ? i * P + k : 0] : bj[k]);
+                *reinterpret_cast<uint4 *>(out + r * y_row + j * 16) = pack2<DT>(y);
             }
+            if constexpr (BITS != 0) {
 #pragma unroll
-            for (int k = 0; k < P; ++k)
-                y[k] = fma_f32x2(mul_f32x2(y[k], r2), kKeep ? w[kKeep ? i * P + k : 0] : wj[k],
-                                 kKeep ? b[kKeep ? i * P + k : 0] : bj[k]);
-            *reinterpret_cast<uint4 *>(out + j * 16) = pack2<DT>(y);
-        }
-        out += y_step;
-        if constexpr (BITS != 0) {
-#pragma unroll
-            for (int i = 0; i < NV; i += 2) {
-                const int64_t blk = t * (a.H / kBlock) + place<DT>(g, i) / 16;
-                quantize_octet<BITS>(v[i], v[i + 1], static_cast<uint32_t *>(a.codes) + blk * 4 * BITS,
-                                     a.scales + blk, row && in[i]);
+                for (int i = 0; i < NV; i += 2) {
+                    const int64_t blk = (t + r) * (a.H / kBlock) + place<DT>(g, i) / 16;
+                    quantize_octet<BITS>(v[i], v[i + 1],
+                                         static_cast<uint32_t *>(a.codes) + blk * 4 * BITS,
+                                         a.scales + blk, t + r < a.T && in[i]);
+                }
+            }
+            if (g.tid == 0 && t + r < a.T) {
+                if (a.mean) a.mean[t + r] = mu[r];
+                if (a.rstd) a.rstd[t + r] = rs[r];
             }
         }
-        if (g.tid == 0 && row) {
-            if (a.mean) a.mean[t] = mu;
-            if (a.rstd) a.rstd[t] = r;
-        }
+        out += step * y_row;
+        from = from == shared + (kStages - 1) * stage_bytes ? shared : from + stage_bytes;
     }
 }
 
@@ -934,7 +952,7 @@ __global__ void __launch_bounds__(kThreads) ln_backward_join_kernel(
         float *out = i < H ? dw : db;
         float s = 0.0f;
         if (i < 2 * H && out) {
-#pragma unroll 8
+#pragma unroll 19
             for (int p = warp; p < P; p += kWarps)
                 s = __fadd_rn(s, __ldg(partials + (int64_t)p * 2 * H + i));
         }
@@ -976,16 +994,17 @@ int resident_ctas(K kernel, int threads, size_t smem, int64_t units) {
 
 template <int DT, int BITS, int NV, int LIMIT>
 cudaError_t forward_rows(const LnForward &a, cudaStream_t st) {
-    constexpr int F = NV * Elem<DT>::kVec;
+    constexpr int F = NV * Elem<DT>::kVec, R = kRows<DT, NV>;
     const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
     const int threads = size * groups;
-    const size_t smem = (size_t)kRing<F> * NV * threads * 16;
+    const size_t smem = (size_t)kRing<F> * R * NV * threads * 16;
     static bool ready[kMaxDevices];
     auto kernel = ln_forward_rows_kernel<DT, BITS, NV, LIMIT>;
-    // a ring of rows of 64 KB, the longest
-    const cudaError_t e = allow_shared(kernel, (size_t)kRing<F> * (F == 32 ? 2 : 1) * 32768, ready);
+    // a ring of rows of 64 KB, the longest; with 16 elements a thread, of 4096 elements
+    const cudaError_t e =
+        allow_shared(kernel, (size_t)kRing<F> * R * (F == 32 ? 65536 : 4096 * Elem<DT>::kSize), ready);
     if (e != cudaSuccess) return e;
-    const int ctas = resident_ctas(kernel, threads, smem, (a.T + groups - 1) / groups);
+    const int ctas = resident_ctas(kernel, threads, smem, (a.T + groups * R - 1) / (groups * R));
     return launch_pdl_clusters(kernel, ctas, threads, 1, smem, st, a, size);
 }
 
