@@ -227,7 +227,13 @@ ln_forward_rows_kernel(const LnForward a, int size) {
     const uint32_t slot_bytes = blockDim.x * 16, stage_bytes = R * NV * slot_bytes;
     bool in[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) in[i] = place<DT>(g, i) < vectors;
+    for (int i = 0; i < NV; ++i) {
+        in[i] = place<DT>(g, i) < vectors;
+        if (in[i]) continue;
+        // beyond the row's end: zeros that no copy overwrites
+        for (int k = 0; k < kStages * R; ++k)
+            store_shared(shared + (k * NV + i) * slot_bytes, make_uint4(0, 0, 0, 0));
+    }
     const int64_t first = (int64_t)blockIdx.x * groups * R;      // of the CTA
     pdl_wait_and_release();
     // the next rows to copy, and their pointer
@@ -264,11 +270,11 @@ ln_forward_rows_kernel(const LnForward a, int size) {
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
         const int64_t t = t0 + g.id * R;
         copies_left<kStages - 2>();
-        // the row's vector i; 0 beyond its end and beyond T
-        auto load = [&](int r, int i) {
-            return t + r < a.T && in[i] ? load_shared(from + (r * NV + i) * slot_bytes)
-                                        : make_uint4(0, 0, 0, 0);
-        };
+        // the row's vector i (beyond T: of an earlier row; nothing of it is kept)
+        auto load = [&](int r, int i) { return load_shared(from + (r * NV + i) * slot_bytes); };
+        bool row[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) row[r] = t + r < a.T;
         float s[R], mu[R], rs[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -306,7 +312,7 @@ ln_forward_rows_kernel(const LnForward a, int size) {
             for (int i = 0; i < NV; ++i) {
                 const int j = place<DT>(g, i);
                 v[i] = load(r, i);
-                if (t + r >= a.T || !in[i]) continue;
+                if (!row[r] || !in[i]) continue;
                 uint64_t y[P], wj[P], bj[P];
                 differences<DT>(v[i], mu[r], y);
                 if constexpr (!kKeep) {
@@ -325,10 +331,10 @@ ln_forward_rows_kernel(const LnForward a, int size) {
                     const int64_t blk = (t + r) * (a.H / kBlock) + place<DT>(g, i) / 16;
                     quantize_octet<BITS>(v[i], v[i + 1],
                                          static_cast<uint32_t *>(a.codes) + blk * 4 * BITS,
-                                         a.scales + blk, t + r < a.T && in[i]);
+                                         a.scales + blk, row[r] && in[i]);
                 }
             }
-            if (g.tid == 0 && t + r < a.T) {
+            if (g.tid == 0 && row[r]) {
                 if (a.mean) a.mean[t + r] = mu[r];
                 if (a.rstd) a.rstd[t + r] = rs[r];
             }
@@ -423,35 +429,56 @@ __host__ __device__ constexpr int row_slots(int H) {
     return (H + 2 * Elem<DT>::kVec - 2) / Elem<DT>::kVec;
 }
 
-// A CTA a row and step, NE elements a thread (tid, tid + threads, ...), whatever the
-// alignment: the rows are copied and written in 16-byte vectors at the boundaries of
-// their own addresses, with shared memory in between.
-template <int DT, int NE>
+// A CTA a row and step, NV vectors a thread, whatever the alignment of x and y: the row
+// is copied in vectors at its own 16-byte boundaries and written in vectors at those of
+// y, with shared memory in between where they differ.  FIXED: all rows of x start at
+// the same place between boundaries, so a thread's weights stay the same and in registers;
+// else they come from shared memory, one array for each residue of the index modulo the
+// vector's length, which neighbouring threads read side by side.
+template <int DT, int NV, bool FIXED>
 __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) {
     using E = Elem<DT>;
     using Word = typename E::Word;
+    constexpr int V = E::kVec, P = V / 2, F = NV * V;
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ __align__(16) float red[2][kRed];
-    if (threadIdx.x < 2 * kRed) (&red[0][0])[threadIdx.x] = 0.0f;
-    if (blockDim.x == 32) red[1][threadIdx.x] = 0.0f;
     const Group g(blockDim.x);
     const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H, vectors = row_slots<DT>(H);
     const float inv = __frcp_rn((float)a.H);
     const int64_t step = gridDim.x;
+    for (int i = tid; i < 2 * kRed; i += threads) (&red[0][0])[i] = 0.0f;
     RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
     uint4 *staged = ring + kAnyStages * vectors;                  // two rows of y
+    // not FIXED: w, then b; residue r from entry 1 on, entry 0 of each is never used
+    const int stride = vectors + 1;
+    float *params = reinterpret_cast<float *>(staged + 2 * vectors);
     pdl_wait_and_release();
 #pragma unroll
     for (int s = 0; s < kAnyStages - 1; ++s) {
         x.fetch(blockIdx.x + s * step, s);
         copies_commit();
     }
-    const int held = (H - tid + threads - 1) / threads;           // elements of this thread
-    float w[NE], b[NE];
+    uint64_t w[FIXED ? F / 2 : 1], b[FIXED ? F / 2 : 1];
+    if constexpr (FIXED) {
+        const int skip = (int)(reinterpret_cast<uintptr_t>(a.x) & 15u) / E::kSize;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        w[i] = i < held ? param<DT>(a.w, a.param_f32, tid + i * threads, 1.0f) : 0.0f;
-        b[i] = i < held ? param<DT>(a.b, a.param_f32, tid + i * threads, 0.0f) : 0.0f;
+        for (int i = 0; i < F; i += 2) {
+            float f[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int e = (tid + i / V * threads) * V - skip + i % V + k;
+                const bool has = e >= 0 && e < H;
+                f[k] = has ? param<DT>(a.w, a.param_f32, e, 1.0f) : 0.0f;
+                f[2 + k] = has ? param<DT>(a.b, a.param_f32, e, 0.0f) : 0.0f;
+            }
+            w[i / 2] = f32x2(f[0], f[1]);
+            b[i / 2] = f32x2(f[2], f[3]);
+        }
+    } else {
+        for (int e = tid; e < H; e += threads) {
+            params[e % V * stride + e / V + 1] = param<DT>(a.w, a.param_f32, e, 1.0f);
+            params[(V + e % V) * stride + e / V + 1] = param<DT>(a.b, a.param_f32, e, 0.0f);
+        }
     }
     int stage = 0, half = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += step) {
@@ -460,33 +487,94 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
         __syncthreads();                                          // the row is complete
         x.fetch(t + (kAnyStages - 1) * step, stage == 0 ? kAnyStages - 1 : stage - 1);
         copies_commit();
-        const Word *row = x.row(t, stage) + tid;
+        const RowCopy<DT> row(elem_at<DT>(a.x, t * a.ldx), H);
+        const uint4 *data = ring + stage * vectors;
         stage = stage + 1 == kAnyStages ? 0 : stage + 1;
-        float f[NE], s[1] = {0.0f}, q[1] = {0.0f};
+        uint4 v[NV];
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            f[i] = i < held ? E::up(row[i * threads]) : 0.0f;
-            s[0] = __fadd_rn(s[0], f[i]);
+        for (int i = 0; i < NV; ++i) {
+            const int j = tid + i * threads;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (j < row.n) v[i] = data[j];
+            if (j < row.from || (j >= row.to && j < row.n)) {      // zeros outside the row
+                Word e[V];
+                __builtin_memcpy(e, &v[i], 16);
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (j * V - row.skip + k < 0 || j * V - row.skip + k >= H) e[k] = Word(0);
+                __builtin_memcpy(&v[i], e, 16);
+            }
+            add_elems<DT>(v[i], sum);
         }
+        float s[1] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]))};
         row_sums(s, red[0], g);
         const float mu = __fmul_rn(s[0], inv);
+        uint64_t d[F / 2], q0 = 0, q1 = 0;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            f[i] = __fsub_rn(f[i], mu);
-            if (i < held) q[0] = __fmaf_rn(f[i], f[i], q[0]);
+        for (int i = 0; i < NV; ++i) {
+            const int j = tid + i * threads;
+            uint64_t *dj = d + i * P;
+            differences<DT>(v[i], mu, dj);
+            if (j < row.from || j >= row.to) {
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    const int e = j * V - row.skip + 2 * k;
+                    dj[k] = f32x2(e >= 0 && e < H ? lo_f32(dj[k]) : 0.0f,
+                                  e + 1 >= 0 && e + 1 < H ? hi_f32(dj[k]) : 0.0f);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < P; k += 2) {
+                q0 = fma_f32x2(dj[k], dj[k], q0);
+                q1 = fma_f32x2(dj[k + 1], dj[k + 1], q1);
+            }
         }
+        float q[1] = {__fadd_rn(sum_pair(q0), sum_pair(q1))};
         row_sums(q, red[1], g);
         const float r = inv_sqrt(__fmaf_rn(q[0], inv, a.eps));
-        void *out = elem_at<DT>(a.y, t * a.ldy);
+        const uint64_t r2 = f32x2(r, r);
+        Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.y, t * a.ldy));
+        const RowCopy<DT> o(out, H);
+        uint4 *ovec = reinterpret_cast<uint4 *>(out - o.skip);
         uint4 *mine = staged + half * vectors;
-        half ^= 1;
-        Word *words = reinterpret_cast<Word *>(mine) +
-                      (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize + tid;
+        const bool level = o.skip == row.skip;
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (i < held) words[i * threads] = E::down(__fmaf_rn(__fmul_rn(f[i], r), w[i], b[i]));
+        for (int i = 0; i < NV; ++i) {
+            const int j = tid + i * threads;
+            if (j >= row.n) continue;
+            uint64_t *y = d + i * P;
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                uint64_t wk, bk;
+                if constexpr (FIXED) {
+                    wk = w[i * P + k];
+                    bk = b[i * P + k];
+                } else {
+                    const int at0 = (2 * k - row.skip) & (V - 1), at1 = (2 * k + 1 - row.skip) & (V - 1);
+                    const int j0 = j + 1 - (2 * k < row.skip), j1 = j + 1 - (2 * k + 1 < row.skip);
+                    wk = f32x2(params[at0 * stride + j0], params[at1 * stride + j1]);
+                    bk = f32x2(params[(V + at0) * stride + j0], params[(V + at1) * stride + j1]);
+                }
+                y[k] = fma_f32x2(mul_f32x2(y[k], r2), wk, bk);
+            }
+            const uint4 packed = pack2<DT>(y);
+            if (level && j >= row.from && j < row.to) ovec[j] = packed;
+            else mine[j] = packed;
+        }
         __syncthreads();
-        write_row<DT>(out, H, mine);
+        // what is not yet written: all vectors of y, each cut from two of x's, or the
+        // elements in vectors that the row fills in part
+        const Word *words = reinterpret_cast<const Word *>(mine) + row.skip;
+        if (!level) {
+            const int shift = ((row.skip - o.skip + V) & (V - 1)) * E::kSize;
+            const int back = row.skip < o.skip;
+            for (int j = o.from + tid; j < o.to; j += threads)
+                ovec[j] = bytes_from(mine[j - back], mine[j - back + 1], shift);
+        }
+        const int e = tid < 16 ? o.edge(tid) : -1;
+        if (e >= 0) out[e] = words[e];
+        half ^= 1;
         if (tid == 0) {
             if (a.mean) a.mean[t] = mu;
             if (a.rstd) a.rstd[t] = r;
@@ -630,14 +718,20 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
     float (*const mine)[2 * R * kRed] = red[size > 32 ? g.id : 0];
     for (int i = threadIdx.x; i < kMaxGroups * 4 * R * kRed; i += threads) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
-    bool in[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) in[i] = place<DT>(g, i) < vectors;
-    pdl_wait_and_release();
     // slot i of part p of row r of stage s: shared + s * stage_bytes +
     // ((r * kParts + p) * NV + i) * slot_bytes
     const uint32_t shared = shared_address(ring + threadIdx.x);
     const uint32_t slot_bytes = threads * 16, stage_bytes = R * kParts * NV * slot_bytes;
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        in[i] = place<DT>(g, i) < vectors;
+        if (in[i]) continue;
+        // beyond the row's end: zeros that no copy overwrites
+        for (int k = 0; k < kStages * R * kParts; ++k)
+            store_shared(shared + (k * NV + i) * slot_bytes, make_uint4(0, 0, 0, 0));
+    }
+    pdl_wait_and_release();
     const int64_t first = (int64_t)blockIdx.x * groups * R;      // of the CTA
     // the next rows to copy, and their pointers
     int64_t tf = first + g.id * R;
@@ -670,7 +764,10 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
     uint32_t lo[R][2], hi[R][2];
     float scale[R], mean[R], rstd[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) scale[r] = mean[r] = rstd[r] = 0.0f;
+    for (int r = 0; r < R; ++r) {
+        scale[r] = mean[r] = rstd[r] = 0.0f;
+        lo[r][0] = lo[r][1] = hi[r][0] = hi[r][1] = 0;
+    }
     auto ahead = [&](int64_t t) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -707,24 +804,21 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
         copies_left<kStages - 2>();
         float mu[R], rs[R], s0[R], s1[R];
         uint4 vx[R][NV];                  // of codes: the dequantized row
-        // the row's vector i of dy and (not of codes) x; 0 beyond its end and beyond T
+        // the row's vector i of dy and x (beyond T: of an earlier row; nothing of it is kept)
         auto load = [&](int r, int i, uint4 &d, uint4 &x) {
-            d = x = make_uint4(0, 0, 0, 0);
-            if (t + r < a.T && in[i]) {
-                d = load_shared(from + (r * kParts * NV + i) * slot_bytes);
-                if constexpr (BITS == 0) x = load_shared(from + ((r * kParts + 1) * NV + i) * slot_bytes);
-            }
-            if constexpr (BITS != 0) x = vx[r][i];
+            d = load_shared(from + (r * kParts * NV + i) * slot_bytes);
+            if constexpr (BITS == 0) x = load_shared(from + ((r * kParts + 1) * NV + i) * slot_bytes);
+            else x = vx[r][i];
         };
+        bool row[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) row[r] = t + r < a.T;
         if constexpr (BITS != 0) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    vx[r][i] = make_uint4(0, 0, 0, 0);
-                    if (t + r < a.T && in[i])
-                        vx[r][i] = dequantize_chunk<BITS>(lo[r][i & 1], hi[r][i & 1], scale[r]);
-                }
+                for (int i = 0; i < NV; ++i)
+                    vx[r][i] = dequantize_chunk<BITS>(lo[r][i & 1], hi[r][i & 1], scale[r]);
         }
         float s[2 * R];
 #pragma unroll
@@ -798,7 +892,7 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
                            s12 = f32x2(-s1[r], -s1[r]);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (t + r >= a.T || !in[i]) continue;
+                if (!row[r] || !in[i]) continue;
                 uint4 vd, v;
                 uint64_t d[P], x[P], o[P];
                 load(r, i, vd, v);
@@ -1013,21 +1107,32 @@ constexpr int kLongRow = 65536;          // bytes
 // Dynamic shared memory of the kernels for any alignment may reach this.
 constexpr size_t kMostShared = 220 * 1024;
 
-template <int DT, int NE>
+// Shared memory of ln_forward_any_kernel: five rows, and the weights.
+template <int DT>
+size_t any_shared(int64_t H, bool fixed) {
+    const size_t slots = row_slots<DT>((int)H);
+    return (kAnyStages + 2) * slots * 16 + (fixed ? 0 : 2 * Elem<DT>::kVec * (slots + 1) * 4);
+}
+
+// Vectors of a row of any alignment, 16 or 32 elements a thread of at most 512.
+template <int DT, int F>
 cudaError_t forward_any(const LnForward &a, cudaStream_t st) {
-    const int threads = (int)((a.H + 32 * NE - 1) / (32 * NE)) * 32;
-    const size_t smem = (size_t)(kAnyStages + 2) * row_slots<DT>((int)a.H) * 16;
-    static bool ready[kMaxDevices];
-    auto kernel = ln_forward_any_kernel<DT, NE>;
-    const cudaError_t e = allow_shared(kernel, kMostShared, ready);
+    constexpr int V = Elem<DT>::kVec, NV = F / V;
+    const int slots = row_slots<DT>((int)a.H);
+    const int threads = (slots + 32 * NV - 1) / (32 * NV) * 32;
+    const bool fixed = F == 16 && (a.T == 1 || a.ldx * Elem<DT>::kSize % 16 == 0);
+    const size_t smem = any_shared<DT>(a.H, fixed);
+    static bool ready[2][kMaxDevices];
+    auto kernel = fixed ? ln_forward_any_kernel<DT, NV, F == 16> : ln_forward_any_kernel<DT, NV, false>;
+    const cudaError_t e = allow_shared(kernel, kMostShared, ready[fixed]);
     if (e != cudaSuccess) return e;
     return launch_pdl_clusters(kernel, resident_ctas(kernel, threads, smem, a.T), threads, 1, smem,
                                st, a);
 }
 
 // The kernel for the rows: whole vectors, 16 elements a thread for rows of up to 4096
-// (w and b in registers too), 32 up to 64 KB; any alignment where five rows fit
-// shared memory; else element by element.
+// (w and b in registers too), 32 up to 64 KB; any alignment where five rows and
+// the weights fit shared memory; else element by element.
 template <int DT, int BITS>
 cudaError_t forward_bits(const LnForward &a, cudaStream_t st) {
     constexpr int V = Elem<DT>::kVec;
@@ -1036,9 +1141,10 @@ cudaError_t forward_bits(const LnForward &a, cudaStream_t st) {
         if (a.H <= 8192) return forward_rows<DT, BITS, 32 / V, 256>(a, st);
         if (a.H <= kLongRow / Elem<DT>::kSize) return forward_rows<DT, BITS, 32 / V, 1024>(a, st);
     }
-    if (a.H <= 512) return forward_any<DT, 4>(a, st);
-    if (a.H <= 16384 && (size_t)(kAnyStages + 2) * row_slots<DT>((int)a.H) * 16 <= kMostShared)
-        return a.H <= 8192 ? forward_any<DT, 16>(a, st) : forward_any<DT, 32>(a, st);
+    if (a.H <= 8192 - V && any_shared<DT>(a.H, false) <= kMostShared)
+        return forward_any<DT, 16>(a, st);
+    if (a.H <= 16384 - V && any_shared<DT>(a.H, false) <= kMostShared)
+        return forward_any<DT, 32>(a, st);
     return launch_pdl(ln_forward_kernel<DT>, grid_for(a.T, 8), kThreads, 0, st, a.x, a.ldx, a.w, a.b,
                       a.param_f32, a.T, a.H, a.eps, a.y, a.ldy, a.mean, a.rstd);
 }

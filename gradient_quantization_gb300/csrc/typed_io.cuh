@@ -170,13 +170,16 @@ __device__ __forceinline__ void add_elems(const uint4 &v, float (&acc)[4]) {
     }
 }
 
-// A vector's elements as binary32 pairs, and back.
+// A vector's elements as binary32 pairs, and back.  (16-bit types: an addition of -0,
+// which changes no value, in place of shifts and masks on the busier integer pipe.)
 template <int DT>
 __device__ __forceinline__ void unpack2(const uint4 &v, uint64_t *p) {
-    float f[Elem<DT>::kVec];
-    Elem<DT>::unpack(v, f);
-#pragma unroll
-    for (int i = 0; i < Elem<DT>::kVec / 2; ++i) p[i] = f32x2(f[2 * i], f[2 * i + 1]);
+    if constexpr (DT == kF32) {
+        p[0] = u32x2(v.x, v.y);
+        p[1] = u32x2(v.z, v.w);
+    } else {
+        differences<DT>(v, 0.0f, p);
+    }
 }
 template <int DT>
 __device__ __forceinline__ uint4 pack2(const uint64_t *p) {
@@ -208,6 +211,11 @@ __device__ __forceinline__ uint4 load_shared(uint32_t at) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
+}
+__device__ __forceinline__ void store_shared(uint32_t at, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
