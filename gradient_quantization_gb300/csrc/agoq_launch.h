@@ -153,11 +153,10 @@ struct LnBackward {
     float *dw, *db;
     float *workspace;        // ln_workspace_floats(T, H) floats if dw or db is wanted
 };
-constexpr int kLnPartials = 304;
-int ln_partials(int64_t T);
+int ln_partials(int64_t T, int64_t H);
 // Partial rows of dw and db.
 inline int64_t ln_workspace_floats(int64_t T, int64_t H) {
-    return (int64_t)ln_partials(T) * 2 * H;
+    return (int64_t)ln_partials(T, H) * 2 * H;
 }
 cudaError_t launch_ln_forward(const LnForward &a, cudaStream_t st);
 cudaError_t launch_ln_backward(const LnBackward &a, cudaStream_t st);

@@ -375,18 +375,6 @@ struct RowCopy {
     }
 };
 
-// Writes the row from shared memory (in the layout of RowCopy for its own address).
-template <int DT>
-__device__ __forceinline__ void write_row(void *row, int H, const uint4 *from_shared) {
-    using Word = typename Elem<DT>::Word;
-    const RowCopy<DT> r(row, H);
-    uint4 *vec = reinterpret_cast<uint4 *>(static_cast<Word *>(row) - r.skip);
-    for (int j = r.from + threadIdx.x; j < r.to; j += blockDim.x) vec[j] = from_shared[j];
-    const int e = threadIdx.x < 16 ? r.edge(threadIdx.x) : -1;
-    if (e >= 0)
-        static_cast<Word *>(row)[e] = reinterpret_cast<const Word *>(from_shared)[r.skip + e];
-}
-
 // The rows of one tensor through a ring of shared memory.  The few elements outside
 // whole vectors take a register on their way: loaded with the row's copies and stored
 // a row later, so that nothing waits for them.
@@ -429,13 +417,54 @@ __host__ __device__ constexpr int row_slots(int H) {
     return (H + 2 * Elem<DT>::kVec - 2) / Elem<DT>::kVec;
 }
 
+// A tensor's rows in the layout of RowCopy: what of it does not change from one row of
+// a CTA to the next, because the CTA's rows are a multiple of eight apart.
+template <int DT>
+struct Place {
+    int skip, from, to, n;
+    __device__ __forceinline__ Place(const void *row, int H) {
+        const RowCopy<DT> r(row, H);
+        skip = r.skip, from = r.from, to = r.to, n = r.n;
+    }
+    // Whether vector j is filled by the row in part, or not at all.
+    __device__ __forceinline__ bool part(int j) const { return j < from || j >= to; }
+    // Vector j with zeros where the row has no element.
+    __device__ __forceinline__ uint4 masked(uint4 v, int j, int H) const {
+        constexpr int V = Elem<DT>::kVec;
+        typename Elem<DT>::Word e[V];
+        __builtin_memcpy(e, &v, 16);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (j * V - skip + k < 0 || j * V - skip + k >= H) e[k] = 0;
+        __builtin_memcpy(&v, e, 16);
+        return v;
+    }
+};
+
+// Writes a row that lies in `mine` in the layout of `in` to `out`, whose boundaries lie
+// elsewhere (or, `level`, only its elements in vectors that it fills in part).
+template <int DT>
+__device__ __forceinline__ void write_any(typename Elem<DT>::Word *out, const Place<DT> &o,
+                                          const Place<DT> &in, const uint4 *mine, int H) {
+    using Word = typename Elem<DT>::Word;
+    constexpr int V = Elem<DT>::kVec;
+    if (o.skip != in.skip) {
+        uint4 *ovec = reinterpret_cast<uint4 *>(out - o.skip);
+        const int shift = ((in.skip - o.skip + V) & (V - 1)) * Elem<DT>::kSize;
+        const uint4 *from = mine - (in.skip < o.skip);
+        for (int j = o.from + threadIdx.x; j < o.to; j += blockDim.x)
+            ovec[j] = bytes_from(from[j], from[j + 1], shift);
+    }
+    const int e = threadIdx.x < 16 ? RowCopy<DT>(out, H).edge(threadIdx.x) : -1;
+    if (e >= 0) out[e] = reinterpret_cast<const Word *>(mine)[in.skip + e];
+}
+
 // A CTA a row and step, NV vectors a thread, whatever the alignment of x and y: the row
 // is copied in vectors at its own 16-byte boundaries and written in vectors at those of
-// y, with shared memory in between where they differ.  FIXED: all rows of x start at
-// the same place between boundaries, so a thread's weights stay the same and in registers;
-// else they come from shared memory, one array for each residue of the index modulo the
-// vector's length, which neighbouring threads read side by side.
-template <int DT, int NV, bool FIXED>
+// y, with shared memory in between where they differ.  The CTAs' steps are multiples of
+// eight rows, so that all rows of a CTA start at the same place between boundaries and a
+// thread's weights stay in registers.
+template <int DT, int NV>
 __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) {
     using E = Elem<DT>;
     using Word = typename E::Word;
@@ -449,36 +478,28 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
     for (int i = tid; i < 2 * kRed; i += threads) (&red[0][0])[i] = 0.0f;
     RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
     uint4 *staged = ring + kAnyStages * vectors;                  // two rows of y
-    // not FIXED: w, then b; residue r from entry 1 on, entry 0 of each is never used
-    const int stride = vectors + 1;
-    float *params = reinterpret_cast<float *>(staged + 2 * vectors);
+    Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.y, blockIdx.x * a.ldy));
+    const Place<DT> in(elem_at<DT>(a.x, blockIdx.x * a.ldx), H), o(out, H);
+    const bool level = o.skip == in.skip;
     pdl_wait_and_release();
 #pragma unroll
     for (int s = 0; s < kAnyStages - 1; ++s) {
         x.fetch(blockIdx.x + s * step, s);
         copies_commit();
     }
-    uint64_t w[FIXED ? F / 2 : 1], b[FIXED ? F / 2 : 1];
-    if constexpr (FIXED) {
-        const int skip = (int)(reinterpret_cast<uintptr_t>(a.x) & 15u) / E::kSize;
+    uint64_t w[F / 2], b[F / 2];
 #pragma unroll
-        for (int i = 0; i < F; i += 2) {
-            float f[4];
+    for (int i = 0; i < F; i += 2) {
+        float f[4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int e = (tid + i / V * threads) * V - skip + i % V + k;
-                const bool has = e >= 0 && e < H;
-                f[k] = has ? param<DT>(a.w, a.param_f32, e, 1.0f) : 0.0f;
-                f[2 + k] = has ? param<DT>(a.b, a.param_f32, e, 0.0f) : 0.0f;
-            }
-            w[i / 2] = f32x2(f[0], f[1]);
-            b[i / 2] = f32x2(f[2], f[3]);
+        for (int k = 0; k < 2; ++k) {
+            const int e = (tid + i / V * threads) * V - in.skip + i % V + k;
+            const bool has = e >= 0 && e < H;
+            f[k] = has ? param<DT>(a.w, a.param_f32, e, 1.0f) : 0.0f;
+            f[2 + k] = has ? param<DT>(a.b, a.param_f32, e, 0.0f) : 0.0f;
         }
-    } else {
-        for (int e = tid; e < H; e += threads) {
-            params[e % V * stride + e / V + 1] = param<DT>(a.w, a.param_f32, e, 1.0f);
-            params[(V + e % V) * stride + e / V + 1] = param<DT>(a.b, a.param_f32, e, 0.0f);
-        }
+        w[i / 2] = f32x2(f[0], f[1]);
+        b[i / 2] = f32x2(f[2], f[3]);
     }
     int stage = 0, half = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += step) {
@@ -487,7 +508,6 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
         __syncthreads();                                          // the row is complete
         x.fetch(t + (kAnyStages - 1) * step, stage == 0 ? kAnyStages - 1 : stage - 1);
         copies_commit();
-        const RowCopy<DT> row(elem_at<DT>(a.x, t * a.ldx), H);
         const uint4 *data = ring + stage * vectors;
         stage = stage + 1 == kAnyStages ? 0 : stage + 1;
         uint4 v[NV];
@@ -496,15 +516,8 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
         for (int i = 0; i < NV; ++i) {
             const int j = tid + i * threads;
             v[i] = make_uint4(0, 0, 0, 0);
-            if (j < row.n) v[i] = data[j];
-            if (j < row.from || (j >= row.to && j < row.n)) {      // zeros outside the row
-                Word e[V];
-                __builtin_memcpy(e, &v[i], 16);
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (j * V - row.skip + k < 0 || j * V - row.skip + k >= H) e[k] = Word(0);
-                __builtin_memcpy(&v[i], e, 16);
-            }
+            if (j < in.n) v[i] = data[j];
+            if (in.part(j)) v[i] = in.masked(v[i], j, H);
             add_elems<DT>(v[i], sum);
         }
         float s[1] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]))};
@@ -516,10 +529,10 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
             const int j = tid + i * threads;
             uint64_t *dj = d + i * P;
             differences<DT>(v[i], mu, dj);
-            if (j < row.from || j >= row.to) {
+            if (in.part(j)) {
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    const int e = j * V - row.skip + 2 * k;
+                    const int e = j * V - in.skip + 2 * k;
                     dj[k] = f32x2(e >= 0 && e < H ? lo_f32(dj[k]) : 0.0f,
                                   e + 1 >= 0 && e + 1 < H ? hi_f32(dj[k]) : 0.0f);
                 }
@@ -534,47 +547,23 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
         row_sums(q, red[1], g);
         const float r = inv_sqrt(__fmaf_rn(q[0], inv, a.eps));
         const uint64_t r2 = f32x2(r, r);
-        Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.y, t * a.ldy));
-        const RowCopy<DT> o(out, H);
-        uint4 *ovec = reinterpret_cast<uint4 *>(out - o.skip);
         uint4 *mine = staged + half * vectors;
-        const bool level = o.skip == row.skip;
+        half ^= 1;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = tid + i * threads;
-            if (j >= row.n) continue;
+            if (j >= in.n) continue;
             uint64_t *y = d + i * P;
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                uint64_t wk, bk;
-                if constexpr (FIXED) {
-                    wk = w[i * P + k];
-                    bk = b[i * P + k];
-                } else {
-                    const int at0 = (2 * k - row.skip) & (V - 1), at1 = (2 * k + 1 - row.skip) & (V - 1);
-                    const int j0 = j + 1 - (2 * k < row.skip), j1 = j + 1 - (2 * k + 1 < row.skip);
-                    wk = f32x2(params[at0 * stride + j0], params[at1 * stride + j1]);
-                    bk = f32x2(params[(V + at0) * stride + j0], params[(V + at1) * stride + j1]);
-                }
-                y[k] = fma_f32x2(mul_f32x2(y[k], r2), wk, bk);
-            }
+            for (int k = 0; k < P; ++k)
+                y[k] = fma_f32x2(mul_f32x2(y[k], r2), w[i * P + k], b[i * P + k]);
             const uint4 packed = pack2<DT>(y);
-            if (level && j >= row.from && j < row.to) ovec[j] = packed;
+            if (level && !in.part(j)) reinterpret_cast<uint4 *>(out - o.skip)[j] = packed;
             else mine[j] = packed;
         }
         __syncthreads();
-        // what is not yet written: all vectors of y, each cut from two of x's, or the
-        // elements in vectors that the row fills in part
-        const Word *words = reinterpret_cast<const Word *>(mine) + row.skip;
-        if (!level) {
-            const int shift = ((row.skip - o.skip + V) & (V - 1)) * E::kSize;
-            const int back = row.skip < o.skip;
-            for (int j = o.from + tid; j < o.to; j += threads)
-                ovec[j] = bytes_from(mine[j - back], mine[j - back + 1], shift);
-        }
-        const int e = tid < 16 ? o.edge(tid) : -1;
-        if (e >= 0) out[e] = words[e];
-        half ^= 1;
+        write_any<DT>(out, o, in, mine, H);
+        out += step * a.ldy;
         if (tid == 0) {
             if (a.mean) a.mean[t] = mu;
             if (a.rstd) a.rstd[t] = r;
@@ -940,22 +929,30 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
     }
 }
 
-// Rows of any alignment: as the forward pass, x and dy through rings, dx through
-// shared memory.
-template <int DT, int NE>
-__global__ void __launch_bounds__(512) ln_backward_any_kernel(const LnBackward a) {
+// Rows of any alignment: as the forward pass, x and dy through rings, in the layout of
+// dy (x's vectors are cut from two of its own where it lies elsewhere), dx through shared
+// memory; dw and db in registers, since a thread's columns stay the same.
+template <int DT, int LIMIT>
+__global__ void __launch_bounds__(LIMIT, LIMIT == 320 ? 2 : 1)
+ln_backward_any_kernel(const LnBackward a) {
     using E = Elem<DT>;
     using Word = typename E::Word;
+    constexpr int V = E::kVec, P = V / 2, F = 16, NV = F / V;
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ __align__(16) float red[2][2 * kRed];
-    for (int i = threadIdx.x; i < 4 * kRed; i += blockDim.x) (&red[0][0])[i] = 0.0f;
     const Group g(blockDim.x);
     const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H, vectors = row_slots<DT>(H);
     const float inv = __frcp_rn((float)a.H);
     const int64_t step = gridDim.x;
+    for (int i = tid; i < 4 * kRed; i += threads) (&red[0][0])[i] = 0.0f;
     RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
     RowRing<DT, kAnyStages> y{a.dy, a.lddy, a.T, step, H, vectors, ring + kAnyStages * vectors};
     uint4 *staged = ring + 2 * kAnyStages * vectors;              // two rows of dx
+    Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.dx, blockIdx.x * a.lddx));
+    const Place<DT> in(elem_at<DT>(a.dy, blockIdx.x * a.lddy), H),
+        ix(elem_at<DT>(a.x, blockIdx.x * a.ldx), H), o(out, H);
+    const bool level = o.skip == in.skip;
+    const int shift = ((ix.skip - in.skip + V) & (V - 1)) * E::kSize, back = ix.skip < in.skip;
     pdl_wait_and_release();
 #pragma unroll
     for (int s = 0; s < kAnyStages - 1; ++s) {
@@ -963,12 +960,17 @@ __global__ void __launch_bounds__(512) ln_backward_any_kernel(const LnBackward a
         y.fetch(blockIdx.x + s * step, s);
         copies_commit();
     }
-    const int held = (H - tid + threads - 1) / threads;           // elements of this thread
-    float w[NE], dw[NE], db[NE];
+    uint64_t w[F / 2], dw[F / 2], db[F / 2];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        w[i] = i < held ? param<DT>(a.w, a.param_f32, tid + i * threads, 1.0f) : 0.0f;
-        dw[i] = db[i] = 0.0f;
+    for (int i = 0; i < F; i += 2) {
+        float f[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int e = (tid + i / V * threads) * V - in.skip + i % V + k;
+            f[k] = e >= 0 && e < H ? param<DT>(a.w, a.param_f32, e, 1.0f) : 0.0f;
+        }
+        w[i / 2] = f32x2(f[0], f[1]);
+        dw[i / 2] = db[i / 2] = 0;
     }
     float mean = 0.0f, rstd = 0.0f;
     auto ahead = [&](int64_t t) {
@@ -990,46 +992,79 @@ __global__ void __launch_bounds__(512) ln_backward_any_kernel(const LnBackward a
         copies_commit();
         const float mu = mean, r = rstd;
         ahead(t + step);
-        const Word *rx = x.row(t, stage) + tid, *ry = y.row(t, stage) + tid;
+        const uint4 *dx = ring + stage * vectors, *dd = dx + kAnyStages * vectors;
         stage = stage + 1 == kAnyStages ? 0 : stage + 1;
-        float xh[NE], d[NE], s[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            xh[i] = d[i] = 0.0f;
-            if (i < held) {
-                xh[i] = __fmul_rn(__fsub_rn(E::up(rx[i * threads]), mu), r);
-                d[i] = E::up(ry[i * threads]);
+        const uint64_t r2 = f32x2(r, r);
+        // vector i of dy, and xh: taken from the ring for the sums and again for the results
+        auto load = [&](int i, uint64_t *d, uint64_t *xh) {
+            const int j = tid + i * threads, k = j - back;
+            uint4 vd = make_uint4(0, 0, 0, 0), vx = vd;
+            if (j < in.n) {
+                vd = dd[j];
+                // (beside the row's end one of the two may not be there: masked below)
+                if (k >= 0 && k < ix.n) vx = dx[k];
+                if (shift) {
+                    uint4 next = make_uint4(0, 0, 0, 0);
+                    if (k + 1 < ix.n) next = dx[k + 1];
+                    vx = bytes_from(vx, next, shift);
+                }
             }
-            const float gi = __fmul_rn(d[i], w[i]);
-            s[0] = __fadd_rn(s[0], gi);
-            s[1] = __fmaf_rn(gi, xh[i], s[1]);
+            if (in.part(j)) {
+                vd = in.masked(vd, j, H);
+                vx = in.masked(vx, j, H);
+            }
+            unpack2<DT>(vd, d);
+            differences<DT>(vx, mu, xh);
+#pragma unroll
+            for (int m = 0; m < P; ++m) xh[m] = mul_f32x2(xh[m], r2);
+        };
+        uint64_t g0 = 0, g1 = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            uint64_t d[P], xh[P];
+            load(i, d, xh);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const uint64_t gk = mul_f32x2(d[k], w[i * P + k]);
+                g0 = add_f32x2(g0, gk);
+                g1 = fma_f32x2(gk, xh[k], g1);
+            }
         }
+        float s[2] = {sum_pair(g0), sum_pair(g1)};
         row_sums(s, red[half], g);
         const float s0 = __fmul_rn(s[0], inv), s1 = __fmul_rn(s[1], inv);
-        void *out = elem_at<DT>(a.dx, t * a.lddx);
+        const uint64_t s02 = f32x2(s0, s0), s12 = f32x2(-s1, -s1);
         uint4 *mine = staged + half * vectors;
         half ^= 1;
-        Word *words = reinterpret_cast<Word *>(mine) +
-                      (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize + tid;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            if (i < held)
-                words[i * threads] = E::down(
-                    __fmul_rn(r, __fmaf_rn(-xh[i], s1, __fsub_rn(__fmul_rn(d[i], w[i]), s0))));
-            dw[i] = __fmaf_rn(d[i], xh[i], dw[i]);
-            db[i] = __fadd_rn(db[i], d[i]);
+        for (int i = 0; i < NV; ++i) {
+            const int j = tid + i * threads;
+            if (j >= in.n) continue;
+            uint64_t d[P], xh[P], p[P];
+            load(i, d, xh);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const int m = i * P + k;
+                p[k] = mul_f32x2(r2, fma_f32x2(xh[k], s12, sub_f32x2(mul_f32x2(d[k], w[m]), s02)));
+                dw[m] = fma_f32x2(d[k], xh[k], dw[m]);
+                db[m] = add_f32x2(db[m], d[k]);
+            }
+            const uint4 packed = pack2<DT>(p);
+            if (level && !in.part(j)) reinterpret_cast<uint4 *>(out - o.skip)[j] = packed;
+            else mine[j] = packed;
         }
         __syncthreads();
-        write_row<DT>(out, H, mine);
+        write_any<DT>(out, o, in, mine, H);
+        out += step * a.lddx;
     }
     if (!a.dw && !a.db) return;
     float *partial = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = tid + i * threads;
-        if (e >= H) break;
-        partial[e] = dw[i];
-        partial[a.H + e] = db[i];
+    for (int i = 0; i < F; ++i) {
+        const int e = (tid + i / V * threads) * V - in.skip + i % V;
+        if (e < 0 || e >= H) continue;
+        partial[e] = i & 1 ? hi_f32(dw[i / 2]) : lo_f32(dw[i / 2]);
+        partial[a.H + e] = i & 1 ? hi_f32(db[i / 2]) : lo_f32(db[i / 2]);
     }
 }
 
@@ -1107,32 +1142,34 @@ constexpr int kLongRow = 65536;          // bytes
 // Dynamic shared memory of the kernels for any alignment may reach this.
 constexpr size_t kMostShared = 220 * 1024;
 
-// Shared memory of ln_forward_any_kernel: five rows, and the weights.
-template <int DT>
-size_t any_shared(int64_t H, bool fixed) {
-    const size_t slots = row_slots<DT>((int)H);
-    return (kAnyStages + 2) * slots * 16 + (fixed ? 0 : 2 * Elem<DT>::kVec * (slots + 1) * 4);
+// CTAs of the kernels for any alignment: a multiple of eight where one takes several
+// rows, so that its rows start at the same place between 16-byte boundaries.
+template <typename K>
+int any_ctas(K kernel, int threads, size_t smem, int64_t T, int most) {
+    int n = resident_ctas(kernel, threads, smem, T);
+    if (n > most) n = most;
+    return n >= T ? n : n > 8 ? n / 8 * 8 : 8;
 }
 
-// Vectors of a row of any alignment, 16 or 32 elements a thread of at most 512.
-template <int DT, int F>
+// Rows of any alignment, 32 elements a thread (few warps a row: with 16 elements rows of
+// 5003 FP16 values took 51 us, with 32 38 us).
+template <int DT>
 cudaError_t forward_any(const LnForward &a, cudaStream_t st) {
-    constexpr int V = Elem<DT>::kVec, NV = F / V;
+    constexpr int NV = 32 / Elem<DT>::kVec;
     const int slots = row_slots<DT>((int)a.H);
     const int threads = (slots + 32 * NV - 1) / (32 * NV) * 32;
-    const bool fixed = F == 16 && (a.T == 1 || a.ldx * Elem<DT>::kSize % 16 == 0);
-    const size_t smem = any_shared<DT>(a.H, fixed);
-    static bool ready[2][kMaxDevices];
-    auto kernel = fixed ? ln_forward_any_kernel<DT, NV, F == 16> : ln_forward_any_kernel<DT, NV, false>;
-    const cudaError_t e = allow_shared(kernel, kMostShared, ready[fixed]);
+    const size_t smem = (size_t)(kAnyStages + 2) * slots * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_forward_any_kernel<DT, NV>;
+    const cudaError_t e = allow_shared(kernel, kMostShared, ready);
     if (e != cudaSuccess) return e;
-    return launch_pdl_clusters(kernel, resident_ctas(kernel, threads, smem, a.T), threads, 1, smem,
-                               st, a);
+    return launch_pdl_clusters(kernel, any_ctas(kernel, threads, smem, a.T, 1 << 20), threads, 1,
+                               smem, st, a);
 }
 
 // The kernel for the rows: whole vectors, 16 elements a thread for rows of up to 4096
-// (w and b in registers too), 32 up to 64 KB; any alignment where five rows and
-// the weights fit shared memory; else element by element.
+// (w and b in registers too), 32 up to 64 KB; any alignment where five rows fit
+// shared memory; else element by element.
 template <int DT, int BITS>
 cudaError_t forward_bits(const LnForward &a, cudaStream_t st) {
     constexpr int V = Elem<DT>::kVec;
@@ -1141,10 +1178,8 @@ cudaError_t forward_bits(const LnForward &a, cudaStream_t st) {
         if (a.H <= 8192) return forward_rows<DT, BITS, 32 / V, 256>(a, st);
         if (a.H <= kLongRow / Elem<DT>::kSize) return forward_rows<DT, BITS, 32 / V, 1024>(a, st);
     }
-    if (a.H <= 8192 - V && any_shared<DT>(a.H, false) <= kMostShared)
-        return forward_any<DT, 16>(a, st);
-    if (a.H <= 16384 - V && any_shared<DT>(a.H, false) <= kMostShared)
-        return forward_any<DT, 32>(a, st);
+    if (a.H <= 16384 - V && (size_t)(kAnyStages + 2) * row_slots<DT>((int)a.H) * 16 <= kMostShared)
+        return forward_any<DT>(a, st);
     return launch_pdl(ln_forward_kernel<DT>, grid_for(a.T, 8), kThreads, 0, st, a.x, a.ldx, a.w, a.b,
                       a.param_f32, a.T, a.H, a.eps, a.y, a.ldy, a.mean, a.rstd);
 }
@@ -1168,21 +1203,22 @@ cudaError_t backward_rows(const LnBackward &a, cudaStream_t st) {
     const cudaError_t e = allow_shared(kernel, (size_t)kSlots * 512 * 16, ready);
     if (e != cudaSuccess) return e;
     int P = resident_ctas(kernel, threads, smem, (a.T + groups * R - 1) / (groups * R));
-    if (P > kLnPartials) P = kLnPartials;
+    if (P > ln_partials(a.T, a.H)) P = ln_partials(a.T, a.H);
     const cudaError_t r = launch_pdl_clusters(kernel, P, threads, 1, smem, st, a, size);
     return r != cudaSuccess ? r : join(a, P, st);
 }
 
-template <int DT, int NE>
+template <int DT, int LIMIT>
 cudaError_t backward_any(const LnBackward &a, cudaStream_t st) {
-    const int threads = (int)((a.H + 32 * NE - 1) / (32 * NE)) * 32;
-    const size_t smem = (size_t)(2 * kAnyStages + 2) * row_slots<DT>((int)a.H) * 16;
+    constexpr int NV = 16 / Elem<DT>::kVec;
+    const int slots = row_slots<DT>((int)a.H);
+    const int threads = (slots + 32 * NV - 1) / (32 * NV) * 32;
+    const size_t smem = (size_t)(2 * kAnyStages + 2) * slots * 16;
     static bool ready[kMaxDevices];
-    auto kernel = ln_backward_any_kernel<DT, NE>;
+    auto kernel = ln_backward_any_kernel<DT, LIMIT>;
     const cudaError_t e = allow_shared(kernel, kMostShared, ready);
     if (e != cudaSuccess) return e;
-    int P = resident_ctas(kernel, threads, smem, a.T);
-    if (P > kLnPartials) P = kLnPartials;
+    const int P = any_ctas(kernel, threads, smem, a.T, ln_partials(a.T, a.H));
     const cudaError_t r = launch_pdl_clusters(kernel, P, threads, 1, smem, st, a);
     return r != cudaSuccess ? r : join(a, P, st);
 }
@@ -1197,12 +1233,12 @@ cudaError_t backward(const Input<DT, BITS> &in, const LnBackward &a, cudaStream_
         a.H % V == 0 && a.H <= 8192)
         return backward_rows<DT, BITS>(a, st);
     if constexpr (BITS == 0) {
-        if (a.H <= 512) return backward_any<DT, 4>(a, st);
-        if (a.H <= 8192 && (size_t)(2 * kAnyStages + 2) * row_slots<DT>((int)a.H) * 16 <= kMostShared)
-            return backward_any<DT, 16>(a, st);
+        // (rows of up to 5112 leave registers for two CTAs an SM)
+        if (a.H <= 8192 - V && (size_t)(2 * kAnyStages + 2) * row_slots<DT>((int)a.H) * 16 <= kMostShared)
+            return a.H <= 5120 - V ? backward_any<DT, 320>(a, st) : backward_any<DT, 512>(a, st);
     }
     const bool sums = a.dw || a.db;
-    const int P = sums ? ln_partials(a.T) : grid_for(a.T, 8);
+    const int P = sums ? ln_partials(a.T, a.H) : grid_for(a.T, 8);
     const cudaError_t e = launch_pdl(ln_backward_kernel<DT, BITS>, P, kThreads, 0, st, in, a.dy,
                                      a.lddy, a.w, a.param_f32, a.mean, a.rstd, a.T, a.H, a.eps,
                                      a.dx, a.lddx, sums ? a.workspace : nullptr);
@@ -1218,8 +1254,12 @@ cudaError_t codes(const LnForward &a, cudaStream_t st) {
 
 }  // namespace
 
-// Rows of partial sums of dw and db: at most kLnPartials.
-int ln_partials(int64_t T) { return (int)(T < kLnPartials ? T : kLnPartials); }
+// Rows of partial sums of dw and db: at most two an SM of 152, and more of short rows,
+// whose CTAs are small (as many bytes as 304 rows of 4096 elements).
+int ln_partials(int64_t T, int64_t H) {
+    const int64_t fit = H < 4096 ? 4096 / H : 1, most = 304 * (fit < 8 ? fit : 8);
+    return (int)(T < most ? T : most);
+}
 
 cudaError_t launch_ln_forward(const LnForward &a, cudaStream_t st) {
     if (a.dtype == kF32) return forward_bits<kF32, 0>(a, st);

@@ -392,8 +392,8 @@ agoq_status agoq_layernorm_forward(const void *x, int64_t ldx, const void *w, co
 
 /*
  * Bytes of scratch the layer norm's backward calls need for dw or db of a [T][H]
- * input (partial rows of both, at most 304: the same for every T beyond that), -1
- * for sizes they do not take.
+ * input (partial rows of both: 304 of them, up to eight times as many for H < 4096,
+ * and no more than T), -1 for sizes they do not take.
  */
 int64_t agoq_layernorm_backward_workspace_bytes(int64_t T, int64_t H);
 
