@@ -462,6 +462,14 @@ def _vector(t, n, what, dtypes):
 _F32 = (torch.float32,)
 
 
+def _out(t, n, other, shape, dtype, device, what):
+    """(tensor, address) of an output: the caller's `t` of n values, or a new one."""
+    if t is None:
+        t = _new(other, shape, dtype, device)
+        return t, t.data_ptr()
+    return t, _vector(t, n, what, (dtype,))
+
+
 def _params(x_dtype, H, w, b=None):
     """(w, b, param_dtype): weight and bias of one type, FP32 or the activation's."""
     kinds = (torch.float32, x_dtype)
@@ -487,22 +495,22 @@ def agoq_layernorm_forward(x, w=None, b=None, eps=1e-5, bits=0, y=None, mean=Non
         yp, ldy = y.data_ptr(), H
     else:
         yp, _, _, ldy = _rows(y, "y", H, T, x.dtype)
-    if mean is None and want_stats:
-        mean = _new(other, T, torch.float32, dev)
-    if rstd is None and want_stats:
-        rstd = _new(other, T, torch.float32, dev)
+    mp = rp = cp = sp = 0
+    if mean is not None or want_stats:
+        mean, mp = _out(mean, T, other, T, torch.float32, dev, "mean")
+    if rstd is not None or want_stats:
+        rstd, rp = _out(rstd, T, other, T, torch.float32, dev, "rstd")
     if bits:
-        if codes is None:
-            codes = _new(other, T * H // BLOCK * record_bytes(bits), torch.uint8, dev)
-        if scales is None:
-            scales = _new(other, T * H // BLOCK, torch.float32, dev)
+        n = T * H // BLOCK
+        m = n * record_bytes(bits)
+        codes, cp = _out(codes, m, other, m, torch.uint8, dev, "codes")
+        scales, sp = _out(scales, n, other, n, torch.float32, dev, "scales")
     else:
         codes = scales = None
-    cp = _vector(codes, T * H // BLOCK * record_bytes(bits), "codes", (torch.uint8,))
-    sp = _vector(scales, T * H // BLOCK, "scales", _F32)
-    _check(lib().agoq_layernorm_forward(
-        xp, ldx, wp, bp, pd, T, H, DTYPES[x.dtype], eps, yp, ldy, _vector(mean, T, "mean", _F32),
-        _vector(rstd, T, "rstd", _F32), cp, sp, bits, handle), "agoq_layernorm_forward")
+    rc = lib().agoq_layernorm_forward(xp, ldx, wp, bp, pd, T, H, DTYPES[x.dtype], eps, yp, ldy,
+                                      mp, rp, cp, sp, bits, handle)
+    if rc:
+        raise AgoqError(rc, "agoq_layernorm_forward")
     return y, mean, rstd, codes, scales
 
 
@@ -655,21 +663,20 @@ def agoq_token_logprobs(logits, tokens, k=0, want_entropy=True, logp=None, entro
     xp, T, V, ld = _rows(logits, "logits")
     dev = logits.device
     handle, other = _launch(stream, dev)
-    if logp is None:
-        logp = _new(other, T, torch.float32, dev)
-    if entropy is None and want_entropy:
-        entropy = _new(other, T, torch.float32, dev)
-    if lse is None:
-        lse = _new(other, T, torch.float32, dev)
-    if k > 0 and top_logp is None:
-        top_logp = _new(other, (T, k), torch.float32, dev)
-    if k > 0 and top_ids is None:
-        top_ids = _new(other, (T, k), torch.int64, dev)
-    _check(lib().agoq_token_logprobs(
-        xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64), T, V, k,
-        _vector(logp, T, "logp", _F32), _vector(entropy, T, "entropy", _F32),
-        _vector(lse, T, "lse", _F32), _vector(top_logp, T * k, "top_logp", _F32),
-        _vector(top_ids, T * k, "top_ids", _I64), handle), "agoq_token_logprobs")
+    f32 = torch.float32
+    logp, pp = _out(logp, T, other, T, f32, dev, "logp")
+    lse, lp = _out(lse, T, other, T, f32, dev, "lse")
+    ep = tp = ip = 0
+    if entropy is not None or want_entropy:
+        entropy, ep = _out(entropy, T, other, T, f32, dev, "entropy")
+    if k > 0:
+        top_logp, tp = _out(top_logp, T * k, other, (T, k), f32, dev, "top_logp")
+        top_ids, ip = _out(top_ids, T * k, other, (T, k), torch.int64, dev, "top_ids")
+    rc = lib().agoq_token_logprobs(xp, ld, DTYPES[logits.dtype],
+                                   _vector(tokens, T, "tokens", _I64), T, V, k, pp, ep, lp, tp, ip,
+                                   handle)
+    if rc:
+        raise AgoqError(rc, "agoq_token_logprobs")
     return logp, entropy, lse, top_logp, top_ids
 
 

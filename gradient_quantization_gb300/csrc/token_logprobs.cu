@@ -278,7 +278,8 @@ constexpr int kStages = 3;                    // of shared memory, each thread's
 constexpr int kStep = kBatch * kStatThreads;
 constexpr int kGroups = 64, kGroupLanes = kStatThreads / kGroups;
 constexpr int kTopMax = 32;
-constexpr int kList = 512, kShortList = 256;
+constexpr int kWarpList = 128;                // candidate vectors of a warp
+constexpr int kList = kWarpList * kStatWarps, kShortList = 256;
 constexpr int kMaxCluster = 8;
 static_assert(kTopMax <= kGroups && kMaxCluster * kTopMax <= kShortList && 3 * kShortList <= 2 * kList,
               "lists hold what they must");
@@ -289,16 +290,17 @@ struct StatShared {
     Sums slice;                   // of the CTA's slice
     float bound;
     float token;                  // the token's logit, in the CTA that holds it
-    int count;                    // candidate vectors (may exceed kList)
+    int found[kStatWarps];        // candidate vectors (may exceed kWarpList)
+    int count;                    // entries of a list
     int above, equal;             // entries of the shorter lists
     unsigned long long best;
     unsigned long long top[kTopMax];
-    // Candidate vectors and their first elements' indices; later lists of keys.
+    // Candidate vectors, by warp, and their first elements' indices; later lists of keys.
     union {
-        uint4 vec[kList];
+        uint4 vec[kStatWarps][kWarpList];
         unsigned long long list[2 * kList];
     };
-    int element[kList];
+    int element[kStatWarps][kWarpList];
     unsigned long long few[kShortList];
     uint4 ring[kStages][kBatch][kStatThreads];
 };
@@ -511,20 +513,24 @@ __global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const Toke
         const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), (int)a.V, C, rank);
         const int64_t token = a.tokens[t];
         if (threadIdx.x == 0) {
-            sh.count = sh.above = 0;
+            sh.above = 0;
             if (s.has(token)) sh.token = Elem<DT>::up(s.row[token]);
         }
         if (threadIdx.x < kTopMax) sh.top[threadIdx.x] = 0;
-        if (want) __syncthreads();                    // before the first candidate
         Online<DT, true> sums;
         uint32_t most = kNegInfWord<DT>;
         float bound = kLowest;                        // -inf is no candidate
-        auto candidate = [&](const uint4 &v, int j) {
-            const int at = atomicAdd(&sh.count, 1);
-            if (at < kList) {
-                sh.vec[at] = v;
-                sh.element[at] = s.at(j);
+        // The vectors of the lanes that call with `yes` join the warp's list, in the order
+        // of the lanes; all lanes call.
+        int found = 0;
+        auto candidates = [&](bool yes, const uint4 &v, int j) {
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, yes);
+            const int at = found + __popc(who & ((1u << lane) - 1u));
+            if (yes && at < kWarpList) {
+                sh.vec[warp][at] = v;
+                sh.element[warp][at] = s.at(j);
             }
+            found += __popc(who);
         };
         for (int j0 = s.from, b = 0; j0 < s.to; j0 += kStep, ++b) {
             const int j = j0 + threadIdx.x;
@@ -556,10 +562,10 @@ __global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const Toke
             }
             most = max_word<DT>(most, all);
             if (vm > sums.limit) sums.raise(vm);
-            if (want && vm >= bound) {
+            if (want && __any_sync(0xFFFFFFFFu, vm >= bound)) {
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
-                    if (word_max<DT>(w[i]) >= bound) candidate(cur[i], j + i * kStatThreads);
+                    candidates(word_max<DT>(w[i]) >= bound, cur[i], j + i * kStatThreads);
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) sums.add(cur[i]);
@@ -567,12 +573,18 @@ __global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const Toke
         // the vectors filled in part
         const int edge = threadIdx.x == 0 && s.from > 0 ? 0
                          : threadIdx.x == 32 && s.to < s.n ? s.to : -1;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        float vm = -INFINITY;
         if (edge >= 0) {
-            const uint4 v = s.part(edge);
+            v = s.part(edge);
             const uint32_t wv = vec_max<DT>(v);
             most = max_word<DT>(most, wv);
-            sums.add(v, word_max<DT>(wv));
-            if (want && word_max<DT>(wv) >= bound) candidate(v, edge);
+            vm = word_max<DT>(wv);
+            sums.add(v, vm);
+        }
+        if (want) {
+            candidates(vm >= bound, v, edge);
+            if (lane == 0) sh.found[warp] = found;
         }
         const Sums mine = warp_join(sums.sums());
         if (lane == 0) sh.warps[warp] = mine;
@@ -580,22 +592,26 @@ __global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const Toke
         else __syncthreads();
         Sums all = warp_join(lane < kStatWarps ? sh.warps[lane] : Sums{kLowest, 0.0f, 0.0f});
         if (want) {
-            const int count = sh.count;
             const float full = sh.bound;
             const bool nan = all.sum != all.sum;
-            if (count > kList || nan) {
+            bool over = false;
+#pragma unroll
+            for (int i = 0; i < kStatWarps; ++i) over |= sh.found[i] > kWarpList;
+            if (over || nan) {
                 read_again<DT>(s, want, nan, sh);
             } else {
                 // their elements that reach it, usually few
                 const float least = fmaxf(full, kLowest);
-                for (int i = threadIdx.x; i < count; i += kStatThreads) {
+                for (int i = lane; i < found; i += 32) {
+                    const uint4 v = sh.vec[warp][i];
+                    if (!(word_max<DT>(vec_max<DT>(v)) >= least)) continue;
                     float f[N];
-                    Elem<DT>::unpack(sh.vec[i], f);
+                    Elem<DT>::unpack(v, f);
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
                         if (!(f[k] >= least)) continue;
                         const int at = atomicAdd(&sh.above, 1);
-                        if (at < kShortList) sh.few[at] = order_key(f[k], sh.element[i] + k);
+                        if (at < kShortList) sh.few[at] = order_key(f[k], sh.element[warp][i] + k);
                     }
                 }
                 __syncthreads();
