@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) ln_forward_kernel(
 // Threads that share a row: the CTA, or for short rows one of several groups in it
 // (8, 16 or 32 lanes, or whole warps with a barrier of their own), each with rows of
 // its own.
-constexpr int kMaxGroups = 4;                 // of more than one warp, in a CTA
+constexpr int kMaxGroups = 8;                 // of more than one warp, in a CTA
 struct Group {
     int size, id, tid;            // threads; which of the CTA's groups; thread in the group
     __device__ __forceinline__ explicit Group(int size_)
@@ -911,7 +911,7 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = place<DT>(g, i);
-            if (j >= vectors) continue;
+            if (!in[i]) continue;
             float *pw = (groups > 1 ? joined : partial) + j * V, *pb = pw + a.H;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
@@ -1194,7 +1194,9 @@ cudaError_t join(const LnBackward &a, int P, cudaStream_t st) {
 template <int DT, int BITS>
 cudaError_t backward_rows(const LnBackward &a, cudaStream_t st) {
     constexpr int NV = 16 / Elem<DT>::kVec, R = kBackRows<DT>;
-    const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
+    // rows of more than 128 threads pair up in a CTA, for half as many partial sums
+    const int size = threads_for(a.H / Elem<DT>::kVec, NV);
+    const int groups = size > 128 && size <= 256 ? 2 : groups_of(size);
     const int threads = size * groups;
     constexpr int kSlots = kBackStages * R * NV * (BITS ? 1 : 2);
     const size_t smem = (size_t)kSlots * threads * 16;
