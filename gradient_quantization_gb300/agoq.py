@@ -520,17 +520,22 @@ def agoq_layernorm_backward_workspace_bytes(T, H):
 
 
 def _norm_sums(other, T, H, dev, dw, db, want_dw, want_db, workspace):
-    if dw is None and want_dw:
-        dw = _new(other, H, torch.float32, dev)
-    if db is None and want_db:
-        db = _new(other, H, torch.float32, dev)
-    if workspace is None and (dw is not None or db is not None):
-        workspace = _new(other, agoq_layernorm_backward_workspace_bytes(T, H), torch.uint8, dev)
+    """(dw, db, workspace) and the addresses and size that the backward calls take."""
+    wp = bp = 0
+    if dw is not None or want_dw:
+        dw, wp = _out(dw, H, other, H, torch.float32, dev, "dw")
+    if db is not None or want_db:
+        db, bp = _out(db, H, other, H, torch.float32, dev, "db")
     if workspace is None:
-        return dw, db, None, 0, 0
+        if not wp and not bp:
+            return dw, db, None, 0, 0, 0, 0
+        n = lib().agoq_layernorm_backward_workspace_bytes(T, H)
+        workspace = _new(other, max(n, 0), torch.uint8, dev)
+        return dw, db, workspace, wp, bp, workspace.data_ptr(), n
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    return dw, db, workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return (dw, db, workspace, wp, bp, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
 
 
 def agoq_layernorm_backward(x, dy, mean, rstd, w=None, dx=None, dw=None, db=None, want_dw=True,
@@ -544,13 +549,17 @@ def agoq_layernorm_backward(x, dy, mean, rstd, w=None, dx=None, dw=None, db=None
     handle, other = _launch(stream, dev)
     if dx is None:
         dx = _new(other, dy.shape, dy.dtype, dev)
-    dxp, _, _, lddx = _rows(dx, "dx", H, T, x.dtype)
-    dw, db, workspace, ws, nws = _norm_sums(other, T, H, dev, dw, db, want_dw, want_db, workspace)
-    _check(lib().agoq_layernorm_backward(
+        dxp, lddx = dx.data_ptr(), H
+    else:
+        dxp, _, _, lddx = _rows(dx, "dx", H, T, x.dtype)
+    dw, db, workspace, dwp, dbp, ws, nws = _norm_sums(other, T, H, dev, dw, db, want_dw, want_db,
+                                                      workspace)
+    rc = lib().agoq_layernorm_backward(
         xp, ldx, dyp, lddy, wp, pd, _vector(mean, T, "mean", _F32),
-        _vector(rstd, T, "rstd", _F32), T, H, DTYPES[x.dtype], dxp, lddx,
-        _vector(dw, H, "dw", _F32), _vector(db, H, "db", _F32), ws, nws, handle),
-        "agoq_layernorm_backward")
+        _vector(rstd, T, "rstd", _F32), T, H, DTYPES[x.dtype], dxp, lddx, dwp, dbp, ws, nws,
+        handle)
+    if rc:
+        raise AgoqError(rc, "agoq_layernorm_backward")
     return dx, dw, db
 
 
@@ -564,14 +573,18 @@ def agoq_layernorm_backward_laaq(codes, scales, bits, dy, eps=1e-5, w=None, dx=N
     handle, other = _launch(stream, dev)
     if dx is None:
         dx = _new(other, dy.shape, dy.dtype, dev)
-    dxp, _, _, lddx = _rows(dx, "dx", H, T, dy.dtype)
-    dw, db, workspace, ws, nws = _norm_sums(other, T, H, dev, dw, db, want_dw, want_db, workspace)
+        dxp, lddx = dx.data_ptr(), H
+    else:
+        dxp, _, _, lddx = _rows(dx, "dx", H, T, dy.dtype)
+    dw, db, workspace, dwp, dbp, ws, nws = _norm_sums(other, T, H, dev, dw, db, want_dw, want_db,
+                                                      workspace)
     blocks = T * H // BLOCK
-    _check(lib().agoq_layernorm_backward_laaq(
+    rc = lib().agoq_layernorm_backward_laaq(
         _vector(codes, blocks * record_bytes(bits), "codes", (torch.uint8,)),
         _vector(scales, blocks, "scales", _F32), bits, dyp, lddy, wp, pd, T, H, eps, dxp, lddx,
-        _vector(dw, H, "dw", _F32), _vector(db, H, "db", _F32), ws, nws, handle),
-        "agoq_layernorm_backward_laaq")
+        dwp, dbp, ws, nws, handle)
+    if rc:
+        raise AgoqError(rc, "agoq_layernorm_backward_laaq")
     return dx, dw, db
 
 
@@ -688,12 +701,15 @@ def agoq_token_logprobs_backward(logits, tokens, lse, dlogp, entropy=None, dentr
     handle, other = _launch(stream, logits.device)
     if dlogits is None:
         dlogits = _new(other, logits.shape, logits.dtype, logits.device)
-    dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
-    _check(lib().agoq_token_logprobs_backward(
+        dp, ldd = dlogits.data_ptr(), V
+    else:
+        dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
+    rc = lib().agoq_token_logprobs_backward(
         xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64), T, V,
         _vector(lse, T, "lse", _F32), _vector(entropy, T, "entropy", _F32),
-        _vector(dlogp, T, "dlogp", _F32), _vector(dentropy, T, "dentropy", _F32), dp, ldd,
-        handle), "agoq_token_logprobs_backward")
+        _vector(dlogp, T, "dlogp", _F32), _vector(dentropy, T, "dentropy", _F32), dp, ldd, handle)
+    if rc:
+        raise AgoqError(rc, "agoq_token_logprobs_backward")
     return dlogits
 
 
@@ -703,15 +719,16 @@ def agoq_token_loss(logits, tokens, weights=None, logp=None, dlogits=None, strea
     xp, T, V, ld = _rows(logits, "logits")
     dev = logits.device
     handle, other = _launch(stream, dev)
-    if logp is None:
-        logp = _new(other, T, torch.float32, dev)
+    logp, pp = _out(logp, T, other, T, torch.float32, dev, "logp")
     if dlogits is None:
         dlogits = _new(other, logits.shape, logits.dtype, dev)
-    dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
-    _check(lib().agoq_token_loss(
-        xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64),
-        _vector(weights, T, "weights", _F32), T, V, _vector(logp, T, "logp", _F32), dp, ldd,
-        handle), "agoq_token_loss")
+        dp, ldd = dlogits.data_ptr(), V
+    else:
+        dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
+    rc = lib().agoq_token_loss(xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64),
+                               _vector(weights, T, "weights", _F32), T, V, pp, dp, ldd, handle)
+    if rc:
+        raise AgoqError(rc, "agoq_token_loss")
     return logp, dlogits
 
 

@@ -905,9 +905,18 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
     float *partial = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
     float *joined = reinterpret_cast<float *>(ring);          // [2][H], for several groups
     copies_left<0>();
-    for (int who = 0; who < groups; ++who) {
+    // groups of a warp first, then one after another
+    for (int o = size; o < 32; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < F / 2; ++i) {
+            dw[i] = add_f32x2(dw[i], __shfl_xor_sync(0xFFFFFFFFu, dw[i], o));
+            db[i] = add_f32x2(db[i], __shfl_xor_sync(0xFFFFFFFFu, db[i], o));
+        }
+    }
+    const int parts = threads / max(size, 32), part = threadIdx.x / max(size, 32);
+    for (int who = 0; who < parts; ++who) {
         if (groups > 1) __syncthreads();
-        if (g.id != who) continue;
+        if (part != who || (size < 32 && (threadIdx.x & 31) >= size)) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = place<DT>(g, i);
@@ -1194,9 +1203,11 @@ cudaError_t join(const LnBackward &a, int P, cudaStream_t st) {
 template <int DT, int BITS>
 cudaError_t backward_rows(const LnBackward &a, cudaStream_t st) {
     constexpr int NV = 16 / Elem<DT>::kVec, R = kBackRows<DT>;
-    // rows of more than 128 threads pair up in a CTA, for half as many partial sums
+    // Rows of more than 128 threads pair up in a CTA, for half as many partial sums (8192 x
+    // 4096: 42 us, 46 us alone), and CTAs of rows of less than a warp are as large
+    // (262144 x 128: 52 us, 64 us with 256 threads; 32768 x 1024: 47 us, 42 us with 256).
     const int size = threads_for(a.H / Elem<DT>::kVec, NV);
-    const int groups = size > 128 && size <= 256 ? 2 : groups_of(size);
+    const int groups = size > 256 ? 1 : (size > 128 || size < 32 ? 512 : 256) / size;
     const int threads = size * groups;
     constexpr int kSlots = kBackStages * R * NV * (BITS ? 1 : 2);
     const size_t smem = (size_t)kSlots * threads * 16;
