@@ -102,46 +102,24 @@ __device__ __forceinline__ int tensor_of(const List<N> &l, int chunk, int t) {
     return lo;
 }
 
-// Sum of the squares of a vector's elements, added to acc.
-template <int DT>
-__device__ __forceinline__ void add_squares(const uint4 &v, float scale, float (&acc)[4]) {
+// Add the squares of sixteen E4M3 codes, times that of their block's scale: the sum of
+// the codes' squares first.
+__device__ __forceinline__ void add_master_squares(const uint4 &v, float scale, float (&acc)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (DT == kF32) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x = __uint_as_float(w[i]);
-            acc[i] = __fmaf_rn(x, x, acc[i]);
-        }
-    } else if constexpr (DT == kE4M3) {
-        // sum of the codes' squares, then times the square of the scale
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            asm("{\n\t.reg .b16 l, h, a, b;\n\t.reg .b32 p, q;\n\tmov.b32 {l, h}, %4;\n\t"
-                "cvt.rn.f16x2.e4m3x2 p, l;\n\tcvt.rn.f16x2.e4m3x2 q, h;\n\t"
-                "mov.b32 {a, b}, p;\n\t"
-                "fma.rn.f32.f16 %0, a, a, %0;\n\tfma.rn.f32.f16 %1, b, b, %1;\n\t"
-                "mov.b32 {a, b}, q;\n\t"
-                "fma.rn.f32.f16 %2, a, a, %2;\n\tfma.rn.f32.f16 %3, b, b, %3;\n\t}"
-                : "+f"(s[0]), "+f"(s[1]), "+f"(s[2]), "+f"(s[3])
-                : "r"(w[i]));
-        }
-        const float t = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
-        acc[0] = __fmaf_rn(t, __fmul_rn(scale, scale), acc[0]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float &lo = acc[(2 * i) & 3], &hi = acc[(2 * i + 1) & 3];
-            if constexpr (DT == kBF16)
-                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-                    "fma.rn.f32.bf16 %0, a, a, %0;\n\tfma.rn.f32.bf16 %1, b, b, %1;\n\t}"
-                    : "+f"(lo), "+f"(hi) : "r"(w[i]));
-            else
-                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-                    "fma.rn.f32.f16 %0, a, a, %0;\n\tfma.rn.f32.f16 %1, b, b, %1;\n\t}"
-                    : "+f"(lo), "+f"(hi) : "r"(w[i]));
-        }
+    for (int i = 0; i < 4; ++i) {
+        asm("{\n\t.reg .b16 l, h, a, b;\n\t.reg .b32 p, q;\n\tmov.b32 {l, h}, %4;\n\t"
+            "cvt.rn.f16x2.e4m3x2 p, l;\n\tcvt.rn.f16x2.e4m3x2 q, h;\n\t"
+            "mov.b32 {a, b}, p;\n\t"
+            "fma.rn.f32.f16 %0, a, a, %0;\n\tfma.rn.f32.f16 %1, b, b, %1;\n\t"
+            "mov.b32 {a, b}, q;\n\t"
+            "fma.rn.f32.f16 %2, a, a, %2;\n\tfma.rn.f32.f16 %3, b, b, %3;\n\t}"
+            : "+f"(s[0]), "+f"(s[1]), "+f"(s[2]), "+f"(s[3])
+            : "r"(w[i]));
     }
+    const float t = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
+    acc[0] = __fmaf_rn(t, __fmul_rn(scale, scale), acc[0]);
 }
 
 // The thread's part of a chunk in binary64, element by element.
@@ -201,7 +179,10 @@ __device__ __forceinline__ double square_part(const Entry &e, int64_t v0) {
     }
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < kPart; ++i) add_squares<DT>(v[i], DT == kE4M3 ? scale[i] : 1.0f, acc);
+    for (int i = 0; i < kPart; ++i) {
+        if constexpr (DT == kE4M3) add_master_squares(v[i], scale[i], acc);
+        else add_squares<DT>(v[i], acc);
+    }
     const float s = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
     if (sum_stands(s)) return (double)s;
     // nothing but zeros (of either sign) is exact too

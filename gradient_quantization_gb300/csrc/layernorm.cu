@@ -26,6 +26,17 @@ __device__ __forceinline__ float param(const void *p, bool f32, int64_t i, float
     return f32 ? load_elem<kF32>(p, i) : load_elem<DT>(p, i);
 }
 
+// Mean and variance from the sums of a row and of its squares.  They stand where the
+// mean is at most one standard deviation: what the difference of the two terms loses
+// is then at most a bit.  Elsewhere (and where the squares may have overflowed) the
+// row takes a second pass over the differences to its mean.
+__device__ __forceinline__ bool moments(float sum, float squares, float inv, float &mu, float &var) {
+    mu = __fmul_rn(sum, inv);
+    const float second = __fmul_rn(squares, inv);
+    var = __fmaf_rn(-mu, mu, second);
+    return __fmul_rn(mu, mu) <= var && second < 1e37f;
+}
+
 // 1 / sqrt(v): the hardware's approximation, off by less than 2^-22.
 __device__ __forceinline__ float inv_sqrt(float v) {
     float r;
@@ -83,15 +94,15 @@ struct Group {
     }
 };
 
-// The sums of N = 1, 2 or 4 values over the group (each thread gets them), in a fixed
+// The sums of N = 1, 2, 4 or 8 values over the group (each thread gets them), in a fixed
 // order; `red` holds kRed floats a value, 0 where no warp writes, and is free again
 // after the group's next barrier.  All threads of a warp call it.  Several values halve
 // in number at each of the first exchanges, a half warp (quarter) going on with its
-// own: six shuffles for four values.
+// own: six shuffles for four values, nine for eight.
 constexpr int kRed = 32;
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float *red, const Group &g) {
-    static_assert(N == 1 || N == 2 || N == 4, "values");
+    static_assert(N == 1 || N == 2 || N == 4 || N == 8, "values");
     const int lane = threadIdx.x & 31;
     if (g.size < 32) {
         for (int o = g.size >> 1; o > 0; o >>= 1) {
@@ -116,7 +127,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float *red, const Group 
     }
 #pragma unroll
     for (; o > 0; o >>= 1) s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xFFFFFFFFu, s[0], o));
-    // lane 32 / N * i has the warp's sum of value i (N = 4: of 0, 1, 2, 3 in order)
+    // lane 32 / N * i has the warp's sum of value i in order
     if (g.size == 32) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, s[0], 32 / N * i);
@@ -214,13 +225,13 @@ ln_forward_rows_kernel(const LnForward a, int size) {
     constexpr int kStages = kRing<F>;
     constexpr bool kKeep = F <= 16;      // w and b stay in registers
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ __align__(16) float red[kMaxGroups][2][R * kRed];
+    __shared__ __align__(16) float red[kMaxGroups][2][2 * R * kRed];
     const Group g(size);
     const int vectors = (int)(a.H / V), groups = blockDim.x / size;
     const int64_t step = (int64_t)gridDim.x * groups * R;
     const float inv = __frcp_rn((float)a.H);
-    float (*const mine)[R * kRed] = red[size > 32 ? g.id : 0];
-    for (int i = threadIdx.x; i < kMaxGroups * 2 * R * kRed; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+    float (*const mine)[2 * R * kRed] = red[size > 32 ? g.id : 0];
+    for (int i = threadIdx.x; i < kMaxGroups * 4 * R * kRed; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
     // slot i of row r of stage s: shared + s * stage_bytes + (r * NV + i) * slot_bytes
     const uint32_t shared = shared_address(ring + threadIdx.x);
@@ -266,6 +277,7 @@ ln_forward_rows_kernel(const LnForward a, int size) {
         }
     }
     uint32_t from = shared;
+    int half = 0;
     char *out = elem_at<DT>(a.y, (first + g.id * R) * a.ldy);
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
         const int64_t t = t0 + g.id * R;
@@ -275,38 +287,52 @@ ln_forward_rows_kernel(const LnForward a, int size) {
         bool row[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) row[r] = t + r < a.T;
-        float s[R], mu[R], rs[R];
+        float s[2 * R], mu[R], var[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < NV; ++i) add_elems<DT>(load(r, i), sum);
-            s[r] = __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]));
-        }
-        fetch();
-        row_sums(s, mine[0], g);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            mu[r] = __fmul_rn(s[r], inv);
-            uint64_t q0 = 0, q1 = 0;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, squares[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                uint64_t d[P];
-                differences<DT>(load(r, i), mu[r], d);
-                if (!in[i]) continue;
-#pragma unroll
-                for (int k = 0; k < P; k += 2) {
-                    q0 = fma_f32x2(d[k], d[k], q0);
-                    q1 = fma_f32x2(d[k + 1], d[k + 1], q1);
-                }
+                const uint4 v = load(r, i);
+                add_elems<DT>(v, sum);
+                add_squares<DT>(v, squares);
             }
-            s[r] = __fadd_rn(sum_pair(q0), sum_pair(q1));
+            s[2 * r] = __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]));
+            s[2 * r + 1] = __fadd_rn(__fadd_rn(squares[0], squares[1]), __fadd_rn(squares[2], squares[3]));
         }
-        row_sums(s, mine[1], g);
+        fetch();
+        row_sums(s, mine[half], g);
+        half ^= 1;
+        bool stand = true;
+#pragma unroll
+        for (int r = 0; r < R; ++r) stand &= moments(s[2 * r], s[2 * r + 1], inv, mu[r], var[r]);
+        if (__any_sync(0xFFFFFFFFu, !stand)) {      // the same for all threads of a group
+            float q[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                uint64_t q0 = 0, q1 = 0;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    uint64_t d[P];
+                    differences<DT>(load(r, i), mu[r], d);
+                    if (!in[i]) continue;
+#pragma unroll
+                    for (int k = 0; k < P; k += 2) {
+                        q0 = fma_f32x2(d[k], d[k], q0);
+                        q1 = fma_f32x2(d[k + 1], d[k + 1], q1);
+                    }
+                }
+                q[r] = __fadd_rn(sum_pair(q0), sum_pair(q1));
+            }
+            row_sums(q, mine[half], g);
+            half ^= 1;
+#pragma unroll
+            for (int r = 0; r < R; ++r) var[r] = __fmul_rn(q[r], inv);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            rs[r] = inv_sqrt(__fmaf_rn(s[r], inv, a.eps));
-            const uint64_t r2 = f32x2(rs[r], rs[r]);
+            const float rs = inv_sqrt(__fadd_rn(var[r], a.eps));
+            const uint64_t r2 = f32x2(rs, rs);
             uint4 v[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -336,7 +362,7 @@ ln_forward_rows_kernel(const LnForward a, int size) {
             }
             if (g.tid == 0 && row[r]) {
                 if (a.mean) a.mean[t + r] = mu[r];
-                if (a.rstd) a.rstd[t + r] = rs[r];
+                if (a.rstd) a.rstd[t + r] = rs;
             }
         }
         out += step * y_row;
@@ -470,12 +496,12 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
     using Word = typename E::Word;
     constexpr int V = E::kVec, P = V / 2, F = NV * V;
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ __align__(16) float red[2][kRed];
+    __shared__ __align__(16) float red[2][2 * kRed];
     const Group g(blockDim.x);
     const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H, vectors = row_slots<DT>(H);
     const float inv = __frcp_rn((float)a.H);
     const int64_t step = gridDim.x;
-    for (int i = tid; i < 2 * kRed; i += threads) (&red[0][0])[i] = 0.0f;
+    for (int i = tid; i < 4 * kRed; i += threads) (&red[0][0])[i] = 0.0f;
     RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
     uint4 *staged = ring + kAnyStages * vectors;                  // two rows of y
     Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.y, blockIdx.x * a.ldy));
@@ -511,7 +537,7 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
         const uint4 *data = ring + stage * vectors;
         stage = stage + 1 == kAnyStages ? 0 : stage + 1;
         uint4 v[NV];
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, squares[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = tid + i * threads;
@@ -519,33 +545,33 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
             if (j < in.n) v[i] = data[j];
             if (in.part(j)) v[i] = in.masked(v[i], j, H);
             add_elems<DT>(v[i], sum);
+            add_squares<DT>(v[i], squares);
         }
-        float s[1] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]))};
+        float s[2] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])),
+                      __fadd_rn(__fadd_rn(squares[0], squares[1]), __fadd_rn(squares[2], squares[3]))};
         row_sums(s, red[0], g);
-        const float mu = __fmul_rn(s[0], inv);
-        uint64_t d[F / 2], q0 = 0, q1 = 0;
+        float mu, var;
+        if (!moments(s[0], s[1], inv, mu, var)) {                 // the same for all threads
+            uint64_t q0 = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = tid + i * threads;
-            uint64_t *dj = d + i * P;
-            differences<DT>(v[i], mu, dj);
-            if (in.part(j)) {
+            for (int i = 0; i < NV; ++i) {
+                const int j = tid + i * threads;
+                uint64_t d[P];
+                differences<DT>(v[i], mu, d);
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
                     const int e = j * V - in.skip + 2 * k;
-                    dj[k] = f32x2(e >= 0 && e < H ? lo_f32(dj[k]) : 0.0f,
-                                  e + 1 >= 0 && e + 1 < H ? hi_f32(dj[k]) : 0.0f);
+                    if (in.part(j))
+                        d[k] = f32x2(e >= 0 && e < H ? lo_f32(d[k]) : 0.0f,
+                                     e + 1 >= 0 && e + 1 < H ? hi_f32(d[k]) : 0.0f);
+                    q0 = fma_f32x2(d[k], d[k], q0);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < P; k += 2) {
-                q0 = fma_f32x2(dj[k], dj[k], q0);
-                q1 = fma_f32x2(dj[k + 1], dj[k + 1], q1);
-            }
+            float q[1] = {sum_pair(q0)};
+            row_sums(q, red[1], g);
+            var = __fmul_rn(q[0], inv);
         }
-        float q[1] = {__fadd_rn(sum_pair(q0), sum_pair(q1))};
-        row_sums(q, red[1], g);
-        const float r = inv_sqrt(__fmaf_rn(q[0], inv, a.eps));
+        const float r = inv_sqrt(__fadd_rn(var, a.eps));
         const uint64_t r2 = f32x2(r, r);
         uint4 *mine = staged + half * vectors;
         half ^= 1;
@@ -553,7 +579,8 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
         for (int i = 0; i < NV; ++i) {
             const int j = tid + i * threads;
             if (j >= in.n) continue;
-            uint64_t *y = d + i * P;
+            uint64_t y[P];
+            differences<DT>(v[i], mu, y);
 #pragma unroll
             for (int k = 0; k < P; ++k)
                 y[k] = fma_f32x2(mul_f32x2(y[k], r2), w[i * P + k], b[i * P + k]);
@@ -699,13 +726,15 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
     constexpr int kStages = kBackStages, kWords = 4 * BITS;
     constexpr int kParts = BITS ? 1 : 2;             // dy, and x
     extern __shared__ __align__(16) uint4 ring[];
-    __shared__ __align__(16) float red[kMaxGroups][2][2 * R * kRed];
+    constexpr int kSums = BITS ? 4 : 2;              // of a row
+    __shared__ __align__(16) float red[kMaxGroups][2][kSums * R * kRed];
     const Group g(size);
     const int threads = blockDim.x, vectors = (int)(a.H / V), groups = threads / size;
     const int64_t step = (int64_t)gridDim.x * groups * R;
     const float inv = __frcp_rn((float)a.H);
-    float (*const mine)[2 * R * kRed] = red[size > 32 ? g.id : 0];
-    for (int i = threadIdx.x; i < kMaxGroups * 4 * R * kRed; i += threads) (&red[0][0][0])[i] = 0.0f;
+    float (*const mine)[kSums * R * kRed] = red[size > 32 ? g.id : 0];
+    for (int i = threadIdx.x; i < kMaxGroups * 2 * kSums * R * kRed; i += threads)
+        (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
     // slot i of part p of row r of stage s: shared + s * stage_bytes +
     // ((r * kParts + p) * NV + i) * slot_bytes
@@ -809,71 +838,93 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
                 for (int i = 0; i < NV; ++i)
                     vx[r][i] = dequantize_chunk<BITS>(lo[r][i & 1], hi[r][i & 1], scale[r]);
         }
-        float s[2 * R];
+        // of a row: sum g and sum g xh; of codes sum g, sum g x, sum x and sum x^2
+        float s[kSums * R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             mu[r] = mean[r];
             rs[r] = rstd[r];
             const uint64_t r2 = f32x2(rs[r], rs[r]);
             uint64_t g0 = 0, g1 = 0;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, squares[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 uint4 vd, v;
                 uint64_t d[P], x[P];
                 load(r, i, vd, v);
                 unpack2<DT>(vd, d);
-                if constexpr (BITS == 0) differences<DT>(v, mu[r], x);
-                else add_elems<DT>(v, sum);
+                if constexpr (BITS == 0) {
+                    differences<DT>(v, mu[r], x);
+                } else {
+                    unpack2<DT>(v, x);
+                    add_elems<DT>(v, sum);
+                    add_squares<DT>(v, squares);
+                }
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
                     const uint64_t gk = mul_f32x2(d[k], w[i * P + k]);
                     g0 = add_f32x2(g0, gk);
-                    if constexpr (BITS == 0) g1 = fma_f32x2(gk, mul_f32x2(x[k], r2), g1);
+                    g1 = fma_f32x2(gk, BITS ? x[k] : mul_f32x2(x[k], r2), g1);
                 }
             }
-            s[2 * r] = sum_pair(g0);
-            s[2 * r + 1] = BITS ? __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]))
-                                : sum_pair(g1);
+            s[kSums * r] = sum_pair(g0);
+            s[kSums * r + 1] = sum_pair(g1);
+            if constexpr (BITS != 0) {
+                s[kSums * r + 2] = __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3]));
+                s[kSums * r + 3] =
+                    __fadd_rn(__fadd_rn(squares[0], squares[1]), __fadd_rn(squares[2], squares[3]));
+            }
         }
         fetch();
         ahead(t + step);
-        row_sums(s, mine[BITS ? 0 : half], g);
+        row_sums(s, mine[half], g);
         half ^= 1;
+        bool stand = true;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            s0[r] = __fmul_rn(s[2 * r], inv);
-            s1[r] = __fmul_rn(s[2 * r + 1], inv);
+            s0[r] = __fmul_rn(s[kSums * r], inv);
+            s1[r] = __fmul_rn(s[kSums * r + 1], inv);
+            if constexpr (BITS != 0) {
+                // sum g (x - mu) / H; the difference loses no more than the variance's
+                float var;
+                stand &= moments(s[kSums * r + 2], s[kSums * r + 3], inv, mu[r], var);
+                s1[r] = __fmaf_rn(-mu[r], s0[r], s1[r]);
+                rs[r] = inv_sqrt(__fadd_rn(var, a.eps));
+            }
         }
         if constexpr (BITS != 0) {
-            // the statistics of the dequantized row, and sum g (x - mu)
+            if (__any_sync(0xFFFFFFFFu, !stand)) {      // the same for all threads of a group
+                float q[2 * R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                mu[r] = s1[r];
-                uint64_t q0 = 0, g1 = 0;
+                for (int r = 0; r < R; ++r) {
+                    uint64_t q0 = 0, g1 = 0;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    uint4 vd, v;
-                    uint64_t d[P], x[P];
-                    load(r, i, vd, v);
-                    unpack2<DT>(vd, d);
-                    differences<DT>(v, mu[r], x);
-                    if (!in[i]) continue;
+                    for (int i = 0; i < NV; ++i) {
+                        uint4 vd, v;
+                        uint64_t d[P], x[P];
+                        load(r, i, vd, v);
+                        unpack2<DT>(vd, d);
+                        differences<DT>(v, mu[r], x);
+                        if (!in[i]) continue;
 #pragma unroll
-                    for (int k = 0; k < P; ++k) {
-                        q0 = fma_f32x2(x[k], x[k], q0);
-                        g1 = fma_f32x2(mul_f32x2(d[k], w[i * P + k]), x[k], g1);
+                        for (int k = 0; k < P; ++k) {
+                            q0 = fma_f32x2(x[k], x[k], q0);
+                            g1 = fma_f32x2(mul_f32x2(d[k], w[i * P + k]), x[k], g1);
+                        }
                     }
+                    q[2 * r] = sum_pair(q0);
+                    q[2 * r + 1] = sum_pair(g1);
                 }
-                s[2 * r] = sum_pair(q0);
-                s[2 * r + 1] = sum_pair(g1);
-            }
-            row_sums(s, mine[1], g);
+                row_sums(q, mine[half], g);
+                half ^= 1;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                rs[r] = inv_sqrt(__fmaf_rn(s[2 * r], inv, a.eps));
-                s1[r] = __fmul_rn(__fmul_rn(s[2 * r + 1], rs[r]), inv);
+                for (int r = 0; r < R; ++r) {
+                    rs[r] = inv_sqrt(__fmaf_rn(q[2 * r], inv, a.eps));
+                    s1[r] = __fmul_rn(q[2 * r + 1], inv);
+                }
             }
+#pragma unroll
+            for (int r = 0; r < R; ++r) s1[r] = __fmul_rn(s1[r], rs[r]);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {

@@ -170,6 +170,28 @@ __device__ __forceinline__ void add_elems(const uint4 &v, float (&acc)[4]) {
     }
 }
 
+// Add the squares of a vector's elements to four sums.
+template <int DT>
+__device__ __forceinline__ void add_squares(const uint4 &v, float (&acc)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float &lo = acc[(2 * i) & 3], &hi = acc[(2 * i + 1) & 3];
+        if constexpr (DT == kF32) {
+            const float x = __uint_as_float(w[i]);
+            acc[i] = __fmaf_rn(x, x, acc[i]);
+        } else if constexpr (DT == kBF16) {
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                "fma.rn.f32.bf16 %0, a, a, %0;\n\tfma.rn.f32.bf16 %1, b, b, %1;\n\t}"
+                : "+f"(lo), "+f"(hi) : "r"(w[i]));
+        } else {
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+                "fma.rn.f32.f16 %0, a, a, %0;\n\tfma.rn.f32.f16 %1, b, b, %1;\n\t}"
+                : "+f"(lo), "+f"(hi) : "r"(w[i]));
+        }
+    }
+}
+
 // A vector's elements as binary32 pairs, and back.  (16-bit types: an addition of -0,
 // which changes no value, in place of shifts and masks on the busier integer pipe.)
 template <int DT>
