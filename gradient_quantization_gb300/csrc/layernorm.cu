@@ -10,11 +10,15 @@
 //   xh = (x - mu) r,  y = xh w + b;
 //   g = dy w,  dx = r (g - sum(g)/H - xh sum(g xh)/H),
 //   dw = sum_t dy xh,  db = sum_t dy.
+#include <cooperative_groups.h>
+
 #include "agoq_launch.h"
 #include "typed_io.cuh"
 
 namespace agoq {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
@@ -146,6 +150,62 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float *red, const Group 
     }
 }
 
+// The columns of a CTA: all of a row's or, of long rows, one of the equal parts that the
+// CTAs of a cluster take.  CTAs or clusters take the rows `unit`, `unit` + `units`, ...
+constexpr int kMaxParts = 8;
+struct Columns {
+    int first, n, rank, parts, unit, units;
+};
+template <bool SPLIT>
+__device__ __forceinline__ Columns columns_of(int64_t H, int part) {
+    if constexpr (!SPLIT) return {0, (int)H, 0, 1, (int)blockIdx.x, (int)gridDim.x};
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int parts = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    return {rank * part,  min(part, (int)H - rank * part), rank, parts, (int)blockIdx.x / parts,
+            (int)gridDim.x / parts};
+}
+
+// Before and after a kernel's accesses.  The next launch may take its places from the
+// start on, but for clusters, and between their launches, only at the end: CTAs that find
+// a place early leave gaps that no whole cluster fits, and the clusters that are left over
+// take as long again (backward of 4096 x 8704 back to back: 111 us, 69 so).
+template <bool SPLIT>
+__device__ __forceinline__ void begin() {
+    if constexpr (SPLIT) {
+        cg::this_cluster().sync();                               // all of it has begun
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    } else {
+        pdl_wait_and_release();
+    }
+}
+template <bool SPLIT>
+__device__ __forceinline__ void end_rows() {
+    if constexpr (SPLIT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Sums over the CTAs' parts of a row, added in the order of the parts: `box` receives
+// them from all, in turn one and the other half, so that one barrier is enough (a CTA
+// writes a half again only after the barrier that follows everyone's reading of it).
+template <int N>
+__device__ __forceinline__ void parts_sums(float (&v)[N], float (&box)[2][kMaxParts * N], int &turn,
+                                           const Columns &c) {
+    cg::cluster_group cluster = cg::this_cluster();
+    float *mine = box[turn];
+    turn ^= 1;
+    if ((int)threadIdx.x < c.parts) {
+        float *to = cluster.map_shared_rank(mine, threadIdx.x) + c.rank * N;
+#pragma unroll
+        for (int i = 0; i < N; ++i) to[i] = v[i];
+    }
+    cluster.sync();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    for (int k = 0; k < c.parts; ++k) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], mine[k * N + i]);
+    }
+}
+
 // The i-th of the NV vectors of a row that a thread of a group holds.  16-bit types:
 // an octet of lanes holds blocks of 128 elements, lane j their vectors j and j + 8.
 template <int DT>
@@ -212,23 +272,23 @@ __device__ __forceinline__ void quantize_octet(const uint4 &a, const uint4 &b, u
 // rows and step (their sums share the exchanges and the barriers), NV vectors of a row a
 // thread.  Copies into a ring of shared memory run kRing - 1 steps ahead; a thread
 // reads only what it copied, so the ring needs no barrier, and the row is read from
-// there for each of its passes.  BITS: the codes of x too.
-template <int F>
-constexpr int kRing = F == 32 ? 3 : 4;       // stages (rows of 64 KB: 192 KB)
-template <int DT, int NV>
-constexpr int kRows = DT != kF32 && NV == 2 ? 2 : 1;
+// there for each of its passes; w and b stay in registers.  BITS: the codes of x too.
+template <int DT>
+constexpr int kRows = DT == kF32 ? 1 : 2;
+constexpr int kRing = 4;                     // stages
 
-template <int DT, int BITS, int NV, int LIMIT>
-__global__ void __launch_bounds__(LIMIT, LIMIT > 256 ? 1 : NV * Elem<DT>::kVec == 32 || BITS ? 2 : 3)
-ln_forward_rows_kernel(const LnForward a, int size) {
-    constexpr int V = Elem<DT>::kVec, F = NV * V, P = V / 2, R = kRows<DT, NV>;
-    constexpr int kStages = kRing<F>;
-    constexpr bool kKeep = F <= 16;      // w and b stay in registers
+template <int DT, int BITS, bool SPLIT>
+__global__ void __launch_bounds__(256, BITS ? 2 : 3)
+ln_forward_rows_kernel(const LnForward a, int size, int part) {
+    constexpr int V = Elem<DT>::kVec, F = 16, NV = F / V, P = V / 2, R = kRows<DT>;
+    constexpr int kStages = kRing;
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ __align__(16) float red[kMaxGroups][2][2 * R * kRed];
+    __shared__ float box1[2][kMaxParts * 2 * R], box2[2][kMaxParts * R];
     const Group g(size);
-    const int vectors = (int)(a.H / V), groups = blockDim.x / size;
-    const int64_t step = (int64_t)gridDim.x * groups * R;
+    const Columns c = columns_of<SPLIT>(a.H, part);
+    const int vectors = c.n / V, groups = SPLIT ? 1 : blockDim.x / size;
+    const int64_t step = (int64_t)c.units * groups * R;
     const float inv = __frcp_rn((float)a.H);
     float (*const mine)[2 * R * kRed] = red[size > 32 ? g.id : 0];
     for (int i = threadIdx.x; i < kMaxGroups * 4 * R * kRed; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
@@ -245,12 +305,12 @@ ln_forward_rows_kernel(const LnForward a, int size) {
         for (int k = 0; k < kStages * R; ++k)
             store_shared(shared + (k * NV + i) * slot_bytes, make_uint4(0, 0, 0, 0));
     }
-    const int64_t first = (int64_t)blockIdx.x * groups * R;      // of the CTA
-    pdl_wait_and_release();
+    const int64_t first = (int64_t)c.unit * groups * R;          // of the CTA
+    begin<SPLIT>();
     // the next rows to copy, and their pointer
     int64_t tf = first + g.id * R;
     const int64_t x_row = a.ldx * Elem<DT>::kSize, y_row = a.ldy * Elem<DT>::kSize;
-    const char *xf = elem_at<DT>(a.x, tf * a.ldx);
+    const char *xf = elem_at<DT>(a.x, tf * a.ldx + c.first);
     uint32_t into = shared;
     auto fetch = [&]() {
 #pragma unroll
@@ -268,17 +328,16 @@ ln_forward_rows_kernel(const LnForward a, int size) {
     };
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) fetch();
-    uint64_t w[kKeep ? F / 2 : 1], b[kKeep ? F / 2 : 1];
-    if constexpr (kKeep) {
+    uint64_t w[F / 2], b[F / 2];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            load_params<DT>(a.w, a.param_f32, in[i] ? place<DT>(g, i) : 0, 1.0f, w + i * P);
-            load_params<DT>(a.b, a.param_f32, in[i] ? place<DT>(g, i) : 0, 0.0f, b + i * P);
-        }
+    for (int i = 0; i < NV; ++i) {
+        const int j = c.first / V + (in[i] ? place<DT>(g, i) : 0);
+        load_params<DT>(a.w, a.param_f32, j, 1.0f, w + i * P);
+        load_params<DT>(a.b, a.param_f32, j, 0.0f, b + i * P);
     }
     uint32_t from = shared;
-    int half = 0;
-    char *out = elem_at<DT>(a.y, (first + g.id * R) * a.ldy);
+    int half = 0, turn1 = 0, turn2 = 0;
+    char *out = elem_at<DT>(a.y, (first + g.id * R) * a.ldy + c.first);
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
         const int64_t t = t0 + g.id * R;
         copies_left<kStages - 2>();
@@ -303,6 +362,7 @@ ln_forward_rows_kernel(const LnForward a, int size) {
         fetch();
         row_sums(s, mine[half], g);
         half ^= 1;
+        if constexpr (SPLIT) parts_sums(s, box1, turn1, c);
         bool stand = true;
 #pragma unroll
         for (int r = 0; r < R; ++r) stand &= moments(s[2 * r], s[2 * r + 1], inv, mu[r], var[r]);
@@ -326,6 +386,7 @@ ln_forward_rows_kernel(const LnForward a, int size) {
             }
             row_sums(q, mine[half], g);
             half ^= 1;
+            if constexpr (SPLIT) parts_sums(q, box2, turn2, c);
 #pragma unroll
             for (int r = 0; r < R; ++r) var[r] = __fmul_rn(q[r], inv);
         }
@@ -336,31 +397,25 @@ ln_forward_rows_kernel(const LnForward a, int size) {
             uint4 v[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int j = place<DT>(g, i);
                 v[i] = load(r, i);
                 if (!row[r] || !in[i]) continue;
-                uint64_t y[P], wj[P], bj[P];
+                uint64_t y[P];
                 differences<DT>(v[i], mu[r], y);
-                if constexpr (!kKeep) {
-                    load_params<DT>(a.w, a.param_f32, j, 1.0f, wj);
-                    load_params<DT>(a.b, a.param_f32, j, 0.0f, bj);
-                }
 #pragma unroll
                 for (int k = 0; k < P; ++k)
-                    y[k] = fma_f32x2(mul_f32x2(y[k], r2), kKeep ? w[kKeep ? i * P + k : 0] : wj[k],
-                                     kKeep ? b[kKeep ? i * P + k : 0] : bj[k]);
-                *reinterpret_cast<uint4 *>(out + r * y_row + j * 16) = pack2<DT>(y);
+                    y[k] = fma_f32x2(mul_f32x2(y[k], r2), w[i * P + k], b[i * P + k]);
+                *reinterpret_cast<uint4 *>(out + r * y_row + place<DT>(g, i) * 16) = pack2<DT>(y);
             }
             if constexpr (BITS != 0) {
 #pragma unroll
                 for (int i = 0; i < NV; i += 2) {
-                    const int64_t blk = (t + r) * (a.H / kBlock) + place<DT>(g, i) / 16;
+                    const int64_t blk = (t + r) * (a.H / kBlock) + c.first / kBlock + place<DT>(g, i) / 16;
                     quantize_octet<BITS>(v[i], v[i + 1],
                                          static_cast<uint32_t *>(a.codes) + blk * 4 * BITS,
                                          a.scales + blk, row[r] && in[i]);
                 }
             }
-            if (g.tid == 0 && row[r]) {
+            if (g.tid == 0 && c.rank == 0 && row[r]) {
                 if (a.mean) a.mean[t + r] = mu[r];
                 if (a.rstd) a.rstd[t + r] = rs;
             }
@@ -368,6 +423,7 @@ ln_forward_rows_kernel(const LnForward a, int size) {
         out += step * y_row;
         from = from == shared + (kStages - 1) * stage_bytes ? shared : from + stage_bytes;
     }
+    end_rows<SPLIT>();
 }
 
 // ---- rows of any alignment ------------------------------------------------------
@@ -490,27 +546,29 @@ __device__ __forceinline__ void write_any(typename Elem<DT>::Word *out, const Pl
 // y, with shared memory in between where they differ.  The CTAs' steps are multiples of
 // eight rows, so that all rows of a CTA start at the same place between boundaries and a
 // thread's weights stay in registers.
-template <int DT, int NV>
-__global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) {
+template <int DT, int NV, bool SPLIT>
+__global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a, int part) {
     using E = Elem<DT>;
     using Word = typename E::Word;
     constexpr int V = E::kVec, P = V / 2, F = NV * V;
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ __align__(16) float red[2][2 * kRed];
     const Group g(blockDim.x);
-    const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H, vectors = row_slots<DT>(H);
+    __shared__ float box1[2][kMaxParts * 2], box2[2][kMaxParts];
+    const Columns c = columns_of<SPLIT>(a.H, part);
+    const int threads = blockDim.x, tid = threadIdx.x, H = c.n, vectors = row_slots<DT>(H);
     const float inv = __frcp_rn((float)a.H);
-    const int64_t step = gridDim.x;
+    const int64_t step = c.units, first = c.unit;
     for (int i = tid; i < 4 * kRed; i += threads) (&red[0][0])[i] = 0.0f;
-    RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
+    RowRing<DT, kAnyStages> x{elem_at<DT>(a.x, c.first), a.ldx, a.T, step, H, vectors, ring};
     uint4 *staged = ring + kAnyStages * vectors;                  // two rows of y
-    Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.y, blockIdx.x * a.ldy));
-    const Place<DT> in(elem_at<DT>(a.x, blockIdx.x * a.ldx), H), o(out, H);
+    Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.y, first * a.ldy + c.first));
+    const Place<DT> in(elem_at<DT>(x.p, first * a.ldx), H), o(out, H);
     const bool level = o.skip == in.skip;
-    pdl_wait_and_release();
+    begin<SPLIT>();
 #pragma unroll
     for (int s = 0; s < kAnyStages - 1; ++s) {
-        x.fetch(blockIdx.x + s * step, s);
+        x.fetch(first + s * step, s);
         copies_commit();
     }
     uint64_t w[F / 2], b[F / 2];
@@ -521,14 +579,14 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
         for (int k = 0; k < 2; ++k) {
             const int e = (tid + i / V * threads) * V - in.skip + i % V + k;
             const bool has = e >= 0 && e < H;
-            f[k] = has ? param<DT>(a.w, a.param_f32, e, 1.0f) : 0.0f;
-            f[2 + k] = has ? param<DT>(a.b, a.param_f32, e, 0.0f) : 0.0f;
+            f[k] = has ? param<DT>(a.w, a.param_f32, c.first + e, 1.0f) : 0.0f;
+            f[2 + k] = has ? param<DT>(a.b, a.param_f32, c.first + e, 0.0f) : 0.0f;
         }
         w[i / 2] = f32x2(f[0], f[1]);
         b[i / 2] = f32x2(f[2], f[3]);
     }
-    int stage = 0, half = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += step) {
+    int stage = 0, half = 0, turn1 = 0, turn2 = 0;
+    for (int64_t t = first; t < a.T; t += step) {
         copies_left<kAnyStages - 2>();
         x.settle();
         __syncthreads();                                          // the row is complete
@@ -550,6 +608,7 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
         float s[2] = {__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])),
                       __fadd_rn(__fadd_rn(squares[0], squares[1]), __fadd_rn(squares[2], squares[3]))};
         row_sums(s, red[0], g);
+        if constexpr (SPLIT) parts_sums(s, box1, turn1, c);
         float mu, var;
         if (!moments(s[0], s[1], inv, mu, var)) {                 // the same for all threads
             uint64_t q0 = 0;
@@ -569,6 +628,7 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
             }
             float q[1] = {sum_pair(q0)};
             row_sums(q, red[1], g);
+            if constexpr (SPLIT) parts_sums(q, box2, turn2, c);
             var = __fmul_rn(q[0], inv);
         }
         const float r = inv_sqrt(__fadd_rn(var, a.eps));
@@ -591,11 +651,12 @@ __global__ void __launch_bounds__(512) ln_forward_any_kernel(const LnForward a) 
         __syncthreads();
         write_any<DT>(out, o, in, mine, H);
         out += step * a.ldy;
-        if (tid == 0) {
+        if (tid == 0 && c.rank == 0) {
             if (a.mean) a.mean[t] = mu;
             if (a.rstd) a.rstd[t] = r;
         }
     }
+    end_rows<SPLIT>();
 }
 
 // The codes of x on their own (rows that the kernels above do not quantize): an octet
@@ -719,8 +780,8 @@ template <int DT>
 constexpr int kBackRows = DT == kF32 ? 1 : 2;
 constexpr int kBackStages = 3;
 
-template <int DT, int BITS>
-__global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward a, int size) {
+template <int DT, int BITS, bool SPLIT>
+__global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward a, int size, int part) {
     using E = Elem<DT>;
     constexpr int V = E::kVec, F = 16, NV = F / V, P = V / 2, R = kBackRows<DT>;
     constexpr int kStages = kBackStages, kWords = 4 * BITS;
@@ -728,9 +789,11 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
     extern __shared__ __align__(16) uint4 ring[];
     constexpr int kSums = BITS ? 4 : 2;              // of a row
     __shared__ __align__(16) float red[kMaxGroups][2][kSums * R * kRed];
+    __shared__ float box1[2][kMaxParts * kSums * R], box2[2][kMaxParts * 2 * R];
     const Group g(size);
-    const int threads = blockDim.x, vectors = (int)(a.H / V), groups = threads / size;
-    const int64_t step = (int64_t)gridDim.x * groups * R;
+    const Columns c = columns_of<SPLIT>(a.H, part);
+    const int threads = blockDim.x, vectors = c.n / V, groups = SPLIT ? 1 : threads / size;
+    const int64_t step = (int64_t)c.units * groups * R;
     const float inv = __frcp_rn((float)a.H);
     float (*const mine)[kSums * R * kRed] = red[size > 32 ? g.id : 0];
     for (int i = threadIdx.x; i < kMaxGroups * 2 * kSums * R * kRed; i += threads)
@@ -749,12 +812,12 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
         for (int k = 0; k < kStages * R * kParts; ++k)
             store_shared(shared + (k * NV + i) * slot_bytes, make_uint4(0, 0, 0, 0));
     }
-    pdl_wait_and_release();
-    const int64_t first = (int64_t)blockIdx.x * groups * R;      // of the CTA
+    begin<SPLIT>();
+    const int64_t first = (int64_t)c.unit * groups * R;          // of the CTA
     // the next rows to copy, and their pointers
     int64_t tf = first + g.id * R;
-    const char *dyf = elem_at<DT>(a.dy, tf * a.lddy);
-    const char *xf = BITS ? nullptr : elem_at<DT>(a.x, tf * a.ldx);
+    const char *dyf = elem_at<DT>(a.dy, tf * a.lddy + c.first);
+    const char *xf = BITS ? nullptr : elem_at<DT>(a.x, tf * a.ldx + c.first);
     const int64_t dy_row = a.lddy * E::kSize, x_row = a.ldx * E::kSize;
     uint32_t into = shared;
     auto fetch = [&]() {
@@ -796,7 +859,7 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
             } else {
                 const int j = place<DT>(g, 0);           // the octet's block
                 if (!in[0]) return;
-                const int64_t blk = (t + r) * (a.H / kBlock) + j / 16;
+                const int64_t blk = (t + r) * (a.H / kBlock) + c.first / kBlock + j / 16;
                 const uint32_t *rec = static_cast<const uint32_t *>(a.x) + blk * kWords;
                 load_chunk<BITS>(rec, j & 7, lo[r][0], hi[r][0]);
                 load_chunk<BITS>(rec, (j & 7) + 8, lo[r][1], hi[r][1]);
@@ -810,12 +873,12 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
     uint64_t w[F / 2], dw[F / 2], db[F / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        load_params<DT>(a.w, a.param_f32, in[i] ? place<DT>(g, i) : 0, 1.0f, w + i * P);
+        load_params<DT>(a.w, a.param_f32, c.first / V + (in[i] ? place<DT>(g, i) : 0), 1.0f, w + i * P);
 #pragma unroll
     for (int i = 0; i < F / 2; ++i) dw[i] = db[i] = 0;
     uint32_t from = shared;
-    int half = 0;
-    char *out = elem_at<DT>(a.dx, (first + g.id * R) * a.lddx);
+    int half = 0, turn1 = 0, turn2 = 0;
+    char *out = elem_at<DT>(a.dx, (first + g.id * R) * a.lddx + c.first);
     const int64_t dx_row = a.lddx * E::kSize;
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
         const int64_t t = t0 + g.id * R;
@@ -879,6 +942,7 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
         ahead(t + step);
         row_sums(s, mine[half], g);
         half ^= 1;
+        if constexpr (SPLIT) parts_sums(s, box1, turn1, c);
         bool stand = true;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -917,6 +981,7 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
                 }
                 row_sums(q, mine[half], g);
                 half ^= 1;
+                if constexpr (SPLIT) parts_sums(q, box2, turn2, c);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     rs[r] = inv_sqrt(__fmaf_rn(q[2 * r], inv, a.eps));
@@ -952,8 +1017,9 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
         out += step * dx_row;
         from = from == shared + (kStages - 1) * stage_bytes ? shared : from + stage_bytes;
     }
+    end_rows<SPLIT>();
     if (!a.dw && !a.db) return;
-    float *partial = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
+    float *partial = a.workspace + (int64_t)c.unit * 2 * a.H + c.first;
     float *joined = reinterpret_cast<float *>(ring);          // [2][H], for several groups
     copies_left<0>();
     // groups of a warp first, then one after another
@@ -964,10 +1030,10 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
             db[i] = add_f32x2(db[i], __shfl_xor_sync(0xFFFFFFFFu, db[i], o));
         }
     }
-    const int parts = threads / max(size, 32), part = threadIdx.x / max(size, 32);
-    for (int who = 0; who < parts; ++who) {
+    const int shares = threads / max(size, 32), share = threadIdx.x / max(size, 32);
+    for (int who = 0; who < shares; ++who) {
         if (groups > 1) __syncthreads();
-        if (part != who || (size < 32 && (threadIdx.x & 31) >= size)) continue;
+        if (share != who || (size < 32 && (threadIdx.x & 31) >= size)) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = place<DT>(g, i);
@@ -992,32 +1058,35 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
 // Rows of any alignment: as the forward pass, x and dy through rings, in the layout of
 // dy (x's vectors are cut from two of its own where it lies elsewhere), dx through shared
 // memory; dw and db in registers, since a thread's columns stay the same.
-template <int DT, int LIMIT>
+template <int DT, int LIMIT, bool SPLIT>
 __global__ void __launch_bounds__(LIMIT, LIMIT == 320 ? 2 : 1)
-ln_backward_any_kernel(const LnBackward a) {
+ln_backward_any_kernel(const LnBackward a, int part) {
     using E = Elem<DT>;
     using Word = typename E::Word;
     constexpr int V = E::kVec, P = V / 2, F = 16, NV = F / V;
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ __align__(16) float red[2][2 * kRed];
     const Group g(blockDim.x);
-    const int threads = blockDim.x, tid = threadIdx.x, H = (int)a.H, vectors = row_slots<DT>(H);
+    __shared__ float box[2][kMaxParts * 2];
+    const Columns c = columns_of<SPLIT>(a.H, part);
+    const int threads = blockDim.x, tid = threadIdx.x, H = c.n, vectors = row_slots<DT>(H);
     const float inv = __frcp_rn((float)a.H);
-    const int64_t step = gridDim.x;
+    const int64_t step = c.units, first = c.unit;
     for (int i = tid; i < 4 * kRed; i += threads) (&red[0][0])[i] = 0.0f;
-    RowRing<DT, kAnyStages> x{a.x, a.ldx, a.T, step, H, vectors, ring};
-    RowRing<DT, kAnyStages> y{a.dy, a.lddy, a.T, step, H, vectors, ring + kAnyStages * vectors};
+    RowRing<DT, kAnyStages> x{elem_at<DT>(a.x, c.first), a.ldx, a.T, step, H, vectors, ring};
+    RowRing<DT, kAnyStages> y{elem_at<DT>(a.dy, c.first), a.lddy, a.T, step, H, vectors,
+                              ring + kAnyStages * vectors};
     uint4 *staged = ring + 2 * kAnyStages * vectors;              // two rows of dx
-    Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.dx, blockIdx.x * a.lddx));
-    const Place<DT> in(elem_at<DT>(a.dy, blockIdx.x * a.lddy), H),
-        ix(elem_at<DT>(a.x, blockIdx.x * a.ldx), H), o(out, H);
+    Word *out = reinterpret_cast<Word *>(elem_at<DT>(a.dx, first * a.lddx + c.first));
+    const Place<DT> in(elem_at<DT>(y.p, first * a.lddy), H), ix(elem_at<DT>(x.p, first * a.ldx), H),
+        o(out, H);
     const bool level = o.skip == in.skip;
     const int shift = ((ix.skip - in.skip + V) & (V - 1)) * E::kSize, back = ix.skip < in.skip;
-    pdl_wait_and_release();
+    begin<SPLIT>();
 #pragma unroll
     for (int s = 0; s < kAnyStages - 1; ++s) {
-        x.fetch(blockIdx.x + s * step, s);
-        y.fetch(blockIdx.x + s * step, s);
+        x.fetch(first + s * step, s);
+        y.fetch(first + s * step, s);
         copies_commit();
     }
     uint64_t w[F / 2], dw[F / 2], db[F / 2];
@@ -1027,7 +1096,7 @@ ln_backward_any_kernel(const LnBackward a) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int e = (tid + i / V * threads) * V - in.skip + i % V + k;
-            f[k] = e >= 0 && e < H ? param<DT>(a.w, a.param_f32, e, 1.0f) : 0.0f;
+            f[k] = e >= 0 && e < H ? param<DT>(a.w, a.param_f32, c.first + e, 1.0f) : 0.0f;
         }
         w[i / 2] = f32x2(f[0], f[1]);
         dw[i / 2] = db[i / 2] = 0;
@@ -1039,9 +1108,9 @@ ln_backward_any_kernel(const LnBackward a) {
             rstd = __ldg(a.rstd + t);
         }
     };
-    ahead(blockIdx.x);
-    int stage = 0, half = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += step) {
+    ahead(first);
+    int stage = 0, half = 0, turn = 0;
+    for (int64_t t = first; t < a.T; t += step) {
         copies_left<kAnyStages - 2>();
         x.settle();
         y.settle();
@@ -1092,6 +1161,7 @@ ln_backward_any_kernel(const LnBackward a) {
         }
         float s[2] = {sum_pair(g0), sum_pair(g1)};
         row_sums(s, red[half], g);
+        if constexpr (SPLIT) parts_sums(s, box, turn, c);
         const float s0 = __fmul_rn(s[0], inv), s1 = __fmul_rn(s[1], inv);
         const uint64_t s02 = f32x2(s0, s0), s12 = f32x2(-s1, -s1);
         uint4 *mine = staged + half * vectors;
@@ -1117,8 +1187,9 @@ ln_backward_any_kernel(const LnBackward a) {
         write_any<DT>(out, o, in, mine, H);
         out += step * a.lddx;
     }
+    end_rows<SPLIT>();
     if (!a.dw && !a.db) return;
-    float *partial = a.workspace + (int64_t)blockIdx.x * 2 * a.H;
+    float *partial = a.workspace + (int64_t)c.unit * 2 * a.H + c.first;
 #pragma unroll
     for (int i = 0; i < F; ++i) {
         const int e = (tid + i / V * threads) * V - in.skip + i % V;
@@ -1130,10 +1201,12 @@ ln_backward_any_kernel(const LnBackward a) {
 
 // dw and db: the P partial rows.  A CTA takes 32 columns; its eight warps add every
 // eighth row, and their sums are added in order.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads) ln_backward_join_kernel(
     const float *__restrict__ partials, int64_t H, int P, float *__restrict__ dw,
     float *__restrict__ db) {
-    pdl_wait_and_release();
+    if constexpr (SPLIT) asm volatile("griddepcontrol.wait;" ::: "memory");
+    else pdl_wait_and_release();
     __shared__ float sums[kWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < 2 * H; c0 += (int64_t)gridDim.x * 32) {
@@ -1154,6 +1227,7 @@ __global__ void __launch_bounds__(kThreads) ln_backward_join_kernel(
         }
         __syncthreads();
     }
+    end_rows<SPLIT>();
 }
 
 int grid_for(int64_t units, int per_sm) {
@@ -1181,32 +1255,86 @@ int resident_ctas(K kernel, int threads, size_t smem, int64_t units) {
     return grid_for(units, per_sm > 0 ? per_sm : 1);
 }
 
-template <int DT, int BITS, int NV, int LIMIT>
-cudaError_t forward_rows(const LnForward &a, cudaStream_t st) {
-    constexpr int F = NV * Elem<DT>::kVec, R = kRows<DT, NV>;
-    const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
-    const int threads = size * groups;
-    const size_t smem = (size_t)kRing<F> * R * NV * threads * 16;
-    static bool ready[kMaxDevices];
-    auto kernel = ln_forward_rows_kernel<DT, BITS, NV, LIMIT>;
-    // a ring of rows of 64 KB, the longest; with 16 elements a thread, of 4096 elements
-    const cudaError_t e =
-        allow_shared(kernel, (size_t)kRing<F> * R * (F == 32 ? 65536 : 4096 * Elem<DT>::kSize), ready);
-    if (e != cudaSuccess) return e;
-    const int ctas = resident_ctas(kernel, threads, smem, (a.T + groups * R - 1) / (groups * R));
-    return launch_pdl_clusters(kernel, ctas, threads, 1, smem, st, a, size);
+// Most columns of a CTA: what registers hold, 16 elements a thread (32 forward from any
+// alignment), and in the kernels for any alignment shared memory (five rows forward,
+// eight backward).
+constexpr int kForwardRows = 4096, kBackwardRows = 8192;
+template <int DT>
+constexpr int kForwardAny = DT == kF32 ? 11136 : 16256;
+template <int DT>
+constexpr int kBackwardAny = DT == kF32 ? 6912 : 8064;
+// Beyond that a row is shared by a cluster, in parts of at most as many columns as leave
+// room for two or three CTAs an SM (parts of up to 8192 instead of 4096: backward of 2048
+// x 12288 54 us, 51 with them; of up to 16256 and 11136 in any alignment: forward of
+// 1024 x 16383 46 us, 36 with them; 2000 x 12001 FP32 94 us, 71).  A row that one CTA
+// holds is not shared: the cluster's barrier costs more than the room gives (backward
+// of 4096 x 8192 55 us, 49 in one; forward of 3000 x 12001 67 us, 49 in one).
+constexpr int kForwardPart = 4096, kBackwardPart = 4096;
+template <int DT>
+constexpr int kAnyPart = DT == kF32 ? 3456 : 4992;
+
+// Long rows: the CTAs of a cluster take parts of `columns` each, a multiple of a block of
+// codes (and so of 16 bytes), the last one what is left.
+struct Parts {
+    int count, columns;
+    Parts(int64_t H, int most) {
+        count = (int)((H + most - 1) / most);
+        columns = (int)((H + count - 1) / count + kBlock - 1) / kBlock * kBlock;
+    }
+};
+
+// Clusters of a kernel whose CTAs stay: as many as are resident.
+template <typename K>
+int resident_clusters(K kernel, int threads, size_t smem, int parts, int64_t units) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(parts);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)parts, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
+    return (int)(units < n ? (units > 0 ? units : 1) : n);
 }
 
-constexpr int kLongRow = 65536;          // bytes
+template <int DT, int BITS>
+cudaError_t forward_rows(const LnForward &a, cudaStream_t st) {
+    constexpr int NV = 16 / Elem<DT>::kVec, R = kRows<DT>;
+    const int size = threads_for(a.H / Elem<DT>::kVec, NV), groups = groups_of(size);
+    const int threads = size * groups;
+    const size_t smem = (size_t)kRing * R * NV * threads * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_forward_rows_kernel<DT, BITS, false>;
+    const cudaError_t e = allow_shared(kernel, (size_t)kRing * R * NV * 256 * 16, ready);
+    if (e != cudaSuccess) return e;
+    const int ctas = resident_ctas(kernel, threads, smem, (a.T + groups * R - 1) / (groups * R));
+    return launch_pdl_clusters(kernel, ctas, threads, 1, smem, st, a, size, 0);
+}
+
+template <int DT, int BITS>
+cudaError_t forward_rows_split(const LnForward &a, cudaStream_t st) {
+    constexpr int V = Elem<DT>::kVec, NV = 16 / V, R = kRows<DT>;
+    const Parts p(a.H, kForwardPart);
+    const int threads = threads_for(p.columns / V, NV);
+    const size_t smem = (size_t)kRing * R * NV * threads * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_forward_rows_kernel<DT, BITS, true>;
+    const cudaError_t e = allow_shared(kernel, (size_t)kRing * R * NV * 256 * 16, ready);
+    if (e != cudaSuccess) return e;
+    const int clusters = resident_clusters(kernel, threads, smem, p.count, (a.T + R - 1) / R);
+    return launch_pdl_clusters(kernel, clusters * p.count, threads, p.count, smem, st, a, threads,
+                               p.columns);
+}
 
 // Dynamic shared memory of the kernels for any alignment may reach this.
 constexpr size_t kMostShared = 220 * 1024;
 
-// CTAs of the kernels for any alignment: a multiple of eight where one takes several
-// rows, so that its rows start at the same place between 16-byte boundaries.
-template <typename K>
-int any_ctas(K kernel, int threads, size_t smem, int64_t T, int most) {
-    int n = resident_ctas(kernel, threads, smem, T);
+// CTAs (clusters) of the kernels for any alignment: a multiple of eight where one takes
+// several rows, so that its rows start at the same place between 16-byte boundaries.
+int by_eights(int n, int64_t T, int most) {
     if (n > most) n = most;
     return n >= T ? n : n > 8 ? n / 8 * 8 : 8;
 }
@@ -1220,34 +1348,48 @@ cudaError_t forward_any(const LnForward &a, cudaStream_t st) {
     const int threads = (slots + 32 * NV - 1) / (32 * NV) * 32;
     const size_t smem = (size_t)(kAnyStages + 2) * slots * 16;
     static bool ready[kMaxDevices];
-    auto kernel = ln_forward_any_kernel<DT, NV>;
+    auto kernel = ln_forward_any_kernel<DT, NV, false>;
     const cudaError_t e = allow_shared(kernel, kMostShared, ready);
     if (e != cudaSuccess) return e;
-    return launch_pdl_clusters(kernel, any_ctas(kernel, threads, smem, a.T, 1 << 20), threads, 1,
-                               smem, st, a);
+    const int n = by_eights(resident_ctas(kernel, threads, smem, a.T), a.T, 1 << 20);
+    return launch_pdl_clusters(kernel, n, threads, 1, smem, st, a, 0);
 }
 
-// The kernel for the rows: whole vectors, 16 elements a thread for rows of up to 4096
-// (w and b in registers too), 32 up to 64 KB; any alignment where five rows fit
-// shared memory; else element by element.
+template <int DT>
+cudaError_t forward_any_split(const LnForward &a, cudaStream_t st) {
+    constexpr int NV = 32 / Elem<DT>::kVec;
+    const Parts p(a.H, kAnyPart<DT>);
+    const int slots = row_slots<DT>(p.columns);
+    const int threads = (slots + 32 * NV - 1) / (32 * NV) * 32;
+    const size_t smem = (size_t)(kAnyStages + 2) * slots * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_forward_any_kernel<DT, NV, true>;
+    const cudaError_t e = allow_shared(kernel, kMostShared, ready);
+    if (e != cudaSuccess) return e;
+    const int n = by_eights(resident_clusters(kernel, threads, smem, p.count, a.T), a.T, 1 << 20);
+    return launch_pdl_clusters(kernel, n * p.count, threads, p.count, smem, st, a, p.columns);
+}
+
+// The kernel for the rows: of whole vectors at 16-byte boundaries, of any alignment (each
+// in parts where long), else (the longest) element by element.
 template <int DT, int BITS>
 cudaError_t forward_bits(const LnForward &a, cudaStream_t st) {
     constexpr int V = Elem<DT>::kVec;
     if (on16(a.x, a.ldx, Elem<DT>::kSize) && on16(a.y, a.ldy, Elem<DT>::kSize) && a.H % V == 0) {
-        if (a.H <= 4096) return forward_rows<DT, BITS, 16 / V, 256>(a, st);
-        if (a.H <= 8192) return forward_rows<DT, BITS, 32 / V, 256>(a, st);
-        if (a.H <= kLongRow / Elem<DT>::kSize) return forward_rows<DT, BITS, 32 / V, 1024>(a, st);
+        if (a.H <= kForwardRows) return forward_rows<DT, BITS>(a, st);
+        if (a.H <= kMaxParts * kForwardPart) return forward_rows_split<DT, BITS>(a, st);
     }
-    if (a.H <= 16384 - V && (size_t)(kAnyStages + 2) * row_slots<DT>((int)a.H) * 16 <= kMostShared)
-        return forward_any<DT>(a, st);
+    if (a.H <= kForwardAny<DT>) return forward_any<DT>(a, st);
+    if (a.H <= kMaxParts * kAnyPart<DT>) return forward_any_split<DT>(a, st);
     return launch_pdl(ln_forward_kernel<DT>, grid_for(a.T, 8), kThreads, 0, st, a.x, a.ldx, a.w, a.b,
                       a.param_f32, a.T, a.H, a.eps, a.y, a.ldy, a.mean, a.rstd);
 }
 
 // Where dw or db is wanted, the partial sums of P CTAs become dw and db.
+template <bool SPLIT = false>
 cudaError_t join(const LnBackward &a, int P, cudaStream_t st) {
     if (!a.dw && !a.db) return cudaSuccess;
-    return launch_pdl(ln_backward_join_kernel, grid_for((2 * a.H + 31) / 32, 8), kThreads, 0, st,
+    return launch_pdl(ln_backward_join_kernel<SPLIT>, grid_for((2 * a.H + 31) / 32, 8), kThreads, 0, st,
                       a.workspace, a.H, P, a.dw, a.db);
 }
 
@@ -1263,13 +1405,31 @@ cudaError_t backward_rows(const LnBackward &a, cudaStream_t st) {
     constexpr int kSlots = kBackStages * R * NV * (BITS ? 1 : 2);
     const size_t smem = (size_t)kSlots * threads * 16;
     static bool ready[kMaxDevices];
-    auto kernel = ln_backward_rows_kernel<DT, BITS>;
+    auto kernel = ln_backward_rows_kernel<DT, BITS, false>;
     const cudaError_t e = allow_shared(kernel, (size_t)kSlots * 512 * 16, ready);
     if (e != cudaSuccess) return e;
     int P = resident_ctas(kernel, threads, smem, (a.T + groups * R - 1) / (groups * R));
     if (P > ln_partials(a.T, a.H)) P = ln_partials(a.T, a.H);
-    const cudaError_t r = launch_pdl_clusters(kernel, P, threads, 1, smem, st, a, size);
+    const cudaError_t r = launch_pdl_clusters(kernel, P, threads, 1, smem, st, a, size, 0);
     return r != cudaSuccess ? r : join(a, P, st);
+}
+
+template <int DT, int BITS>
+cudaError_t backward_rows_split(const LnBackward &a, cudaStream_t st) {
+    constexpr int V = Elem<DT>::kVec, NV = 16 / V, R = kBackRows<DT>;
+    const Parts p(a.H, kBackwardPart);
+    const int threads = threads_for(p.columns / V, NV);
+    constexpr int kSlots = kBackStages * R * NV * (BITS ? 1 : 2);
+    const size_t smem = (size_t)kSlots * threads * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_backward_rows_kernel<DT, BITS, true>;
+    const cudaError_t e = allow_shared(kernel, (size_t)kSlots * 256 * 16, ready);
+    if (e != cudaSuccess) return e;
+    int P = resident_clusters(kernel, threads, smem, p.count, (a.T + R - 1) / R);
+    if (P > ln_partials(a.T, a.H)) P = ln_partials(a.T, a.H);
+    const cudaError_t r =
+        launch_pdl_clusters(kernel, P * p.count, threads, p.count, smem, st, a, threads, p.columns);
+    return r != cudaSuccess ? r : join<true>(a, P, st);
 }
 
 template <int DT, int LIMIT>
@@ -1279,27 +1439,45 @@ cudaError_t backward_any(const LnBackward &a, cudaStream_t st) {
     const int threads = (slots + 32 * NV - 1) / (32 * NV) * 32;
     const size_t smem = (size_t)(2 * kAnyStages + 2) * slots * 16;
     static bool ready[kMaxDevices];
-    auto kernel = ln_backward_any_kernel<DT, LIMIT>;
+    auto kernel = ln_backward_any_kernel<DT, LIMIT, false>;
     const cudaError_t e = allow_shared(kernel, kMostShared, ready);
     if (e != cudaSuccess) return e;
-    const int P = any_ctas(kernel, threads, smem, a.T, ln_partials(a.T, a.H));
-    const cudaError_t r = launch_pdl_clusters(kernel, P, threads, 1, smem, st, a);
+    const int P = by_eights(resident_ctas(kernel, threads, smem, a.T), a.T, ln_partials(a.T, a.H));
+    const cudaError_t r = launch_pdl_clusters(kernel, P, threads, 1, smem, st, a, 0);
     return r != cudaSuccess ? r : join(a, P, st);
 }
 
-// Whole vectors and any alignment for rows of up to 8192 (16 elements a thread: more
-// would not leave registers for dw and db), any alignment from a tensor only and where
-// eight rows fit shared memory; else element by element.
+template <int DT>
+cudaError_t backward_any_split(const LnBackward &a, cudaStream_t st) {
+    constexpr int NV = 16 / Elem<DT>::kVec;
+    const Parts p(a.H, kAnyPart<DT>);
+    const int slots = row_slots<DT>(p.columns);
+    const int threads = (slots + 32 * NV - 1) / (32 * NV) * 32;
+    const size_t smem = (size_t)(2 * kAnyStages + 2) * slots * 16;
+    static bool ready[kMaxDevices];
+    auto kernel = ln_backward_any_kernel<DT, 320, true>;
+    const cudaError_t e = allow_shared(kernel, kMostShared, ready);
+    if (e != cudaSuccess) return e;
+    const int P = by_eights(resident_clusters(kernel, threads, smem, p.count, a.T), a.T,
+                            ln_partials(a.T, a.H));
+    const cudaError_t r = launch_pdl_clusters(kernel, P * p.count, threads, p.count, smem, st, a, p.columns);
+    return r != cudaSuccess ? r : join<true>(a, P, st);
+}
+
+// As the forward pass; any alignment from a tensor only.
 template <int DT, int BITS>
 cudaError_t backward(const Input<DT, BITS> &in, const LnBackward &a, cudaStream_t st) {
     constexpr int kSize = Elem<DT>::kSize, V = Elem<DT>::kVec;
     if ((BITS || on16(a.x, a.ldx, kSize)) && on16(a.dy, a.lddy, kSize) && on16(a.dx, a.lddx, kSize) &&
-        a.H % V == 0 && a.H <= 8192)
-        return backward_rows<DT, BITS>(a, st);
+        a.H % V == 0) {
+        if (a.H <= kBackwardRows) return backward_rows<DT, BITS>(a, st);
+        if (a.H <= kMaxParts * kBackwardPart) return backward_rows_split<DT, BITS>(a, st);
+    }
     if constexpr (BITS == 0) {
-        // (rows of up to 5112 leave registers for two CTAs an SM)
-        if (a.H <= 8192 - V && (size_t)(2 * kAnyStages + 2) * row_slots<DT>((int)a.H) * 16 <= kMostShared)
-            return a.H <= 5120 - V ? backward_any<DT, 320>(a, st) : backward_any<DT, 512>(a, st);
+        // (rows of up to 4992 leave registers for two CTAs an SM)
+        if (a.H <= 4992) return backward_any<DT, 320>(a, st);
+        if (a.H <= kBackwardAny<DT>) return backward_any<DT, 512>(a, st);
+        if (a.H <= kMaxParts * kAnyPart<DT>) return backward_any_split<DT>(a, st);
     }
     const bool sums = a.dw || a.db;
     const int P = sums ? ln_partials(a.T, a.H) : grid_for(a.T, 8);
@@ -1330,7 +1508,7 @@ cudaError_t launch_ln_forward(const LnForward &a, cudaStream_t st) {
     if (a.dtype == kF16) return forward_bits<kF16, 0>(a, st);
     if (!a.codes) return forward_bits<kBF16, 0>(a, st);
     // y may be x's place: rows that the norm does not quantize are quantized first
-    const bool rows = on16(a.x, a.ldx, 2) && on16(a.y, a.ldy, 2) && a.H <= kLongRow / 2;
+    const bool rows = on16(a.x, a.ldx, 2) && on16(a.y, a.ldy, 2) && a.H <= kMaxParts * kForwardPart;
     if (!rows) {
         const cudaError_t e = a.bits == 4   ? codes<4>(a, st)
                               : a.bits == 5 ? codes<5>(a, st)

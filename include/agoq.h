@@ -1,6 +1,8 @@
 /*
- * agoq.h -- C ABI of libagoq.so: the AGoQ element-wise quantization kernels
- * and the INT4-dequant-fused weight-gradient GEMM, for NVIDIA GB300 (sm_103a).
+ * agoq.h -- C ABI of libagoq.so: the AGoQ element-wise quantization kernels,
+ * the INT4-dequant-fused weight-gradient GEMM, and the output end of a training
+ * step around them (layer norm, loss and log probabilities of tokens, gradient
+ * norm and clipping), for NVIDIA GB300 (sm_103a).
  *
  * Method: "AGoQ: Activation and Gradient Quantization for Memory-Efficient
  * Distributed Training of LLMs" (gist.science summary page), sections
@@ -32,8 +34,11 @@
  *   - Arguments are validated before anything is launched.  On any error the
  *     call returns a non-zero status and touches no buffer.
  *   - n counts elements; n must be a multiple of 128 (ragged tails are not
- *     supported: AGOQ_ERR_SHAPE); n == 0 is a valid no-op.
+ *     supported: AGOQ_ERR_SHAPE); n == 0 is a valid no-op.  The calls from
+ *     agoq_layernorm_forward on take rows of any length.
  *   - Data pointers must be 16-byte aligned (AGOQ_ERR_ALIGN); scale arrays 4-byte.
+ *     From agoq_layernorm_forward on, tensors need the alignment of their
+ *     elements only; codes and workspaces 16 bytes.
  *   - Outputs must not overlap inputs (AGOQ_ERR_ALIAS), except where a call is
  *     documented as in place.
  *   - Inputs must be finite; NaN or infinite inputs give unspecified codes.
@@ -362,10 +367,14 @@ agoq_status agoq_fwd_gemm_quant(const void *x_bf16, const void *w_bf16, int T, i
 agoq_status agoq_dbca_pp_bits(int stages, int microbatches, int base_bits, int *bits);
 
 /*
- * Layer norm, forward.  Per row of x [T][H], in binary32 (the variance from the
- * differences to the mean, not from the sum of squares):
+ * Layer norm, forward.  Per row of x [T][H], in binary32:
  *   mu = sum_i x[i] / H;  r = 1 / sqrt(sum_i (x[i] - mu)^2 / H + eps);
  *   y[i] = R(((x[i] - mu) * r) * w[i] + b[i]),  R rounding to the type of y.
+ * The variance is taken from the sum of squares where mu^2 is at most the variance
+ * (the subtraction then costs one bit), and from a second pass over the differences
+ * to the mean in every other row, so that a large common offset costs no accuracy.
+ * The divisions by H are products with the rounded 1/H, and r is the hardware's
+ * approximate reciprocal root (relative error below 2^-22).
  * With `codes` the same call also writes the LAAQ codes of x (exactly
  * agoq_quant_act(x, T*H, bits)): the low-bit input that a training step keeps
  * for agoq_layernorm_backward_laaq instead of x (AGoQ section 2.A,
@@ -378,12 +387,13 @@ agoq_status agoq_dbca_pp_bits(int stages, int microbatches, int base_bits, int *
  *   mean, rstd : out, FP32 [T] (mu and r), or NULL to skip either.
  *   codes, scales, bits : out, as agoq_quant_act writes them (codes 16-byte
  *            aligned; then x must be BF16 and H a multiple of 128), or both NULL.
- * 1 <= H <= 2^24; T may be 0.  x, w, b and y need the alignment of their
- * elements only; rows whose addresses are all 16-byte aligned move in 16-byte
- * accesses, others element by element (slower, the same values).  y must not
- * overlap x except in place (the same address and row distance; not with codes
- * being anywhere else than outside of both); the outputs must not overlap one
- * another.  A row with a NaN or an infinity is NaN throughout.
+ * 1 <= H <= 2^24; T may be 0.  x, w, b and y need the alignment of their elements
+ * only.  Rows of up to 32768 elements (of up to 27648 where a row or a row distance is
+ * not 16-byte aligned) move in 16-byte accesses, longer ones element by element.  The
+ * output of either is within the same bounds, not the same bits.
+ * y must not overlap x except in place (the same address and row distance), and
+ * the outputs must not overlap one another.  A row with a NaN or an infinity is NaN
+ * throughout.
  */
 agoq_status agoq_layernorm_forward(const void *x, int64_t ldx, const void *w, const void *b,
                                    int param_dtype, int64_t T, int64_t H, int dtype, float eps,

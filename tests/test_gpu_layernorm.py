@@ -99,6 +99,49 @@ def test_strides_and_alignment(dtype, H, pad, shift):
                     *agoq.agoq_layernorm_backward(x, dy, mean, rstd, w, dx=dx))
 
 
+# Rows that one CTA does not hold: of whole vectors and of any alignment, from the first
+# such length to the last, and beyond; few rows, and more than the GPU takes at a time.
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T,H,pad", [(3, 8200, 0), (301, 12296, 8), (2, 32768, 0), (2, 32776, 0),
+                                     (5, 4999, 0), (3, 8065, 3), (307, 11137, 2), (3, 16257, 0),
+                                     (2, 27651, 1), (2, 39937, 0), (1300, 9001, 0)])
+def test_long_rows(dtype, T, H, pad):
+    x, dy = _rand((T, H), dtype, 31, 1.5, 0.5), _rand((T, H), dtype, 32)
+    x[T - 1] += 50                                       # a row whose mean is far off 0
+    if pad:
+        x, dy = _strided(x, pad), _strided(dy, pad, 1)
+    w, b = _params(("none", "same", "f32")[H % 3], dtype, H)
+    y, mean, rstd, _, _ = agoq.agoq_layernorm_forward(x, w, b, EPS)
+    _check_forward(x, w, b, y, mean, rstd)
+    got = agoq.agoq_layernorm_backward(x, dy, mean, rstd, w)
+    _check_backward(x, dy, w, mean, rstd, *got)
+    again = agoq.agoq_layernorm_backward(x, dy, mean, rstd, w)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))        # sums in a fixed order
+    if pad == 0:
+        agoq.agoq_layernorm_backward(x, dy, mean, rstd, w, dx=dy)
+        assert torch.equal(dy, got[0])
+        agoq.agoq_layernorm_forward(x, w, b, EPS, y=x)
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("bits", [4, 5, 6, 8])
+@pytest.mark.parametrize("T,H", [(3, 8320), (330, 12288), (2, 32768), (1, 32896)])
+def test_codes_of_long_rows(bits, T, H):
+    x = _rand((T, H), BF16, 33, 2.0, 0.2)
+    x[T - 1] += 30                                       # a row whose mean is far off 0
+    w, b = _params("same", BF16, H)
+    y, mean, rstd, codes, scales = agoq.agoq_layernorm_forward(x, w, b, EPS, bits=bits)
+    _check_forward(x, w, b, y, mean, rstd)
+    qc, qs = agoq.agoq_quant_act(x, bits)
+    assert torch.equal(codes, qc) and torch.equal(scales, qs)
+    kept = agoq.agoq_dequant_act(codes, scales, T * H, bits).view(T, H)
+    dy = _rand((T, H), BF16, 34)
+    got = agoq.agoq_layernorm_backward_laaq(codes, scales, bits, dy, EPS, w)
+    k64 = kept.double()
+    _, mu, r = P.layernorm(k64, None, None, EPS)
+    _check_backward(kept, dy, w, mu, r, *got, *P.stats_bounds(k64, EPS))
+
+
 def test_nothing_outside_the_outputs():
     T, H = 37, 1000
     x, dy = _rand((T, H), F16, 5), _rand((T, H), F16, 6)
