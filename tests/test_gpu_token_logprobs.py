@@ -44,7 +44,12 @@ def _close(got, want, bound, what):
 
 
 def _check(x, tokens, k):
-    logp, ent, lse, top_logp, top_ids = agoq.agoq_token_logprobs(x, tokens, k=k)
+    _check_rows(x, tokens, k, slice(None), agoq.agoq_token_logprobs(x, tokens, k=k))
+
+
+def _check_rows(x, tokens, k, rows, got):
+    logp, ent, lse, top_logp, top_ids = (v if v is None else v[rows] for v in got)
+    x, tokens = x[rows], tokens[rows]
     x64 = x.double()
     ep, ee, el, logs = P.token_logprobs(x64, tokens)
     blogp, bent, blse = P.token_bounds(x64, logs, el)
@@ -68,6 +73,43 @@ VOCABS = [(3, 1), (5, 2), (4, 7), (9, 33), (3, 257), (2, 1000), (7, 4099), (5, 3
 @pytest.mark.parametrize("T,V", VOCABS)
 def test_values_and_alternatives(dtype, T, V):
     _check(_logits(T, V, dtype, 1), _tokens(T, V), min(V, (0, 1, 5, 20, 32)[(T + V) % 5]))
+
+
+# Around the lengths at which a warp holds more vectors, or a CTA takes the row, from any
+# start; the rows differ in kind: masked, equal, ascending, with one NaN or +inf.
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("V", [3, 31, 63, 250, 256, 505, 509, 1017, 1018, 2033, 2041, 2042, 4081,
+                               4082, 4090])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (3, 1)])
+def test_short_rows(dtype, V, pad, shift):
+    x = _logits(70, V, dtype, 41, pad=pad, shift=shift)
+    x[1] = -math.inf
+    x[2, V // 3:] = -math.inf
+    x[3, ::2] = torch.finfo(dtype).min
+    x[4] = 1.5
+    x[5] = torch.arange(V, device="cuda").div(64, rounding_mode="floor").to(dtype)
+    x[6, V // 2] = math.nan
+    x[7, V - 1] = math.inf
+    tokens = _tokens(70, V)
+    tokens[2], tokens[8] = 0, -100
+    good = [i for i in range(70) if i not in (6, 7)]
+    for k in {0, 1, min(V, 17), min(V, 32)}:
+        got = agoq.agoq_token_logprobs(x, tokens, k=k)
+        assert all(bool(torch.isnan(v[6:8]).all()) for v in got[:3])
+        if k:
+            assert torch.equal(got[4][6:8], P.top(x[6:8].double(), k))
+        _check_rows(x, tokens, k, good, got)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("V", [1, 2041, 2042, 4090, 8190, 16380])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (5, 3)])
+def test_loss_of_short_rows(dtype, V, pad, shift):
+    x, tokens = _logits(300, V, dtype, 42, pad=pad, shift=shift), _tokens(300, V)
+    x[1, V // 3:] = -math.inf
+    tokens[1], tokens[2] = 0, -100
+    w = torch.rand(300, device="cuda") + 0.1
+    _check_loss(x, tokens, w, *agoq.agoq_token_loss(x, tokens, w))
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
