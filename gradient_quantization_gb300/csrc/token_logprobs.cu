@@ -273,11 +273,11 @@ struct Slice {
 // again: elements above the bound and equal to it in two lists, of the equal ones the
 // first in order; and where even the former are too many, the k largest one by one.
 //
-// 2048 x 128000 BF16 with 20 alternatives: 112 us (4.7 TB/s), without them 91 us.  Bound by
+// 2048 x 128000 BF16 with 20 alternatives: 108 us (4.9 TB/s), without them 91 us.  Bound by
 // instruction issue (72%: the exponential, its two sums and the maximum of each element)
-// and by the last round, since 2048 rows on 912 CTAs are 2.25 rounds (2280 rows take 113
-// us).  128 threads and six CTAs an SM, so that one CTA's end of a row hides behind
-// another's stream: 8208 x 32000 155 us, 190 us with 256 threads and three.
+// and by the last round, since 2048 rows on 912 CTAs are 2.25 rounds.  128 threads and six
+// CTAs an SM, so that one CTA's end of a row hides behind another's stream (8208 x 32000
+// 155 us, with 256 threads and three 190 us, before the bound was found by bits; now 144).
 constexpr int kStatThreads = 128, kStatWarps = kStatThreads / 32;
 constexpr int kBatch = 4;                     // vectors a thread and stage
 constexpr int kStages = 3;                    // of shared memory, each thread's own
@@ -287,11 +287,11 @@ constexpr int kTopMax = 32;
 constexpr int kWarpList = 128;                // candidate vectors of a warp
 constexpr int kList = kWarpList * kStatWarps, kShortList = 256;
 constexpr int kMaxCluster = 8;
-static_assert(kTopMax <= kGroups && kMaxCluster * kTopMax <= kShortList && 3 * kShortList <= 2 * kList,
+static_assert(kTopMax <= kGroups && kGroups == 64 && kMaxCluster * kTopMax <= kShortList && 3 * kShortList <= 2 * kList,
               "lists hold what they must");
 
 struct StatShared {
-    float groups[kGroups];        // 16-byte aligned
+    uint32_t groups[kGroups];     // ordered() of the largest element of each; 16-byte aligned
     Sums warps[kStatWarps];
     Sums slice;                   // of the CTA's slice
     float bound;
@@ -311,30 +311,55 @@ struct StatShared {
     uint4 ring[kStages][kBatch][kStatThreads];
 };
 
-__device__ __forceinline__ float key_value(uint64_t key) {
-    const uint32_t k = (uint32_t)(key >> 32);
-    return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
-}
 __device__ __forceinline__ uint32_t key_index(uint64_t key) { return 0xFFFFFFFFu - (uint32_t)key; }
 
-// sh.bound: the want-th largest maximum of the groups, whose threads hold `most`.
+// A float's place in the order of its values, and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// sh.bound: the want-th largest maximum of the groups, whose threads hold `most`.  Of the
+// 16-bit types, whose values as binary32 differ in the upper 16 (BF16) or 19 bits only, one
+// warp finds it bit by bit, each time counting the maxima that reach the bits so far; of
+// FP32 a thread a group counts the larger ones.  (2048 x 128000 BF16 108 us, counting 113
+// us; 8208 x 32000 144 us, 155 us; 2048 x 64000 FP32 106 us, counting 101 us.)
+template <int DT>
 __device__ __forceinline__ void find_bound(float most, int want, StatShared &sh) {
 #pragma unroll
     for (int o = 1; o < kGroupLanes; o <<= 1)
         most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-    if (threadIdx.x % kGroupLanes == 0) sh.groups[threadIdx.x / kGroupLanes] = most;
+    if (threadIdx.x % kGroupLanes == 0) sh.groups[threadIdx.x / kGroupLanes] = ordered(most);
     __syncthreads();
-    if (threadIdx.x < kGroups) {
-        const float g = sh.groups[threadIdx.x];
-        int larger = 0;
+    if constexpr (DT == kF32) {
+        if (threadIdx.x < kGroups) {
+            const uint32_t g = sh.groups[threadIdx.x];
+            int larger = 0;
 #pragma unroll
-        for (int i = 0; i < kGroups; i += 4) {
-            const float4 o = *reinterpret_cast<const float4 *>(sh.groups + i);
-            const int me = threadIdx.x;
-            larger += (o.x > g || (o.x == g && i < me)) + (o.y > g || (o.y == g && i + 1 < me)) +
-                      (o.z > g || (o.z == g && i + 2 < me)) + (o.w > g || (o.w == g && i + 3 < me));
+            for (int i = 0; i < kGroups; i += 4) {
+                const uint4 o = *reinterpret_cast<const uint4 *>(sh.groups + i);
+                const int me = threadIdx.x;
+                larger += (o.x > g || (o.x == g && i < me)) + (o.y > g || (o.y == g && i + 1 < me)) +
+                          (o.z > g || (o.z == g && i + 2 < me)) + (o.w > g || (o.w == g && i + 3 < me));
+            }
+            if (larger == want - 1) sh.bound = from_ordered(g);
         }
-        if (larger == want - 1) sh.bound = g;
+    } else if (threadIdx.x < 32) {
+        constexpr int kLow = DT == kBF16 ? 16 : 13;
+        const uint32_t a = sh.groups[threadIdx.x], b = sh.groups[threadIdx.x + 32];
+        uint32_t key = 0;
+#pragma unroll
+        for (int bit = 31; bit >= kLow; --bit) {
+            const uint32_t next = key | 1u << bit;
+            const int reach = __popc(__ballot_sync(0xFFFFFFFFu, a >= next)) +
+                              __popc(__ballot_sync(0xFFFFFFFFu, b >= next));
+            if (reach >= want) key = next;
+        }
+        if (!(key & 0x80000000u)) key |= (1u << kLow) - 1u;
+        if (threadIdx.x == 0) sh.bound = from_ordered(key);
     }
     __syncthreads();
 }
@@ -563,7 +588,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const Toke
             const float vm = word_max<DT>(all);
             // a bound from the first batch, from the first 4, 16, 64, ...
             if (want && (b == 0 || ((b & (b - 1)) == 0 && (b & 0x55555554)))) {
-                find_bound(b == 0 ? vm : word_max<DT>(most), want, sh);
+                find_bound<DT>(b == 0 ? vm : word_max<DT>(most), want, sh);
                 bound = fmaxf(sh.bound, kLowest);
             }
             most = max_word<DT>(most, all);
@@ -594,7 +619,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const Toke
         }
         const Sums mine = warp_join(sums.sums());
         if (lane == 0) sh.warps[warp] = mine;
-        if (want) find_bound(word_max<DT>(most), want, sh);
+        if (want) find_bound<DT>(word_max<DT>(most), want, sh);
         else __syncthreads();
         Sums all = warp_join(lane < kStatWarps ? sh.warps[lane] : Sums{kLowest, 0.0f, 0.0f});
         if (want) {
@@ -680,7 +705,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const Toke
             }
             if (threadIdx.x < want) {
                 const uint64_t key = sh.top[threadIdx.x];
-                const float x = key_value(key);
+                const float x = from_ordered((uint32_t)(key >> 32));
                 a.top_ids[t * want + threadIdx.x] = key_index(key);
                 a.top_logp[t * want + threadIdx.x] =
                     x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), ls);
@@ -825,7 +850,7 @@ __global__ void __launch_bounds__(kShortWarps * 32) token_stats_short_kernel(con
         }
         if (lane < want) {
             const uint64_t key = top[lane];
-            const float x = key_value(key);
+            const float x = from_ordered((uint32_t)(key >> 32));
             a.top_ids[t * want + lane] = key_index(key);
             a.top_logp[t * want + lane] = x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), ls);
         }
