@@ -274,7 +274,7 @@ struct Slice {
 // first in order; and where even the former are too many, the k largest one by one.
 //
 // 2048 x 128000 BF16 with 20 alternatives: 108 us (4.9 TB/s), without them 91 us.  Bound by
-// instruction issue (72%: the exponential, its two sums and the maximum of each element)
+// instruction issue (71%: the exponential, its two sums and the maximum of each element)
 // and by the last round, since 2048 rows on 912 CTAs are 2.25 rounds.  128 threads and six
 // CTAs an SM, so that one CTA's end of a row hides behind another's stream (8208 x 32000
 // 155 us, with 256 threads and three 190 us, before the bound was found by bits; now 144).
