@@ -345,7 +345,7 @@ ln_forward_rows_kernel(const LnForward a, int size, int part) {
     for (int64_t t0 = first; t0 < a.T; t0 += step) {
         const int64_t t = t0 + g.id * R;
         copies_left<kStages - 2>();
-        // the row's vector i (beyond T: of an earlier row; nothing of it is kept)
+        // the row's vector i (beyond T: whatever the slot holds; nothing of it is kept)
         auto load = [&](int r, int i) { return load_shared(from + (r * NV + i) * slot_bytes); };
         bool row[R];
 #pragma unroll
@@ -367,10 +367,16 @@ ln_forward_rows_kernel(const LnForward a, int size, int part) {
         row_sums(s, mine[half], g);
         half ^= 1;
         if constexpr (SPLIT) parts_sums(s, box1, turn1, c);
-        bool stand = true;
+        // A row takes the second pass for its own moments alone: what shares a step or a warp
+        // with it may cost time, but not bits, and slots of rows beyond T (an earlier row's, or
+        // never written) count for nothing.  The same for all threads of a group.
+        bool stand[R], none = true;
 #pragma unroll
-        for (int r = 0; r < R; ++r) stand &= moments(s[2 * r], s[2 * r + 1], inv, mu[r], var[r]);
-        if (__any_sync(0xFFFFFFFFu, !stand)) {      // the same for all threads of a group
+        for (int r = 0; r < R; ++r) {
+            stand[r] = moments(s[2 * r], s[2 * r + 1], inv, mu[r], var[r]) || !row[r];
+            none &= stand[r];
+        }
+        if (__any_sync(0xFFFFFFFFu, !none)) {
             float q[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -392,7 +398,8 @@ ln_forward_rows_kernel(const LnForward a, int size, int part) {
             half ^= 1;
             if constexpr (SPLIT) parts_sums(q, box2, turn2, c);
 #pragma unroll
-            for (int r = 0; r < R; ++r) var[r] = __fmul_rn(q[r], inv);
+            for (int r = 0; r < R; ++r)
+                if (!stand[r]) var[r] = __fmul_rn(q[r], inv);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
