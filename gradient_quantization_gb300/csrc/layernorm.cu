@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
         row_sums(s, mine[half], g);
         half ^= 1;
         if constexpr (SPLIT) parts_sums(s, box1, turn1, c);
-        bool stand = true;
+        bool stand[R], none = true;       // as in the forward pass, of each row by itself
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             s0[r] = __fmul_rn(s[kSums * r], inv);
@@ -968,13 +968,14 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
             if constexpr (BITS != 0) {
                 // sum g (x - mu) / H; the difference loses no more than the variance's
                 float var;
-                stand &= moments(s[kSums * r + 2], s[kSums * r + 3], inv, mu[r], var);
+                stand[r] = moments(s[kSums * r + 2], s[kSums * r + 3], inv, mu[r], var) || !row[r];
+                none &= stand[r];
                 s1[r] = __fmaf_rn(-mu[r], s0[r], s1[r]);
                 rs[r] = inv_sqrt(__fadd_rn(var, a.eps));
             }
         }
         if constexpr (BITS != 0) {
-            if (__any_sync(0xFFFFFFFFu, !stand)) {      // the same for all threads of a group
+            if (__any_sync(0xFFFFFFFFu, !none)) {       // the same for all threads of a group
                 float q[2 * R];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -1001,6 +1002,7 @@ __global__ void __launch_bounds__(512) ln_backward_rows_kernel(const LnBackward 
                 if constexpr (SPLIT) parts_sums(q, box2, turn2, c);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
+                    if (stand[r]) continue;
                     rs[r] = inv_sqrt(__fmaf_rn(q[2 * r], inv, a.eps));
                     s1[r] = __fmul_rn(q[2 * r + 1], inv);
                 }

@@ -62,3 +62,22 @@ def test_forward_after_other_calls(dtype, T, H):
             wanted = kept
         for i, (p, q) in enumerate(zip(kept, wanted)):
             assert all(torch.equal(a, b) for a, b in zip(p, q)), (offset, i)
+
+
+@pytest.mark.parametrize("bits", [4, 5, 6, 8])
+@pytest.mark.parametrize("H", [128, 256, 640, 4096, 8320])
+def test_backward_row_alone_from_codes(bits, H):
+    """dx of a row, and its terms of dw and db where all other rows' dy is 0 (sums with zeros
+    are exact)."""
+    T = 7
+    x = _rows(T, H, BF16, 4, 40.0)
+    dy, w = _rows(T, H, BF16, 5), _rows(1, H, BF16, 6)[0]
+    _, _, _, codes, scales = agoq.agoq_layernorm_forward(x, w, None, EPS, bits=bits)
+    codes, scales = codes.view(T, -1), scales.view(T, -1)
+    dx = agoq.agoq_layernorm_backward_laaq(codes, scales, bits, dy, EPS, w)[0]
+    for t in range(T):
+        only = torch.zeros_like(dy)
+        only[t] = dy[t]
+        _, dw, db = agoq.agoq_layernorm_backward_laaq(codes, scales, bits, only, EPS, w)
+        ax, aw, ab = agoq.agoq_layernorm_backward_laaq(codes[t], scales[t], bits, dy[t:t + 1], EPS, w)
+        assert torch.equal(dx[t:t + 1], ax) and torch.equal(dw, aw) and torch.equal(db, ab), t
