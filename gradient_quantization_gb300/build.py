@@ -34,7 +34,7 @@ UNITS = {
     "token_logprobs.cu": ["-fmad=false"],
 }
 HEADERS = ["agoq_device.cuh", "agoq_launch.h", "gemm_common.cuh", "wgrad_gemm_impl.cuh", "fwd_gemm_impl.cuh",
-           "typed_io.cuh"]
+           "typed_io.cuh", "row_units.h"]
 
 
 def _nvcc():

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/agoq.h"
+#include "row_units.h"
 
 namespace agoq {
 
@@ -153,7 +154,6 @@ struct LnBackward {
     float *dw, *db;
     float *workspace;        // ln_workspace_floats(T, H) floats if dw or db is wanted
 };
-int ln_partials(int64_t T, int64_t H);
 // Partial rows of dw and db.
 inline int64_t ln_workspace_floats(int64_t T, int64_t H) {
     return (int64_t)ln_partials(T, H) * 2 * H;

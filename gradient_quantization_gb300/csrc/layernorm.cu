@@ -13,6 +13,7 @@
 #include <cooperative_groups.h>
 
 #include "agoq_launch.h"
+#include "row_units.h"
 #include "typed_io.cuh"
 
 namespace agoq {
@@ -1353,13 +1354,6 @@ cudaError_t forward_rows_split(const LnForward &a, cudaStream_t st) {
 // Dynamic shared memory of the kernels for any alignment may reach this.
 constexpr size_t kMostShared = 220 * 1024;
 
-// CTAs (clusters) of the kernels for any alignment: a multiple of eight where one takes
-// several rows, so that its rows start at the same place between 16-byte boundaries.
-int by_eights(int n, int64_t T, int most) {
-    if (n > most) n = most;
-    return n >= T ? n : n > 8 ? n / 8 * 8 : 8;
-}
-
 // Rows of any alignment, 32 elements a thread (few warps a row: with 16 elements rows of
 // 5003 FP16 values took 51 us, with 32 38 us).
 template <int DT>
@@ -1516,13 +1510,6 @@ cudaError_t codes(const LnForward &a, cudaStream_t st) {
 }
 
 }  // namespace
-
-// Rows of partial sums of dw and db: at most two an SM of 152, and more of short rows,
-// whose CTAs are small (as many bytes as 304 rows of 4096 elements).
-int ln_partials(int64_t T, int64_t H) {
-    const int64_t fit = H < 4096 ? 4096 / H : 1, most = 304 * (fit < 8 ? fit : 8);
-    return (int)(T < most ? T : most);
-}
 
 cudaError_t launch_ln_forward(const LnForward &a, cudaStream_t st) {
     if (a.dtype == kF32) return forward_bits<kF32, 0>(a, st);
