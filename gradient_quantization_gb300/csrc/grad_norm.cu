@@ -190,12 +190,13 @@ __device__ __forceinline__ double square_part(const Entry &e, int64_t v0) {
     }
     const float s = __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
     if (sum_stands(s)) return (double)s;
-    // nothing but zeros (of either sign) is exact too
+    // nothing but zeros (of either sign) is exact too, unless a scale is not finite, which
+    // makes the sum NaN
     uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < kPart; ++i) any |= v[i].x | v[i].y | v[i].z | v[i].w;
     constexpr uint32_t kMagnitude = DT == kF32 ? 0x7FFFFFFFu : DT == kE4M3 ? 0x7F7F7F7Fu : 0x7FFF7FFFu;
-    if ((any & kMagnitude) == 0) return 0.0;
+    if (s == 0.0f && (any & kMagnitude) == 0) return 0.0;
     return exact_part(e, v0);
 }
 
