@@ -49,6 +49,13 @@ __device__ __forceinline__ float below_max(float x, float m) {
     return d;
 }
 
+// Log probability of a logit x, from the row's reference, its sum and the sum's logarithm.
+// (x = -inf in a row of nothing else would be a difference of infinities; in a row whose
+// statistics are NaN it is NaN like every other.)
+__device__ __forceinline__ float log_prob(float x, float ref, float sum, float ln) {
+    return x == -INFINITY && sum == sum ? x : __fsub_rn(__fsub_rn(x, ref), ln);
+}
+
 // The loss of rows too long for a cluster's shared memory: a CTA a row, every pass
 // reading the logits again.
 template <int DT>
@@ -69,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) token_loss_long_kernel(const TokenLo
         s = cta_sum<kWarps>(s, red[1]);
         const bool ignored = token < 0, beyond = token >= a.V, empty = s == 0.0f;
         if (threadIdx.x == 0 && a.logp) {
-            const float lp = at == -INFINITY ? at : __fsub_rn(__fsub_rn(at, m), logf(s));
+            const float lp = log_prob(at, m, s, logf(s));
             a.logp[t] = ignored ? 0.0f : beyond ? NAN : lp;
         }
         float w = a.weights ? a.weights[t] : 1.0f;
@@ -676,7 +683,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const Toke
                     // (rank 0's slice is the longest, and starts at -skip)
                     const int owner = C > 1 ? ((int)token - s.start) / N / s.n : 0;
                     const float x = cluster.map_shared_rank(&sh, owner)->token;
-                    lp = x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), ls);
+                    lp = log_prob(x, all.ref, all.sum, ls);
                 }
                 if (a.logp) a.logp[t] = lp;
                 if (a.entropy)
@@ -707,8 +714,7 @@ __global__ void __launch_bounds__(kStatThreads, 6) token_stats_kernel(const Toke
                 const uint64_t key = sh.top[threadIdx.x];
                 const float x = from_ordered((uint32_t)(key >> 32));
                 a.top_ids[t * want + threadIdx.x] = key_index(key);
-                a.top_logp[t * want + threadIdx.x] =
-                    x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), ls);
+                a.top_logp[t * want + threadIdx.x] = log_prob(x, all.ref, all.sum, ls);
             }
         }
         if (C > 1) cluster.sync();     // the leader has read this CTA's shared memory
@@ -842,7 +848,7 @@ __global__ void __launch_bounds__(kShortWarps * 32) token_stats_short_kernel(con
             float lp = 0.0f;
             if (token >= a.V) lp = NAN;
             else if (token >= 0)
-                lp = at_token == -INFINITY ? at_token : __fsub_rn(__fsub_rn(at_token, all.ref), ls);
+                lp = log_prob(at_token, all.ref, all.sum, ls);
             if (a.logp) a.logp[t] = lp;
             if (a.entropy)
                 a.entropy[t] = all.sum == 0.0f ? 0.0f : __fsub_rn(ls, __fdiv_rn(all.first, all.sum));
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(kShortWarps * 32) token_stats_short_kernel(con
             const uint64_t key = top[lane];
             const float x = from_ordered((uint32_t)(key >> 32));
             a.top_ids[t * want + lane] = key_index(key);
-            a.top_logp[t * want + lane] = x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), ls);
+            a.top_logp[t * want + lane] = log_prob(x, all.ref, all.sum, ls);
         }
         __syncwarp();                             // the lists are written again
     }
@@ -971,7 +977,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
         // the CTA that holds the token (the first one for a token outside)
         if (threadIdx.x == 0 && a.logp && (ignored || beyond ? rank == 0 : s.has(token))) {
             const float x = sh.token;
-            const float lp = x == -INFINITY ? x : __fsub_rn(__fsub_rn(x, all.ref), logf(all.sum));
+            const float lp = log_prob(x, all.ref, all.sum, logf(all.sum));
             a.logp[t] = ignored ? 0.0f : beyond ? NAN : lp;
         }
         float w = a.weights ? a.weights[t] : 1.0f;
