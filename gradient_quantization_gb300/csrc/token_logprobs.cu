@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(kThreads) token_loss_long_kernel(const TokenLo
             a.logp[t] = ignored ? 0.0f : beyond ? NAN : lp;
         }
         float w = a.weights ? a.weights[t] : 1.0f;
-        if (ignored || empty) w = 0.0f;
-        if (beyond) w = NAN;
+        if (beyond || s != s) w = NAN;                // 0 times a row of NaN is NaN too
+        if (ignored || (empty && !beyond)) w = 0.0f;
         char *out = elem_at<DT>(a.dlogits, t * a.ldd);
         for (int64_t i = threadIdx.x; i < a.V; i += kThreads) {
             const float x = load_now<DT>(row, i);
@@ -981,8 +981,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
             a.logp[t] = ignored ? 0.0f : beyond ? NAN : lp;
         }
         float w = a.weights ? a.weights[t] : 1.0f;
-        if (ignored || empty) w = 0.0f;
-        if (beyond) w = NAN;
+        if (beyond || all.sum != all.sum) w = NAN;    // 0 times a row of NaN is NaN too
+        if (ignored || (empty && !beyond)) w = 0.0f;
         const float scale = __fdiv_rn(w, all.sum);
         char *out = elem_at<DT>(a.dlogits, t * a.ldd);
         const int mine_token = s.has(token) ? (int)token : -1;

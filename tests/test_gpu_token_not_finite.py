@@ -44,3 +44,13 @@ def test_alternatives_of_probability_zero(dtype, V):
     _, _, _, top, ids = agoq.agoq_token_logprobs(x, tokens, k=4)
     assert ids[3].tolist() == [7, 0, 1, 2]                            # NaN, then -inf in order
     assert torch.isnan(top[1:4]).all() and torch.isfinite(top[[0, 4]]).all()
+
+
+@pytest.mark.parametrize("dtype,V", CASES)
+def test_a_weight_of_zero(dtype, V):
+    """0 times the probabilities of such a row is NaN; of any other row 0."""
+    x, tokens = _logits(V, dtype)
+    grad = agoq.agoq_token_loss(x, tokens, torch.zeros(5, device="cuda"))[1]
+    assert torch.isnan(grad[1:4]).all() and not grad[[0, 4]].any()
+    tokens[1:4] = -1
+    assert not agoq.agoq_token_loss(x, tokens)[1][1:4].any()          # ignored: 0
