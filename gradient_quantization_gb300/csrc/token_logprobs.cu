@@ -1148,15 +1148,14 @@ token_logprobs_backward_kernel(const TokenLogprobsBackward a, int tiles) {
             }
         }
         const int64_t token = a.tokens[t];
-        const float lse = a.lse[t];
-        float dl = a.dlogp[t], de = 0.0f, h = 0.0f;
+        float lse = a.lse[t], dl = a.dlogp[t], de = 0.0f, h = 0.0f;
         if (a.dentropy) {
             de = a.dentropy[t];
             h = a.entropy[t];
         }
-        const bool empty = lse == -INFINITY;
         if (token < 0) dl = 0.0f;
-        if (token >= a.V) dl = NAN;
+        if (token >= a.V) lse = NAN;              // a row of NaN, empty or not
+        const bool empty = lse == -INFINITY;
         // g = p (c0 + c1 l), l = x - lse
         const float c0 = -__fmaf_rn(de, h, dl), c1 = -de;
         const int at = token >= 0 && token < a.V ? (int)token : -1;
