@@ -395,12 +395,27 @@ F32, BF16, F16, E4M3 = 0, 1, 2, 3
 
 _empty = torch.empty
 _raw_stream = torch._C._cuda_getCurrentRawStream      # torch.cuda.current_stream() costs 2 us
+_current_device = torch._C._cuda_getDevice
+
+
+def _refuse(t, what, at):
+    """Raise for an operand that is not on the device `at` of the others."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % what)
+    raise ValueError("%s is on cuda:%d, the other operands are on cuda:%d"
+                     % (what, t.get_device(), at))
 
 
 def _launch(stream, device):
     """(handle, other) of a call's stream: other is None for torch's current stream, else the
-    stream to allocate on (see _new)."""
-    current = _raw_stream(device.index)
+    stream to allocate on (see _new).  The operands' device must be the current one: a handle
+    may mean another device's stream there (0 is every device's default stream), whose kernels
+    would meet foreign addresses."""
+    at = device.index
+    if at != _current_device():
+        raise ValueError("the operands are on cuda:%d, but the current device is cuda:%d (make the "
+                         "call within torch.cuda.device)" % (at, _current_device()))
+    current = _raw_stream(at)
     if stream is None:
         return current, None
     handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
@@ -419,11 +434,12 @@ def _new(other, shape, dtype, device):
         return _empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t, what, n=None, T=None, dtype=None):
-    """(address, rows, row length, row distance) of a CUDA tensor of FP32, BF16 or FP16
-    whose last dimension is contiguous: two-dimensional, or contiguous throughout."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % what)
+def _rows(t, what, n=None, T=None, dtype=None, at=None):
+    """(address, rows, row length, row distance) of a CUDA tensor (on device `at`, where given)
+    of FP32, BF16 or FP16 whose last dimension is contiguous: two-dimensional, or contiguous
+    throughout."""
+    if not isinstance(t, torch.Tensor) or (not t.is_cuda if at is None else t.get_device() != at):
+        _refuse(t, what, at)
     if t.dtype not in DTYPES or (dtype is not None and t.dtype != dtype):
         raise TypeError("%s must be %s, got %s" % (what, dtype or "float32, bfloat16 or float16",
                                                    t.dtype))
@@ -446,12 +462,12 @@ def _rows(t, what, n=None, T=None, dtype=None):
     return t.data_ptr(), rows, length, ld
 
 
-def _vector(t, n, what, dtypes):
-    """Address of a contiguous CUDA tensor of n elements (None: 0)."""
+def _vector(t, n, what, dtypes, at):
+    """Address of a contiguous tensor of n elements on device `at` (None: 0)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % what)
+    if not isinstance(t, torch.Tensor) or t.get_device() != at:
+        _refuse(t, what, at)
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
     if t.numel() != n or not t.is_contiguous():
@@ -467,13 +483,13 @@ def _out(t, n, other, shape, dtype, device, what):
     if t is None:
         t = _new(other, shape, dtype, device)
         return t, t.data_ptr()
-    return t, _vector(t, n, what, (dtype,))
+    return t, _vector(t, n, what, (dtype,), device.index)
 
 
-def _params(x_dtype, H, w, b=None):
+def _params(x_dtype, H, at, w, b=None):
     """(w, b, param_dtype): weight and bias of one type, FP32 or the activation's."""
     kinds = (torch.float32, x_dtype)
-    wp, bp = _vector(w, H, "w", kinds), _vector(b, H, "b", kinds)
+    wp, bp = _vector(w, H, "w", kinds, at), _vector(b, H, "b", kinds, at)
     if w is not None and b is not None and w.dtype != b.dtype:
         raise TypeError("w and b must have one type")
     ref = w if w is not None else b
@@ -487,14 +503,14 @@ def agoq_layernorm_forward(x, w=None, b=None, eps=1e-5, bits=0, y=None, mean=Non
     rows a multiple of 128).  Returns (y, mean, rstd, codes, scales); codes and scales are None
     for bits = 0, mean and rstd None unless given or wanted."""
     xp, T, H, ldx = _rows(x, "x")
-    wp, bp, pd = _params(x.dtype, H, w, b)
     dev = x.device
     handle, other = _launch(stream, dev)
+    wp, bp, pd = _params(x.dtype, H, dev.index, w, b)
     if y is None:
         y = _new(other, x.shape, x.dtype, dev)
         yp, ldy = y.data_ptr(), H
     else:
-        yp, _, _, ldy = _rows(y, "y", H, T, x.dtype)
+        yp, _, _, ldy = _rows(y, "y", H, T, x.dtype, dev.index)
     mp = rp = cp = sp = 0
     if mean is not None or want_stats:
         mean, mp = _out(mean, T, other, T, torch.float32, dev, "mean")
@@ -534,6 +550,8 @@ def _norm_sums(other, T, H, dev, dw, db, want_dw, want_db, workspace):
         return dw, db, workspace, wp, bp, workspace.data_ptr(), n
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
+    if workspace.get_device() != dev.index:
+        _refuse(workspace, "workspace", dev.index)
     return (dw, db, workspace, wp, bp, workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
 
@@ -543,20 +561,21 @@ def agoq_layernorm_backward(x, dy, mean, rstd, w=None, dx=None, dw=None, db=None
     """Layer norm backward from the input and its statistics: returns (dx, dw, db), dw and db
     FP32 (None unless given or wanted).  dx may be dy or x."""
     xp, T, H, ldx = _rows(x, "x")
-    dyp, _, _, lddy = _rows(dy, "dy", H, T, x.dtype)
-    wp, _, pd = _params(x.dtype, H, w)
     dev = x.device
+    at = dev.index
     handle, other = _launch(stream, dev)
+    dyp, _, _, lddy = _rows(dy, "dy", H, T, x.dtype, at)
+    wp, _, pd = _params(x.dtype, H, at, w)
     if dx is None:
         dx = _new(other, dy.shape, dy.dtype, dev)
         dxp, lddx = dx.data_ptr(), H
     else:
-        dxp, _, _, lddx = _rows(dx, "dx", H, T, x.dtype)
+        dxp, _, _, lddx = _rows(dx, "dx", H, T, x.dtype, at)
     dw, db, workspace, dwp, dbp, ws, nws = _norm_sums(other, T, H, dev, dw, db, want_dw, want_db,
                                                       workspace)
     rc = lib().agoq_layernorm_backward(
-        xp, ldx, dyp, lddy, wp, pd, _vector(mean, T, "mean", _F32),
-        _vector(rstd, T, "rstd", _F32), T, H, DTYPES[x.dtype], dxp, lddx, dwp, dbp, ws, nws,
+        xp, ldx, dyp, lddy, wp, pd, _vector(mean, T, "mean", _F32, at),
+        _vector(rstd, T, "rstd", _F32, at), T, H, DTYPES[x.dtype], dxp, lddx, dwp, dbp, ws, nws,
         handle)
     if rc:
         raise AgoqError(rc, "agoq_layernorm_backward")
@@ -568,20 +587,21 @@ def agoq_layernorm_backward_laaq(codes, scales, bits, dy, eps=1e-5, w=None, dx=N
     """Layer norm backward from the LAAQ codes of the input (statistics recomputed from the
     dequantized values): returns (dx, dw, db) as agoq_layernorm_backward."""
     dyp, T, H, lddy = _rows(dy, "dy", dtype=torch.bfloat16)
-    wp, _, pd = _params(dy.dtype, H, w)
     dev = dy.device
+    at = dev.index
     handle, other = _launch(stream, dev)
+    wp, _, pd = _params(dy.dtype, H, at, w)
     if dx is None:
         dx = _new(other, dy.shape, dy.dtype, dev)
         dxp, lddx = dx.data_ptr(), H
     else:
-        dxp, _, _, lddx = _rows(dx, "dx", H, T, dy.dtype)
+        dxp, _, _, lddx = _rows(dx, "dx", H, T, dy.dtype, at)
     dw, db, workspace, dwp, dbp, ws, nws = _norm_sums(other, T, H, dev, dw, db, want_dw, want_db,
                                                       workspace)
     blocks = T * H // BLOCK
     rc = lib().agoq_layernorm_backward_laaq(
-        _vector(codes, blocks * record_bytes(bits), "codes", (torch.uint8,)),
-        _vector(scales, blocks, "scales", _F32), bits, dyp, lddy, wp, pd, T, H, eps, dxp, lddx,
+        _vector(codes, blocks * record_bytes(bits), "codes", (torch.uint8,), at),
+        _vector(scales, blocks, "scales", _F32, at), bits, dyp, lddy, wp, pd, T, H, eps, dxp, lddx,
         dwp, dbp, ws, nws, handle)
     if rc:
         raise AgoqError(rc, "agoq_layernorm_backward_laaq")
@@ -609,22 +629,24 @@ class GradList:
             raise ValueError("outs must match grads")
         self.entries = (_GradTensor * max(1, len(grads)))()
         self.count = len(grads)
-        self.device = None
+        first = grads[0] if grads else None
+        first = first[0] if isinstance(first, tuple) else first
+        cuda = isinstance(first, torch.Tensor) and first.is_cuda
+        at = first.get_device() if cuda else _current_device()
         for e, g, o in zip(self.entries, grads, outs):
             codes, scales = g if isinstance(g, tuple) else (g, None)
             n = codes.numel() if isinstance(codes, torch.Tensor) else 0
             if scales is None:
-                e.data = _vector(codes, n, "gradient", tuple(DTYPES))
-                e.out = e.data if o is None else _vector(o, n, "out", (codes.dtype,))
+                e.data = _vector(codes, n, "gradient", tuple(DTYPES), at)
+                e.out = e.data if o is None else _vector(o, n, "out", (codes.dtype,), at)
                 e.dtype = DTYPES[codes.dtype]
             else:
-                e.data = _vector(codes, n, "codes", (torch.uint8,))
-                e.scales = _vector(scales, n // BLOCK, "scales", _F32)
-                e.out = e.scales if o is None else _vector(o, n // BLOCK, "out", _F32)
+                e.data = _vector(codes, n, "codes", (torch.uint8,), at)
+                e.scales = _vector(scales, n // BLOCK, "scales", _F32, at)
+                e.out = e.scales if o is None else _vector(o, n // BLOCK, "out", _F32, at)
                 e.dtype = E4M3
             e.n = n
-            self.device = self.device or codes.device
-        self.device = self.device or torch.device("cuda", torch.cuda.current_device())
+        self.device = torch.device("cuda", at)
         self.tensors = (grads, outs)
         _check(lib().agoq_grad_list_check(self.entries, self.count), "agoq_grad_list_check")
         self.workspace = torch.empty(
@@ -640,7 +662,8 @@ def agoq_grad_norm(grads, norm=None, stream=None):
     handle, other = _launch(stream, grads.device)
     if norm is None:
         norm = _new(other, 1, torch.float32, grads.device)
-    _check(lib().agoq_grad_norm(grads.entries, grads.count, _vector(norm, 1, "norm", _F32),
+    _check(lib().agoq_grad_norm(grads.entries, grads.count,
+                                _vector(norm, 1, "norm", _F32, grads.device.index),
                                 *grads._scratch(), handle), "agoq_grad_norm")
     return norm
 
@@ -650,7 +673,8 @@ def agoq_clip_grads(grads, max_norm, norm, stream=None):
     times min(1, max_norm / (norm + 1e-6)); of FP8 masters the scales alone change."""
     handle, other = _launch(stream, grads.device)
     _check(lib().agoq_clip_grads(grads.entries, grads.count, max_norm,
-                                 _vector(norm, 1, "norm", _F32), handle), "agoq_clip_grads")
+                                 _vector(norm, 1, "norm", _F32, grads.device.index), handle),
+           "agoq_clip_grads")
 
 
 def agoq_clip_grad_norm(grads, max_norm, norm=None, stream=None):
@@ -659,8 +683,8 @@ def agoq_clip_grad_norm(grads, max_norm, norm=None, stream=None):
     if norm is None:
         norm = _new(other, 1, torch.float32, grads.device)
     _check(lib().agoq_clip_grad_norm(grads.entries, grads.count, max_norm,
-                                     _vector(norm, 1, "norm", _F32), *grads._scratch(),
-                                     handle), "agoq_clip_grad_norm")
+                                     _vector(norm, 1, "norm", _F32, grads.device.index),
+                                     *grads._scratch(), handle), "agoq_clip_grad_norm")
     return norm
 
 
@@ -675,6 +699,7 @@ def agoq_token_logprobs(logits, tokens, k=0, want_entropy=True, logp=None, entro
     entropy is None unless given or wanted."""
     xp, T, V, ld = _rows(logits, "logits")
     dev = logits.device
+    at = dev.index
     handle, other = _launch(stream, dev)
     f32 = torch.float32
     logp, pp = _out(logp, T, other, T, f32, dev, "logp")
@@ -686,8 +711,8 @@ def agoq_token_logprobs(logits, tokens, k=0, want_entropy=True, logp=None, entro
         top_logp, tp = _out(top_logp, T * k, other, (T, k), f32, dev, "top_logp")
         top_ids, ip = _out(top_ids, T * k, other, (T, k), torch.int64, dev, "top_ids")
     rc = lib().agoq_token_logprobs(xp, ld, DTYPES[logits.dtype],
-                                   _vector(tokens, T, "tokens", _I64), T, V, k, pp, ep, lp, tp, ip,
-                                   handle)
+                                   _vector(tokens, T, "tokens", _I64, at), T, V, k, pp, ep, lp, tp,
+                                   ip, handle)
     if rc:
         raise AgoqError(rc, "agoq_token_logprobs")
     return logp, entropy, lse, top_logp, top_ids
@@ -698,16 +723,19 @@ def agoq_token_logprobs_backward(logits, tokens, lse, dlogp, entropy=None, dentr
     """Gradient of agoq_token_logprobs' logp (and entropy, with `dentropy`) -> dlogits of the
     logits' type; `dlogits` may be the logits themselves."""
     xp, T, V, ld = _rows(logits, "logits")
-    handle, other = _launch(stream, logits.device)
+    dev = logits.device
+    at = dev.index
+    handle, other = _launch(stream, dev)
     if dlogits is None:
-        dlogits = _new(other, logits.shape, logits.dtype, logits.device)
+        dlogits = _new(other, logits.shape, logits.dtype, dev)
         dp, ldd = dlogits.data_ptr(), V
     else:
-        dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
+        dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype, at)
     rc = lib().agoq_token_logprobs_backward(
-        xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64), T, V,
-        _vector(lse, T, "lse", _F32), _vector(entropy, T, "entropy", _F32),
-        _vector(dlogp, T, "dlogp", _F32), _vector(dentropy, T, "dentropy", _F32), dp, ldd, handle)
+        xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64, at), T, V,
+        _vector(lse, T, "lse", _F32, at), _vector(entropy, T, "entropy", _F32, at),
+        _vector(dlogp, T, "dlogp", _F32, at), _vector(dentropy, T, "dentropy", _F32, at), dp, ldd,
+        handle)
     if rc:
         raise AgoqError(rc, "agoq_token_logprobs_backward")
     return dlogits
@@ -718,15 +746,16 @@ def agoq_token_loss(logits, tokens, weights=None, logp=None, dlogits=None, strea
     (logp FP32 [T], dlogits of the logits' type); `dlogits` may be the logits themselves."""
     xp, T, V, ld = _rows(logits, "logits")
     dev = logits.device
+    at = dev.index
     handle, other = _launch(stream, dev)
     logp, pp = _out(logp, T, other, T, torch.float32, dev, "logp")
     if dlogits is None:
         dlogits = _new(other, logits.shape, logits.dtype, dev)
         dp, ldd = dlogits.data_ptr(), V
     else:
-        dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype)
-    rc = lib().agoq_token_loss(xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64),
-                               _vector(weights, T, "weights", _F32), T, V, pp, dp, ldd, handle)
+        dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype, at)
+    rc = lib().agoq_token_loss(xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64, at),
+                               _vector(weights, T, "weights", _F32, at), T, V, pp, dp, ldd, handle)
     if rc:
         raise AgoqError(rc, "agoq_token_loss")
     return logp, dlogits
