@@ -629,13 +629,13 @@ class GradList:
             raise ValueError("outs must match grads")
         self.entries = (_GradTensor * max(1, len(grads)))()
         self.count = len(grads)
-        first = grads[0] if grads else None
-        first = first[0] if isinstance(first, tuple) else first
-        cuda = isinstance(first, torch.Tensor) and first.is_cuda
-        at = first.get_device() if cuda else _current_device()
-        for e, g, o in zip(self.entries, grads, outs):
-            codes, scales = g if isinstance(g, tuple) else (g, None)
-            n = codes.numel() if isinstance(codes, torch.Tensor) else 0
+        pairs = [g if isinstance(g, tuple) else (g, None) for g in grads]
+        for p in pairs:
+            if len(p) != 2 or not isinstance(p[0], torch.Tensor) or not p[0].is_cuda:
+                raise TypeError("a gradient must be a CUDA tensor or a pair of codes and scales")
+        at = pairs[0][0].get_device() if pairs else _current_device()
+        for e, (codes, scales), o in zip(self.entries, pairs, outs):
+            n = codes.numel()
             if scales is None:
                 e.data = _vector(codes, n, "gradient", tuple(DTYPES), at)
                 e.out = e.data if o is None else _vector(o, n, "out", (codes.dtype,), at)

@@ -112,3 +112,11 @@ def test_host_tensors(library):
                              dlogits=_on(0, (2, 8), F32))
     with pytest.raises(TypeError, match="CUDA"):
         agoq.GradList([torch.zeros(3)])
+
+
+@pytest.mark.parametrize("bad", [None, 3.0, (None, None), ("x", "y"), (None,), ()])
+def test_what_is_no_gradient(library, bad):
+    """A parameter without a gradient, say."""
+    for grads in ([bad], [_on(0, (64,), F32), bad]):
+        with pytest.raises(TypeError, match="gradient"):
+            agoq.GradList(grads)
