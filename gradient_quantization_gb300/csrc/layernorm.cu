@@ -274,10 +274,11 @@ __device__ __forceinline__ void quantize_octet(const uint4 &a, const uint4 &b, u
 // thread.  Copies into a ring of shared memory run kRing - 1 steps ahead; a thread
 // reads only what it copied, so the ring needs no barrier, and the row is read from
 // there for each of its passes; w and b stay in registers.  BITS: the codes of x too.
-// Bound by HBM: 8192 x 4096 BF16 23 us (5.8 TB/s), 4096 x 4096 FP32 22 us (6.1 TB/s); in
-// parts 4096 x 8192 31 us, 2048 x 16384 32 us.  With 4-bit codes by instruction issue
-// (8192 x 4096: 36 us, 24 million warp instructions, issue 60%): the codes are a
-// quotient, a rounding and a field for each element.
+// Bound by HBM: 8192 x 4096 BF16 23 us (5.8 TB/s), 4096 x 4096 FP32 22 us (6.1 TB/s).  In
+// parts by the exchange, which a step's results wait for: 4096 x 8192 31 us, 2048 x 16384
+// 32 us (4.3 and 4.2 TB/s).  With 4-bit codes 8192 x 4096 takes 36 us (4.2 TB/s): half as
+// many instructions more (a quotient, a rounding and a field for each element) and 120
+// registers, which leave 16 warps an SM; neither HBM (34%) nor issue (62%) is full.
 template <int DT>
 constexpr int kRows = DT == kF32 ? 1 : 2;
 constexpr int kRing = 4;                     // stages
@@ -791,9 +792,10 @@ __global__ void __launch_bounds__(kThreads) ln_backward_kernel(
 // its group; the groups of a CTA join theirs in order, and the CTA writes one row of the
 // partial sums ([grid][2][H]).
 // 8192 x 4096 BF16: 40 us, and 2 us for the join (4.7 TB/s); from 4-bit codes 46 us.  HBM
-// would allow 30 us: w, dw and db of 16 columns take 48 of a thread's 127 registers, so 16
-// warps an SM hide what they can (issue 54% and 61%, 23 and 31 million instructions).
-// In parts 2048 x 12288 BF16 51 us, 1024 x 16384 FP32 49 us.
+// would allow 30 us: w, dw and db of 16 columns take 48 of a thread's 128 registers, so 16
+// warps an SM hide what they can (issue 52% and 63%, 23 and 32 million instructions).
+// In parts 2048 x 12288 BF16 51 us, 1024 x 16384 FP32 49 us (3.0 and 4.1 TB/s), which the
+// exchange bounds.
 template <int DT>
 constexpr int kBackRows = DT == kF32 ? 1 : 2;
 constexpr int kBackStages = 3;
@@ -1479,7 +1481,8 @@ cudaError_t backward_any_split(const LnBackward &a, cudaStream_t st) {
     return r != cudaSuccess ? r : join<true>(a, P, st);
 }
 
-// As the forward pass; any alignment from a tensor only.
+// As the forward pass; any alignment from a tensor only (from codes with rows of dy 4099
+// elements apart 8192 x 4096 takes 430 us element by element, 48 us aligned).
 template <int DT, int BITS>
 cudaError_t backward(const Input<DT, BITS> &in, const LnBackward &a, cudaStream_t st) {
     constexpr int kSize = Elem<DT>::kSize, V = Elem<DT>::kVec;
