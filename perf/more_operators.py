@@ -370,9 +370,10 @@ def _run_own(s):
     case = s["case"]
     op = case["op"]
     if op == "policy":
+        terms = POLICY if s["ref"] is not None else dict(POLICY, kl_coef=0.0)
         loss, logp, kl, dlogits = agoq.agoq_policy_loss(
             s["logits"], s["tokens"], s["old"], s["advantages"], ref_logp=s["ref"],
-            weights=s["weights"], **POLICY)
+            weights=s["weights"], **terms)
         out = {"logp": logp, "loss": loss, "dlogits": dlogits}
         if s["ref"] is not None:
             out["kl"] = kl
