@@ -86,6 +86,17 @@ def _lib_handle():
         L.agoq_token_logprobs_backward.argtypes = [vp, i64, i32, vp, i64, i64, vp, vp, vp, vp,
                                                    vp, i64, vp]
         L.agoq_token_loss.argtypes = [vp, i64, i32, vp, vp, i64, i64, vp, vp, i64, vp]
+        L.agoq_policy_loss.argtypes = [vp, i64, i32, vp, vp, vp, vp, vp, i64, i64, f32, f32, f32,
+                                       vp, vp, vp, vp, i64, vp]
+        L.agoq_preference_loss.argtypes = [vp, vp, vp, vp, i64, i64, f32, f32, vp, vp, vp, vp]
+        L.agoq_fp4_code_bytes.argtypes = [i64, i64]
+        L.agoq_fp4_code_bytes.restype = i64
+        L.agoq_fp4_scale_bytes.argtypes = [i64, i64, i32]
+        L.agoq_fp4_scale_bytes.restype = i64
+        L.agoq_amax.argtypes = [vp, i64, i64, i64, i32, vp, vp]
+        L.agoq_fp4_quant.argtypes = [vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp]
+        L.agoq_fp4_dequant.argtypes = [vp, vp, vp, i64, i64, i32, vp, i64, i32, vp]
+        L.agoq_fp4_gemm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, i32, vp]
         L.agoq_fwd_gemm_quant.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
         for name in ("agoq_quant_act", "agoq_dequant_act", "agoq_grad_accum_fp8",
                      "agoq_reduce_fp8_shards", "agoq_wgrad_gemm_int4",
@@ -98,7 +109,9 @@ def _lib_handle():
                      "agoq_layernorm_forward", "agoq_layernorm_backward",
                      "agoq_layernorm_backward_laaq", "agoq_grad_list_check", "agoq_grad_norm",
                      "agoq_clip_grads", "agoq_clip_grad_norm", "agoq_token_logprobs",
-                     "agoq_token_logprobs_backward", "agoq_token_loss"):
+                     "agoq_token_logprobs_backward", "agoq_token_loss", "agoq_policy_loss",
+                     "agoq_preference_loss", "agoq_amax", "agoq_fp4_quant", "agoq_fp4_dequant",
+                     "agoq_fp4_gemm"):
             getattr(L, name).restype = i32
         _L = L
     return _L
@@ -759,6 +772,190 @@ def agoq_token_loss(logits, tokens, weights=None, logp=None, dlogits=None, strea
     if rc:
         raise AgoqError(rc, "agoq_token_loss")
     return logp, dlogits
+
+
+def agoq_policy_loss(logits, tokens, old_logp, advantages, ref_logp=None, weights=None,
+                     clip_low=0.2, clip_high=0.2, kl_coef=0.0, loss=None, logp=None, kl=None,
+                     dlogits=None, stream=None):
+    """Clipped policy loss of sampled `tokens` (int64, one a row; negative: ignored) with a KL
+    term to the reference policy whose log probabilities are `ref_logp` (None: no such term),
+    and its gradient -> (loss, logp, kl FP32 [T], dlogits of the logits' type); kl is None
+    without a reference.  `dlogits` may be the logits themselves."""
+    xp, T, V, ld = _rows(logits, "logits")
+    dev = logits.device
+    at = dev.index
+    handle, other = _launch(stream, dev)
+    f32 = torch.float32
+    loss, lp = _out(loss, T, other, T, f32, dev, "loss")
+    logp, pp = _out(logp, T, other, T, f32, dev, "logp")
+    kp = 0
+    if ref_logp is not None or kl is not None:
+        kl, kp = _out(kl, T, other, T, f32, dev, "kl")
+    if dlogits is None:
+        dlogits = _new(other, logits.shape, logits.dtype, dev)
+        dp, ldd = dlogits.data_ptr(), V
+    else:
+        dp, _, _, ldd = _rows(dlogits, "dlogits", V, T, logits.dtype, at)
+    rc = lib().agoq_policy_loss(
+        xp, ld, DTYPES[logits.dtype], _vector(tokens, T, "tokens", _I64, at),
+        _vector(old_logp, T, "old_logp", _F32, at), _vector(ref_logp, T, "ref_logp", _F32, at),
+        _vector(advantages, T, "advantages", _F32, at), _vector(weights, T, "weights", _F32, at),
+        T, V, clip_low, clip_high, kl_coef, lp, pp, kp, dp, ldd, handle)
+    if rc:
+        raise AgoqError(rc, "agoq_policy_loss")
+    return loss, logp, kl, dlogits
+
+
+def agoq_preference_loss(logp, offsets, ref_logp=None, weights=None, beta=0.1,
+                         label_smoothing=0.0, loss=None, margin=None, dlogp=None, stream=None):
+    """Preference loss of pairs of answers from the log probabilities of their tokens
+    (`offsets`: int64 [2 P + 1], the chosen and the rejected answer of each pair) and its
+    gradient -> (loss FP32 [P], margin FP32 [P], dlogp FP32 [T]).  A dlogp made here is 0 at the
+    tokens of no answer; a given one is left as it was there."""
+    if not isinstance(logp, torch.Tensor) or not logp.is_cuda:
+        raise TypeError("logp must be a CUDA tensor")
+    dev = logp.device
+    at = dev.index
+    handle, other = _launch(stream, dev)
+    T = logp.numel()
+    if not isinstance(offsets, torch.Tensor) or offsets.numel() % 2 != 1:
+        raise ValueError("offsets must hold 2 P + 1 values")
+    P = offsets.numel() // 2
+    f32 = torch.float32
+    loss, lp = _out(loss, P, other, P, f32, dev, "loss")
+    margin, mp = _out(margin, P, other, P, f32, dev, "margin")
+    if dlogp is None:
+        with torch.cuda.stream(other):         # (None: the current stream)
+            dlogp = torch.zeros(T, dtype=f32, device=dev)
+    rc = lib().agoq_preference_loss(
+        _vector(logp, T, "logp", _F32, at), _vector(ref_logp, T, "ref_logp", _F32, at),
+        _vector(offsets, 2 * P + 1, "offsets", _I64, at), _vector(weights, P, "weights", _F32, at),
+        T, P, beta, label_smoothing, lp, mp, _vector(dlogp, T, "dlogp", _F32, at), handle)
+    if rc:
+        raise AgoqError(rc, "agoq_preference_loss")
+    return loss, margin, dlogp
+
+
+MXFP4, NVFP4 = 0, 1
+_U8 = (torch.uint8,)
+
+
+def agoq_fp4_code_bytes(rows, K):
+    """Bytes of the FP4 codes of [rows][K]."""
+    return int(lib().agoq_fp4_code_bytes(int(rows), int(K)))
+
+
+def agoq_fp4_scale_bytes(rows, K, fmt):
+    """Bytes of the FP4 scales of [rows][K]."""
+    return int(lib().agoq_fp4_scale_bytes(int(rows), int(K), int(fmt)))
+
+
+def agoq_amax(x, amax=None, stream=None):
+    """Largest magnitude of `x` -> FP32 CUDA tensor of one element."""
+    xp, T, K, ldx = _rows(x, "x")
+    dev = x.device
+    handle, other = _launch(stream, dev)
+    amax, ap = _out(amax, 1, other, 1, torch.float32, dev, "amax")
+    rc = lib().agoq_amax(xp, ldx, T, K, DTYPES[x.dtype], ap, handle)
+    if rc:
+        raise AgoqError(rc, "agoq_amax")
+    return amax
+
+
+def _fp4_out(codes, scales, rows, K, fmt, other, dev, suffix):
+    L = lib()
+    n, m = L.agoq_fp4_code_bytes(rows, K), L.agoq_fp4_scale_bytes(rows, K, fmt)
+    if n < 0 or m < 0:
+        raise ValueError("no FP4 format %r of %d rows of %d" % (fmt, rows, K))
+    codes, cp = _out(codes, n, other, (rows, n // rows if rows else 0), torch.uint8, dev,
+                     "codes" + suffix)
+    scales, sp = _out(scales, m, other, m, torch.uint8, dev, "scales" + suffix)
+    return codes, scales, cp, sp
+
+
+def agoq_fp4_quant(x, fmt, amax=None, rows=True, columns=False, codes=None, scales=None,
+                   codes_t=None, scales_t=None, stream=None):
+    """Quantise `x` [T][K] (FP32, BF16 or FP16 rows) to MXFP4 or NVFP4 (then with the tensor's
+    `amax`) along its rows, its columns, or both in one reading -> (codes, scales, codes_t,
+    scales_t), uint8; the pair that is not wanted is None.  codes_t and scales_t are those of
+    the transposed [K][T]."""
+    xp, T, K, ldx = _rows(x, "x")
+    dev = x.device
+    handle, other = _launch(stream, dev)
+    cp = sp = ctp = stp = 0
+    if rows:
+        codes, scales, cp, sp = _fp4_out(codes, scales, T, K, fmt, other, dev, "")
+    else:
+        codes = scales = None
+    if columns:
+        if T == 0:
+            raise ValueError("x has no rows to quantise columns of")
+        codes_t, scales_t, ctp, stp = _fp4_out(codes_t, scales_t, K, T, fmt, other, dev, "_t")
+    else:
+        codes_t = scales_t = None
+    if T == 0 and rows:
+        return codes, scales, None, None
+    rc = lib().agoq_fp4_quant(xp, ldx, T, K, DTYPES[x.dtype], fmt,
+                              _vector(amax, 1, "amax", _F32, dev.index), cp, sp, ctp, stp, handle)
+    if rc:
+        raise AgoqError(rc, "agoq_fp4_quant")
+    return codes, scales, codes_t, scales_t
+
+
+def _fp4_in(codes, scales, amax, rows, K, fmt, at, name):
+    L = lib()
+    n, m = L.agoq_fp4_code_bytes(rows, K), L.agoq_fp4_scale_bytes(rows, K, fmt)
+    if n < 0 or m < 0:
+        raise ValueError("no FP4 format %r of %d rows of %d" % (fmt, rows, K))
+    return (_vector(codes, n, name + "codes", _U8, at), _vector(scales, m, name + "scales", _U8, at),
+            _vector(amax, 1, name + "amax", _F32, at))
+
+
+def _device_of(t, what):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % what)
+    return t.device
+
+
+def agoq_fp4_dequant(codes, scales, T, K, fmt, amax=None, dtype=torch.bfloat16, y=None,
+                     stream=None):
+    """The values [T][K] of FP4 codes as `dtype` (or into `y`, of its type)."""
+    dev = _device_of(codes, "codes")
+    handle, other = _launch(stream, dev)
+    cp, sp, ap = _fp4_in(codes, scales, amax, T, K, fmt, dev.index, "")
+    if y is None:
+        if dtype not in DTYPES:
+            raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % dtype)
+        y = _new(other, (T, K), dtype, dev)
+        yp, ldy = y.data_ptr(), K
+    else:
+        yp, _, _, ldy = _rows(y, "y", K, T, None, dev.index)
+    rc = lib().agoq_fp4_dequant(cp, sp, ap, T, K, fmt, yp, ldy, DTYPES[y.dtype], handle)
+    if rc:
+        raise AgoqError(rc, "agoq_fp4_dequant")
+    return y
+
+
+def agoq_fp4_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, fmt, a_amax=None, b_amax=None,
+                  dtype=torch.bfloat16, d=None, stream=None):
+    """D[M][N] = A B^T of the FP4 operands A [M][K] and B [N][K] as `dtype` (or into `d`, of its
+    type); NVFP4 takes both tensors' amax."""
+    dev = _device_of(a_codes, "a_codes")
+    at = dev.index
+    handle, other = _launch(stream, dev)
+    ac, as_, aa = _fp4_in(a_codes, a_scales, a_amax, M, K, fmt, at, "a_")
+    bc, bs, ba = _fp4_in(b_codes, b_scales, b_amax, N, K, fmt, at, "b_")
+    if d is None:
+        if dtype not in DTYPES:
+            raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % dtype)
+        d = _new(other, (M, N), dtype, dev)
+        dp, ldd = d.data_ptr(), N
+    else:
+        dp, _, _, ldd = _rows(d, "d", N, M, None, at)
+    rc = lib().agoq_fp4_gemm(ac, as_, aa, bc, bs, ba, M, N, K, fmt, dp, ldd, DTYPES[d.dtype], handle)
+    if rc:
+        raise AgoqError(rc, "agoq_fp4_gemm")
+    return d
 
 
 def agoq_test_wait_timeout(limit_cycles, stream=None):

@@ -32,9 +32,12 @@ UNITS = {
     "layernorm.cu": ["-fmad=false"],
     "grad_norm.cu": ["-fmad=false"],
     "token_logprobs.cu": ["-fmad=false"],
+    "fp4_quant.cu": ["-fmad=false"],
+    "fp4_gemm.cu": ["-fmad=false"],
+    "preference.cu": ["-fmad=false"],
 }
 HEADERS = ["agoq_device.cuh", "agoq_launch.h", "gemm_common.cuh", "wgrad_gemm_impl.cuh", "fwd_gemm_impl.cuh",
-           "typed_io.cuh", "row_units.h"]
+           "typed_io.cuh", "row_units.h", "fp4_format.cuh"]
 
 
 def _nvcc():

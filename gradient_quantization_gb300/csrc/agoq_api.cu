@@ -7,6 +7,7 @@
 // agoq_device_status, whose purpose is to synchronise).
 #include "../../include/agoq.h"
 #include "agoq_launch.h"
+#include "fp4_format.cuh"
 
 #include <algorithm>
 #include <cstdint>
@@ -86,6 +87,11 @@ bool rows_ok(int64_t T, int64_t n, int64_t ld) {
 }
 
 constexpr int64_t kMaxHidden = 1ll << 24, kMaxVocab = 1ll << 30;
+// Rows and row length of the FP4 calls (row numbers and lengths stay within 31 bits).
+constexpr int64_t kMaxFp4 = 1ll << 30, kMaxFp4K = 1ll << 24;
+bool fp4_size_ok(int64_t rows, int64_t K) {
+    return rows >= 0 && rows <= kMaxFp4 && K >= 1 && K <= kMaxFp4K;
+}
 constexpr int kMaxTop = 32;
 
 }  // namespace
@@ -729,19 +735,174 @@ agoq_status agoq_token_loss(const void *logits, int64_t ld, int dtype, const int
     return from_cuda(launch_token_logprobs(a, as_stream(stream)));
 }
 
+agoq_status agoq_policy_loss(const void *logits, int64_t ld, int dtype, const int64_t *tokens,
+                             const float *old_logp, const float *ref_logp, const float *advantages,
+                             const float *weights, int64_t T, int64_t V, float clip_low,
+                             float clip_high, float kl_coef, float *loss, float *logp, float *kl,
+                             void *dlogits, int64_t ldd, void *stream) {
+    using namespace agoq;
+    if (!float_dtype(dtype)) return AGOQ_ERR_FORMAT;
+    if (T < 0 || V < 1 || V > kMaxVocab || !rows_ok(T, V, ld) || !rows_ok(T, V, ldd))
+        return AGOQ_ERR_SHAPE;
+    if (!(clip_low >= 0.0f && clip_low <= 1.0f) || !(clip_high >= 0.0f && clip_high <= 1e6f) ||
+        !(kl_coef >= 0.0f && kl_coef <= 1e6f))
+        return AGOQ_ERR_SHAPE;
+    if (T == 0) return AGOQ_OK;
+    if (!logits || !tokens || !old_logp || !advantages || !dlogits) return AGOQ_ERR_NULL;
+    if (!ref_logp && (kl || kl_coef != 0.0f)) return AGOQ_ERR_NULL;
+    const int es = elem_size(dtype);
+    if (!aligned(logits, es) || !aligned(tokens, 8) || !aligned(old_logp, 4) ||
+        !aligned(ref_logp, 4) || !aligned(advantages, 4) || !aligned(weights, 4) ||
+        !aligned(loss, 4) || !aligned(logp, 4) || !aligned(kl, 4) || !aligned(dlogits, es))
+        return AGOQ_ERR_ALIGN;
+    const Range out[4] = {rows(dlogits, T, V, ldd, es), vec(loss, T, 4), vec(logp, T, 4),
+                          vec(kl, T, 4)};
+    const bool in_place = logits == dlogits && ld == ldd;
+    const Range in[6] = {rows(logits, in_place ? 0 : T, V, ld, es), vec(tokens, T, 8),
+                         vec(old_logp, T, 4), vec(ref_logp, T, 4), vec(advantages, T, 4),
+                         vec(weights, T, 4)};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    const PolicyLoss a{logits, ld, dtype, tokens, old_logp, ref_logp, advantages, weights, T, V,
+                       1.0f - clip_low, 1.0f + clip_high, kl_coef, loss, logp, kl, dlogits, ldd};
+    return from_cuda(launch_policy_loss(a, as_stream(stream)));
+}
+
+agoq_status agoq_preference_loss(const float *logp, const float *ref_logp, const int64_t *offsets,
+                                 const float *weights, int64_t T, int64_t P, float beta,
+                                 float label_smoothing, float *loss, float *margin, float *dlogp,
+                                 void *stream) {
+    using namespace agoq;
+    if (T < 0 || T > 1ll << 40 || P < 0 || P > 1ll << 30) return AGOQ_ERR_SHAPE;
+    if (!(beta >= 0.0f && beta <= 1e6f) || !(label_smoothing >= 0.0f && label_smoothing <= 1.0f))
+        return AGOQ_ERR_SHAPE;
+    if (P == 0) return AGOQ_OK;
+    if (!offsets || (T > 0 && (!logp || !dlogp))) return AGOQ_ERR_NULL;
+    if (!aligned(logp, 4) || !aligned(ref_logp, 4) || !aligned(offsets, 8) || !aligned(weights, 4) ||
+        !aligned(loss, 4) || !aligned(margin, 4) || !aligned(dlogp, 4))
+        return AGOQ_ERR_ALIGN;
+    const Range out[3] = {vec(dlogp, T, 4), vec(loss, P, 4), vec(margin, P, 4)};
+    const Range in[4] = {vec(logp, T, 4), vec(ref_logp, T, 4), vec(offsets, 2 * P + 1, 8),
+                         vec(weights, P, 4)};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    const PreferenceLoss a{logp, ref_logp, offsets, weights, T, P, beta, label_smoothing,
+                           loss, margin, dlogp};
+    return from_cuda(launch_preference_loss(a, as_stream(stream)));
+}
+
+int64_t agoq_fp4_code_bytes(int64_t rows, int64_t K) {
+    return agoq::fp4_size_ok(rows, K) ? rows * agoq::fp4_row_bytes(K) : -1;
+}
+
+int64_t agoq_fp4_scale_bytes(int64_t rows, int64_t K, int format) {
+    using namespace agoq;
+    if (!fp4_size_ok(rows, K) || (format != kMx && format != kNv)) return -1;
+    return fp4_tiles_down(rows) * fp4_tiles_across(K, format) * kScaleTile;
+}
+
+agoq_status agoq_amax(const void *x, int64_t ldx, int64_t T, int64_t K, int dtype, float *amax,
+                      void *stream) {
+    using namespace agoq;
+    if (!float_dtype(dtype)) return AGOQ_ERR_FORMAT;
+    if (T < 0 || K < 0 || T > kMaxFp4 || K > 1ll << 40 || !rows_ok(T, K, ldx)) return AGOQ_ERR_SHAPE;
+    if (!amax || (T > 0 && K > 0 && !x)) return AGOQ_ERR_NULL;
+    const int es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(amax, 4)) return AGOQ_ERR_ALIGN;
+    const Range out[1] = {vec(amax, 1, 4)}, in[1] = {rows(x, T, K, ldx, es)};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    return from_cuda(launch_amax(x, ldx, T, K, dtype, amax, as_stream(stream)));
+}
+
+agoq_status agoq_fp4_quant(const void *x, int64_t ldx, int64_t T, int64_t K, int dtype, int format,
+                           const float *amax, void *codes, void *scales, void *codes_t,
+                           void *scales_t, void *stream) {
+    using namespace agoq;
+    if (!float_dtype(dtype) || (format != kMx && format != kNv)) return AGOQ_ERR_FORMAT;
+    if (!fp4_size_ok(T, K) || !rows_ok(T, K, ldx)) return AGOQ_ERR_SHAPE;
+    if (!codes != !scales || !codes_t != !scales_t || (!codes && !codes_t)) return AGOQ_ERR_NULL;
+    if (codes_t && (T > kMaxFp4K || fp4_tiles_down(T) * fp4_tiles_down(K) > 0x7FFFFFFF))
+        return AGOQ_ERR_SHAPE;
+    if (T == 0) return AGOQ_OK;
+    if (!x || (format == kNv && !amax)) return AGOQ_ERR_NULL;
+    const int es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(amax, 4) || !aligned(codes, 16) || !aligned(scales, 16) ||
+        !aligned(codes_t, 16) || !aligned(scales_t, 16))
+        return AGOQ_ERR_ALIGN;
+    const Range out[4] = {vec(codes, agoq_fp4_code_bytes(T, K), 1),
+                          vec(scales, agoq_fp4_scale_bytes(T, K, format), 1),
+                          vec(codes_t, agoq_fp4_code_bytes(K, T), 1),
+                          vec(scales_t, agoq_fp4_scale_bytes(K, T, format), 1)};
+    const Range in[2] = {rows(x, T, K, ldx, es), vec(format == kNv ? amax : nullptr, 1, 4)};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    const Fp4Quant a{x, ldx, T, K, dtype, format, amax, static_cast<uint8_t *>(codes),
+                     static_cast<uint8_t *>(scales), static_cast<uint8_t *>(codes_t),
+                     static_cast<uint8_t *>(scales_t)};
+    return from_cuda(launch_fp4_quant(a, as_stream(stream)));
+}
+
+agoq_status agoq_fp4_dequant(const void *codes, const void *scales, const float *amax, int64_t T,
+                             int64_t K, int format, void *y, int64_t ldy, int dtype, void *stream) {
+    using namespace agoq;
+    if (!float_dtype(dtype) || (format != kMx && format != kNv)) return AGOQ_ERR_FORMAT;
+    if (!fp4_size_ok(T, K) || !rows_ok(T, K, ldy)) return AGOQ_ERR_SHAPE;
+    if (T == 0) return AGOQ_OK;
+    if (!codes || !scales || !y || (format == kNv && !amax)) return AGOQ_ERR_NULL;
+    const int es = elem_size(dtype);
+    if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(y, es) || !aligned(amax, 4))
+        return AGOQ_ERR_ALIGN;
+    const Range out[1] = {rows(y, T, K, ldy, es)};
+    const Range in[3] = {vec(codes, agoq_fp4_code_bytes(T, K), 1),
+                         vec(scales, agoq_fp4_scale_bytes(T, K, format), 1),
+                         vec(format == kNv ? amax : nullptr, 1, 4)};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    return from_cuda(launch_fp4_dequant(static_cast<const uint8_t *>(codes),
+                                        static_cast<const uint8_t *>(scales), amax, T, K, format, y,
+                                        ldy, dtype, as_stream(stream)));
+}
+
+agoq_status agoq_fp4_gemm(const void *a_codes, const void *a_scales, const float *a_amax,
+                          const void *b_codes, const void *b_scales, const float *b_amax,
+                          int64_t M, int64_t N, int64_t K, int format, void *d, int64_t ldd,
+                          int dtype, void *stream) {
+    using namespace agoq;
+    if (!float_dtype(dtype) || (format != kMx && format != kNv)) return AGOQ_ERR_FORMAT;
+    if (!fp4_size_ok(M, K) || !fp4_size_ok(N, K) || !rows_ok(M, N, ldd) ||
+        fp4_tiles_down(M) * fp4_tiles_down(N) > 1 << 26)
+        return AGOQ_ERR_SHAPE;
+    if (M == 0 || N == 0) return AGOQ_OK;
+    if (!a_codes || !a_scales || !b_codes || !b_scales || !d ||
+        (format == kNv && (!a_amax || !b_amax)))
+        return AGOQ_ERR_NULL;
+    const int es = elem_size(dtype);
+    if (!aligned(a_codes, 16) || !aligned(a_scales, 16) || !aligned(b_codes, 16) ||
+        !aligned(b_scales, 16) || !aligned(a_amax, 4) || !aligned(b_amax, 4) || !aligned(d, es))
+        return AGOQ_ERR_ALIGN;
+    const bool nv = format == kNv;
+    const Range out[1] = {rows(d, M, N, ldd, es)};
+    const Range in[6] = {vec(a_codes, agoq_fp4_code_bytes(M, K), 1),
+                         vec(a_scales, agoq_fp4_scale_bytes(M, K, format), 1),
+                         vec(b_codes, agoq_fp4_code_bytes(N, K), 1),
+                         vec(b_scales, agoq_fp4_scale_bytes(N, K, format), 1),
+                         vec(nv ? a_amax : nullptr, 1, 4), vec(nv ? b_amax : nullptr, 1, 4)};
+    if (any_overlap(out, in)) return AGOQ_ERR_ALIAS;
+    const Fp4Operand A{static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales), a_amax};
+    const Fp4Operand B{static_cast<const uint8_t *>(b_codes), static_cast<const uint8_t *>(b_scales), b_amax};
+    return from_cuda(launch_fp4_gemm(A, B, M, N, K, format, d, ldd, dtype, as_stream(stream)));
+}
+
 agoq_status agoq_test_wait_timeout(int64_t limit_cycles, void *stream) {
     if (limit_cycles <= 0 || limit_cycles > 4000000000ll) return AGOQ_ERR_SHAPE;
     return agoq::from_cuda(agoq::launch_wait_timeout_probe(limit_cycles, agoq::as_stream(stream)));
 }
 
 agoq_status agoq_device_status(void *stream) {
-    unsigned status = 0, fwd = 0, red = 0, rms = 0;
+    unsigned status = 0, fwd = 0, red = 0, rms = 0, fp4 = 0;
     if (agoq::read_and_clear_device_status(agoq::as_stream(stream), &status) != cudaSuccess ||
         agoq::read_and_clear_fwd_status(&fwd) != cudaSuccess ||
         agoq::read_and_clear_reduce_status(&red) != cudaSuccess ||
-        agoq::read_and_clear_rmsnorm_status(&rms) != cudaSuccess)
+        agoq::read_and_clear_rmsnorm_status(&rms) != cudaSuccess ||
+        agoq::read_and_clear_fp4_status(&fp4) != cudaSuccess)
         return AGOQ_ERR_CUDA;
-    return (status || fwd || red || rms) ? AGOQ_ERR_TIMEOUT : AGOQ_OK;
+    return (status || fwd || red || rms || fp4) ? AGOQ_ERR_TIMEOUT : AGOQ_OK;
 }
 
 }  // extern "C"

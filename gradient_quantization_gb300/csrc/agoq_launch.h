@@ -194,6 +194,54 @@ struct TokenLogprobsBackward {
 };
 cudaError_t launch_token_logprobs(const TokenLogprobs &a, cudaStream_t st);
 cudaError_t launch_token_logprobs_backward(const TokenLogprobsBackward &a, cudaStream_t st);
+// The clipped policy loss (token_logprobs.cu).
+struct PolicyLoss {
+    const void *logits;
+    int64_t ld;
+    int dtype;
+    const int64_t *tokens;
+    const float *old_logp, *ref_logp, *advantages, *weights;   // ref_logp, weights may be NULL
+    int64_t T, V;
+    float low, high, kl_coef;                 // bounds of the ratio: 1 - clip_low, 1 + clip_high
+    float *loss, *logp, *kl;                  // any may be NULL
+    void *dlogits;
+    int64_t ldd;
+};
+cudaError_t launch_policy_loss(const PolicyLoss &a, cudaStream_t st);
+// The preference loss (preference.cu).
+struct PreferenceLoss {
+    const float *logp, *ref_logp;             // ref_logp may be NULL
+    const int64_t *offsets;                   // [2 P + 1]
+    const float *weights;                     // [P], or NULL
+    int64_t T, P;
+    float beta, smoothing;
+    float *loss, *margin, *dlogp;             // loss, margin may be NULL
+};
+cudaError_t launch_preference_loss(const PreferenceLoss &a, cudaStream_t st);
+// Micro-scaled 4-bit quantisation (fp4_quant.cu); fmt: fp4_format.cuh.
+cudaError_t launch_amax(const void *x, int64_t ldx, int64_t T, int64_t K, int dtype, float *amax,
+                        cudaStream_t st);
+struct Fp4Quant {
+    const void *x;
+    int64_t ldx;
+    int64_t T, K;
+    int dtype, fmt;
+    const float *amax;                        // NVFP4
+    uint8_t *codes, *scales;                  // of the rows, or NULL
+    uint8_t *codes_t, *scales_t;              // of the columns, or NULL
+};
+cudaError_t launch_fp4_quant(const Fp4Quant &a, cudaStream_t st);
+cudaError_t launch_fp4_dequant(const uint8_t *codes, const uint8_t *scales, const float *amax,
+                               int64_t T, int64_t K, int fmt, void *y, int64_t ldy, int dtype,
+                               cudaStream_t st);
+// Their product (fp4_gemm.cu).
+struct Fp4Operand {
+    const uint8_t *codes, *scales;
+    const float *amax;                        // NVFP4
+};
+cudaError_t launch_fp4_gemm(const Fp4Operand &a, const Fp4Operand &b, int64_t M, int64_t N,
+                            int64_t K, int fmt, void *d, int64_t ldd, int dtype, cudaStream_t st);
+cudaError_t read_and_clear_fp4_status(unsigned *status);
 // A kernel whose one pipeline wait runs out after `limit_cycles` (failure-path test).
 cudaError_t launch_wait_timeout_probe(long long limit_cycles, cudaStream_t st);
 // Read and clear the forward GEMM's status word (call after synchronising).

@@ -1,0 +1,134 @@
+// fp4_format.cuh -- the micro-scaled 4-bit format of the FP4 calls (include/agoq.h):
+// sizes and places of codes and scales, and the rounding of a block.
+//
+// Codes are E2M1 (values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), two to a byte, rows of
+// ceil(K / 32) * 16 bytes.  A scale byte stands for 32 elements of a row (MXFP4: E8M0, a power
+// of two) or 16 (NVFP4: E4M3, times the tensor's scale).  Scales lie in tiles of 128 rows by
+// 4 blocks, 512 bytes: block b of row r at (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4 of tile
+// (r / 128, b / 4).  That is how the tensor cores take them: a tile is copied as it is into four
+// columns of tensor memory.
+#pragma once
+
+#include <cstdint>
+
+namespace agoq {
+
+constexpr int kMx = 0, kNv = 1;                 // agoq_fp4_format
+
+__host__ __device__ constexpr int fp4_block(int fmt) { return fmt == kNv ? 16 : 32; }
+// Elements that a scale tile spans.
+__host__ __device__ constexpr int fp4_tile_elems(int fmt) { return 4 * fp4_block(fmt); }
+__host__ __device__ inline int64_t fp4_row_bytes(int64_t K) { return (K + 31) / 32 * 16; }
+// Tiles of a row block: ceil(K / 64) for NVFP4, ceil(K / 128) for MXFP4.
+__host__ __device__ inline int64_t fp4_tiles_across(int64_t K, int fmt) {
+    return (K + fp4_tile_elems(fmt) - 1) / fp4_tile_elems(fmt);
+}
+__host__ __device__ inline int64_t fp4_tiles_down(int64_t rows) { return (rows + 127) / 128; }
+
+constexpr int kScaleTile = 512;
+
+#ifdef __CUDACC__
+}  // namespace agoq
+#include "agoq_device.cuh"
+namespace agoq {
+
+constexpr float kE2M1Max = 6.0f;
+constexpr float kTensorSpan = 2688.0f;          // 6 * 448
+constexpr float kLowestTensorScale = 0x1p-100f; // products with a block's scale stay normal
+
+// A tensor's scale from its largest magnitude (not finite: the scale is not used, since all
+// blocks' scales are NaN then).
+__device__ __forceinline__ float tensor_scale(float amax) {
+    return fmaxf(__fdiv_rn(amax, kTensorSpan), kLowestTensorScale);
+}
+
+__device__ __forceinline__ bool finite_bits(float v) {
+    return (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
+}
+
+// max.NaN(|a|, |b|, |c|): a NaN stays.
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Scale byte of a block and the factor of its elements, from its largest magnitude.  A block
+// with a NaN or an infinity (or, NVFP4, of a tensor with one) has the NaN of its scale's type
+// and, by a factor that the caller does not use, codes of 0.
+template <int FMT>
+struct BlockScale {
+    uint32_t byte;
+    float inverse;
+    bool finite;
+};
+template <int FMT>
+__device__ __forceinline__ BlockScale<FMT> block_scale(float top, float g, float six_g, bool ok) {
+    BlockScale<FMT> s;
+    if constexpr (FMT == kMx) {
+        // 2^(floor(log2 top) - 2), not below 2^-127: the exponent field less 2
+        const int field = (int)(__float_as_uint(top) >> 23) - 2;
+        s.finite = finite_bits(top);
+        const uint32_t byte = field > 0 ? field : 0;
+        s.byte = s.finite ? byte : 255u;
+        s.inverse = __uint_as_float((254u - byte) << 23);
+    } else {
+        s.finite = ok && finite_bits(top);
+        const uint32_t byte = e4m3x2_from_f32(__fdiv_rn(top, six_g), 0.0f);
+        float lo, hi;
+        e4m3x2_to_f32(byte, lo, hi);
+        const float step = __fmul_rn(lo, g);
+        s.byte = s.finite ? byte : 127u;
+        s.inverse = byte ? __frcp_rn(step) : 0.0f;
+    }
+    return s;
+}
+
+// Eight values times `inverse`, rounded to E2M1 (to nearest, ties to the even code, beyond 6
+// to 6): a word of eight codes.
+__device__ __forceinline__ uint32_t e2m1x8(const uint64_t (&p)[4], float inverse) {
+    const uint64_t r2 = f32x2(inverse, inverse);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t q = mul_f32x2(p[i], r2);
+        f[2 * i] = lo_f32(q);
+        f[2 * i + 1] = hi_f32(q);
+    }
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+    return w;
+}
+
+// Eight codes to FP16 pairs (exact).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// Value of a scale byte (NaN among them).
+template <int FMT>
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    if constexpr (FMT == kMx)
+        return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
+    float lo, hi;
+    e4m3x2_to_f32(byte, lo, hi);
+    return lo;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace agoq

@@ -1,0 +1,548 @@
+// fp4_quant.cu -- micro-scaled 4-bit quantisation of a matrix along its rows, its columns or
+// both, the largest magnitude that NVFP4's tensor scale is taken from, and the way back.
+//
+// Per block of 32 (MXFP4) or 16 (NVFP4) elements, in binary32:
+//   MXFP4: s = 2^e, e = max(floor(log2 absmax) - 2, -127);   code = E2M1(x 2^-e)
+//   NVFP4: g = max(fl(amax / 2688), 2^-100); s = E4M3(fl(absmax / fl(6 g)));
+//          code = E2M1(fl(x fl(1 / fl(s g)))), 0 where s is 0
+// E2M1 and E4M3 round to nearest even and saturate.
+#include <cooperative_groups.h>
+
+#include "agoq_launch.h"
+#include "fp4_format.cuh"
+#include "typed_io.cuh"
+
+namespace agoq {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 256;
+constexpr int kGroup = 16;                     // elements of a thread's group
+
+template <int DT>
+struct Group {
+    static constexpr int kVecs = kGroup * Elem<DT>::kSize / 16;
+    uint4 v[kVecs];
+    // Elements e .. e + 15 of a row of K (0 beyond it).
+    __device__ __forceinline__ void load(const char *row, int64_t e, int64_t K) {
+        using E = Elem<DT>;
+        const char *p = row + e * E::kSize;
+        const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+        if (shift == 0 && e + kGroup <= K) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            return;
+        }
+        // the 16-byte vectors around the group, where they lie within the row
+        if (p - shift >= row && e + kGroup + (16 - shift) / E::kSize <= K) {
+            const uint4 *from = reinterpret_cast<const uint4 *>(p - shift);
+            uint4 last = __ldg(from);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const uint4 next = __ldg(from + i + 1);
+                v[i] = bytes_from(last, next, shift);
+                last = next;
+            }
+            return;
+        }
+        typename E::Word w[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+            w[i] = e + i < K ? __ldg(reinterpret_cast<const typename E::Word *>(row) + e + i)
+                             : typename E::Word(0);
+        __builtin_memcpy(v, w, sizeof v);
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    }
+    // Largest magnitude; NaN if there is one.
+    __device__ __forceinline__ float absmax() const {
+        if constexpr (DT == kF32) {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                m = max_abs_nan(m, __uint_as_float(v[i].x), __uint_as_float(v[i].y));
+                m = max_abs_nan(m, __uint_as_float(v[i].z), __uint_as_float(v[i].w));
+            }
+            return m;
+        } else {
+            // magnitudes of 16-bit floats in the order of their bits, NaN last
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                         __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
+            }
+            const uint32_t lo = m & 0xFFFFu, hi = m >> 16;
+            return Elem<DT>::up((uint16_t)(lo > hi ? lo : hi));
+        }
+    }
+    __device__ __forceinline__ uint2 codes(float inverse) const {
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint64_t p[4];
+            if constexpr (DT == kF32) {
+                unpack2<DT>(v[2 * h], p);
+                unpack2<DT>(v[2 * h + 1], p + 2);
+            } else {
+                unpack2<DT>(v[h], p);
+            }
+            w[h] = e2m1x8(p, inverse);
+        }
+        return make_uint2(w[0], w[1]);
+    }
+};
+
+struct TensorScale {
+    float g = 0.0f, six_g = 0.0f;
+    bool ok = true;
+    template <int FMT>
+    __device__ __forceinline__ static TensorScale of(const float *amax) {
+        TensorScale t;
+        if constexpr (FMT == kNv) {
+            const float m = __ldg(amax);
+            t.g = tensor_scale(m);
+            t.six_g = __fmul_rn(t.g, kE2M1Max);
+            t.ok = finite_bits(m);
+        }
+        return t;
+    }
+};
+
+// Two NaN-keeping magnitudes.
+__device__ __forceinline__ float larger(float a, float b) { return max_abs_nan(a, b, 0.0f); }
+
+// The word of four scales that a thread's block belongs to, from the threads of four blocks
+// (a block is one thread's group, NVFP4, or two threads', MXFP4).
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_word(uint32_t byte, int lane) {
+    constexpr int kPer = FMT == kMx ? 1 : 0;
+    uint32_t w = byte << (8 * ((lane >> kPer) & 3));
+    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 1 << kPer);
+    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 << kPer);
+    return w;
+}
+
+// Place of the word of blocks 4 t .. 4 t + 3 of a row.
+__device__ __forceinline__ int64_t word_at(int64_t row, int64_t t, int64_t across) {
+    return ((row >> 7) * across + t) * kScaleTile + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+// ---- rows -------------------------------------------------------------------------
+//
+// A thread takes 16 elements of a row; rows are padded to whole scale words (64 or 128
+// elements) and to whole tiles of 128, so that every scale byte is written (0 where there is
+// no block).
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kThreads) fp4_rows_kernel(const Fp4Quant a, uint32_t units,
+                                                            uint32_t per_row) {
+    pdl_wait_and_release();
+    const TensorScale ts = TensorScale::of<FMT>(a.amax);
+    const int lane = threadIdx.x & 31;
+    const int64_t across = fp4_tiles_across(a.K, FMT), row_bytes = fp4_row_bytes(a.K);
+    for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
+        const uint32_t row = u / per_row, g = u - row * per_row;
+        const bool live = row < a.T;
+        Group<DT> x;
+        if (live) x.load(elem_at<DT>(a.x, row * a.ldx), (int64_t)g * kGroup, a.K);
+        else x.clear();
+        float top = x.absmax();
+        if constexpr (FMT == kMx) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        const BlockScale<FMT> s = block_scale<FMT>(top, ts.g, ts.six_g, ts.ok);
+        uint2 c = x.codes(s.inverse);
+        if (!s.finite) c = make_uint2(0, 0);
+        if (live && (int64_t)g * 8 < row_bytes)
+            *reinterpret_cast<uint2 *>(a.codes + row * row_bytes + (int64_t)g * 8) = c;
+        const uint32_t w = scale_word<FMT>(s.byte, lane);
+        constexpr uint32_t kWord = FMT == kMx ? 8 : 4;     // threads of a word
+        if (g % kWord == 0)
+            *reinterpret_cast<uint32_t *>(a.scales + word_at(row, g / kWord, across)) = w;
+    }
+}
+
+// ---- columns, and both -------------------------------------------------------------
+//
+// A CTA takes a tile of 128 x 128: its rows are quantised as they are loaded (ROWS), the tile
+// goes to shared memory, and a thread then takes a block of two neighbouring columns.  The
+// tile's codes of the columns and its scale tiles are gathered in shared memory and leave in
+// whole rows.
+constexpr int kTile = 128;
+constexpr int kCodePitch = 72;                 // bytes of a column's 64 bytes of codes
+
+template <int DT, int FMT, bool ROWS>
+__global__ void __launch_bounds__(kThreads) fp4_tiles_kernel(const Fp4Quant a, int64_t tiles_k) {
+    using E = Elem<DT>;
+    constexpr int kPitch = kTile * E::kSize;
+    constexpr int kBlockLen = fp4_block(FMT);
+    constexpr int kTilesHere = kTile / fp4_tile_elems(FMT);    // scale tiles along 128 elements
+    extern __shared__ __align__(16) uint8_t tile[];
+    uint8_t *out = tile + kTile * kPitch;                      // codes of the columns
+    uint8_t *scales = out + kTile * kCodePitch;                // their scale tiles
+    uint8_t *row_scales = scales + kTilesHere * kScaleTile;
+    pdl_wait_and_release();
+    const TensorScale ts = TensorScale::of<FMT>(a.amax);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t0 = blockIdx.x / tiles_k * kTile, k0 = blockIdx.x % tiles_k * kTile;
+    const int64_t row_bytes = fp4_row_bytes(a.K), col_bytes = fp4_row_bytes(a.T);
+    // rows: eight threads a row, 32 rows a step
+    const int g = threadIdx.x & 7;
+    Group<DT> x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t t = t0 + 32 * i + (threadIdx.x >> 3);
+        if (t < a.T && k0 + g * kGroup < a.K)
+            x[i].load(elem_at<DT>(a.x, t * a.ldx), k0 + g * kGroup, a.K);
+        else
+            x[i].clear();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 32 * i + (threadIdx.x >> 3);
+        uint4 *to = reinterpret_cast<uint4 *>(tile + r * kPitch + g * kGroup * E::kSize);
+#pragma unroll
+        for (int j = 0; j < Group<DT>::kVecs; ++j) to[j] = x[i].v[j];
+        if constexpr (ROWS) {
+            float top = x[i].absmax();
+            if constexpr (FMT == kMx) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            const BlockScale<FMT> s = block_scale<FMT>(top, ts.g, ts.six_g, ts.ok);
+            uint2 c = x[i].codes(s.inverse);
+            if (!s.finite) c = make_uint2(0, 0);
+            const int64_t at = k0 / 2 + g * 8;
+            if (t0 + r < a.T && at < row_bytes)
+                *reinterpret_cast<uint2 *>(a.codes + (t0 + r) * row_bytes + at) = c;
+            const uint32_t w = scale_word<FMT>(s.byte, lane);
+            constexpr int kWord = FMT == kMx ? 8 : 4;
+            if (g % kWord == 0)
+                *reinterpret_cast<uint32_t *>(row_scales + g / kWord * kScaleTile + (r & 31) * 16 +
+                                              (r >> 5) * 4) = w;
+        }
+    }
+    __syncthreads();
+    // columns 2 c and 2 c + 1, blocks of kBlockLen rows
+    constexpr int kTasks = kTile / kBlockLen * (kTile / 2);
+    for (int task = threadIdx.x; task < kTasks; task += kThreads) {
+        const int c = task & 63, b = task >> 6;
+        float lo[kBlockLen], hi[kBlockLen];
+        float top_lo, top_hi;
+        if constexpr (DT == kF32) {
+            top_lo = top_hi = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kBlockLen; ++i) {
+                const float2 v = *reinterpret_cast<const float2 *>(
+                    tile + (b * kBlockLen + i) * kPitch + c * 8);
+                lo[i] = v.x;
+                hi[i] = v.y;
+            }
+#pragma unroll
+            for (int i = 0; i < kBlockLen; i += 2) {
+                top_lo = max_abs_nan(top_lo, lo[i], lo[i + 1]);
+                top_hi = max_abs_nan(top_hi, hi[i], hi[i + 1]);
+            }
+        } else {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < kBlockLen; ++i) {
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                    tile + (b * kBlockLen + i) * kPitch + c * 4);
+                m = __vmaxu2(m, w & 0x7FFF7FFFu);
+                lo[i] = E::up((uint16_t)w);
+                hi[i] = E::up((uint16_t)(w >> 16));
+            }
+            top_lo = E::up((uint16_t)m);
+            top_hi = E::up((uint16_t)(m >> 16));
+        }
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            const float *f = side ? hi : lo;
+            const BlockScale<FMT> s =
+                block_scale<FMT>(side ? top_hi : top_lo, ts.g, ts.six_g, ts.ok);
+            const int col = 2 * c + side;
+#pragma unroll
+            for (int h = 0; h < kBlockLen / 16; ++h) {
+                uint32_t w[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint64_t p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        p[i] = f32x2(f[16 * h + 8 * q + 2 * i], f[16 * h + 8 * q + 2 * i + 1]);
+                    w[q] = s.finite ? e2m1x8(p, s.inverse) : 0u;
+                }
+                *reinterpret_cast<uint2 *>(out + col * kCodePitch + b * (kBlockLen / 2) + 8 * h) =
+                    make_uint2(w[0], w[1]);
+            }
+            scales[(b >> 2) * kScaleTile + (col & 31) * 16 + (col >> 5) * 4 + (b & 3)] =
+                (uint8_t)s.byte;
+        }
+    }
+    __syncthreads();
+    // eight threads a column
+    for (int col = threadIdx.x >> 3; col < kTile; col += kThreads / 8) {
+        const int64_t at = t0 / 2 + g * 8;
+        if (k0 + col < a.K && at < col_bytes)
+            *reinterpret_cast<uint2 *>(a.codes_t + (k0 + col) * col_bytes + at) =
+                *reinterpret_cast<const uint2 *>(out + col * kCodePitch + g * 8);
+    }
+    // scale tiles, a warp each
+    const int64_t down_t = fp4_tiles_across(a.T, FMT), across = fp4_tiles_across(a.K, FMT);
+    if (warp < kTilesHere) {
+        const int64_t at = t0 / fp4_tile_elems(FMT) + warp;
+        if (at < down_t)
+            *reinterpret_cast<uint4 *>(a.scales_t + ((k0 >> 7) * down_t + at) * kScaleTile +
+                                       lane * 16) =
+                *reinterpret_cast<const uint4 *>(scales + warp * kScaleTile + lane * 16);
+    } else if (ROWS && warp < 2 * kTilesHere) {
+        const int w = warp - kTilesHere;
+        const int64_t at = k0 / fp4_tile_elems(FMT) + w;
+        if (at < across)
+            *reinterpret_cast<uint4 *>(a.scales + ((t0 >> 7) * across + at) * kScaleTile +
+                                       lane * 16) =
+                *reinterpret_cast<const uint4 *>(row_scales + w * kScaleTile + lane * 16);
+    }
+}
+
+// ---- the largest magnitude -----------------------------------------------------------
+
+// Magnitudes as binary32 bits are in the order of their values, NaN last.
+template <int DT>
+__device__ __forceinline__ uint32_t absmax_of(const void *x, int64_t ldx, int64_t T, int64_t K,
+                                              int64_t first, int64_t step) {
+    const int64_t per_row = (K + kGroup - 1) / kGroup;
+    uint32_t m = 0;
+    if (T == 1) {
+#pragma unroll 2
+        for (int64_t g = first; g < per_row; g += step) {
+            Group<DT> v;
+            v.load(static_cast<const char *>(x), g * kGroup, K);
+            m = max(m, __float_as_uint(v.absmax()));
+        }
+        return m;
+    }
+    int64_t row = first / per_row, g = first % per_row;
+    const int64_t rows_step = step / per_row, g_step = step % per_row;
+    while (row < T) {
+        Group<DT> v;
+        v.load(elem_at<DT>(x, row * ldx), g * kGroup, K);
+        m = max(m, __float_as_uint(v.absmax()));
+        row += rows_step;
+        g += g_step;
+        if (g >= per_row) {
+            g -= per_row;
+            ++row;
+        }
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint32_t cta_largest(uint32_t m, uint32_t *red, int warps) {
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = (int)(threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0u;
+    return __reduce_max_sync(0xFFFFFFFFu, m);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) amax_kernel(const void *x, int64_t ldx, int64_t T,
+                                                        int64_t K, uint32_t *amax) {
+    __shared__ uint32_t red[kThreads / 32];
+    pdl_wait_and_release();
+    uint32_t m = absmax_of<DT>(x, ldx, T, K, (int64_t)blockIdx.x * kThreads + threadIdx.x,
+                               (int64_t)gridDim.x * kThreads);
+    m = cta_largest(m, red, kThreads / 32);
+    if (threadIdx.x == 0) atomicMax(amax, m);      // whole numbers: in any order the same
+}
+
+// One cluster over the whole tensor: no initial value in memory, no second launch.
+constexpr int kSmallCluster = 8, kSmallThreads = 512;
+template <int DT>
+__global__ void __launch_bounds__(kSmallThreads) amax_small_kernel(const void *x, int64_t ldx,
+                                                                   int64_t T, int64_t K,
+                                                                   uint32_t *amax) {
+    __shared__ uint32_t red[kSmallThreads / 32], mine;
+    cg::cluster_group cluster = cg::this_cluster();
+    pdl_wait_and_release();
+    uint32_t m = absmax_of<DT>(x, ldx, T, K, (int64_t)blockIdx.x * kSmallThreads + threadIdx.x,
+                               (int64_t)kSmallCluster * kSmallThreads);
+    m = cta_largest(m, red, kSmallThreads / 32);
+    if (threadIdx.x == 0) mine = m;
+    cluster.sync();
+    if (blockIdx.x == 0 && threadIdx.x < 32) {
+        m = threadIdx.x < kSmallCluster ? *cluster.map_shared_rank(&mine, threadIdx.x) : 0u;
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (threadIdx.x == 0) *amax = m;
+    }
+    cluster.sync();
+}
+
+// ---- the way back ----------------------------------------------------------------------
+//
+// A thread takes 16 elements of a row: y = R(fl(fl(code s) g)); code s is exact.
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kThreads)
+fp4_dequant_kernel(const uint8_t *codes, const uint8_t *scales, const float *amax, int64_t T,
+                   int64_t K, void *y, int64_t ldy, uint32_t units, uint32_t per_row) {
+    using E = Elem<DT>;
+    constexpr int kVecs = Group<DT>::kVecs;
+    pdl_wait_and_release();
+    const TensorScale ts = TensorScale::of<FMT>(amax);
+    const int64_t across = fp4_tiles_across(K, FMT), row_bytes = fp4_row_bytes(K);
+    constexpr int kShift = FMT == kMx ? 1 : 0;          // groups of a block
+    for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
+        const uint32_t row = u / per_row, g = u - row * per_row;
+        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + row * row_bytes) + g);
+        const uint32_t b = g >> kShift;
+        const uint32_t byte = __ldg(scales + word_at(row, b >> 2, across) + (b & 3));
+        const float s = scale_value<FMT>(byte);
+        float f[kGroup];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[4];
+            e2m1x8_to_f16(h ? c.y : c.x, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = __half22float2(*reinterpret_cast<__half2 *>(&w[i]));
+                uint64_t p = mul_f32x2(f32x2(v.x, v.y), f32x2(s, s));
+                if constexpr (FMT == kNv) p = mul_f32x2(p, f32x2(ts.g, ts.g));
+                f[8 * h + 2 * i] = lo_f32(p);
+                f[8 * h + 2 * i + 1] = hi_f32(p);
+            }
+        }
+        char *to = elem_at<DT>(y, row * ldy + (int64_t)g * kGroup);
+        if ((int64_t)(g + 1) * kGroup <= K && (reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                reinterpret_cast<uint4 *>(to)[i] = E::pack(f + i * E::kVec);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+                if ((int64_t)g * kGroup + i < K) store_elem<DT>(to, i, f[i]);
+        }
+    }
+}
+
+// ---- launches ------------------------------------------------------------------------------
+
+// Rows of a launch: thread numbers and rows stay within 31 bits.
+int64_t rows_a_launch(int64_t per_row) {
+    const int64_t most = (1ll << 30) / per_row / 128 * 128;
+    return most > 0 ? most : 128;
+}
+
+int grid_of(int64_t units) {
+    const int64_t ctas = (units + kThreads - 1) / kThreads, most = 64ll * sm_count();
+    return (int)(ctas < most ? ctas : most);
+}
+
+template <int DT, int FMT>
+cudaError_t launch_rows(const Fp4Quant &all, cudaStream_t st) {
+    constexpr int64_t kWord = fp4_tile_elems(FMT) / kGroup;
+    const int64_t per_row = fp4_tiles_across(all.K, FMT) * kWord;
+    const int64_t step = rows_a_launch(per_row);
+    for (int64_t r = 0; r < all.T; r += step) {
+        Fp4Quant a = all;
+        a.T = all.T - r < step ? all.T - r : step;
+        a.x = static_cast<const char *>(all.x) + r * all.ldx * Elem<DT>::kSize;
+        a.codes += r * fp4_row_bytes(all.K);
+        a.scales += r / 128 * fp4_tiles_across(all.K, FMT) * kScaleTile;
+        const int64_t units = fp4_tiles_down(a.T) * 128 * per_row;
+        const cudaError_t e = launch_pdl(fp4_rows_kernel<DT, FMT>, grid_of(units), kThreads, 0, st,
+                                         a, (uint32_t)units, (uint32_t)per_row);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <int DT, int FMT, bool ROWS>
+cudaError_t launch_tiles(const Fp4Quant &a, cudaStream_t st) {
+    static bool ready[kMaxDevices];
+    constexpr int kTilesHere = kTile / fp4_tile_elems(FMT);
+    constexpr size_t bytes = kTile * kTile * Elem<DT>::kSize + kTile * kCodePitch +
+                             2 * kTilesHere * kScaleTile;
+    auto kernel = fp4_tiles_kernel<DT, FMT, ROWS>;
+    const cudaError_t e = allow_shared(kernel, bytes, ready);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles_k = (a.K + kTile - 1) / kTile, tiles = (a.T + kTile - 1) / kTile * tiles_k;
+    if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    return launch_pdl(kernel, (int)tiles, kThreads, bytes, st, a, tiles_k);
+}
+
+template <int DT, int FMT>
+cudaError_t launch_quant(const Fp4Quant &a, cudaStream_t st) {
+    if (!a.codes_t) return launch_rows<DT, FMT>(a, st);
+    return a.codes ? launch_tiles<DT, FMT, true>(a, st) : launch_tiles<DT, FMT, false>(a, st);
+}
+
+template <int DT, int FMT>
+cudaError_t launch_dequant(const uint8_t *codes, const uint8_t *scales, const float *amax,
+                           int64_t T, int64_t K, void *y, int64_t ldy, cudaStream_t st) {
+    const int64_t per_row = (K + kGroup - 1) / kGroup, step = rows_a_launch(per_row);
+    for (int64_t r = 0; r < T; r += step) {
+        const int64_t n = T - r < step ? T - r : step, units = n * per_row;
+        const cudaError_t e = launch_pdl(
+            fp4_dequant_kernel<DT, FMT>, grid_of(units), kThreads, 0, st,
+            codes + r * fp4_row_bytes(K), scales + r / 128 * fp4_tiles_across(K, FMT) * kScaleTile,
+            amax, n, K, static_cast<void *>(static_cast<char *>(y) + r * ldy * Elem<DT>::kSize),
+            ldy, (uint32_t)units, (uint32_t)per_row);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <int DT>
+cudaError_t launch_amax_type(const void *x, int64_t ldx, int64_t T, int64_t K, float *amax,
+                             cudaStream_t st) {
+    if (T == 0 || K == 0) {
+        T = 1;
+        K = 0;
+    } else if (ldx == K) {                     // one long row
+        K *= T;
+        T = 1;
+    }
+    uint32_t *to = reinterpret_cast<uint32_t *>(amax);
+    if (T * K <= (1 << 20))
+        return launch_pdl_clusters(amax_small_kernel<DT>, kSmallCluster, kSmallThreads,
+                                   kSmallCluster, 0, st, x, ldx, T, K, to);
+    cudaError_t e = cudaMemsetAsync(amax, 0, 4, st);
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = (T * ((K + kGroup - 1) / kGroup) + kThreads - 1) / kThreads;
+    const int64_t most = 8ll * sm_count();
+    return launch_pdl(amax_kernel<DT>, (int)(ctas < most ? ctas : most), kThreads, 0, st, x, ldx,
+                      T, K, to);
+}
+
+}  // namespace
+
+cudaError_t launch_amax(const void *x, int64_t ldx, int64_t T, int64_t K, int dtype, float *amax,
+                        cudaStream_t st) {
+    return dtype == kF32    ? launch_amax_type<kF32>(x, ldx, T, K, amax, st)
+           : dtype == kBF16 ? launch_amax_type<kBF16>(x, ldx, T, K, amax, st)
+                            : launch_amax_type<kF16>(x, ldx, T, K, amax, st);
+}
+
+cudaError_t launch_fp4_quant(const Fp4Quant &a, cudaStream_t st) {
+    if (a.fmt == kMx)
+        return a.dtype == kF32    ? launch_quant<kF32, kMx>(a, st)
+               : a.dtype == kBF16 ? launch_quant<kBF16, kMx>(a, st)
+                                  : launch_quant<kF16, kMx>(a, st);
+    return a.dtype == kF32    ? launch_quant<kF32, kNv>(a, st)
+           : a.dtype == kBF16 ? launch_quant<kBF16, kNv>(a, st)
+                              : launch_quant<kF16, kNv>(a, st);
+}
+
+cudaError_t launch_fp4_dequant(const uint8_t *codes, const uint8_t *scales, const float *amax,
+                               int64_t T, int64_t K, int fmt, void *y, int64_t ldy, int dtype,
+                               cudaStream_t st) {
+    auto pick = [&](auto mx, auto nv) {
+        return fmt == kMx ? mx(codes, scales, amax, T, K, y, ldy, st)
+                          : nv(codes, scales, amax, T, K, y, ldy, st);
+    };
+    return dtype == kF32    ? pick(launch_dequant<kF32, kMx>, launch_dequant<kF32, kNv>)
+           : dtype == kBF16 ? pick(launch_dequant<kBF16, kMx>, launch_dequant<kBF16, kNv>)
+                            : pick(launch_dequant<kF16, kMx>, launch_dequant<kF16, kNv>);
+}
+
+}  // namespace agoq

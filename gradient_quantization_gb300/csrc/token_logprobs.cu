@@ -1,12 +1,16 @@
 // token_logprobs.cu -- log probabilities of given tokens under a row of logits,
 // with the row's entropy and its most likely alternatives; their gradient; and
-// the loss of given tokens with its gradient in one call.
+// the loss of given tokens, or the clipped policy loss of sampled ones, with its gradient
+// in one call.
 //
 // Per row x of V logits, in binary32:
 //   m = max x,  S = sum e^(x - m),  lse = m + ln S,  logp = x[token] - lse,
 //   entropy = ln S - sum (x - m) e^(x - m) / S,
 //   the k largest logits by (value descending, index ascending);
 //   loss: d x_i = w (p_i - [i = token]),  p_i = e^(x_i - m) / S;
+//   policy loss, with r = e^(logp - old), d = ref - logp, A the advantage:
+//     loss = w (-min(r A, clip(r) A) + b (e^d - d - 1)),
+//     d x_i = c (p_i - [i = token]),  c = w (r A [r A <= clip(r) A] + b (e^d - 1));
 //   gradient of the statistics:
 //     d x_i = dlogp ([i = token] - p_i) - dentropy p_i (ln p_i + entropy).
 // A logit of -inf has probability 0.  A row of nothing but -inf has lse = -inf,
@@ -56,10 +60,81 @@ __device__ __forceinline__ float log_prob(float x, float ref, float sum, float l
     return x == -INFINITY && sum == sum ? x : __fsub_rn(__fsub_rn(x, ref), ln);
 }
 
+// ---- a row's factor of p_i - [i = token] in the gradient, and its losses -------------
+//
+// write(): the row's results, by one thread; factor(): w or c, NaN for a row of NaN.
+
+__device__ __forceinline__ bool finite_f32(float v) { return fabsf(v) <= 3.402823466e38f; }
+
+struct TokenRow {
+    float w, logp;
+    // at: the token's logit; the row's reference, sum and the sum's logarithm
+    __device__ __forceinline__ TokenRow(const TokenLogprobs &a, int64_t t, float at, float ref,
+                                        float sum, float ln) {
+        w = a.weights ? a.weights[t] : 1.0f;
+        logp = log_prob(at, ref, sum, ln);
+    }
+    __device__ __forceinline__ void write(const TokenLogprobs &a, int64_t t, bool ignored,
+                                          bool beyond) const {
+        if (a.logp) a.logp[t] = ignored ? 0.0f : beyond ? NAN : logp;
+    }
+    static constexpr bool kNeedsToken = false;      // by every thread, for the factor
+};
+
+struct PolicyRow {
+    float w, logp, loss, kl;
+    __device__ __forceinline__ PolicyRow(const PolicyLoss &a, int64_t t, float at, float ref,
+                                         float sum, float ln) {
+        logp = log_prob(at, ref, sum, ln);
+        const float weight = a.weights ? a.weights[t] : 1.0f, A = a.advantages[t];
+        const float r = expf(__fsub_rn(logp, a.old_logp[t]));
+        const bool clipped = (A > 0.0f && r > a.high) || (A < 0.0f && r < a.low);
+        const float gain = __fmul_rn(clipped ? (A > 0.0f ? a.high : a.low) : r, A);
+        float slope = clipped ? 0.0f : gain;
+        loss = -gain;
+        kl = 0.0f;
+        if (a.ref_logp) {
+            const float d = __fsub_rn(a.ref_logp[t], logp), e = expm1f(d);
+            // e^d - 1 - d, by its series where the terms cancel (next term below 2^-24 of it)
+            if (fabsf(d) < 0.5f) {
+                float s = 1.0f / 362880;
+                s = __fmaf_rn(s, d, 1.0f / 40320);
+                s = __fmaf_rn(s, d, 1.0f / 5040);
+                s = __fmaf_rn(s, d, 1.0f / 720);
+                s = __fmaf_rn(s, d, 1.0f / 120);
+                s = __fmaf_rn(s, d, 1.0f / 24);
+                s = __fmaf_rn(s, d, 1.0f / 6);
+                s = __fmaf_rn(s, d, 0.5f);
+                kl = __fmul_rn(__fmul_rn(d, d), s);
+            } else {
+                kl = e == INFINITY ? e : __fsub_rn(e, d);
+            }
+            // without a coefficient an infinite term takes no part
+            if (a.kl_coef != 0.0f) {
+                loss = __fmaf_rn(a.kl_coef, kl, loss);
+                slope = __fmaf_rn(a.kl_coef, e, slope);
+            }
+        }
+        loss = __fmul_rn(weight, loss);
+        w = __fmul_rn(weight, slope);
+        if (!finite_f32(w)) w = NAN;
+    }
+    __device__ __forceinline__ void write(const PolicyLoss &a, int64_t t, bool ignored,
+                                          bool beyond) const {
+        if (a.logp) a.logp[t] = ignored ? 0.0f : beyond ? NAN : logp;
+        if (a.loss) a.loss[t] = ignored ? 0.0f : beyond ? NAN : loss;
+        if (a.kl) a.kl[t] = ignored ? 0.0f : beyond ? NAN : kl;
+    }
+    static constexpr bool kNeedsToken = true;
+};
+
+template <class Args> struct RowOf { using Row = TokenRow; };
+template <> struct RowOf<PolicyLoss> { using Row = PolicyRow; };
+
 // The loss of rows too long for a cluster's shared memory: a CTA a row, every pass
 // reading the logits again.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) token_loss_long_kernel(const TokenLogprobs a) {
+template <int DT, class Args>
+__global__ void __launch_bounds__(kThreads) token_loss_long_kernel(const Args a) {
     pdl_wait_and_release();
     __shared__ float red[2][kWarps];
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
@@ -75,11 +150,9 @@ __global__ void __launch_bounds__(kThreads) token_loss_long_kernel(const TokenLo
             s = __fadd_rn(s, expf(__fsub_rn(load_now<DT>(row, i), m)));
         s = cta_sum<kWarps>(s, red[1]);
         const bool ignored = token < 0, beyond = token >= a.V, empty = s == 0.0f;
-        if (threadIdx.x == 0 && a.logp) {
-            const float lp = log_prob(at, m, s, logf(s));
-            a.logp[t] = ignored ? 0.0f : beyond ? NAN : lp;
-        }
-        float w = a.weights ? a.weights[t] : 1.0f;
+        const typename RowOf<Args>::Row r(a, t, at, m, s, logf(s));
+        if (threadIdx.x == 0) r.write(a, t, ignored, beyond);
+        float w = r.w;
         if (beyond || s != s) w = NAN;                // 0 times a row of NaN is NaN too
         if (ignored || (empty && !beyond)) w = 0.0f;
         char *out = elem_at<DT>(a.dlogits, t * a.ldd);
@@ -892,6 +965,8 @@ struct RowShared {
     Sums warps[kRowWarps];
     Sums slice, row;
     float token;                  // the token's logit, in the CTA that holds it
+    int holds;                    // whether this one does
+    float row_token;
 };
 
 // Gradient of a vector of logits: scale e^(x - ref).
@@ -910,9 +985,10 @@ __device__ __forceinline__ void loss_grad(const uint4 &v, float ref, float scale
     }
 }
 
-template <int DT, int THREADS>
-__global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(const TokenLogprobs a) {
+template <int DT, int THREADS, class Args>
+__global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(const Args a) {
     using E = Elem<DT>;
+    using Row = typename RowOf<Args>::Row;
     using Word = typename E::Word;
     constexpr int N = E::kVec;
     extern __shared__ __align__(16) uint4 data[];
@@ -965,27 +1041,35 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
         if (lane == 0) sh.warps[warp] = mine;
         __syncthreads();
         Sums all = warp_join(lane < kWarpsHere ? sh.warps[lane] : Sums{kLowest, 0.0f, 0.0f});
-        if (threadIdx.x == 0 && s.has(token)) sh.token = E::up(words[token - s.start]);
+        float at = s.has(token) ? E::up(words[token - s.start]) : 0.0f;
         if (C > 1) {
-            if (threadIdx.x == 0) sh.slice = all;
+            if (threadIdx.x == 0) {
+                sh.slice = all;
+                if constexpr (Row::kNeedsToken) {
+                    sh.token = at;
+                    sh.holds = s.has(token);
+                }
+            }
             cluster.sync();
             if (warp == 0) {
-                all = warp_join(lane < C ? cluster.map_shared_rank(&sh, lane)->slice
-                                         : Sums{kLowest, 0.0f, 0.0f});
+                const RowShared *from = cluster.map_shared_rank(&sh, lane < C ? lane : 0);
+                all = warp_join(lane < C ? from->slice : Sums{kLowest, 0.0f, 0.0f});
                 if (lane == 0) sh.row = all;
+                if constexpr (Row::kNeedsToken)
+                    if (lane < C && from->holds) sh.row_token = from->token;
             }
             __syncthreads();
             all = sh.row;
+            if constexpr (Row::kNeedsToken)
+                if (token >= 0 && token < a.V) at = sh.row_token;
             cluster_arrive();              // the others' shared memory has been read
         }
         const bool ignored = token < 0, beyond = token >= a.V, empty = all.sum == 0.0f;
+        const Row r(a, t, at, all.ref, all.sum, logf(all.sum));
         // the CTA that holds the token (the first one for a token outside)
-        if (threadIdx.x == 0 && a.logp && (ignored || beyond ? rank == 0 : s.has(token))) {
-            const float x = sh.token;
-            const float lp = log_prob(x, all.ref, all.sum, logf(all.sum));
-            a.logp[t] = ignored ? 0.0f : beyond ? NAN : lp;
-        }
-        float w = a.weights ? a.weights[t] : 1.0f;
+        if (threadIdx.x == 0 && (ignored || beyond ? rank == 0 : s.has(token)))
+            r.write(a, t, ignored, beyond);
+        float w = r.w;
         if (beyond || all.sum != all.sum) w = NAN;    // 0 times a row of NaN is NaN too
         if (ignored || (empty && !beyond)) w = 0.0f;
         const float scale = __fdiv_rn(w, all.sum);
@@ -1060,10 +1144,10 @@ int stats_cluster(int64_t T, int64_t V, int size) {
 
 int row_grid(int64_t T, int c) { return (int)(T < (1 << 24) ? T : 1 << 24) * c; }
 
-template <int DT, int THREADS>
-cudaError_t launch_loss_threads(const TokenLogprobs &a, int c, int64_t slice, cudaStream_t st) {
+template <int DT, int THREADS, class Args>
+cudaError_t launch_loss_threads(const Args &a, int c, int64_t slice, cudaStream_t st) {
     static bool ready[kMaxDevices];
-    auto kernel = token_loss_kernel<DT, THREADS>;
+    auto kernel = token_loss_kernel<DT, THREADS, Args>;
     const cudaError_t e =
         allow_shared(kernel, THREADS == kRowThreads ? kMaxSliceBytes + 32 : 16 * THREADS * 16, ready);
     if (e != cudaSuccess) return e;
@@ -1073,8 +1157,8 @@ cudaError_t launch_loss_threads(const TokenLogprobs &a, int c, int64_t slice, cu
 // A CTA of as few threads as leave each at least eight vectors of its slice: 9870 rows of
 // 691 FP16 values take 28 us with a warp a row, 49 us with eight; 4000 rows of 10000 BF16
 // values 27 us with four warps, 45 us with eight.
-template <int DT>
-cudaError_t launch_loss(const TokenLogprobs &a, int c, cudaStream_t st) {
+template <int DT, class Args>
+cudaError_t launch_loss(const Args &a, int c, cudaStream_t st) {
     // a row that starts inside a vector has one vector more
     const int64_t vectors = (a.V + 2 * Elem<DT>::kVec - 2) / Elem<DT>::kVec;
     const int64_t slice = (vectors + c - 1) / c;
@@ -1224,6 +1308,20 @@ int grid_for(int64_t rows) {
     return (int)(rows < most ? rows : most);
 }
 
+template <class Args>
+cudaError_t launch_any_loss(const Args &a, cudaStream_t st) {
+    const int c = loss_cluster(a.T, a.V, a.dtype == kF32 ? 4 : 2);
+    if (c) {
+        return a.dtype == kF32    ? launch_loss<kF32>(a, c, st)
+               : a.dtype == kBF16 ? launch_loss<kBF16>(a, c, st)
+                                  : launch_loss<kF16>(a, c, st);
+    }
+    auto k = a.dtype == kF32    ? token_loss_long_kernel<kF32, Args>
+             : a.dtype == kBF16 ? token_loss_long_kernel<kBF16, Args>
+                                : token_loss_long_kernel<kF16, Args>;
+    return launch_pdl(k, grid_for(a.T), kThreads, 0, st, a);
+}
+
 }  // namespace
 
 cudaError_t launch_token_logprobs(const TokenLogprobs &a, cudaStream_t st) {
@@ -1232,16 +1330,11 @@ cudaError_t launch_token_logprobs(const TokenLogprobs &a, cudaStream_t st) {
                : a.dtype == kBF16 ? launch_stats<kBF16>(a, st)
                                   : launch_stats<kF16>(a, st);
     }
-    const int c = loss_cluster(a.T, a.V, a.dtype == kF32 ? 4 : 2);
-    if (c) {
-        return a.dtype == kF32    ? launch_loss<kF32>(a, c, st)
-               : a.dtype == kBF16 ? launch_loss<kBF16>(a, c, st)
-                                  : launch_loss<kF16>(a, c, st);
-    }
-    auto k = a.dtype == kF32    ? token_loss_long_kernel<kF32>
-             : a.dtype == kBF16 ? token_loss_long_kernel<kBF16>
-                                : token_loss_long_kernel<kF16>;
-    return launch_pdl(k, grid_for(a.T), kThreads, 0, st, a);
+    return launch_any_loss(a, st);
+}
+
+cudaError_t launch_policy_loss(const PolicyLoss &a, cudaStream_t st) {
+    return launch_any_loss(a, st);
 }
 
 namespace {

@@ -1,8 +1,8 @@
 /*
  * agoq.h -- C ABI of libagoq.so: the AGoQ element-wise quantization kernels,
- * the INT4-dequant-fused weight-gradient GEMM, and the output end of a training
- * step around them (layer norm, loss and log probabilities of tokens, gradient
- * norm and clipping), for NVIDIA GB300 (sm_103a).
+ * the INT4-dequant-fused weight-gradient GEMM, the output end of a training
+ * step around them (layer norm, losses and log probabilities of tokens, gradient
+ * norm and clipping), and micro-scaled 4-bit products, for NVIDIA GB300 (sm_103a).
  *
  * Method: "AGoQ: Activation and Gradient Quantization for Memory-Efficient
  * Distributed Training of LLMs" (gist.science summary page), sections
@@ -61,8 +61,8 @@ typedef enum {
     AGOQ_ERR_ALIAS = 5,   /* an output overlaps an input */
     AGOQ_ERR_CUDA = 6,    /* the CUDA runtime reported an error at launch */
     AGOQ_ERR_TIMEOUT = 7, /* a pipeline wait gave up (see agoq_device_status) */
-    AGOQ_ERR_FORMAT = 8   /* unsupported intermediate format (agoq_grad_accum_fp8_mid) or
-                             element type (agoq_dtype) */
+    AGOQ_ERR_FORMAT = 8   /* unsupported intermediate format (agoq_grad_accum_fp8_mid),
+                             element type (agoq_dtype) or agoq_fp4_format */
 } agoq_status;
 
 /* Intermediate formats of the QuanGrad accumulation (agoq_grad_accum_fp8_mid). */
@@ -577,9 +577,144 @@ agoq_status agoq_token_loss(const void *logits, int64_t ld, int dtype, const int
                             int64_t ldd, void *stream);
 
 /*
+ * The clipped policy loss of sampled tokens, with a KL term to a reference policy, and its
+ * gradient, reading the logits once where a row fits on chip.  With logp as
+ * agoq_token_logprobs, per row, in binary32:
+ *   r = e^(logp - old_logp);  lo = 1 - clip_low, hi = 1 + clip_high;
+ *   d = ref_logp - logp;      kl = e^d - d - 1     (an estimate of the divergence, >= 0)
+ *   loss = weights (-min(r A, min(max(r, lo), hi) A) + kl_coef kl),   A = advantages[t];
+ *   c = weights (r A + kl_coef (e^d - 1)), without r A where the ratio is clipped (A > 0 and
+ *       r > hi, or A < 0 and r < lo; at a bound itself it is not);
+ *   dlogits_i = R(c (p_i - [i = token])),  p_i = e^(x_i - m) / S.
+ *   tokens     : in, int64 [T].  A negative one is ignored: loss, logp, kl and the row of the
+ *                gradient are 0.  One >= V gives NaN in all of them.
+ *   old_logp, advantages : in, FP32 [T].
+ *   ref_logp   : in, FP32 [T], or NULL: no KL term (then kl is NULL and kl_coef 0).
+ *   weights    : in, FP32 [T], or NULL: 1.
+ *   clip_low   : 0 .. 1;  clip_high, kl_coef : 0 .. 10^6 (AGOQ_ERR_SHAPE).  With kl_coef 0
+ *                and a ref_logp, kl is reported and takes no part in the loss.
+ *   loss, logp, kl : out, FP32 [T]; any may be NULL.
+ *   dlogits    : out, rows of `dtype`, ldd >= V elements apart; in place of the logits is
+ *                allowed (the same address and row distance).
+ * A row with a NaN or +inf, and one whose c is not finite (a ratio or e^d beyond binary32, a
+ * NaN among its statistics), has a gradient of NaN.  A row of nothing but -inf has a gradient
+ * of 0.  A token of probability 0 has ratio 0 and, with a KL term, an infinite loss.  Other
+ * rules as agoq_token_loss.
+ */
+agoq_status agoq_policy_loss(const void *logits, int64_t ld, int dtype, const int64_t *tokens,
+                             const float *old_logp, const float *ref_logp, const float *advantages,
+                             const float *weights, int64_t T, int64_t V, float clip_low,
+                             float clip_high, float kl_coef, float *loss, float *logp, float *kl,
+                             void *dlogits, int64_t ldd, void *stream);
+
+/*
+ * The preference loss of P pairs of answers from the log probabilities of their tokens (paired
+ * log ratios), and its gradient in those.  Pair p has the chosen answer's tokens
+ * offsets[2p] .. offsets[2p+1] - 1 and the rejected one's offsets[2p+1] .. offsets[2p+2] - 1.
+ *   h = beta (sum_chosen (logp - ref_logp) - sum_rejected (logp - ref_logp));
+ *   loss = weights ((1 - e) ln(1 + e^-h) + e ln(1 + e^h)),  e = label_smoothing;
+ *   dlogp = -c at the chosen tokens, c at the rejected ones,  c = weights beta (1/(1+e^h) - e).
+ *   logp     : in, FP32 [T], as agoq_token_logprobs gives it (0 at ignored tokens, which
+ *              agoq_token_logprobs_backward then skips).
+ *   ref_logp : in, FP32 [T], or NULL: 0.
+ *   offsets  : in, int64 [2 P + 1] (device), ascending, within 0 .. T; answers may be empty.
+ *              A pair whose offsets are not has loss and margin NaN, and its dlogp is not
+ *              written.
+ *   weights  : in, FP32 [P], or NULL: 1.
+ *   beta     : 0 .. 10^6;  label_smoothing : 0 .. 1 (AGOQ_ERR_SHAPE).
+ *   loss, margin : out, FP32 [P] (margin is h), or NULL.
+ *   dlogp    : out, FP32 [T].  Tokens before the first and behind the last answer are left
+ *              as they were.
+ * Sums are kept with their rounding errors and joined in binary64, in a fixed order: results
+ * are deterministic.  T <= 2^40, P <= 2^30.
+ */
+agoq_status agoq_preference_loss(const float *logp, const float *ref_logp, const int64_t *offsets,
+                                 const float *weights, int64_t T, int64_t P, float beta,
+                                 float label_smoothing, float *loss, float *margin, float *dlogp,
+                                 void *stream);
+
+/*
+ * Micro-scaled 4-bit floating point (FP4): codes of E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a
+ * sign; bit 3 the sign) with a scale byte for every block of consecutive elements of a row.
+ *   AGOQ_MXFP4: blocks of 32, scale E8M0 (2^(byte - 127), 255 NaN).
+ *     e = max(floor(log2 absmax) - 2, -127), byte e + 127;  code = E2M1(x 2^-e)
+ *   AGOQ_NVFP4: blocks of 16, scale s E4M3, times the tensor's scale g, both in binary32:
+ *     g = max(fl(amax / 2688), 2^-100);  s = E4M3(fl(absmax / fl(6 g)));
+ *     code = E2M1(fl(x fl(1 / fl(s g)))), 0 where s is 0
+ * E2M1 and E4M3 round to nearest even and saturate.  The value is code 2^e or code s g.
+ * Storage of [rows][K]:
+ *   codes  : rows of ceil(K/32) * 16 bytes, two codes to a byte, the even element in the low
+ *            half; elements from K on are 0.
+ *   scales : tiles of 128 rows by 4 blocks, 512 bytes each, row blocks slowest
+ *            (ceil(rows/128) x ceil(blocks/4) tiles): block b of row r is byte
+ *            (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4 of tile (r / 128, b / 4); 0 where
+ *            there is no block.  (The tensor cores' own order: the product copies tiles as
+ *            they are.)
+ * Both 16-byte aligned.  1 <= K <= 2^24, rows <= 2^30.
+ */
+typedef enum { AGOQ_MXFP4 = 0, AGOQ_NVFP4 = 1 } agoq_fp4_format;
+
+/* Bytes of codes and scales of [rows][K] (-1 for sizes that the calls do not take). */
+int64_t agoq_fp4_code_bytes(int64_t rows, int64_t K);
+int64_t agoq_fp4_scale_bytes(int64_t rows, int64_t K, int format);
+
+/*
+ * *amax = the largest magnitude of x (0 of nothing, NaN if there is one): the tensor scale of
+ * AGOQ_NVFP4 is taken from it.  A user with a magnitude at hand (a running one, the largest
+ * over ranks) passes that instead; larger elements saturate.
+ *   x    : in, T <= 2^30 rows of K <= 2^40 elements of `dtype`, ldx >= K apart.
+ *   amax : out, one FP32 (device).
+ */
+agoq_status agoq_amax(const void *x, int64_t ldx, int64_t T, int64_t K, int dtype, float *amax,
+                      void *stream);
+
+/*
+ * Quantise x [T][K] along its rows (codes, scales: of [T][K]), along its columns (codes_t,
+ * scales_t: of the transposed [K][T], blocks along T), or both in one reading.  A linear layer
+ * Y = X W^T multiplies rows of X by rows of W; its gradients dX = dY W and dW = dY^T X sum over
+ * the other dimension of W, dY and X and take their columns.
+ *   x      : in, rows of `dtype`, ldx >= K elements apart, aligned to its elements.
+ *   format : agoq_fp4_format.
+ *   amax   : in, one FP32 (device); AGOQ_NVFP4 only.
+ *   codes and scales, codes_t and scales_t : out; a pair may be NULL, not both.  With codes_t
+ *            T <= 2^24.
+ * A block with a NaN or an infinity has the NaN of its scale's type and codes of 0; with an
+ * amax that is not finite every block has.  Whole codes and scales are written, padding
+ * included.
+ */
+agoq_status agoq_fp4_quant(const void *x, int64_t ldx, int64_t T, int64_t K, int dtype, int format,
+                           const float *amax, void *codes, void *scales, void *codes_t,
+                           void *scales_t, void *stream);
+
+/*
+ * The values again: y = R(fl(fl(code s) g)), or R(fl(code 2^e)).
+ *   y : out, T rows of K elements of `dtype`, ldy >= K apart.
+ */
+agoq_status agoq_fp4_dequant(const void *codes, const void *scales, const float *amax, int64_t T,
+                             int64_t K, int format, void *y, int64_t ldy, int dtype, void *stream);
+
+/*
+ * Product of two stored operands on the block-scaled tensor cores:
+ *   d[m][n] = R(fl(fl(acc g) g')),  acc = sum_k a[m][k] b[n][k] of code times block scale,
+ * g the smaller, g' the larger of the operands' tensor scales (AGOQ_MXFP4: R(acc)).  The sum is
+ * the tensor cores', in binary32, in an order of theirs.
+ *   a_codes, a_scales, a_amax : in, [M][K] as agoq_fp4_quant writes it (amax AGOQ_NVFP4 only);
+ *   b_codes, b_scales, b_amax : in, [N][K], of the same format.
+ *   d : out, M rows of N elements of `dtype`, ldd >= N apart, aligned to its elements (rows at
+ *       16-byte boundaries are written in vectors).
+ * M and N from 0 (a no-op), ceil(M/128) * ceil(N/128) <= 2^26.  Where one of them is at most
+ * 64, the CTAs of a tile share its K and join their sums in a fixed order.  An operand's NaN
+ * scale gives NaN in its row of d.  Pipeline waits are time-limited: see agoq_device_status.
+ */
+agoq_status agoq_fp4_gemm(const void *a_codes, const void *a_scales, const float *a_amax,
+                          const void *b_codes, const void *b_scales, const float *b_amax,
+                          int64_t M, int64_t N, int64_t K, int format, void *d, int64_t ldd,
+                          int dtype, void *stream);
+
+/*
  * Synchronise `stream`, then read and clear the library's device-side status
  * words for the current device.  Returns AGOQ_ERR_TIMEOUT if a pipeline wait
- * of a GEMM (agoq_wgrad_gemm_int4*, agoq_fwd_gemm_quant), of the staged
+ * of a GEMM (agoq_wgrad_gemm_int4*, agoq_fwd_gemm_quant, agoq_fp4_gemm), of the staged
  * shard reduce (agoq_reduce_fp8_shards), of the staged QuanGrad accumulation
  * (agoq_grad_accum_fp8, agoq_grad_accum_fp8_mid) or of the staged RMSNorm dw
  * (agoq_rmsnorm_backward) exceeded its time limit since the last call (that
