@@ -9,12 +9,13 @@
 //   warp 0      TMA: a stage is 256 elements of K: 128-byte rows of codes of P and Q with the
 //               128-byte swizzle, and the scale tiles of those rows, which lie in memory one
 //               after another, by plain bulk copies;
-//   warp 1      copies the stage's scale tiles to tensor memory (tcgen05.cp) and issues an MMA
-//               for every 64 elements of K that the operands have (the last stage of a K that
-//               is no multiple of 256 has fewer: what lies behind them is never read);
-//   the others  the epilogue, a row of D a thread.
-// Every stage has scale columns of its own, so a copy never overwrites scales that an MMA may
-// still read.  Every wait is time-limited (gemm_common.cuh).
+//   warps 2-5   write a stage's scales to tensor memory, each to the lanes that it reaches: the
+//               MMA wants them in all four lane quarters;
+//   warp 1      issues an MMA for every 64 elements of K that the operands have (the last stage
+//               of a K that is no multiple of 256 has fewer: what lies behind is never used);
+//   the others  the epilogue (SPLIT: warps 2-5).
+// Every stage has scale columns of its own, so that a write never meets an MMA that still reads.
+// Every wait is time-limited (gemm_common.cuh).
 #include <algorithm>
 
 #include "agoq_launch.h"
@@ -31,7 +32,6 @@ __device__ unsigned g_fp4_status;
 
 constexpr int BM = 128, BK = 256;                   // P rows of a CTA, elements of a stage
 constexpr int kRowBytes = BK / 2;                   // 128: the swizzle's span
-constexpr int kThreadsMma = 64;                     // warps 0 and 1
 
 struct Fp4Args {
     const uint8_t *p_scales, *q_scales;
@@ -42,30 +42,22 @@ struct Fp4Args {
     int64_t ldd;
     int dtype;
     bool swapped;                                   // P is B: D[q][p]
-    bool vectors;                                   // rows of D at 16-byte boundaries
+    bool vectors, whole;                            // rows of D begin, and end, at 16-byte boundaries
 };
 
 // ---- instructions -----------------------------------------------------------------------
-template <int GROUP>
-__device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc) {
-    if constexpr (GROUP == 2)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
-
 #define AGOQ_FP4_MMA(GROUP, KIND)                                                                   \
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                  \
                  "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%5], [%6], p;" \
                  "\n\t}" ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) \
                  : "memory")
-template <int FMT, int GROUP>
+template <int FMT, bool PAIR>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-    if constexpr (FMT == kNv && GROUP == 1) AGOQ_FP4_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
-    if constexpr (FMT == kNv && GROUP == 2) AGOQ_FP4_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
-    if constexpr (FMT == kMx && GROUP == 1) AGOQ_FP4_MMA("1", "mxf4.block_scale.scale_vec::2X");
-    if constexpr (FMT == kMx && GROUP == 2) AGOQ_FP4_MMA("2", "mxf4.block_scale.scale_vec::2X");
+    if constexpr (FMT == kNv && !PAIR) AGOQ_FP4_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    if constexpr (FMT == kNv && PAIR) AGOQ_FP4_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    if constexpr (FMT == kMx && !PAIR) AGOQ_FP4_MMA("1", "mxf4.block_scale.scale_vec::2X");
+    if constexpr (FMT == kMx && PAIR) AGOQ_FP4_MMA("2", "mxf4.block_scale.scale_vec::2X");
 }
 #undef AGOQ_FP4_MMA
 
@@ -75,16 +67,6 @@ __device__ __forceinline__ void commit_one(uint64_t *bar) {
                  : "memory");
 }
 
-// A scale tile in shared memory: 32 rows of 16 bytes without swizzle, 8-row groups 128 bytes
-// apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(128u >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    return d;
-}
-
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -92,43 +74,88 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
 }
+// To the same place in every CTA of `mask`, and to its barrier.
+__device__ __forceinline__ void bulk_load_multicast(void *dst, const void *src, uint32_t bytes,
+                                                    uint64_t *bar, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"(mask)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_multicast(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                                      int x, int y, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "h"(mask)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Wait until at most N of this thread's stores still read shared memory.
+template <int N>
+__device__ __forceinline__ void stores_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 
 // ---- shapes of a variant ------------------------------------------------------------------
 //
-// BN columns of D a tile.  PAIR: the two CTAs of a cluster share an MMA over 256 rows of P and
-// BN of Q, half of whose codes each of them loads (the scales of all BN both need).  SPLIT: the
-// CTAs of a cluster each take a part of K of one tile and join their sums.
-template <int FMT, int BN_, bool PAIR_, bool SPLIT_>
+// BN columns of D a tile.  PAIRS > 0: the two CTAs of a pair share an MMA over 256 rows of P and
+// BN of Q, half of whose codes each of them holds; the PAIRS pairs of a cluster take tiles next
+// to each other along P, and what their CTAs hold alike (codes of Q, scales of Q) is loaded
+// once, a part by each, and multicast.  SPLIT: the CTAs of a cluster each take a part of K of
+// one tile and join their sums.
+template <int FMT, int BN_, int PAIRS_, bool SPLIT_>
 struct Shape {
-    static constexpr int BN = BN_;
-    static constexpr bool PAIR = PAIR_, SPLIT = SPLIT_;
-    static constexpr int kCtas = PAIR ? 2 : 1;
-    static constexpr int kTileRows = BM * kCtas;
-    static constexpr int kQRows = BN / kCtas;
+    static constexpr int BN = BN_, PAIRS = PAIRS_;
+    static constexpr bool PAIR = PAIRS > 0, SPLIT = SPLIT_;
+    static constexpr int kCluster = PAIR ? 2 * PAIRS : 1;       // (SPLIT: given at launch)
+    static constexpr int kTileRows = BM * kCluster;             // of a cluster
+    static constexpr int kQRows = PAIR ? BN / 2 : BN;           // held by a CTA
+    static constexpr int kQLoad = PAIR ? kQRows / PAIRS : BN;   // loaded by a CTA
     static constexpr int kQTiles = (BN + 127) / 128;            // row blocks of Q's scales
     static constexpr int kTiles = BK / fp4_tile_elems(FMT);     // scale tiles of a stage
     static constexpr int kPBytes = BM * kRowBytes, kQBytes = kQRows * kRowBytes;
     static constexpr int kPScales = kTiles * kScaleTile, kQScales = kQTiles * kTiles * kScaleTile;
-    static constexpr int kStages = SPLIT ? (BN > 32 ? 3 : 4) : 5;
-    static constexpr int kEpiWarps = SPLIT ? 4 : 8;
-    static constexpr int kThreads = kThreadsMma + 32 * kEpiWarps;
+    static constexpr int kStages = SPLIT && BN > 32 ? 3 : 4;
+    static constexpr int kScaleWarps = 4, kEpiWarps = SPLIT ? 0 : 8;
+    static constexpr int kThreads = 64 + 32 * (kScaleWarps + kEpiWarps);
     static constexpr int kBuffers = !SPLIT && BN <= 128 ? 2 : 1;   // accumulators
     static constexpr int kScaleCols = 4 * kTiles * (1 + kQTiles);
     static constexpr int kUsedCols = kBuffers * BN + kStages * kScaleCols;
     static constexpr int kTmemCols = kUsedCols <= 256 ? 256 : 512;
     static constexpr int kOffQ = kStages * kPBytes;
-    static constexpr int kOffPS = kOffQ + kStages * kQBytes;
+    static constexpr int kOffOut = kOffQ + kStages * kQBytes;
+    static constexpr int kOutBytes = SPLIT ? 0 : 2 * 4096;      // an epilogue warp's two buffers
+    static constexpr int kOffPS = kOffOut + kEpiWarps * kOutBytes;
     static constexpr int kOffQS = kOffPS + kStages * kPScales;
-    static constexpr int kOffRows = kOffQS + kStages * kQScales;
-    static constexpr int kPitch = 17;                           // staged rows of 16 values
-    static constexpr int kRowsBytes = SPLIT ? 0 : kEpiWarps * 32 * kPitch * 4;
-    static constexpr int kOffBar = kOffRows + kRowsBytes;
+    static constexpr int kOffBar = kOffQS + kStages * kQScales;
     static constexpr int kBars = 3 * kStages + 2 * kBuffers + 1;
     static constexpr int kOffMisc = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffMisc + 16 + 1024;
     static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
                                        (FMT == kMx ? 1u << 23 : 0u) |
-                                       ((uint32_t)(kTileRows >> 4) << 24);
+                                       ((uint32_t)((PAIR ? 256 : 128) >> 4) << 24);
     static_assert(kUsedCols <= 512, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(!SPLIT || BM * BN * 4 <= kStages * kPBytes, "the sums take the stages' place");
@@ -144,46 +171,106 @@ __device__ __forceinline__ void tile_at(int tile, int num_p, int num_q, int &tp,
     tq = band * kBand + r % nb;
 }
 
-// 32 columns of D's row, as vectors.
-__device__ __forceinline__ void store32(void *row, int64_t col, int dtype, const float *v) {
-    if (dtype == kF32) {
-        uint4 *to = reinterpret_cast<uint4 *>(static_cast<float *>(row) + col);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) to[i] = Elem<kF32>::pack(v + 4 * i);
-    } else if (dtype == kBF16) {
-        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] = Elem<kBF16>::pack(v + 8 * i);
-    } else {
-        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] = Elem<kF16>::pack(v + 8 * i);
-    }
-}
 __device__ __forceinline__ void store1(void *d, int64_t i, int dtype, float v) {
     if (dtype == kF32) store_elem<kF32>(d, i, v);
     else if (dtype == kBF16) store_elem<kBF16>(d, i, v);
     else store_elem<kF16>(d, i, v);
 }
 
+// 128 bytes of an output row: from 32 or 64 columns of the accumulator on.
+template <int FMT, int DT>
+__device__ __forceinline__ void load_out(uint32_t from, float g0, float g1, uint4 (&o)[8]) {
+    constexpr int N = DT == kF32 ? 1 : 2;
+#pragma unroll
+    for (int h = 0; h < N; ++h) {
+        uint32_t w[32];
+        tmem_ld32(from + 32 * h, w);
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            v[i] = __uint_as_float(w[i]);
+            if constexpr (FMT == kNv) v[i] = __fmul_rn(__fmul_rn(v[i], g0), g1);
+        }
+#pragma unroll
+        for (int i = 0; i < 8 / N; ++i) o[8 / N * h + i] = Elem<DT>::pack(v + Elem<DT>::kVec * i);
+    }
+}
+
+// An epilogue warp's 32 rows x CW columns by TMA: 128-byte wide boxes, swizzled so that the
+// lanes' 16-byte stores meet no bank twice; two buffers in turn.  `free_acc` is called once the
+// accumulator has been read.
+template <int FMT, int DT, int CW, class F>
+__device__ __forceinline__ void store_boxes(const CUtensorMap *map, uint8_t *buf, uint32_t from, int row,
+                                            int col, const Fp4Args &a, float g0, float g1, int lane,
+                                            F free_acc) {
+    constexpr int kCols = DT == kF32 ? 32 : 64;
+#pragma unroll
+    for (int c = 0; c < CW / kCols; ++c) {
+        uint4 o[8];
+        load_out<FMT, DT>(from + c * kCols, g0, g1, o);
+        if (c == CW / kCols - 1) free_acc();
+        uint8_t *to = buf + (c & 1) * 4096;
+        if (lane == 0) stores_read<CW / kCols >= 2 ? 1 : 0>();   // this buffer's last store
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(to + lane * 128 + ((i ^ (lane & 7)) << 4)) = o[i];
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            if (row < a.P && col + c * kCols < a.Q) tma_store_2d(map, to, col + c * kCols, row);
+            else asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+
+// The same where D's rows do not lie at 16-byte boundaries: a row of 32 values at a time.
+template <int FMT, int CW, class F>
+__device__ __forceinline__ void store_rows(uint8_t *buf, uint32_t from, int row0, int col, const Fp4Args &a,
+                                           float g0, float g1, int lane, F free_acc) {
+    constexpr int kPitch = 33;
+    float *rows = reinterpret_cast<float *>(buf);
+    if (lane == 0) stores_read<0>();                // boxes of an earlier tile
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < CW; c += 32) {
+        uint32_t w[32];
+        __syncwarp();
+        tmem_ld32(from + c, w);
+        if (c == CW - 32) free_acc();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            float v = __uint_as_float(w[i]);
+            if constexpr (FMT == kNv) v = __fmul_rn(__fmul_rn(v, g0), g1);
+            rows[lane * kPitch + i] = v;
+        }
+        __syncwarp();
+        const int n = min(32, a.P - row0);
+        if (col + c + lane < a.Q)
+            for (int r = 0; r < n; ++r)
+                store1(a.d, (int64_t)(row0 + r) * a.ldd + col + c + lane, a.dtype, rows[r * kPitch + lane]);
+    }
+    __syncwarp();
+}
+
 template <int FMT, class S>
 __global__ void __launch_bounds__(S::kThreads, 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-                const Fp4Args a) {
-    constexpr int NS = S::kStages, BN = S::BN, kGroup = S::PAIR ? 2 : 1;
+                const __grid_constant__ CUtensorMap map_d, const Fp4Args a) {
+    constexpr int NS = S::kStages, BN = S::BN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *sp = smem, *sq = smem + S::kOffQ, *sps = smem + S::kOffPS, *sqs = smem + S::kOffQS;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kOffBar);
-    uint64_t *full = bars, *empty = bars + NS, *ready = bars + 2 * NS, *tfull = bars + 3 * NS,
+    uint64_t *full = bars, *empty = bars + NS, *scaled = bars + 2 * NS, *tfull = bars + 3 * NS,
              *tempty = tfull + S::kBuffers, *drain = tempty + S::kBuffers;
     uint32_t *tmem_addr = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
     unsigned *status = &g_fp4_status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S::PAIR || S::SPLIT ? (int)cluster_ctarank() : 0;
-    const int pair_rank = S::PAIR ? rank : 0;
+    const int pair = S::PAIR ? rank >> 1 : 0, side = S::PAIR ? rank & 1 : 0;
     uint32_t csize = 1;
     if constexpr (S::PAIR || S::SPLIT) asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
     const int C = (int)csize;
@@ -201,12 +288,12 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-            mbar_init(&ready[s], 1);
+            mbar_init(&empty[s], S::PAIR ? S::PAIRS : 1);       // all that read what is multicast
+            mbar_init(&scaled[s], S::kScaleWarps * (S::PAIR ? 2 : 1));
         }
         for (int b = 0; b < S::kBuffers; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], S::kEpiWarps * S::kCtas);
+            mbar_init(&tempty[b], S::SPLIT ? 1 : S::kEpiWarps * (S::PAIR ? 2 : 1));
         }
         mbar_init(drain, 1);
         *abort = 0;
@@ -226,20 +313,25 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if constexpr (S::PAIR) cluster_sync_all();       // the peer's barriers are initialised
+    if constexpr (S::PAIR) cluster_sync_all();       // the others' barriers are initialised
     const uint32_t tmem = *tmem_addr;
+    const uint32_t scale_cols = tmem + S::kBuffers * BN;
     // (after the allocation: a following launch may start and allocate only once every CTA of
     // this one has its columns)
     pdl_wait_and_release();
 
     if (warp == 0) {
         if (lane == 0) {
+            const uint16_t everyone = (uint16_t)((1u << S::kCluster) - 1);
+            uint16_t alike = 0;                      // CTAs that hold the same codes of Q
+#pragma unroll
+            for (int i = 0; i < (S::PAIR ? S::PAIRS : 0); ++i) alike |= (uint16_t)(1u << (2 * i + side));
             uint32_t it = 0;
             bool ok = true;
             for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
                 int tp, tq;
                 tile_at(tile, num_p, num_q, tp, tq);
-                const int p0 = tp * S::kTileRows + BM * pair_rank, q0 = tq * BN;
+                const int p0 = tp * S::kTileRows + BM * (S::PAIR ? rank : 0), q0 = tq * BN;
                 const int p_block = p0 / 128, q_block = q0 / 128;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % NS;
@@ -256,18 +348,30 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                         if (q_block + i < a.q_down) all += bytes;
                     mbar_expect_tx(&full[s], all);
                     tma_load_2d(sp + s * S::kPBytes, &map_p, &full[s], kb * kRowBytes, p0);
-                    tma_load_2d(sq + s * S::kQBytes, &map_q, &full[s], kb * kRowBytes,
-                                q0 + S::kQRows * pair_rank);
+                    uint8_t *qto = sq + s * S::kQBytes + pair * S::kQLoad * kRowBytes;
+                    const int qrow = q0 + S::kQRows * side + S::kQLoad * pair;
+                    if constexpr (S::PAIRS > 1)
+                        tma_load_2d_multicast(qto, &map_q, &full[s], kb * kRowBytes, qrow, alike);
+                    else
+                        tma_load_2d(qto, &map_q, &full[s], kb * kRowBytes, qrow);
                     if (p_block < a.p_down)
                         bulk_load(sps + s * S::kPScales,
                                   a.p_scales + ((int64_t)p_block * a.across + kb * S::kTiles) * kScaleTile,
                                   bytes, &full[s]);
-#pragma unroll
-                    for (int i = 0; i < S::kQTiles; ++i)
-                        if (q_block + i < a.q_down)
-                            bulk_load(sqs + s * S::kQScales + i * S::kTiles * kScaleTile,
-                                      a.q_scales + ((int64_t)(q_block + i) * a.across + kb * S::kTiles) * kScaleTile,
-                                      bytes, &full[s]);
+                    if constexpr (S::PAIR) {
+                        // side 0 the first row block's scales, side 1 the second's, a part by each
+                        // pair
+                        const uint32_t part = bytes / S::PAIRS;
+                        if (q_block + side < a.q_down)
+                            bulk_load_multicast(
+                                sqs + s * S::kQScales + side * S::kTiles * kScaleTile + pair * part,
+                                a.q_scales + ((int64_t)(q_block + side) * a.across + kb * S::kTiles) * kScaleTile + pair * part,
+                                part, &full[s], everyone);
+                    } else if (q_block < a.q_down) {
+                        bulk_load(sqs + s * S::kQScales,
+                                  a.q_scales + ((int64_t)q_block * a.across + kb * S::kTiles) * kScaleTile,
+                                  bytes, &full[s]);
+                    }
                 }
             }
             for (int d = 0; d < NS && d < (int)it; ++d) {
@@ -276,34 +380,26 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && pair_rank == 0) {
+        if (lane == 0 && side == 0) {
+            const uint16_t everyone = (uint16_t)((1u << S::kCluster) - 1), mine = (uint16_t)(3u << (2 * pair));
             uint32_t it = 0, t = 0;
             bool ok = true, issued = false;
             for (int tile = cid; ok && tile < num_tiles; tile += ncl, ++t) {
                 const int buf = t % S::kBuffers;
-                if (!wait_bar(&tempty[buf], ((t / S::kBuffers) & 1u) ^ 1u, abort, status)) break;
+                if (!S::SPLIT && !wait_bar(&tempty[buf], ((t / S::kBuffers) & 1u) ^ 1u, abort, status)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % NS;
+                    // both CTAs' scales are in place, and with them their codes
                     if (!wait_bar(&full[s], (it / NS) & 1u, abort, status) ||
-                        (S::PAIR && !wait_bar(&ready[s], (it / NS) & 1u, abort, status))) {
+                        !wait_bar(&scaled[s], (it / NS) & 1u, abort, status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t cols = tmem + S::kBuffers * BN + s * S::kScaleCols;
-                    const uint32_t qcols = cols + 4 * S::kTiles;
-                    const uint32_t ps = smem_u32(sps + s * S::kPScales), qs = smem_u32(sqs + s * S::kQScales);
-                    const int tiles = min(S::kTiles, a.across - kb * S::kTiles);
+                    const uint32_t cols = scale_cols + s * S::kScaleCols, qcols = cols + 4 * S::kTiles;
                     const int steps = min(4, (a.K - kb * BK + 63) / 64);
-                    for (int j = 0; j < tiles; ++j) {
-                        scale_copy<kGroup>(cols + 4 * j, scale_desc(ps + j * kScaleTile));
-#pragma unroll
-                        for (int i = 0; i < S::kQTiles; ++i)
-                            scale_copy<kGroup>(qcols + 4 * (j * S::kQTiles + i),
-                                               scale_desc(qs + (i * S::kTiles + j) * kScaleTile));
-                    }
                     const uint64_t pd = sw128_kmajor_desc(smem_u32(sp + s * S::kPBytes));
                     const uint64_t qd = sw128_kmajor_desc(smem_u32(sq + s * S::kQBytes));
 #pragma unroll
@@ -312,16 +408,15 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                         // a step is 32 bytes of a row; MXFP4: two scales of a tile's four
                         const int j = FMT == kNv ? kk : kk >> 1;
                         const uint32_t id = FMT == kNv ? 0 : 2 * (kk & 1);
-                        mma_fp4<FMT, kGroup>(d, pd + 2 * kk, qd + 2 * kk,
-                                             S::kIdesc | (id << 29) | (id << 4), cols + 4 * j,
-                                             qcols + 4 * j * S::kQTiles, kb > kb0 || kk > 0);
+                        mma_fp4<FMT, S::PAIR>(d, pd + 2 * kk, qd + 2 * kk, S::kIdesc | (id << 29) | (id << 4),
+                                              cols + 4 * j, qcols + 4 * j * S::kQTiles, kb > kb0 || kk > 0);
                     }
                     issued = true;
-                    if constexpr (S::PAIR) umma_commit_pair_multicast(&empty[s], 3);
+                    if constexpr (S::PAIR) umma_commit_pair_multicast(&empty[s], everyone);
                     else commit_one(&empty[s]);
                 }
                 if (!ok) break;
-                if constexpr (S::PAIR) umma_commit_pair_multicast(&tfull[buf], 3);
+                if constexpr (S::PAIR) umma_commit_pair_multicast(&tfull[buf], mine);
                 else if (kb0 < kb1) commit_one(&tfull[buf]);
             }
             if (issued) {
@@ -329,28 +424,77 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 else commit_one(drain);
                 wait_bar(drain, 0u, abort, status, true);
             }
-        } else if (S::PAIR && lane == 0) {
-            // CTA 1: each landed stage is announced to CTA 0
-            const uint32_t ready0 = mapa_shared(smem_u32(ready), 0);
-            uint32_t it = 0;
-            bool ok = true;
-            for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % NS;
-                    if (!wait_bar(&full[s], (it / NS) & 1u, abort, status)) {
-                        ok = false;
-                        break;
+        }
+    } else if (warp < 2 + S::kScaleWarps) {
+        // scales: P's tiles, then Q's, four columns each
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t scaled0 = S::PAIR ? mapa_shared(smem_u32(scaled), rank & ~1) : 0u;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % NS;
+                if (!warp_wait(&full[s], (it / NS) & 1u, abort, status)) {
+                    ok = false;
+                    break;
+                }
+                uint32_t w[S::kScaleCols];
+#pragma unroll
+                for (int j = 0; j < S::kTiles; ++j) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(sps + s * S::kPScales + j * kScaleTile + lane * 16);
+                    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+                }
+#pragma unroll
+                for (int j = 0; j < S::kTiles; ++j) {
+#pragma unroll
+                    for (int i = 0; i < S::kQTiles; ++i) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            sqs + s * S::kQScales + (i * S::kTiles + j) * kScaleTile + lane * 16);
+                        const int c = 4 * (S::kTiles + j * S::kQTiles + i);
+                        w[c] = v.x, w[c + 1] = v.y, w[c + 2] = v.z, w[c + 3] = v.w;
                     }
-                    mbar_arrive_remote(ready0 + (uint32_t)s * 8u);
+                }
+                const uint32_t to = scale_cols + s * S::kScaleCols + lanes;
+#pragma unroll
+                for (int c = 0; c + 16 <= S::kScaleCols; c += 16) tmem_st16(to + c, w + c);
+                if constexpr (S::kScaleCols % 16 != 0) tmem_st8(to + S::kScaleCols / 16 * 16, w + S::kScaleCols / 16 * 16);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (S::PAIR && side != 0) mbar_arrive_remote(scaled0 + (uint32_t)s * 8u);
+                    else mbar_arrive(&scaled[s]);
                 }
             }
         }
-    } else if constexpr (!S::SPLIT) {
+        if constexpr (S::SPLIT) {
+            // this CTA's part of the sums, as [column][row], in the stages' place
+            float *sums = reinterpret_cast<float *>(smem);
+            const bool any = kb0 < kb1;
+            if (any) {
+                ok = ok && warp_wait(&tfull[0], 0u, abort, status);
+                tc_fence_after();
+            }
+            if (ok) {
+#pragma unroll
+                for (int c = 0; c < BN; c += 32) {
+                    uint32_t w[32];
+                    if (any) {
+                        __syncwarp();
+                        tmem_ld32(tmem + lanes + c, w);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        sums[(c + i) * BM + 32 * (warp & 3) + lane] = any ? __uint_as_float(w[i]) : 0.0f;
+                }
+            }
+        }
+    } else {
         // lane quarter of tensor memory: warp % 4; columns: half of the tile's
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        constexpr int CW = BN / (S::kEpiWarps / 4);
-        float *rows = reinterpret_cast<float *>(smem + S::kOffRows) + (warp - 2) * 32 * S::kPitch;
-        const uint32_t tempty0 = S::PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
+        const int q = warp & 3, e = warp - 2 - S::kScaleWarps, half = e >> 2;
+        constexpr int CW = BN / 2;
+        uint8_t *buf_out = smem + S::kOffOut + e * S::kOutBytes;
+        const uint32_t tempty0 = S::PAIR ? mapa_shared(smem_u32(tempty), rank & ~1) : 0u;
         // the smaller tensor scale first: no overflow or underflow on the way
         float g0 = 1.0f, g1 = 1.0f;
         if constexpr (FMT == kNv) {
@@ -358,7 +502,6 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             g0 = fminf(gp, gq);
             g1 = fmaxf(gp, gq);
         }
-        const int es = a.dtype == kF32 ? 4 : 2;
         uint32_t t = 0;
         for (int tile = cid; tile < num_tiles; tile += ncl, ++t) {
             const int buf = t % S::kBuffers;
@@ -367,78 +510,25 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             int tp, tq;
             tile_at(tile, num_p, num_q, tp, tq);
             const uint32_t from = tmem + ((uint32_t)(32 * q) << 16) + buf * BN + half * CW;
-            float v[CW];
-#pragma unroll
-            for (int c = 0; c < CW; c += 32) {
-                uint32_t w[32];
-                tmem_ld32(from + c, w);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[c + i] = __uint_as_float(w[i]);
-            }
+            const int row = tp * S::kTileRows + BM * (S::PAIR ? rank : 0) + 32 * q, col = tq * BN + half * CW;
             // the accumulator is free as soon as it has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (S::PAIR && rank != 0) mbar_arrive_remote(tempty0 + (uint32_t)buf * 8u);
-                else mbar_arrive(&tempty[buf]);
-            }
-            if constexpr (FMT == kNv) {
-#pragma unroll
-                for (int i = 0; i < CW; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], g0), g1);
-            }
-            const int r0 = tp * S::kTileRows + BM * pair_rank + 32 * q, row = r0 + lane;
-            const int c0 = tq * BN + half * CW;
-            if (a.swapped) {
-#pragma unroll
-                for (int i = 0; i < CW; ++i)
-                    if (c0 + i < a.Q && row < a.P) store1(a.d, (int64_t)(c0 + i) * a.ldd + row, a.dtype, v[i]);
-                continue;
-            }
-            char *out = static_cast<char *>(a.d) + (int64_t)row * a.ldd * es;
-#pragma unroll
-            for (int c = 0; c < CW; c += 32) {
-                if (a.vectors && c0 + c + 32 <= a.Q) {
-                    if (row < a.P) store32(out, c0 + c, a.dtype, v + c);
-                    continue;
+            auto free_acc = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (S::PAIR && side != 0) mbar_arrive_remote(tempty0 + (uint32_t)buf * 8u);
+                    else mbar_arrive(&tempty[buf]);
                 }
-                // rows that no vector fits: two rows of 16 values a step
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) rows[lane * S::kPitch + i] = v[c + 16 * h + i];
-                    __syncwarp();
-                    const int col = c0 + c + 16 * h + (lane & 15);
-                    for (int r = lane >> 4; r < 32; r += 2)
-                        if (r0 + r < a.P && col < a.Q)
-                            store1(a.d, (int64_t)(r0 + r) * a.ldd + col, a.dtype,
-                                   rows[r * S::kPitch + (lane & 15)]);
-                }
-            }
+            };
+            // (a box across the end of rows that are no whole 16-byte vectors would write up to the
+            // next vector's end)
+            const bool boxes = a.vectors && (a.whole || col + CW <= a.Q);
+            if (!boxes) store_rows<FMT, CW>(buf_out, from, row, col, a, g0, g1, lane, free_acc);
+            else if (a.dtype == kF32) store_boxes<FMT, kF32, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
+            else if (a.dtype == kBF16) store_boxes<FMT, kBF16, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
+            else store_boxes<FMT, kF16, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
         }
-    } else {
-        // this CTA's part of the sums, as [column][row], in the stages' place
-        const int q = warp & 3;
-        float *sums = reinterpret_cast<float *>(smem);
-        const bool any = kb0 < kb1;
-        bool ok = true;
-        if (any) {
-            ok = warp_wait(&tfull[0], 0u, abort, status);
-            tc_fence_after();
-        }
-        if (ok) {
-#pragma unroll
-            for (int c = 0; c < BN; c += 32) {
-                uint32_t w[32];
-                if (any) {
-                    __syncwarp();
-                    tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + c, w);
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    sums[(c + i) * BM + 32 * q + lane] = any ? __uint_as_float(w[i]) : 0.0f;
-            }
-        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     tc_fence_before();
@@ -477,7 +567,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         }
     }
     // No CTA of a cluster frees tensor memory or exits while another may arrive on its barriers,
-    // read its shared memory or have a shared MMA run on it.
+    // read or write its shared memory or have a shared MMA run on it.
     if constexpr (S::PAIR || S::SPLIT) cluster_sync_all();
     if (warp == 1) {
         __syncwarp();
@@ -497,23 +587,59 @@ bool encode_codes(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64_t 
                      kRowBytes, (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Clusters that can be resident at once (once a device).
+template <class K>
+int resident_clusters(K kernel, int cluster, int threads, size_t smem, int *cache) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDevices) dev = 0;
+    if (cache[dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(sm_count() / cluster * cluster);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0)
+            n = std::max(1, sm_count() / cluster);
+        cache[dev] = n;
+    }
+    return cache[dev];
+}
+
 template <int FMT, class S>
 cudaError_t launch_shape(const Fp4Args &a, const uint8_t *p_codes, const uint8_t *q_codes, int split,
                          cudaStream_t st) {
-    CUtensorMap mp, mq;
-    if (!encode_codes(&mp, p_codes, a.P, a.K, BM) || !encode_codes(&mq, q_codes, a.Q, a.K, S::kQRows))
+    CUtensorMap mp, mq, md{};
+    if (!encode_codes(&mp, p_codes, a.P, a.K, BM) || !encode_codes(&mq, q_codes, a.Q, a.K, S::kQLoad))
         return cudaErrorInvalidValue;
+    if (!S::SPLIT && a.vectors) {
+        const int es = a.dtype == kF32 ? 4 : 2;
+        const CUtensorMapDataType dt = a.dtype == kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : a.dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        if (!encode_2d(&md, dt, a.d, (uint64_t)a.Q, (uint64_t)a.P, (uint64_t)a.ldd * es, 128 / es, 32,
+                       CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
     auto kernel = fp4_gemm_kernel<FMT, S>;
     static bool ready[kMaxDevices];
     const cudaError_t e = allow_shared(kernel, S::kSmem, ready);
     if (e != cudaSuccess) return e;
-    const int cluster = S::PAIR ? 2 : split;
+    const int cluster = S::SPLIT ? split : S::kCluster;
     const int64_t tiles = ((int64_t)a.P + S::kTileRows - 1) / S::kTileRows * (((int64_t)a.Q + S::BN - 1) / S::BN);
     int64_t clusters = tiles;
-    if (!S::SPLIT) clusters = std::min<int64_t>(tiles, sm_count() / cluster);   // persistent
-    if (tiles * S::kCtas > 0x3FFFFFFF || clusters * cluster > 0x3FFFFFFF) return cudaErrorInvalidValue;
+    if (!S::SPLIT) {                           // persistent
+        static int resident[kMaxDevices];
+        clusters = std::min<int64_t>(tiles, resident_clusters(kernel, cluster, S::kThreads, S::kSmem, resident));
+    }
+    if (tiles > 0x3FFFFFFF || clusters * cluster > 0x3FFFFFFF) return cudaErrorInvalidValue;
     return launch_pdl_clusters(kernel, (int)clusters * cluster, S::kThreads, cluster, S::kSmem, st,
-                               mp, mq, a);
+                               mp, mq, md, a);
 }
 
 template <int FMT>
@@ -530,20 +656,24 @@ cudaError_t launch_fmt(const Fp4Operand &A, const Fp4Operand &B, int64_t M, int6
     a.p_down = (int)fp4_tiles_down(a.P), a.q_down = (int)fp4_tiles_down(a.Q);
     a.d = d, a.ldd = ldd, a.dtype = dtype, a.swapped = swapped;
     const int es = dtype == kF32 ? 4 : 2;
-    a.vectors = reinterpret_cast<uintptr_t>(d) % 16 == 0 && (ldd * es) % 16 == 0;
+    // (a tensor map's rows are less than 2^40 bytes apart)
+    a.vectors = reinterpret_cast<uintptr_t>(d) % 16 == 0 && (ldd * es) % 16 == 0 && ldd < 1ll << 37;
+    a.whole = (N * es) % 16 == 0;
     if (small <= 64) {
         // the CTAs of a tile: as many as the GPU has room for, with two stages each at least
         const int64_t tiles = fp4_tiles_down(a.P), stages = (K + BK - 1) / BK;
         int split = 1;
         while (split < 8 && tiles * split * 2 <= 2 * sm_count() && stages >= split * 4) split *= 2;
-        return small <= 32 ? launch_shape<FMT, Shape<FMT, 32, false, true>>(a, p.codes, q.codes, split, st)
-                           : launch_shape<FMT, Shape<FMT, 64, false, true>>(a, p.codes, q.codes, split, st);
+        return small <= 32 ? launch_shape<FMT, Shape<FMT, 32, 0, true>>(a, p.codes, q.codes, split, st)
+                           : launch_shape<FMT, Shape<FMT, 64, 0, true>>(a, p.codes, q.codes, split, st);
     }
     // tiles of 256 x 256 by CTA pairs where they fill the GPU
     const int64_t pairs = (M + 255) / 256 * ((N + 255) / 256);
     if (pairs * 2 >= sm_count())
-        return launch_shape<FMT, Shape<FMT, 256, true, false>>(a, p.codes, q.codes, 1, st);
-    return launch_shape<FMT, Shape<FMT, 128, false, false>>(a, p.codes, q.codes, 1, st);
+        return pairs >= 2 * sm_count()
+                   ? launch_shape<FMT, Shape<FMT, 256, 2, false>>(a, p.codes, q.codes, 1, st)
+                   : launch_shape<FMT, Shape<FMT, 256, 1, false>>(a, p.codes, q.codes, 1, st);
+    return launch_shape<FMT, Shape<FMT, 128, 0, false>>(a, p.codes, q.codes, 1, st);
 }
 
 }  // namespace
