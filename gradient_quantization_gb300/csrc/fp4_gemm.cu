@@ -7,8 +7,9 @@
 //
 // The operand that fills the 128 lanes of an MMA is called P here, the one along its columns Q.
 //   warp 0      TMA: a stage is 256 elements of K: 128-byte rows of codes of P and Q with the
-//               128-byte swizzle, and the scale tiles of those rows, which lie in memory one
-//               after another, by plain bulk copies;
+//               128-byte swizzle;
+//   last warp   the scale tiles of those rows, which lie in memory one after another, by plain
+//               bulk copies into a ring of their own that runs ahead of the codes;
 //   warps 2-5   write a stage's scales to tensor memory, each to the lanes that it reaches: the
 //               MMA wants them in all four lane quarters;
 //   warp 1      issues an MMA for every 64 elements of K that the operands have (the last stage
@@ -74,21 +75,14 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
 }
-// To the same place in every CTA of `mask`, and to its barrier.
-__device__ __forceinline__ void bulk_load_multicast(void *dst, const void *src, uint32_t bytes,
-                                                    uint64_t *bar, uint16_t mask) {
+// A tile load of one CTA of a pair whose bytes count on a barrier of either (`bar`: its address
+// in the cluster).
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x,
+                                                 int y) {
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"(mask)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_multicast(void *dst, const CUtensorMap *map, uint64_t *bar,
-                                                      int x, int y, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "h"(mask)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
@@ -98,10 +92,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// Wait until at most N of this thread's stores still read shared memory.
-template <int N>
+// Wait until none of this thread's stores still reads shared memory.
 __device__ __forceinline__ void stores_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *v) {
@@ -120,42 +113,40 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
 
 // ---- shapes of a variant ------------------------------------------------------------------
 //
-// BN columns of D a tile.  PAIRS > 0: the two CTAs of a pair share an MMA over 256 rows of P and
-// BN of Q, half of whose codes each of them holds; the PAIRS pairs of a cluster take tiles next
-// to each other along P, and what their CTAs hold alike (codes of Q, scales of Q) is loaded
-// once, a part by each, and multicast.  SPLIT: the CTAs of a cluster each take a part of K of
-// one tile and join their sums.
-template <int FMT, int BN_, int PAIRS_, bool SPLIT_>
+// BN columns of D a tile.  PAIR: the two CTAs of a cluster share an MMA over 256 rows of P and
+// BN of Q, half of whose codes each of them holds (the scales of all BN both need).  SPLIT: the
+// CTAs of a cluster each take a part of K of one tile and join their sums.
+template <int FMT, int BN_, bool PAIR_, bool SPLIT_>
 struct Shape {
-    static constexpr int BN = BN_, PAIRS = PAIRS_;
-    static constexpr bool PAIR = PAIRS > 0, SPLIT = SPLIT_;
-    static constexpr int kCluster = PAIR ? 2 * PAIRS : 1;       // (SPLIT: given at launch)
+    static constexpr int BN = BN_;
+    static constexpr bool PAIR = PAIR_, SPLIT = SPLIT_;
+    static constexpr int kCluster = PAIR ? 2 : 1;               // (SPLIT: given at launch)
     static constexpr int kTileRows = BM * kCluster;             // of a cluster
-    static constexpr int kQRows = PAIR ? BN / 2 : BN;           // held by a CTA
-    static constexpr int kQLoad = PAIR ? kQRows / PAIRS : BN;   // loaded by a CTA
+    static constexpr int kQRows = BN / kCluster;
     static constexpr int kQTiles = (BN + 127) / 128;            // row blocks of Q's scales
     static constexpr int kTiles = BK / fp4_tile_elems(FMT);     // scale tiles of a stage
     static constexpr int kPBytes = BM * kRowBytes, kQBytes = kQRows * kRowBytes;
     static constexpr int kPScales = kTiles * kScaleTile, kQScales = kQTiles * kTiles * kScaleTile;
-    static constexpr int kStages = SPLIT && BN > 32 ? 3 : 4;
+    static constexpr int kStages = SPLIT ? (BN > 32 ? 3 : 4) : 5;
     static constexpr int kScaleWarps = 4, kEpiWarps = SPLIT ? 0 : 8;
-    static constexpr int kThreads = 64 + 32 * (kScaleWarps + kEpiWarps);
+    static constexpr int kScaleTmaWarp = 2 + kScaleWarps + kEpiWarps;
+    static constexpr int kThreads = 32 * (kScaleTmaWarp + 1);
     static constexpr int kBuffers = !SPLIT && BN <= 128 ? 2 : 1;   // accumulators
     static constexpr int kScaleCols = 4 * kTiles * (1 + kQTiles);
     static constexpr int kUsedCols = kBuffers * BN + kStages * kScaleCols;
     static constexpr int kTmemCols = kUsedCols <= 256 ? 256 : 512;
     static constexpr int kOffQ = kStages * kPBytes;
     static constexpr int kOffOut = kOffQ + kStages * kQBytes;
-    static constexpr int kOutBytes = SPLIT ? 0 : 2 * 4096;      // an epilogue warp's two buffers
+    static constexpr int kOutBytes = 4096;                      // an epilogue warp's buffer
     static constexpr int kOffPS = kOffOut + kEpiWarps * kOutBytes;
     static constexpr int kOffQS = kOffPS + kStages * kPScales;
     static constexpr int kOffBar = kOffQS + kStages * kQScales;
-    static constexpr int kBars = 3 * kStages + 2 * kBuffers + 1;
+    static constexpr int kBars = 5 * kStages + 2 * kBuffers + 1;
     static constexpr int kOffMisc = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffMisc + 16 + 1024;
     static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
                                        (FMT == kMx ? 1u << 23 : 0u) |
-                                       ((uint32_t)((PAIR ? 256 : 128) >> 4) << 24);
+                                       ((uint32_t)(kTileRows >> 4) << 24);
     static_assert(kUsedCols <= 512, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(!SPLIT || BM * BN * 4 <= kStages * kPBytes, "the sums take the stages' place");
@@ -197,8 +188,8 @@ __device__ __forceinline__ void load_out(uint32_t from, float g0, float g1, uint
 }
 
 // An epilogue warp's 32 rows x CW columns by TMA: 128-byte wide boxes, swizzled so that the
-// lanes' 16-byte stores meet no bank twice; two buffers in turn.  `free_acc` is called once the
-// accumulator has been read.
+// lanes' 16-byte stores meet no bank twice.  `free_acc` is called once the accumulator has been
+// read.
 template <int FMT, int DT, int CW, class F>
 __device__ __forceinline__ void store_boxes(const CUtensorMap *map, uint8_t *buf, uint32_t from, int row,
                                             int col, const Fp4Args &a, float g0, float g1, int lane,
@@ -209,29 +200,25 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap *map, uint8_t *buf
         uint4 o[8];
         load_out<FMT, DT>(from + c * kCols, g0, g1, o);
         if (c == CW / kCols - 1) free_acc();
-        uint8_t *to = buf + (c & 1) * 4096;
-        if (lane == 0) stores_read<CW / kCols >= 2 ? 1 : 0>();   // this buffer's last store
+        if (lane == 0) stores_read();
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4 *>(to + lane * 128 + ((i ^ (lane & 7)) << 4)) = o[i];
+            *reinterpret_cast<uint4 *>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) = o[i];
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-            if (row < a.P && col + c * kCols < a.Q) tma_store_2d(map, to, col + c * kCols, row);
-            else asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        if (lane == 0 && row < a.P && col + c * kCols < a.Q) tma_store_2d(map, buf, col + c * kCols, row);
     }
 }
 
-// The same where D's rows do not lie at 16-byte boundaries: a row of 32 values at a time.
+// The same where D's rows do not lie at 16-byte boundaries: two rows of 16 values at a time.
 template <int FMT, int CW, class F>
 __device__ __forceinline__ void store_rows(uint8_t *buf, uint32_t from, int row0, int col, const Fp4Args &a,
                                            float g0, float g1, int lane, F free_acc) {
-    constexpr int kPitch = 33;
+    constexpr int kPitch = 17;
     float *rows = reinterpret_cast<float *>(buf);
-    if (lane == 0) stores_read<0>();                // boxes of an earlier tile
-    __syncwarp();
+    if (lane == 0) stores_read();                   // boxes of an earlier tile
+    const int n = min(32, a.P - row0);
 #pragma unroll 1
     for (int c = 0; c < CW; c += 32) {
         uint32_t w[32];
@@ -239,16 +226,20 @@ __device__ __forceinline__ void store_rows(uint8_t *buf, uint32_t from, int row0
         tmem_ld32(from + c, w);
         if (c == CW - 32) free_acc();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            float v = __uint_as_float(w[i]);
-            if constexpr (FMT == kNv) v = __fmul_rn(__fmul_rn(v, g0), g1);
-            rows[lane * kPitch + i] = v;
+        for (int h = 0; h < 2; ++h) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float v = __uint_as_float(w[16 * h + i]);
+                if constexpr (FMT == kNv) v = __fmul_rn(__fmul_rn(v, g0), g1);
+                rows[lane * kPitch + i] = v;
+            }
+            __syncwarp();
+            const int at = col + c + 16 * h + (lane & 15);
+            if (at < a.Q)
+                for (int r = lane >> 4; r < n; r += 2)
+                    store1(a.d, (int64_t)(row0 + r) * a.ldd + at, a.dtype, rows[r * kPitch + (lane & 15)]);
         }
-        __syncwarp();
-        const int n = min(32, a.P - row0);
-        if (col + c + lane < a.Q)
-            for (int r = 0; r < n; ++r)
-                store1(a.d, (int64_t)(row0 + r) * a.ldd + col + c + lane, a.dtype, rows[r * kPitch + lane]);
     }
     __syncwarp();
 }
@@ -263,14 +254,15 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *sp = smem, *sq = smem + S::kOffQ, *sps = smem + S::kOffPS, *sqs = smem + S::kOffQS;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kOffBar);
-    uint64_t *full = bars, *empty = bars + NS, *scaled = bars + 2 * NS, *tfull = bars + 3 * NS,
-             *tempty = tfull + S::kBuffers, *drain = tempty + S::kBuffers;
+    uint64_t *full = bars, *empty = bars + NS, *scaled = bars + 2 * NS, *sfull = bars + 3 * NS,
+             *sempty = bars + 4 * NS, *tfull = bars + 5 * NS, *tempty = tfull + S::kBuffers,
+             *drain = tempty + S::kBuffers;
     uint32_t *tmem_addr = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
     unsigned *status = &g_fp4_status;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S::PAIR || S::SPLIT ? (int)cluster_ctarank() : 0;
-    const int pair = S::PAIR ? rank >> 1 : 0, side = S::PAIR ? rank & 1 : 0;
+    const int side = S::PAIR ? rank : 0;
     uint32_t csize = 1;
     if constexpr (S::PAIR || S::SPLIT) asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
     const int C = (int)csize;
@@ -288,12 +280,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], S::PAIR ? S::PAIRS : 1);       // all that read what is multicast
-            mbar_init(&scaled[s], S::kScaleWarps * (S::PAIR ? 2 : 1));
+            mbar_init(&empty[s], 1);
+            mbar_init(&scaled[s], S::kScaleWarps * S::kCluster);
+            mbar_init(&sfull[s], 1);
+            mbar_init(&sempty[s], S::kScaleWarps);
         }
         for (int b = 0; b < S::kBuffers; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], S::SPLIT ? 1 : S::kEpiWarps * (S::PAIR ? 2 : 1));
+            mbar_init(&tempty[b], S::SPLIT ? 1 : S::kEpiWarps * S::kCluster);
         }
         mbar_init(drain, 1);
         *abort = 0;
@@ -322,66 +316,75 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
 
     if (warp == 0) {
         if (lane == 0) {
-            const uint16_t everyone = (uint16_t)((1u << S::kCluster) - 1);
-            uint16_t alike = 0;                      // CTAs that hold the same codes of Q
-#pragma unroll
-            for (int i = 0; i < (S::PAIR ? S::PAIRS : 0); ++i) alike |= (uint16_t)(1u << (2 * i + side));
+            // A pair's codes all count on the barrier of its CTA 0, which issues the MMAs.
+            const uint32_t full0 = S::PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
             uint32_t it = 0;
             bool ok = true;
             for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
                 int tp, tq;
                 tile_at(tile, num_p, num_q, tp, tq);
-                const int p0 = tp * S::kTileRows + BM * (S::PAIR ? rank : 0), q0 = tq * BN;
-                const int p_block = p0 / 128, q_block = q0 / 128;
+                const int p0 = tp * S::kTileRows + BM * side, q0 = tq * BN + S::kQRows * side;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % NS;
                     if (!wait_bar(&empty[s], ((it / NS) & 1u) ^ 1u, abort, status)) {
                         ok = false;
                         break;
                     }
-                    // the scale tiles that exist
-                    const uint32_t bytes = min(S::kTiles, a.across - kb * S::kTiles) * kScaleTile;
-                    uint32_t all = S::kPBytes + S::kQBytes;
-                    if (p_block < a.p_down) all += bytes;
-#pragma unroll
-                    for (int i = 0; i < S::kQTiles; ++i)
-                        if (q_block + i < a.q_down) all += bytes;
-                    mbar_expect_tx(&full[s], all);
-                    tma_load_2d(sp + s * S::kPBytes, &map_p, &full[s], kb * kRowBytes, p0);
-                    uint8_t *qto = sq + s * S::kQBytes + pair * S::kQLoad * kRowBytes;
-                    const int qrow = q0 + S::kQRows * side + S::kQLoad * pair;
-                    if constexpr (S::PAIRS > 1)
-                        tma_load_2d_multicast(qto, &map_q, &full[s], kb * kRowBytes, qrow, alike);
-                    else
-                        tma_load_2d(qto, &map_q, &full[s], kb * kRowBytes, qrow);
-                    if (p_block < a.p_down)
-                        bulk_load(sps + s * S::kPScales,
-                                  a.p_scales + ((int64_t)p_block * a.across + kb * S::kTiles) * kScaleTile,
-                                  bytes, &full[s]);
+                    if (side == 0) mbar_expect_tx(&full[s], (S::kPBytes + S::kQBytes) * S::kCluster);
                     if constexpr (S::PAIR) {
-                        // side 0 the first row block's scales, side 1 the second's, a part by each
-                        // pair
-                        const uint32_t part = bytes / S::PAIRS;
-                        if (q_block + side < a.q_down)
-                            bulk_load_multicast(
-                                sqs + s * S::kQScales + side * S::kTiles * kScaleTile + pair * part,
-                                a.q_scales + ((int64_t)(q_block + side) * a.across + kb * S::kTiles) * kScaleTile + pair * part,
-                                part, &full[s], everyone);
-                    } else if (q_block < a.q_down) {
-                        bulk_load(sqs + s * S::kQScales,
-                                  a.q_scales + ((int64_t)q_block * a.across + kb * S::kTiles) * kScaleTile,
-                                  bytes, &full[s]);
+                        tma_load_2d_pair(sp + s * S::kPBytes, &map_p, full0 + 8u * s, kb * kRowBytes, p0);
+                        tma_load_2d_pair(sq + s * S::kQBytes, &map_q, full0 + 8u * s, kb * kRowBytes, q0);
+                    } else {
+                        tma_load_2d(sp + s * S::kPBytes, &map_p, &full[s], kb * kRowBytes, p0);
+                        tma_load_2d(sq + s * S::kQBytes, &map_q, &full[s], kb * kRowBytes, q0);
                     }
                 }
             }
-            for (int d = 0; d < NS && d < (int)it; ++d) {
+            // (CTA 1 of a pair leaves the wait for its copies to CTA 0, which sees both's: neither
+            // exits before the other)
+            for (int d = 0; side == 0 && d < NS && d < (int)it; ++d) {
                 const uint32_t last = it - 1 - d;
                 wait_bar(&full[last % NS], (last / NS) & 1u, abort, status, true);
             }
         }
+    } else if (warp == S::kScaleTmaWarp) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
+                int tp, tq;
+                tile_at(tile, num_p, num_q, tp, tq);
+                const int p_block = (tp * S::kTileRows) / 128 + side, q_block = tq * BN / 128;
+                const uint8_t *ps = a.p_scales + (int64_t)p_block * a.across * kScaleTile;
+                const uint8_t *qs = a.q_scales + (int64_t)q_block * a.across * kScaleTile;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % NS;
+                    if (!wait_bar(&sempty[s], ((it / NS) & 1u) ^ 1u, abort, status)) {
+                        ok = false;
+                        break;
+                    }
+                    // the scale tiles that exist
+                    const uint32_t bytes = min(S::kTiles, a.across - kb * S::kTiles) * kScaleTile;
+                    const int64_t at = (int64_t)kb * S::kTiles * kScaleTile;
+                    uint32_t all = p_block < a.p_down ? bytes : 0u;
+#pragma unroll
+                    for (int i = 0; i < S::kQTiles; ++i) all += q_block + i < a.q_down ? bytes : 0u;
+                    mbar_expect_tx(&sfull[s], all);
+                    if (p_block < a.p_down) bulk_load(sps + s * S::kPScales, ps + at, bytes, &sfull[s]);
+#pragma unroll
+                    for (int i = 0; i < S::kQTiles; ++i)
+                        if (q_block + i < a.q_down)
+                            bulk_load(sqs + s * S::kQScales + i * S::kTiles * kScaleTile,
+                                      qs + (int64_t)i * a.across * kScaleTile + at, bytes, &sfull[s]);
+                }
+            }
+            for (int d = 0; d < NS && d < (int)it; ++d) {
+                const uint32_t last = it - 1 - d;
+                wait_bar(&sfull[last % NS], (last / NS) & 1u, abort, status, true);
+            }
+        }
     } else if (warp == 1) {
         if (lane == 0 && side == 0) {
-            const uint16_t everyone = (uint16_t)((1u << S::kCluster) - 1), mine = (uint16_t)(3u << (2 * pair));
             uint32_t it = 0, t = 0;
             bool ok = true, issued = false;
             for (int tile = cid; ok && tile < num_tiles; tile += ncl, ++t) {
@@ -391,9 +394,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 const uint32_t d = tmem + buf * BN;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % NS;
-                    // both CTAs' scales are in place, and with them their codes
-                    if (!wait_bar(&full[s], (it / NS) & 1u, abort, status) ||
-                        !wait_bar(&scaled[s], (it / NS) & 1u, abort, status)) {
+                    if (!wait_bar(&scaled[s], (it / NS) & 1u, abort, status) ||
+                        !wait_bar(&full[s], (it / NS) & 1u, abort, status)) {
                         ok = false;
                         break;
                     }
@@ -412,11 +414,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                                               cols + 4 * j, qcols + 4 * j * S::kQTiles, kb > kb0 || kk > 0);
                     }
                     issued = true;
-                    if constexpr (S::PAIR) umma_commit_pair_multicast(&empty[s], everyone);
+                    if constexpr (S::PAIR) umma_commit_pair_multicast(&empty[s], 3);
                     else commit_one(&empty[s]);
                 }
                 if (!ok) break;
-                if constexpr (S::PAIR) umma_commit_pair_multicast(&tfull[buf], mine);
+                if constexpr (S::PAIR) umma_commit_pair_multicast(&tfull[buf], 3);
                 else if (kb0 < kb1) commit_one(&tfull[buf]);
             }
             if (issued) {
@@ -428,13 +430,13 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     } else if (warp < 2 + S::kScaleWarps) {
         // scales: P's tiles, then Q's, four columns each
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t scaled0 = S::PAIR ? mapa_shared(smem_u32(scaled), rank & ~1) : 0u;
+        const uint32_t scaled0 = S::PAIR ? mapa_shared(smem_u32(scaled), 0) : 0u;
         uint32_t it = 0;
         bool ok = true;
         for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % NS;
-                if (!warp_wait(&full[s], (it / NS) & 1u, abort, status)) {
+                if (!warp_wait(&sfull[s], (it / NS) & 1u, abort, status)) {
                     ok = false;
                     break;
                 }
@@ -454,6 +456,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                         w[c] = v.x, w[c + 1] = v.y, w[c + 2] = v.z, w[c + 3] = v.w;
                     }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sempty[s]);
+                // the MMAs that used these columns are done
+                if (!warp_wait(&empty[s], ((it / NS) & 1u) ^ 1u, abort, status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
                 const uint32_t to = scale_cols + s * S::kScaleCols + lanes;
 #pragma unroll
                 for (int c = 0; c + 16 <= S::kScaleCols; c += 16) tmem_st16(to + c, w + c);
@@ -494,7 +504,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         const int q = warp & 3, e = warp - 2 - S::kScaleWarps, half = e >> 2;
         constexpr int CW = BN / 2;
         uint8_t *buf_out = smem + S::kOffOut + e * S::kOutBytes;
-        const uint32_t tempty0 = S::PAIR ? mapa_shared(smem_u32(tempty), rank & ~1) : 0u;
+        const uint32_t tempty0 = S::PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
         // the smaller tensor scale first: no overflow or underflow on the way
         float g0 = 1.0f, g1 = 1.0f;
         if constexpr (FMT == kNv) {
@@ -510,7 +520,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             int tp, tq;
             tile_at(tile, num_p, num_q, tp, tq);
             const uint32_t from = tmem + ((uint32_t)(32 * q) << 16) + buf * BN + half * CW;
-            const int row = tp * S::kTileRows + BM * (S::PAIR ? rank : 0) + 32 * q, col = tq * BN + half * CW;
+            const int row = tp * S::kTileRows + BM * side + 32 * q, col = tq * BN + half * CW;
             // the accumulator is free as soon as it has been read
             auto free_acc = [&] {
                 tc_fence_before();
@@ -536,7 +546,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     tc_fence_after();
     if constexpr (S::SPLIT) {
         cluster_sync_all();                          // all parts are there
-        if (warp >= 2) {
+        if (warp >= 2 && warp < 2 + S::kScaleWarps) {
             float g0 = 1.0f, g1 = 1.0f;
             if constexpr (FMT == kNv) {
                 const float gp = tensor_scale(__ldg(a.p_amax)), gq = tensor_scale(__ldg(a.q_amax));
@@ -615,7 +625,7 @@ template <int FMT, class S>
 cudaError_t launch_shape(const Fp4Args &a, const uint8_t *p_codes, const uint8_t *q_codes, int split,
                          cudaStream_t st) {
     CUtensorMap mp, mq, md{};
-    if (!encode_codes(&mp, p_codes, a.P, a.K, BM) || !encode_codes(&mq, q_codes, a.Q, a.K, S::kQLoad))
+    if (!encode_codes(&mp, p_codes, a.P, a.K, BM) || !encode_codes(&mq, q_codes, a.Q, a.K, S::kQRows))
         return cudaErrorInvalidValue;
     if (!S::SPLIT && a.vectors) {
         const int es = a.dtype == kF32 ? 4 : 2;
@@ -664,16 +674,14 @@ cudaError_t launch_fmt(const Fp4Operand &A, const Fp4Operand &B, int64_t M, int6
         const int64_t tiles = fp4_tiles_down(a.P), stages = (K + BK - 1) / BK;
         int split = 1;
         while (split < 8 && tiles * split * 2 <= 2 * sm_count() && stages >= split * 4) split *= 2;
-        return small <= 32 ? launch_shape<FMT, Shape<FMT, 32, 0, true>>(a, p.codes, q.codes, split, st)
-                           : launch_shape<FMT, Shape<FMT, 64, 0, true>>(a, p.codes, q.codes, split, st);
+        return small <= 32 ? launch_shape<FMT, Shape<FMT, 32, false, true>>(a, p.codes, q.codes, split, st)
+                           : launch_shape<FMT, Shape<FMT, 64, false, true>>(a, p.codes, q.codes, split, st);
     }
     // tiles of 256 x 256 by CTA pairs where they fill the GPU
     const int64_t pairs = (M + 255) / 256 * ((N + 255) / 256);
     if (pairs * 2 >= sm_count())
-        return pairs >= 2 * sm_count()
-                   ? launch_shape<FMT, Shape<FMT, 256, 2, false>>(a, p.codes, q.codes, 1, st)
-                   : launch_shape<FMT, Shape<FMT, 256, 1, false>>(a, p.codes, q.codes, 1, st);
-    return launch_shape<FMT, Shape<FMT, 128, 0, false>>(a, p.codes, q.codes, 1, st);
+        return launch_shape<FMT, Shape<FMT, 256, true, false>>(a, p.codes, q.codes, 1, st);
+    return launch_shape<FMT, Shape<FMT, 128, false, false>>(a, p.codes, q.codes, 1, st);
 }
 
 }  // namespace
