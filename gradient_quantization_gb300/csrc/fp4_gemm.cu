@@ -8,13 +8,13 @@
 // The operand that fills the 128 lanes of an MMA is called P here, the one along its columns Q.
 //   warp 0      TMA: a stage is 256 elements of K: 128-byte rows of codes of P and Q with the
 //               128-byte swizzle;
-//   last warp   the scale tiles of those rows, which lie in memory one after another, by plain
+//   warp 2      the scale tiles of those rows, which lie in memory one after another, by plain
 //               bulk copies into a ring of their own that runs ahead of the codes;
-//   warps 2-5   write a stage's scales to tensor memory, each to the lanes that it reaches: the
+//   warps 4-7   write a stage's scales to tensor memory, each to the lanes that it reaches: the
 //               MMA wants them in all four lane quarters;
 //   warp 1      issues an MMA for every 64 elements of K that the operands have (the last stage
 //               of a K that is no multiple of 256 has fewer: what lies behind is never used);
-//   the others  the epilogue (SPLIT: warps 2-5).
+//   the others  the epilogue (SPLIT: warps 4-7).
 // Every stage has scale columns of its own, so that a write never meets an MMA that still reads.
 // Every wait is time-limited (gemm_common.cuh).
 #include <algorithm>
@@ -33,6 +33,8 @@ __device__ unsigned g_fp4_status;
 
 constexpr int BM = 128, BK = 256;                   // P rows of a CTA, elements of a stage
 constexpr int kRowBytes = BK / 2;                   // 128: the swizzle's span
+// Warps of a role make up whole warpgroups, whose registers can be shared out.
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kScaleTmaWarp = 2, kScaleWarp0 = 4;
 
 struct Fp4Args {
     const uint8_t *p_scales, *q_scales;
@@ -129,8 +131,7 @@ struct Shape {
     static constexpr int kPScales = kTiles * kScaleTile, kQScales = kQTiles * kTiles * kScaleTile;
     static constexpr int kStages = SPLIT ? (BN > 32 ? 3 : 4) : 5;
     static constexpr int kScaleWarps = 4, kEpiWarps = SPLIT ? 0 : 8;
-    static constexpr int kScaleTmaWarp = 2 + kScaleWarps + kEpiWarps;
-    static constexpr int kThreads = 32 * (kScaleTmaWarp + 1);
+    static constexpr int kThreads = 32 * (kScaleWarp0 + kScaleWarps + kEpiWarps);
     static constexpr int kBuffers = !SPLIT && BN <= 128 ? 2 : 1;   // accumulators
     static constexpr int kScaleCols = 4 * kTiles * (1 + kQTiles);
     static constexpr int kUsedCols = kBuffers * BN + kStages * kScaleCols;
@@ -151,6 +152,23 @@ struct Shape {
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(!SPLIT || BM * BN * 4 <= kStages * kPBytes, "the sums take the stages' place");
 };
+
+// A place in a ring of NS stages and the parity of its use.
+template <int NS>
+struct Ring {
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == NS) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// Waits that are long as a rule let the thread sleep: a poll takes an issue slot and a cycle of
+// the shared memory that the MMAs read from.
+constexpr uint32_t kSleepNs = 20000;
 
 // Tiles in bands of kBand along Q: the CTAs at work share a few rows of both operands.
 constexpr int kBand = 16;
@@ -188,18 +206,15 @@ __device__ __forceinline__ void load_out(uint32_t from, float g0, float g1, uint
 }
 
 // An epilogue warp's 32 rows x CW columns by TMA: 128-byte wide boxes, swizzled so that the
-// lanes' 16-byte stores meet no bank twice.  `free_acc` is called once the accumulator has been
-// read.
+// lanes' 16-byte stores meet no bank twice.  `free_acc` is called as soon as the accumulator has
+// been read: the next tile's MMAs have five stages to run through and so make up for a short
+// pause.
 template <int FMT, int DT, int CW, class F>
 __device__ __forceinline__ void store_boxes(const CUtensorMap *map, uint8_t *buf, uint32_t from, int row,
                                             int col, const Fp4Args &a, float g0, float g1, int lane,
                                             F free_acc) {
-    constexpr int kCols = DT == kF32 ? 32 : 64;
-#pragma unroll
-    for (int c = 0; c < CW / kCols; ++c) {
-        uint4 o[8];
-        load_out<FMT, DT>(from + c * kCols, g0, g1, o);
-        if (c == CW / kCols - 1) free_acc();
+    constexpr int kCols = DT == kF32 ? 32 : 64, kBoxes = CW / kCols;
+    auto put = [&](int c, const uint4 (&o)[8]) {
         if (lane == 0) stores_read();
         __syncwarp();
 #pragma unroll
@@ -208,7 +223,13 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap *map, uint8_t *buf
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0 && row < a.P && col + c * kCols < a.Q) tma_store_2d(map, buf, col + c * kCols, row);
-    }
+    };
+    uint4 o[kBoxes][8];
+#pragma unroll
+    for (int c = 0; c < kBoxes; ++c) load_out<FMT, DT>(from + c * kCols, g0, g1, o[c]);
+    free_acc();
+#pragma unroll
+    for (int c = 0; c < kBoxes; ++c) put(c, o[c]);
 }
 
 // The same where D's rows do not lie at 16-byte boundaries: two rows of 16 values at a time.
@@ -293,7 +314,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         if constexpr (S::PAIR) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                              smem_u32(tmem_addr)), "r"(S::kTmemCols) : "memory");
@@ -313,20 +334,24 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     // (after the allocation: a following launch may start and allocate only once every CTA of
     // this one has its columns)
     pdl_wait_and_release();
-
-    if (warp == 0) {
+    // The epilogue holds 128 columns of a row.  512 threads were launched with 128 registers each:
+    // 64 + 96 + 2 * 168 a thread of the four warpgroups is below 4 * 128.
+    if (warp < kScaleWarp0) {
+    if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == kTmaWarp) {
         if (lane == 0) {
             // A pair's codes all count on the barrier of its CTA 0, which issues the MMAs.
             const uint32_t full0 = S::PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
             uint32_t it = 0;
             bool ok = true;
+            Ring<NS> ring;
             for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
                 int tp, tq;
                 tile_at(tile, num_p, num_q, tp, tq);
                 const int p0 = tp * S::kTileRows + BM * side, q0 = tq * BN + S::kQRows * side;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % NS;
-                    if (!wait_bar(&empty[s], ((it / NS) & 1u) ^ 1u, abort, status)) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next()) {
+                    const int s = ring.s;
+                    if (!wait_bar(&empty[s], ring.parity ^ 1u, abort, status, false, kSleepNs)) {
                         ok = false;
                         break;
                     }
@@ -347,19 +372,20 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 wait_bar(&full[last % NS], (last / NS) & 1u, abort, status, true);
             }
         }
-    } else if (warp == S::kScaleTmaWarp) {
+    } else if (warp == kScaleTmaWarp) {
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
+            Ring<NS> ring;
             for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
                 int tp, tq;
                 tile_at(tile, num_p, num_q, tp, tq);
                 const int p_block = (tp * S::kTileRows) / 128 + side, q_block = tq * BN / 128;
                 const uint8_t *ps = a.p_scales + (int64_t)p_block * a.across * kScaleTile;
                 const uint8_t *qs = a.q_scales + (int64_t)q_block * a.across * kScaleTile;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % NS;
-                    if (!wait_bar(&sempty[s], ((it / NS) & 1u) ^ 1u, abort, status)) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next()) {
+                    const int s = ring.s;
+                    if (!wait_bar(&sempty[s], ring.parity ^ 1u, abort, status, false, kSleepNs)) {
                         ok = false;
                         break;
                     }
@@ -383,35 +409,43 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 wait_bar(&sfull[last % NS], (last / NS) & 1u, abort, status, true);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == kMmaWarp) {
         if (lane == 0 && side == 0) {
-            uint32_t it = 0, t = 0;
+            uint32_t t = 0;
             bool ok = true, issued = false;
+            Ring<NS> ring;
+            const uint64_t pd0 = sw128_kmajor_desc(smem_u32(sp)), qd0 = sw128_kmajor_desc(smem_u32(sq));
             for (int tile = cid; ok && tile < num_tiles; tile += ncl, ++t) {
                 const int buf = t % S::kBuffers;
                 if (!S::SPLIT && !wait_bar(&tempty[buf], ((t / S::kBuffers) & 1u) ^ 1u, abort, status)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int s = it % NS;
-                    if (!wait_bar(&scaled[s], (it / NS) & 1u, abort, status) ||
-                        !wait_bar(&full[s], (it / NS) & 1u, abort, status)) {
+                int left = a.K - kb0 * BK;           // elements of K from this stage on
+                for (int kb = kb0; kb < kb1; ++kb, left -= BK, ring.next()) {
+                    const int s = ring.s;
+                    if (!wait_bar(&scaled[s], ring.parity, abort, status) ||
+                        !wait_bar(&full[s], ring.parity, abort, status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t cols = scale_cols + s * S::kScaleCols, qcols = cols + 4 * S::kTiles;
-                    const int steps = min(4, (a.K - kb * BK + 63) / 64);
-                    const uint64_t pd = sw128_kmajor_desc(smem_u32(sp + s * S::kPBytes));
-                    const uint64_t qd = sw128_kmajor_desc(smem_u32(sq + s * S::kQBytes));
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (kk >= steps) break;
+                    const uint64_t pd = pd0 + (uint32_t)s * (S::kPBytes >> 4), qd = qd0 + (uint32_t)s * (S::kQBytes >> 4);
+                    auto step = [&](int kk, uint32_t accumulate) {
                         // a step is 32 bytes of a row; MXFP4: two scales of a tile's four
                         const int j = FMT == kNv ? kk : kk >> 1;
                         const uint32_t id = FMT == kNv ? 0 : 2 * (kk & 1);
                         mma_fp4<FMT, S::PAIR>(d, pd + 2 * kk, qd + 2 * kk, S::kIdesc | (id << 29) | (id << 4),
-                                              cols + 4 * j, qcols + 4 * j * S::kQTiles, kb > kb0 || kk > 0);
+                                              cols + 4 * j, qcols + 4 * j * S::kQTiles, accumulate);
+                    };
+                    step(0, kb > kb0);
+                    if (left > 192) {
+                        step(1, 1);
+                        step(2, 1);
+                        step(3, 1);
+                    } else {
+                        if (left > 64) step(1, 1);
+                        if (left > 128) step(2, 1);
                     }
                     issued = true;
                     if constexpr (S::PAIR) umma_commit_pair_multicast(&empty[s], 3);
@@ -427,16 +461,18 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 wait_bar(drain, 0u, abort, status, true);
             }
         }
-    } else if (warp < 2 + S::kScaleWarps) {
+    }
+    } else if (warp < kScaleWarp0 + S::kScaleWarps) {
+        if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         // scales: P's tiles, then Q's, four columns each
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t scaled0 = S::PAIR ? mapa_shared(smem_u32(scaled), 0) : 0u;
-        uint32_t it = 0;
         bool ok = true;
+        Ring<NS> ring;
         for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % NS;
-                if (!warp_wait(&sfull[s], (it / NS) & 1u, abort, status)) {
+            for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+                const int s = ring.s;
+                if (!warp_wait(&sfull[s], ring.parity, abort, status, kSleepNs)) {
                     ok = false;
                     break;
                 }
@@ -459,7 +495,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sempty[s]);
                 // the MMAs that used these columns are done
-                if (!warp_wait(&empty[s], ((it / NS) & 1u) ^ 1u, abort, status)) {
+                if (!warp_wait(&empty[s], ring.parity ^ 1u, abort, status, kSleepNs)) {
                     ok = false;
                     break;
                 }
@@ -482,7 +518,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             float *sums = reinterpret_cast<float *>(smem);
             const bool any = kb0 < kb1;
             if (any) {
-                ok = ok && warp_wait(&tfull[0], 0u, abort, status);
+                ok = ok && warp_wait(&tfull[0], 0u, abort, status, kSleepNs);
                 tc_fence_after();
             }
             if (ok) {
@@ -499,9 +535,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 }
             }
         }
-    } else {
+    } else if constexpr (!S::SPLIT) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // lane quarter of tensor memory: warp % 4; columns: half of the tile's
-        const int q = warp & 3, e = warp - 2 - S::kScaleWarps, half = e >> 2;
+        const int q = warp & 3, e = warp - kScaleWarp0 - S::kScaleWarps, half = e >> 2;
         constexpr int CW = BN / 2;
         uint8_t *buf_out = smem + S::kOffOut + e * S::kOutBytes;
         const uint32_t tempty0 = S::PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
@@ -515,7 +552,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         uint32_t t = 0;
         for (int tile = cid; tile < num_tiles; tile += ncl, ++t) {
             const int buf = t % S::kBuffers;
-            if (!warp_wait(&tfull[buf], (t / S::kBuffers) & 1u, abort, status)) break;
+            if (!warp_wait(&tfull[buf], (t / S::kBuffers) & 1u, abort, status, kSleepNs)) break;
             tc_fence_after();
             int tp, tq;
             tile_at(tile, num_p, num_q, tp, tq);
@@ -546,7 +583,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     tc_fence_after();
     if constexpr (S::SPLIT) {
         cluster_sync_all();                          // all parts are there
-        if (warp >= 2 && warp < 2 + S::kScaleWarps) {
+        if (warp >= kScaleWarp0) {
             float g0 = 1.0f, g1 = 1.0f;
             if constexpr (FMT == kNv) {
                 const float gp = tensor_scale(__ldg(a.p_amax)), gq = tensor_scale(__ldg(a.q_amax));
@@ -555,7 +592,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             }
             int tp, tq;
             tile_at(cid, num_p, num_q, tp, tq);
-            const int r = (warp - 2) * 32 + lane, row = tp * BM + r;
+            const int r = (warp - kScaleWarp0) * 32 + lane, row = tp * BM + r;
             const uint32_t mine = smem_u32(smem);
             for (int c = rank; c < BN; c += C) {
                 const int col = tq * BN + c;
@@ -579,7 +616,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     // No CTA of a cluster frees tensor memory or exits while another may arrive on its barriers,
     // read or write its shared memory or have a shared MMA run on it.
     if constexpr (S::PAIR || S::SPLIT) cluster_sync_all();
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         __syncwarp();
         if constexpr (S::PAIR)
             asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
