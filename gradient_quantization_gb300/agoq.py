@@ -825,8 +825,11 @@ def agoq_preference_loss(logp, offsets, ref_logp=None, weights=None, beta=0.1,
     loss, lp = _out(loss, P, other, P, f32, dev, "loss")
     margin, mp = _out(margin, P, other, P, f32, dev, "margin")
     if dlogp is None:
-        with torch.cuda.stream(other):         # (None: the current stream)
+        if other is None:
             dlogp = torch.zeros(T, dtype=f32, device=dev)
+        else:
+            with torch.cuda.stream(other):
+                dlogp = torch.zeros(T, dtype=f32, device=dev)
     rc = lib().agoq_preference_loss(
         _vector(logp, T, "logp", _F32, at), _vector(ref_logp, T, "ref_logp", _F32, at),
         _vector(offsets, 2 * P + 1, "offsets", _I64, at), _vector(weights, P, "weights", _F32, at),
@@ -850,6 +853,16 @@ def agoq_fp4_scale_bytes(rows, K, fmt):
     return int(lib().agoq_fp4_scale_bytes(int(rows), int(K), int(fmt)))
 
 
+def _fp4_sizes(rows, K, fmt):
+    """(bytes of a row's codes, of all codes, of all scales): the library's own sizes, without
+    calls into it (each call of a small product would make four)."""
+    if not (0 <= rows <= 1 << 30 and 1 <= K <= 1 << 24 and (fmt == 0 or fmt == 1)):
+        raise ValueError("no FP4 format %r of %r rows of %r" % (fmt, rows, K))
+    words = (K + 31) >> 5
+    tiles = (words + 1) >> 1 if fmt else (words + 3) >> 2
+    return words * 16, rows * words * 16, ((rows + 127) >> 7) * tiles * 512
+
+
 def agoq_amax(x, amax=None, stream=None):
     """Largest magnitude of `x` -> FP32 CUDA tensor of one element."""
     xp, T, K, ldx = _rows(x, "x")
@@ -863,12 +876,8 @@ def agoq_amax(x, amax=None, stream=None):
 
 
 def _fp4_out(codes, scales, rows, K, fmt, other, dev, suffix):
-    L = lib()
-    n, m = L.agoq_fp4_code_bytes(rows, K), L.agoq_fp4_scale_bytes(rows, K, fmt)
-    if n < 0 or m < 0:
-        raise ValueError("no FP4 format %r of %d rows of %d" % (fmt, rows, K))
-    codes, cp = _out(codes, n, other, (rows, n // rows if rows else 0), torch.uint8, dev,
-                     "codes" + suffix)
+    row, n, m = _fp4_sizes(rows, K, fmt)
+    codes, cp = _out(codes, n, other, (rows, row), torch.uint8, dev, "codes" + suffix)
     scales, sp = _out(scales, m, other, m, torch.uint8, dev, "scales" + suffix)
     return codes, scales, cp, sp
 
@@ -902,15 +911,6 @@ def agoq_fp4_quant(x, fmt, amax=None, rows=True, columns=False, codes=None, scal
     return codes, scales, codes_t, scales_t
 
 
-def _fp4_in(codes, scales, amax, rows, K, fmt, at, name):
-    L = lib()
-    n, m = L.agoq_fp4_code_bytes(rows, K), L.agoq_fp4_scale_bytes(rows, K, fmt)
-    if n < 0 or m < 0:
-        raise ValueError("no FP4 format %r of %d rows of %d" % (fmt, rows, K))
-    return (_vector(codes, n, name + "codes", _U8, at), _vector(scales, m, name + "scales", _U8, at),
-            _vector(amax, 1, name + "amax", _F32, at))
-
-
 def _device_of(t, what):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % what)
@@ -921,16 +921,20 @@ def agoq_fp4_dequant(codes, scales, T, K, fmt, amax=None, dtype=torch.bfloat16, 
                      stream=None):
     """The values [T][K] of FP4 codes as `dtype` (or into `y`, of its type)."""
     dev = _device_of(codes, "codes")
+    at = dev.index
     handle, other = _launch(stream, dev)
-    cp, sp, ap = _fp4_in(codes, scales, amax, T, K, fmt, dev.index, "")
+    _, n, m = _fp4_sizes(T, K, fmt)
     if y is None:
         if dtype not in DTYPES:
             raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % dtype)
         y = _new(other, (T, K), dtype, dev)
         yp, ldy = y.data_ptr(), K
     else:
-        yp, _, _, ldy = _rows(y, "y", K, T, None, dev.index)
-    rc = lib().agoq_fp4_dequant(cp, sp, ap, T, K, fmt, yp, ldy, DTYPES[y.dtype], handle)
+        yp, _, _, ldy = _rows(y, "y", K, T, None, at)
+        dtype = y.dtype
+    rc = lib().agoq_fp4_dequant(
+        _vector(codes, n, "codes", _U8, at), _vector(scales, m, "scales", _U8, at),
+        _vector(amax, 1, "amax", _F32, at), T, K, fmt, yp, ldy, DTYPES[dtype], handle)
     if rc:
         raise AgoqError(rc, "agoq_fp4_dequant")
     return y
@@ -943,8 +947,8 @@ def agoq_fp4_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, fmt, a_amax=Non
     dev = _device_of(a_codes, "a_codes")
     at = dev.index
     handle, other = _launch(stream, dev)
-    ac, as_, aa = _fp4_in(a_codes, a_scales, a_amax, M, K, fmt, at, "a_")
-    bc, bs, ba = _fp4_in(b_codes, b_scales, b_amax, N, K, fmt, at, "b_")
+    _, an, am = _fp4_sizes(M, K, fmt)
+    _, bn, bm = _fp4_sizes(N, K, fmt)
     if d is None:
         if dtype not in DTYPES:
             raise TypeError("dtype must be float32, bfloat16 or float16, got %s" % dtype)
@@ -952,7 +956,12 @@ def agoq_fp4_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, fmt, a_amax=Non
         dp, ldd = d.data_ptr(), N
     else:
         dp, _, _, ldd = _rows(d, "d", N, M, None, at)
-    rc = lib().agoq_fp4_gemm(ac, as_, aa, bc, bs, ba, M, N, K, fmt, dp, ldd, DTYPES[d.dtype], handle)
+        dtype = d.dtype
+    rc = lib().agoq_fp4_gemm(
+        _vector(a_codes, an, "a_codes", _U8, at), _vector(a_scales, am, "a_scales", _U8, at),
+        _vector(a_amax, 1, "a_amax", _F32, at), _vector(b_codes, bn, "b_codes", _U8, at),
+        _vector(b_scales, bm, "b_scales", _U8, at), _vector(b_amax, 1, "b_amax", _F32, at),
+        M, N, K, fmt, dp, ldd, DTYPES[dtype], handle)
     if rc:
         raise AgoqError(rc, "agoq_fp4_gemm")
     return d

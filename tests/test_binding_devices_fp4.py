@@ -1,6 +1,6 @@
 """The FP4, policy and preference calls refuse operands that are not on the current device, before
 anything is launched (CPU: tensors that claim a device, and a library that only counts its
-calls and says that codes and scales take 2^16 bytes)."""
+calls)."""
 import pytest
 import torch
 
@@ -20,14 +20,15 @@ def library(monkeypatch):
 
 
 T, V = 4, 50
-X, COL, TOK, BYTES, ONE = ((T, V), BF16), ((T,), F32), ((T,), I64), ((1 << 16,), U8), ((1,), F32)
+X, COL, TOK, ONE = ((T, V), BF16), ((T,), F32), ((T,), I64), ((1,), F32)
+CODES, SCALES, CODES_T, BYTES = ((T * 32,), U8), ((512,), U8), ((V * 16,), U8), ((1600,), U8)
 CALLS = {
     "amax": (dict(x=X, amax=ONE), lambda a: agoq.agoq_amax(**a)),
-    "quant": (dict(x=X, amax=ONE, codes=BYTES, scales=BYTES, codes_t=BYTES, scales_t=BYTES),
+    "quant": (dict(x=X, amax=ONE, codes=CODES, scales=SCALES, codes_t=CODES_T, scales_t=SCALES),
               lambda a: agoq.agoq_fp4_quant(fmt=agoq.NVFP4, columns=True, **a)),
-    "dequant": (dict(codes=BYTES, scales=BYTES, amax=ONE, y=X),
+    "dequant": (dict(codes=CODES, scales=SCALES, amax=ONE, y=X),
                 lambda a: agoq.agoq_fp4_dequant(T=T, K=V, fmt=agoq.NVFP4, **a)),
-    "gemm": (dict(a_codes=BYTES, a_scales=BYTES, b_codes=BYTES, b_scales=BYTES, a_amax=ONE, b_amax=ONE,
+    "gemm": (dict(a_codes=CODES, a_scales=SCALES, b_codes=BYTES, b_scales=SCALES, a_amax=ONE, b_amax=ONE,
                   d=X), lambda a: agoq.agoq_fp4_gemm(M=T, N=V, K=64, fmt=agoq.NVFP4, **a)),
     "policy": (dict(logits=X, tokens=TOK, old_logp=COL, advantages=COL, ref_logp=COL, weights=COL,
                     loss=COL, logp=COL, kl=COL, dlogits=X), lambda a: agoq.agoq_policy_loss(**a)),
@@ -64,3 +65,16 @@ def test_host_tensors(library, name):
     for bad in kinds:
         with pytest.raises(TypeError, match="CUDA"):
             call({k: torch.zeros(*v[:1], dtype=v[1]) if k == bad else _on(0, *v) for k, v in kinds.items()})
+
+
+def test_sizes_are_the_librarys():
+    """The binding's own sizes against the library's."""
+    for rows in (0, 1, 127, 128, 129, 1000, 1 << 30):
+        for K in (1, 16, 17, 32, 33, 64, 65, 127, 128, 129, 5003, 1 << 24):
+            for fmt in (agoq.MXFP4, agoq.NVFP4):
+                row, codes, scales = agoq._fp4_sizes(rows, K, fmt)
+                assert codes == agoq.agoq_fp4_code_bytes(rows, K) == rows * row
+                assert scales == agoq.agoq_fp4_scale_bytes(rows, K, fmt)
+    for bad in ((-1, 8, 0), (1, 0, 0), (1, (1 << 24) + 1, 0), ((1 << 30) + 1, 8, 0), (1, 8, 2), (1, 8, None)):
+        with pytest.raises(ValueError):
+            agoq._fp4_sizes(*bad)
