@@ -131,36 +131,60 @@ __device__ __forceinline__ int64_t word_at(int64_t row, int64_t t, int64_t acros
     return ((row >> 7) * across + t) * kScaleTile + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 }
 
+// Rows of a 128-row block whose scales share a 32-byte sector of every tile: two neighbours, and
+// the same 32, 64 and 96 rows further on.  A CTA takes such eight rows, one a warp, so that a
+// sector of scales is read once and written whole.
+constexpr int kOctet = 8;
+__device__ __forceinline__ int octet_row(int octet, int warp) {       // within the block
+    return 2 * octet + (warp & 1) + 32 * (warp >> 1);
+}
+
 // ---- rows -------------------------------------------------------------------------
 //
-// A thread takes 16 elements of a row; rows are padded to whole scale words (64 or 128
-// elements) and to whole tiles of 128, so that every scale byte is written (0 where there is
-// no block).
-template <int DT, int FMT>
-__global__ void __launch_bounds__(kThreads) fp4_rows_kernel(const Fp4Quant a, uint32_t units,
-                                                            uint32_t per_row) {
+// A warp takes PARTS runs of 512 elements of a row, a lane 16 of each.  Rows are padded to whole
+// scale words (64 or 128 elements) and to whole tiles of 128, so that every scale byte is
+// written (0 where there is no block).
+constexpr int kRun = 32 * kGroup;
+
+template <int DT, int FMT, int PARTS>
+__global__ void __launch_bounds__(kThreads) fp4_rows_kernel(const Fp4Quant a, uint32_t chunks) {
+    constexpr int kWord = fp4_tile_elems(FMT) / kGroup;        // lanes of a scale word
+    constexpr int kWords = 32 / kWord;                         // of a run
+    __shared__ uint32_t words[PARTS * kWords][kOctet];
     pdl_wait_and_release();
     const TensorScale ts = TensorScale::of<FMT>(a.amax);
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t octet = blockIdx.x / chunks, chunk = blockIdx.x - octet * chunks;
+    const int64_t block = octet >> 4, row = block * 128 + octet_row(octet & 15, warp);
     const int64_t across = fp4_tiles_across(a.K, FMT), row_bytes = fp4_row_bytes(a.K);
-    for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
-        const uint32_t row = u / per_row, g = u - row * per_row;
-        const bool live = row < a.T;
-        Group<DT> x;
-        if (live) x.load(elem_at<DT>(a.x, row * a.ldx), (int64_t)g * kGroup, a.K);
-        else x.clear();
-        float top = x.absmax();
+    const bool live = row < a.T;
+    const char *from = elem_at<DT>(a.x, live ? row * a.ldx : 0);
+    Group<DT> x[PARTS];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+        const int64_t e = ((int64_t)chunk * PARTS + p) * kRun + lane * kGroup;
+        if (live && e < a.K) x[p].load(from, e, a.K);
+        else x[p].clear();
+    }
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+        float top = x[p].absmax();
         if constexpr (FMT == kMx) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         const BlockScale<FMT> s = block_scale<FMT>(top, ts.g, ts.six_g, ts.ok);
-        uint2 c = x.codes(s.inverse);
+        uint2 c = x[p].codes(s.inverse);
         if (!s.finite) c = make_uint2(0, 0);
-        if (live && (int64_t)g * 8 < row_bytes)
-            *reinterpret_cast<uint2 *>(a.codes + row * row_bytes + (int64_t)g * 8) = c;
+        const int64_t at = ((int64_t)chunk * PARTS + p) * (kRun / 2) + lane * 8;
+        if (live && at < row_bytes) *reinterpret_cast<uint2 *>(a.codes + row * row_bytes + at) = c;
         const uint32_t w = scale_word<FMT>(s.byte, lane);
-        constexpr uint32_t kWord = FMT == kMx ? 8 : 4;     // threads of a word
-        if (g % kWord == 0)
-            *reinterpret_cast<uint32_t *>(a.scales + word_at(row, g / kWord, across)) = w;
+        // (word of the sector: neighbours are 16 bytes apart, the other rows 4)
+        if (lane % kWord == 0) words[p * kWords + lane / kWord][(warp & 1) * 4 + (warp >> 1)] = w;
     }
+    __syncthreads();
+    const int i = threadIdx.x, t = i >> 3;
+    const int64_t tile = (int64_t)chunk * PARTS * kWords + t;
+    if (t < PARTS * kWords && tile < across)
+        *reinterpret_cast<uint32_t *>(a.scales + (block * across + tile) * kScaleTile +
+                                      2 * (octet & 15) * 16 + (i & 7) * 4) = words[t][i & 7];
 }
 
 // ---- columns, and both -------------------------------------------------------------
@@ -380,77 +404,102 @@ __global__ void __launch_bounds__(kSmallThreads) amax_small_kernel(const void *x
 
 // ---- the way back ----------------------------------------------------------------------
 //
-// A thread takes 16 elements of a row: y = R(fl(fl(code s) g)); code s is exact.
-template <int DT, int FMT>
+// y = R(fl(fl(code s) g)); code s is exact.  A lane takes a 16-byte vector of the output at a
+// time, so that a warp writes whole lines whatever the rows' alignment; of rows that do not begin
+// at such a boundary (SHIFTED) a vector's codes begin anywhere and may belong to two blocks.
+template <int DT, int FMT, bool SHIFTED, int PARTS>
 __global__ void __launch_bounds__(kThreads)
 fp4_dequant_kernel(const uint8_t *codes, const uint8_t *scales, const float *amax, int64_t T,
-                   int64_t K, void *y, int64_t ldy, uint32_t units, uint32_t per_row) {
+                   int64_t K, void *y, int64_t ldy, uint32_t chunks) {
     using E = Elem<DT>;
-    constexpr int kVecs = Group<DT>::kVecs;
+    constexpr int N = E::kVec, kLen = fp4_block(FMT);
     pdl_wait_and_release();
     const TensorScale ts = TensorScale::of<FMT>(amax);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t octet = blockIdx.x / chunks, chunk = blockIdx.x - octet * chunks;
+    const int64_t row = (int64_t)(octet >> 4) * 128 + octet_row(octet & 15, warp);
+    if (row >= T) return;
     const int64_t across = fp4_tiles_across(K, FMT), row_bytes = fp4_row_bytes(K);
-    constexpr int kShift = FMT == kMx ? 1 : 0;          // groups of a block
-    for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
-        const uint32_t row = u / per_row, g = u - row * per_row;
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + row * row_bytes) + g);
-        const uint32_t b = g >> kShift;
-        const uint32_t byte = __ldg(scales + word_at(row, b >> 2, across) + (b & 3));
-        const float s = scale_value<FMT>(byte);
-        float f[kGroup];
+    const uint8_t *from = codes + row * row_bytes;
+    const uint8_t *scale = scales + word_at(row, 0, across);
+    char *out = elem_at<DT>(y, row * ldy);
+    const int skip = SHIFTED ? (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize : 0;
+    auto step_of = [&](int64_t e) {             // value of the scale of element e's block
+        const int64_t b = e / kLen;
+        return scale_value<FMT>(__ldg(scale + (b >> 2) * kScaleTile + (b & 3)));
+    };
+    uint32_t w[PARTS];
+    float lo[PARTS], hi[PARTS];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[4];
-            e2m1x8_to_f16(h ? c.y : c.x, w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 v = __half22float2(*reinterpret_cast<__half2 *>(&w[i]));
-                uint64_t p = mul_f32x2(f32x2(v.x, v.y), f32x2(s, s));
-                if constexpr (FMT == kNv) p = mul_f32x2(p, f32x2(ts.g, ts.g));
-                f[8 * h + 2 * i] = lo_f32(p);
-                f[8 * h + 2 * i + 1] = hi_f32(p);
-            }
+    for (int p = 0; p < PARTS; ++p) {
+        const int64_t e = (((int64_t)chunk * PARTS + p) * 32 + lane) * N - skip;
+        w[p] = 0;
+        lo[p] = hi[p] = 0.0f;
+        if (e >= K || e + N <= 0) continue;
+        if constexpr (!SHIFTED) {
+            if constexpr (N == 8) w[p] = __ldg(reinterpret_cast<const uint32_t *>(from + e / 2));
+            else w[p] = __ldg(reinterpret_cast<const uint16_t *>(from + e / 2));
+            lo[p] = step_of(e);
+        } else {
+            // eight codes from e on out of two words (before the row's first: none)
+            const int64_t at = e < 0 ? 0 : e & ~7ll;
+            const uint32_t a0 = __ldg(reinterpret_cast<const uint32_t *>(from + at / 2));
+            const uint32_t a1 = at / 2 + 4 < row_bytes ? __ldg(reinterpret_cast<const uint32_t *>(from + at / 2 + 4)) : 0u;
+            w[p] = e < 0 ? a0 << (-4 * (int)e) : __funnelshift_r(a0, a1, 4 * (int)(e & 7));
+            const int64_t first = e < 0 ? 0 : e, last = e + N - 1 < K ? e + N - 1 : K - 1;
+            lo[p] = step_of(first);
+            hi[p] = step_of(last);
         }
-        char *to = elem_at<DT>(y, row * ldy + (int64_t)g * kGroup);
-        if ((int64_t)(g + 1) * kGroup <= K && (reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
+    }
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i)
-                reinterpret_cast<uint4 *>(to)[i] = E::pack(f + i * E::kVec);
+    for (int p = 0; p < PARTS; ++p) {
+        const int64_t e = (((int64_t)chunk * PARTS + p) * 32 + lane) * N - skip;
+        if (e >= K || e + N <= 0) continue;
+        uint32_t h[4];
+        e2m1x8_to_f16(w[p], h);
+        const int border = SHIFTED ? kLen - (int)(e & (kLen - 1)) : N;   // elements of the first block
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 v = __half22float2(*reinterpret_cast<__half2 *>(&h[i]));
+            const uint64_t s2 = SHIFTED ? f32x2(2 * i < border ? lo[p] : hi[p], 2 * i + 1 < border ? lo[p] : hi[p])
+                                        : f32x2(lo[p], lo[p]);
+            uint64_t q = mul_f32x2(f32x2(v.x, v.y), s2);
+            if constexpr (FMT == kNv) q = mul_f32x2(q, f32x2(ts.g, ts.g));
+            f[2 * i] = lo_f32(q);
+            f[2 * i + 1] = hi_f32(q);
+        }
+        char *to = out + e * E::kSize;
+        if (e >= 0 && e + N <= K) {
+            *reinterpret_cast<uint4 *>(to) = E::pack(f);
         } else {
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-                if ((int64_t)g * kGroup + i < K) store_elem<DT>(to, i, f[i]);
+            for (int i = 0; i < N; ++i)
+                if (e + i >= 0 && e + i < K) store_elem<DT>(to, i, f[i]);
         }
     }
 }
 
 // ---- launches ------------------------------------------------------------------------------
 
-// Rows of a launch: thread numbers and rows stay within 31 bits.
-int64_t rows_a_launch(int64_t per_row) {
-    const int64_t most = (1ll << 30) / per_row / 128 * 128;
-    return most > 0 ? most : 128;
-}
-
-int grid_of(int64_t units) {
-    const int64_t ctas = (units + kThreads - 1) / kThreads, most = 64ll * sm_count();
-    return (int)(ctas < most ? ctas : most);
-}
+// Rows of a launch whose octets take `chunks` CTAs each: CTA numbers stay within 31 bits.
+int64_t rows_a_launch(int64_t chunks) { return ((1ll << 30) / chunks / 16 + 1) * 128; }
+int octets(int64_t rows) { return (int)fp4_tiles_down(rows) * 16; }
 
 template <int DT, int FMT>
 cudaError_t launch_rows(const Fp4Quant &all, cudaStream_t st) {
-    constexpr int64_t kWord = fp4_tile_elems(FMT) / kGroup;
-    const int64_t per_row = fp4_tiles_across(all.K, FMT) * kWord;
-    const int64_t step = rows_a_launch(per_row);
+    constexpr int kParts = DT == kF32 ? 1 : 2;             // 64 bytes a lane in flight
+    // whole scale words
+    const int64_t width = fp4_tiles_across(all.K, FMT) * fp4_tile_elems(FMT);
+    const int64_t chunks = (width + kParts * kRun - 1) / (kParts * kRun), step = rows_a_launch(chunks);
     for (int64_t r = 0; r < all.T; r += step) {
         Fp4Quant a = all;
         a.T = all.T - r < step ? all.T - r : step;
         a.x = static_cast<const char *>(all.x) + r * all.ldx * Elem<DT>::kSize;
         a.codes += r * fp4_row_bytes(all.K);
         a.scales += r / 128 * fp4_tiles_across(all.K, FMT) * kScaleTile;
-        const int64_t units = fp4_tiles_down(a.T) * 128 * per_row;
-        const cudaError_t e = launch_pdl(fp4_rows_kernel<DT, FMT>, grid_of(units), kThreads, 0, st,
-                                         a, (uint32_t)units, (uint32_t)per_row);
+        const cudaError_t e = launch_pdl(fp4_rows_kernel<DT, FMT, kParts>, octets(a.T) * (int)chunks,
+                                         kThreads, 0, st, a, (uint32_t)chunks);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -476,20 +525,29 @@ cudaError_t launch_quant(const Fp4Quant &a, cudaStream_t st) {
     return a.codes ? launch_tiles<DT, FMT, true>(a, st) : launch_tiles<DT, FMT, false>(a, st);
 }
 
-template <int DT, int FMT>
-cudaError_t launch_dequant(const uint8_t *codes, const uint8_t *scales, const float *amax,
-                           int64_t T, int64_t K, void *y, int64_t ldy, cudaStream_t st) {
-    const int64_t per_row = (K + kGroup - 1) / kGroup, step = rows_a_launch(per_row);
+template <int DT, int FMT, bool SHIFTED>
+cudaError_t launch_dequant_rows(const uint8_t *codes, const uint8_t *scales, const float *amax,
+                                int64_t T, int64_t K, char *y, int64_t ldy, cudaStream_t st) {
+    constexpr int kParts = 4, N = Elem<DT>::kVec;
+    const int64_t vectors = (K + N - 1 + (SHIFTED ? N - 1 : 0)) / N;
+    const int64_t chunks = (vectors + 32 * kParts - 1) / (32 * kParts), step = rows_a_launch(chunks);
     for (int64_t r = 0; r < T; r += step) {
-        const int64_t n = T - r < step ? T - r : step, units = n * per_row;
+        const int64_t n = T - r < step ? T - r : step;
         const cudaError_t e = launch_pdl(
-            fp4_dequant_kernel<DT, FMT>, grid_of(units), kThreads, 0, st,
+            fp4_dequant_kernel<DT, FMT, SHIFTED, kParts>, octets(n) * (int)chunks, kThreads, 0, st,
             codes + r * fp4_row_bytes(K), scales + r / 128 * fp4_tiles_across(K, FMT) * kScaleTile,
-            amax, n, K, static_cast<void *>(static_cast<char *>(y) + r * ldy * Elem<DT>::kSize),
-            ldy, (uint32_t)units, (uint32_t)per_row);
+            amax, n, K, static_cast<void *>(y + r * ldy * Elem<DT>::kSize), ldy, (uint32_t)chunks);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+template <int DT, int FMT>
+cudaError_t launch_dequant(const uint8_t *codes, const uint8_t *scales, const float *amax,
+                           int64_t T, int64_t K, void *y, int64_t ldy, cudaStream_t st) {
+    const bool level = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (T == 1 || ldy * Elem<DT>::kSize % 16 == 0);
+    return level ? launch_dequant_rows<DT, FMT, false>(codes, scales, amax, T, K, static_cast<char *>(y), ldy, st)
+                 : launch_dequant_rows<DT, FMT, true>(codes, scales, amax, T, K, static_cast<char *>(y), ldy, st);
 }
 
 template <int DT>
