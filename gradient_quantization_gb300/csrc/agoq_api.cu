@@ -819,7 +819,7 @@ agoq_status agoq_fp4_quant(const void *x, int64_t ldx, int64_t T, int64_t K, int
     if (!float_dtype(dtype) || (format != kMx && format != kNv)) return AGOQ_ERR_FORMAT;
     if (!fp4_size_ok(T, K) || !rows_ok(T, K, ldx)) return AGOQ_ERR_SHAPE;
     if (!codes != !scales || !codes_t != !scales_t || (!codes && !codes_t)) return AGOQ_ERR_NULL;
-    if (codes_t && (T > kMaxFp4K || fp4_tiles_down(T) * fp4_tiles_down(K) > 0x7FFFFFFF))
+    if (codes_t && (T > kMaxFp4K || fp4_tiles_down(T) * fp4_tiles_down(K) >= 1 << 30))
         return AGOQ_ERR_SHAPE;
     if (T == 0) return AGOQ_OK;
     if (!x || (format == kNv && !amax)) return AGOQ_ERR_NULL;

@@ -53,18 +53,48 @@ __device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
     return d;
 }
 
+// What a thread needs to scale blocks: NVFP4 the tensor's scale, and a table in shared memory of
+// the factor fl(1 / fl(s g)) of every scale s that E4M3 has (0 for 0): a look-up takes the place
+// of a conversion, a product and a division a block.
+struct Scaling {
+    float g = 0.0f, six_g = 0.0f, per_six_g = 0.0f;
+    bool ok = true;
+    const float *table = nullptr;
+};
+constexpr int kScaleTable = 128;
+
+// By all threads of a CTA (at least kScaleTable); the table may be read after a barrier.
+template <int FMT>
+__device__ __forceinline__ Scaling scaling_of(const float *amax, float *table) {
+    Scaling t;
+    if constexpr (FMT == kNv) {
+        const float m = __ldg(amax);
+        t.g = tensor_scale(m);
+        t.six_g = __fmul_rn(t.g, kE2M1Max);
+        t.per_six_g = __frcp_rn(t.six_g);
+        t.ok = finite_bits(m);
+        t.table = table;
+        const int i = threadIdx.x;
+        if (i < kScaleTable) {
+            float lo, hi;
+            e4m3x2_to_f32(i, lo, hi);
+            table[i] = i ? __frcp_rn(__fmul_rn(lo, t.g)) : 0.0f;
+        }
+    }
+    return t;
+}
+
 // Scale byte of a block and the factor of its elements, from its largest magnitude.  A block
 // with a NaN or an infinity (or, NVFP4, of a tensor with one) has the NaN of its scale's type
-// and, by a factor that the caller does not use, codes of 0.
-template <int FMT>
+// and codes of 0, by the caller.
 struct BlockScale {
     uint32_t byte;
     float inverse;
     bool finite;
 };
 template <int FMT>
-__device__ __forceinline__ BlockScale<FMT> block_scale(float top, float g, float six_g, bool ok) {
-    BlockScale<FMT> s;
+__device__ __forceinline__ BlockScale block_scale(float top, const Scaling &t) {
+    BlockScale s;
     if constexpr (FMT == kMx) {
         // 2^(floor(log2 top) - 2), not below 2^-127: the exponent field less 2
         const int field = (int)(__float_as_uint(top) >> 23) - 2;
@@ -73,13 +103,16 @@ __device__ __forceinline__ BlockScale<FMT> block_scale(float top, float g, float
         s.byte = s.finite ? byte : 255u;
         s.inverse = __uint_as_float((254u - byte) << 23);
     } else {
-        s.finite = ok && finite_bits(top);
-        const uint32_t byte = e4m3x2_from_f32(__fdiv_rn(top, six_g), 0.0f);
-        float lo, hi;
-        e4m3x2_to_f32(byte, lo, hi);
-        const float step = __fmul_rn(lo, g);
+        s.finite = t.ok && finite_bits(top);
+        // top times fl(1 / 6 g) is within 3 * 2^-24 of fl(top / 6 g) (relative; results below
+        // binary32's normal range are far below E4M3's): where both sides of it round to one
+        // code, that is the quotient's; else, about once in 2^15 blocks, it is divided
+        const float q = __fmul_rn(top, t.per_six_g);
+        const uint32_t both = e4m3x2_from_f32(__fmul_rn(q, 1.0f - 0x1p-20f), __fmul_rn(q, 1.0f + 0x1p-20f));
+        uint32_t byte = both & 0xFFu;
+        if (byte != both >> 8) byte = e4m3x2_from_f32(__fdiv_rn(top, t.six_g), 0.0f);
+        s.inverse = t.table[byte & 127u];
         s.byte = s.finite ? byte : 127u;
-        s.inverse = byte ? __frcp_rn(step) : 0.0f;
     }
     return s;
 }

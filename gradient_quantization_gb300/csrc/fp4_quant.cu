@@ -8,6 +8,8 @@
 // E2M1 and E4M3 round to nearest even and saturate.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "agoq_launch.h"
 #include "fp4_format.cuh"
 #include "typed_io.cuh"
@@ -19,6 +21,15 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kGroup = 16;                     // elements of a thread's group
+
+// The larger magnitudes of two pairs, NaN before all; the signs are those of the products.
+template <int DT>
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (DT == kBF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 
 template <int DT>
 struct Group {
@@ -68,14 +79,12 @@ struct Group {
             }
             return m;
         } else {
-            // magnitudes of 16-bit floats in the order of their bits, NaN last
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
-                                         __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
-            }
-            const uint32_t lo = m & 0xFFFFu, hi = m >> 16;
+            for (int i = 0; i < kVecs; ++i)
+                m = larger2<DT>(m, larger2<DT>(larger2<DT>(v[i].x, v[i].y), larger2<DT>(v[i].z, v[i].w)));
+            // magnitudes of 16-bit floats in the order of their bits, NaN last
+            const uint32_t lo = m & 0x7FFFu, hi = m >> 16 & 0x7FFFu;
             return Elem<DT>::up((uint16_t)(lo > hi ? lo : hi));
         }
     }
@@ -93,22 +102,6 @@ struct Group {
             w[h] = e2m1x8(p, inverse);
         }
         return make_uint2(w[0], w[1]);
-    }
-};
-
-struct TensorScale {
-    float g = 0.0f, six_g = 0.0f;
-    bool ok = true;
-    template <int FMT>
-    __device__ __forceinline__ static TensorScale of(const float *amax) {
-        TensorScale t;
-        if constexpr (FMT == kNv) {
-            const float m = __ldg(amax);
-            t.g = tensor_scale(m);
-            t.six_g = __fmul_rn(t.g, kE2M1Max);
-            t.ok = finite_bits(m);
-        }
-        return t;
     }
 };
 
@@ -151,8 +144,8 @@ __global__ void __launch_bounds__(kThreads) fp4_rows_kernel(const Fp4Quant a, ui
     constexpr int kWord = fp4_tile_elems(FMT) / kGroup;        // lanes of a scale word
     constexpr int kWords = 32 / kWord;                         // of a run
     __shared__ uint32_t words[PARTS * kWords][kOctet];
+    __shared__ float table[kScaleTable];
     pdl_wait_and_release();
-    const TensorScale ts = TensorScale::of<FMT>(a.amax);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t octet = blockIdx.x / chunks, chunk = blockIdx.x - octet * chunks;
     const int64_t block = octet >> 4, row = block * 128 + octet_row(octet & 15, warp);
@@ -166,16 +159,20 @@ __global__ void __launch_bounds__(kThreads) fp4_rows_kernel(const Fp4Quant a, ui
         if (live && e < a.K) x[p].load(from, e, a.K);
         else x[p].clear();
     }
+    const Scaling scaling = scaling_of<FMT>(a.amax, table);
+    if constexpr (FMT == kNv) __syncthreads();
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
         float top = x[p].absmax();
         if constexpr (FMT == kMx) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        const BlockScale<FMT> s = block_scale<FMT>(top, ts.g, ts.six_g, ts.ok);
+        const BlockScale s = block_scale<FMT>(top, scaling);
         uint2 c = x[p].codes(s.inverse);
         if (!s.finite) c = make_uint2(0, 0);
         const int64_t at = ((int64_t)chunk * PARTS + p) * (kRun / 2) + lane * 8;
         if (live && at < row_bytes) *reinterpret_cast<uint2 *>(a.codes + row * row_bytes + at) = c;
-        const uint32_t w = scale_word<FMT>(s.byte, lane);
+        // (no block begins behind the row's end)
+        const int64_t first = ((int64_t)chunk * PARTS + p) * kRun + (FMT == kMx ? lane & ~1 : lane) * kGroup;
+        const uint32_t w = scale_word<FMT>(live && first < a.K ? s.byte : 0u, lane);
         // (word of the sector: neighbours are 16 bytes apart, the other rows 4)
         if (lane % kWord == 0) words[p * kWords + lane / kWord][(warp & 1) * 4 + (warp >> 1)] = w;
     }
@@ -189,41 +186,49 @@ __global__ void __launch_bounds__(kThreads) fp4_rows_kernel(const Fp4Quant a, ui
 
 // ---- columns, and both -------------------------------------------------------------
 //
-// A CTA takes a tile of 128 x 128: its rows are quantised as they are loaded (ROWS), the tile
-// goes to shared memory, and a thread then takes a block of two neighbouring columns.  The
-// tile's codes of the columns and its scale tiles are gathered in shared memory and leave in
-// whole rows.
+// A CTA takes a tile of 128 columns by 128 rows (FP32: 64): its rows are quantised as they are
+// loaded (ROWS), the tile goes to shared memory, and a thread then takes a block of two
+// neighbouring columns.  The tile's codes of the columns and its scale tiles are gathered in
+// shared memory and leave in whole rows.
 constexpr int kTile = 128;
-constexpr int kCodePitch = 72;                 // bytes of a column's 64 bytes of codes
+template <int DT>
+struct TileShape {
+    static constexpr int kRows = DT == kF32 ? 64 : 128;        // 32 KB of elements
+    static constexpr int kCodePitch = kRows / 2 + 8;           // bytes of a column's codes
+};
 
 template <int DT, int FMT, bool ROWS>
-__global__ void __launch_bounds__(kThreads) fp4_tiles_kernel(const Fp4Quant a, int64_t tiles_k) {
+__global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a, int64_t tiles_k) {
     using E = Elem<DT>;
-    constexpr int kPitch = kTile * E::kSize;
-    constexpr int kBlockLen = fp4_block(FMT);
-    constexpr int kTilesHere = kTile / fp4_tile_elems(FMT);    // scale tiles along 128 elements
+    using S = TileShape<DT>;
+    constexpr int kPitch = kTile * E::kSize, kRows = S::kRows, kSteps = kRows / 32;
+    constexpr int kBlockLen = fp4_block(FMT), kSpan = fp4_tile_elems(FMT);
+    constexpr int kTilesK = kTile / kSpan;                     // scale tiles along the columns
+    constexpr int kTilesT = kRows > kSpan ? kRows / kSpan : 1; // and along the rows
     extern __shared__ __align__(16) uint8_t tile[];
-    uint8_t *out = tile + kTile * kPitch;                      // codes of the columns
-    uint8_t *scales = out + kTile * kCodePitch;                // their scale tiles
-    uint8_t *row_scales = scales + kTilesHere * kScaleTile;
+    uint8_t *out = tile + kRows * kPitch;                      // codes of the columns
+    uint8_t *scales = out + kTile * S::kCodePitch;             // their scale tiles
+    uint8_t *row_scales = scales + kTilesT * kScaleTile;
+    __shared__ float table[kScaleTable];
     pdl_wait_and_release();
-    const TensorScale ts = TensorScale::of<FMT>(a.amax);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t0 = blockIdx.x / tiles_k * kTile, k0 = blockIdx.x % tiles_k * kTile;
+    const int64_t t0 = blockIdx.x / tiles_k * kRows, k0 = blockIdx.x % tiles_k * kTile;
     const int64_t row_bytes = fp4_row_bytes(a.K), col_bytes = fp4_row_bytes(a.T);
     // rows: eight threads a row, 32 rows a step
     const int g = threadIdx.x & 7;
-    Group<DT> x[4];
+    Group<DT> x[kSteps];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kSteps; ++i) {
         const int64_t t = t0 + 32 * i + (threadIdx.x >> 3);
         if (t < a.T && k0 + g * kGroup < a.K)
             x[i].load(elem_at<DT>(a.x, t * a.ldx), k0 + g * kGroup, a.K);
         else
             x[i].clear();
     }
+    const Scaling scaling = scaling_of<FMT>(a.amax, table);
+    if constexpr (FMT == kNv && ROWS) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kSteps; ++i) {
         const int r = 32 * i + (threadIdx.x >> 3);
         uint4 *to = reinterpret_cast<uint4 *>(tile + r * kPitch + g * kGroup * E::kSize);
 #pragma unroll
@@ -231,13 +236,14 @@ __global__ void __launch_bounds__(kThreads) fp4_tiles_kernel(const Fp4Quant a, i
         if constexpr (ROWS) {
             float top = x[i].absmax();
             if constexpr (FMT == kMx) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            const BlockScale<FMT> s = block_scale<FMT>(top, ts.g, ts.six_g, ts.ok);
+            const BlockScale s = block_scale<FMT>(top, scaling);
             uint2 c = x[i].codes(s.inverse);
             if (!s.finite) c = make_uint2(0, 0);
             const int64_t at = k0 / 2 + g * 8;
             if (t0 + r < a.T && at < row_bytes)
                 *reinterpret_cast<uint2 *>(a.codes + (t0 + r) * row_bytes + at) = c;
-            const uint32_t w = scale_word<FMT>(s.byte, lane);
+            const bool block = t0 + r < a.T && k0 + (FMT == kMx ? g & ~1 : g) * kGroup < a.K;
+            const uint32_t w = scale_word<FMT>(block ? s.byte : 0u, lane);
             constexpr int kWord = FMT == kMx ? 8 : 4;
             if (g % kWord == 0)
                 *reinterpret_cast<uint32_t *>(row_scales + g / kWord * kScaleTile + (r & 31) * 16 +
@@ -246,44 +252,37 @@ __global__ void __launch_bounds__(kThreads) fp4_tiles_kernel(const Fp4Quant a, i
     }
     __syncthreads();
     // columns 2 c and 2 c + 1, blocks of kBlockLen rows
-    constexpr int kTasks = kTile / kBlockLen * (kTile / 2);
+    constexpr int kTasks = kRows / kBlockLen * (kTile / 2);
     for (int task = threadIdx.x; task < kTasks; task += kThreads) {
         const int c = task & 63, b = task >> 6;
-        float lo[kBlockLen], hi[kBlockLen];
-        float top_lo, top_hi;
-        if constexpr (DT == kF32) {
-            top_lo = top_hi = 0.0f;
+        // the two columns' elements as they lie in the tile
+        using Pair = typename std::conditional<DT == kF32, float2, uint32_t>::type;
+        Pair v[kBlockLen];
+        float top[2] = {0.0f, 0.0f};
+        uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < kBlockLen; ++i) {
-                const float2 v = *reinterpret_cast<const float2 *>(
-                    tile + (b * kBlockLen + i) * kPitch + c * 8);
-                lo[i] = v.x;
-                hi[i] = v.y;
-            }
+        for (int i = 0; i < kBlockLen; ++i)
+            v[i] = *reinterpret_cast<const Pair *>(tile + (b * kBlockLen + i) * kPitch + c * sizeof(Pair));
+        if constexpr (DT == kF32) {
 #pragma unroll
             for (int i = 0; i < kBlockLen; i += 2) {
-                top_lo = max_abs_nan(top_lo, lo[i], lo[i + 1]);
-                top_hi = max_abs_nan(top_hi, hi[i], hi[i + 1]);
+                top[0] = max_abs_nan(top[0], v[i].x, v[i + 1].x);
+                top[1] = max_abs_nan(top[1], v[i].y, v[i + 1].y);
             }
         } else {
-            uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < kBlockLen; ++i) {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                    tile + (b * kBlockLen + i) * kPitch + c * 4);
-                m = __vmaxu2(m, w & 0x7FFF7FFFu);
-                lo[i] = E::up((uint16_t)w);
-                hi[i] = E::up((uint16_t)(w >> 16));
-            }
-            top_lo = E::up((uint16_t)m);
-            top_hi = E::up((uint16_t)(m >> 16));
+            for (int i = 0; i < kBlockLen; ++i) m = larger2<DT>(m, v[i]);
+            top[0] = E::up((uint16_t)(m & 0x7FFFu));
+            top[1] = E::up((uint16_t)(m >> 16 & 0x7FFFu));
         }
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            const float *f = side ? hi : lo;
-            const BlockScale<FMT> s =
-                block_scale<FMT>(side ? top_hi : top_lo, ts.g, ts.six_g, ts.ok);
+            const BlockScale s = block_scale<FMT>(top[side], scaling);
             const int col = 2 * c + side;
+            auto element = [&](int i) {
+                if constexpr (DT == kF32) return side ? v[i].y : v[i].x;
+                else return E::up((uint16_t)(side ? v[i] >> 16 : v[i]));
+            };
 #pragma unroll
             for (int h = 0; h < kBlockLen / 16; ++h) {
                 uint32_t w[2];
@@ -291,40 +290,59 @@ __global__ void __launch_bounds__(kThreads) fp4_tiles_kernel(const Fp4Quant a, i
                 for (int q = 0; q < 2; ++q) {
                     uint64_t p[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        p[i] = f32x2(f[16 * h + 8 * q + 2 * i], f[16 * h + 8 * q + 2 * i + 1]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = 16 * h + 8 * q + 2 * i;
+                        p[i] = f32x2(element(at), element(at + 1));
+                    }
                     w[q] = s.finite ? e2m1x8(p, s.inverse) : 0u;
                 }
-                *reinterpret_cast<uint2 *>(out + col * kCodePitch + b * (kBlockLen / 2) + 8 * h) =
+                *reinterpret_cast<uint2 *>(out + col * S::kCodePitch + b * (kBlockLen / 2) + 8 * h) =
                     make_uint2(w[0], w[1]);
             }
             scales[(b >> 2) * kScaleTile + (col & 31) * 16 + (col >> 5) * 4 + (b & 3)] =
-                (uint8_t)s.byte;
+                (uint8_t)(k0 + col < a.K && t0 + b * kBlockLen < a.T ? s.byte : 0u);
         }
     }
     __syncthreads();
-    // eight threads a column
-    for (int col = threadIdx.x >> 3; col < kTile; col += kThreads / 8) {
-        const int64_t at = t0 / 2 + g * 8;
+    // codes: kRows / 16 threads a column
+    constexpr int kPer = kRows / 16;
+    const int j = threadIdx.x % kPer;
+    for (int col = threadIdx.x / kPer; col < kTile; col += kThreads / kPer) {
+        const int64_t at = t0 / 2 + j * 8;
         if (k0 + col < a.K && at < col_bytes)
             *reinterpret_cast<uint2 *>(a.codes_t + (k0 + col) * col_bytes + at) =
-                *reinterpret_cast<const uint2 *>(out + col * kCodePitch + g * 8);
+                *reinterpret_cast<const uint2 *>(out + col * S::kCodePitch + j * 8);
     }
-    // scale tiles, a warp each
+    // Scale tiles, a warp each.  A tile of 64 rows fills half of a scale tile's rows, and of MXFP4
+    // half of its blocks; where no rows follow, it clears the other half.
     const int64_t down_t = fp4_tiles_across(a.T, FMT), across = fp4_tiles_across(a.K, FMT);
-    if (warp < kTilesHere) {
-        const int64_t at = t0 / fp4_tile_elems(FMT) + warp;
-        if (at < down_t)
-            *reinterpret_cast<uint4 *>(a.scales_t + ((k0 >> 7) * down_t + at) * kScaleTile +
-                                       lane * 16) =
-                *reinterpret_cast<const uint4 *>(scales + warp * kScaleTile + lane * 16);
-    } else if (ROWS && warp < 2 * kTilesHere) {
-        const int w = warp - kTilesHere;
-        const int64_t at = k0 / fp4_tile_elems(FMT) + w;
-        if (at < across)
-            *reinterpret_cast<uint4 *>(a.scales + ((t0 >> 7) * across + at) * kScaleTile +
-                                       lane * 16) =
-                *reinterpret_cast<const uint4 *>(row_scales + w * kScaleTile + lane * 16);
+    const bool second = kRows == 64 && (t0 & 64), last = kRows == 64 && !second && t0 + 64 >= a.T;
+    if (warp < kTilesT) {
+        const int64_t at = t0 / kSpan + warp;
+        uint8_t *to = a.scales_t + ((k0 >> 7) * down_t + at) * kScaleTile + lane * 16;
+        const uint4 v = *reinterpret_cast<const uint4 *>(scales + warp * kScaleTile + lane * 16);
+        if (at < down_t) {
+            if constexpr (kRows >= kSpan) {
+                *reinterpret_cast<uint4 *>(to) = v;
+            } else {
+                const uint32_t w[4] = {v.x & 0xFFFFu, v.y & 0xFFFFu, v.z & 0xFFFFu, v.w & 0xFFFFu};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (last) reinterpret_cast<uint32_t *>(to)[i] = w[i];
+                    else reinterpret_cast<uint16_t *>(to)[2 * i + second] = (uint16_t)w[i];
+                }
+            }
+        }
+    } else if (ROWS && warp < kTilesT + kTilesK) {
+        const int w = warp - kTilesT;
+        const int64_t at = k0 / kSpan + w;
+        uint8_t *to = a.scales + ((t0 >> 7) * across + at) * kScaleTile + lane * 16;
+        const uint4 v = *reinterpret_cast<const uint4 *>(row_scales + w * kScaleTile + lane * 16);
+        if (at < across) {
+            if constexpr (kRows == 128) *reinterpret_cast<uint4 *>(to) = v;
+            else if (last) *reinterpret_cast<uint4 *>(to) = make_uint4(v.x, v.y, 0, 0);
+            else reinterpret_cast<uint2 *>(to)[second] = make_uint2(v.x, v.y);
+        }
     }
 }
 
@@ -414,7 +432,7 @@ fp4_dequant_kernel(const uint8_t *codes, const uint8_t *scales, const float *ama
     using E = Elem<DT>;
     constexpr int N = E::kVec, kLen = fp4_block(FMT);
     pdl_wait_and_release();
-    const TensorScale ts = TensorScale::of<FMT>(amax);
+    const float g = FMT == kNv ? tensor_scale(__ldg(amax)) : 1.0f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t octet = blockIdx.x / chunks, chunk = blockIdx.x - octet * chunks;
     const int64_t row = (int64_t)(octet >> 4) * 128 + octet_row(octet & 15, warp);
@@ -465,7 +483,7 @@ fp4_dequant_kernel(const uint8_t *codes, const uint8_t *scales, const float *ama
             const uint64_t s2 = SHIFTED ? f32x2(2 * i < border ? lo[p] : hi[p], 2 * i + 1 < border ? lo[p] : hi[p])
                                         : f32x2(lo[p], lo[p]);
             uint64_t q = mul_f32x2(f32x2(v.x, v.y), s2);
-            if constexpr (FMT == kNv) q = mul_f32x2(q, f32x2(ts.g, ts.g));
+            if constexpr (FMT == kNv) q = mul_f32x2(q, f32x2(g, g));
             f[2 * i] = lo_f32(q);
             f[2 * i + 1] = hi_f32(q);
         }
@@ -508,13 +526,15 @@ cudaError_t launch_rows(const Fp4Quant &all, cudaStream_t st) {
 template <int DT, int FMT, bool ROWS>
 cudaError_t launch_tiles(const Fp4Quant &a, cudaStream_t st) {
     static bool ready[kMaxDevices];
-    constexpr int kTilesHere = kTile / fp4_tile_elems(FMT);
-    constexpr size_t bytes = kTile * kTile * Elem<DT>::kSize + kTile * kCodePitch +
-                             2 * kTilesHere * kScaleTile;
+    using S = TileShape<DT>;
+    constexpr int kSpan = fp4_tile_elems(FMT);
+    constexpr int kScaleTiles = kTile / kSpan + (S::kRows > kSpan ? S::kRows / kSpan : 1);
+    constexpr size_t bytes = S::kRows * kTile * Elem<DT>::kSize + kTile * S::kCodePitch +
+                             kScaleTiles * kScaleTile;
     auto kernel = fp4_tiles_kernel<DT, FMT, ROWS>;
     const cudaError_t e = allow_shared(kernel, bytes, ready);
     if (e != cudaSuccess) return e;
-    const int64_t tiles_k = (a.K + kTile - 1) / kTile, tiles = (a.T + kTile - 1) / kTile * tiles_k;
+    const int64_t tiles_k = (a.K + kTile - 1) / kTile, tiles = (a.T + S::kRows - 1) / S::kRows * tiles_k;
     if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     return launch_pdl(kernel, (int)tiles, kThreads, bytes, st, a, tiles_k);
 }

@@ -648,7 +648,7 @@ agoq_status agoq_preference_loss(const float *logp, const float *ref_logp, const
  *   scales : tiles of 128 rows by 4 blocks, 512 bytes each, row blocks slowest
  *            (ceil(rows/128) x ceil(blocks/4) tiles): block b of row r is byte
  *            (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4 of tile (r / 128, b / 4); 0 where
- *            there is no block.  (The tensor cores' own order: the product copies tiles as
+ *            there is no such row or where a block would begin behind the row's end.  (The tensor cores' own order: the product copies tiles as
  *            they are.)
  * Both 16-byte aligned.  1 <= K <= 2^24, rows <= 2^30.
  */

@@ -80,7 +80,9 @@ def quantise(x, fmt, amax=None):
         nan = 127
     codes = e2m1(f32(b * inverse[:, :, None]))
     codes = torch.where(fine[:, :, None], codes, torch.zeros_like(codes)).view(T, -1)
-    return codes, torch.where(fine, byte, torch.full_like(byte, nan)), step
+    byte = torch.where(fine, byte, torch.full_like(byte, nan))
+    byte[:, -(-K // BLOCK[fmt]):] = 0               # no block begins there
+    return codes, byte, step
 
 
 def pack(codes):
@@ -103,15 +105,8 @@ def place(r, b, across):
 
 
 def stored(x, fmt, amax=None):
-    """(codes, scales) as the library writes them.  (The last tile of a row block may reach
-    beyond the last block of 32: those scales are 0, or NaN with an amax that is not finite.)"""
+    """(codes, scales) as the library writes them."""
     codes, scales, _ = quantise(x, fmt, amax)
-    bad = amax is not None and not (abs(amax) < float("inf"))
-    if bad:
-        R, nb = scales.shape
-        full = torch.full((-(-R // 128) * 128, -(-nb // 4) * 4), 127, dtype=torch.uint8,
-                          device=x.device)
-        return pack(codes), tile(full)
     return pack(codes), tile(scales)
 
 
