@@ -229,6 +229,7 @@ struct Fp4Quant {
     const float *amax;                        // NVFP4
     uint8_t *codes, *scales;                  // of the rows, or NULL
     uint8_t *codes_t, *scales_t;              // of the columns, or NULL
+    bool level = false;                       // rows begin at 16-byte boundaries (set at launch)
 };
 cudaError_t launch_fp4_quant(const Fp4Quant &a, cudaStream_t st);
 cudaError_t launch_fp4_dequant(const uint8_t *codes, const uint8_t *scales, const float *amax,

@@ -186,9 +186,8 @@ __global__ void __launch_bounds__(kThreads) fp4_rows_kernel(const Fp4Quant a, ui
 
 // ---- columns, and both -------------------------------------------------------------
 //
-// A CTA takes a tile of 128 columns by 128 rows (FP32: 64): its rows are quantised as they are
-// loaded (ROWS), the tile goes to shared memory, and a thread then takes a block of two
-// neighbouring columns.  The tile's codes of the columns and its scale tiles are gathered in
+// A CTA copies a tile of 128 columns by 128 rows (FP32: 64) to shared memory; eight threads take
+// a row (ROWS), and a thread then takes a block of two neighbouring columns.  The tile's codes of the columns and its scale tiles are gathered in
 // shared memory and leave in whole rows.
 constexpr int kTile = 128;
 template <int DT>
@@ -214,30 +213,64 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t0 = blockIdx.x / tiles_k * kRows, k0 = blockIdx.x % tiles_k * kTile;
     const int64_t row_bytes = fp4_row_bytes(a.K), col_bytes = fp4_row_bytes(a.T);
-    // rows: eight threads a row, 32 rows a step
     const int g = threadIdx.x & 7;
-    Group<DT> x[kSteps];
+    // Where vector v of a row lies: the vectors of eight threads' groups in eight different places
+    // between 128-byte lines.
+    auto place = [](int v) { return v ^ (v >> 3 & (Group<DT>::kVecs - 1)); };
+    if (a.level) {
+        // 16-byte vectors, a warp whole lines of a row
+        constexpr int kVecs = kPitch / 16;
+        for (int i = threadIdx.x; i < kRows * kVecs; i += kThreads) {
+            const int r = i / kVecs, v = i % kVecs;
+            const int64_t e = k0 + v * E::kVec;
+            uint8_t *to = tile + r * kPitch + place(v) * 16;
+            const char *row = elem_at<DT>(a.x, (t0 + r) * a.ldx);
+            if (t0 + r < a.T && e + E::kVec <= a.K) {
+                copy16(to, row + e * E::kSize);
+            } else {
+                typename E::Word w[E::kVec];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int64_t t = t0 + 32 * i + (threadIdx.x >> 3);
-        if (t < a.T && k0 + g * kGroup < a.K)
-            x[i].load(elem_at<DT>(a.x, t * a.ldx), k0 + g * kGroup, a.K);
-        else
-            x[i].clear();
+                for (int j = 0; j < E::kVec; ++j)
+                    w[j] = t0 + r < a.T && e + j < a.K ? reinterpret_cast<const typename E::Word *>(row)[e + j]
+                                                       : typename E::Word(0);
+                __builtin_memcpy(to, w, 16);
+            }
+        }
+        copies_commit();
+    } else {
+        Group<DT> x[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int64_t t = t0 + 32 * i + (threadIdx.x >> 3);
+            if (t < a.T && k0 + g * kGroup < a.K)
+                x[i].load(elem_at<DT>(a.x, t * a.ldx), k0 + g * kGroup, a.K);
+            else
+                x[i].clear();
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            uint8_t *to = tile + (32 * i + (threadIdx.x >> 3)) * kPitch;
+#pragma unroll
+            for (int j = 0; j < Group<DT>::kVecs; ++j)
+                *reinterpret_cast<uint4 *>(to + place(g * Group<DT>::kVecs + j) * 16) = x[i].v[j];
+        }
     }
     const Scaling scaling = scaling_of<FMT>(a.amax, table);
-    if constexpr (FMT == kNv && ROWS) __syncthreads();
+    copies_left<0>();
+    __syncthreads();
+    // rows: eight threads a row, 32 rows a step
+    if constexpr (ROWS) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int r = 32 * i + (threadIdx.x >> 3);
-        uint4 *to = reinterpret_cast<uint4 *>(tile + r * kPitch + g * kGroup * E::kSize);
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = 32 * i + (threadIdx.x >> 3);
+            Group<DT> x;
 #pragma unroll
-        for (int j = 0; j < Group<DT>::kVecs; ++j) to[j] = x[i].v[j];
-        if constexpr (ROWS) {
-            float top = x[i].absmax();
+            for (int j = 0; j < Group<DT>::kVecs; ++j)
+                x.v[j] = *reinterpret_cast<const uint4 *>(tile + r * kPitch + place(g * Group<DT>::kVecs + j) * 16);
+            float top = x.absmax();
             if constexpr (FMT == kMx) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             const BlockScale s = block_scale<FMT>(top, scaling);
-            uint2 c = x[i].codes(s.inverse);
+            uint2 c = x.codes(s.inverse);
             if (!s.finite) c = make_uint2(0, 0);
             const int64_t at = k0 / 2 + g * 8;
             if (t0 + r < a.T && at < row_bytes)
@@ -250,11 +283,12 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a
                                               (r >> 5) * 4) = w;
         }
     }
-    __syncthreads();
     // columns 2 c and 2 c + 1, blocks of kBlockLen rows
     constexpr int kTasks = kRows / kBlockLen * (kTile / 2);
     for (int task = threadIdx.x; task < kTasks; task += kThreads) {
         const int c = task & 63, b = task >> 6;
+        constexpr int kPairs = 8 / E::kSize;           // column pairs of a vector
+        const int at_c = place(c / kPairs) * 16 + c % kPairs * 2 * E::kSize;
         // the two columns' elements as they lie in the tile
         using Pair = typename std::conditional<DT == kF32, float2, uint32_t>::type;
         Pair v[kBlockLen];
@@ -262,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < kBlockLen; ++i)
-            v[i] = *reinterpret_cast<const Pair *>(tile + (b * kBlockLen + i) * kPitch + c * sizeof(Pair));
+            v[i] = *reinterpret_cast<const Pair *>(tile + (b * kBlockLen + i) * kPitch + at_c);
         if constexpr (DT == kF32) {
 #pragma unroll
             for (int i = 0; i < kBlockLen; i += 2) {
@@ -536,7 +570,9 @@ cudaError_t launch_tiles(const Fp4Quant &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t tiles_k = (a.K + kTile - 1) / kTile, tiles = (a.T + S::kRows - 1) / S::kRows * tiles_k;
     if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    return launch_pdl(kernel, (int)tiles, kThreads, bytes, st, a, tiles_k);
+    Fp4Quant b = a;
+    b.level = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.T == 1 || a.ldx * Elem<DT>::kSize % 16 == 0);
+    return launch_pdl(kernel, (int)tiles, kThreads, bytes, st, b, tiles_k);
 }
 
 template <int DT, int FMT>
