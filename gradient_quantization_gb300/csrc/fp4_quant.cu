@@ -36,9 +36,10 @@ struct Group {
     static constexpr int kVecs = kGroup * Elem<DT>::kSize / 16;
     uint4 v[kVecs];
     // Elements e .. e + 15 of a row of K (0 beyond it).
-    __device__ __forceinline__ void load(const char *row, int64_t e, int64_t K) {
+    template <typename I>                          // int where rows are short enough
+    __device__ __forceinline__ void load(const char *row, I e, I K) {
         using E = Elem<DT>;
-        const char *p = row + e * E::kSize;
+        const char *p = row + (int64_t)e * E::kSize;
         const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
         if (shift == 0 && e + kGroup <= K) {
 #pragma unroll
@@ -140,7 +141,7 @@ __device__ __forceinline__ int octet_row(int octet, int warp) {       // within 
 constexpr int kRun = 32 * kGroup;
 
 template <int DT, int FMT, int PARTS>
-__global__ void __launch_bounds__(kThreads) fp4_rows_kernel(const Fp4Quant a, uint32_t chunks) {
+__global__ void __launch_bounds__(kThreads, 6) fp4_rows_kernel(const Fp4Quant a, uint32_t chunks) {
     constexpr int kWord = fp4_tile_elems(FMT) / kGroup;        // lanes of a scale word
     constexpr int kWords = 32 / kWord;                         // of a run
     __shared__ uint32_t words[PARTS * kWords][kOctet];
@@ -148,39 +149,41 @@ __global__ void __launch_bounds__(kThreads) fp4_rows_kernel(const Fp4Quant a, ui
     pdl_wait_and_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t octet = blockIdx.x / chunks, chunk = blockIdx.x - octet * chunks;
-    const int64_t block = octet >> 4, row = block * 128 + octet_row(octet & 15, warp);
-    const int64_t across = fp4_tiles_across(a.K, FMT), row_bytes = fp4_row_bytes(a.K);
+    const int64_t block_row = octet >> 4, row = block_row * 128 + octet_row(octet & 15, warp);
+    // (places within a row, of at most 2^24 elements, in 32 bits)
+    const int len = (int)a.K, across = (int)fp4_tiles_across(a.K, FMT), row_bytes = (int)fp4_row_bytes(a.K);
     const bool live = row < a.T;
     const char *from = elem_at<DT>(a.x, live ? row * a.ldx : 0);
+    const int e0 = (int)chunk * PARTS * kRun + lane * kGroup;
     Group<DT> x[PARTS];
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-        const int64_t e = ((int64_t)chunk * PARTS + p) * kRun + lane * kGroup;
-        if (live && e < a.K) x[p].load(from, e, a.K);
+        if (live && e0 + p * kRun < len) x[p].load(from, e0 + p * kRun, len);
         else x[p].clear();
     }
     const Scaling scaling = scaling_of<FMT>(a.amax, table);
     if constexpr (FMT == kNv) __syncthreads();
+    uint8_t *codes = a.codes + (live ? row * row_bytes : 0);
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
+        const int e = e0 + p * kRun;
         float top = x[p].absmax();
         if constexpr (FMT == kMx) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         const BlockScale s = block_scale<FMT>(top, scaling);
         uint2 c = x[p].codes(s.inverse);
         if (!s.finite) c = make_uint2(0, 0);
-        const int64_t at = ((int64_t)chunk * PARTS + p) * (kRun / 2) + lane * 8;
-        if (live && at < row_bytes) *reinterpret_cast<uint2 *>(a.codes + row * row_bytes + at) = c;
+        if (live && e / 2 < row_bytes) *reinterpret_cast<uint2 *>(codes + e / 2) = c;
         // (no block begins behind the row's end)
-        const int64_t first = ((int64_t)chunk * PARTS + p) * kRun + (FMT == kMx ? lane & ~1 : lane) * kGroup;
-        const uint32_t w = scale_word<FMT>(live && first < a.K ? s.byte : 0u, lane);
+        const bool block = live && (FMT == kMx ? e & ~(2 * kGroup - 1) : e) < len;
+        const uint32_t w = scale_word<FMT>(block ? s.byte : 0u, lane);
         // (word of the sector: neighbours are 16 bytes apart, the other rows 4)
         if (lane % kWord == 0) words[p * kWords + lane / kWord][(warp & 1) * 4 + (warp >> 1)] = w;
     }
     __syncthreads();
     const int i = threadIdx.x, t = i >> 3;
-    const int64_t tile = (int64_t)chunk * PARTS * kWords + t;
+    const int tile = (int)chunk * PARTS * kWords + t;
     if (t < PARTS * kWords && tile < across)
-        *reinterpret_cast<uint32_t *>(a.scales + (block * across + tile) * kScaleTile +
+        *reinterpret_cast<uint32_t *>(a.scales + (block_row * across + tile) * kScaleTile +
                                       2 * (octet & 15) * 16 + (i & 7) * 4) = words[t][i & 7];
 }
 
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a
         for (int i = 0; i < kSteps; ++i) {
             const int64_t t = t0 + 32 * i + (threadIdx.x >> 3);
             if (t < a.T && k0 + g * kGroup < a.K)
-                x[i].load(elem_at<DT>(a.x, t * a.ldx), k0 + g * kGroup, a.K);
+                x[i].load(elem_at<DT>(a.x, t * a.ldx), (int)k0 + g * kGroup, (int)a.K);
             else
                 x[i].clear();
         }
@@ -386,17 +389,44 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a
 template <int DT>
 __device__ __forceinline__ uint32_t absmax_of(const void *x, int64_t ldx, int64_t T, int64_t K,
                                               int64_t first, int64_t step) {
-    const int64_t per_row = (K + kGroup - 1) / kGroup;
     uint32_t m = 0;
     if (T == 1) {
-#pragma unroll 2
-        for (int64_t g = first; g < per_row; g += step) {
-            Group<DT> v;
-            v.load(static_cast<const char *>(x), g * kGroup, K);
-            m = max(m, __float_as_uint(v.absmax()));
+        // one long row: whole lines a warp; single elements before and behind its 16-byte vectors
+        using Word = typename Elem<DT>::Word;
+        constexpr int N = Elem<DT>::kVec;
+        const Word *row = static_cast<const Word *>(x);
+        const int64_t skip = (16 - (reinterpret_cast<uintptr_t>(x) & 15u)) % 16 / Elem<DT>::kSize;
+        const int64_t head = skip < K ? skip : K, n = (K - head) / N;
+        const uint4 *vec = reinterpret_cast<const uint4 *>(row + head);
+        float top = 0.0f;
+        uint32_t two = 0;
+        auto add = [&](const uint4 &v) {
+            if constexpr (DT == kF32) {
+                top = max_abs_nan(top, __uint_as_float(v.x), __uint_as_float(v.y));
+                top = max_abs_nan(top, __uint_as_float(v.z), __uint_as_float(v.w));
+            } else {
+                two = larger2<DT>(two, larger2<DT>(larger2<DT>(v.x, v.y), larger2<DT>(v.z, v.w)));
+            }
+        };
+        int64_t i = first;
+        for (; i + 3 * step < n; i += 4 * step) {
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = __ldg(vec + i + j * step);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add(v[j]);
         }
-        return m;
+        for (; i < n; i += step) add(__ldg(vec + i));
+        if constexpr (DT != kF32) {
+            const uint32_t lo = two & 0x7FFFu, hi = two >> 16 & 0x7FFFu;
+            top = Elem<DT>::up((uint16_t)(lo > hi ? lo : hi));
+        }
+        const int64_t tail = K - head - n * N;
+        if (first < head) top = larger(top, Elem<DT>::up(__ldg(row + first)));
+        if (first < tail) top = larger(top, Elem<DT>::up(__ldg(row + head + n * N + first)));
+        return __float_as_uint(top);
     }
+    const int64_t per_row = (K + kGroup - 1) / kGroup;
     int64_t row = first / per_row, g = first % per_row;
     const int64_t rows_step = step / per_row, g_step = step % per_row;
     while (row < T) {
@@ -471,45 +501,46 @@ fp4_dequant_kernel(const uint8_t *codes, const uint8_t *scales, const float *ama
     const uint32_t octet = blockIdx.x / chunks, chunk = blockIdx.x - octet * chunks;
     const int64_t row = (int64_t)(octet >> 4) * 128 + octet_row(octet & 15, warp);
     if (row >= T) return;
-    const int64_t across = fp4_tiles_across(K, FMT), row_bytes = fp4_row_bytes(K);
+    // (places within a row, of at most 2^24 elements, in 32 bits)
+    const int len = (int)K, row_bytes = (int)fp4_row_bytes(K);
     const uint8_t *from = codes + row * row_bytes;
-    const uint8_t *scale = scales + word_at(row, 0, across);
+    const uint8_t *scale = scales + word_at(row, 0, fp4_tiles_across(K, FMT));
     char *out = elem_at<DT>(y, row * ldy);
     const int skip = SHIFTED ? (int)(reinterpret_cast<uintptr_t>(out) & 15u) / E::kSize : 0;
-    auto step_of = [&](int64_t e) {             // value of the scale of element e's block
-        const int64_t b = e / kLen;
+    auto step_of = [&](int e) {                 // value of the scale of element e's block
+        const uint32_t b = (uint32_t)e / kLen;
         return scale_value<FMT>(__ldg(scale + (b >> 2) * kScaleTile + (b & 3)));
     };
+    const int e0 = ((int)chunk * PARTS * 32 + lane) * N - skip;
     uint32_t w[PARTS];
     float lo[PARTS], hi[PARTS];
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-        const int64_t e = (((int64_t)chunk * PARTS + p) * 32 + lane) * N - skip;
+        const int e = e0 + 32 * N * p;
         w[p] = 0;
         lo[p] = hi[p] = 0.0f;
-        if (e >= K || e + N <= 0) continue;
+        if (e >= len || e + N <= 0) continue;
         if constexpr (!SHIFTED) {
             if constexpr (N == 8) w[p] = __ldg(reinterpret_cast<const uint32_t *>(from + e / 2));
             else w[p] = __ldg(reinterpret_cast<const uint16_t *>(from + e / 2));
             lo[p] = step_of(e);
         } else {
             // eight codes from e on out of two words (before the row's first: none)
-            const int64_t at = e < 0 ? 0 : e & ~7ll;
+            const int at = e < 0 ? 0 : e & ~7;
             const uint32_t a0 = __ldg(reinterpret_cast<const uint32_t *>(from + at / 2));
             const uint32_t a1 = at / 2 + 4 < row_bytes ? __ldg(reinterpret_cast<const uint32_t *>(from + at / 2 + 4)) : 0u;
-            w[p] = e < 0 ? a0 << (-4 * (int)e) : __funnelshift_r(a0, a1, 4 * (int)(e & 7));
-            const int64_t first = e < 0 ? 0 : e, last = e + N - 1 < K ? e + N - 1 : K - 1;
-            lo[p] = step_of(first);
-            hi[p] = step_of(last);
+            w[p] = e < 0 ? a0 << (-4 * e) : __funnelshift_r(a0, a1, 4 * (e & 7));
+            lo[p] = step_of(e < 0 ? 0 : e);
+            hi[p] = step_of(e + N - 1 < len ? e + N - 1 : len - 1);
         }
     }
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-        const int64_t e = (((int64_t)chunk * PARTS + p) * 32 + lane) * N - skip;
-        if (e >= K || e + N <= 0) continue;
+        const int e = e0 + 32 * N * p;
+        if (e >= len || e + N <= 0) continue;
         uint32_t h[4];
         e2m1x8_to_f16(w[p], h);
-        const int border = SHIFTED ? kLen - (int)(e & (kLen - 1)) : N;   // elements of the first block
+        const int border = SHIFTED ? kLen - (e & (kLen - 1)) : N;   // elements of the first block
         float f[N];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
@@ -521,13 +552,13 @@ fp4_dequant_kernel(const uint8_t *codes, const uint8_t *scales, const float *ama
             f[2 * i] = lo_f32(q);
             f[2 * i + 1] = hi_f32(q);
         }
-        char *to = out + e * E::kSize;
-        if (e >= 0 && e + N <= K) {
+        char *to = out + (int64_t)e * E::kSize;
+        if (e >= 0 && e + N <= len) {
             *reinterpret_cast<uint4 *>(to) = E::pack(f);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (e + i >= 0 && e + i < K) store_elem<DT>(to, i, f[i]);
+                if (e + i >= 0 && e + i < len) store_elem<DT>(to, i, f[i]);
         }
     }
 }
@@ -623,7 +654,7 @@ cudaError_t launch_amax_type(const void *x, int64_t ldx, int64_t T, int64_t K, f
     cudaError_t e = cudaMemsetAsync(amax, 0, 4, st);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (T * ((K + kGroup - 1) / kGroup) + kThreads - 1) / kThreads;
-    const int64_t most = 8ll * sm_count();
+    const int64_t most = 6ll * sm_count();
     return launch_pdl(amax_kernel<DT>, (int)(ctas < most ? ctas : most), kThreads, 0, st, x, ldx,
                       T, K, to);
 }

@@ -17,25 +17,34 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxCluster = 8;
+constexpr int kThreads = 128, kWarps = kThreads / 32, kMaxCluster = 8;
 
 // A sum of binary32 differences held in two binary32 numbers: the roundings of every
-// difference and addition are added up too (binary64 additions would take longer than the
-// loads).
+// difference and addition are added up too.  (No binary64: of its additions an SM makes a few a
+// clock, and 30 of them a thread, to join the threads' sums, took 86 us for 4000 short pairs.)
 struct Sum {
     float s = 0.0f, c = 0.0f;
-    __device__ __forceinline__ void add(float a, float b) {      // a - b
-        const float d = __fsub_rn(a, b);
-        const float bb = __fsub_rn(a, d);
-        c = __fadd_rn(c, __fadd_rn(__fsub_rn(a, __fadd_rn(d, bb)), __fsub_rn(bb, b)));
+    __device__ __forceinline__ void plus(float d) {
         const float t = __fadd_rn(s, d);
         const float z = __fsub_rn(t, s);
         c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(d, z)));
         s = t;
     }
+    __device__ __forceinline__ void add(float a, float b) {      // a - b
+        const float d = __fsub_rn(a, b);
+        const float bb = __fsub_rn(a, d);
+        c = __fadd_rn(c, __fadd_rn(__fsub_rn(a, __fadd_rn(d, bb)), __fsub_rn(bb, b)));
+        plus(d);
+    }
+    __device__ __forceinline__ void join(const Sum &o) {
+        plus(o.s);
+        c = __fadd_rn(c, o.c);
+    }
     // (c of a sum that is not finite is NaN.)
-    __device__ __forceinline__ double value() const {
-        return fabsf(s) <= 3.402823466e38f ? (double)s + (double)c : (double)s;
+    __device__ __forceinline__ float times(float k) const {
+        const float p = __fmul_rn(k, s);
+        if (!(fabsf(p) <= 3.402823466e38f)) return p;
+        return __fadd_rn(p, __fmaf_rn(k, c, __fmaf_rn(k, s, -p)));
     }
 };
 
@@ -48,15 +57,16 @@ __device__ __forceinline__ void cut(int64_t a, int64_t b, int C, int rank, int64
 }
 
 // f(i) for single elements and g(i) for four from i on, where the address of p + i is a
-// multiple of 16 bytes.
-template <typename F, typename G>
+// multiple of 16 bytes, by THREADS threads.
+template <int THREADS, typename F, typename G>
 __device__ __forceinline__ void each(const float *p, int64_t from, int64_t to, F f, G g) {
+    const int me = threadIdx.x % THREADS;
     const int64_t skip = (16 - (reinterpret_cast<uintptr_t>(p + from) & 15u)) / 4 % 4;
     const int64_t head = from + skip < to ? from + skip : to, n = (to - head) / 4;
-    for (int64_t i = from + threadIdx.x; i < head; i += kThreads) f(i);
+    for (int64_t i = from + me; i < head; i += THREADS) f(i);
 #pragma unroll 4
-    for (int64_t j = threadIdx.x; j < n; j += kThreads) g(head + 4 * j);
-    for (int64_t i = head + 4 * n + threadIdx.x; i < to; i += kThreads) f(i);
+    for (int64_t j = me; j < n; j += THREADS) g(head + 4 * j);
+    for (int64_t i = head + 4 * n + me; i < to; i += THREADS) f(i);
 }
 
 __device__ __forceinline__ float4 load4(const float *p) {
@@ -67,13 +77,19 @@ __device__ __forceinline__ float4 load4_any(const float *p) {
     return make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
 }
 
+// A pair by THREADS threads: a warp, or the CTAs of a cluster.  Bound by the latency of three
+// loads one after another (offsets, tokens, weight) and the join.
+template <int THREADS>
 __global__ void __launch_bounds__(kThreads) preference_kernel(const PreferenceLoss a) {
-    __shared__ double part[kWarps], mine;
+    constexpr bool kOne = THREADS == 32;
+    __shared__ Sum part[kWarps], mine;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait_and_release();
-    for (int64_t p = blockIdx.x / C; p < a.P; p += gridDim.x / C) {
+    const int64_t p0 = kOne ? (int64_t)blockIdx.x * kWarps + warp : blockIdx.x / C;
+    const int64_t step = kOne ? (int64_t)gridDim.x * kWarps : gridDim.x / C;
+    for (int64_t p = p0; p < a.P; p += step) {
         const int64_t o0 = __ldg(a.offsets + 2 * p), o1 = __ldg(a.offsets + 2 * p + 1),
                       o2 = __ldg(a.offsets + 2 * p + 2);
         const bool valid = o0 >= 0 && o0 <= o1 && o1 <= o2 && o2 <= a.T;
@@ -84,44 +100,54 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const PreferenceLo
         }
         const bool together =
             ((reinterpret_cast<uintptr_t>(a.logp) ^ reinterpret_cast<uintptr_t>(a.ref_logp)) & 15u) == 0;
-        double h = 0.0;
+        Sum total;
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            Sum s;
-            each(a.logp, from[side], to[side],
-                 [&](int64_t i) { s.add(__ldg(a.logp + i), a.ref_logp ? __ldg(a.ref_logp + i) : 0.0f); },
+            const float *l = a.logp, *r = a.ref_logp;
+            Sum s[4];                          // four chains: each addition waits for the last
+            each<THREADS>(l, from[side], to[side], [&](int64_t i) { s[0].add(__ldg(l + i), r ? __ldg(r + i) : 0.0f); },
                  [&](int64_t i) {
-                     const float4 l = load4(a.logp + i);
-                     const float4 r = !a.ref_logp ? make_float4(0, 0, 0, 0)
-                                      : together  ? load4(a.ref_logp + i)
-                                                  : load4_any(a.ref_logp + i);
-                     s.add(l.x, r.x);
-                     s.add(l.y, r.y);
-                     s.add(l.z, r.z);
-                     s.add(l.w, r.w);
+                     const float4 x = load4(l + i);
+                     const float4 y = !r ? make_float4(0, 0, 0, 0) : together ? load4(r + i) : load4_any(r + i);
+                     s[0].add(x.x, y.x);
+                     s[1].add(x.y, y.y);
+                     s[2].add(x.z, y.z);
+                     s[3].add(x.w, y.w);
                  });
-            h += side ? -s.value() : s.value();
+            s[0].join(s[1]);
+            s[2].join(s[3]);
+            s[0].join(s[2]);
+            if (side) s[0].s = -s[0].s, s[0].c = -s[0].c;
+            total.join(s[0]);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) h += __shfl_xor_sync(0xFFFFFFFFu, h, o);
-        if (lane == 0) part[warp] = h;
-        __syncthreads();
-        double total = 0.0;
+        for (int o = 16; o > 0; o >>= 1) {
+            Sum other;
+            other.s = __shfl_xor_sync(0xFFFFFFFFu, total.s, o);
+            other.c = __shfl_xor_sync(0xFFFFFFFFu, total.c, o);
+            total.join(other);
+        }
+        if constexpr (!kOne) {
+            if (lane == 0) part[warp] = total;
+            __syncthreads();
+            total = part[0];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) total += part[w];
-        if (C > 1) {
+            for (int w = 1; w < kWarps; ++w) total.join(part[w]);
+        }
+        if (kOne) {
+        } else if (C > 1) {
             if (threadIdx.x == 0) mine = total;
             cluster.sync();
-            total = 0.0;
-            for (int r = 0; r < C; ++r) total += *cluster.map_shared_rank(&mine, r);
+            total = *cluster.map_shared_rank(&mine, 0);
+            for (int r = 1; r < C; ++r) total.join(*cluster.map_shared_rank(&mine, r));
             cluster.sync();                    // all have read before the next pair
         } else {
             __syncthreads();
         }
-        const float hf = valid ? (float)((double)a.beta * total) : NAN;
+        const float hf = valid ? total.times(a.beta) : NAN;
         const float w = a.weights ? __ldg(a.weights + p) : 1.0f;
         const float small = expf(-fabsf(hf)), tail = log1pf(small);
-        if (rank == 0 && threadIdx.x == 0) {
+        if (rank == 0 && threadIdx.x % THREADS == 0) {
             const float down = __fadd_rn(fmaxf(-hf, 0.0f), tail), up = __fadd_rn(fmaxf(hf, 0.0f), tail);
             float loss = __fmul_rn(1.0f - a.smoothing, down);
             if (a.smoothing > 0.0f) loss = __fmaf_rn(a.smoothing, up, loss);   // up may be infinite
@@ -134,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const PreferenceLo
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
             const float v = side ? c : -c;
-            each(a.dlogp, from[side], to[side], [&](int64_t i) { a.dlogp[i] = v; },
+            each<THREADS>(a.dlogp, from[side], to[side], [&](int64_t i) { a.dlogp[i] = v; },
                  [&](int64_t i) {
                      *reinterpret_cast<float4 *>(a.dlogp + i) = make_float4(v, v, v, v);
                  });
@@ -145,13 +171,20 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const PreferenceLo
 }  // namespace
 
 cudaError_t launch_preference_loss(const PreferenceLoss &a, cudaStream_t st) {
-    // a CTA for 2048 tokens of an average pair
+    // A warp for a pair of up to 256 tokens on average (4000 pairs of 73: 8.0 us, 17.8 us with a CTA
+    // each; 8 pairs of 423: 5.7 us, 4.4 us); else a CTA for 2048 of them (512 pairs of 3400: 13.6 us
+    // with two CTAs a pair, 20 us with one, 27 us with eight).
     const int64_t mean = a.T / a.P;
+    if (mean <= 256) {
+        const int64_t ctas = (a.P + kWarps - 1) / kWarps, most = 1 << 24;
+        return launch_pdl_clusters(preference_kernel<32>, (int)(ctas < most ? ctas : most), kThreads,
+                                   1, 0, st, a);
+    }
     int c = 1;
     while (c < kMaxCluster && mean > c * 2048ll) c *= 2;
     const int64_t most = (1 << 24) / c;
-    return launch_pdl_clusters(preference_kernel, (int)(a.P < most ? a.P : most) * c, kThreads, c,
-                               0, st, a);
+    return launch_pdl_clusters(preference_kernel<kThreads>, (int)(a.P < most ? a.P : most) * c,
+                               kThreads, c, 0, st, a);
 }
 
 }  // namespace agoq
