@@ -87,6 +87,9 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
@@ -129,7 +132,7 @@ struct Shape {
     static constexpr int kTiles = BK / fp4_tile_elems(FMT);     // scale tiles of a stage
     static constexpr int kPBytes = BM * kRowBytes, kQBytes = kQRows * kRowBytes;
     static constexpr int kPScales = kTiles * kScaleTile, kQScales = kQTiles * kTiles * kScaleTile;
-    static constexpr int kStages = SPLIT ? (BN > 32 ? 3 : 4) : 5;
+    static constexpr int kStages = !SPLIT ? 5 : BN == 64 ? 3 : 4;    // (SPLIT, BN < 128: two CTAs an SM)
     static constexpr int kScaleWarps = 4, kEpiWarps = SPLIT ? 0 : 8;
     static constexpr int kThreads = 32 * (kScaleWarp0 + kScaleWarps + kEpiWarps);
     static constexpr int kBuffers = !SPLIT && BN <= 128 ? 2 : 1;   // accumulators
@@ -298,6 +301,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         kb1 = min(kb0 + per, kall);
     }
 
+    if (threadIdx.x == 32 * kScaleTmaWarp) {         // (their first use would wait for them)
+        prefetch_map(&map_p);
+        prefetch_map(&map_q);
+        if (!S::SPLIT && a.vectors) prefetch_map(&map_d);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
@@ -335,9 +343,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     // this one has its columns)
     pdl_wait_and_release();
     // The epilogue holds 128 columns of a row.  512 threads were launched with 128 registers each:
-    // 64 + 96 + 2 * 168 a thread of the four warpgroups is below 4 * 128.
+    // 72 + 96 + 2 * 168 a thread of the four warpgroups is below 4 * 128.
     if (warp < kScaleWarp0) {
-    if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kTmaWarp) {
         if (lane == 0) {
             // A pair's codes all count on the barrier of its CTA 0, which issues the MMAs.
@@ -517,6 +525,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             // this CTA's part of the sums, as [column][row], in the stages' place
             float *sums = reinterpret_cast<float *>(smem);
             const bool any = kb0 < kb1;
+            int tile_p, tile_q;
+            tile_at(cid, num_p, num_q, tile_p, tile_q);
             if (any) {
                 ok = ok && warp_wait(&tfull[0], 0u, abort, status, kSleepNs);
                 tc_fence_after();
@@ -524,6 +534,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             if (ok) {
 #pragma unroll
                 for (int c = 0; c < BN; c += 32) {
+                    if (tile_q * BN + c >= a.Q) break;
                     uint32_t w[32];
                     if (any) {
                         __syncwarp();
@@ -582,40 +593,76 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     __syncthreads();
     tc_fence_after();
     if constexpr (S::SPLIT) {
-        cluster_sync_all();                          // all parts are there
-        if (warp >= kScaleWarp0) {
-            float g0 = 1.0f, g1 = 1.0f;
-            if constexpr (FMT == kNv) {
-                const float gp = tensor_scale(__ldg(a.p_amax)), gq = tensor_scale(__ldg(a.q_amax));
-                g0 = fminf(gp, gq);
-                g1 = fmaxf(gp, gq);
-            }
-            int tp, tq;
-            tile_at(cid, num_p, num_q, tp, tq);
-            const int r = (warp - kScaleWarp0) * 32 + lane, row = tp * BM + r;
-            const uint32_t mine = smem_u32(smem);
-            for (int c = rank; c < BN; c += C) {
-                const int col = tq * BN + c;
-                if (col >= a.Q) break;
-                float v = 0.0f;
+        if (C > 1) cluster_sync_all();               // all parts are there
+        float g0 = 1.0f, g1 = 1.0f;
+        if constexpr (FMT == kNv) {
+            const float gp = tensor_scale(__ldg(a.p_amax)), gq = tensor_scale(__ldg(a.q_amax));
+            g0 = fminf(gp, gq);
+            g1 = fmaxf(gp, gq);
+        }
+        int tp, tq;
+        tile_at(cid, num_p, num_q, tp, tq);
+        const uint32_t mine = smem_u32(smem);
+        const int cols = min(BN, a.Q - tq * BN), rows_left = a.P - tp * BM;
+        auto out_of = [&](float v) { return FMT == kNv ? __fmul_rn(__fmul_rn(v, g0), g1) : v; };
+        if (a.swapped) {
+            // a warp a column of the tile (a row of D), four values a lane
+            for (int c = rank + C * warp; c < cols; c += C * (S::kThreads / 32)) {
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
                 for (int k = 0; k < C; ++k) {
-                    float part;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(part)
-                                 : "r"(mapa_shared(mine + (c * BM + r) * 4, k))
+                    float p[4];
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(p[0]), "=f"(p[1]), "=f"(p[2]), "=f"(p[3])
+                                 : "r"(mapa_shared(mine + (c * BM + 4 * lane) * 4, k))
                                  : "memory");
-                    v = __fadd_rn(v, part);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = __fadd_rn(v[i], p[i]);
                 }
-                if constexpr (FMT == kNv) v = __fmul_rn(__fmul_rn(v, g0), g1);
-                if (row < a.P)
-                    store1(a.d, a.swapped ? (int64_t)col * a.ldd + row : (int64_t)row * a.ldd + col,
-                           a.dtype, v);
+                const int64_t at = (int64_t)(tq * BN + c) * a.ldd + tp * BM + 4 * lane;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (4 * lane + i < rows_left) store1(a.d, at + i, a.dtype, out_of(v[i]));
+            }
+        } else {
+            // a thread a row of D, eight values at a time
+            constexpr int kGroups = S::kThreads / BM;
+            const int r = threadIdx.x % BM;
+            for (int c = 8 * (rank + C * (threadIdx.x / BM)); c < cols; c += 8 * C * kGroups) {
+                float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                for (int k = 0; k < C; ++k) {
+                    const uint32_t from = mapa_shared(mine + (c * BM + r) * 4, k);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float p;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(from + i * BM * 4) : "memory");
+                        v[i] = __fadd_rn(v[i], p);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = out_of(v[i]);
+                if (r >= rows_left) continue;
+                const int64_t at = (int64_t)(tp * BM + r) * a.ldd + tq * BN + c;
+                if (a.vectors && c + 8 <= cols) {
+                    if (a.dtype == kF32) {
+                        uint4 *to = reinterpret_cast<uint4 *>(static_cast<float *>(a.d) + at);
+                        to[0] = Elem<kF32>::pack(v);
+                        to[1] = Elem<kF32>::pack(v + 4);
+                    } else {
+                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.d) + at) =
+                            a.dtype == kBF16 ? Elem<kBF16>::pack(v) : Elem<kF16>::pack(v);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i < cols) store1(a.d, at + i, a.dtype, v[i]);
+                }
             }
         }
     }
     // No CTA of a cluster frees tensor memory or exits while another may arrive on its barriers,
     // read or write its shared memory or have a shared MMA run on it.
-    if constexpr (S::PAIR || S::SPLIT) cluster_sync_all();
+    if (S::PAIR || (S::SPLIT && C > 1)) cluster_sync_all();
     if (warp == kMmaWarp) {
         __syncwarp();
         if constexpr (S::PAIR)
@@ -707,13 +754,21 @@ cudaError_t launch_fmt(const Fp4Operand &A, const Fp4Operand &B, int64_t M, int6
     a.vectors = reinterpret_cast<uintptr_t>(d) % 16 == 0 && (ldd * es) % 16 == 0 && ldd < 1ll << 37;
     a.whole = (N * es) % 16 == 0;
     if (small <= 64) {
-        // the CTAs of a tile: as many as the GPU has room for, with two stages each at least
+        // The CTAs of a tile: as many as the GPU has room for (two an SM), with four stages each, or
+        // four CTAs where the stages are few.  1 x 11008 x 4096: 8.7 us with three, 9.2 with two, 13.8
+        // with four (more than fit); 16 x 4096 x 4096: 7.0 us with four, 7.5 with eight, 10.6 with one;
+        // 32 x 1024 x 1024: 5.5 us with four, 6.5 with one.
         const int64_t tiles = fp4_tiles_down(a.P), stages = (K + BK - 1) / BK;
-        int split = 1;
-        while (split < 8 && tiles * split * 2 <= 2 * sm_count() && stages >= split * 4) split *= 2;
+        const int64_t room = 2 * sm_count() / tiles, most = std::max(stages / 4, std::min<int64_t>(stages, 4));
+        const int split = (int)std::max<int64_t>(1, std::min<int64_t>({8, room, most}));
         return small <= 32 ? launch_shape<FMT, Shape<FMT, 32, false, true>>(a, p.codes, q.codes, split, st)
                            : launch_shape<FMT, Shape<FMT, 64, false, true>>(a, p.codes, q.codes, split, st);
     }
+    // few tiles of 128 x 128 over a long K: the same, a CTA an SM
+    const int64_t tiles = fp4_tiles_down(M) * fp4_tiles_down(N), stages = (K + BK - 1) / BK;
+    const int split = (int)std::min<int64_t>({8, sm_count() / tiles, stages / 4});
+    if (split > 1)
+        return launch_shape<FMT, Shape<FMT, 128, false, true>>(a, p.codes, q.codes, split, st);
     // tiles of 256 x 256 by CTA pairs where they fill the GPU
     const int64_t pairs = (M + 255) / 256 * ((N + 255) / 256);
     if (pairs * 2 >= sm_count())
