@@ -208,24 +208,67 @@ __device__ __forceinline__ void load_out(uint32_t from, float g0, float g1, uint
     }
 }
 
-// An epilogue warp's 32 rows x CW columns by TMA: 128-byte wide boxes, swizzled so that the
-// lanes' 16-byte stores meet no bank twice.  `free_acc` is called as soon as the accumulator has
-// been read: the next tile's MMAs have five stages to run through and so make up for a short
-// pause.
+// 32 rows of 128 bytes, 16-byte vectors swizzled (`buf`), to rows of D that lie anywhere: a row
+// at a time, its 16-bit values in aligned pairs.
+template <int DT>
+__device__ __forceinline__ void store_lines(const uint8_t *buf, char *out, int64_t row_step, int rows, int cols,
+                                            int lane) {
+    auto at = [&](int r, int e) {
+        constexpr int kVec = Elem<DT>::kVec;
+        return buf + r * 128 + (((e / kVec) ^ (r & 7)) << 4) + e % kVec * Elem<DT>::kSize;
+    };
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r, out += row_step) {
+        if constexpr (DT == kF32) {
+            if (lane < cols) reinterpret_cast<float *>(out)[lane] = *reinterpret_cast<const float *>(at(r, lane));
+        } else {
+            uint16_t *to = reinterpret_cast<uint16_t *>(out);
+            const int odd = (int)(reinterpret_cast<uintptr_t>(out) >> 1) & 1, e = 2 * lane + odd;
+            if (e < cols) {
+                const uint32_t lo = *reinterpret_cast<const uint16_t *>(at(r, e));
+                if (e + 1 < cols) {
+                    const uint32_t hi = *reinterpret_cast<const uint16_t *>(at(r, e + 1));
+                    *reinterpret_cast<uint32_t *>(to + e) = lo | hi << 16;
+                } else {
+                    to[e] = (uint16_t)lo;
+                }
+            }
+            if (odd && lane == 0) to[0] = *reinterpret_cast<const uint16_t *>(at(r, 0));
+        }
+    }
+}
+
+// An epilogue warp's 32 rows x CW columns, by way of 128-byte wide boxes in shared memory, swizzled
+// so that the lanes' 16-byte stores meet no bank twice: by TMA, or where D's rows do not lie at
+// 16-byte boundaries line by line.  `free_acc` is called as soon as the accumulator has been read:
+// the next tile's MMAs have five stages to run through and so make up for a short pause.
 template <int FMT, int DT, int CW, class F>
-__device__ __forceinline__ void store_boxes(const CUtensorMap *map, uint8_t *buf, uint32_t from, int row,
-                                            int col, const Fp4Args &a, float g0, float g1, int lane,
-                                            F free_acc) {
+__device__ __forceinline__ void store_tile(const CUtensorMap *map, uint8_t *buf, uint32_t from, int row,
+                                           int col, const Fp4Args &a, float g0, float g1, int lane,
+                                           F free_acc) {
     constexpr int kCols = DT == kF32 ? 32 : 64, kBoxes = CW / kCols;
+    // (a box across the end of rows that are no whole 16-byte vectors would write up to the next
+    // vector's end)
+    const bool boxes = a.vectors && (a.whole || col + CW <= a.Q);
     auto put = [&](int c, const uint4 (&o)[8]) {
         if (lane == 0) stores_read();
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             *reinterpret_cast<uint4 *>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) = o[i];
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0 && row < a.P && col + c * kCols < a.Q) tma_store_2d(map, buf, col + c * kCols, row);
+        const int at = col + c * kCols;
+        if (boxes) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && row < a.P && at < a.Q) tma_store_2d(map, buf, at, row);
+        } else {
+            __syncwarp();
+            constexpr int kSize = Elem<DT>::kSize;
+            if (at < a.Q)
+                store_lines<DT>(buf, static_cast<char *>(a.d) + ((int64_t)row * a.ldd + at) * kSize,
+                                a.ldd * kSize, min(32, a.P - row), min(kCols, a.Q - at), lane);
+            __syncwarp();
+        }
     };
     uint4 o[kBoxes][8];
 #pragma unroll
@@ -233,39 +276,6 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap *map, uint8_t *buf
     free_acc();
 #pragma unroll
     for (int c = 0; c < kBoxes; ++c) put(c, o[c]);
-}
-
-// The same where D's rows do not lie at 16-byte boundaries: two rows of 16 values at a time.
-template <int FMT, int CW, class F>
-__device__ __forceinline__ void store_rows(uint8_t *buf, uint32_t from, int row0, int col, const Fp4Args &a,
-                                           float g0, float g1, int lane, F free_acc) {
-    constexpr int kPitch = 17;
-    float *rows = reinterpret_cast<float *>(buf);
-    if (lane == 0) stores_read();                   // boxes of an earlier tile
-    const int n = min(32, a.P - row0);
-#pragma unroll 1
-    for (int c = 0; c < CW; c += 32) {
-        uint32_t w[32];
-        __syncwarp();
-        tmem_ld32(from + c, w);
-        if (c == CW - 32) free_acc();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float v = __uint_as_float(w[16 * h + i]);
-                if constexpr (FMT == kNv) v = __fmul_rn(__fmul_rn(v, g0), g1);
-                rows[lane * kPitch + i] = v;
-            }
-            __syncwarp();
-            const int at = col + c + 16 * h + (lane & 15);
-            if (at < a.Q)
-                for (int r = lane >> 4; r < n; r += 2)
-                    store1(a.d, (int64_t)(row0 + r) * a.ldd + at, a.dtype, rows[r * kPitch + (lane & 15)]);
-        }
-    }
-    __syncwarp();
 }
 
 template <int FMT, class S>
@@ -578,13 +588,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                     else mbar_arrive(&tempty[buf]);
                 }
             };
-            // (a box across the end of rows that are no whole 16-byte vectors would write up to the
-            // next vector's end)
-            const bool boxes = a.vectors && (a.whole || col + CW <= a.Q);
-            if (!boxes) store_rows<FMT, CW>(buf_out, from, row, col, a, g0, g1, lane, free_acc);
-            else if (a.dtype == kF32) store_boxes<FMT, kF32, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
-            else if (a.dtype == kBF16) store_boxes<FMT, kBF16, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
-            else store_boxes<FMT, kF16, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
+            if (a.dtype == kF32) store_tile<FMT, kF32, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
+            else if (a.dtype == kBF16) store_tile<FMT, kBF16, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
+            else store_tile<FMT, kF16, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
