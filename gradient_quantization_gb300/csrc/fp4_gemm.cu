@@ -145,7 +145,7 @@ struct Shape {
     static constexpr int kOffPS = kOffOut + kEpiWarps * kOutBytes;
     static constexpr int kOffQS = kOffPS + kStages * kPScales;
     static constexpr int kOffBar = kOffQS + kStages * kQScales;
-    static constexpr int kBars = 5 * kStages + 2 * kBuffers + 1;
+    static constexpr int kBars = 4 * kStages + 2 * kBuffers + 1;
     static constexpr int kOffMisc = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffMisc + 16 + 1024;
     static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
@@ -155,6 +155,32 @@ struct Shape {
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(!SPLIT || BM * BN * 4 <= kStages * kPBytes, "the sums take the stages' place");
 };
+
+// The wait of a whole warp, all lanes at once.  A phase that is complete, as most are in a loop
+// that runs behind its producers, costs one test (with a lane that waits and tells the others,
+// 250 cycles of a stage's 500).  Returns false as wait_bar does.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait_all(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                              unsigned *status, uint32_t hint_ns) {
+    if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+    return warp_wait(bar, parity, abort, status, hint_ns);
+}
+// One lane of a converged warp; what runs under it keeps its operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
+}
 
 // A place in a ring of NS stages and the parity of its use.
 template <int NS>
@@ -288,8 +314,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *sp = smem, *sq = smem + S::kOffQ, *sps = smem + S::kOffPS, *sqs = smem + S::kOffQS;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kOffBar);
-    uint64_t *full = bars, *empty = bars + NS, *scaled = bars + 2 * NS, *sfull = bars + 3 * NS,
-             *sempty = bars + 4 * NS, *tfull = bars + 5 * NS, *tempty = tfull + S::kBuffers,
+    uint64_t *full = bars, *empty = bars + NS, *sfull = bars + 2 * NS, *sempty = bars + 3 * NS,
+             *tfull = bars + 4 * NS, *tempty = tfull + S::kBuffers,
              *drain = tempty + S::kBuffers;
     uint32_t *tmem_addr = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
@@ -318,9 +344,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + S::kScaleWarps * S::kCluster);   // codes, and scales written
             mbar_init(&empty[s], 1);
-            mbar_init(&scaled[s], S::kScaleWarps * S::kCluster);
             mbar_init(&sfull[s], 1);
             mbar_init(&sempty[s], S::kScaleWarps);
         }
@@ -358,7 +383,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            // A pair's codes all count on the barrier of its CTA 0, which issues the MMAs.
+            // A pair's codes all count on the barrier of its CTA 0, which issues the MMAs; so do the
+            // warps that write scales.
             const uint32_t full0 = S::PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
             uint32_t it = 0;
             bool ok = true;
@@ -428,21 +454,21 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             }
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0 && side == 0) {
+        if (side == 0) {
+            // the whole warp runs the loop, one lane issues
             uint32_t t = 0;
             bool ok = true, issued = false;
             Ring<NS> ring;
             const uint64_t pd0 = sw128_kmajor_desc(smem_u32(sp)), qd0 = sw128_kmajor_desc(smem_u32(sq));
             for (int tile = cid; ok && tile < num_tiles; tile += ncl, ++t) {
                 const int buf = t % S::kBuffers;
-                if (!S::SPLIT && !wait_bar(&tempty[buf], ((t / S::kBuffers) & 1u) ^ 1u, abort, status)) break;
+                if (!S::SPLIT && !warp_wait_all(&tempty[buf], ((t / S::kBuffers) & 1u) ^ 1u, abort, status, 0)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
                 int left = a.K - kb0 * BK;           // elements of K from this stage on
                 for (int kb = kb0; kb < kb1; ++kb, left -= BK, ring.next()) {
                     const int s = ring.s;
-                    if (!wait_bar(&scaled[s], ring.parity, abort, status) ||
-                        !wait_bar(&full[s], ring.parity, abort, status)) {
+                    if (!warp_wait_all(&full[s], ring.parity, abort, status, 0)) {
                         ok = false;
                         break;
                     }
@@ -456,27 +482,37 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                         mma_fp4<FMT, S::PAIR>(d, pd + 2 * kk, qd + 2 * kk, S::kIdesc | (id << 29) | (id << 4),
                                               cols + 4 * j, qcols + 4 * j * S::kQTiles, accumulate);
                     };
-                    step(0, kb > kb0);
-                    if (left > 192) {
-                        step(1, 1);
-                        step(2, 1);
-                        step(3, 1);
-                    } else {
-                        if (left > 64) step(1, 1);
-                        if (left > 128) step(2, 1);
+                    if (elect_one()) {
+                        step(0, kb > kb0);
+                        if (left > 192) {
+                            step(1, 1);
+                            step(2, 1);
+                            step(3, 1);
+                        } else {
+                            if (left > 64) step(1, 1);
+                            if (left > 128) step(2, 1);
+                        }
+                        if constexpr (S::PAIR) umma_commit_pair_multicast(&empty[s], 3);
+                        else commit_one(&empty[s]);
                     }
+                    __syncwarp();
                     issued = true;
-                    if constexpr (S::PAIR) umma_commit_pair_multicast(&empty[s], 3);
-                    else commit_one(&empty[s]);
                 }
                 if (!ok) break;
-                if constexpr (S::PAIR) umma_commit_pair_multicast(&tfull[buf], 3);
-                else if (kb0 < kb1) commit_one(&tfull[buf]);
+                if (elect_one()) {
+                    if constexpr (S::PAIR) umma_commit_pair_multicast(&tfull[buf], 3);
+                    else if (kb0 < kb1) commit_one(&tfull[buf]);
+                }
+                __syncwarp();
             }
+            // (elect_one names the same lane each time: the commits are of the thread that issued)
             if (issued) {
-                if constexpr (S::PAIR) umma_commit_pair(drain);
-                else commit_one(drain);
-                wait_bar(drain, 0u, abort, status, true);
+                if (elect_one()) {
+                    if constexpr (S::PAIR) umma_commit_pair(drain);
+                    else commit_one(drain);
+                    wait_bar(drain, 0u, abort, status, true);
+                }
+                __syncwarp();
             }
         }
     }
@@ -484,13 +520,13 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         // scales: P's tiles, then Q's, four columns each
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t scaled0 = S::PAIR ? mapa_shared(smem_u32(scaled), 0) : 0u;
+        const uint32_t full0 = S::PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
         bool ok = true;
         Ring<NS> ring;
         for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
                 const int s = ring.s;
-                if (!warp_wait(&sfull[s], ring.parity, abort, status, kSleepNs)) {
+                if (!warp_wait_all(&sfull[s], ring.parity, abort, status, kSleepNs)) {
                     ok = false;
                     break;
                 }
@@ -513,7 +549,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sempty[s]);
                 // the MMAs that used these columns are done
-                if (!warp_wait(&empty[s], ring.parity ^ 1u, abort, status, kSleepNs)) {
+                if (!warp_wait_all(&empty[s], ring.parity ^ 1u, abort, status, kSleepNs)) {
                     ok = false;
                     break;
                 }
@@ -526,8 +562,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (S::PAIR && side != 0) mbar_arrive_remote(scaled0 + (uint32_t)s * 8u);
-                    else mbar_arrive(&scaled[s]);
+                    if (S::PAIR && side != 0) mbar_arrive_remote(full0 + (uint32_t)s * 8u);
+                    else mbar_arrive(&full[s]);
                 }
             }
         }
