@@ -215,25 +215,6 @@ __device__ __forceinline__ void store1(void *d, int64_t i, int dtype, float v) {
     else store_elem<kF16>(d, i, v);
 }
 
-// 128 bytes of an output row: from 32 or 64 columns of the accumulator on.
-template <int FMT, int DT>
-__device__ __forceinline__ void load_out(uint32_t from, float g0, float g1, uint4 (&o)[8]) {
-    constexpr int N = DT == kF32 ? 1 : 2;
-#pragma unroll
-    for (int h = 0; h < N; ++h) {
-        uint32_t w[32];
-        tmem_ld32(from + 32 * h, w);
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            v[i] = __uint_as_float(w[i]);
-            if constexpr (FMT == kNv) v[i] = __fmul_rn(__fmul_rn(v[i], g0), g1);
-        }
-#pragma unroll
-        for (int i = 0; i < 8 / N; ++i) o[8 / N * h + i] = Elem<DT>::pack(v + Elem<DT>::kVec * i);
-    }
-}
-
 // 32 rows of 128 bytes, 16-byte vectors swizzled (`buf`), to rows of D that lie anywhere: a row
 // at a time, its 16-bit values in aligned pairs.
 template <int DT>
@@ -296,12 +277,28 @@ __device__ __forceinline__ void store_tile(const CUtensorMap *map, uint8_t *buf,
             __syncwarp();
         }
     };
-    uint4 o[kBoxes][8];
+    // all loads of the accumulator in flight at once
+    uint32_t w[CW / 16][16];
 #pragma unroll
-    for (int c = 0; c < kBoxes; ++c) load_out<FMT, DT>(from + c * kCols, g0, g1, o[c]);
+    for (int c = 0; c < CW / 16; ++c) tmem_ld16_nowait(from + 16 * c, w[c]);
+    tmem_wait_ld();
     free_acc();
 #pragma unroll
-    for (int c = 0; c < kBoxes; ++c) put(c, o[c]);
+    for (int c = 0; c < kBoxes; ++c) {
+        uint4 o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float v[Elem<DT>::kVec];
+#pragma unroll
+            for (int j = 0; j < Elem<DT>::kVec; ++j) {
+                const int at = c * kCols + i * Elem<DT>::kVec + j;
+                v[j] = __uint_as_float(w[at / 16][at % 16]);
+                if constexpr (FMT == kNv) v[j] = __fmul_rn(__fmul_rn(v[j], g0), g1);
+            }
+            o[i] = Elem<DT>::pack(v);
+        }
+        put(c, o);
+    }
 }
 
 template <int FMT, class S>
@@ -378,7 +375,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     // this one has its columns)
     pdl_wait_and_release();
     // The epilogue holds 128 columns of a row.  512 threads were launched with 128 registers each:
-    // 72 + 96 + 2 * 168 a thread of the four warpgroups is below 4 * 128.
+    // 72 + 80 + 2 * 176 a thread of the four warpgroups is below 4 * 128.
     if (warp < kScaleWarp0) {
     if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kTmaWarp) {
@@ -517,7 +514,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         }
     }
     } else if (warp < kScaleWarp0 + S::kScaleWarps) {
-        if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // scales: P's tiles, then Q's, four columns each
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t full0 = S::PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
@@ -593,7 +590,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             }
         }
     } else if constexpr (!S::SPLIT) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         // lane quarter of tensor memory: warp % 4; columns: half of the tile's
         const int q = warp & 3, e = warp - kScaleWarp0 - S::kScaleWarps, half = e >> 2;
         constexpr int CW = BN / 2;
@@ -609,7 +606,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         uint32_t t = 0;
         for (int tile = cid; tile < num_tiles; tile += ncl, ++t) {
             const int buf = t % S::kBuffers;
-            if (!warp_wait(&tfull[buf], (t / S::kBuffers) & 1u, abort, status, kSleepNs)) break;
+            if (!warp_wait_all(&tfull[buf], (t / S::kBuffers) & 1u, abort, status, 500)) break;
             tc_fence_after();
             int tp, tq;
             tile_at(tile, num_p, num_q, tp, tq);
