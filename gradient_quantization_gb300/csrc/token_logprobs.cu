@@ -62,16 +62,22 @@ __device__ __forceinline__ float log_prob(float x, float ref, float sum, float l
 
 // ---- a row's factor of p_i - [i = token] in the gradient, and its losses -------------
 //
-// write(): the row's results, by one thread; factor(): w or c, NaN for a row of NaN.
+// Inputs: the row's scalars, loaded before its logits have arrived; w: the factor; write(): the
+// row's results, by one thread.
 
 __device__ __forceinline__ bool finite_f32(float v) { return fabsf(v) <= 3.402823466e38f; }
 
 struct TokenRow {
+    struct Inputs {
+        float w;
+        __device__ __forceinline__ Inputs(const TokenLogprobs &a, int64_t t)
+            : w(a.weights ? a.weights[t] : 1.0f) {}
+    };
     float w, logp;
     // at: the token's logit; the row's reference, sum and the sum's logarithm
-    __device__ __forceinline__ TokenRow(const TokenLogprobs &a, int64_t t, float at, float ref,
+    __device__ __forceinline__ TokenRow(const TokenLogprobs &, const Inputs &in, float at, float ref,
                                         float sum, float ln) {
-        w = a.weights ? a.weights[t] : 1.0f;
+        w = in.w;
         logp = log_prob(at, ref, sum, ln);
     }
     __device__ __forceinline__ void write(const TokenLogprobs &a, int64_t t, bool ignored,
@@ -82,19 +88,25 @@ struct TokenRow {
 };
 
 struct PolicyRow {
+    struct Inputs {
+        float w, A, old, ref;
+        __device__ __forceinline__ Inputs(const PolicyLoss &a, int64_t t)
+            : w(a.weights ? a.weights[t] : 1.0f), A(a.advantages[t]), old(a.old_logp[t]),
+              ref(a.ref_logp ? a.ref_logp[t] : 0.0f) {}
+    };
     float w, logp, loss, kl;
-    __device__ __forceinline__ PolicyRow(const PolicyLoss &a, int64_t t, float at, float ref,
+    __device__ __forceinline__ PolicyRow(const PolicyLoss &a, const Inputs &in, float at, float ref,
                                          float sum, float ln) {
         logp = log_prob(at, ref, sum, ln);
-        const float weight = a.weights ? a.weights[t] : 1.0f, A = a.advantages[t];
-        const float r = expf(__fsub_rn(logp, a.old_logp[t]));
+        const float weight = in.w, A = in.A;
+        const float r = expf(__fsub_rn(logp, in.old));
         const bool clipped = (A > 0.0f && r > a.high) || (A < 0.0f && r < a.low);
         const float gain = __fmul_rn(clipped ? (A > 0.0f ? a.high : a.low) : r, A);
         float slope = clipped ? 0.0f : gain;
         loss = -gain;
         kl = 0.0f;
         if (a.ref_logp) {
-            const float d = __fsub_rn(a.ref_logp[t], logp), e = expm1f(d);
+            const float d = __fsub_rn(in.ref, logp), e = expm1f(d);
             // e^d - 1 - d, by its series where the terms cancel (next term below 2^-24 of it)
             if (fabsf(d) < 0.5f) {
                 float s = 1.0f / 362880;
@@ -150,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) token_loss_long_kernel(const Args a)
             s = __fadd_rn(s, expf(__fsub_rn(load_now<DT>(row, i), m)));
         s = cta_sum<kWarps>(s, red[1]);
         const bool ignored = token < 0, beyond = token >= a.V, empty = s == 0.0f;
-        const typename RowOf<Args>::Row r(a, t, at, m, s, logf(s));
+        const typename RowOf<Args>::Row r(a, typename RowOf<Args>::Row::Inputs(a, t), at, m, s, logf(s));
         if (threadIdx.x == 0) r.write(a, t, ignored, beyond);
         float w = r.w;
         if (beyond || s != s) w = NAN;                // 0 times a row of NaN is NaN too
@@ -1002,6 +1014,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
     for (int64_t t = blockIdx.x / C; t < a.T; t += gridDim.x / C) {
         const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), (int)a.V, C, rank);
         const int64_t token = a.tokens[t];
+        const typename Row::Inputs inputs(a, t);
         const int steps = (s.to - s.from + THREADS - 1) / THREADS;
         auto part_of = [&](int q) {       // vectors of the q-th of four groups of copies
             return min(s.to, s.from + steps * q / 4 * THREADS);
@@ -1065,7 +1078,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
             cluster_arrive();              // the others' shared memory has been read
         }
         const bool ignored = token < 0, beyond = token >= a.V, empty = all.sum == 0.0f;
-        const Row r(a, t, at, all.ref, all.sum, logf(all.sum));
+        const Row r(a, inputs, at, all.ref, all.sum, logf(all.sum));
         // the CTA that holds the token (the first one for a token outside)
         if (threadIdx.x == 0 && (ignored || beyond ? rank == 0 : s.has(token)))
             r.write(a, t, ignored, beyond);
