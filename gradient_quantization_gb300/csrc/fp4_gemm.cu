@@ -374,6 +374,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     // (after the allocation: a following launch may start and allocate only once every CTA of
     // this one has its columns)
     pdl_wait_and_release();
+    // (long before they are needed.  The smaller tensor scale is multiplied first: no overflow or
+    // underflow on the way.)
+    float g0 = 1.0f, g1 = 1.0f;
+    if (FMT == kNv && (S::SPLIT || warp >= kScaleWarp0)) {
+        const float gp = tensor_scale(__ldg(a.p_amax)), gq = tensor_scale(__ldg(a.q_amax));
+        g0 = fminf(gp, gq);
+        g1 = fmaxf(gp, gq);
+    }
     // The epilogue holds 128 columns of a row.  512 threads were launched with 128 registers each:
     // 72 + 80 + 2 * 176 a thread of the four warpgroups is below 4 * 128.
     if (warp < kScaleWarp0) {
@@ -596,13 +604,6 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         constexpr int CW = BN / 2;
         uint8_t *buf_out = smem + S::kOffOut + e * S::kOutBytes;
         const uint32_t tempty0 = S::PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
-        // the smaller tensor scale first: no overflow or underflow on the way
-        float g0 = 1.0f, g1 = 1.0f;
-        if constexpr (FMT == kNv) {
-            const float gp = tensor_scale(__ldg(a.p_amax)), gq = tensor_scale(__ldg(a.q_amax));
-            g0 = fminf(gp, gq);
-            g1 = fmaxf(gp, gq);
-        }
         uint32_t t = 0;
         for (int tile = cid; tile < num_tiles; tile += ncl, ++t) {
             const int buf = t % S::kBuffers;
@@ -633,12 +634,6 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     tc_fence_after();
     if constexpr (S::SPLIT) {
         if (C > 1) cluster_sync_all();               // all parts are there
-        float g0 = 1.0f, g1 = 1.0f;
-        if constexpr (FMT == kNv) {
-            const float gp = tensor_scale(__ldg(a.p_amax)), gq = tensor_scale(__ldg(a.q_amax));
-            g0 = fminf(gp, gq);
-            g1 = fmaxf(gp, gq);
-        }
         int tp, tq;
         tile_at(cid, num_p, num_q, tp, tq);
         const uint32_t mine = smem_u32(smem);
