@@ -17,6 +17,8 @@
 // logp = -inf, entropy 0 and gradient 0.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "agoq_launch.h"
 #include "typed_io.cuh"
 
@@ -62,27 +64,25 @@ __device__ __forceinline__ float log_prob(float x, float ref, float sum, float l
 
 // ---- a row's factor of p_i - [i = token] in the gradient, and its losses -------------
 //
-// Inputs: the row's scalars, loaded before its logits have arrived; w: the factor; write(): the
-// row's results, by one thread.
+// Inputs: the row's scalars; w: the factor; write(): the row's results, by one thread.
 
 __device__ __forceinline__ bool finite_f32(float v) { return fabsf(v) <= 3.402823466e38f; }
 
 struct TokenRow {
     struct Inputs {
         float w;
-        __device__ __forceinline__ Inputs(const TokenLogprobs &a, int64_t t)
-            : w(a.weights ? a.weights[t] : 1.0f) {}
+        __device__ __forceinline__ void load(const TokenLogprobs &a, int64_t t) {
+            w = a.weights ? a.weights[t] : 1.0f;
+        }
     };
-    float w, logp;
-    // at: the token's logit; the row's reference, sum and the sum's logarithm
-    __device__ __forceinline__ TokenRow(const TokenLogprobs &, const Inputs &in, float at, float ref,
-                                        float sum, float ln) {
-        w = in.w;
-        logp = log_prob(at, ref, sum, ln);
-    }
-    __device__ __forceinline__ void write(const TokenLogprobs &a, int64_t t, bool ignored,
-                                          bool beyond) const {
-        if (a.logp) a.logp[t] = ignored ? 0.0f : beyond ? NAN : logp;
+    float w;
+    __device__ __forceinline__ TokenRow(const TokenLogprobs &, const Inputs &in, float, float, float)
+        : w(in.w) {}
+    __device__ __forceinline__ void write(const TokenLogprobs &a, int64_t t, bool ignored, bool beyond,
+                                          float at, float ref, float sum) const {
+        if (!a.logp) return;
+        const float lp = log_prob(at, ref, sum, logf(sum));
+        a.logp[t] = ignored ? 0.0f : beyond ? NAN : lp;
     }
     static constexpr bool kNeedsToken = false;      // by every thread, for the factor
 };
@@ -90,14 +90,18 @@ struct TokenRow {
 struct PolicyRow {
     struct Inputs {
         float w, A, old, ref;
-        __device__ __forceinline__ Inputs(const PolicyLoss &a, int64_t t)
-            : w(a.weights ? a.weights[t] : 1.0f), A(a.advantages[t]), old(a.old_logp[t]),
-              ref(a.ref_logp ? a.ref_logp[t] : 0.0f) {}
+        __device__ __forceinline__ void load(const PolicyLoss &a, int64_t t) {
+            w = a.weights ? a.weights[t] : 1.0f;
+            A = a.advantages[t];
+            old = a.old_logp[t];
+            ref = a.ref_logp ? a.ref_logp[t] : 0.0f;
+        }
     };
     float w, logp, loss, kl;
+    // at: the token's logit; the row's reference and sum
     __device__ __forceinline__ PolicyRow(const PolicyLoss &a, const Inputs &in, float at, float ref,
-                                         float sum, float ln) {
-        logp = log_prob(at, ref, sum, ln);
+                                         float sum) {
+        logp = log_prob(at, ref, sum, logf(sum));
         const float weight = in.w, A = in.A;
         const float r = expf(__fsub_rn(logp, in.old));
         const bool clipped = (A > 0.0f && r > a.high) || (A < 0.0f && r < a.low);
@@ -131,8 +135,8 @@ struct PolicyRow {
         w = __fmul_rn(weight, slope);
         if (!finite_f32(w)) w = NAN;
     }
-    __device__ __forceinline__ void write(const PolicyLoss &a, int64_t t, bool ignored,
-                                          bool beyond) const {
+    __device__ __forceinline__ void write(const PolicyLoss &a, int64_t t, bool ignored, bool beyond,
+                                          float, float, float) const {
         if (a.logp) a.logp[t] = ignored ? 0.0f : beyond ? NAN : logp;
         if (a.loss) a.loss[t] = ignored ? 0.0f : beyond ? NAN : loss;
         if (a.kl) a.kl[t] = ignored ? 0.0f : beyond ? NAN : kl;
@@ -162,8 +166,10 @@ __global__ void __launch_bounds__(kThreads) token_loss_long_kernel(const Args a)
             s = __fadd_rn(s, expf(__fsub_rn(load_now<DT>(row, i), m)));
         s = cta_sum<kWarps>(s, red[1]);
         const bool ignored = token < 0, beyond = token >= a.V, empty = s == 0.0f;
-        const typename RowOf<Args>::Row r(a, typename RowOf<Args>::Row::Inputs(a, t), at, m, s, logf(s));
-        if (threadIdx.x == 0) r.write(a, t, ignored, beyond);
+        typename RowOf<Args>::Row::Inputs inputs;
+        inputs.load(a, t);
+        const typename RowOf<Args>::Row r(a, inputs, at, m, s);
+        if (threadIdx.x == 0) r.write(a, t, ignored, beyond, at, m, s);
         float w = r.w;
         if (beyond || s != s) w = NAN;                // 0 times a row of NaN is NaN too
         if (ignored || (empty && !beyond)) w = 0.0f;
@@ -977,7 +983,10 @@ struct RowShared {
     Sums warps[kRowWarps];
     Sums slice, row;
     float token;                  // the token's logit, in the CTA that holds it
-    int holds;                    // whether this one does
+};
+// Where every CTA of the row needs that logit.
+struct RowSharedToken : RowShared {
+    int holds;                    // whether this CTA has it
     float row_token;
 };
 
@@ -1003,8 +1012,9 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
     using Row = typename RowOf<Args>::Row;
     using Word = typename E::Word;
     constexpr int N = E::kVec;
-    extern __shared__ __align__(16) uint4 data[];
-    __shared__ RowShared sh;
+    // (lines of 128 bytes: from another place on, rows of 131072 BF16 values took 4% longer)
+    extern __shared__ __align__(128) uint4 data[];
+    __shared__ typename std::conditional<Row::kNeedsToken, RowSharedToken, RowShared>::type sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     constexpr int kWarpsHere = THREADS / 32;
@@ -1014,7 +1024,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
     for (int64_t t = blockIdx.x / C; t < a.T; t += gridDim.x / C) {
         const Slice<DT> s(elem_at<DT>(a.logits, t * a.ld), (int)a.V, C, rank);
         const int64_t token = a.tokens[t];
-        const typename Row::Inputs inputs(a, t);
+        typename Row::Inputs inputs;           // long before they are needed
+        inputs.load(a, t);
         const int steps = (s.to - s.from + THREADS - 1) / THREADS;
         auto part_of = [&](int q) {       // vectors of the q-th of four groups of copies
             return min(s.to, s.from + steps * q / 4 * THREADS);
@@ -1054,7 +1065,12 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
         if (lane == 0) sh.warps[warp] = mine;
         __syncthreads();
         Sums all = warp_join(lane < kWarpsHere ? sh.warps[lane] : Sums{kLowest, 0.0f, 0.0f});
-        float at = s.has(token) ? E::up(words[token - s.start]) : 0.0f;
+        float at = 0.0f;
+        if constexpr (Row::kNeedsToken) {
+            if (s.has(token)) at = E::up(words[token - s.start]);
+        } else {
+            if (threadIdx.x == 0 && s.has(token)) sh.token = E::up(words[token - s.start]);
+        }
         if (C > 1) {
             if (threadIdx.x == 0) {
                 sh.slice = all;
@@ -1065,11 +1081,15 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
             }
             cluster.sync();
             if (warp == 0) {
-                const RowShared *from = cluster.map_shared_rank(&sh, lane < C ? lane : 0);
-                all = warp_join(lane < C ? from->slice : Sums{kLowest, 0.0f, 0.0f});
+                if constexpr (Row::kNeedsToken) {
+                    if (lane < C) {
+                        const RowSharedToken *from = cluster.map_shared_rank(&sh, lane);
+                        if (from->holds) sh.row_token = from->token;
+                    }
+                }
+                all = warp_join(lane < C ? cluster.map_shared_rank(&sh, lane)->slice
+                                         : Sums{kLowest, 0.0f, 0.0f});
                 if (lane == 0) sh.row = all;
-                if constexpr (Row::kNeedsToken)
-                    if (lane < C && from->holds) sh.row_token = from->token;
             }
             __syncthreads();
             all = sh.row;
@@ -1078,10 +1098,10 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) token_loss_kernel(cons
             cluster_arrive();              // the others' shared memory has been read
         }
         const bool ignored = token < 0, beyond = token >= a.V, empty = all.sum == 0.0f;
-        const Row r(a, inputs, at, all.ref, all.sum, logf(all.sum));
+        const Row r(a, inputs, at, all.ref, all.sum);
         // the CTA that holds the token (the first one for a token outside)
         if (threadIdx.x == 0 && (ignored || beyond ? rank == 0 : s.has(token)))
-            r.write(a, t, ignored, beyond);
+            r.write(a, t, ignored, beyond, sh.token, all.ref, all.sum);
         float w = r.w;
         if (beyond || all.sum != all.sum) w = NAN;    // 0 times a row of NaN is NaN too
         if (ignored || (empty && !beyond)) w = 0.0f;
