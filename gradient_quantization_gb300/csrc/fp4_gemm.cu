@@ -798,14 +798,21 @@ cudaError_t launch_fmt(const Fp4Operand &A, const Fp4Operand &B, int64_t M, int6
         return small <= 32 ? launch_shape<FMT, Shape<FMT, 32, false, true>>(a, p.codes, q.codes, split, st)
                            : launch_shape<FMT, Shape<FMT, 64, false, true>>(a, p.codes, q.codes, split, st);
     }
-    // few tiles of 128 x 128 over a long K: the same, a CTA an SM
     const int64_t tiles = fp4_tiles_down(M) * fp4_tiles_down(N), stages = (K + BK - 1) / BK;
-    const int split = (int)std::min<int64_t>({8, sm_count() / tiles, stages / 4});
-    if (split > 1)
+    // Few tiles of 128 x 128 over a long K: shared as above, a CTA an SM.  300 x 200 x 9000: 10 us,
+    // 15 us without; but 512 x 512 x 4096, with four CTAs of four stages each: 8.8 us, 8.2 without.
+    const int split = (int)std::min<int64_t>({8, sm_count() / tiles, stages / 8});
+    if (split > 2)
         return launch_shape<FMT, Shape<FMT, 128, false, true>>(a, p.codes, q.codes, split, st);
-    // tiles of 256 x 256 by CTA pairs where they fill the GPU
-    const int64_t pairs = (M + 255) / 256 * ((N + 255) / 256);
-    if (pairs * 2 >= sm_count())
+    // Tiles of 256 x 256 by CTA pairs, or of 128 x 128 by single CTAs, by what their rounds take (in
+    // tenths of a microsecond, from measurements at both sides: 256 x 11008 x 4096 11.6 us by pairs,
+    // 14.0 by single CTAs; 300 x 11008 x 4096 16.8 and 14.1; 2048 x 4096 x 4096 18.1 and 23.9;
+    // 2500 x 2504 x 500 to FP32 10.4 and 8.2).  A pair's round is 2.7 a stage and 23 for the
+    // accumulator, which has no second one beside it; a single CTA's 3.4 a stage.
+    const int64_t pair_tiles = (M + 255) / 256 * ((N + 255) / 256), pairs = sm_count() / 2;
+    const int64_t pair_time = 49 + (pair_tiles + pairs - 1) / pairs * (27 * stages / 10 + 23);
+    const int64_t single_time = 33 + (tiles + sm_count() - 1) / sm_count() * std::max<int64_t>(34 * stages / 10, 15);
+    if (pair_time < single_time)
         return launch_shape<FMT, Shape<FMT, 256, true, false>>(a, p.codes, q.codes, 1, st);
     return launch_shape<FMT, Shape<FMT, 128, false, false>>(a, p.codes, q.codes, 1, st);
 }

@@ -40,12 +40,15 @@ def test_columns_of_many_rows():
     assert not codes[:-256].any()
 
 
-def test_a_large_product():
-    """65600 x 33000, by CTA pairs: exact sums, the last rows against a product of those rows."""
-    M, N, K = 65600, 33000, 64
+@pytest.mark.parametrize("K", [64, 3000])
+def test_a_large_product(K):
+    """65600 x 33000: exact sums, the last rows against a product of those rows; by single CTAs and
+    by CTA pairs."""
+    M, N = 65600, 33000
     g = torch.Generator(device="cuda").manual_seed(3)
     a, b = (torch.randint(0, 16, (n, K), generator=g, device="cuda").to(torch.uint8) for n in (M, N))
-    sa, sb = (F.tile(torch.randint(127, 129, (n, 2), generator=g, device="cuda").to(torch.uint8)) for n in (M, N))
+    a, b = (torch.nn.functional.pad(v, (0, -K % 32)) for v in (a, b))
+    sa, sb = (F.tile(torch.randint(127, 129, (n, a.shape[1] // 32), generator=g, device="cuda").to(torch.uint8)) for n in (M, N))
     d = agoq.agoq_fp4_gemm(F.pack(a), sa, F.pack(b), sb, M, N, K, agoq.MXFP4)
     agoq.agoq_device_status()
     assert d.numel() > 2 ** 31

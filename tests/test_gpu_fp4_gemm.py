@@ -59,7 +59,8 @@ def _check(a, b, d):
 SIZES = [(1, 1, 1), (1, 128, 64), (1, 300, 1000), (2, 129, 65), (17, 1000, 333), (32, 128, 4096),
          (33, 257, 777), (64, 64, 64), (64, 1000, 2000), (65, 65, 65), (65, 64, 300), (1000, 1, 500),
          (300, 31, 129), (5000, 64, 200), (128, 128, 256), (129, 127, 257), (200, 300, 512),
-         (517, 1003, 1999), (100, 2500, 100), (1, 5000, 33), (3, 200, 20000), (200, 40, 9000)]
+         (517, 1003, 1999), (100, 2500, 100), (1, 5000, 33), (3, 200, 20000), (200, 40, 9000), (300, 200, 9000),
+         (513, 130, 6200)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -71,11 +72,15 @@ def test_sizes(fmt, M, N, K):
     agoq.agoq_device_status()
 
 
+# Sizes of the CTA pairs (a long K, a round or two of 256 x 256 tiles), whole and ragged.
+PAIRS = [(1024, 4096, 4096), (1001, 4090, 3999), (2561, 2177, 4000), (130, 9001, 4100)]
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,N,K", [(2560, 2048, 64), (2561, 2177, 300), (2304, 4097, 1000),
-                                   (5000, 3000, 513)])
+                                   (5000, 3000, 513)] + PAIRS)
 def test_large(fmt, M, N, K):
-    """Sizes of the CTA pairs: several tiles a pair, odd edges."""
+    """Several tiles a CTA, odd edges."""
     a, b = _operand(M, K, fmt, 3), _operand(N, K, fmt, 4)
     for dtype in TYPES:
         _check(a, b, _gemm(a, b, fmt, dtype=dtype))
@@ -103,7 +108,8 @@ def _exact_operand(rows, K, fmt, seed):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,N,K", [(5, 400, 3001), (40, 300, 700), (300, 200, 1000), (2600, 2100, 500),
-                                   (1, 1000, 4096), (3000, 20, 100)])
+                                   (1, 1000, 4096), (3000, 20, 100), (300, 200, 4000),
+                                   (300, 200, 6500), (1001, 4090, 3999), (1024, 4096, 4096)])
 def test_exact_sums(fmt, M, N, K):
     """Bit for bit: every element of K once, with its own scale, in the right place."""
     a, b = _exact_operand(M, K, fmt, 5), _exact_operand(N, K, fmt, 6)
@@ -131,10 +137,11 @@ def test_one_hot_rows_give_columns(fmt, M, N):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,N", [(5, 200), (70, 333), (333, 40), (2600, 2117)])
-def test_rows_of_d(dtype, M, N):
+@pytest.mark.parametrize("M,N,K", [(5, 200, 200), (70, 333, 200), (333, 40, 200), (2600, 2117, 200),
+                                   (1001, 4090, 3999)])
+def test_rows_of_d(dtype, M, N, K):
     """Distances and alignments of d's rows; nothing between them is written."""
-    a, b = _operand(M, 200, agoq.NVFP4, 8), _operand(N, 200, agoq.NVFP4, 9)
+    a, b = _operand(M, K, agoq.NVFP4, 8), _operand(N, K, agoq.NVFP4, 9)
     want = _gemm(a, b, agoq.NVFP4, dtype=dtype)
     for pad, shift in ((0, 1), (3, 0), (-N % 8 + 8, 0), (-N % 8, 8), (5, 3)):
         buf = torch.full((M * (N + pad) + shift + 8,), 7.0, dtype=dtype, device="cuda")
@@ -145,19 +152,18 @@ def test_rows_of_d(dtype, M, N):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("M,N", [(2, 130), (130, 100), (2600, 2100)])
-def test_nothing_outside_d(fmt, M, N):
-    a, b = _operand(M, 100, fmt, 10), _operand(N, 100, fmt, 11)
+@pytest.mark.parametrize("M,N,K", [(2, 130, 100), (130, 100, 100), (2600, 2100, 100), (1001, 4090, 3999)])
+def test_nothing_outside_d(fmt, M, N, K):
+    a, b = _operand(M, K, fmt, 10), _operand(N, K, fmt, 11)
     d = Guarded(2 * M * N, BF16)
     _gemm(a, b, fmt, d=d.view.view(M, N))
     assert d.intact()
     _check(a, b, d.view.view(M, N))
 
 
-@pytest.mark.parametrize("M,N", [(4, 300), (300, 200), (2600, 2100)])
-def test_scales_far_apart(M, N):
+@pytest.mark.parametrize("M,N,K", [(4, 300, 320), (300, 200, 320), (2600, 2100, 320), (1001, 4090, 3999)])
+def test_scales_far_apart(M, N, K):
     """MXFP4 rows from 2^-40 to 2^40."""
-    K = 320
     g = torch.Generator(device="cuda").manual_seed(12)
     spread = lambda n: torch.exp2(torch.randint(-40, 41, (n, 1), generator=g, device="cuda").float())
     a = Operand(torch.randn(M, K, generator=g, device="cuda") * spread(M), agoq.MXFP4)
@@ -175,9 +181,9 @@ def test_tensor_scales_far_apart():
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("M,N", [(5, 300), (300, 200), (2600, 2100)])
-def test_nan_stays_in_its_row(fmt, M, N):
-    K = 500
+@pytest.mark.parametrize("M,N,K", [(5, 300, 500), (300, 200, 500), (300, 200, 6500), (2600, 2100, 500),
+                                   (1001, 4090, 3999)])
+def test_nan_stays_in_its_row(fmt, M, N, K):
     g = torch.Generator(device="cuda").manual_seed(15)
     x, w = torch.randn(M, K, generator=g, device="cuda"), torch.randn(N, K, generator=g, device="cuda")
     x[M // 2, 300], w[N - 1, 5] = math.nan, math.inf
@@ -198,7 +204,7 @@ def test_zeros_and_nothing():
 
 
 def test_the_same_bits_again():
-    for M, N, K in ((3, 500, 5000), (300, 300, 700), (2600, 2100, 300)):
+    for M, N, K in ((3, 500, 5000), (300, 300, 700), (2600, 2100, 300), (1001, 4090, 3999), (300, 200, 7000)):
         a, b = _operand(M, K, agoq.NVFP4, 17), _operand(N, K, agoq.NVFP4, 18)
         first = _gemm(a, b, agoq.NVFP4, dtype=F32)
         for _ in range(5):
@@ -206,9 +212,10 @@ def test_the_same_bits_again():
 
 
 def test_streams_at_the_same_time():
-    """Calls of every variant in four streams at once."""
-    ops = [(_operand(M, 900, agoq.NVFP4, 19), _operand(N, 900, agoq.NVFP4, 20))
-           for M, N in ((2, 700), (50, 700), (300, 500), (2600, 2100))]
+    """Calls of every variant in six streams at once."""
+    ops = [(_operand(M, K, agoq.NVFP4, 19), _operand(N, K, agoq.NVFP4, 20))
+           for M, N, K in ((2, 700, 900), (50, 700, 900), (300, 500, 900), (2600, 2100, 900), (300, 200, 4000),
+                           (1001, 4090, 3999))]
     want = [_gemm(a, b, agoq.NVFP4) for a, b in ops]
     streams = [torch.cuda.Stream() for _ in ops]
     torch.cuda.synchronize()
