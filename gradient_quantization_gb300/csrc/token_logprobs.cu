@@ -101,16 +101,21 @@ struct PolicyRow {
     // at: the token's logit; the row's reference and sum
     __device__ __forceinline__ PolicyRow(const PolicyLoss &a, const Inputs &in, float at, float ref,
                                          float sum) {
-        logp = log_prob(at, ref, sum, logf(sum));
+        const float ln = logf(sum), t = __fsub_rn(at, ref);
+        logp = log_prob(at, ref, sum, ln);
         const float weight = in.w, A = in.A;
-        const float r = expf(__fsub_rn(logp, in.old));
+        const float r = expf(__fsub_rn(logp, in.old));   // 1 where old is this call's own logp
         const bool clipped = (A > 0.0f && r > a.high) || (A < 0.0f && r < a.low);
         const float gain = __fmul_rn(clipped ? (A > 0.0f ? a.high : a.low) : r, A);
         float slope = clipped ? 0.0f : gain;
         loss = -gain;
         kl = 0.0f;
         if (a.ref_logp) {
-            const float d = __fsub_rn(in.ref, logp), e = expm1f(d);
+            // without the rounding of logp, which is larger than e^d - 1 - d may be (a token of
+            // probability 0 has no such parts)
+            const float d = logp == -INFINITY ? __fsub_rn(in.ref, logp)
+                                              : __fadd_rn(__fsub_rn(in.ref, t), ln);
+            const float e = expm1f(d);
             // e^d - 1 - d, by its series where the terms cancel (next term below 2^-24 of it)
             if (fabsf(d) < 0.5f) {
                 float s = 1.0f / 362880;

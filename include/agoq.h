@@ -581,7 +581,8 @@ agoq_status agoq_token_loss(const void *logits, int64_t ld, int dtype, const int
  * gradient, reading the logits once where a row fits on chip.  With logp as
  * agoq_token_logprobs, per row, in binary32:
  *   r = e^(logp - old_logp);  lo = 1 - clip_low, hi = 1 + clip_high;
- *   d = ref_logp - logp;      kl = e^d - d - 1     (an estimate of the divergence, >= 0)
+ *   d = ref_logp - logp (before logp is rounded);  kl = e^d - d - 1 (an estimate of the
+ *       divergence, >= 0)
  *   loss = weights (-min(r A, min(max(r, lo), hi) A) + kl_coef kl),   A = advantages[t];
  *   c = weights (r A + kl_coef (e^d - 1)), without r A where the ratio is clipped (A > 0 and
  *       r > hi, or A < 0 and r < lo; at a bound itself it is not);
