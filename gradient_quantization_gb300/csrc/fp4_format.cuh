@@ -155,8 +155,10 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
 // Value of a scale byte (NaN among them).
 template <int FMT>
 __device__ __forceinline__ float scale_value(uint32_t byte) {
+    // (0: 2^-127, a subnormal; 255: NaN.  Without a comparison: 8192 x 11008 back to BF16 35 us, 46
+    // us with.)
     if constexpr (FMT == kMx)
-        return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
+        return __uint_as_float(max(byte << 23, 0x00400000u) | (byte + 1) >> 8 << 22);
     float lo, hi;
     e4m3x2_to_f32(byte, lo, hi);
     return lo;

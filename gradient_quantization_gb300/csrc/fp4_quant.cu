@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kSmallThreads) amax_small_kernel(const void *x
 // time, so that a warp writes whole lines whatever the rows' alignment; of rows that do not begin
 // at such a boundary (SHIFTED) a vector's codes begin anywhere and may belong to two blocks.
 template <int DT, int FMT, bool SHIFTED, int PARTS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
 fp4_dequant_kernel(const uint8_t *codes, const uint8_t *scales, const float *amax, int64_t T,
                    int64_t K, void *y, int64_t ldy, uint32_t chunks) {
     using E = Elem<DT>;
