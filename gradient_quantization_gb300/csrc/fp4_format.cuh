@@ -86,11 +86,11 @@ __device__ __forceinline__ Scaling scaling_of(const float *amax, float *table) {
 
 // Scale byte of a block and the factor of its elements, from its largest magnitude.  A block
 // with a NaN or an infinity (or, NVFP4, of a tensor with one) has the NaN of its scale's type
-// and codes of 0, by the caller.
+// and codes of 0: the caller masks them with `keep`.
 struct BlockScale {
     uint32_t byte;
     float inverse;
-    bool finite;
+    uint32_t keep;
 };
 template <int FMT>
 __device__ __forceinline__ BlockScale block_scale(float top, const Scaling &t) {
@@ -98,12 +98,12 @@ __device__ __forceinline__ BlockScale block_scale(float top, const Scaling &t) {
     if constexpr (FMT == kMx) {
         // 2^(floor(log2 top) - 2), not below 2^-127: the exponent field less 2
         const int field = (int)(__float_as_uint(top) >> 23) - 2;
-        s.finite = finite_bits(top);
-        const uint32_t byte = field > 0 ? field : 0;
-        s.byte = s.finite ? byte : 255u;
+        s.keep = finite_bits(top) ? 0xFFFFFFFFu : 0u;
+        const uint32_t byte = max(field, 0);
+        s.byte = (byte | ~s.keep) & 0xFFu;
         s.inverse = __uint_as_float((254u - byte) << 23);
     } else {
-        s.finite = t.ok && finite_bits(top);
+        s.keep = t.ok && finite_bits(top) ? 0xFFFFFFFFu : 0u;
         // top times fl(1 / 6 g) is within 3 * 2^-24 of fl(top / 6 g) (relative; results below
         // binary32's normal range are far below E4M3's): where both sides of it round to one
         // code, that is the quotient's; else, about once in 2^15 blocks, it is divided
@@ -112,7 +112,7 @@ __device__ __forceinline__ BlockScale block_scale(float top, const Scaling &t) {
         uint32_t byte = both & 0xFFu;
         if (byte != both >> 8) byte = e4m3x2_from_f32(__fdiv_rn(top, t.six_g), 0.0f);
         s.inverse = t.table[byte & 127u];
-        s.byte = s.finite ? byte : 127u;
+        s.byte = (byte | ~s.keep) & 127u;
     }
     return s;
 }

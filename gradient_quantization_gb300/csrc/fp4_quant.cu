@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 6) fp4_rows_kernel(const Fp4Quant a,
         if constexpr (FMT == kMx) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         const BlockScale s = block_scale<FMT>(top, scaling);
         uint2 c = x[p].codes(s.inverse);
-        if (!s.finite) c = make_uint2(0, 0);
+        c.x &= s.keep;
+        c.y &= s.keep;
         if (live && e / 2 < row_bytes) *reinterpret_cast<uint2 *>(codes + e / 2) = c;
         // (no block begins behind the row's end)
         const bool block = live && (FMT == kMx ? e & ~(2 * kGroup - 1) : e) < len;
@@ -274,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a
             if constexpr (FMT == kMx) top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             const BlockScale s = block_scale<FMT>(top, scaling);
             uint2 c = x.codes(s.inverse);
-            if (!s.finite) c = make_uint2(0, 0);
+            c.x &= s.keep;
+            c.y &= s.keep;
             const int64_t at = k0 / 2 + g * 8;
             if (t0 + r < a.T && at < row_bytes)
                 *reinterpret_cast<uint2 *>(a.codes + (t0 + r) * row_bytes + at) = c;
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a
                         const int at = 16 * h + 8 * q + 2 * i;
                         p[i] = f32x2(element(at), element(at + 1));
                     }
-                    w[q] = s.finite ? e2m1x8(p, s.inverse) : 0u;
+                    w[q] = e2m1x8(p, s.inverse) & s.keep;
                 }
                 *reinterpret_cast<uint2 *>(out + col * S::kCodePitch + b * (kBlockLen / 2) + 8 * h) =
                     make_uint2(w[0], w[1]);
