@@ -137,11 +137,14 @@ __device__ __forceinline__ int octet_row(int octet, int warp) {       // within 
 //
 // A warp takes PARTS runs of 512 elements of a row, a lane 16 of each.  Rows are padded to whole
 // scale words (64 or 128 elements) and to whole tiles of 128, so that every scale byte is
-// written (0 where there is no block).
+// written (0 where there is no block).  Bound by HBM for MXFP4 and FP32: 8192 x 11008 BF16 to MXFP4
+// 33.7 us (6.8 TB/s), 8192 x 8192 FP32 to NVFP4 44.3 us (6.9 TB/s).  BF16 to NVFP4 39.3 us (5.9 TB/s)
+// by instruction issue, with a scale every 16 elements.  Eight CTAs an SM (32 registers): with six
+// 41 us, with four 45; a lane with one run instead of two (BF16) 51 us.
 constexpr int kRun = 32 * kGroup;
 
 template <int DT, int FMT, int PARTS>
-__global__ void __launch_bounds__(kThreads, 6) fp4_rows_kernel(const Fp4Quant a, uint32_t chunks) {
+__global__ void __launch_bounds__(kThreads, 8) fp4_rows_kernel(const Fp4Quant a, uint32_t chunks) {
     constexpr int kWord = fp4_tile_elems(FMT) / kGroup;        // lanes of a scale word
     constexpr int kWords = 32 / kWord;                         // of a run
     __shared__ uint32_t words[PARTS * kWords][kOctet];
@@ -190,9 +193,14 @@ __global__ void __launch_bounds__(kThreads, 6) fp4_rows_kernel(const Fp4Quant a,
 
 // ---- columns, and both -------------------------------------------------------------
 //
-// A CTA copies a tile of 128 columns by 128 rows (FP32: 64) to shared memory; eight threads take
-// a row (ROWS), and a thread then takes a block of two neighbouring columns.  The tile's codes of the columns and its scale tiles are gathered in
-// shared memory and leave in whole rows.
+// A CTA copies a tile of 128 columns by 128 rows (FP32: 64) to shared memory; eight threads take a
+// row (ROWS), and a thread then takes a block of two neighbouring columns.  The tile's codes of
+// the columns and its scale tiles are gathered in shared memory and leave in whole rows.
+// 8192 x 11008 BF16: columns 38 us (MXFP4, 6.0 TB/s) and 42 us (NVFP4), both ways 52 us and 60 us (5.3
+// and 4.7 TB/s), bound by instruction issue (63% of the slots, the integer pipe 60% busy);
+// 8192 x 8192 FP32 to NVFP4 52 us and 60 us (5.8 and 5.7 TB/s).  Five CTAs an SM for MXFP4 (columns
+// 41 us with four), four for NVFP4 (columns 47 us with five).  FP32 tiles of 128 rows left room for
+// two CTAs: both ways 93 us.
 constexpr int kTile = 128;
 template <int DT>
 struct TileShape {
@@ -201,7 +209,7 @@ struct TileShape {
 };
 
 template <int DT, int FMT, bool ROWS>
-__global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a, int64_t tiles_k) {
+__global__ void __launch_bounds__(kThreads, FMT == kMx ? 5 : 4) fp4_tiles_kernel(const Fp4Quant a, int64_t tiles_k) {
     using E = Elem<DT>;
     using S = TileShape<DT>;
     constexpr int kPitch = kTile * E::kSize, kRows = S::kRows, kSteps = kRows / 32;
@@ -387,7 +395,8 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_tiles_kernel(const Fp4Quant a
 
 // ---- the largest magnitude -----------------------------------------------------------
 
-// Magnitudes as binary32 bits are in the order of their values, NaN last.
+// Magnitudes as binary32 bits are in the order of their values, NaN last.  Bound by HBM: 8192 x 11008
+// BF16 29.7 us (6.1 TB/s); 16 x 4096 by one cluster 2.1 us.
 template <int DT>
 __device__ __forceinline__ uint32_t absmax_of(const void *x, int64_t ldx, int64_t T, int64_t K,
                                               int64_t first, int64_t step) {
@@ -490,7 +499,9 @@ __global__ void __launch_bounds__(kSmallThreads) amax_small_kernel(const void *x
 //
 // y = R(fl(fl(code s) g)); code s is exact.  A lane takes a 16-byte vector of the output at a
 // time, so that a warp writes whole lines whatever the rows' alignment; of rows that do not begin
-// at such a boundary (SHIFTED) a vector's codes begin anywhere and may belong to two blocks.
+// at such a boundary (SHIFTED) a vector's codes begin anywhere and may belong to two blocks.  Bound
+// by HBM: 8192 x 11008 to BF16 35 us (MXFP4, 6.5 TB/s) and 36 us (NVFP4); 1021 x 5003 to FP32 rows
+// of any alignment 6.0 us (a group of 16 a lane, element by element: 21 us).
 template <int DT, int FMT, bool SHIFTED, int PARTS>
 __global__ void __launch_bounds__(kThreads, 8)
 fp4_dequant_kernel(const uint8_t *codes, const uint8_t *scales, const float *amax, int64_t T,
