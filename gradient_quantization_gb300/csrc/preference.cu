@@ -151,8 +151,9 @@ __global__ void __launch_bounds__(kThreads) preference_kernel(const PreferenceLo
         const float small = expf(-fabsf(hf)), tail = log1pf(small);
         if (rank == 0 && threadIdx.x % THREADS == 0) {
             const float down = __fadd_rn(fmaxf(-hf, 0.0f), tail), up = __fadd_rn(fmaxf(hf, 0.0f), tail);
-            float loss = __fmul_rn(1.0f - a.smoothing, down);
-            if (a.smoothing > 0.0f) loss = __fmaf_rn(a.smoothing, up, loss);   // up may be infinite
+            // (down or up may be infinite: a factor of 0 takes no part)
+            float loss = a.smoothing < 1.0f ? __fmul_rn(1.0f - a.smoothing, down) : 0.0f;
+            if (a.smoothing > 0.0f) loss = __fmaf_rn(a.smoothing, up, loss);
             if (a.loss) a.loss[p] = hf != hf ? NAN : __fmul_rn(w, loss);
             if (a.margin) a.margin[p] = hf;
         }

@@ -626,8 +626,10 @@ agoq_status agoq_policy_loss(const void *logits, int64_t ld, int dtype, const in
  *   loss, margin : out, FP32 [P] (margin is h), or NULL.
  *   dlogp    : out, FP32 [T].  Tokens before the first and behind the last answer are left
  *              as they were.
- * Sums are kept with their rounding errors and joined in binary64, in a fixed order: results
- * are deterministic.  T <= 2^40, P <= 2^30.
+ * An infinite h takes its limit: the term whose factor (1 - e or e) is 0 is left out.  Sums are
+ * kept in pairs of binary32 numbers, the second for the roundings of the first, and joined in a
+ * fixed order: results are deterministic.  (Where offsets fall, so that two valid pairs around
+ * one that is not share tokens, dlogp there is either's.)  T <= 2^40, P <= 2^30.
  */
 agoq_status agoq_preference_loss(const float *logp, const float *ref_logp, const int64_t *offsets,
                                  const float *weights, int64_t T, int64_t P, float beta,
@@ -649,8 +651,8 @@ agoq_status agoq_preference_loss(const float *logp, const float *ref_logp, const
  *   scales : tiles of 128 rows by 4 blocks, 512 bytes each, row blocks slowest
  *            (ceil(rows/128) x ceil(blocks/4) tiles): block b of row r is byte
  *            (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4 of tile (r / 128, b / 4); 0 where
- *            there is no such row or where a block would begin behind the row's end.  (The tensor cores' own order: the product copies tiles as
- *            they are.)
+ *            there is no such row or where a block would begin behind the row's end.  (The
+ *            tensor cores' own order: the product copies tiles as they are.)
  * Both 16-byte aligned.  1 <= K <= 2^24, rows <= 2^30.
  */
 typedef enum { AGOQ_MXFP4 = 0, AGOQ_NVFP4 = 1 } agoq_fp4_format;
@@ -704,7 +706,8 @@ agoq_status agoq_fp4_dequant(const void *codes, const void *scales, const float 
  *   d : out, M rows of N elements of `dtype`, ldd >= N apart, aligned to its elements (rows at
  *       16-byte boundaries are written in vectors).
  * M and N from 0 (a no-op), ceil(M/128) * ceil(N/128) <= 2^26.  Where one of them is at most
- * 64, the CTAs of a tile share its K and join their sums in a fixed order.  An operand's NaN
+ * 64, and for few tiles of a long K, the CTAs of a tile share its K and join their sums in a
+ * fixed order.  An operand's NaN
  * scale gives NaN in its row of d.  Pipeline waits are time-limited: see agoq_device_status.
  */
 agoq_status agoq_fp4_gemm(const void *a_codes, const void *a_scales, const float *a_amax,
