@@ -20,6 +20,7 @@
 // Measured: 8192^3 NVFP4 to BF16 166 us (6.6 PFLOP/s), 8192 x 11008 x 4096 128 us (5.8), 11008 x 4096 x
 // 8192 MXFP4 to FP32 120 us (6.1); 1 x 11008 x 4096 8.0 us (3.2 TB/s of operands).  An MMA of a pair
 // takes 128 cycles for 256 x 256 x 64, which is 10.2 PFLOP/s at 2.05 GHz; a stage of four takes about 540.
+// (The chip's nominal rate, 13.5, is that of an MMA of 96 elements of K, which is not used here.)
 // What is left at large sizes is the end of a tile, 2500 cycles: the two CTAs' 256 columns are the only
 // accumulator (with the scales, tensor memory has no room for a second one), and the next tile waits
 // for both CTAs to have read it; and the last round (8192 x 11008 is 18.1 rounds of 76 pairs).  What

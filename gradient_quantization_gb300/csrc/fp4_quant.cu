@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 8) fp4_rows_kernel(const Fp4Quant a,
 // and 4.7 TB/s), bound by instruction issue (63% of the slots, the integer pipe 60% busy);
 // 8192 x 8192 FP32 to NVFP4 52 us and 60 us (5.8 and 5.7 TB/s).  Five CTAs an SM for MXFP4 (columns
 // 41 us with four), four for NVFP4 (columns 47 us with five).  FP32 tiles of 128 rows left room for
-// two CTAs: both ways 93 us.
+// two CTAs: both ways 86 us.
 constexpr int kTile = 128;
 template <int DT>
 struct TileShape {
