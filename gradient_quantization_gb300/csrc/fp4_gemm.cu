@@ -17,16 +17,19 @@
 //   the others  the epilogue (SPLIT: warps 4-7).
 // Every stage has scale columns of its own, so that a write never meets an MMA that still reads.
 //
-// Measured: 8192^3 NVFP4 to BF16 166 us (6.6 PFLOP/s), 8192 x 11008 x 4096 128 us (5.8), 11008 x 4096 x
-// 8192 MXFP4 to FP32 120 us (6.1); 1 x 11008 x 4096 8.0 us (3.2 TB/s of operands).  An MMA of a pair
-// takes 128 cycles for 256 x 256 x 64, which is 10.2 PFLOP/s at 2.05 GHz; a stage of four takes about 540.
-// (The chip's nominal rate, 13.5, is that of an MMA of 96 elements of K, which is not used here.)
-// What is left at large sizes is the end of a tile, 2500 cycles: the two CTAs' 256 columns are the only
-// accumulator (with the scales, tensor memory has no room for a second one), and the next tile waits
-// for both CTAs to have read it; and the last round (8192 x 11008 is 18.1 rounds of 76 pairs).  What
-// bounded it before: the thread that issues MMAs, whose two waits, four MMAs and commit took 940
-// cycles a stage with operands in ordinary registers (now one wait of the whole warp and an elected
-// lane); scale tiles by tcgen05.cp, 50 to 110 cycles of the MMAs' own pipe for each of a stage's
+// Measured (in a graph, inputs warm): 8192^3 NVFP4 to BF16 163 us (6.7 PFLOP/s), 8192 x 11008 x 4096
+// 124 us (6.0), 11008 x 4096 x 8192 MXFP4 to FP32 118 us (6.3); 1 x 11008 x 4096 8.4 us (3.0 TB/s of
+// operands).  An MMA of a pair takes 128 cycles for 256 x 256 x 64, which is 10.2 PFLOP/s at 2.05 GHz; a
+// stage of four takes 542 (MXFP4) or 584 (NVFP4) where its operands come from the L2 cache, by one pair
+// or by all, and about 730 at 4096 x 4864 x 16384 on all pairs, by the traffic of the L2 (584 again where
+// the same number of tiles read the same rows).  (The chip's nominal rate, 13.5, is that of an MMA
+// of 96 elements of K, which is not used here.)  The rest at large sizes: the end of a tile, 1.3 us
+// before its halves were ordered apart (below: kHold; 129, 121 and 167 us without), as the two CTAs' 256
+// columns are the only accumulator (tensor memory has no room for a second one beside the scales); the
+// last round (8192 x 11008 is 18.1 rounds of 76 pairs); and the clock, which falls from 2070 MHz to
+// 1750 in a second of such products.  What bounded it before: the thread that issues MMAs, whose two
+// waits, four MMAs and commit took 940 cycles a stage with operands in ordinary registers (now one wait
+// of the whole warp and an elected lane); scale tiles by tcgen05.cp, 50 to 110 cycles of the MMAs' own pipe for each of a stage's
 // twelve (266 us for 8192 x 11008 x 4096); clusters of two pairs that share Q by multicast, of which
 // 36 fit the GPU (72 of 76 pairs) and which moved less without being faster (81 us for 4096 x 4864 x
 // 8192, 67 us then by pairs).  Few rows are bound by latency: a call of one tile and one stage takes
@@ -153,6 +156,9 @@ struct Shape {
     static constexpr int kScaleWarps = 4, kEpiWarps = SPLIT ? 0 : 8;
     static constexpr int kThreads = 32 * (kScaleWarp0 + kScaleWarps + kEpiWarps);
     static constexpr int kBuffers = !SPLIT && BN <= 128 ? 2 : 1;   // accumulators
+    // A pair's accumulator is two halves of its columns, each with MMAs and barriers of its own.
+    static constexpr int kHalves = PAIR ? 2 : 1;
+    static constexpr int kAccs = kBuffers * kHalves, kAccCols = BN / kHalves;
     static constexpr int kScaleCols = 4 * kTiles * (1 + kQTiles);
     static constexpr int kUsedCols = kBuffers * BN + kStages * kScaleCols;
     static constexpr int kTmemCols = kUsedCols <= 256 ? 256 : 512;
@@ -162,10 +168,10 @@ struct Shape {
     static constexpr int kOffPS = kOffOut + kEpiWarps * kOutBytes;
     static constexpr int kOffQS = kOffPS + kStages * kPScales;
     static constexpr int kOffBar = kOffQS + kStages * kQScales;
-    static constexpr int kBars = 4 * kStages + 2 * kBuffers + 1;
+    static constexpr int kBars = 4 * kStages + 2 * kAccs + 1;
     static constexpr int kOffMisc = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffMisc + 16 + 1024;
-    static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
+    static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(kAccCols >> 3) << 17) |
                                        (FMT == kMx ? 1u << 23 : 0u) |
                                        ((uint32_t)(kTileRows >> 4) << 24);
     static_assert(kUsedCols <= 512, "tensor memory");
@@ -215,6 +221,13 @@ struct Ring {
 // Waits that are long as a rule let the thread sleep: a poll takes an issue slot and a cycle of
 // the shared memory that the MMAs read from.
 constexpr uint32_t kSleepNs = 20000;
+
+// Stages of a pair whose MMAs are ordered by halves of the accumulator at a tile's end and the next
+// one's begin: the first half is read while the second half's last MMAs run, and the second while
+// the next tile's first MMAs run in the first.  They are held until the second half's MMAs are done.
+// 8192 x 11008 x 4096: 124 us with three, 125 with two, 129 without; four 2% slower than three.
+constexpr int kHold = 3;
+static_assert(kHold >= 1 && kHold < 5, "stages held, of five");
 
 // Tiles in bands of kBand along Q: the CTAs at work share a few rows of both operands.
 constexpr int kBand = 16;
@@ -329,8 +342,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     uint8_t *sp = smem, *sq = smem + S::kOffQ, *sps = smem + S::kOffPS, *sqs = smem + S::kOffQS;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kOffBar);
     uint64_t *full = bars, *empty = bars + NS, *sfull = bars + 2 * NS, *sempty = bars + 3 * NS,
-             *tfull = bars + 4 * NS, *tempty = tfull + S::kBuffers,
-             *drain = tempty + S::kBuffers;
+             *tfull = bars + 4 * NS, *tempty = tfull + S::kAccs,
+             *drain = tempty + S::kAccs;
     uint32_t *tmem_addr = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
     unsigned *status = &g_fp4_status;
@@ -363,9 +376,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             mbar_init(&sfull[s], 1);
             mbar_init(&sempty[s], S::kScaleWarps);
         }
-        for (int b = 0; b < S::kBuffers; ++b) {
+        for (int b = 0; b < S::kAccs; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], S::SPLIT ? 1 : S::kEpiWarps * S::kCluster);
+            mbar_init(&tempty[b], S::SPLIT ? 1 : S::kEpiWarps * S::kCluster / S::kHalves);
         }
         mbar_init(drain, 1);
         *abort = 0;
@@ -400,9 +413,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         g1 = fmaxf(gp, gq);
     }
     // The epilogue holds 128 columns of a row.  512 threads were launched with 128 registers each:
-    // 72 + 80 + 2 * 176 a thread of the four warpgroups is below 4 * 128.
+    // 2 * 80 + 2 * 176 a thread of the four warpgroups is 4 * 128.
     if (warp < kScaleWarp0) {
-    if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == kTmaWarp) {
         if (lane == 0) {
             // A pair's codes all count on the barrier of its CTA 0, which issues the MMAs; so do the
@@ -414,7 +427,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
                 int tp, tq;
                 tile_at(tile, num_p, num_q, tp, tq);
-                const int p0 = tp * S::kTileRows + BM * side, q0 = tq * BN + S::kQRows * side;
+                const int p0 = tp * S::kTileRows + BM * side, q0 = tq * BN + S::kQRows / S::kHalves * side;
                 for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next()) {
                     const int s = ring.s;
                     if (!wait_bar(&empty[s], ring.parity ^ 1u, abort, status, false, kSleepNs)) {
@@ -424,7 +437,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                     if (side == 0) mbar_expect_tx(&full[s], (S::kPBytes + S::kQBytes) * S::kCluster);
                     if constexpr (S::PAIR) {
                         tma_load_2d_pair(sp + s * S::kPBytes, &map_p, full0 + 8u * s, kb * kRowBytes, p0);
-                        tma_load_2d_pair(sq + s * S::kQBytes, &map_q, full0 + 8u * s, kb * kRowBytes, q0);
+                        // (an MMA of one half of the columns takes half of them from each CTA)
+#pragma unroll
+                        for (int h = 0; h < S::kHalves; ++h)
+                            tma_load_2d_pair(sq + s * S::kQBytes + h * (S::kQBytes / S::kHalves), &map_q,
+                                             full0 + 8u * s, kb * kRowBytes, q0 + h * S::kAccCols);
                     } else {
                         tma_load_2d(sp + s * S::kPBytes, &map_p, &full[s], kb * kRowBytes, p0);
                         tma_load_2d(sq + s * S::kQBytes, &map_q, &full[s], kb * kRowBytes, q0);
@@ -480,52 +497,106 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
             // the whole warp runs the loop, one lane issues
             uint32_t t = 0;
             bool ok = true, issued = false;
-            Ring<NS> ring;
+            Ring<NS> ring, second;               // stages of the first half's MMAs and the second's
             const uint64_t pd0 = sw128_kmajor_desc(smem_u32(sp)), qd0 = sw128_kmajor_desc(smem_u32(sq));
             for (int tile = cid; ok && tile < num_tiles; tile += ncl, ++t) {
                 const int buf = t % S::kBuffers;
-                if (!S::SPLIT && !warp_wait_all(&tempty[buf], ((t / S::kBuffers) & 1u) ^ 1u, abort, status, 0)) break;
+                const uint32_t free_parity = ((t / S::kBuffers) & 1u) ^ 1u;
+                if (!S::SPLIT && !warp_wait_all(&tempty[buf], free_parity, abort, status, 0)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
-                int left = a.K - kb0 * BK;           // elements of K from this stage on
-                for (int kb = kb0; kb < kb1; ++kb, left -= BK, ring.next()) {
-                    const int s = ring.s;
-                    if (!warp_wait_all(&full[s], ring.parity, abort, status, 0)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                // the MMAs of stage kb, in place s, for halves h0 .. h1 - 1
+                auto issue = [&](int s, int kb, int h0, int h1) {
+                    const int left = a.K - kb * BK;          // elements of K from this stage on
                     const uint32_t cols = scale_cols + s * S::kScaleCols, qcols = cols + 4 * S::kTiles;
-                    const uint64_t pd = pd0 + (uint32_t)s * (S::kPBytes >> 4), qd = qd0 + (uint32_t)s * (S::kQBytes >> 4);
+                    const uint64_t pd = pd0 + (uint32_t)s * (S::kPBytes >> 4);
+                    const uint64_t qd = qd0 + (uint32_t)s * (S::kQBytes >> 4);
                     auto step = [&](int kk, uint32_t accumulate) {
                         // a step is 32 bytes of a row; MXFP4: two scales of a tile's four
                         const int j = FMT == kNv ? kk : kk >> 1;
                         const uint32_t id = FMT == kNv ? 0 : 2 * (kk & 1);
-                        mma_fp4<FMT, S::PAIR>(d, pd + 2 * kk, qd + 2 * kk, S::kIdesc | (id << 29) | (id << 4),
-                                              cols + 4 * j, qcols + 4 * j * S::kQTiles, accumulate);
+#pragma unroll
+                        for (int h = 0; h < S::kHalves; ++h)
+                            if (h >= h0 && h < h1)
+                                mma_fp4<FMT, S::PAIR>(d + h * S::kAccCols, pd + 2 * kk,
+                                                      qd + h * (S::kQBytes / S::kHalves >> 4) + 2 * kk,
+                                                      S::kIdesc | (id << 29) | (id << 4), cols + 4 * j,
+                                                      qcols + 4 * (j * S::kQTiles + h), accumulate);
                     };
-                    if (elect_one()) {
-                        step(0, kb > kb0);
-                        if (left > 192) {
-                            step(1, 1);
-                            step(2, 1);
-                            step(3, 1);
-                        } else {
-                            if (left > 64) step(1, 1);
-                            if (left > 128) step(2, 1);
-                        }
-                        if constexpr (S::PAIR) umma_commit_pair_multicast(&empty[s], 3);
-                        else commit_one(&empty[s]);
+                    step(0, kb > kb0);
+                    if (left > 192) {
+                        step(1, 1);
+                        step(2, 1);
+                        step(3, 1);
+                    } else {
+                        if (left > 64) step(1, 1);
+                        if (left > 128) step(2, 1);
                     }
-                    __syncwarp();
-                    issued = true;
+                };
+                if constexpr (S::PAIR) {
+                    // kHold stages at a tile's begin and its end: all MMAs of the first half, then those
+                    // of the second.  Between them both halves of a stage at a time.
+                    int kb = 0;
+                    auto by_halves = [&](bool begin, bool end, int some) {
+                        for (int i = 0; i < some; ++i, ring.next()) {
+                            if (!warp_wait_all(&full[ring.s], ring.parity, abort, status, 0)) return false;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                issue(ring.s, kb + i, 0, 1);
+                                if (end && i == some - 1) umma_commit_pair_multicast(&tfull[0], 3);
+                            }
+                            __syncwarp();
+                            issued = true;
+                        }
+                        if (begin) {
+                            if (!warp_wait_all(&tempty[1], free_parity, abort, status, 0)) return false;
+                            tc_fence_after();
+                        }
+                        for (int i = 0; i < some; ++i, ++kb, second.next()) {
+                            if (elect_one()) {
+                                issue(second.s, kb, 1, 2);
+                                umma_commit_pair_multicast(&empty[second.s], 3);
+                                if (end && i == some - 1) umma_commit_pair_multicast(&tfull[1], 3);
+                            }
+                            __syncwarp();
+                        }
+                        return true;
+                    };
+                    // (at the first tile no accumulator is being read)
+                    const int held = t > 0 ? min(kHold, kall) : 0;
+                    ok = by_halves(true, held == kall, held);
+                    for (; ok && kb < kall - kHold; ++kb, ring.next()) {
+                        if (!warp_wait_all(&full[ring.s], ring.parity, abort, status, 0)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            issue(ring.s, kb, 0, 2);
+                            umma_commit_pair_multicast(&empty[ring.s], 3);
+                        }
+                        __syncwarp();
+                    }
+                    second = ring;
+                    if (ok && kb < kall) ok = by_halves(false, true, kall - kb);
+                } else {
+                    for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+                        const int s = ring.s;
+                        if (!warp_wait_all(&full[s], ring.parity, abort, status, 0)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            issue(s, kb, 0, 1);
+                            commit_one(&empty[s]);
+                            if (kb == kb1 - 1) commit_one(&tfull[buf]);
+                        }
+                        __syncwarp();
+                        issued = true;
+                    }
                 }
                 if (!ok) break;
-                if (elect_one()) {
-                    if constexpr (S::PAIR) umma_commit_pair_multicast(&tfull[buf], 3);
-                    else if (kb0 < kb1) commit_one(&tfull[buf]);
-                }
-                __syncwarp();
             }
             // (elect_one names the same lane each time: the commits are of the thread that issued)
             if (issued) {
@@ -623,8 +694,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         const uint32_t tempty0 = S::PAIR ? mapa_shared(smem_u32(tempty), 0) : 0u;
         uint32_t t = 0;
         for (int tile = cid; tile < num_tiles; tile += ncl, ++t) {
-            const int buf = t % S::kBuffers;
-            if (!warp_wait_all(&tfull[buf], (t / S::kBuffers) & 1u, abort, status, 500)) break;
+            const int buf = t % S::kBuffers, acc = S::PAIR ? half : buf;
+            if (!warp_wait_all(&tfull[acc], (t / S::kBuffers) & 1u, abort, status, 500)) break;
             tc_fence_after();
             int tp, tq;
             tile_at(tile, num_p, num_q, tp, tq);
@@ -635,8 +706,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (S::PAIR && side != 0) mbar_arrive_remote(tempty0 + (uint32_t)buf * 8u);
-                    else mbar_arrive(&tempty[buf]);
+                    if (S::PAIR && side != 0) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
+                    else mbar_arrive(&tempty[acc]);
                 }
             };
             if (a.dtype == kF32) store_tile<FMT, kF32, CW>(&map_d, buf_out, from, row, col, a, g0, g1, lane, free_acc);
@@ -760,7 +831,7 @@ template <int FMT, class S>
 cudaError_t launch_shape(const Fp4Args &a, const uint8_t *p_codes, const uint8_t *q_codes, int split,
                          cudaStream_t st) {
     CUtensorMap mp, mq, md{};
-    if (!encode_codes(&mp, p_codes, a.P, a.K, BM) || !encode_codes(&mq, q_codes, a.Q, a.K, S::kQRows))
+    if (!encode_codes(&mp, p_codes, a.P, a.K, BM) || !encode_codes(&mq, q_codes, a.Q, a.K, S::kQRows / S::kHalves))
         return cudaErrorInvalidValue;
     if (!S::SPLIT && a.vectors) {
         const int es = a.dtype == kF32 ? 4 : 2;
@@ -821,15 +892,16 @@ cudaError_t launch_fmt(const Fp4Operand &A, const Fp4Operand &B, int64_t M, int6
     const int split = (int)std::min<int64_t>({8, sm_count() / tiles, stages / 8});
     if (split > 2)
         return launch_shape<FMT, Shape<FMT, 128, false, true>>(a, p.codes, q.codes, split, st);
-    // Tiles of 256 x 256 by CTA pairs, or of 128 x 128 by single CTAs, by what their rounds take (in
-    // tenths of a microsecond, from measurements at both sides: 256 x 11008 x 4096 11.6 us by pairs,
-    // 14.0 by single CTAs; 300 x 11008 x 4096 16.8 and 14.1; 2048 x 4096 x 4096 18.1 and 23.9;
-    // 2500 x 2504 x 500 to FP32 10.4 and 8.2).  A pair's round is 2.7 a stage and 23 for the
-    // accumulator, which has no second one beside it; a single CTA's 3.4 a stage.
+    // Tiles of 256 x 256 by CTA pairs, or of 128 x 128 by single CTAs, by what their rounds take, in
+    // tenths of a microsecond: a pair's 2.7 a stage and 1.8 for its end, a single CTA's 3.4 a stage
+    // and 0.2 (its second accumulator hides the rest), but 1.6 at least for its stores.  From 35 sizes
+    // timed both ways, of which it misses five by 6% at most (pairs, then single CTAs): 4096 x 4096 x
+    // 2048 20.5 and 23.8 us, 700 x 11008 x 4096 18.0 and 23.7, 300 x 11008 x 4096 16.6 and 14.1,
+    // 517 x 5003 x 1999 16.7 and 14.8, 2500 x 2504 x 500 to FP32 10.2 and 8.5.
     const int64_t pair_tiles = (M + 255) / 256 * ((N + 255) / 256), pairs = sm_count() / 2;
-    const int64_t pair_time = 49 + (pair_tiles + pairs - 1) / pairs * (27 * stages / 10 + 23);
-    const int64_t single_time = 33 + (tiles + sm_count() - 1) / sm_count() * std::max<int64_t>(34 * stages / 10, 15);
-    if (pair_time < single_time)
+    const int64_t pair_time = 58 + (pair_tiles + pairs - 1) / pairs * (27 * stages / 10 + 18);
+    const int64_t single_time = 38 + (tiles + sm_count() - 1) / sm_count() * std::max<int64_t>(34 * stages / 10 + 2, 16);
+    if (pair_time <= single_time)
         return launch_shape<FMT, Shape<FMT, 256, true, false>>(a, p.codes, q.codes, 1, st);
     return launch_shape<FMT, Shape<FMT, 128, false, false>>(a, p.codes, q.codes, 1, st);
 }
