@@ -590,10 +590,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                         if (elect_one()) {
                             issue(s, kb, 0, 1);
                             commit_one(&empty[s]);
-                            if (kb == kb1 - 1) commit_one(&tfull[buf]);
                         }
                         __syncwarp();
                         issued = true;
+                    }
+                    // (a condition among the stage's own instructions: 512 x 4096 x 4096 9.3 us, 8.7 here)
+                    if (ok && kb0 < kb1) {
+                        if (elect_one()) commit_one(&tfull[buf]);
+                        __syncwarp();
                     }
                 }
                 if (!ok) break;
@@ -894,7 +898,7 @@ cudaError_t launch_fmt(const Fp4Operand &A, const Fp4Operand &B, int64_t M, int6
         return launch_shape<FMT, Shape<FMT, 128, false, true>>(a, p.codes, q.codes, split, st);
     // Tiles of 256 x 256 by CTA pairs, or of 128 x 128 by single CTAs, by what their rounds take, in
     // tenths of a microsecond: a pair's 2.7 a stage and 1.8 for its end, a single CTA's 3.4 a stage
-    // and 0.2 (its second accumulator hides the rest), but 1.6 at least for its stores.  From 35 sizes
+    // and 0.2 (its second accumulator hides the rest), but 1.6 at least for its stores.  From 36 sizes
     // timed both ways, of which it misses five by 6% at most (pairs, then single CTAs): 4096 x 4096 x
     // 2048 20.5 and 23.8 us, 700 x 11008 x 4096 18.0 and 23.7, 300 x 11008 x 4096 16.6 and 14.1,
     // 517 x 5003 x 1999 16.7 and 14.8, 2500 x 2504 x 500 to FP32 10.2 and 8.5.
