@@ -18,7 +18,7 @@
 // Every stage has scale columns of its own, so that a write never meets an MMA that still reads.
 //
 // Measured (in a graph, inputs warm): 8192^3 NVFP4 to BF16 163 us (6.7 PFLOP/s), 8192 x 11008 x 4096
-// 124 us (6.0), 11008 x 4096 x 8192 MXFP4 to FP32 118 us (6.3); 1 x 11008 x 4096 8.4 us (3.0 TB/s of
+// 124 us (6.0), 11008 x 4096 x 8192 MXFP4 to FP32 118 us (6.3); 1 x 11008 x 4096 8.1 us (3.1 TB/s of
 // operands).  An MMA of a pair takes 128 cycles for 256 x 256 x 64, which is 10.2 PFLOP/s at 2.05 GHz; a
 // stage of four takes 542 (MXFP4) or 584 (NVFP4) where its operands come from the L2 cache, by one pair
 // or by all, and about 730 at 4096 x 4864 x 16384 on all pairs, by the traffic of the L2 (584 again where
