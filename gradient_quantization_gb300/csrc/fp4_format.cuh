@@ -36,10 +36,22 @@ constexpr float kE2M1Max = 6.0f;
 constexpr float kTensorSpan = 2688.0f;          // 6 * 448
 constexpr float kLowestTensorScale = 0x1p-100f; // products with a block's scale stay normal
 
-// A tensor's scale from its largest magnitude (not finite: the scale is not used, since all
-// blocks' scales are NaN then).
+// The larger and the smaller of two; a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// A tensor's scale from its largest magnitude.  Of one that is not finite, codes made with it have
+// NaN block scales; codes from before may not, so a NaN must stay.
 __device__ __forceinline__ float tensor_scale(float amax) {
-    return fmaxf(__fdiv_rn(amax, kTensorSpan), kLowestTensorScale);
+    return max_nan(__fdiv_rn(amax, kTensorSpan), kLowestTensorScale);
 }
 
 __device__ __forceinline__ bool finite_bits(float v) {

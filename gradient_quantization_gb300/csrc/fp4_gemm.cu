@@ -409,8 +409,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     float g0 = 1.0f, g1 = 1.0f;
     if (FMT == kNv && (S::SPLIT || warp >= kScaleWarp0)) {
         const float gp = tensor_scale(__ldg(a.p_amax)), gq = tensor_scale(__ldg(a.q_amax));
-        g0 = fminf(gp, gq);
-        g1 = fmaxf(gp, gq);
+        g0 = min_nan(gp, gq);
+        g1 = max_nan(gp, gq);
     }
     // The epilogue holds 128 columns of a row.  512 threads were launched with 128 registers each:
     // 2 * 80 + 2 * 176 a thread of the four warpgroups is 4 * 128.

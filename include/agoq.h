@@ -691,7 +691,9 @@ agoq_status agoq_fp4_quant(const void *x, int64_t ldx, int64_t T, int64_t K, int
 
 /*
  * The values again: y = R(fl(fl(code s) g)), or R(fl(code 2^e)).
- *   y : out, T rows of K elements of `dtype`, ldy >= K apart.
+ *   amax : in, one FP32 (device), as at the quantisation; AGOQ_NVFP4 only.  A NaN gives NaN
+ *          throughout, whatever the codes.
+ *   y    : out, T rows of K elements of `dtype`, ldy >= K apart.
  */
 agoq_status agoq_fp4_dequant(const void *codes, const void *scales, const float *amax, int64_t T,
                              int64_t K, int format, void *y, int64_t ldy, int dtype, void *stream);
@@ -708,7 +710,7 @@ agoq_status agoq_fp4_dequant(const void *codes, const void *scales, const float 
  * M and N from 0 (a no-op), ceil(M/128) * ceil(N/128) <= 2^26.  Where one of them is at most
  * 64, and for few tiles of a long K, the CTAs of a tile share its K and join their sums in a
  * fixed order.  An operand's NaN
- * scale gives NaN in its row of d.  Pipeline waits are time-limited: see agoq_device_status.
+ * scale gives NaN in its row of d, a NaN amax throughout.  Pipeline waits are time-limited: see agoq_device_status.
  */
 agoq_status agoq_fp4_gemm(const void *a_codes, const void *a_scales, const float *a_amax,
                           const void *b_codes, const void *b_scales, const float *b_amax,
