@@ -505,6 +505,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 if (!S::SPLIT && !warp_wait_all(&tempty[buf], free_parity, abort, status, 0)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * BN;
+                // Waits for the ring's stage, which is issued next: from then on MMAs may be in flight,
+                // however the loop ends, and the drain below waits for them.
+                auto stage_there = [&] {
+                    if (!warp_wait_all(&full[ring.s], ring.parity, abort, status, 0)) return false;
+                    tc_fence_after();
+                    issued = true;
+                    return true;
+                };
                 // the MMAs of stage kb, in place s, for halves h0 .. h1 - 1
                 auto issue = [&](int s, int kb, int h0, int h1) {
                     const int left = a.K - kb * BK;          // elements of K from this stage on
@@ -539,14 +547,12 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                     int kb = 0;
                     auto by_halves = [&](bool begin, bool end, int some) {
                         for (int i = 0; i < some; ++i, ring.next()) {
-                            if (!warp_wait_all(&full[ring.s], ring.parity, abort, status, 0)) return false;
-                            tc_fence_after();
+                            if (!stage_there()) return false;
                             if (elect_one()) {
                                 issue(ring.s, kb + i, 0, 1);
                                 if (end && i == some - 1) umma_commit_pair_multicast(&tfull[0], 3);
                             }
                             __syncwarp();
-                            issued = true;
                         }
                         if (begin) {
                             if (!warp_wait_all(&tempty[1], free_parity, abort, status, 0)) return false;
@@ -566,11 +572,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                     const int held = t > 0 ? min(kHold, kall) : 0;
                     ok = by_halves(true, held == kall, held);
                     for (; ok && kb < kall - kHold; ++kb, ring.next()) {
-                        if (!warp_wait_all(&full[ring.s], ring.parity, abort, status, 0)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
+                        ok = stage_there();
+                        if (!ok) break;
                         if (elect_one()) {
                             issue(ring.s, kb, 0, 2);
                             umma_commit_pair_multicast(&empty[ring.s], 3);
@@ -582,17 +585,13 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                 } else {
                     for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
                         const int s = ring.s;
-                        if (!warp_wait_all(&full[s], ring.parity, abort, status, 0)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
+                        ok = stage_there();
+                        if (!ok) break;
                         if (elect_one()) {
                             issue(s, kb, 0, 1);
                             commit_one(&empty[s]);
                         }
                         __syncwarp();
-                        issued = true;
                     }
                     // (a condition among the stage's own instructions: 512 x 4096 x 4096 9.3 us, 8.7 here)
                     if (ok && kb0 < kb1) {
