@@ -37,7 +37,7 @@ UNITS = {
     "preference.cu": ["-fmad=false"],
 }
 HEADERS = ["agoq_device.cuh", "agoq_launch.h", "gemm_common.cuh", "wgrad_gemm_impl.cuh", "fwd_gemm_impl.cuh",
-           "typed_io.cuh", "row_units.h", "fp4_format.cuh"]
+           "typed_io.cuh", "row_units.h", "fp4_format.cuh", "fp4_split.h"]
 
 
 def _nvcc():

@@ -41,6 +41,7 @@
 
 #include "agoq_launch.h"
 #include "fp4_format.cuh"
+#include "fp4_split.h"
 #include "gemm_common.cuh"
 #include "typed_io.cuh"
 
@@ -359,8 +360,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     const int kall = (a.K + BK - 1) / BK;
     int kb0 = 0, kb1 = kall;                         // stages of this CTA
     if constexpr (S::SPLIT) {
-        const int per = (kall + C - 1) / C;
-        kb0 = min(rank * per, kall);
+        const int per = (kall + C - 1) / C;          // (fp4_split.h: every CTA has stages)
+        kb0 = rank * per;
         kb1 = min(kb0 + per, kall);
     }
 
@@ -594,7 +595,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
                         __syncwarp();
                     }
                     // (a condition among the stage's own instructions: 512 x 4096 x 4096 9.3 us, 8.7 here)
-                    if (ok && kb0 < kb1) {
+                    if (ok) {
                         if (elect_one()) commit_one(&tfull[buf]);
                         __syncwarp();
                     }
@@ -666,25 +667,20 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
         if constexpr (S::SPLIT) {
             // this CTA's part of the sums, as [column][row], in the stages' place
             float *sums = reinterpret_cast<float *>(smem);
-            const bool any = kb0 < kb1;
             int tile_p, tile_q;
             tile_at(cid, num_p, num_q, tile_p, tile_q);
-            if (any) {
-                ok = ok && warp_wait(&tfull[0], 0u, abort, status, kSleepNs);
-                tc_fence_after();
-            }
+            ok = ok && warp_wait(&tfull[0], 0u, abort, status, kSleepNs);
+            tc_fence_after();
             if (ok) {
 #pragma unroll
                 for (int c = 0; c < BN; c += 32) {
                     if (tile_q * BN + c >= a.Q) break;
                     uint32_t w[32];
-                    if (any) {
-                        __syncwarp();
-                        tmem_ld32(tmem + lanes + c, w);
-                    }
+                    __syncwarp();
+                    tmem_ld32(tmem + lanes + c, w);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        sums[(c + i) * BM + 32 * (warp & 3) + lane] = any ? __uint_as_float(w[i]) : 0.0f;
+                        sums[(c + i) * BM + 32 * (warp & 3) + lane] = __uint_as_float(w[i]);
                 }
             }
         }
@@ -879,20 +875,12 @@ cudaError_t launch_fmt(const Fp4Operand &A, const Fp4Operand &B, int64_t M, int6
     a.vectors = reinterpret_cast<uintptr_t>(d) % 16 == 0 && (ldd * es) % 16 == 0 && ldd < 1ll << 37;
     a.whole = (N * es) % 16 == 0;
     if (small <= 64) {
-        // The CTAs of a tile: as many as the GPU has room for (two an SM), with four stages each, or
-        // four CTAs where the stages are few.  1 x 11008 x 4096: 8.7 us with three, 9.2 with two, 13.8
-        // with four (more than fit); 16 x 4096 x 4096: 7.0 us with four, 7.5 with eight, 10.6 with one;
-        // 32 x 1024 x 1024: 5.5 us with four, 6.5 with one.
-        const int64_t tiles = fp4_tiles_down(a.P), stages = (K + BK - 1) / BK;
-        const int64_t room = 2 * sm_count() / tiles, most = std::max(stages / 4, std::min<int64_t>(stages, 4));
-        const int split = (int)std::max<int64_t>(1, std::min<int64_t>({8, room, most}));
+        const int split = fp4_split_few_rows((K + BK - 1) / BK, fp4_tiles_down(a.P), sm_count());
         return small <= 32 ? launch_shape<FMT, Shape<FMT, 32, false, true>>(a, p.codes, q.codes, split, st)
                            : launch_shape<FMT, Shape<FMT, 64, false, true>>(a, p.codes, q.codes, split, st);
     }
     const int64_t tiles = fp4_tiles_down(M) * fp4_tiles_down(N), stages = (K + BK - 1) / BK;
-    // Few tiles of 128 x 128 over a long K: shared as above, a CTA an SM.  300 x 200 x 9000: 10 us,
-    // 15 us without; but 512 x 512 x 4096, with four CTAs of four stages each: 8.8 us, 8.2 without.
-    const int split = (int)std::min<int64_t>({8, sm_count() / tiles, stages / 8});
+    const int split = fp4_split_few_tiles(stages, tiles, sm_count());
     if (split > 2)
         return launch_shape<FMT, Shape<FMT, 128, false, true>>(a, p.codes, q.codes, split, st);
     // Tiles of 256 x 256 by CTA pairs, or of 128 x 128 by single CTAs, by what their rounds take, in
