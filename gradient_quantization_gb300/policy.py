@@ -39,19 +39,19 @@ class PolicyHead:
         self.grads = agoq.GradList([(self.master, self.master_scales), self.norm_dw, self.norm_db])
         self.requantise()
 
-    def _operand(self, x, rows=True, columns=True):
+    def _operand(self, x, columns=True):
         """(codes, scales, codes_t, scales_t, amax) of a matrix."""
         amax = agoq.agoq_amax(x) if self.fmt == agoq.NVFP4 else None
-        return (*agoq.agoq_fp4_quant(x, self.fmt, amax, rows=rows, columns=columns), amax)
+        return (*agoq.agoq_fp4_quant(x, self.fmt, amax, columns=columns), amax)
 
     def requantise(self):
         """The projection's operands from the weight as it is now: its rows for the logits, its
         columns for the gradient of their input."""
         self.operand = self._operand(self.weight)
 
-    def _logits(self, y):
-        """(logits, FP4 operand) of the normed input."""
-        op = self._operand(y)
+    def _logits(self, y, columns=True):
+        """(logits, FP4 operand) of the normed input; its columns are for the weight gradient."""
+        op = self._operand(y, columns)
         w = self.operand
         V, H = self.weight.shape
         return agoq.agoq_fp4_gemm(op[0], op[1], w[0], w[1], y.shape[0], V, H, self.fmt, op[4],
@@ -60,7 +60,8 @@ class PolicyHead:
     def logprobs(self, x, tokens):
         """Log probabilities of tokens, FP32 [T]: of the policy that samples, or a reference."""
         y = agoq.agoq_layernorm_forward(x, self.norm_w, self.norm_b, self.eps, want_stats=False)[0]
-        return agoq.agoq_token_logprobs(self._logits(y)[0], tokens, want_entropy=False)[0]
+        logits, _ = self._logits(y, columns=False)
+        return agoq.agoq_token_logprobs(logits, tokens, want_entropy=False)[0]
 
     def _forward(self, x):
         y, _, _, codes, scales = agoq.agoq_layernorm_forward(
