@@ -5,7 +5,8 @@ Quantization for Memory-Efficient Distributed Training of LLMs", sections 2.A an
 the last layer of a policy).
 
 Between the forward and the backward pass of a micro-batch the norm's input is kept as low-bit
-codes and the projection's operand in FP4; the logits become their own gradient in place.
+codes and the projection's operand in FP4, along its columns alone; the logits become their own
+gradient in place.
 
     head = PolicyHead(norm_w, norm_b, weight)              # BF16 [H], [H], [V][H]
     old = head.logprobs(x, tokens)                         # of the sampling policy, FP32 [T]
@@ -64,18 +65,21 @@ class PolicyHead:
         return agoq.agoq_token_logprobs(logits, tokens, want_entropy=False)[0]
 
     def _forward(self, x):
+        """(logits, what is kept for _backward): the columns of the projection's operand (its rows
+        are done with) and the codes of the norm's input."""
         y, _, _, codes, scales = agoq.agoq_layernorm_forward(
             x, self.norm_w, self.norm_b, self.eps, bits=self.bits, want_stats=False)
         logits, op = self._logits(y)
-        return logits, op, codes, scales
+        return logits, op[2:], codes, scales
 
-    def _backward(self, dlogits, op, codes, scales):
+    def _backward(self, dlogits, y_columns, codes, scales):
         """dx of the logits' gradient; adds this micro-batch's gradients."""
         T, V = dlogits.shape
         H = self.weight.shape[1]
         d, w = self._operand(dlogits), self.operand
         # dW = dlogits^T y, summed over the tokens: columns of both
-        dweight = agoq.agoq_fp4_gemm(d[2], d[3], op[2], op[3], V, H, T, self.fmt, d[4], op[4],
+        yc, ys, y_amax = y_columns
+        dweight = agoq.agoq_fp4_gemm(d[2], d[3], yc, ys, V, H, T, self.fmt, d[4], y_amax,
                                      dtype=dlogits.dtype)
         agoq.agoq_grad_accum_fp8(self.master, self.master_scales, dweight)
         # dy = dlogits W, summed over the vocabulary: rows of the gradient, columns of the weight

@@ -1,5 +1,7 @@
 """What the policy head (gradient_quantization_gb300/policy.py) asks of the library and keeps between
 its calls (CPU: stand-ins that record their calls and give tensors of the right kind)."""
+import weakref
+
 import pytest
 import torch
 
@@ -96,3 +98,22 @@ def test_training_takes_columns_too(calls):
         del calls.quants[:]
         step()
         assert [q[:3] for q in calls.quants] == [((T, H), True, True), ((T, V), True, True)]
+
+
+@pytest.mark.parametrize("fmt", [agoq.MXFP4, agoq.NVFP4])
+def test_rows_are_not_kept_through_the_loss(calls, fmt):
+    """Between the passes the head keeps the columns of the projection's operand, not its rows."""
+    head = _head(fmt)
+    seen = []
+
+    def at_the_loss():
+        (_, _, _, out), = calls.quants
+        seen.append([weakref.ref(t) for t in out])
+        calls.quants[:] = [q[:3] for q in calls.quants]
+        del out
+        seen[-1] = [r() is not None for r in seen[-1]]
+    calls.at.update(agoq_policy_loss=at_the_loss, agoq_preference_loss=at_the_loss)
+    for step in (lambda: head.policy(X, IDS, COL, COL), lambda: head.preference(X, IDS, IDS[:1])):
+        del calls.quants[:]
+        step()
+    assert seen == [[False, False, True, True]] * 2
