@@ -109,7 +109,7 @@ const char *agoq_status_string(agoq_status s) {
         case AGOQ_ERR_ALIAS: return "AGOQ_ERR_ALIAS: an output overlaps an input";
         case AGOQ_ERR_CUDA: return "AGOQ_ERR_CUDA: CUDA runtime error";
         case AGOQ_ERR_TIMEOUT: return "AGOQ_ERR_TIMEOUT: a pipeline wait gave up";
-        case AGOQ_ERR_FORMAT: return "AGOQ_ERR_FORMAT: unsupported intermediate format or element type";
+        case AGOQ_ERR_FORMAT: return "AGOQ_ERR_FORMAT: unsupported intermediate format, element type or FP4 format";
     }
     return "AGOQ_ERR_UNKNOWN";
 }

@@ -19,18 +19,21 @@
 //
 // Measured (in a graph, inputs warm): 8192^3 NVFP4 to BF16 163 us (6.7 PFLOP/s), 8192 x 11008 x 4096
 // 124 us (6.0), 11008 x 4096 x 8192 MXFP4 to FP32 118 us (6.3); 1 x 11008 x 4096 8.1 us (3.1 TB/s of
-// operands).  An MMA of a pair takes 128 cycles for 256 x 256 x 64, which is 10.2 PFLOP/s at 2.05 GHz; a
-// stage of four takes 542 (MXFP4) or 584 (NVFP4) where its operands come from the L2 cache, by one pair
-// or by all, and about 730 at 4096 x 4864 x 16384 on all pairs, by the traffic of the L2 (584 again where
-// the same number of tiles read the same rows).  (The chip's nominal rate, 13.5, is that of an MMA
-// of 96 elements of K, which is not used here.)  The rest at large sizes: the end of a tile, 1.3 us
+// operands).  Products one after another for a second, with operands that change, or on another GPU of
+// the same kind, take up to 16% longer, by the clock (8192 x 11008 x 4096 123 to 139 us).  The MMAs of a
+// pair for 256 x 256 x 64, two of 128 columns, take 128 cycles together, which is 10.2 PFLOP/s at 2.05
+// GHz; a stage of four such steps takes 542 (MXFP4) or 584 (NVFP4) where its operands come from the L2
+// cache, by one pair or by all, and about 730 at 4096 x 4864 x 16384 on all pairs, by the traffic of the
+// L2 (584 again where the same number of tiles read the same rows).  (The chip's nominal rate, 13.5, is
+// that of an MMA of 96 elements of K, which is not used here: where all pairs read rows of their own, the
+// L2's traffic is the nearer bound.)  The rest at large sizes: the end of a tile, 1.3 us
 // before its halves were ordered apart (below: kHold; 129, 121 and 167 us without), as the two CTAs' 256
 // columns are the only accumulator (tensor memory has no room for a second one beside the scales); the
 // last round (8192 x 11008 is 18.1 rounds of 76 pairs); and the clock, which falls from 2070 MHz to
 // 1750 in a second of such products.  What bounded it before: the thread that issues MMAs, whose two
 // waits, four MMAs and commit took 940 cycles a stage with operands in ordinary registers (now one wait
-// of the whole warp and an elected lane); scale tiles by tcgen05.cp, 50 to 110 cycles of the MMAs' own pipe for each of a stage's
-// twelve (266 us for 8192 x 11008 x 4096); clusters of two pairs that share Q by multicast, of which
+// of the whole warp and an elected lane); scale tiles by tcgen05.cp, 50 to 110 cycles of the MMAs' own
+// pipe for each of a stage's twelve (266 us for 8192 x 11008 x 4096); clusters of two pairs that share Q by multicast, of which
 // 36 fit the GPU (72 of 76 pairs) and which moved less without being faster (81 us for 4096 x 4864 x
 // 8192, 67 us then by pairs).  Few rows are bound by latency: a call of one tile and one stage takes
 // 4.7 us, of which the loads are 1.1, the scales' way to tensor memory 0.7, the MMAs and their
@@ -416,203 +419,203 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant
     // The epilogue holds 128 columns of a row.  512 threads were launched with 128 registers each:
     // 2 * 80 + 2 * 176 a thread of the four warpgroups is 4 * 128.
     if (warp < kScaleWarp0) {
-    if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == kTmaWarp) {
-        if (lane == 0) {
-            // A pair's codes all count on the barrier of its CTA 0, which issues the MMAs; so do the
-            // warps that write scales.
-            const uint32_t full0 = S::PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
-            uint32_t it = 0;
-            bool ok = true;
-            Ring<NS> ring;
-            for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
-                int tp, tq;
-                tile_at(tile, num_p, num_q, tp, tq);
-                const int p0 = tp * S::kTileRows + BM * side, q0 = tq * BN + S::kQRows / S::kHalves * side;
-                for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next()) {
-                    const int s = ring.s;
-                    if (!wait_bar(&empty[s], ring.parity ^ 1u, abort, status, false, kSleepNs)) {
-                        ok = false;
-                        break;
-                    }
-                    if (side == 0) mbar_expect_tx(&full[s], (S::kPBytes + S::kQBytes) * S::kCluster);
-                    if constexpr (S::PAIR) {
-                        tma_load_2d_pair(sp + s * S::kPBytes, &map_p, full0 + 8u * s, kb * kRowBytes, p0);
-                        // (an MMA of one half of the columns takes half of them from each CTA)
+        if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == kTmaWarp) {
+            if (lane == 0) {
+                // A pair's codes all count on the barrier of its CTA 0, which issues the MMAs; so do the
+                // warps that write scales.
+                const uint32_t full0 = S::PAIR ? mapa_shared(smem_u32(full), 0) : 0u;
+                uint32_t it = 0;
+                bool ok = true;
+                Ring<NS> ring;
+                for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
+                    int tp, tq;
+                    tile_at(tile, num_p, num_q, tp, tq);
+                    const int p0 = tp * S::kTileRows + BM * side, q0 = tq * BN + S::kQRows / S::kHalves * side;
+                    for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next()) {
+                        const int s = ring.s;
+                        if (!wait_bar(&empty[s], ring.parity ^ 1u, abort, status, false, kSleepNs)) {
+                            ok = false;
+                            break;
+                        }
+                        if (side == 0) mbar_expect_tx(&full[s], (S::kPBytes + S::kQBytes) * S::kCluster);
+                        if constexpr (S::PAIR) {
+                            tma_load_2d_pair(sp + s * S::kPBytes, &map_p, full0 + 8u * s, kb * kRowBytes, p0);
+                            // (an MMA of one half of the columns takes half of them from each CTA)
 #pragma unroll
-                        for (int h = 0; h < S::kHalves; ++h)
-                            tma_load_2d_pair(sq + s * S::kQBytes + h * (S::kQBytes / S::kHalves), &map_q,
-                                             full0 + 8u * s, kb * kRowBytes, q0 + h * S::kAccCols);
-                    } else {
-                        tma_load_2d(sp + s * S::kPBytes, &map_p, &full[s], kb * kRowBytes, p0);
-                        tma_load_2d(sq + s * S::kQBytes, &map_q, &full[s], kb * kRowBytes, q0);
+                            for (int h = 0; h < S::kHalves; ++h)
+                                tma_load_2d_pair(sq + s * S::kQBytes + h * (S::kQBytes / S::kHalves), &map_q,
+                                                 full0 + 8u * s, kb * kRowBytes, q0 + h * S::kAccCols);
+                        } else {
+                            tma_load_2d(sp + s * S::kPBytes, &map_p, &full[s], kb * kRowBytes, p0);
+                            tma_load_2d(sq + s * S::kQBytes, &map_q, &full[s], kb * kRowBytes, q0);
+                        }
                     }
                 }
-            }
-            // (CTA 1 of a pair leaves the wait for its copies to CTA 0, which sees both's: neither
-            // exits before the other)
-            for (int d = 0; side == 0 && d < NS && d < (int)it; ++d) {
-                const uint32_t last = it - 1 - d;
-                wait_bar(&full[last % NS], (last / NS) & 1u, abort, status, true);
-            }
-        }
-    } else if (warp == kScaleTmaWarp) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            Ring<NS> ring;
-            for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
-                int tp, tq;
-                tile_at(tile, num_p, num_q, tp, tq);
-                const int p_block = (tp * S::kTileRows) / 128 + side, q_block = tq * BN / 128;
-                const uint8_t *ps = a.p_scales + (int64_t)p_block * a.across * kScaleTile;
-                const uint8_t *qs = a.q_scales + (int64_t)q_block * a.across * kScaleTile;
-                for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next()) {
-                    const int s = ring.s;
-                    if (!wait_bar(&sempty[s], ring.parity ^ 1u, abort, status, false, kSleepNs)) {
-                        ok = false;
-                        break;
-                    }
-                    // the scale tiles that exist
-                    const uint32_t bytes = min(S::kTiles, a.across - kb * S::kTiles) * kScaleTile;
-                    const int64_t at = (int64_t)kb * S::kTiles * kScaleTile;
-                    uint32_t all = p_block < a.p_down ? bytes : 0u;
-#pragma unroll
-                    for (int i = 0; i < S::kQTiles; ++i) all += q_block + i < a.q_down ? bytes : 0u;
-                    mbar_expect_tx(&sfull[s], all);
-                    if (p_block < a.p_down) bulk_load(sps + s * S::kPScales, ps + at, bytes, &sfull[s]);
-#pragma unroll
-                    for (int i = 0; i < S::kQTiles; ++i)
-                        if (q_block + i < a.q_down)
-                            bulk_load(sqs + s * S::kQScales + i * S::kTiles * kScaleTile,
-                                      qs + (int64_t)i * a.across * kScaleTile + at, bytes, &sfull[s]);
+                // (CTA 1 of a pair leaves the wait for its copies to CTA 0, which sees both's: neither
+                // exits before the other)
+                for (int d = 0; side == 0 && d < NS && d < (int)it; ++d) {
+                    const uint32_t last = it - 1 - d;
+                    wait_bar(&full[last % NS], (last / NS) & 1u, abort, status, true);
                 }
             }
-            for (int d = 0; d < NS && d < (int)it; ++d) {
-                const uint32_t last = it - 1 - d;
-                wait_bar(&sfull[last % NS], (last / NS) & 1u, abort, status, true);
+        } else if (warp == kScaleTmaWarp) {
+            if (lane == 0) {
+                uint32_t it = 0;
+                bool ok = true;
+                Ring<NS> ring;
+                for (int tile = cid; ok && tile < num_tiles; tile += ncl) {
+                    int tp, tq;
+                    tile_at(tile, num_p, num_q, tp, tq);
+                    const int p_block = (tp * S::kTileRows) / 128 + side, q_block = tq * BN / 128;
+                    const uint8_t *ps = a.p_scales + (int64_t)p_block * a.across * kScaleTile;
+                    const uint8_t *qs = a.q_scales + (int64_t)q_block * a.across * kScaleTile;
+                    for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next()) {
+                        const int s = ring.s;
+                        if (!wait_bar(&sempty[s], ring.parity ^ 1u, abort, status, false, kSleepNs)) {
+                            ok = false;
+                            break;
+                        }
+                        // the scale tiles that exist
+                        const uint32_t bytes = min(S::kTiles, a.across - kb * S::kTiles) * kScaleTile;
+                        const int64_t at = (int64_t)kb * S::kTiles * kScaleTile;
+                        uint32_t all = p_block < a.p_down ? bytes : 0u;
+#pragma unroll
+                        for (int i = 0; i < S::kQTiles; ++i) all += q_block + i < a.q_down ? bytes : 0u;
+                        mbar_expect_tx(&sfull[s], all);
+                        if (p_block < a.p_down) bulk_load(sps + s * S::kPScales, ps + at, bytes, &sfull[s]);
+#pragma unroll
+                        for (int i = 0; i < S::kQTiles; ++i)
+                            if (q_block + i < a.q_down)
+                                bulk_load(sqs + s * S::kQScales + i * S::kTiles * kScaleTile,
+                                          qs + (int64_t)i * a.across * kScaleTile + at, bytes, &sfull[s]);
+                    }
+                }
+                for (int d = 0; d < NS && d < (int)it; ++d) {
+                    const uint32_t last = it - 1 - d;
+                    wait_bar(&sfull[last % NS], (last / NS) & 1u, abort, status, true);
+                }
             }
-        }
-    } else if (warp == kMmaWarp) {
-        if (side == 0) {
-            // the whole warp runs the loop, one lane issues
-            uint32_t t = 0;
-            bool ok = true, issued = false;
-            Ring<NS> ring, second;               // stages of the first half's MMAs and the second's
-            const uint64_t pd0 = sw128_kmajor_desc(smem_u32(sp)), qd0 = sw128_kmajor_desc(smem_u32(sq));
-            for (int tile = cid; ok && tile < num_tiles; tile += ncl, ++t) {
-                const int buf = t % S::kBuffers;
-                const uint32_t free_parity = ((t / S::kBuffers) & 1u) ^ 1u;
-                if (!S::SPLIT && !warp_wait_all(&tempty[buf], free_parity, abort, status, 0)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + buf * BN;
-                // Waits for the ring's stage, which is issued next: from then on MMAs may be in flight,
-                // however the loop ends, and the drain below waits for them.
-                auto stage_there = [&] {
-                    if (!warp_wait_all(&full[ring.s], ring.parity, abort, status, 0)) return false;
+        } else if (warp == kMmaWarp) {
+            if (side == 0) {
+                // the whole warp runs the loop, one lane issues
+                uint32_t t = 0;
+                bool ok = true, issued = false;
+                Ring<NS> ring, second;               // stages of the first half's MMAs and the second's
+                const uint64_t pd0 = sw128_kmajor_desc(smem_u32(sp)), qd0 = sw128_kmajor_desc(smem_u32(sq));
+                for (int tile = cid; ok && tile < num_tiles; tile += ncl, ++t) {
+                    const int buf = t % S::kBuffers;
+                    const uint32_t free_parity = ((t / S::kBuffers) & 1u) ^ 1u;
+                    if (!S::SPLIT && !warp_wait_all(&tempty[buf], free_parity, abort, status, 0)) break;
                     tc_fence_after();
-                    issued = true;
-                    return true;
-                };
-                // the MMAs of stage kb, in place s, for halves h0 .. h1 - 1
-                auto issue = [&](int s, int kb, int h0, int h1) {
-                    const int left = a.K - kb * BK;          // elements of K from this stage on
-                    const uint32_t cols = scale_cols + s * S::kScaleCols, qcols = cols + 4 * S::kTiles;
-                    const uint64_t pd = pd0 + (uint32_t)s * (S::kPBytes >> 4);
-                    const uint64_t qd = qd0 + (uint32_t)s * (S::kQBytes >> 4);
-                    auto step = [&](int kk, uint32_t accumulate) {
-                        // a step is 32 bytes of a row; MXFP4: two scales of a tile's four
-                        const int j = FMT == kNv ? kk : kk >> 1;
-                        const uint32_t id = FMT == kNv ? 0 : 2 * (kk & 1);
-#pragma unroll
-                        for (int h = 0; h < S::kHalves; ++h)
-                            if (h >= h0 && h < h1)
-                                mma_fp4<FMT, S::PAIR>(d + h * S::kAccCols, pd + 2 * kk,
-                                                      qd + h * (S::kQBytes / S::kHalves >> 4) + 2 * kk,
-                                                      S::kIdesc | (id << 29) | (id << 4), cols + 4 * j,
-                                                      qcols + 4 * (j * S::kQTiles + h), accumulate);
-                    };
-                    step(0, kb > kb0);
-                    if (left > 192) {
-                        step(1, 1);
-                        step(2, 1);
-                        step(3, 1);
-                    } else {
-                        if (left > 64) step(1, 1);
-                        if (left > 128) step(2, 1);
-                    }
-                };
-                if constexpr (S::PAIR) {
-                    // kHold stages at a tile's begin and its end: all MMAs of the first half, then those
-                    // of the second.  Between them both halves of a stage at a time.
-                    int kb = 0;
-                    auto by_halves = [&](bool begin, bool end, int some) {
-                        for (int i = 0; i < some; ++i, ring.next()) {
-                            if (!stage_there()) return false;
-                            if (elect_one()) {
-                                issue(ring.s, kb + i, 0, 1);
-                                if (end && i == some - 1) umma_commit_pair_multicast(&tfull[0], 3);
-                            }
-                            __syncwarp();
-                        }
-                        if (begin) {
-                            if (!warp_wait_all(&tempty[1], free_parity, abort, status, 0)) return false;
-                            tc_fence_after();
-                        }
-                        for (int i = 0; i < some; ++i, ++kb, second.next()) {
-                            if (elect_one()) {
-                                issue(second.s, kb, 1, 2);
-                                umma_commit_pair_multicast(&empty[second.s], 3);
-                                if (end && i == some - 1) umma_commit_pair_multicast(&tfull[1], 3);
-                            }
-                            __syncwarp();
-                        }
+                    const uint32_t d = tmem + buf * BN;
+                    // Waits for the ring's stage, which is issued next: from then on MMAs may be in flight,
+                    // however the loop ends, and the drain below waits for them.
+                    auto stage_there = [&] {
+                        if (!warp_wait_all(&full[ring.s], ring.parity, abort, status, 0)) return false;
+                        tc_fence_after();
+                        issued = true;
                         return true;
                     };
-                    // (at the first tile no accumulator is being read)
-                    const int held = t > 0 ? min(kHold, kall) : 0;
-                    ok = by_halves(true, held == kall, held);
-                    for (; ok && kb < kall - kHold; ++kb, ring.next()) {
-                        ok = stage_there();
-                        if (!ok) break;
-                        if (elect_one()) {
-                            issue(ring.s, kb, 0, 2);
-                            umma_commit_pair_multicast(&empty[ring.s], 3);
+                    // the MMAs of stage kb, in place s, for halves h0 .. h1 - 1
+                    auto issue = [&](int s, int kb, int h0, int h1) {
+                        const int left = a.K - kb * BK;          // elements of K from this stage on
+                        const uint32_t cols = scale_cols + s * S::kScaleCols, qcols = cols + 4 * S::kTiles;
+                        const uint64_t pd = pd0 + (uint32_t)s * (S::kPBytes >> 4);
+                        const uint64_t qd = qd0 + (uint32_t)s * (S::kQBytes >> 4);
+                        auto step = [&](int kk, uint32_t accumulate) {
+                            // a step is 32 bytes of a row; MXFP4: two scales of a tile's four
+                            const int j = FMT == kNv ? kk : kk >> 1;
+                            const uint32_t id = FMT == kNv ? 0 : 2 * (kk & 1);
+#pragma unroll
+                            for (int h = 0; h < S::kHalves; ++h)
+                                if (h >= h0 && h < h1)
+                                    mma_fp4<FMT, S::PAIR>(d + h * S::kAccCols, pd + 2 * kk,
+                                                          qd + h * (S::kQBytes / S::kHalves >> 4) + 2 * kk,
+                                                          S::kIdesc | (id << 29) | (id << 4), cols + 4 * j,
+                                                          qcols + 4 * (j * S::kQTiles + h), accumulate);
+                        };
+                        step(0, kb > kb0);
+                        if (left > 192) {
+                            step(1, 1);
+                            step(2, 1);
+                            step(3, 1);
+                        } else {
+                            if (left > 64) step(1, 1);
+                            if (left > 128) step(2, 1);
                         }
-                        __syncwarp();
-                    }
-                    second = ring;
-                    if (ok && kb < kall) ok = by_halves(false, true, kall - kb);
-                } else {
-                    for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-                        const int s = ring.s;
-                        ok = stage_there();
-                        if (!ok) break;
-                        if (elect_one()) {
-                            issue(s, kb, 0, 1);
-                            commit_one(&empty[s]);
+                    };
+                    if constexpr (S::PAIR) {
+                        // kHold stages at a tile's begin and its end: all MMAs of the first half, then those
+                        // of the second.  Between them both halves of a stage at a time.
+                        int kb = 0;
+                        auto by_halves = [&](bool begin, bool end, int some) {
+                            for (int i = 0; i < some; ++i, ring.next()) {
+                                if (!stage_there()) return false;
+                                if (elect_one()) {
+                                    issue(ring.s, kb + i, 0, 1);
+                                    if (end && i == some - 1) umma_commit_pair_multicast(&tfull[0], 3);
+                                }
+                                __syncwarp();
+                            }
+                            if (begin) {
+                                if (!warp_wait_all(&tempty[1], free_parity, abort, status, 0)) return false;
+                                tc_fence_after();
+                            }
+                            for (int i = 0; i < some; ++i, ++kb, second.next()) {
+                                if (elect_one()) {
+                                    issue(second.s, kb, 1, 2);
+                                    umma_commit_pair_multicast(&empty[second.s], 3);
+                                    if (end && i == some - 1) umma_commit_pair_multicast(&tfull[1], 3);
+                                }
+                                __syncwarp();
+                            }
+                            return true;
+                        };
+                        // (at the first tile no accumulator is being read)
+                        const int held = t > 0 ? min(kHold, kall) : 0;
+                        ok = by_halves(true, held == kall, held);
+                        for (; ok && kb < kall - kHold; ++kb, ring.next()) {
+                            ok = stage_there();
+                            if (!ok) break;
+                            if (elect_one()) {
+                                issue(ring.s, kb, 0, 2);
+                                umma_commit_pair_multicast(&empty[ring.s], 3);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        second = ring;
+                        if (ok && kb < kall) ok = by_halves(false, true, kall - kb);
+                    } else {
+                        for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+                            const int s = ring.s;
+                            ok = stage_there();
+                            if (!ok) break;
+                            if (elect_one()) {
+                                issue(s, kb, 0, 1);
+                                commit_one(&empty[s]);
+                            }
+                            __syncwarp();
+                        }
+                        // (a condition among the stage's own instructions: 512 x 4096 x 4096 9.3 us, 8.7 here)
+                        if (ok) {
+                            if (elect_one()) commit_one(&tfull[buf]);
+                            __syncwarp();
+                        }
                     }
-                    // (a condition among the stage's own instructions: 512 x 4096 x 4096 9.3 us, 8.7 here)
-                    if (ok) {
-                        if (elect_one()) commit_one(&tfull[buf]);
-                        __syncwarp();
+                    if (!ok) break;
+                }
+                // (elect_one names the same lane each time: the commits are of the thread that issued)
+                if (issued) {
+                    if (elect_one()) {
+                        if constexpr (S::PAIR) umma_commit_pair(drain);
+                        else commit_one(drain);
+                        wait_bar(drain, 0u, abort, status, true);
                     }
+                    __syncwarp();
                 }
-                if (!ok) break;
-            }
-            // (elect_one names the same lane each time: the commits are of the thread that issued)
-            if (issued) {
-                if (elect_one()) {
-                    if constexpr (S::PAIR) umma_commit_pair(drain);
-                    else commit_one(drain);
-                    wait_bar(drain, 0u, abort, status, true);
-                }
-                __syncwarp();
             }
         }
-    }
     } else if (warp < kScaleWarp0 + S::kScaleWarps) {
         if constexpr (!S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // scales: P's tiles, then Q's, four columns each
@@ -883,9 +886,11 @@ cudaError_t launch_fmt(const Fp4Operand &A, const Fp4Operand &B, int64_t M, int6
     const int split = fp4_split_few_tiles(stages, tiles, sm_count());
     if (split > 2)
         return launch_shape<FMT, Shape<FMT, 128, false, true>>(a, p.codes, q.codes, split, st);
-    // Tiles of 256 x 256 by CTA pairs, or of 128 x 128 by single CTAs, by what their rounds take, in
-    // tenths of a microsecond: a pair's 2.7 a stage and 1.8 for its end, a single CTA's 3.4 a stage
-    // and 0.2 (its second accumulator hides the rest), but 1.6 at least for its stores.  From 36 sizes
+    // Tiles of 256 x 256 by CTA pairs, or of 128 x 128 by single CTAs, by what their rounds take: a
+    // pair's 0.27 us a stage and 1.8 for its end, a single CTA's 0.34 a stage and 0.2 (its second
+    // accumulator hides the rest), but 1.6 at least for its stores.  What a call takes beside its
+    // rounds (launch, first loads, last stores) is 5.8 us for pairs and 3.8 for single CTAs.  Below in
+    // tenths of a microsecond (a stage in hundredths, divided).  From 36 sizes
     // timed both ways, of which it misses five by 6% at most (pairs, then single CTAs): 4096 x 4096 x
     // 2048 20.5 and 23.8 us, 700 x 11008 x 4096 18.0 and 23.7, 300 x 11008 x 4096 16.6 and 14.1,
     // 517 x 5003 x 1999 16.7 and 14.8, 2500 x 2504 x 500 to FP32 10.2 and 8.5.

@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kSmallThreads) amax_small_kernel(const void *x
 // y = R(fl(fl(code s) g)); code s is exact.  A lane takes a 16-byte vector of the output at a
 // time, so that a warp writes whole lines whatever the rows' alignment; of rows that do not begin
 // at such a boundary (SHIFTED) a vector's codes begin anywhere and may belong to two blocks.  Bound
-// by HBM: 8192 x 11008 to BF16 35 us (MXFP4, 6.5 TB/s) and 36 us (NVFP4); 1021 x 5003 to FP32 rows
+// by HBM: 8192 x 11008 to BF16 35 us (MXFP4, 6.5 TB/s) and 35 us (NVFP4); 1021 x 5003 to FP32 rows
 // of any alignment 6.0 us (a group of 16 a lane, element by element: 21 us).
 template <int DT, int FMT, bool SHIFTED, int PARTS>
 __global__ void __launch_bounds__(kThreads, 8)

@@ -6,7 +6,8 @@ the last layer of a policy).
 
 Between the forward and the backward pass of a micro-batch the norm's input is kept as low-bit
 codes and the projection's operand in FP4, along its columns alone; the logits become their own
-gradient in place.
+gradient in place.  The gradient's operands are rounded to the nearest code, not stochastically:
+elements below half a step of their block are 0.
 
     head = PolicyHead(norm_w, norm_b, weight)              # BF16 [H], [H], [V][H]
     old = head.logprobs(x, tokens)                         # of the sampling policy, FP32 [T]

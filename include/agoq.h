@@ -683,7 +683,8 @@ agoq_status agoq_amax(const void *x, int64_t ldx, int64_t T, int64_t K, int dtyp
  *            T <= 2^24.
  * A block with a NaN or an infinity has the NaN of its scale's type and codes of 0; with an
  * amax that is not finite every block has.  Whole codes and scales are written, padding
- * included.
+ * included.  Rounding is to the nearest only, never stochastic: elements below half of their
+ * block's smallest step are 0, so that sums over many small gradients are biased towards 0.
  */
 agoq_status agoq_fp4_quant(const void *x, int64_t ldx, int64_t T, int64_t K, int dtype, int format,
                            const float *amax, void *codes, void *scales, void *codes_t,
