@@ -1,0 +1,22 @@
+"""Shared memory that asynchronous copies fill again is released only once no load of it can be in
+flight (CPU, from the sources: an arrival on a barrier does not wait for loads issued before it, and
+a copy is not ordered behind them; the race is too rare to provoke)."""
+import os
+import re
+
+from gradient_quantization_gb300 import agoq
+
+
+def _source(name):
+    text = open(os.path.join(agoq.HERE, "csrc", name)).read()
+    return re.sub(r"//.*", "", text)
+
+
+def test_scales_of_the_fp4_product():
+    """Released when the loaded scales have been written to tensor memory."""
+    code = _source("fp4_gemm.cu")
+    assert code.count("mbar_arrive(&sempty[s])") == 1
+    start = code.index("uint32_t w[S::kScaleCols];")
+    order = [code.index(s, start) for s in ("tmem_st16(to + c, w + c)", "tcgen05.wait::st.sync.aligned",
+                                            "__syncwarp()", "mbar_arrive(&sempty[s])")]
+    assert order == sorted(order)
