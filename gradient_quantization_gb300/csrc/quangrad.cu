@@ -632,10 +632,10 @@ reduce_shards_staged_kernel(
 // blocks go round-robin to the CTAs; the producer copies each tile's BF16
 // gradient, master codes and master scales with cp.async.bulk into a
 // kAcStages-deep ring, and half warp h takes blocks h, h + 2 kAcWarps, ... of
-// the tile (lane j: elements 8j .. 8j+7), loads them from shared memory,
-// releases the stage and writes the new codes and scale straight back over the
-// master (the producer never reads a tile twice, so the in-place update races
-// nothing).  The arithmetic is accum_block, as in grad_accum_kernel.  Waits are
+// the tile (lane j: elements 8j .. 8j+7), loads them from shared memory, writes
+// the new codes and scale straight back over the master (the producer never
+// reads a tile twice, so the in-place update races nothing) and releases the
+// stage.  The arithmetic is accum_block, as in grad_accum_kernel.  Waits are
 // time-limited (status in g_reduce_status, this file's pipeline status word).
 constexpr int kAcWarps = 16;
 constexpr int kAcThreads = (kAcWarps + 1) * 32;
@@ -716,12 +716,6 @@ grad_accum_staged_kernel(uint8_t *__restrict__ master, float *__restrict__ scale
             mc[r] = reinterpret_cast<const uint2 *>(st + kAcGradBytes)[lb * 16 + j];
             sc[r] = reinterpret_cast<const float *>(st + kAcGradBytes + kAcCodeBytes)[lb];
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == kAcStages) {
-            stage = 0;
-            phase ^= 1u;
-        }
         const int64_t b0 = tile * kAcTile;
 #pragma unroll
         for (int r = 0; r < kAcRep; ++r) {
@@ -732,6 +726,16 @@ grad_accum_staged_kernel(uint8_t *__restrict__ master, float *__restrict__ scale
                 reinterpret_cast<uint2 *>(master)[blk * 16 + j] = out;
                 if (j == 0) scales[blk] = snew;
             }
+        }
+        // Released only now: the stores need the values, so that no load of the stage can still be in
+        // flight when the next bulk copies overwrite it (an arrival does not wait for the loads before
+        // it, and the copies are not ordered behind them).  2^30 elements 629 us; released early behind
+        // a proxy fence 647 us.
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == kAcStages) {
+            stage = 0;
+            phase ^= 1u;
         }
     }
 }

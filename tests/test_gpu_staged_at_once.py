@@ -1,0 +1,56 @@
+"""The kernels whose shared memory bulk copies fill again and again, from six threads on streams of
+their own beside products that share their SMs: each result is the one of a call alone, bit for
+bit."""
+import random
+import threading
+import time
+
+import pytest
+import torch
+
+from gradient_quantization_gb300 import agoq
+from tests.test_gpu_fp4_gemm import _gemm, _operand
+
+pytestmark = pytest.mark.gpu
+
+
+def _at_once(calls, seconds=4):
+    """`calls`: functions that return tensors, the same at every call."""
+    a, b = _operand(1, 4096, agoq.NVFP4, 1), _operand(4096, 4096, agoq.NVFP4, 2)
+    calls = calls + [lambda: [_gemm(a, b, agoq.NVFP4)]]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    stop, bad, done = time.time() + seconds, [], []
+
+    def work(seed):
+        pick, stream = random.Random(seed), torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            while time.time() < stop:
+                some = [pick.randrange(len(calls)) for _ in range(10)]
+                got = [calls[i]() for i in some]
+                stream.synchronize()
+                bad.extend(i for i, r in zip(some, got) if not all(torch.equal(x, y) for x, y in zip(r, want[i])))
+                done.append(len(some))
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    agoq.agoq_device_status()
+    assert not bad and sum(done) > 0, (len(bad), sum(done))
+
+
+def test_accumulations():
+    calls = []
+    for seed, n in ((1, 1 << 20), (2, 96 * 128 * 152 * 7 + 512)):     # one tile a CTA or none; several
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        grad = torch.randn(n, generator=g, device="cuda").bfloat16()
+        start = torch.zeros(n, dtype=torch.uint8, device="cuda"), torch.zeros(n // 128, device="cuda")
+        agoq.agoq_grad_accum_fp8(*start, torch.randn(n, generator=g, device="cuda").bfloat16())
+
+        def call(grad=grad, start=start):
+            master, scales = (t.clone() for t in start)
+            return agoq.agoq_grad_accum_fp8(master, scales, grad)
+        calls.append(call)
+    _at_once(calls)

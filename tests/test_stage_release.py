@@ -20,3 +20,19 @@ def test_scales_of_the_fp4_product():
     order = [code.index(s, start) for s in ("tmem_st16(to + c, w + c)", "tcgen05.wait::st.sync.aligned",
                                             "__syncwarp()", "mbar_arrive(&sempty[s])")]
     assert order == sorted(order)
+
+
+def _kernel(code, name):
+    """The text from a kernel's name to the next kernel or launch."""
+    start = code.index(name + "(")
+    ends = [code.find(s, start) for s in ("__global__", "cudaError_t launch")]
+    return code[start:min(e for e in ends if e > 0)]
+
+
+def test_the_staged_accumulation():
+    """Released when the results, which need every loaded value, have been stored."""
+    code = _kernel(_source("quangrad.cu"), "grad_accum_staged_kernel")
+    assert code.count("mbar_arrive(&empty[stage])") == 1
+    order = [code.index(s) for s in ("accum_block<MID>(", "reinterpret_cast<uint2 *>(master)[blk * 16 + j] = out",
+                                     "__syncwarp()", "mbar_arrive(&empty[stage])")]
+    assert order == sorted(order)
