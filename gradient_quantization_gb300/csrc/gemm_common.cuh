@@ -28,6 +28,12 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
                  : "memory");
 }
 
+// Orders this thread's loads of shared memory before bulk copies that overwrite it, issued by whoever
+// sees its warp's next arrival: the arrival alone does not wait for them.
+__device__ __forceinline__ void reads_before_copies() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }

@@ -551,7 +551,7 @@ reduce_shards_staged_kernel(
             auto ld = [&](int j) { return *reinterpret_cast<const uint4 *>(cs + (size_t)j * kStTile * 128); };
             // Shards are read from the stage two at a time, the next pair's
             // loads issued before the current pair is added; the stage is
-            // released once its last loads are issued (the arrive orders them).
+            // released once its last loads are there.
             if (k == kStShards) {
                 // a full stage: every bound and the rank-0 test are compile-time
                 auto full_stage = [&](auto first_stage) {
@@ -568,6 +568,7 @@ reduce_shards_staged_kernel(
                             t0 = ss[(j + 2) * kStTile];
                             t1 = ss[(j + 3) * kStTile];
                         } else {
+                            reads_before_copies();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&empty[stage]);
                         }
@@ -604,6 +605,7 @@ reduce_shards_staged_kernel(
                             t1 = ss[(j + 3) * kStTile];
                         }
                     } else {
+                        reads_before_copies();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&empty[stage]);
                     }

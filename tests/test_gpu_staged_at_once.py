@@ -54,3 +54,18 @@ def test_accumulations():
             return agoq.agoq_grad_accum_fp8(master, scales, grad)
         calls.append(call)
     _at_once(calls)
+
+
+def test_reduces():
+    calls = []
+    for W, n, count in ((3, 1 << 18, False), (8, 1 << 20, True), (13, 64 * 128 * 152 * 3 + 512, False)):
+        g = torch.Generator(device="cuda").manual_seed(W)
+        shards = torch.randint(0, 120, (W, n), generator=g, device="cuda").to(torch.uint8)
+        scales = torch.rand(W, n // 128, generator=g, device="cuda")
+
+        def call(W=W, n=n, count=count, shards=shards, scales=scales):
+            c = torch.zeros(1, dtype=torch.int64, device="cuda") if count else None
+            out = agoq.agoq_reduce_fp8_shards(shards, scales, W, n, naive_overflow_count=c)
+            return list(out) + ([c] if count else [])
+        calls.append(call)
+    _at_once(calls)

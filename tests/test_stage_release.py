@@ -36,3 +36,11 @@ def test_the_staged_accumulation():
     order = [code.index(s) for s in ("accum_block<MID>(", "reinterpret_cast<uint2 *>(master)[blk * 16 + j] = out",
                                      "__syncwarp()", "mbar_arrive(&empty[stage])")]
     assert order == sorted(order)
+
+
+def test_the_staged_reduce():
+    """Released behind a fence between the loads and copies to come, executed by every lane."""
+    code = _kernel(_source("quangrad.cu"), "reduce_shards_staged_kernel")
+    release = r"reads_before_copies\(\);\s*__syncwarp\(\);\s*if \(lane == 0\) mbar_arrive\(&empty\[stage\]\);"
+    assert len(re.findall(release, code)) == code.count("mbar_arrive(") == 2
+    assert "fence.proxy.async.shared::cta" in _source("gemm_common.cuh")
