@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(kDwTmaThreads, kDwTmaMinCtas) rmsnorm_dw_tma_k
                 const uint4 d = reinterpret_cast<const uint4 *>(st + St::kDy + row * 256)[l16];
                 dw_accum8(acc, d, xh, r);
             }
+            reads_before_copies();
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
         }

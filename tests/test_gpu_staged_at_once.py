@@ -69,3 +69,14 @@ def test_reduces():
             return list(out) + ([c] if count else [])
         calls.append(call)
     _at_once(calls)
+
+
+def test_rmsnorm_backwards():
+    calls = []
+    for T, H, bits in ((512, 512, 4), (4096, 1024, 8), (8192, 4096, 4)):
+        g = torch.Generator(device="cuda").manual_seed(T)
+        x, dy = (torch.randn(T, H, generator=g, device="cuda").bfloat16() for _ in range(2))
+        w = torch.randn(H, generator=g, device="cuda").bfloat16()
+        codes, scales = agoq.agoq_quant_act(x, bits)
+        calls.append(lambda a=(codes, scales, dy, w, T, H, bits): list(agoq.agoq_rmsnorm_backward(*a, 1e-5)))
+    _at_once(calls)

@@ -44,3 +44,18 @@ def test_the_staged_reduce():
     release = r"reads_before_copies\(\);\s*__syncwarp\(\);\s*if \(lane == 0\) mbar_arrive\(&empty\[stage\]\);"
     assert len(re.findall(release, code)) == code.count("mbar_arrive(") == 2
     assert "fence.proxy.async.shared::cta" in _source("gemm_common.cuh")
+
+
+def test_the_weight_gradient_of_rmsnorm():
+    """The same fence."""
+    code = _kernel(_source("rmsnorm.cu"), "rmsnorm_dw_tma_kernel")
+    release = r"reads_before_copies\(\);\s*__syncwarp\(\);\s*if \(lane == 0\) mbar_arrive\(&empty\[s\]\);"
+    assert len(re.findall(release, code)) == code.count("mbar_arrive(") == 1
+
+
+def test_the_codes_of_the_weight_gradient_product():
+    """As it was: released after the stores of what the codes were turned into."""
+    code = _source("wgrad_gemm_impl.cuh")
+    assert code.count("mbar_arrive(&sh.empty_x[sx])") == 1
+    stores, release = code.index("*reinterpret_cast<uint4 *>(dst) = y;"), code.index("mbar_arrive(&sh.empty_x[sx])")
+    assert stores < code.index("fence.proxy.async.shared::cta", stores) < release
